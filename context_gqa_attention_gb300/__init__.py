@@ -29,11 +29,16 @@ __all__ = [
     "cp_decode_workspace_size", "cp_decode_attention", "cp_decode_attention_noalloc",
     "cp_kv_cache_write", "cp_select_prefill_mode", "cp_attn_prefill_fused",
     "cp_prefill_fused_workspace_size", "STATUS",
+    "CP_ROPE_HALF", "CP_ROPE_PAIRS", "cp_rope_kv_cache_write", "cp_kv_cache_read",
+    "cp_q4_record_bytes", "cp_attn_prefill_mod", "cp_decode_mod_plan",
+    "cp_partial_attn_decode_mod", "cp_decode_attention_mod", "cp_partial_attn_decode_q4",
+    "cp_decode_attention_q4",
 ]
 
 CP_F32, CP_BF16 = 0, 1
 CP_PASS_KV, CP_PASS_Q = 0, 1
 CP_IMPL_AUTO, CP_IMPL_TCGEN05, CP_IMPL_SIMT, CP_IMPL_TCGEN05_SINGLE = 0, 1, 2, 3
+CP_ROPE_HALF, CP_ROPE_PAIRS = 0, 1
 STATUS = {0: "CP_OK", 1: "CP_ERR_INVALID_ARG", 2: "CP_ERR_UNSUPPORTED", 3: "CP_ERR_CUDA",
           4: "CP_ERR_TIMEOUT", 5: "CP_ERR_DEVICE_BOUNDS"}
 
@@ -76,6 +81,30 @@ class DecodeArgs(ctypes.Structure):
     ]
 
 
+class ScoreMod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("alibi_slopes", _vp),
+                ("kv_start", _vp), ("prefix_lens", _vp)]
+
+
+class RopeWriteArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "cache_q4", "num_seqs", "total_new", "num_q_heads", "num_kv_heads", "head_dim",
+                 "cp", "interleave", "block_size", "max_blocks", "rope_style", "rot_dim", "reserved")] + \
+               [(n, ctypes.c_int64) for n in
+                ("pool_pages", "q_stride", "k_stride", "v_stride", "q_out_stride")] + \
+               [(n, _vp) for n in ("q", "k", "v", "cu_new", "start_pos", "inv_freq", "block_tables",
+                                   "k_cache", "v_cache", "q_out", "k_out", "err")]
+
+
+class KvReadArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("out_dtype", "cache_q4", "num_seqs", "total", "num_kv_heads", "head_dim", "cp",
+                 "interleave", "block_size", "max_blocks")] + \
+               [("pool_pages", ctypes.c_int64)] + \
+               [(n, _vp) for n in ("k_cache", "v_cache", "block_tables", "cu_out", "start_pos", "k_out",
+                                   "v_out", "err")]
+
+
 _LIB = None
 
 # (name, restype, argtypes)
@@ -108,7 +137,20 @@ _SIGS = [
     ("cp_decode_attention", ctypes.c_int32, [ctypes.POINTER(DecodeArgs), _vp, ctypes.c_size_t, _vp,
                                              _vp, _vp]),
     ("cp_decode_attention_noalloc", ctypes.c_int32, [ctypes.POINTER(DecodeArgs), _vp, _vp, _vp]),
-]
+    ("cp_rope_write_args_size", ctypes.c_size_t, []),
+    ("cp_kv_read_args_size", ctypes.c_size_t, []),
+    ("cp_score_mod_size", ctypes.c_size_t, []),
+    ("cp_q4_record_bytes", ctypes.c_int64, [ctypes.c_int32]),
+    ("cp_rope_kv_cache_write", ctypes.c_int32, [ctypes.POINTER(RopeWriteArgs), _vp]),
+    ("cp_kv_cache_read", ctypes.c_int32, [ctypes.POINTER(KvReadArgs), _vp]),
+    ("cp_attn_prefill_mod", ctypes.c_int32, [ctypes.POINTER(PrefillArgs), ctypes.POINTER(ScoreMod), _vp,
+                                             _vp, _vp]),
+    ("cp_decode_mod_plan", ctypes.c_int32, [ctypes.c_int32] * 7 + [ctypes.POINTER(ctypes.c_int32)] * 2),
+] + [(f"cp_partial_attn_decode_{n}", ctypes.c_int32,
+      [ctypes.POINTER(DecodeArgs), ctypes.POINTER(ScoreMod), _vp]) for n in ("mod", "q4")] + \
+    [(f"cp_decode_attention_{n}", ctypes.c_int32,
+      [ctypes.POINTER(DecodeArgs), ctypes.POINTER(ScoreMod), _vp, ctypes.c_size_t, _vp, _vp, _vp])
+     for n in ("mod", "q4")]
 
 EXPORTED = [s[0] for s in _SIGS]
 
@@ -137,6 +179,10 @@ def load(build_if_missing: bool = False):
         raise CPError(1, "cp_prefill_args layout mismatch between binding and library")
     if lib.cp_decode_args_size() != ctypes.sizeof(DecodeArgs):
         raise CPError(1, "cp_decode_args layout mismatch between binding and library")
+    for name, struct in (("cp_rope_write_args", RopeWriteArgs), ("cp_kv_read_args", KvReadArgs),
+                         ("cp_score_mod", ScoreMod)):
+        if getattr(lib, name + "_size")() != ctypes.sizeof(struct):
+            raise CPError(1, f"{name} layout mismatch between binding and library")
     _LIB = lib
     return lib
 
@@ -560,6 +606,339 @@ def cp_lse_merge(partial_out, partial_lse, out=None, out_dtype=torch.bfloat16, o
     _check(_LIB.cp_lse_merge(_ptr(partial_out), _ptr(partial_lse), P, rows, H, d, _ptr(out),
                              _cp_dtype(out), _ptr(out_lse), _stream(stream)))
     return out, out_lse
+
+
+# ---------------------------------------------------------- rotation, 4-bit cache, modified scores
+
+def cp_q4_record_bytes(head_dim):
+    """Bytes of one record of the 4-bit cache (one kv head's 16 tokens): 9 * head_dim."""
+    load()
+    return _LIB.cp_q4_record_bytes(head_dim)
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise CPError(1, f"{name} must be {list(shape)} (got {list(t.shape)})")
+
+
+def _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, dtype):
+    """Checks of the paged pools and their tables; whether they hold 4-bit records (uint8)."""
+    q4 = k_cache.dtype == torch.uint8
+    if k_cache.dim() != (4 if q4 else 5):
+        raise CPError(1, "k_cache must be [cp, pool, Hkv, 16, d], or uint8 [cp, pool, Hkv, 9 d] (4-bit)")
+    _dev(k_cache, "k_cache", torch.uint8 if q4 else dtype)
+    _dev(v_cache, "v_cache", k_cache.dtype)
+    _dev(block_tables, "block_tables", torch.int32)
+    pool, heads = k_cache.shape[1], k_cache.shape[2] if Hkv is None else Hkv
+    want = (cp, pool, heads, 9 * d) if q4 else (cp, pool, heads, k_cache.shape[3], d)
+    _shape(k_cache, "k_cache", want)
+    _shape(v_cache, "v_cache", want)
+    if block_tables.dim() != 3 or tuple(block_tables.shape[:2]) != (cp, B):
+        raise CPError(1, f"block_tables must be [cp, B, max_blocks] = [{cp}, {B}, ..] "
+                         f"(got {list(block_tables.shape)})")
+    return q4
+
+
+def _token_rows(t, name, dtype):
+    """A [N, H, d] tensor whose heads are dense within a token; its token stride."""
+    if not t.is_cuda or t.device != _CALL.device:
+        raise CPError(1, f"{name} must be a CUDA tensor on {_CALL.device}")
+    if t.dim() != 3 or t.dtype != dtype:
+        raise CPError(1, f"{name} must be a {dtype} tensor [N, H, d]")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise CPError(1, f"the heads of a token of {name} must be contiguous (only the token stride is free)")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _index(t, name, n):
+    _dev(t, name, torch.int32)
+    if t.numel() != n:
+        raise CPError(1, f"{name} must have {n} entries (got {t.numel()})")
+
+
+@_on_first_tensors_device
+def cp_rope_kv_cache_write(k_new, v_new, cu_new, start_pos, k_cache, v_cache, block_tables, cp,
+                           interleave, *, inv_freq=None, rope_style=CP_ROPE_HALF, q=None, q_out=None,
+                           k_out=None, err=None, stream=None):
+    """Append new K/V rows [N, Hkv, d] to the per-rank pools at their round-robin slots with the
+    rotary embedding applied on the way, and rotate the queries q [N, Hq, d] (see cpattn.h).
+
+    The pools are [cp, pool, Hkv, 16, d] of the rows' dtype, or uint8 [cp, pool, Hkv, 9 d] (4-bit
+    records).  inv_freq: float64 CUDA tensor [rot_dim / 2] of radians per position (None: no
+    rotation).  k_new, v_new and q may be column slices of a wider tensor (any token stride).
+    q_out may be q.  Returns (q_out or None, k_out or None); k_out is written only if given."""
+    load()
+    N, Hkv, d = k_new.shape
+    B = cu_new.numel() - 1
+    a = RopeWriteArgs()
+    a.dtype = _cp_dtype(k_new)
+    a.k_stride = _token_rows(k_new, "k_new", k_new.dtype)
+    a.v_stride = _token_rows(v_new, "v_new", k_new.dtype)
+    _shape(v_new, "v_new", (N, Hkv, d))
+    _index(cu_new, "cu_new", B + 1)
+    _index(start_pos, "start_pos", B)
+    a.cache_q4 = _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, k_new.dtype)
+    a.num_seqs, a.total_new, a.num_kv_heads, a.head_dim = B, N, Hkv, d
+    a.cp, a.interleave, a.block_size = cp, interleave, 16 if a.cache_q4 else k_cache.shape[3]
+    a.max_blocks, a.pool_pages, a.rope_style = block_tables.shape[-1], k_cache.shape[1], rope_style
+    if inv_freq is not None:
+        _dev(inv_freq, "inv_freq", torch.float64)
+        a.rot_dim, a.inv_freq = 2 * inv_freq.numel(), _ptr(inv_freq)
+    if q is not None:
+        a.q_stride, a.num_q_heads = _token_rows(q, "q", k_new.dtype), q.shape[1]
+        _shape(q, "q", (N, q.shape[1], d))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        a.q_out_stride = _token_rows(q_out, "q_out", q.dtype)
+        _shape(q_out, "q_out", q.shape)
+        a.q, a.q_out = _ptr(q), _ptr(q_out)
+    elif q_out is not None:
+        raise CPError(1, "q_out without q")
+    if k_out is not None:
+        _dev(k_out, "k_out", k_new.dtype)
+        _shape(k_out, "k_out", (N, Hkv, d))
+        a.k_out = _ptr(k_out)
+    _dev(err, "err", torch.int32)
+    a.k, a.v, a.cu_new, a.start_pos = _ptr(k_new), _ptr(v_new), _ptr(cu_new), _ptr(start_pos)
+    a.block_tables, a.k_cache, a.v_cache, a.err = _ptr(block_tables), _ptr(k_cache), _ptr(v_cache), _ptr(err)
+    if N:
+        _check(_LIB.cp_rope_kv_cache_write(ctypes.byref(a), _stream(stream)))
+    return q_out, k_out
+
+
+@_on_first_tensors_device
+def cp_kv_cache_read(k_cache, v_cache, cu_out, start_pos, block_tables, cp, interleave, *, total=None,
+                     out_dtype=None, k_out=None, v_out=None, err=None, stream=None):
+    """Positions start_pos[b] + i of every sequence from the paged round-robin cache to contiguous
+    rows cu_out[b] + i of k_out, v_out [N, Hkv, d] (see cpattn.h): the K/V of a pass-KV prefill over
+    a cached context.  4-bit records (uint8 pools) come back as the values they stand for, in
+    out_dtype (bf16 or f32; the pools' own dtype otherwise).  total: N, when cu_out[B] is not to be
+    fetched from the device.  Returns (k_out, v_out)."""
+    load()
+    B = cu_out.numel() - 1
+    q4 = k_cache.dtype == torch.uint8
+    d = k_cache.shape[-1] // 9 if q4 else k_cache.shape[-1]
+    if out_dtype is None:
+        out_dtype = k_out.dtype if k_out is not None else torch.bfloat16 if q4 else k_cache.dtype
+    if not q4 and out_dtype != k_cache.dtype:
+        raise CPError(1, f"out_dtype must be the cache's {k_cache.dtype} (got {out_dtype})")
+    _paged(k_cache, v_cache, block_tables, cp, B, d, None, k_cache.dtype)
+    Hkv = k_cache.shape[2]
+    _index(cu_out, "cu_out", B + 1)
+    _index(start_pos, "start_pos", B)
+    _dev(err, "err", torch.int32)
+    if total is None:
+        total = k_out.shape[0] if k_out is not None else int(cu_out[-1].item())
+    if k_out is None:
+        k_out = torch.empty(total, Hkv, d, dtype=out_dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(total, Hkv, d, dtype=out_dtype, device=k_cache.device)
+    for n, t in (("k_out", k_out), ("v_out", v_out)):
+        _dev(t, n, out_dtype)
+        _shape(t, n, (total, Hkv, d))
+    a = KvReadArgs()
+    a.out_dtype, a.cache_q4, a.num_seqs, a.total, a.num_kv_heads, a.head_dim = (
+        _cp_dtype(k_out), q4, B, total, Hkv, d)
+    a.cp, a.interleave, a.block_size = cp, interleave, 16 if q4 else k_cache.shape[3]
+    a.max_blocks, a.pool_pages = block_tables.shape[-1], k_cache.shape[1]
+    a.k_cache, a.v_cache, a.block_tables = _ptr(k_cache), _ptr(v_cache), _ptr(block_tables)
+    a.cu_out, a.start_pos, a.k_out, a.v_out, a.err = (_ptr(cu_out), _ptr(start_pos), _ptr(k_out),
+                                                      _ptr(v_out), _ptr(err))
+    if total:
+        _check(_LIB.cp_kv_cache_read(ctypes.byref(a), _stream(stream)))
+    return k_out, v_out
+
+
+def _score_mod(Hq, softcap, window, alibi_slopes, kv_start, rows, prefix_lens=None, B=0):
+    m = ScoreMod()
+    m.softcap, m.window = softcap, window
+    if alibi_slopes is not None:
+        _dev(alibi_slopes, "alibi_slopes", torch.float32)
+        _shape(alibi_slopes, "alibi_slopes", (Hq,))
+        m.alibi_slopes = _ptr(alibi_slopes)
+    if kv_start is not None:
+        _index(kv_start, "kv_start", rows)
+        m.kv_start = _ptr(kv_start)
+    if prefix_lens is not None:
+        _index(prefix_lens, "prefix_lens", B)
+        m.prefix_lens = _ptr(prefix_lens)
+    return m
+
+
+@_on_first_tensors_device
+def cp_attn_prefill_mod(q, cu_seqlens_q, k, v, *, cu_seqlens_kv=None, softcap=0.0, window=0,
+                        alibi_slopes=None, kv_start=None, prefix_lens=None, max_seqlen_q=None,
+                        softmax_scale=0.0, out=None, out_lse=None, err=None, stream=None):
+    """Prefill attention with modified scores over contiguous k, v [Nkv, Hkv, d] (see cpattn.h): a
+    tanh cap, a distance bias alibi_slopes f32 [Hq], a sliding window, kv_start int32 [Nq] (first
+    visible position of each row: its document) and prefix_lens int32 [B] (keys every query sees).
+    bf16.  Returns (out [Nq, Hq, d] bf16, lse [Nq, Hq] f32)."""
+    load()
+    Nq, Hq, d = q.shape
+    B = cu_seqlens_q.numel() - 1
+    if out is None:
+        out = torch.empty(Nq, Hq, d, dtype=torch.bfloat16, device=q.device)
+    if out_lse is None:
+        out_lse = torch.empty(Nq, Hq, dtype=torch.float32, device=q.device)
+    for n, t, dt in (("q", q, torch.bfloat16), ("cu_seqlens_q", cu_seqlens_q, torch.int32),
+                     ("out", out, torch.bfloat16), ("out_lse", out_lse, torch.float32),
+                     ("err", err, torch.int32)):
+        _dev(t, n, dt)
+    _shape(out, "out", (Nq, Hq, d))
+    _shape(out_lse, "out_lse", (Nq, Hq))
+    if max_seqlen_q is None:
+        max_seqlen_q = int((cu_seqlens_q[1:] - cu_seqlens_q[:-1]).max().item()) if B else 0
+    a = PrefillArgs()
+    a.mode, a.dtype, a.impl = CP_PASS_KV, CP_BF16, CP_IMPL_AUTO
+    a.num_seqs, a.num_q_heads, a.head_dim, a.cp = B, Hq, d, 1
+    a.softmax_scale, a.total_q, a.max_seqlen_q = softmax_scale, Nq, max_seqlen_q
+    a.q_shard = a.kv_shard = -1
+    a.cu_seqlens_q, a.q, a.err = _ptr(cu_seqlens_q), _ptr(q), _ptr(err)
+    _kv_source(a, k, v, cu_seqlens_kv, torch.bfloat16)
+    if k.dim() != 3 or k.shape[2] != d or (cu_seqlens_kv is None and k.shape[0] != Nq):
+        raise CPError(1, f"k and v must be [Nkv, Hkv, {d}] (Nkv = {Nq} without cu_seqlens_kv)")
+    if cu_seqlens_kv is not None:
+        _index(cu_seqlens_kv, "cu_seqlens_kv", B + 1)
+    m = _score_mod(Hq, softcap, window, alibi_slopes, kv_start, Nq, prefix_lens, B)
+    _check(_LIB.cp_attn_prefill_mod(ctypes.byref(a), ctypes.byref(m), _ptr(out), _ptr(out_lse),
+                                    _stream(stream)))
+    return out, out_lse
+
+
+def cp_decode_mod_plan(num_seqs, num_kv_heads, cp, interleave, max_seq_len, *, window=0, q4=False):
+    """(num_splits, split_tokens) for the decode calls with modified scores or a 4-bit cache."""
+    load()
+    ns, st = ctypes.c_int32(), ctypes.c_int32()
+    _check(_LIB.cp_decode_mod_plan(num_seqs, num_kv_heads, cp, interleave, max_seq_len, window, q4,
+                                   ctypes.byref(ns), ctypes.byref(st)))
+    return ns.value, st.value
+
+
+def _decode_mod_args(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, q4, softcap, window,
+                     alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens, softmax_scale, err):
+    if q.dim() != 3:
+        raise CPError(1, "q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    _dev(q, "q")
+    if _paged(k_cache, v_cache, block_tables, cp, B, d, None, q.dtype) != q4:
+        raise CPError(1, "uint8 pools hold 4-bit records (the *_q4 calls); the *_mod calls take pools of q's dtype")
+    _index(seq_lens, "seq_lens", B)
+    _dev(err, "err", torch.int32)
+    Hkv = k_cache.shape[2]
+    if num_splits is None or split_tokens is None:
+        if max_seq_len is None:
+            max_seq_len = max(1, int(seq_lens.max().item()))
+        num_splits, split_tokens = cp_decode_mod_plan(B, Hkv, cp, interleave, max_seq_len, window=window,
+                                                      q4=q4)
+    a = DecodeArgs()
+    a.dtype, a.num_seqs, a.num_q_heads, a.num_kv_heads, a.head_dim = _cp_dtype(q), B, Hq, Hkv, d
+    a.cp, a.interleave, a.block_size = cp, interleave, 16 if q4 else k_cache.shape[3]
+    a.num_splits, a.split_tokens, a.softmax_scale = num_splits, split_tokens, softmax_scale
+    a.max_blocks, a.pool_pages = block_tables.shape[-1], k_cache.shape[1]
+    a.q, a.k_cache, a.v_cache = _ptr(q), _ptr(k_cache), _ptr(v_cache)
+    a.block_tables, a.seq_lens, a.err = _ptr(block_tables), _ptr(seq_lens), _ptr(err)
+    return a, _score_mod(Hq, softcap, window, alibi_slopes, kv_start, B)
+
+
+def _partial_decode(call, q4, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
+                    window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
+                    softmax_scale, out, lse, err, stream):
+    a, m = _decode_mod_args(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, q4, softcap,
+                            window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
+                            softmax_scale, err)
+    P, (B, Hq, d) = cp * a.num_splits, q.shape
+    if out is None:
+        out = torch.empty(P, B, Hq, d, dtype=torch.float32, device=q.device)
+    if lse is None:
+        lse = torch.empty(P, B, Hq, dtype=torch.float32, device=q.device)
+    _dev(out, "out", torch.float32)
+    _dev(lse, "lse", torch.float32)
+    _shape(out, "out", (P, B, Hq, d))
+    _shape(lse, "lse", (P, B, Hq))
+    a.out, a.lse = _ptr(out), _ptr(lse)
+    _check(call(ctypes.byref(a), ctypes.byref(m), _stream(stream)))
+    return out, lse
+
+
+def _fused_decode(call, q4, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
+                  window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
+                  softmax_scale, workspace, out, out_lse, want_lse, err, stream):
+    a, m = _decode_mod_args(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, q4, softcap,
+                            window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
+                            softmax_scale, err)
+    B, Hq, d = q.shape
+    if workspace is None:
+        need = cp_decode_workspace_size(B, Hq, a.num_kv_heads, d, cp, a.num_splits)
+        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty(B, Hq, d, dtype=q.dtype, device=q.device)
+    if out_lse is None and want_lse:
+        out_lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+    _dev(workspace, "workspace", torch.uint8)
+    _dev(out, "out", q.dtype)
+    _shape(out, "out", (B, Hq, d))
+    if out_lse is not None:
+        _dev(out_lse, "out_lse", torch.float32)
+        _shape(out_lse, "out_lse", (B, Hq))
+    _check(call(ctypes.byref(a), ctypes.byref(m), _ptr(workspace), workspace.numel(), _ptr(out),
+                _ptr(out_lse), _stream(stream)))
+    return out, out_lse
+
+
+@_on_first_tensors_device
+def cp_partial_attn_decode_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
+                               softcap=0.0, window=0, alibi_slopes=None, kv_start=None,
+                               max_seq_len=None, num_splits=None, split_tokens=None,
+                               softmax_scale=0.0, out=None, lse=None, err=None, stream=None):
+    """cp_partial_attn_decode with modified scores (see cpattn.h): a tanh cap, a sliding window, a
+    distance bias alibi_slopes f32 [Hq] and kv_start int32 [B] (first visible position).
+    Returns (out [P, B, Hq, d], lse [P, B, Hq]), P = cp * num_splits."""
+    load()
+    return _partial_decode(_LIB.cp_partial_attn_decode_mod, False, q, k_cache, v_cache, block_tables,
+                           seq_lens, cp, interleave, softcap, window, alibi_slopes, kv_start,
+                           max_seq_len, num_splits, split_tokens, softmax_scale, out, lse, err, stream)
+
+
+@_on_first_tensors_device
+def cp_decode_attention_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
+                            softcap=0.0, window=0, alibi_slopes=None, kv_start=None,
+                            max_seq_len=None, num_splits=None, split_tokens=None, softmax_scale=0.0,
+                            workspace=None, out=None, out_lse=None, want_lse=True, err=None,
+                            stream=None):
+    """cp_decode_attention with modified scores (see cp_partial_attn_decode_mod and cpattn.h).
+    Returns (out [B, Hq, d] dtype of q, lse [B, Hq] f32 or None)."""
+    load()
+    return _fused_decode(_LIB.cp_decode_attention_mod, False, q, k_cache, v_cache, block_tables,
+                         seq_lens, cp, interleave, softcap, window, alibi_slopes, kv_start,
+                         max_seq_len, num_splits, split_tokens, softmax_scale, workspace, out, out_lse,
+                         want_lse, err, stream)
+
+
+@_on_first_tensors_device
+def cp_partial_attn_decode_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
+                              softcap=0.0, window=0, alibi_slopes=None, kv_start=None,
+                              max_seq_len=None, num_splits=None, split_tokens=None,
+                              softmax_scale=0.0, out=None, lse=None, err=None, stream=None):
+    """cp_partial_attn_decode over the 4-bit cache, uint8 [cp, pool, Hkv, 9 d] (see cpattn.h), bf16
+    queries; scores may be modified as in cp_partial_attn_decode_mod."""
+    load()
+    return _partial_decode(_LIB.cp_partial_attn_decode_q4, True, q, k_cache, v_cache, block_tables,
+                           seq_lens, cp, interleave, softcap, window, alibi_slopes, kv_start,
+                           max_seq_len, num_splits, split_tokens, softmax_scale, out, lse, err, stream)
+
+
+@_on_first_tensors_device
+def cp_decode_attention_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
+                           softcap=0.0, window=0, alibi_slopes=None, kv_start=None, max_seq_len=None,
+                           num_splits=None, split_tokens=None, softmax_scale=0.0, workspace=None,
+                           out=None, out_lse=None, want_lse=True, err=None, stream=None):
+    """cp_decode_attention over the 4-bit cache, uint8 [cp, pool, Hkv, 9 d] (see cpattn.h), bf16
+    queries; scores may be modified as in cp_partial_attn_decode_mod."""
+    load()
+    return _fused_decode(_LIB.cp_decode_attention_q4, True, q, k_cache, v_cache, block_tables, seq_lens,
+                         cp, interleave, softcap, window, alibi_slopes, kv_start, max_seq_len,
+                         num_splits, split_tokens, softmax_scale, workspace, out, out_lse, want_lse,
+                         err, stream)
 
 
 def default_scale(head_dim):

@@ -735,6 +735,205 @@ static cp_status check_decode_args(const cp_decode_args* a, bool need_partials) 
   return ok();
 }
 
+int64_t cp_q4_record_bytes(int32_t head_dim) { return 9ll * head_dim; }
+size_t cp_rope_write_args_size(void) { return sizeof(cp_rope_write_args); }
+size_t cp_kv_read_args_size(void) { return sizeof(cp_kv_read_args); }
+size_t cp_score_mod_size(void) { return sizeof(cp_score_mod); }
+
+// Shape arguments that every call on the paged cache shares.
+static cp_status check_cache_shape(int32_t head_dim, int32_t cp, int32_t interleave, int32_t block_size,
+                                   int32_t max_blocks, int64_t pool_pages) {
+  if (head_dim != 64 && head_dim != 128)
+    return fail(CP_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
+  if (block_size != 16) return fail(CP_ERR_UNSUPPORTED, "block_size must be 16 (got %d)", block_size);
+  REQUIRE(cp >= 1 && cp <= 64, "cp must be in [1, 64] (got %d)", cp);
+  REQUIRE(interleave >= 1, "interleave must be >= 1");
+  REQUIRE(max_blocks >= 1 && pool_pages >= 1, "max_blocks and pool_pages must be >= 1");
+  return CP_OK;
+}
+
+cp_status cp_rope_kv_cache_write(const cp_rope_write_args* a, void* stream) {
+  REQUIRE(a != nullptr, "args is null");
+  REQUIRE(a->dtype == CP_F32 || a->dtype == CP_BF16, "dtype must be CP_F32 or CP_BF16");
+  REQUIRE(a->cache_q4 == 0 || a->cache_q4 == 1, "cache_q4 must be 0 or 1");
+  REQUIRE(a->num_seqs >= 1 && a->total_new >= 0 && a->num_kv_heads >= 1 && a->num_kv_heads <= 65536,
+          "bad num_seqs / total_new / num_kv_heads");
+  const cp_status st = check_cache_shape(a->head_dim, a->cp, a->interleave, a->block_size, a->max_blocks,
+                                         a->pool_pages);
+  if (st != CP_OK) return st;
+  REQUIRE(a->rope_style == CP_ROPE_HALF || a->rope_style == CP_ROPE_PAIRS, "unknown rope_style %d", a->rope_style);
+  REQUIRE(a->rot_dim >= 0 && a->rot_dim <= a->head_dim && a->rot_dim % 16 == 0,
+          "rot_dim must be a multiple of 16 in [0, head_dim] (got %d)", a->rot_dim);
+  REQUIRE(a->rot_dim == 0 || a->inv_freq != nullptr, "inv_freq is null");
+  REQUIRE(a->reserved == 0, "reserved must be 0");
+  REQUIRE(a->cu_new && a->start_pos && a->block_tables, "cu_new, start_pos and block_tables are required");
+  REQUIRE_PTR(a->k);
+  REQUIRE_PTR(a->v);
+  REQUIRE_PTR(a->k_cache);
+  REQUIRE_PTR(a->v_cache);
+  REQUIRE(aligned16(a->k_out), "k_out must be 16-byte aligned");
+  const int per16 = a->dtype == CP_BF16 ? 8 : 4;  // elements in 16 bytes
+  const int64_t kv_row = (int64_t)a->num_kv_heads * a->head_dim;
+  auto stride_ok = [&](int64_t stride, int64_t row) { return stride % per16 == 0 && stride >= row; };
+  REQUIRE(stride_ok(a->k_stride, kv_row) && stride_ok(a->v_stride, kv_row),
+          "k_stride / v_stride must hold a row and be a multiple of 16 bytes");
+  if (a->q != nullptr) {
+    REQUIRE(a->num_q_heads >= 1 && a->num_q_heads <= 65536, "num_q_heads must be >= 1 with q");
+    REQUIRE_PTR(a->q);
+    REQUIRE_PTR(a->q_out);
+    const int64_t q_row = (int64_t)a->num_q_heads * a->head_dim;
+    REQUIRE(stride_ok(a->q_stride, q_row) && stride_ok(a->q_out_stride, q_row),
+            "q_stride / q_out_stride must hold a row and be a multiple of 16 bytes");
+    REQUIRE(a->q_out != a->q || a->q_out_stride == a->q_stride, "q in place needs q_out_stride = q_stride");
+  } else {
+    REQUIRE(a->q_out == nullptr, "q_out without q");
+  }
+  if (a->total_new == 0) return ok();
+  return launched(cp_launch_rope_write(*a, as_stream(stream)), "cp_rope_kv_cache_write launch");
+}
+
+cp_status cp_kv_cache_read(const cp_kv_read_args* a, void* stream) {
+  REQUIRE(a != nullptr, "args is null");
+  REQUIRE(a->out_dtype == CP_F32 || a->out_dtype == CP_BF16, "out_dtype must be CP_F32 or CP_BF16");
+  REQUIRE(a->cache_q4 == 0 || a->cache_q4 == 1, "cache_q4 must be 0 or 1");
+  REQUIRE(a->num_seqs >= 1 && a->total >= 0 && a->num_kv_heads >= 1 && a->num_kv_heads <= 65536,
+          "bad num_seqs / total / num_kv_heads");
+  const cp_status st = check_cache_shape(a->head_dim, a->cp, a->interleave, a->block_size, a->max_blocks,
+                                         a->pool_pages);
+  if (st != CP_OK) return st;
+  REQUIRE(a->cu_out && a->start_pos && a->block_tables, "cu_out, start_pos and block_tables are required");
+  REQUIRE_PTR(a->k_cache);
+  REQUIRE_PTR(a->v_cache);
+  if (a->total == 0) return ok();
+  REQUIRE_PTR(a->k_out);
+  REQUIRE_PTR(a->v_out);
+  return launched(cp_launch_kv_read(*a, as_stream(stream)), "cp_kv_cache_read launch");
+}
+
+static cp_status check_mod(const cp_score_mod* m, bool prefill) {
+  REQUIRE(isfinite(m->softcap) && m->softcap >= 0.f, "softcap must be finite and >= 0");
+  REQUIRE(m->window >= 0, "window must be >= 0");
+  REQUIRE(prefill || m->prefix_lens == nullptr, "prefix_lens is a prefill argument");
+  return CP_OK;
+}
+
+cp_status cp_attn_prefill_mod(const cp_prefill_args* a, const cp_score_mod* mod, void* out, float* out_lse,
+                              void* stream) {
+  cp_status st = check_fused_shape(a);
+  if (st != CP_OK) return st;
+  if (a->mode != CP_PASS_KV) return fail(CP_ERR_UNSUPPORTED, "modified scores take contiguous k / v (CP_PASS_KV)");
+  if (a->impl != CP_IMPL_AUTO && a->impl != CP_IMPL_TCGEN05)
+    return fail(CP_ERR_UNSUPPORTED, "impl must be CP_IMPL_AUTO or CP_IMPL_TCGEN05 (got %d)", a->impl);
+  REQUIRE(a->cu_seqlens_q != nullptr, "cu_seqlens_q is null");
+  REQUIRE_PTR(a->q);
+  st = check_kv_source(a);
+  if (st != CP_OK) return st;
+  REQUIRE_PTR(out);
+  REQUIRE(out_lse != nullptr, "out_lse is null");
+  REQUIRE(a->debug == 0, "debug must be 0");
+  const cp_score_mod none = {0.f, 0, nullptr, nullptr, nullptr};
+  if (mod == nullptr) mod = &none;
+  st = check_mod(mod, true);
+  if (st != CP_OK) return st;
+  if (a->total_q == 0) return ok();
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / sqrtf((float)a->head_dim);
+  return launched(cp_launch_prefill_mod(*a, *mod, scale, out, out_lse, as_stream(stream)),
+                  "cp_attn_prefill_mod launch");
+}
+
+cp_status cp_decode_mod_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t cp, int32_t interleave,
+                             int32_t max_seq_len, int32_t window, int32_t q4, int32_t* num_splits,
+                             int32_t* split_tokens) {
+  REQUIRE(num_seqs >= 1 && num_kv_heads >= 1 && cp >= 1 && cp <= 64 && interleave >= 1 && max_seq_len >= 1 &&
+              window >= 0,
+          "all sizes must be >= 1 and window >= 0");
+  REQUIRE(num_splits && split_tokens, "outputs are null");
+  constexpr long long page = 16;
+  // most tokens of a span of n consecutive positions that one rank can hold
+  const long long period = (long long)interleave * cp;
+  auto share_of = [&](long long n) {
+    const long long rem = n % period;
+    return n / period * interleave + (rem < interleave ? rem : interleave);
+  };
+  long long share = share_of(max_seq_len);
+  if (window > 0 && window < max_seq_len) {  // splits start at a page: up to 15 tokens before it
+    const long long w = share_of(window) + page - 1;
+    share = share < w ? share : w;
+  }
+  // Tokens per CTA: about `most`, fewer where that would leave SMs without work, and no fewer than
+  // a page for each of its four warps.
+  const long long most = q4 ? 2048 : 2048, least = 4 * page;
+  const long long base = (long long)num_seqs * num_kv_heads * cp;
+  long long S = (share + most - 1) / most;
+  const long long want = (8ll * 152 + base - 1) / base;
+  if (S < want) S = want;
+  if (S > (share + least - 1) / least) S = (share + least - 1) / least;
+  if (S > 256 / cp) S = 256 / cp;
+  if (S < 1) S = 1;
+  long long st = (share + S - 1) / S;
+  st = (st + page - 1) / page * page;
+  S = (share + st - 1) / st;
+  *num_splits = (int32_t)S;
+  *split_tokens = (int32_t)st;
+  return ok();
+}
+
+static cp_status decode_mod_partials(const cp_decode_args* a, const cp_score_mod* mod, bool q4, void* stream) {
+  cp_status st = check_decode_args(a, true);
+  if (st != CP_OK) return st;
+  if (q4 && a->dtype != CP_BF16) return fail(CP_ERR_UNSUPPORTED, "a 4-bit cache takes bf16 queries");
+  const cp_score_mod none = {0.f, 0, nullptr, nullptr, nullptr};
+  if (mod == nullptr) mod = &none;
+  st = check_mod(mod, false);
+  if (st != CP_OK) return st;
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / sqrtf((float)a->head_dim);
+  return launched(cp_launch_decode_mod(*a, *mod, q4, scale, nullptr, nullptr, nullptr, as_stream(stream)),
+                  "decode launch");
+}
+
+static cp_status decode_mod_fused(const cp_decode_args* a, const cp_score_mod* mod, bool q4, void* workspace,
+                                  size_t workspace_bytes, void* out, float* out_lse, void* stream) {
+  cp_status st = check_decode_args(a, false);
+  if (st != CP_OK) return st;
+  if (q4 && a->dtype != CP_BF16) return fail(CP_ERR_UNSUPPORTED, "a 4-bit cache takes bf16 queries");
+  const cp_score_mod none = {0.f, 0, nullptr, nullptr, nullptr};
+  if (mod == nullptr) mod = &none;
+  st = check_mod(mod, false);
+  if (st != CP_OK) return st;
+  REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
+          "workspace must be a non-null 256-byte aligned pointer");
+  REQUIRE_PTR(out);
+  if ((long long)a->cp * a->num_splits > 256)
+    return fail(CP_ERR_UNSUPPORTED, "cp * num_splits must be <= 256 for the fused decode (got %lld)",
+                (long long)a->cp * a->num_splits);
+  size_t ol, oo;
+  const size_t need = cp_decode_ws_layout(a->num_seqs, a->num_q_heads, a->num_kv_heads, a->head_dim,
+                                          a->cp * a->num_splits, &ol, &oo);
+  REQUIRE(workspace_bytes >= need, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+  CpDecodeWorkspace ws;
+  ws.counters = static_cast<int32_t*>(workspace);
+  ws.partial_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + ol);
+  ws.partial_out = reinterpret_cast<float*>(static_cast<char*>(workspace) + oo);
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / sqrtf((float)a->head_dim);
+  return launched(cp_launch_decode_mod(*a, *mod, q4, scale, &ws, out, out_lse, as_stream(stream)),
+                  "fused decode launch");
+}
+
+cp_status cp_partial_attn_decode_mod(const cp_decode_args* a, const cp_score_mod* mod, void* stream) {
+  return decode_mod_partials(a, mod, false, stream);
+}
+cp_status cp_partial_attn_decode_q4(const cp_decode_args* a, const cp_score_mod* mod, void* stream) {
+  return decode_mod_partials(a, mod, true, stream);
+}
+cp_status cp_decode_attention_mod(const cp_decode_args* a, const cp_score_mod* mod, void* workspace,
+                                  size_t workspace_bytes, void* out, float* out_lse, void* stream) {
+  return decode_mod_fused(a, mod, false, workspace, workspace_bytes, out, out_lse, stream);
+}
+cp_status cp_decode_attention_q4(const cp_decode_args* a, const cp_score_mod* mod, void* workspace,
+                                 size_t workspace_bytes, void* out, float* out_lse, void* stream) {
+  return decode_mod_fused(a, mod, true, workspace, workspace_bytes, out, out_lse, stream);
+}
+
 }  // extern "C"
 
 // ------------------------------------------------------------------ helpers for other units

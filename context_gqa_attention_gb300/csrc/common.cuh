@@ -140,6 +140,15 @@ inline size_t cp_decode_ws_layout(int B, int Hq, int Hkv, int d, int P, size_t* 
 cudaError_t cp_launch_decode_fused(const cp_decode_args& a, float scale, const CpDecodeWorkspace& ws,
                                    void* out, float* out_lse, cudaStream_t s);
 
+// ws: the fused call's scratch, NULL for partials (a.out / a.lse); out / out_lse: the fused result
+cudaError_t cp_launch_decode_mod(const cp_decode_args& a, const cp_score_mod& mod, bool q4, float scale,
+                                 const CpDecodeWorkspace* ws, void* out, float* out_lse,
+                                 cudaStream_t s);
+cudaError_t cp_launch_prefill_mod(const cp_prefill_args& a, const cp_score_mod& mod, float scale, void* out,
+                                  float* out_lse, cudaStream_t s);
+cudaError_t cp_launch_rope_write(const cp_rope_write_args& a, cudaStream_t s);
+cudaError_t cp_launch_kv_read(const cp_kv_read_args& a, cudaStream_t s);
+
 // Host helpers exported by api.cu for entry points defined in other translation units.
 cp_status cp_check_decode_args_for_fused(const cp_decode_args* a, const void* out);
 cp_status cp_fail_detail(cp_status st, const char* fmt, ...);

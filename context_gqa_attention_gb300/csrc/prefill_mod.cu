@@ -1,0 +1,730 @@
+// Prefill attention with modified scores (cp_attn_prefill_mod) on the 5th-generation tensor cores:
+// bf16 in, f32 accumulate, contiguous K / V.
+//
+// "Add utility functions to enable pass-kv prefill and allgather decode" (vLLM PR 26059),
+// Purpose: pass-KV prefill and the combination of a Q row's partials (folded in: no partials).
+//
+//   s_ij = scale q_i.k_j;  s_ij = cap tanh(s_ij / cap);  s_ij -= slope |i - j|   (each optional)
+//   out_i = softmax over the keys j in [lo_i, hi_i) of s_ij, times V
+//
+// One CTA works on two "tiles" of 128 query rows that share every K / V tile of 128 keys: two
+// query heads of a kv group (even group), or two consecutive row tiles of one head.  Warps:
+//   0     TMA producer: both Q tiles once, then K and V tiles through a 4-slot ring
+//   1     TMEM owner and MMA issuer (one thread): S = Q K^T into the tile's TMEM columns, then
+//         O += P V with P read from TMEM; order PV0(t) | QK0(t+1) | PV1(t) | QK1(t+1), so a tile's
+//         softmax overlaps the other tile's two MMAs
+//   2-3   V guards: in a key tile that some row sees only in part they clear what must not reach
+//         the MMA (0 times an infinity is NaN), see below
+//   4-11  two softmax warpgroups, one thread per query row
+// The keys a CTA walks are the union [key_lo, key_hi) of its rows' ranges, so windows and short
+// documents load their own keys only; tiles start at key_lo, not at a multiple of 128.
+//
+// Bound: the softmax warps' instruction issue (2 x 128 x 128 scores per key tile) against the
+// tensor pipe's 16.8 MFLOP per key tile.  The cap is therefore a polynomial on the packed fp32
+// pipe wherever a warp's scores allow it (tanh(y) / y in y^2, own least-maximum fits), and only
+// else 1 - 2 / (1 + e^2y), whose two special-function operations per score would bound the kernel.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+
+namespace cpattn {
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128;  // query rows per tile (TMEM lanes)
+constexpr int BN = 128;  // keys per tile
+constexpr int kThreads = 384;
+constexpr int kSlots = 4;                    // K / V ring
+constexpr int kRegsProducer = 88, kRegsSoftmax = 208;
+constexpr int kRegsLaunch = 168;             // registers a thread of the 384-thread launch
+static_assert(kRegsProducer + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register budgets exceed the launch");
+constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
+constexpr float kMaxGrowth = 8.f;            // log2 units the scores may exceed the running reference
+
+struct PrefillModParams {
+  int B, Hq, Hkv, G, Nq, window, tiles;  // tiles: row tiles (items) of the longest sequence
+  float scale_log2, softcap, cap_in;  // cap_in = scale / cap: y = cap_in q.k
+  const int32_t* cu_q;
+  const int32_t* cu_kv;  // null: the query rows
+  const int32_t* kv_start;
+  const int32_t* prefix;
+  const float* slopes;
+  const __nv_bfloat16* v;  // for the rows of a tile that held infinities or NaN
+  __nv_bfloat16* out;
+  float* lse;
+  int32_t* err;
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kQ = BM * D * 2;
+  static constexpr int kKV = BN * D * 2;
+  static constexpr int oQ = 0;
+  static constexpr int oKV = 2 * kQ;
+  static constexpr int oBar = oKV + kSlots * kKV;
+  static constexpr int bQ = 0, bFull = 1, bEmpty = bFull + kSlots, bS = bEmpty + kSlots, bP = bS + 2,
+                       bO = bP + 2, bFix = bO + 2, bDone = bFix + 2, nBar = bDone + 1;
+  static constexpr int oMisc = oBar + nBar * 8;  // TMEM base, abort flag, first / last unclean tile
+  static constexpr int kBytes = oMisc + 16;
+  // the base is rounded up to the 1 KB swizzle atom; never below 120 KB, so that one CTA (and its
+  // 512 TMEM columns) has an SM to itself
+  static constexpr int kAlloc = (kBytes + 1024) > 120 * 1024 ? (kBytes + 1024) : 120 * 1024;
+  static_assert(kAlloc <= 232448, "dynamic shared memory beyond the 227 KB per-CTA limit");
+};
+
+// ------------------------------------------------------------------------------ packed fp32
+CP_DEV uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+CP_DEV void f2u(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+CP_DEV uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+CP_DEV uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+CP_DEV uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+CP_DEV float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+CP_DEV uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A row's 128 scores: four chunks of 32 TMEM columns.
+struct Row {
+  float c[4][32];
+};
+CP_DEV float row_max(const Row& v) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], v.c[i][k], v.c[i][k + 1]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+CP_DEV float row_abs_max(const Row& v) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], fabsf(v.c[i][k]), fabsf(v.c[i][k + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// cap tanh(y) in log2 units from y = cap_in * (q.k), N + 1 coefficients of tanh(y) / y in y^2.
+template <int N>
+CP_DEV void cap_poly(Row& v, float cap_in, float cap_log2, const float (&a)[N + 1]) {
+  const uint64_t in2 = f2(cap_in, cap_in);
+  uint64_t c[N + 1];
+#pragma unroll
+  for (int i = 0; i <= N; ++i) c[i] = f2(a[i] * cap_log2, a[i] * cap_log2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const uint64_t y = fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2), u = fmul2(y, y);
+      uint64_t r = c[N];
+#pragma unroll
+      for (int j = N - 1; j >= 0; --j) r = ffma2(r, u, c[j]);
+      f2u(fmul2(r, y), v.c[i][k], v.c[i][k + 1]);
+    }
+}
+// Relative errors 5.5e-7 on |y| <= 0.5 and 6.3e-7 on |y| <= 1.25 (least-maximum fits to tanh).
+constexpr float kCapNear = 0.5f, kCapFar = 1.25f;
+CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2) {
+  const float y = row_abs_max(v) * cap_in;
+  if (__all_sync(0xffffffffu, y <= kCapNear)) {
+    const float a[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
+    cap_poly<3>(v, cap_in, cap_log2, a);
+  } else if (__all_sync(0xffffffffu, y <= kCapFar)) {
+    const float a[7] = {0.9999994039535522f, -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
+                        0.018229125067591667f, -0.004626906011253595f, 0.0005844940315000713f};
+    cap_poly<6>(v, cap_in, cap_log2, a);
+  } else {  // 1 - 2 / (1 + e^2y): absolute error about 2^-22
+    const float in = 2.f * kLog2e * cap_in;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        v.c[i][k] = cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(v.c[i][k] * in));
+  }
+}
+
+// P = 2^(x - ref) of 32 columns, packed as bf16 pairs over the row's own S columns in TMEM (the A
+// operand of the PV MMA; bf16 is the tensor core's operand type), the sum kept in fp32.
+CP_DEV void exp_chunk(float (&a)[32], uint64_t sc2, uint64_t n2, uint64_t& sum2, uint32_t taddr) {
+  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+  uint32_t pk[16];
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    float x, y;
+    f2u(ffma2(f2(a[k], a[k + 1]), sc2, n2), x, y);
+    x = ex2(x);
+    y = ex2(y);
+    acc[(k >> 1) & 3] = fadd2(acc[(k >> 1) & 3], f2(x, y));
+    pk[k >> 1] = pack_bf16(x, y);
+  }
+  sum2 = fadd2(sum2, fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])));
+  tmem_st16(taddr, pk);
+}
+
+// O row *= alpha in TMEM (nothing to do when no lane of the warp needs it).
+template <int D>
+CP_DEV void rescale_o(uint32_t tO, float alpha) {
+  if (!__any_sync(0xffffffffu, alpha != 1.f)) return;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    tmem_ld32(tO + c * 32, o);
+    tmem_wait_ld(o);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] *= alpha;
+    tmem_st32(tO + c * 32, o);
+  }
+  tmem_wait_st();
+}
+
+// ------------------------------------------------------------------------------ V guard
+// 0 times an infinity or a NaN is NaN, so such a V element must not meet a row that does not see
+// its key.  In a key tile that some row of the CTA sees only in part, the two guard warps clear
+// the V rows behind the last key that any row sees (another sequence's tokens, or anything behind
+// the last sequence), and in the others every element that is not finite; they say whether there
+// was one, and the rows that do see it add it back at the end (see restore).
+template <int D>
+CP_DEV bool guard_v(uint8_t* sv, int last, int part) {
+  bool unclean = false;
+  // 16-byte vectors of the tile's two (one) 64-column blocks, 128 rows of 128 bytes each; the
+  // swizzle only permutes the vectors within a row
+  constexpr int kVec = BN * D * 2 / 16;
+#pragma unroll 4
+  for (int i = part; i < kVec; i += 64) {
+    const int row = (i >> 3) & (BN - 1);
+    uint4* p = reinterpret_cast<uint4*>(sv) + i;
+    if (row >= last) {
+      *p = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    uint4 x = *p;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+    uint32_t any = 0;
+    // exponent of all ones: adding one to it carries into the sign's place
+#pragma unroll
+    for (int e = 0; e < 4; ++e) any |= ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    if (any != 0u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t bad = ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        w[e] &= ~((bad >> 15) * 0xffffu);  // 0xffff in each half that is not finite
+      }
+      *p = x;
+      unclean = true;
+    }
+  }
+  return unclean;
+}
+
+// What the guard took out of V for a row that sees it: p > 0 times an infinity or a NaN is that
+// infinity or NaN, whatever p is.  Rare and slow: the row's keys within the unclean tiles.
+template <int D>
+CP_DEV void restore(float (&o)[32], const __nv_bfloat16* v, long long stride, int col, int k0, int k1) {
+  for (int j = k0; j < k1; ++j)
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float x = __bfloat162float(v[(long long)j * stride + col + k]);
+      if (!isfinite(x)) o[k] += x;
+    }
+}
+
+// ------------------------------------------------------------------------------ kernel
+template <int D, bool TT>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_mod_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const PrefillModParams p) {
+  using Sm = Smem<D>;
+  constexpr int KB = D / 64;
+  constexpr int SPAN = TT ? 2 * BM : BM;  // query rows of an item
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_range[kThreads / 32][4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- the item: heads fastest, then row tiles (the last, longest one first), then sequences
+  const int h0 = blockIdx.x * (TT ? 1 : 2), b = blockIdx.z;
+  const int q0 = __ldg(p.cu_q + b), Tq = __ldg(p.cu_q + b + 1) - q0;
+  const int q_lo = (p.tiles - 1 - (int)blockIdx.y) * SPAN;
+  if (q_lo >= Tq) return;
+  const int q_hi = min(q_lo + SPAN, Tq);
+  int kv0 = q0, Tkv = Tq;
+  if (p.cu_kv != nullptr) {
+    kv0 = __ldg(p.cu_kv + b);
+    Tkv = __ldg(p.cu_kv + b + 1) - kv0;
+  }
+  const int C = Tkv - Tq;  // cached tokens before the new ones
+  if (C < 0) {             // fewer kv tokens than new queries: flagged, the item is skipped
+    if (threadIdx.x == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  const int pre = p.prefix != nullptr ? min(__ldg(p.prefix + b), Tkv) : 0;
+  // keys [lo, hi) of a row of the sequence
+  auto lo_of = [&](int row) -> int {
+    int lo = 0;
+    if (p.window > 0 && C + row >= p.window) lo = C + row - p.window + 1;
+    if (p.kv_start != nullptr) lo = max(lo, __ldg(p.kv_start + q0 + row));
+    return min(lo, Tkv);
+  };
+  auto hi_of = [&](int row) -> int { return max(C + row + 1, pre); };
+  // union of the rows' ranges and the range that every row sees
+  int key_lo, key_hi, all_lo, all_hi;
+  if (p.kv_start == nullptr) {
+    key_lo = lo_of(q_lo);
+    key_hi = hi_of(q_hi - 1);
+    all_lo = lo_of(q_hi - 1);
+    all_hi = hi_of(q_lo);
+    if (q_hi - q_lo < SPAN) all_hi = -1;  // rows past the sequence see nothing
+  } else {
+    int v[4] = {0x7fffffff, 0, 0, 0x7fffffff};
+    for (int i = threadIdx.x; i < SPAN; i += kThreads) {
+      const int row = q_lo + i;
+      const int lo = row < q_hi ? lo_of(row) : 1, hi = row < q_hi ? hi_of(row) : 0;
+      if (lo < hi) {
+        v[0] = min(v[0], lo);
+        v[1] = max(v[1], hi);
+        v[2] = max(v[2], lo);
+        v[3] = min(v[3], hi);
+      } else {  // a row without keys: no tile is seen by every row
+        v[3] = -1;
+      }
+    }
+    v[0] = __reduce_min_sync(0xffffffffu, v[0]);
+    v[1] = __reduce_max_sync(0xffffffffu, v[1]);
+    v[2] = __reduce_max_sync(0xffffffffu, v[2]);
+    v[3] = __reduce_min_sync(0xffffffffu, v[3]);
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_range[warp][i] = v[i];
+    }
+    __syncthreads();
+    key_lo = 0x7fffffff, key_hi = 0, all_lo = 0, all_hi = 0x7fffffff;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      key_lo = min(key_lo, s_range[w][0]);
+      key_hi = max(key_hi, s_range[w][1]);
+      all_lo = max(all_lo, s_range[w][2]);
+      all_hi = min(all_hi, s_range[w][3]);
+    }
+  }
+  const int ntiles = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
+  auto in_part = [&](int t) -> bool {  // some row of the CTA sees only a part of key tile t
+    const int k0 = key_lo + t * BN;
+    return k0 < all_lo || k0 + BN > all_hi;
+  };
+
+  if (ntiles == 0) {  // no row sees a key
+    for (int i = threadIdx.x; i < (q_hi - q_lo) * (TT ? 1 : 2); i += kThreads) {
+      const long long row = (long long)(q0 + q_lo + (TT ? i : i >> 1)) * p.Hq + h0 + (TT ? 0 : i & 1);
+      for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(p.out + row * D + c) = make_uint4(0u, 0u, 0u, 0u);
+      p.lse[row] = -INFINITY;
+    }
+    return;
+  }
+
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base - raw);
+  const uint32_t sQ = base + Sm::oQ, sKV = base + Sm::oKV;
+  auto bar = [&](int i) -> uint32_t { return base + (uint32_t)Sm::oBar + 8u * (uint32_t)i; };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sbase + Sm::oMisc);
+  volatile uint32_t* abort_flag = misc + 1;
+  int* unclean = reinterpret_cast<int*>(misc + 2);  // first, last key tile whose V was unclean
+  auto fail = [&]() {
+    *abort_flag = 1u;
+    report(p.err, CP_ERR_TIMEOUT);
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(Sm::bQ), 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar(Sm::bFull + s), 1);
+      mbar_init(bar(Sm::bEmpty + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Sm::bS + i), 1);
+      mbar_init(bar(Sm::bP + i), 4);
+      mbar_init(bar(Sm::bO + i), 1);
+      mbar_init(bar(Sm::bFix + i), 2);
+    }
+    mbar_init(bar(Sm::bDone), 1);
+    misc[1] = 0u;
+    unclean[0] = 0x7fffffff;
+    unclean[1] = -1;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_q);
+    mbar_expect_tx(bar(Sm::bQ), 2 * Sm::kQ);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        tma_load_2d(sQ + i * Sm::kQ + kb * BM * 128, &map_q, (h0 + (TT ? 0 : i)) * D + kb * 64,
+                    q0 + q_lo + (TT ? i * BM : 0), bar(Sm::bQ));
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(misc), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const int g = h0 / p.G;
+
+  if (warp < 4) {
+    regs_dec<kRegsProducer>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+        bool ok = true;
+        int issued = 0;  // ring fills: K(t) is fill 2 t, V(t) fill 2 t + 1
+        for (int i = 0; i < 2 * ntiles; ++i) {
+          const int slot = i % kSlots;
+          if (!mbar_wait(bar(Sm::bEmpty + slot), ((uint32_t)(i / kSlots) & 1u) ^ 1u, abort_flag, kBudget)) {
+            ok = false;
+            break;
+          }
+          const CUtensorMap* map = (i & 1) ? &map_v : &map_k;
+          mbar_expect_tx(bar(Sm::bFull + slot), Sm::kKV);
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+            tma_load_2d(sKV + slot * Sm::kKV + kb * BN * 128, map, g * D + kb * 64, kv0 + key_lo + (i >> 1) * BN,
+                        bar(Sm::bFull + slot));
+          issued = i + 1;
+        }
+        if (!ok) fail();
+        // every copy issued into this CTA's shared memory has landed before it exits
+        mbar_wait(bar(Sm::bQ), 0u, nullptr, kBudget);
+        for (int i = max(0, issued - kSlots); i < issued; ++i)
+          mbar_wait(bar(Sm::bFull + i % kSlots), (uint32_t)(i / kSlots) & 1u, nullptr, kBudget);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        const uint32_t id_qk = idesc_bf16_f32(BM, BN, false, false);
+        const uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
+        // descriptors built once and advanced: this thread is on the critical path
+        const uint64_t dq0 = desc_sw128(sQ, 16, 1024);
+        const uint64_t dk0 = desc_sw128(sKV, 16, 1024);
+        const uint64_t dv0 = desc_sw128(sKV, BN * 128, 1024);
+        auto issue_qk = [&](int tile, int slot) {
+          const uint64_t dq = desc_advance(dq0, (uint32_t)(tile * Sm::kQ));
+          const uint64_t dk = desc_advance(dk0, (uint32_t)(slot * Sm::kKV));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (BM * 128) + (kk % 4) * 32;
+            mma_ss(tmem + (uint32_t)(tile * BN), desc_advance(dq, off), desc_advance(dk, off), id_qk, kk > 0);
+          }
+        };
+        auto issue_pv = [&](int tile, int slot, bool acc) {
+          const uint64_t dv = desc_advance(dv0, (uint32_t)(slot * Sm::kKV));
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + 256u + (uint32_t)(tile * D), tmem + (uint32_t)(tile * BN + kk * 8),
+                   desc_advance(dv, kk * 16u * 128u), id_pv, acc || kk > 0);
+        };
+        bool ok = mbar_wait(bar(Sm::bQ), 0u, abort_flag, kBudget) &&
+                  mbar_wait(bar(Sm::bFull), 0u, abort_flag, kBudget);
+        if (ok) {
+          tc_fence_after();
+          issue_qk(0, 0);
+          mma_commit(bar(Sm::bS + 0));
+          issue_qk(1, 0);
+          mma_commit(bar(Sm::bS + 1));
+          mma_commit(bar(Sm::bEmpty + 0));
+        }
+        for (int t = 0; ok && t < ntiles; ++t) {
+          const int iv = 2 * t + 1, ik = 2 * t + 2, sv = iv % kSlots, sk = ik % kSlots;
+          // V(t) as the guards leave it (they have seen it land)
+          ok = mbar_wait(bar(Sm::bFix + (t & 1)), (uint32_t)(t >> 1) & 1u, abort_flag, kBudget) &&
+               mbar_wait(bar(Sm::bFull + sv), (uint32_t)(iv / kSlots) & 1u, abort_flag, kBudget);
+          if (!ok) break;
+          ok = mbar_wait(bar(Sm::bP + 0), (uint32_t)t & 1u, abort_flag, kBudget);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(0, sv, t > 0);
+          mma_commit(bar(Sm::bO + 0));
+          const bool more = t + 1 < ntiles;
+          if (more) {
+            ok = mbar_wait(bar(Sm::bFull + sk), (uint32_t)(ik / kSlots) & 1u, abort_flag, kBudget);
+            if (!ok) break;
+            tc_fence_after();
+            issue_qk(0, sk);
+            mma_commit(bar(Sm::bS + 0));
+          }
+          ok = mbar_wait(bar(Sm::bP + 1), (uint32_t)t & 1u, abort_flag, kBudget);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(1, sv, t > 0);
+          mma_commit(bar(Sm::bO + 1));
+          mma_commit(bar(Sm::bEmpty + sv));
+          if (more) {
+            issue_qk(1, sk);
+            mma_commit(bar(Sm::bS + 1));
+            mma_commit(bar(Sm::bEmpty + sk));
+          }
+        }
+        if (!ok) fail();
+        // every MMA issued by this thread has retired before TMEM is released
+        mma_commit(bar(Sm::bDone));
+        mbar_wait(bar(Sm::bDone), 0u, nullptr, kBudget);
+      }
+    } else {
+      // ---------------------------------------------------------------- V guards
+      // every tile, in step with the MMA issuer: a barrier's phases are told apart by parity alone
+      for (int t = 0; t < ntiles; ++t) {
+        const int iv = 2 * t + 1, sv = iv % kSlots;
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bFull + sv), (uint32_t)(iv / kSlots) & 1u,
+                                                          abort_flag, kBudget));
+        if (!ok) {
+          if (lane == 0) fail();
+          break;
+        }
+        if (in_part(t)) {
+          if (guard_v<D>(sbase + Sm::oKV + sv * Sm::kKV, key_hi - key_lo - t * BN, (warp - 2) * 32 + lane)) {
+            atomicMin(unclean, t);
+            atomicMax(unclean + 1, t);
+          }
+          fence_proxy_async_smem();  // the MMA reads what was written here
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Sm::bFix + (t & 1)));
+      }
+    }
+  } else {
+    regs_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------------ softmax, one WG per tile
+    const int tile = (warp - 4) >> 2, q4 = warp & 3;
+    const int row = q_lo + (TT ? tile * BM : 0) + q4 * 32 + lane;  // within the sequence
+    const int head = h0 + (TT ? 0 : tile);
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = tmem + lane_off + (uint32_t)(tile * BN);
+    const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(tile * D);
+    const bool valid = row < q_hi;
+    const int lo = valid ? lo_of(row) : 0, hi = valid ? hi_of(row) : 0;
+    const bool cap = p.softcap > 0.f;
+    const float cap_log2 = p.softcap * kLog2e;
+    const bool biased = p.slopes != nullptr;
+    const float slope = biased ? __ldg(p.slopes + head) * kLog2e : 0.f;
+    // scores come out of cap and bias in log2 units; untouched ones are scaled within the exponent
+    const float sc = cap || biased ? 1.f : p.scale_log2;
+    const uint64_t sc2 = f2(sc, sc);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int t = 0; t < ntiles; ++t) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
+      if (!ok) break;
+      tc_fence_after();
+      Row v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, v.c[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_wait_ld(v.c[i]);
+      const int k0 = key_lo + t * BN;
+      if (cap) cap_scores(v, p.cap_in, cap_log2);
+      if (biased) {
+        const float s0 = cap ? 1.f : p.scale_log2;
+        const int far = k0 + BN - 1 - (C + row);  // > 0: keys behind the query in this tile
+        if (__any_sync(0xffffffffu, far > 0 && hi > C + row + 1 && k0 < hi)) {
+          const float d0 = (float)(k0 - (C + row));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              v.c[i][k] = fmaf(-slope, fabsf(d0 + (float)(32 * i + k)), v.c[i][k] * s0);
+        } else {  // every visible key is at or before the query: the bias is linear in the column
+          const uint64_t sl2 = f2(slope, slope), s02 = f2(s0, s0);
+          const float b0 = slope * (float)(k0 - (C + row));
+          const uint64_t b2 = f2(b0, b0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const uint64_t bias = ffma2(sl2, f2((float)(32 * i + k), (float)(32 * i + k + 1)), b2);
+              f2u(ffma2(f2(v.c[i][k], v.c[i][k + 1]), s02, bias), v.c[i][k], v.c[i][k + 1]);
+            }
+        }
+      }
+      const int c0 = lo - k0, c1 = hi - k0;  // visible columns [c0, c1)
+      if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= BN)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            v.c[i][k] = 32 * i + k >= c0 && 32 * i + k < c1 ? v.c[i][k] : -INFINITY;
+      }
+      const float mt = row_max(v) * sc;
+      float alpha = 1.f;
+      if (mt > m + kMaxGrowth) {  // the first visible tile, or the scores grew a lot
+        alpha = ex2(m - mt);
+        m = mt;
+      }
+      const float neg = m == -INFINITY ? 0.f : -m;
+      const uint64_t n2 = f2(neg, neg);
+      uint64_t sum2 = f2(0.f, 0.f);
+      // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S
+      // columns may take P(t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) exp_chunk(v.c[i], sc2, n2, sum2, tS + 16 * i);
+      tmem_wait_st();
+      float s_lo, s_hi;
+      f2u(sum2, s_lo, s_hi);
+      l = l * alpha + (s_lo + s_hi);
+      if (t > 0) rescale_o<D>(tO, alpha);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Sm::bP + tile));
+    }
+    if (ok)
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait(bar(Sm::bO + tile), (uint32_t)(ntiles - 1) & 1u, abort_flag, kBudget));
+    if (ok) {
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const long long orow = (long long)(q0 + row) * p.Hq + head;
+      // keys of this row within the tiles whose V the guards changed (none, nearly always)
+      const int u0 = *(volatile int*)unclean, u1 = *(volatile int*)(unclean + 1);
+      const int r0 = u1 < 0 ? 0 : max(lo, key_lo + u0 * BN), r1 = u1 < 0 ? 0 : min(hi, key_lo + (u1 + 1) * BN);
+      const bool whole = row - lane + 32 <= q_hi;  // all 32 rows of this warp are real
+      // whole warps stage their rows in shared memory (tile 0 over the Q tiles, free since its last
+      // PV came after the other tile's last QK; tile 1 over the ring, its last PV being the CTA's
+      // last MMA) and write one contiguous output row per store instruction
+      const uint32_t sb = (tile == 0 ? sQ : sKV) + (uint32_t)(q4 * 32 * D * 2);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= inv;
+        if (r0 < r1) restore<D>(o, p.v + (long long)kv0 * p.Hkv * D, (long long)p.Hkv * D, g * D + c * 32, r0, r1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                     pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+          if (whole)  // 64-column boxes of 32 rows, 16-byte vectors swizzled by the row
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             sb + (uint32_t)((c >> 1) * 4096 + lane * 128) +
+                             ((uint32_t)(((c & 1) * 4 + j) ^ (lane & 7)) << 4)),
+                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                         : "memory");
+          else if (valid)
+            *reinterpret_cast<uint4*>(p.out + orow * D + c * 32 + 8 * j) = x;
+        }
+      }
+      if (whole) {
+        __syncwarp();
+        constexpr int E = D / 32;  // columns per lane
+        const int col = E * lane, cin = col % 64;
+        const uint32_t a0 = sb + (uint32_t)((col / 64) * 4096 + (cin % 8) * 2);
+        __nv_bfloat16* dst = p.out + ((long long)(q0 + row - lane) * p.Hq + head) * D + col;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+          const uint32_t a = a0 + (uint32_t)(r * 128) + ((uint32_t)((cin / 8) ^ (r & 7)) << 4);
+          __nv_bfloat16* q = dst + (long long)r * p.Hq * D;
+          if constexpr (E == 4) {
+            uint2 x;
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
+            *reinterpret_cast<uint2*>(q) = x;
+          } else {
+            uint32_t x;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
+            *reinterpret_cast<uint32_t*>(q) = x;
+          }
+        }
+      }
+      if (valid) p.lse[orow] = l == 0.f ? -INFINITY : (log2f(l) - (m == -INFINITY ? 0.f : -m)) * kLn2;
+    } else if (lane == 0) {
+      fail();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scale, void* out, float* lse,
+                   cudaStream_t s) {
+  const unsigned long long hq = (unsigned long long)a.num_q_heads * D, hkv = (unsigned long long)a.num_kv_heads * D;
+  const unsigned long long nkv = a.cu_seqlens_kv ? (unsigned long long)a.total_kv : (unsigned long long)a.total_q;
+  CUtensorMap mq, mk, mv;
+  if (!cp_make_bf16_map_2d(&mq, a.q, hq, (unsigned long long)a.total_q, hq, BM) ||
+      !cp_make_bf16_map_2d(&mk, a.k, hkv, nkv, hkv, BN) || !cp_make_bf16_map_2d(&mv, a.v, hkv, nkv, hkv, BN))
+    return cudaErrorInvalidValue;
+  PrefillModParams p;
+  p.B = a.num_seqs;
+  p.Hq = a.num_q_heads;
+  p.Hkv = a.num_kv_heads;
+  p.G = a.num_q_heads / a.num_kv_heads;
+  p.Nq = a.total_q;
+  p.window = mod.window;
+  p.scale_log2 = scale * kLog2e;
+  p.softcap = mod.softcap;
+  p.cap_in = mod.softcap > 0.f ? scale / mod.softcap : 0.f;
+  p.cu_q = a.cu_seqlens_q;
+  p.cu_kv = a.cu_seqlens_kv;
+  p.kv_start = mod.kv_start;
+  p.prefix = mod.prefix_lens;
+  p.slopes = mod.alibi_slopes;
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.err = a.err;
+  const bool tt = p.G % 2 != 0;  // odd groups: two row tiles of one head share the K / V tiles
+  const int span = tt ? 2 * BM : BM;
+  p.tiles = (a.max_seqlen_q + span - 1) / span;
+  if (p.tiles == 0) return cudaSuccess;
+  if (p.tiles > 65535 || a.num_seqs > 65535) return cudaErrorInvalidConfiguration;
+  const dim3 grid(tt ? a.num_q_heads : a.num_q_heads / 2, p.tiles, a.num_seqs);
+  auto kern = tt ? prefill_mod_kernel<D, true> : prefill_mod_kernel<D, false>;
+  // the register budgets assume the registers a thread of this launch gets; a build that gave the
+  // kernel another count would leave an increase waiting, so refuse it
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, Smem<D>::kAlloc, s>>>(mq, mk, mv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace cpattn
+
+cudaError_t cp_launch_prefill_mod(const cp_prefill_args& a, const cp_score_mod& mod, float scale, void* out,
+                                  float* out_lse, cudaStream_t s) {
+  return a.head_dim == 64 ? cpattn::launch<64>(a, mod, scale, out, out_lse, s)
+                          : cpattn::launch<128>(a, mod, scale, out, out_lse, s);
+}

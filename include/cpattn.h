@@ -387,9 +387,178 @@ cp_status cp_lse_merge(const float* partial_out, const float* partial_lse, int32
 cp_status cp_decode_attention_noalloc(const cp_decode_args* args, void* out, float* out_lse,
                                       void* stream);
 
+/* ------------------------------------------------------------------------------
+ * The 4-bit K/V cache (no counterpart on the pages, which keep the model's type; the placement
+ * -- round-robin over the CP ranks, per-rank pools and block tables -- is theirs).
+ *
+ * k_cache, v_cache are device uint8 [cp][pool_pages][Hkv][9 d]: one record of 9 d bytes holds one
+ * kv head's 16 tokens (block_size 16, d in {64, 128}):
+ *   bytes [0, 8 d)    row t (d / 2 bytes) = token t's 4-bit codes; 32-bit word w of a row holds
+ *                     8 consecutive dims, lowest nibble first, from dim 8 w (d = 64) or
+ *                     64 (w mod 2) + 8 (w div 2) (d = 128: the two groups' words alternate);
+ *   bytes [8 d, 9 d)  per token and group of 64 dims (token-major) the bf16 pair scale, minimum.
+ * A code n stands for minimum + scale * n.  Written as: minimum = the group's least value rounded
+ * to bf16, scale = (greatest value - minimum) / 15 rounded to bf16, n = the nearest integer to
+ * (value - minimum) / scale (ties to even) within 0 .. 15, 0 where the scale is 0.  A group that
+ * holds an infinity or a NaN stands for NaN throughout.
+ * ---------------------------------------------------------------------------- */
+/* Bytes of one record (9 * head_dim). */
+int64_t cp_q4_record_bytes(int32_t head_dim);
+
+/* ------------------------------------------------------------------------------
+ * cp_rope_kv_cache_write -- append new tokens' K/V to the per-rank paged pools as
+ * cp_kv_cache_write does, with the rotary position embedding applied on the way ([PKV] Purpose:
+ * KV kept round-robin on the CP ranks; [PCP] Purpose: per-rank block tables).
+ *
+ * Row i of sequence b (token-major row cu_new[b] + i) has position p = start_pos[b] + i and angles
+ * p * inv_freq[j], j < rot_dim / 2.  Pair j of a q or k head, dims (j, j + rot_dim / 2)
+ * (CP_ROPE_HALF) or (2 j, 2 j + 1) (CP_ROPE_PAIRS), becomes (x cos - y sin, y cos + x sin); dims
+ * from rot_dim on stay.  V is not rotated.  Whole turns are dropped exactly, so far positions keep
+ * full fp32 accuracy; results are rounded once, to `dtype`, or quantised from fp32 (cache_q4).
+ * Rotated queries go to q_out; rotated keys go to the cache and, if k_out is given, there too.
+ *   - q, k, v, q_out may be rows of a wider tensor: token t starts `*_stride` elements after token
+ *     t - 1 (a fused projection's columns); the strides in bytes are multiples of 16.
+ *   - q may be NULL (no query heads to rotate); q_out may be q with the same stride (in place).
+ *     rot_dim = 0 with inv_freq NULL appends without rotating.
+ *   - rows from cu_new[B] on (a padded batch) are neither read nor written, and a row with a
+ *     negative position is skipped and reported.
+ *   - err: CP_ERR_DEVICE_BOUNDS for a row whose table entry is missing or outside the pool (its K/V
+ *     are not written).  Rows that map to the same slot race.
+ * ---------------------------------------------------------------------------- */
+typedef enum { CP_ROPE_HALF = 0, CP_ROPE_PAIRS = 1 } cp_rope_style;
+typedef struct cp_rope_write_args {
+  int32_t dtype;                /* cp_dtype of q, k, v, q_out, k_out and (cache_q4 = 0) the caches */
+  int32_t cache_q4;             /* 1: the caches are 4-bit records                      */
+  int32_t num_seqs;             /* B                                                    */
+  int32_t total_new;            /* rows of k and v (>= cu_new[B])                       */
+  int32_t num_q_heads;          /* heads of q (ignored without q)                       */
+  int32_t num_kv_heads;         /* Hkv                                                  */
+  int32_t head_dim;             /* d in {64, 128}                                       */
+  int32_t cp;                   /* logical ranks, 1..64                                 */
+  int32_t interleave;           /* I >= 1                                               */
+  int32_t block_size;           /* 16                                                   */
+  int32_t max_blocks;           /* columns of block_tables                              */
+  int32_t rope_style;           /* cp_rope_style                                        */
+  int32_t rot_dim;              /* multiple of 16 in [0, d]                             */
+  int32_t reserved;             /* 0                                                    */
+  int64_t pool_pages;           /* pages in each rank's pool                            */
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  /* elements between tokens       */
+  const void* q;                /* device [N][num_q_heads][d] or NULL                   */
+  const void* k;                /* device [N][Hkv][d]                                   */
+  const void* v;                /* device [N][Hkv][d]                                   */
+  const int32_t* cu_new;        /* device [B+1]                                         */
+  const int32_t* start_pos;     /* device [B]                                           */
+  const double* inv_freq;       /* device [rot_dim / 2], radians per position           */
+  const int32_t* block_tables;  /* device [cp][B][max_blocks]                           */
+  void* k_cache;                /* device [cp][pool_pages][Hkv][16][d], or 4-bit records */
+  void* v_cache;
+  void* q_out;                  /* device [N][num_q_heads][d] (with q)                  */
+  void* k_out;                  /* device [N][Hkv][d] dense, or NULL                    */
+  int32_t* err;                 /* device int32 or NULL                                 */
+} cp_rope_write_args;
+
+cp_status cp_rope_kv_cache_write(const cp_rope_write_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * cp_kv_cache_read -- positions of the paged round-robin cache back to contiguous rows: the K/V of
+ * a PASS_KV prefill over a cached context (cu_seqlens_kv), whatever the cache holds them as.
+ *
+ * Row cu_out[b] + i of k_out / v_out ([N][Hkv][d]) becomes position start_pos[b] + i of sequence b.
+ *   cache_q4 = 0: the caches hold out_dtype and rows are copied bit for bit;
+ *   cache_q4 = 1: 4-bit records; values minimum + scale * n in fp32, rounded to out_dtype.
+ * Rows from cu_out[B] on are left as they are; a row whose position is negative or has no page in
+ * the pool is reported in err (CP_ERR_DEVICE_BOUNDS) and left as it is.  Positions the cache was
+ * never written at give whatever lies there.
+ * ---------------------------------------------------------------------------- */
+typedef struct cp_kv_read_args {
+  int32_t out_dtype;            /* cp_dtype of k_out, v_out                             */
+  int32_t cache_q4;             /* 1: the caches are 4-bit records                      */
+  int32_t num_seqs;             /* B                                                    */
+  int32_t total;                /* rows of k_out and v_out                              */
+  int32_t num_kv_heads;         /* Hkv                                                  */
+  int32_t head_dim;             /* d in {64, 128}                                       */
+  int32_t cp;                   /* logical ranks, 1..64                                 */
+  int32_t interleave;           /* I >= 1                                               */
+  int32_t block_size;           /* 16                                                   */
+  int32_t max_blocks;           /* columns of block_tables                              */
+  int64_t pool_pages;           /* pages in each rank's pool                            */
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;  /* device [cp][B][max_blocks]                           */
+  const int32_t* cu_out;        /* device [B+1]                                         */
+  const int32_t* start_pos;     /* device [B]                                           */
+  void* k_out;                  /* device [N][Hkv][d]                                   */
+  void* v_out;
+  int32_t* err;                 /* device int32 or NULL                                 */
+} cp_kv_read_args;
+
+cp_status cp_kv_cache_read(const cp_kv_read_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Modified attention scores.  For a query at position i and a key at position j
+ *   s = softmax_scale q.k;
+ *   s = softcap * tanh(s / softcap)                  if softcap > 0;
+ *   s = s - alibi_slopes[h] * |i - j|                if alibi_slopes;
+ * over the keys j in [lo, hi):
+ *   lo = max(0, i - window + 1 if window > 0, kv_start of the row if given),
+ *   hi = i + 1, or the sequence's prefix length (at most its kv length) where that is larger.
+ * So `window` keys up to and with the query's own are seen; kv_start gives each row the first
+ * position of its document in a packed sequence; keys of the prefix are seen by every query.
+ * A row without a key (lo >= hi) gives output 0 and LSE -inf.  Keys a row does not see do not
+ * touch it, whatever they hold.
+ * ---------------------------------------------------------------------------- */
+typedef struct cp_score_mod {
+  float softcap;                /* 0: none; finite, >= 0                                */
+  int32_t window;               /* 0: none                                              */
+  const float* alibi_slopes;    /* device f32 [Hq] or NULL                              */
+  const int32_t* kv_start;      /* device: decode [B], prefill [Nq] (token-major); or NULL */
+  const int32_t* prefix_lens;   /* device [B] or NULL; prefill only                     */
+} cp_score_mod;
+
+/* ------------------------------------------------------------------------------
+ * cp_attn_prefill_mod -- cp_attn_prefill_fused (CP_PASS_KV: contiguous k / v, optionally over a
+ * cached context through cu_seqlens_kv) with modified scores; `mod` may be NULL (none).  bf16,
+ * d in {64, 128}, any ratio of query to kv heads; mode must be CP_PASS_KV and impl CP_IMPL_AUTO or
+ * CP_IMPL_TCGEN05.  The result does not depend on args->cp (no partials are made).  Only the key
+ * tiles some row of a query tile sees are loaded, so a window or short documents cost their own
+ * keys.  args->out / args->lse are not used; args->err takes device-side errors.
+ *   out      device bf16 [Nq][Hq][d];  out_lse  device f32 [Nq][Hq] (natural log).
+ * Rows from cu_seqlens_q[B] on are left as they are.
+ * ---------------------------------------------------------------------------- */
+cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* mod, void* out,
+                              float* out_lse, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Decode with modified scores (cp_partial_attn_decode_mod, cp_decode_attention_mod) and over the
+ * 4-bit cache (cp_partial_attn_decode_q4, cp_decode_attention_q4; their args->dtype, the type of q
+ * and out, is CP_BF16).  Arguments as in cp_partial_attn_decode / cp_decode_attention plus `mod`
+ * (NULL: none; prefix_lens must be NULL: a prefix is behind the query here).
+ *
+ * Splits are counted within the visible tokens: split s of a rank covers split_tokens local tokens
+ * from s * split_tokens past the page of the first visible one, so a window needs splits for its
+ * own tokens only.  cp_decode_mod_plan picks num_splits and split_tokens to cover max_seq_len
+ * tokens (the window, if one is given and smaller) with cp * num_splits <= 256; a plan too small
+ * for a sequence is reported in err (CP_ERR_DEVICE_BOUNDS).  A sequence without a visible token
+ * gives output 0 and LSE -inf (partials: all empty).
+ * The fused calls take the workspace of cp_decode_attention (cp_decode_workspace_size, zero-filled
+ * before its first use and left reusable); calls that use one workspace must not overlap.
+ * ---------------------------------------------------------------------------- */
+cp_status cp_decode_mod_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t cp, int32_t interleave,
+                             int32_t max_seq_len, int32_t window, int32_t q4, int32_t* num_splits,
+                             int32_t* split_tokens);
+cp_status cp_partial_attn_decode_mod(const cp_decode_args* args, const cp_score_mod* mod, void* stream);
+cp_status cp_decode_attention_mod(const cp_decode_args* args, const cp_score_mod* mod, void* workspace,
+                                  size_t workspace_bytes, void* out, float* out_lse, void* stream);
+cp_status cp_partial_attn_decode_q4(const cp_decode_args* args, const cp_score_mod* mod, void* stream);
+cp_status cp_decode_attention_q4(const cp_decode_args* args, const cp_score_mod* mod, void* workspace,
+                                 size_t workspace_bytes, void* out, float* out_lse, void* stream);
+
 /* sizeof() of the argument structs, so bindings can check their mirror. */
 size_t cp_prefill_args_size(void);
 size_t cp_decode_args_size(void);
+size_t cp_rope_write_args_size(void);
+size_t cp_kv_read_args_size(void);
+size_t cp_score_mod_size(void);
 
 #ifdef __cplusplus
 }
