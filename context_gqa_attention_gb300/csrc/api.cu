@@ -862,7 +862,7 @@ cp_status cp_decode_mod_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t cp,
   }
   // Tokens per CTA: about `most`, fewer where that would leave SMs without work, and no fewer than
   // a page for each of its four warps.
-  const long long most = q4 ? 2048 : 2048, least = 4 * page;
+  const long long most = q4 ? 4096 : 2048, least = 4 * page;
   const long long base = (long long)num_seqs * num_kv_heads * cp;
   long long S = (share + most - 1) / most;
   const long long want = (8ll * 152 + base - 1) / base;
@@ -887,8 +887,8 @@ static cp_status decode_mod_partials(const cp_decode_args* a, const cp_score_mod
   st = check_mod(mod, false);
   if (st != CP_OK) return st;
   const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / sqrtf((float)a->head_dim);
-  return launched(cp_launch_decode_mod(*a, *mod, q4, scale, nullptr, nullptr, nullptr, as_stream(stream)),
-                  "decode launch");
+  const auto go = q4 ? cp_launch_decode_q4 : cp_launch_decode_mod;
+  return launched(go(*a, *mod, scale, nullptr, nullptr, nullptr, as_stream(stream)), "decode launch");
 }
 
 static cp_status decode_mod_fused(const cp_decode_args* a, const cp_score_mod* mod, bool q4, void* workspace,
@@ -915,8 +915,8 @@ static cp_status decode_mod_fused(const cp_decode_args* a, const cp_score_mod* m
   ws.partial_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + ol);
   ws.partial_out = reinterpret_cast<float*>(static_cast<char*>(workspace) + oo);
   const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / sqrtf((float)a->head_dim);
-  return launched(cp_launch_decode_mod(*a, *mod, q4, scale, &ws, out, out_lse, as_stream(stream)),
-                  "fused decode launch");
+  const auto go = q4 ? cp_launch_decode_q4 : cp_launch_decode_mod;
+  return launched(go(*a, *mod, scale, &ws, out, out_lse, as_stream(stream)), "fused decode launch");
 }
 
 cp_status cp_partial_attn_decode_mod(const cp_decode_args* a, const cp_score_mod* mod, void* stream) {

@@ -141,9 +141,10 @@ cudaError_t cp_launch_decode_fused(const cp_decode_args& a, float scale, const C
                                    void* out, float* out_lse, cudaStream_t s);
 
 // ws: the fused call's scratch, NULL for partials (a.out / a.lse); out / out_lse: the fused result
-cudaError_t cp_launch_decode_mod(const cp_decode_args& a, const cp_score_mod& mod, bool q4, float scale,
-                                 const CpDecodeWorkspace* ws, void* out, float* out_lse,
-                                 cudaStream_t s);
+cudaError_t cp_launch_decode_mod(const cp_decode_args& a, const cp_score_mod& mod, float scale,
+                                 const CpDecodeWorkspace* ws, void* out, float* out_lse, cudaStream_t s);
+cudaError_t cp_launch_decode_q4(const cp_decode_args& a, const cp_score_mod& mod, float scale,
+                                const CpDecodeWorkspace* ws, void* out, float* out_lse, cudaStream_t s);
 cudaError_t cp_launch_prefill_mod(const cp_prefill_args& a, const cp_score_mod& mod, float scale, void* out,
                                   float* out_lse, cudaStream_t s);
 cudaError_t cp_launch_rope_write(const cp_rope_write_args& a, cudaStream_t s);

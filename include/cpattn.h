@@ -397,7 +397,7 @@ cp_status cp_decode_attention_noalloc(const cp_decode_args* args, void* out, flo
  *                     8 consecutive dims, lowest nibble first, from dim 8 w (d = 64) or
  *                     64 (w mod 2) + 8 (w div 2) (d = 128: the two groups' words alternate);
  *   bytes [8 d, 9 d)  per token and group of 64 dims (token-major) the bf16 pair scale, minimum.
- * A code n stands for minimum + scale * n.  Written as: minimum = the group's least value rounded
+ * A code n stands for minimum + scale * n, scale >= 0.  Written as: minimum = the group's least value rounded
  * to bf16, scale = (greatest value - minimum) / 15 rounded to bf16, n = the nearest integer to
  * (value - minimum) / scale (ties to even) within 0 .. 15, 0 where the scale is 0.  A group that
  * holds an infinity or a NaN stands for NaN throughout.
