@@ -194,14 +194,21 @@ def _check(st):
         raise CPError(st, buf.value.decode(errors="replace"))
 
 
+# the current stream's handle and device without the objects around them (torch.cuda's own functions
+# cost a few microseconds a call, as much as a small launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 _CALL = threading.local()
@@ -215,10 +222,13 @@ def _on_first_tensors_device(fn):
     def wrapper(first, *args, **kwargs):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise CPError(1, f"{fn.__name__}: the first argument must be a CUDA tensor")
+        device = first.device
         prev = getattr(_CALL, "device", None)
-        _CALL.device = first.device
+        _CALL.device = device
         try:
-            with torch.cuda.device(first.device):
+            if device.index == torch.cuda.current_device():
+                return fn(first, *args, **kwargs)
+            with torch.cuda.device(device):
                 return fn(first, *args, **kwargs)
         finally:
             _CALL.device = prev
@@ -617,7 +627,7 @@ def cp_q4_record_bytes(head_dim):
 
 
 def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise CPError(1, f"{name} must be {list(shape)} (got {list(t.shape)})")
 
 
@@ -633,7 +643,7 @@ def _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, dtype):
     want = (cp, pool, heads, 9 * d) if q4 else (cp, pool, heads, k_cache.shape[3], d)
     _shape(k_cache, "k_cache", want)
     _shape(v_cache, "v_cache", want)
-    if block_tables.dim() != 3 or tuple(block_tables.shape[:2]) != (cp, B):
+    if block_tables.dim() != 3 or block_tables.shape[:2] != (cp, B):
         raise CPError(1, f"block_tables must be [cp, B, max_blocks] = [{cp}, {B}, ..] "
                          f"(got {list(block_tables.shape)})")
     return q4
@@ -670,37 +680,34 @@ def cp_rope_kv_cache_write(k_new, v_new, cu_new, start_pos, k_cache, v_cache, bl
     load()
     N, Hkv, d = k_new.shape
     B = cu_new.numel() - 1
-    a = RopeWriteArgs()
-    a.dtype = _cp_dtype(k_new)
-    a.k_stride = _token_rows(k_new, "k_new", k_new.dtype)
-    a.v_stride = _token_rows(v_new, "v_new", k_new.dtype)
+    k_stride = _token_rows(k_new, "k_new", k_new.dtype)
+    v_stride = _token_rows(v_new, "v_new", k_new.dtype)
     _shape(v_new, "v_new", (N, Hkv, d))
     _index(cu_new, "cu_new", B + 1)
     _index(start_pos, "start_pos", B)
-    a.cache_q4 = _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, k_new.dtype)
-    a.num_seqs, a.total_new, a.num_kv_heads, a.head_dim = B, N, Hkv, d
-    a.cp, a.interleave, a.block_size = cp, interleave, 16 if a.cache_q4 else k_cache.shape[3]
-    a.max_blocks, a.pool_pages, a.rope_style = block_tables.shape[-1], k_cache.shape[1], rope_style
+    q4 = _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, k_new.dtype)
+    rot_dim = Hq = q_stride = q_out_stride = 0
     if inv_freq is not None:
         _dev(inv_freq, "inv_freq", torch.float64)
-        a.rot_dim, a.inv_freq = 2 * inv_freq.numel(), _ptr(inv_freq)
+        rot_dim = 2 * inv_freq.numel()
     if q is not None:
-        a.q_stride, a.num_q_heads = _token_rows(q, "q", k_new.dtype), q.shape[1]
-        _shape(q, "q", (N, q.shape[1], d))
+        q_stride, Hq = _token_rows(q, "q", k_new.dtype), q.shape[1]
+        _shape(q, "q", (N, Hq, d))
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        a.q_out_stride = _token_rows(q_out, "q_out", q.dtype)
-        _shape(q_out, "q_out", q.shape)
-        a.q, a.q_out = _ptr(q), _ptr(q_out)
+            q_out = q.new_empty(q.shape)
+        q_out_stride = _token_rows(q_out, "q_out", q.dtype)
+        _shape(q_out, "q_out", (N, Hq, d))
     elif q_out is not None:
         raise CPError(1, "q_out without q")
     if k_out is not None:
         _dev(k_out, "k_out", k_new.dtype)
         _shape(k_out, "k_out", (N, Hkv, d))
-        a.k_out = _ptr(k_out)
     _dev(err, "err", torch.int32)
-    a.k, a.v, a.cu_new, a.start_pos = _ptr(k_new), _ptr(v_new), _ptr(cu_new), _ptr(start_pos)
-    a.block_tables, a.k_cache, a.v_cache, a.err = _ptr(block_tables), _ptr(k_cache), _ptr(v_cache), _ptr(err)
+    a = RopeWriteArgs(_cp_dtype(k_new), q4, B, N, Hq, Hkv, d, cp, interleave, 16 if q4 else k_cache.shape[3],
+                      block_tables.shape[2], rope_style, rot_dim, 0, k_cache.shape[1], q_stride, k_stride,
+                      v_stride, q_out_stride, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cu_new), _ptr(start_pos),
+                      _ptr(inv_freq), _ptr(block_tables), _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _ptr(k_out),
+                      _ptr(err))
     if N:
         _check(_LIB.cp_rope_kv_cache_write(ctypes.byref(a), _stream(stream)))
     return q_out, k_out
@@ -730,39 +737,29 @@ def cp_kv_cache_read(k_cache, v_cache, cu_out, start_pos, block_tables, cp, inte
     if total is None:
         total = k_out.shape[0] if k_out is not None else int(cu_out[-1].item())
     if k_out is None:
-        k_out = torch.empty(total, Hkv, d, dtype=out_dtype, device=k_cache.device)
+        k_out = k_cache.new_empty((total, Hkv, d), dtype=out_dtype)
     if v_out is None:
-        v_out = torch.empty(total, Hkv, d, dtype=out_dtype, device=k_cache.device)
+        v_out = k_cache.new_empty((total, Hkv, d), dtype=out_dtype)
     for n, t in (("k_out", k_out), ("v_out", v_out)):
         _dev(t, n, out_dtype)
         _shape(t, n, (total, Hkv, d))
-    a = KvReadArgs()
-    a.out_dtype, a.cache_q4, a.num_seqs, a.total, a.num_kv_heads, a.head_dim = (
-        _cp_dtype(k_out), q4, B, total, Hkv, d)
-    a.cp, a.interleave, a.block_size = cp, interleave, 16 if q4 else k_cache.shape[3]
-    a.max_blocks, a.pool_pages = block_tables.shape[-1], k_cache.shape[1]
-    a.k_cache, a.v_cache, a.block_tables = _ptr(k_cache), _ptr(v_cache), _ptr(block_tables)
-    a.cu_out, a.start_pos, a.k_out, a.v_out, a.err = (_ptr(cu_out), _ptr(start_pos), _ptr(k_out),
-                                                      _ptr(v_out), _ptr(err))
+    a = KvReadArgs(_cp_dtype(k_out), q4, B, total, Hkv, d, cp, interleave, 16 if q4 else k_cache.shape[3],
+                   block_tables.shape[2], k_cache.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                   _ptr(cu_out), _ptr(start_pos), _ptr(k_out), _ptr(v_out), _ptr(err))
     if total:
         _check(_LIB.cp_kv_cache_read(ctypes.byref(a), _stream(stream)))
     return k_out, v_out
 
 
 def _score_mod(Hq, softcap, window, alibi_slopes, kv_start, rows, prefix_lens=None, B=0):
-    m = ScoreMod()
-    m.softcap, m.window = softcap, window
     if alibi_slopes is not None:
         _dev(alibi_slopes, "alibi_slopes", torch.float32)
         _shape(alibi_slopes, "alibi_slopes", (Hq,))
-        m.alibi_slopes = _ptr(alibi_slopes)
     if kv_start is not None:
         _index(kv_start, "kv_start", rows)
-        m.kv_start = _ptr(kv_start)
     if prefix_lens is not None:
         _index(prefix_lens, "prefix_lens", B)
-        m.prefix_lens = _ptr(prefix_lens)
-    return m
+    return ScoreMod(softcap, window, _ptr(alibi_slopes), _ptr(kv_start), _ptr(prefix_lens))
 
 
 @_on_first_tensors_device
@@ -777,9 +774,9 @@ def cp_attn_prefill_mod(q, cu_seqlens_q, k, v, *, cu_seqlens_kv=None, softcap=0.
     Nq, Hq, d = q.shape
     B = cu_seqlens_q.numel() - 1
     if out is None:
-        out = torch.empty(Nq, Hq, d, dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty(q.shape)
     if out_lse is None:
-        out_lse = torch.empty(Nq, Hq, dtype=torch.float32, device=q.device)
+        out_lse = q.new_empty((Nq, Hq), dtype=torch.float32)
     for n, t, dt in (("q", q, torch.bfloat16), ("cu_seqlens_q", cu_seqlens_q, torch.int32),
                      ("out", out, torch.bfloat16), ("out_lse", out_lse, torch.float32),
                      ("err", err, torch.int32)):
@@ -830,13 +827,9 @@ def _decode_mod_args(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave
             max_seq_len = max(1, int(seq_lens.max().item()))
         num_splits, split_tokens = cp_decode_mod_plan(B, Hkv, cp, interleave, max_seq_len, window=window,
                                                       q4=q4)
-    a = DecodeArgs()
-    a.dtype, a.num_seqs, a.num_q_heads, a.num_kv_heads, a.head_dim = _cp_dtype(q), B, Hq, Hkv, d
-    a.cp, a.interleave, a.block_size = cp, interleave, 16 if q4 else k_cache.shape[3]
-    a.num_splits, a.split_tokens, a.softmax_scale = num_splits, split_tokens, softmax_scale
-    a.max_blocks, a.pool_pages = block_tables.shape[-1], k_cache.shape[1]
-    a.q, a.k_cache, a.v_cache = _ptr(q), _ptr(k_cache), _ptr(v_cache)
-    a.block_tables, a.seq_lens, a.err = _ptr(block_tables), _ptr(seq_lens), _ptr(err)
+    a = DecodeArgs(_cp_dtype(q), B, Hq, Hkv, d, cp, interleave, 16 if q4 else k_cache.shape[3], num_splits,
+                   split_tokens, softmax_scale, block_tables.shape[2], k_cache.shape[1], _ptr(q), _ptr(k_cache),
+                   _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens), None, None, _ptr(err))
     return a, _score_mod(Hq, softcap, window, alibi_slopes, kv_start, B)
 
 
@@ -871,9 +864,9 @@ def _fused_decode(call, q4, q, k_cache, v_cache, block_tables, seq_lens, cp, int
         need = cp_decode_workspace_size(B, Hq, a.num_kv_heads, d, cp, a.num_splits)
         workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty(B, Hq, d, dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
     if out_lse is None and want_lse:
-        out_lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        out_lse = q.new_empty((B, Hq), dtype=torch.float32)
     _dev(workspace, "workspace", torch.uint8)
     _dev(out, "out", q.dtype)
     _shape(out, "out", (B, Hq, d))

@@ -7,9 +7,9 @@
 // support" (PR 28718), Purpose: per-rank block tables.
 //
 // Both are bound by HBM: every input row is read once, every output row written once, 16 bytes a
-// thread.  A CTA owns a few consecutive tokens: it finds their sequences, positions and page slots
-// once (and, when rotating, the cosines and sines of all their angles, shared by every head) in
-// shared memory, and its threads then stream the tokens' rows.
+// thread.  A warp owns a few consecutive tokens: its lanes find their sequences, positions and page
+// slots once (and, when rotating, the cosines and sines of all their angles, shared by every head),
+// and then stream the tokens' rows.
 #include <math.h>
 
 #include "common.cuh"
@@ -19,7 +19,7 @@ namespace cpattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 64;  // tokens a CTA may own
+constexpr int kWarps = kThreads / 32;
 
 // Where a token's K and V rows live: the record index of kv head 0 (page (rank, id) of the pool
 // times the kv heads) and the row within the page; head < 0: no row to touch.
@@ -28,39 +28,50 @@ struct Slot {
   int row;
 };
 
-// Number of sequences that end at or before `row` (the sequence of `row`, or B behind the last):
-// the CTA's threads compare all ends at once, so the search costs one load latency.
-CP_DEV int cta_seq_of_row(const int32_t* __restrict__ cu, int B, int row) {
-  int n = 0;
-  for (int b0 = 0; b0 < B; b0 += kThreads) {
-    const int b = b0 + (int)threadIdx.x;
-    n += __syncthreads_count(b < B && __ldg(cu + b + 1) <= row);
+struct Placement {
+  int B, Hkv, cp, I, max_blocks;
+  long long pool;
+  const int32_t *cu, *start, *tables;
+  int32_t* err;
+};
+
+// The sequence of token row `row`, B if it lies behind the last one (the whole warp, one row a lane).
+// A few hundred sequences: the lanes compare all ends with the warp's first row at once, one load
+// latency, and each walks on from there; more: a binary search each.
+CP_DEV int seq_of(const Placement& p, int row0, int row) {
+  if (p.B > 256) {
+    const int s = seq_of_row(p.cu, p.B, row);
+    return row < __ldg(p.cu + s + 1) ? s : p.B;
   }
-  return n;
+  int s = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + (int)(threadIdx.x & 31);
+    s += __popc(__ballot_sync(0xffffffffu, b < p.B && __ldg(p.cu + b + 1) <= row0));
+  }
+  while (s < p.B && __ldg(p.cu + s + 1) <= row) ++s;
+  return s;
 }
 
-// Position and slot of token row `row` (first candidate sequence s0).  false: behind the last
-// sequence.  A position without a page (negative, past the table, an id outside the pool) is
-// reported and its slot left empty.
-CP_DEV bool locate(const int32_t* __restrict__ cu, const int32_t* __restrict__ start, int B, int s0,
-                   int row, int cp, int I, const int32_t* __restrict__ tables, int max_blocks,
-                   long long pool, int Hkv, int32_t* err, long long& pos, Slot& slot) {
+// Position and slot of token row `row`.  false: behind the last sequence.  A position without a page
+// (negative, past the table, an id outside the pool) is reported and its slot left empty.
+CP_DEV bool locate(const Placement& p, int row0, int row, long long& pos, Slot& slot) {
   slot.head = -1;
   slot.row = 0;
-  int s = s0;
-  while (s < B && __ldg(cu + s + 1) <= row) ++s;
-  if (s >= B || row < __ldg(cu + s)) return false;
-  pos = (long long)__ldg(start + s) + (row - __ldg(cu + s));
+  pos = -1;
+  const int s = seq_of(p, row0, row);
+  if (s >= p.B || row < __ldg(p.cu + s)) return false;
+  pos = (long long)__ldg(p.start + s) + (row - __ldg(p.cu + s));
   if (pos >= 0) {
-    const long long turn = pos / I, l = (turn / cp) * I + pos % I, col = l / kQ4Page;
-    const int r = (int)(turn % cp);
-    const int id = col < max_blocks ? __ldg(tables + ((long long)r * B + s) * max_blocks + col) : -1;
-    if (id >= 0 && id < pool) {
-      slot.head = (r * pool + id) * Hkv;
-      slot.row = (int)(l % kQ4Page);
+    const unsigned turn = (unsigned)pos / (unsigned)p.I, l = turn / (unsigned)p.cp;  // positions fit 32 bits
+    const int r = (int)(turn - l * (unsigned)p.cp);
+    const long long local = (long long)l * p.I + ((unsigned)pos - turn * (unsigned)p.I), col = local / kQ4Page;
+    const int id = col < p.max_blocks ? __ldg(p.tables + ((long long)r * p.B + s) * p.max_blocks + col) : -1;
+    if (id >= 0 && id < p.pool) {
+      slot.head = (r * p.pool + id) * p.Hkv;
+      slot.row = (int)(local % kQ4Page);
     }
   }
-  if (slot.head < 0) report(err, CP_ERR_DEVICE_BOUNDS);
+  if (slot.head < 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
   return true;
 }
 
@@ -93,15 +104,15 @@ CP_DEV void store8(__nv_bfloat16* p, const float (&x)[8]) {
 
 // ------------------------------------------------------------------------------ write
 struct WriteParams {
-  int B, N, T, Hq, Hkv, cp, I, max_blocks, half, rot;
-  long long pool, q_stride, k_stride, v_stride, qo_stride;
+  Placement at;
+  int N, T, Hq, heads, half, rot;  // T: tokens per warp; heads: heads (of q, k and v) per warp
+  long long q_stride, k_stride, v_stride, qo_stride;
   const void *q, *k, *v;
   void *q_out, *k_out;
   uint8_t *k_cache, *v_cache;
-  const int32_t *cu, *start, *tables;
   const double* inv_freq;
-  int32_t* err;
 };
+constexpr int kWriteTokens = 2;  // most tokens a warp owns
 
 // Rotation.  The angle pos * inv_freq of a far position needs more bits than fp32 has, so it is
 // kept in turns: inv_freq / 2 pi as a 64-bit fraction of a turn (one fp64 multiply per frequency),
@@ -189,111 +200,166 @@ CP_DEV void quantise(const float (&a)[8], const float (&b)[8], const Pieces& s, 
   }
 }
 
-template <typename T, int D, bool Q4>
-__global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteParams p) {
-  constexpr int LPH = D / 16;  // threads per head, 16 dims each
-  constexpr int U = 2;         // rows in flight per thread
-  extern __shared__ float2 cs[];  // [T][rot / 2] cosine, sine
-  __shared__ unsigned long long freq[D / 2];
-  __shared__ Slot slots[kMaxTokens];
-  __shared__ long long posn[kMaxTokens];  // position, or -1: no row (behind the last sequence)
-  const int row0 = blockIdx.x * p.T, nt = min(p.T, p.N - row0), h = p.rot >> 1;
-  const int nh = p.Hq + 2 * p.Hkv;
-  if ((int)threadIdx.x < h) freq[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
-  const int s0 = cta_seq_of_row(p.cu, p.B, row0);
-  if ((int)threadIdx.x < nt) {
-    const int t = threadIdx.x;
-    long long pos = 0;
-    const bool in = locate(p.cu, p.start, p.B, s0, row0 + t, p.cp, p.I, p.tables, p.max_blocks, p.pool,
-                           p.Hkv, p.err, pos, slots[t]);
-    posn[t] = in && pos >= 0 ? pos : -1ll;  // a negative position (reported): the row is skipped
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nt * h; i += kThreads) {
-    const int t = i / h;
-    const unsigned long long f = freq[i - t * h] * (unsigned long long)posn[t];
-    const float turn = (float)(int)(uint32_t)(f >> 32) * 2.3283064365386963e-10f;  // 2^-32
-    float sn, c;
-    sincospif(2.f * turn, &sn, &c);
-    cs[i] = make_float2(c, sn);
-  }
-  __syncthreads();
+// Two fp32 values per instruction (the f32x2 forms of the sm_100 family).
+CP_DEV uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+CP_DEV void f2u(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+CP_DEV uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+CP_DEV uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
-  const int items = nt * nh * LPH;
-  for (int i0 = 0; i0 < items; i0 += U * kThreads) {  // uniform: whole warps stay in the loop
-    float a[U][8], b[U][8];
-    int tok[U], hd[U];
-    Pieces ps[U];
-    const int j = threadIdx.x % LPH;
+// Cosines and sines of the 8 pairs a lane rotates, as packed pairs of neighbours.
+struct Turns {
+  uint64_t c[4], s[4];
+};
+// x, y <- x cos - y sin, y cos + x sin
+CP_DEV void turn2(uint64_t& x, uint64_t& y, uint64_t c, uint64_t s) {
+  const uint64_t u = x, minus = s ^ 0x8000000080000000ull;
+  x = ffma2(y, minus, fmul2(u, c));
+  y = ffma2(u, s, fmul2(y, c));
+}
+CP_DEV void rotate(float (&a)[8], float (&b)[8], const Turns& w, int half) {
+  if (half) {  // (a[e], b[e])
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads + (int)threadIdx.x;
-      const unsigned unit = (unsigned)i / LPH;
-      tok[u] = i < items ? (int)(unit / (unsigned)nh) : -1;
-      hd[u] = (int)(unit % (unsigned)nh);
-      if (tok[u] >= 0 && posn[tok[u]] < 0) tok[u] = -1;
-      ps[u] = pieces_of(j, p.rot, p.half);
-      if (tok[u] >= 0) {
-        const long long row = row0 + tok[u];
-        const T* src = hd[u] < p.Hq ? static_cast<const T*>(p.q) + row * p.q_stride + hd[u] * D
-                       : hd[u] < p.Hq + p.Hkv
-                           ? static_cast<const T*>(p.k) + row * p.k_stride + (hd[u] - p.Hq) * D
-                           : static_cast<const T*>(p.v) + row * p.v_stride + (hd[u] - p.Hq - p.Hkv) * D;
-        load8(src + 8 * ps[u].c0, a[u]);
-        load8(src + 8 * ps[u].c1, b[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[u][e] = b[u][e] = 0.f;
-      }
+    for (int e = 0; e < 4; ++e) {
+      uint64_t x = f2(a[2 * e], a[2 * e + 1]), y = f2(b[2 * e], b[2 * e + 1]);
+      turn2(x, y, w.c[e], w.s[e]);
+      f2u(x, a[2 * e], a[2 * e + 1]);
+      f2u(y, b[2 * e], b[2 * e + 1]);
     }
+  } else {  // (a[2 e], a[2 e + 1]), then b's
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool live = tok[u] >= 0;
-      const bool is_v = hd[u] >= p.Hq + p.Hkv;
-      if (live && ps[u].rot && !is_v) {
-        const float2* c = cs + tok[u] * h;
-        if (p.half) {
+    for (int e = 0; e < 2; ++e) {
+      uint64_t x = f2(a[4 * e], a[4 * e + 2]), y = f2(a[4 * e + 1], a[4 * e + 3]);
+      turn2(x, y, w.c[e], w.s[e]);
+      f2u(x, a[4 * e], a[4 * e + 2]);
+      f2u(y, a[4 * e + 1], a[4 * e + 3]);
+      x = f2(b[4 * e], b[4 * e + 2]), y = f2(b[4 * e + 1], b[4 * e + 3]);
+      turn2(x, y, w.c[e + 2], w.s[e + 2]);
+      f2u(x, b[4 * e], b[4 * e + 2]);
+      f2u(y, b[4 * e + 1], b[4 * e + 3]);
+    }
+  }
+}
+
+// Cosine and sine of an angle in turns.  fp32 rows take the full-accuracy function; rows that are
+// bf16 take the special-function unit's (off by 2^-21.4 at most on half a turn either way, 2^12 below
+// the rows' own rounding), a fifth of the instructions.
+template <typename T>
+CP_DEV void cos_sin(float turn, float& c, float& s) {
+  if constexpr (sizeof(T) == 4) {
+    sincospif(2.f * turn, &s, &c);
+  } else {
+    const float x = turn * 6.283185307179586f;
+    c = __cosf(x);
+    s = __sinf(x);
+  }
+}
+
+// A warp owns T tokens (and `heads` of their q, k and v heads): its lanes find the tokens' slots, share
+// the cosines and sines of their angles in shared memory, and then take D / 16 lanes per head, 16 dims
+// (two 16-byte pieces of bf16) a lane.  A lane's dims are the same for every head, so its cosines and
+// sines stay in registers for a token.  No barrier of the CTA: the chain of dependent loads before the
+// first store (sequence ends, start, page table) is one warp's, hidden behind the others.  Many warps
+// with one row each in flight beat fewer with two or three (2 x 32768 tokens, 16/2 heads: 145 us at
+// 32 warps per SM against 172 at 24 and 181 at 16), and the instructions per row are what is left to
+// save: heads are walked by adding to a pointer, and the rotation runs on packed pairs.
+template <typename T, int D, bool Q4>
+__global__ void __launch_bounds__(kThreads, 4) rope_write_kernel(const WriteParams p) {
+  constexpr int LPH = D / 16;    // lanes per head
+  constexpr int HPW = 32 / LPH;  // heads the warp takes at a time
+  __shared__ __align__(16) float cs_all[kWarps][2][D / 2];  // cosines, sines of a token's angles
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long first = ((long long)blockIdx.x * kWarps + warp) * p.T;
+  if (first >= p.N) return;
+  const int row0 = (int)first, nt = min(p.T, p.N - row0), h = p.rot >> 1, Hkv = p.at.Hkv;
+  // q heads [q_lo, q_hi) and k, v heads [m_lo, m_hi) (v's after k's) are this warp's
+  const int h_lo = blockIdx.y * p.heads, h_hi = min(p.Hq + 2 * Hkv, h_lo + p.heads);
+  const int q_lo = min(h_lo, p.Hq), q_hi = min(h_hi, p.Hq), m_lo = max(h_lo - p.Hq, 0), m_hi = max(h_hi - p.Hq, 0);
+  const int j = lane % LPH, hw = lane / LPH;
+  const Pieces ps = pieces_of(j, p.rot, p.half);
+  const int d0 = 8 * ps.c0, d1 = 8 * ps.c1;
+
+  unsigned long long f[D / 64];  // frequencies lane, lane + 32 in turns per position
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 w = c[8 * ps[u].c0 + e];
-            const float x = a[u][e], y = b[u][e];
-            a[u][e] = x * w.x - y * w.y;
-            b[u][e] = y * w.x + x * w.y;
-          }
-        } else {
+  for (int i = 0; i < D / 64; ++i) f[i] = lane + 32 * i < h ? turns_of(__ldg(p.inv_freq + lane + 32 * i)) : 0ull;
+  Slot mine;
+  long long my_pos = -1;
+  const bool in = locate(p.at, row0, min(row0 + lane, row0 + nt - 1), my_pos, mine);
+  if (!in) my_pos = -1;  // behind the last sequence; a negative position (reported) is skipped too
+
+  for (int t = 0; t < nt; ++t) {
+    const int row = row0 + t;
+    const long long pos = __shfl_sync(0xffffffffu, my_pos, t);
+    if (pos < 0) continue;
+    Turns w;
+    if (h > 0) {
+      float(*const cs)[D / 2] = cs_all[warp];
+      __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 w = c[4 * ps[u].c0 + e / 2], z = c[4 * ps[u].c1 + e / 2];
-            const float x = a[u][e], y = a[u][e + 1], s = b[u][e], t = b[u][e + 1];
-            a[u][e] = x * w.x - y * w.y;
-            a[u][e + 1] = y * w.x + x * w.y;
-            b[u][e] = s * z.x - t * z.y;
-            b[u][e + 1] = t * z.x + s * z.y;
-          }
+      for (int i = 0; i < D / 64; ++i)
+        if (lane + 32 * i < h) {
+          const float turn = (float)(int)(uint32_t)((f[i] * (unsigned long long)pos) >> 32) * 2.3283064365386963e-10f;  // 2^-32
+          cos_sin<T>(turn, cs[0][lane + 32 * i], cs[1][lane + 32 * i]);
+        }
+      __syncwarp();
+      if (ps.rot) {  // half style: the 8 angles of piece c0; pairs style: 4 of each piece
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w.c[e] = *reinterpret_cast<const uint64_t*>(&cs[0][8 * j + 2 * e]);
+          w.s[e] = *reinterpret_cast<const uint64_t*>(&cs[1][8 * j + 2 * e]);
         }
       }
-      const long long row = row0 + tok[u];
-      if (live && hd[u] < p.Hq) {
-        T* dst = static_cast<T*>(p.q_out) + row * p.qo_stride + hd[u] * D;
-        store8(dst + 8 * ps[u].c0, a[u]);
-        store8(dst + 8 * ps[u].c1, b[u]);
+    }
+    {
+      const T* src = static_cast<const T*>(p.q) + row * p.q_stride + (q_lo + hw) * D;
+      T* dst = static_cast<T*>(p.q_out) + row * p.qo_stride + (q_lo + hw) * D;
+      for (int hd = q_lo + hw; hd < q_hi; hd += HPW, src += HPW * D, dst += HPW * D) {
+        float a[8], b[8];
+        load8(src + d0, a);
+        load8(src + d1, b);
+        if (ps.rot) rotate(a, b, w, p.half);
+        store8(dst + d0, a);
+        store8(dst + d1, b);
       }
-      const int g = hd[u] - p.Hq - (is_v ? p.Hkv : 0);
-      if (live && g >= 0 && !is_v && p.k_out != nullptr) {
-        T* dst = static_cast<T*>(p.k_out) + (row * p.Hkv + g) * D;
-        store8(dst + 8 * ps[u].c0, a[u]);
-        store8(dst + 8 * ps[u].c1, b[u]);
+    }
+    Slot sl;
+    sl.head = __shfl_sync(0xffffffffu, mine.head, t);
+    sl.row = __shfl_sync(0xffffffffu, mine.row, t);
+    for (int m0 = m_lo; m0 < m_hi; m0 += HPW) {  // whole warps: the 4-bit form reduces over a head's lanes
+      const int m = m0 + hw;
+      const bool live = m < m_hi, is_v = m >= Hkv;
+      const int g = is_v ? m - Hkv : m;
+      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (live) {
+        const T* src = (is_v ? static_cast<const T*>(p.v) + row * p.v_stride : static_cast<const T*>(p.k) + row * p.k_stride) + g * D;
+        load8(src + d0, a);
+        load8(src + d1, b);
+        if (ps.rot && !is_v) rotate(a, b, w, p.half);
+        if (!is_v && p.k_out != nullptr) {
+          T* dst = static_cast<T*>(p.k_out) + ((long long)row * Hkv + g) * D;
+          store8(dst + d0, a);
+          store8(dst + d1, b);
+        }
       }
-      const Slot sl = live ? slots[tok[u]] : Slot{-1, 0};
-      const bool put = live && g >= 0 && sl.head >= 0;
       uint8_t* cache = is_v ? p.v_cache : p.k_cache;
       if constexpr (Q4) {
-        uint8_t* rec = put ? cache + (sl.head + g) * q4_record_bytes(D) : nullptr;
-        quantise<D>(a[u], b[u], ps[u], rec, sl.row, j, put);
-      } else if (put) {
+        if (sl.head >= 0)
+          quantise<D>(a, b, ps, cache + (sl.head + g) * q4_record_bytes(D), sl.row, j, live);
+      } else if (live && sl.head >= 0) {
         T* dst = reinterpret_cast<T*>(cache) + ((sl.head + g) * kQ4Page + sl.row) * D;
-        store8(dst + 8 * ps[u].c0, a[u]);
-        store8(dst + 8 * ps[u].c1, b[u]);
+        store8(dst + d0, a);
+        store8(dst + d1, b);
       }
     }
   }
@@ -301,113 +367,93 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteParams 
 
 // ------------------------------------------------------------------------------ read
 struct ReadParams {
-  int B, N, T, Hkv, cp, I, max_blocks;
-  long long pool;
+  Placement at;
+  int N, T;  // T: tokens per warp
   const uint8_t *k_cache, *v_cache;
   void *k_out, *v_out;
-  const int32_t *cu, *start, *tables;
-  int32_t* err;
 };
 
-// Rows of the cache's own type (E 16-byte vectors each) copied; U vectors in flight per thread.
-template <int E>
-__global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadParams p) {
-  constexpr int U = 4;
-  __shared__ Slot slots[kMaxTokens];
-  const int row0 = blockIdx.x * p.T, nt = min(p.T, p.N - row0);
-  const int s0 = cta_seq_of_row(p.cu, p.B, row0);
-  if ((int)threadIdx.x < nt) {
-    long long pos;
-    locate(p.cu, p.start, p.B, s0, row0 + threadIdx.x, p.cp, p.I, p.tables, p.max_blocks, p.pool, p.Hkv,
-           p.err, pos, slots[threadIdx.x]);
-  }
-  __syncthreads();
-  const int items = nt * p.Hkv * 2 * E;  // token, K or V, kv head, vector
-  for (int i0 = threadIdx.x; i0 < items; i0 += U * kThreads) {
-    uint4 x[U];
-    uint4* dst[U];
+// A warp owns T <= 32 tokens: lane t finds token t's slot, then V lanes per row stream the tokens' rows
+// (K's heads, then V's), 16 output bytes a lane, U of them in flight.  `load` brings what one needs.
+template <int V, int U, typename Load, typename Store>
+CP_DEV void stream_rows(const ReadParams& p, Slot* slots, Load load, Store store) {
+  constexpr int RPW = 32 / V;  // rows the warp takes at a time
+  const int lane = threadIdx.x & 31;
+  const long long first = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.T;
+  if (first >= p.N) return;
+  const int row0 = (int)first, nt = min(p.T, p.N - row0), Hkv = p.at.Hkv;
+  long long pos;
+  Slot mine;
+  locate(p.at, row0, min(row0 + lane, row0 + nt - 1), pos, mine);
+  slots[lane] = mine;
+  __syncwarp();
+  const int v = lane % V, m_first = lane / V;
+  int t = 0, m0 = 0;  // token, and first of the rows (of 2 Hkv) taken at this step: the same in all lanes
+  while (t < nt) {
+    decltype(load(true, 0ll, 0, 0)) x[U];
+    long long dst[U];  // 16-byte piece of the output (K's or V's), -1: none
+    bool is_v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      dst[u] = nullptr;
-      if (i < items) {
-        const unsigned unit = (unsigned)i / E, v = (unsigned)i % E;
-        const unsigned t = unit / (2u * p.Hkv), m = unit % (2u * p.Hkv);
-        const int g = (int)(m >= (unsigned)p.Hkv ? m - p.Hkv : m);
+      const int m = m0 + m_first;
+      is_v[u] = m >= Hkv;
+      const int g = is_v[u] ? m - Hkv : m;
+      dst[u] = -1;
+      if (t < nt && m < 2 * Hkv) {
         const Slot sl = slots[t];
         if (sl.head >= 0) {
-          const uint8_t* cache = m >= (unsigned)p.Hkv ? p.v_cache : p.k_cache;
-          x[u] = __ldg(reinterpret_cast<const uint4*>(cache) + ((sl.head + g) * kQ4Page + sl.row) * E + v);
-          dst[u] = static_cast<uint4*>(m >= (unsigned)p.Hkv ? p.v_out : p.k_out) +
-                   ((long long)(row0 + t) * p.Hkv + g) * E + v;
+          x[u] = load(is_v[u], sl.head + g, sl.row, v);
+          dst[u] = ((long long)(row0 + t) * Hkv + g) * V + v;
         }
       }
+      m0 += RPW;
+      if (m0 >= 2 * Hkv) m0 = 0, ++t;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (dst[u] != nullptr) *dst[u] = x[u];
+      if (dst[u] >= 0) store(is_v[u], dst[u], x[u]);
   }
 }
 
-// 4-bit rows to the values they stand for: a thread turns one word (8 codes) into 8 values.
+// Rows of the cache's own type, V 16-byte pieces each, copied.
+template <int V>
+__global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadParams p) {
+  __shared__ Slot slots[kWarps][32];
+  stream_rows<V, 4>(
+      p, slots[threadIdx.x >> 5],
+      [&](bool is_v, long long head, int row, int v) {
+        return __ldg(reinterpret_cast<const uint4*>(is_v ? p.v_cache : p.k_cache) + (head * kQ4Page + row) * V + v);
+      },
+      [&](bool is_v, long long at, const uint4& x) { static_cast<uint4*>(is_v ? p.v_out : p.k_out)[at] = x; });
+}
+
+// 4-bit rows to the values they stand for: a lane turns one word (8 codes) into 8 values.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadParams p) {
-  constexpr int U = 4, W = D / 8, GR = D / kQ4Group;
-  __shared__ Slot slots[kMaxTokens];
-  const int row0 = blockIdx.x * p.T, nt = min(p.T, p.N - row0);
-  const int s0 = cta_seq_of_row(p.cu, p.B, row0);
-  if ((int)threadIdx.x < nt) {
-    long long pos;
-    locate(p.cu, p.start, p.B, s0, row0 + threadIdx.x, p.cp, p.I, p.tables, p.max_blocks, p.pool, p.Hkv,
-           p.err, pos, slots[threadIdx.x]);
-  }
-  __syncthreads();
-  const int items = nt * p.Hkv * 2 * W;
-  for (int i0 = threadIdx.x; i0 < items; i0 += U * kThreads) {
-    uint32_t w[U], sm[U];
-    T* dst[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      dst[u] = nullptr;
-      if (i < items) {
-        const unsigned unit = (unsigned)i / W;
-        const int c = (int)((unsigned)i % W);  // dims 8 c ..
-        const unsigned t = unit / (2u * p.Hkv), m = unit % (2u * p.Hkv);
-        const int g = (int)(m >= (unsigned)p.Hkv ? m - p.Hkv : m);
-        const Slot sl = slots[t];
-        if (sl.head >= 0) {
-          const uint8_t* rec =
-              (m >= (unsigned)p.Hkv ? p.v_cache : p.k_cache) + (sl.head + g) * q4_record_bytes(D);
-          w[u] = __ldg(reinterpret_cast<const uint32_t*>(rec + sl.row * (D / 2)) + q4_word<D>(c));
-          sm[u] = __ldg(reinterpret_cast<const uint32_t*>(rec + 8 * D) + sl.row * GR + (GR == 1 ? 0 : c >> 3));
-          dst[u] = static_cast<T*>(m >= (unsigned)p.Hkv ? p.v_out : p.k_out) +
-                   ((long long)(row0 + t) * p.Hkv + g) * D + 8 * c;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (dst[u] != nullptr) {
+  constexpr int GR = D / kQ4Group;
+  __shared__ Slot slots[kWarps][32];
+  stream_rows<D / 8, 4>(
+      p, slots[threadIdx.x >> 5],
+      [&](bool is_v, long long head, int row, int c) {
+        const uint8_t* rec = (is_v ? p.v_cache : p.k_cache) + head * q4_record_bytes(D);
+        return make_uint2(
+            __ldg(reinterpret_cast<const uint32_t*>(rec + row * (D / 2)) + q4_word<D>(c)),
+            __ldg(reinterpret_cast<const uint32_t*>(rec + 8 * D) + row * GR + (GR == 1 ? 0 : c >> 3)));
+      },
+      [&](bool is_v, long long at, const uint2& w) {
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = q4_value(sm[u], (w[u] >> (4 * e)) & 15u);
-        store8(dst[u], x);
-      }
-  }
+        for (int e = 0; e < 8; ++e) x[e] = q4_value(w.y, (w.x >> (4 * e)) & 15u);
+        store8(static_cast<T*>(is_v ? p.v_out : p.k_out) + 8 * at, x);
+      });
 }
 
-// Tokens per CTA: about `want` items of work for its threads, fewer when that would leave SMs
-// without a CTA (a step of 64 single tokens runs 64 CTAs of one token each).
-int tokens_per_cta(long long N, long long items_per_token, long long want) {
+int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     sms = 152;
-  long long t = want / (items_per_token > 0 ? items_per_token : 1);
-  const long long spread = N / (4ll * sms);  // at least ~4 CTAs per SM
-  t = t < spread ? t : spread;
-  return (int)(t < 1 ? 1 : (t > kMaxTokens ? kMaxTokens : t));
+  return sms;
 }
 
 }  // namespace
@@ -416,16 +462,12 @@ int tokens_per_cta(long long N, long long items_per_token, long long want) {
 cudaError_t cp_launch_rope_write(const cp_rope_write_args& a, cudaStream_t s) {
   using namespace cpattn;
   WriteParams p;
-  p.B = a.num_seqs;
+  p.at = Placement{a.num_seqs, a.num_kv_heads, a.cp, a.interleave, a.max_blocks, a.pool_pages,
+                   a.cu_new, a.start_pos, a.block_tables, a.err};
   p.N = a.total_new;
   p.Hq = a.q != nullptr ? a.num_q_heads : 0;
-  p.Hkv = a.num_kv_heads;
-  p.cp = a.cp;
-  p.I = a.interleave;
-  p.max_blocks = a.max_blocks;
   p.half = a.rope_style == CP_ROPE_HALF;
   p.rot = a.rot_dim;
-  p.pool = a.pool_pages;
   p.q_stride = a.q_stride;
   p.k_stride = a.k_stride;
   p.v_stride = a.v_stride;
@@ -437,17 +479,22 @@ cudaError_t cp_launch_rope_write(const cp_rope_write_args& a, cudaStream_t s) {
   p.k_out = a.k_out;
   p.k_cache = static_cast<uint8_t*>(a.k_cache);
   p.v_cache = static_cast<uint8_t*>(a.v_cache);
-  p.cu = a.cu_new;
-  p.start = a.start_pos;
-  p.tables = a.block_tables;
   p.inv_freq = a.inv_freq;
-  p.err = a.err;
-  p.T = tokens_per_cta(p.N, (long long)(p.Hq + 2 * p.Hkv) * (a.head_dim / 16), 1280);
-  if (p.T > 16) p.T = 16;  // the angles of 16 tokens: 8 KB of shared memory
-  const unsigned grid = (unsigned)((p.N + p.T - 1) / p.T);
-  const size_t smem = (size_t)p.T * (p.rot / 2) * sizeof(float2);
+  // tokens per warp: few enough that every SM gets its warps; with fewer tokens than that, a token's
+  // heads are split over warps too (each then computes the token's angles again)
+  const long long warps = 32ll * sm_count();
+  const int nh = p.Hq + 2 * a.num_kv_heads, at_a_time = 32 / (a.head_dim / 16);
+  long long t = p.N / warps;
+  p.T = (int)(t < 1 ? 1 : (t > kWriteTokens ? kWriteTokens : t));
+  long long pieces = p.T == 1 ? warps / p.N : 1;
+  const long long most = (nh + at_a_time - 1) / at_a_time;
+  pieces = pieces < 1 ? 1 : (pieces > most ? most : pieces);
+  const long long each = ((nh + pieces - 1) / pieces + at_a_time - 1) / at_a_time * at_a_time;
+  p.heads = (int)each;
+  const long long per_cta = (long long)kWarps * p.T;
+  const dim3 grid((unsigned)((p.N + per_cta - 1) / per_cta), (unsigned)((nh + each - 1) / each));
   auto go = [&](auto kern) -> cudaError_t {
-    kern<<<grid, kThreads, smem, s>>>(p);
+    kern<<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
   };
   const bool q4 = a.cache_q4 != 0, bf = a.dtype == CP_BF16;
@@ -464,39 +511,29 @@ cudaError_t cp_launch_rope_write(const cp_rope_write_args& a, cudaStream_t s) {
 cudaError_t cp_launch_kv_read(const cp_kv_read_args& a, cudaStream_t s) {
   using namespace cpattn;
   ReadParams p;
-  p.B = a.num_seqs;
+  p.at = Placement{a.num_seqs, a.num_kv_heads, a.cp, a.interleave, a.max_blocks, a.pool_pages,
+                   a.cu_out, a.start_pos, a.block_tables, a.err};
   p.N = a.total;
-  p.Hkv = a.num_kv_heads;
-  p.cp = a.cp;
-  p.I = a.interleave;
-  p.max_blocks = a.max_blocks;
-  p.pool = a.pool_pages;
   p.k_cache = static_cast<const uint8_t*>(a.k_cache);
   p.v_cache = static_cast<const uint8_t*>(a.v_cache);
   p.k_out = a.k_out;
   p.v_out = a.v_out;
-  p.cu = a.cu_out;
-  p.start = a.start_pos;
-  p.tables = a.block_tables;
-  p.err = a.err;
   const int d = a.head_dim;
   const int row_bytes = d * (a.out_dtype == CP_BF16 ? 2 : 4);
-  p.T = tokens_per_cta(p.N, 2ll * p.Hkv * (a.cache_q4 ? d / 8 : row_bytes / 16), 4 * kThreads);
-  const unsigned grid = (unsigned)((p.N + p.T - 1) / p.T);
+  // tokens per warp: a lane each, fewer where that would leave SMs without their warps
+  const long long t = p.N / (32ll * sm_count());
+  p.T = (int)(t < 1 ? 1 : (t > 8 ? 8 : t));
+  const long long per_cta = (long long)kWarps * p.T;
+  const unsigned grid = (unsigned)((p.N + per_cta - 1) / per_cta);
+  auto go = [&](auto kern) -> cudaError_t {
+    kern<<<grid, kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  };
   if (a.cache_q4) {
-    if (d == 128) {
-      if (a.out_dtype == CP_BF16) read_q4_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, s>>>(p);
-      else read_q4_kernel<float, 128><<<grid, kThreads, 0, s>>>(p);
-    } else {
-      if (a.out_dtype == CP_BF16) read_q4_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, s>>>(p);
-      else read_q4_kernel<float, 64><<<grid, kThreads, 0, s>>>(p);
-    }
-  } else if (row_bytes == 128) {
-    read_rows_kernel<8><<<grid, kThreads, 0, s>>>(p);
-  } else if (row_bytes == 256) {
-    read_rows_kernel<16><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    read_rows_kernel<32><<<grid, kThreads, 0, s>>>(p);
+    if (d == 128) return a.out_dtype == CP_BF16 ? go(read_q4_kernel<__nv_bfloat16, 128>) : go(read_q4_kernel<float, 128>);
+    return a.out_dtype == CP_BF16 ? go(read_q4_kernel<__nv_bfloat16, 64>) : go(read_q4_kernel<float, 64>);
   }
-  return cudaGetLastError();
+  if (row_bytes == 128) return go(read_rows_kernel<8>);
+  if (row_bytes == 256) return go(read_rows_kernel<16>);
+  return go(read_rows_kernel<32>);
 }

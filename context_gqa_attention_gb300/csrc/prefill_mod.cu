@@ -46,6 +46,7 @@ constexpr float kMaxGrowth = 8.f;            // log2 units the scores may exceed
 struct PrefillModParams {
   int B, Hq, Hkv, G, Nq, window, tiles;  // tiles: row tiles (items) of the longest sequence
   float scale_log2, softcap, cap_in;  // cap_in = scale / cap: y = cap_in q.k
+  float cap_ref;  // CAP: the fixed reference of the scores, log2 units
   const int32_t* cu_q;
   const int32_t* cu_kv;  // null: the query rows
   const int32_t* kv_start;
@@ -151,8 +152,8 @@ CP_DEV void cap_poly(Row& v, float cap_in, float cap_log2, const float (&a)[N + 
 }
 // Relative errors 5.5e-7 on |y| <= 0.5 and 6.3e-7 on |y| <= 1.25 (least-maximum fits to tanh).
 constexpr float kCapNear = 0.5f, kCapFar = 1.25f;
-CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2) {
-  const float y = row_abs_max(v) * cap_in;
+// y: the row's largest |cap_in s|.
+CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y) {
   if (__all_sync(0xffffffffu, y <= kCapNear)) {
     const float a[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
     cap_poly<3>(v, cap_in, cap_log2, a);
@@ -168,6 +169,71 @@ CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2) {
       for (int k = 0; k < 32; ++k)
         v.c[i][k] = cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(v.c[i][k] * in));
   }
+}
+
+// Capped scores are bounded, |x| <= cap log2(e), so with a cap of at most kMaxCapLog2 they need no
+// running maximum: against the fixed reference max(0, cap log2(e) - 40) every P lies within
+// [2^-120, 2^40], which fp32 sums and bf16 operands hold.  P then follows from the score in one chain
+// without a dependence on the rest of the row, and the polynomial's packed FMAs run under the
+// exponentials' special-function time.
+constexpr float kMaxCapLog2 = 80.f;   // cap <= 55.4
+constexpr float kMinCapIn = 1e-5f;    // the folded coefficients stay normal numbers
+constexpr float kCapRefBelow = 40.f;
+
+// P of a row, packed as bf16 pairs over its S columns in TMEM; returns the row's sum.  Columns
+// outside [c0, c1) are masked when MASK.
+template <bool MASK, typename X>
+CP_DEV float cap_exp_row(Row& v, uint32_t tS, int c0, int c1, X&& x2) {
+  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float x, y;
+      f2u(x2(f2(v.c[i][k], v.c[i][k + 1])), x, y);
+      if constexpr (MASK) {
+        x = 32 * i + k >= c0 && 32 * i + k < c1 ? x : -INFINITY;
+        y = 32 * i + k + 1 >= c0 && 32 * i + k + 1 < c1 ? y : -INFINITY;
+      }
+      x = ex2(x);
+      y = ex2(y);
+      acc[(k >> 1) & 3] = fadd2(acc[(k >> 1) & 3], f2(x, y));
+      pk[k >> 1] = pack_bf16(x, y);
+    }
+    tmem_st16(tS + 16 * i, pk);
+  }
+  float lo, hi;
+  f2u(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), lo, hi);
+  return lo + hi;
+}
+struct CapCoefficients {
+  uint64_t c[4];  // x = s (c0 + u (c1 + u (c2 + u c3))), u = s^2, for |cap_in s| <= kCapNear
+};
+CP_DEV CapCoefficients cap_coefficients(float cap_in, float scale_log2) {
+  const float a[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
+  CapCoefficients r;
+  float k = scale_log2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.c[i] = f2(a[i] * k, a[i] * k);
+    k *= cap_in * cap_in;
+  }
+  return r;
+}
+template <bool MASK>
+CP_DEV float cap_row(Row& v, uint32_t tS, int c0, int c1, const CapCoefficients& w, float cap_in, float cap_log2,
+                     float ref) {
+  const uint64_t neg = f2(-ref, -ref);
+  const float y = row_abs_max(v) * cap_in;
+  if (__all_sync(0xffffffffu, y <= kCapNear)) {
+    return cap_exp_row<MASK>(v, tS, c0, c1, [&](uint64_t s) {
+      const uint64_t u = fmul2(s, s);
+      return ffma2(s, ffma2(ffma2(ffma2(w.c[3], u, w.c[2]), u, w.c[1]), u, w.c[0]), neg);
+    });
+  }
+  cap_scores(v, cap_in, cap_log2, y);
+  return cap_exp_row<MASK>(v, tS, c0, c1, [&](uint64_t s) { return fadd2(s, neg); });
 }
 
 // P = 2^(x - ref) of 32 columns, packed as bf16 pairs over the row's own S columns in TMEM (the A
@@ -256,7 +322,9 @@ CP_DEV void restore(float (&o)[32], const __nv_bfloat16* v, long long stride, in
 }
 
 // ------------------------------------------------------------------------------ kernel
-template <int D, bool TT>
+// TT: the two tiles are two row tiles of one head.  CAP: scores with nothing but a cap that allows the
+// fixed reference.
+template <int D, bool TT, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_mod_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const PrefillModParams p) {
@@ -535,7 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scores come out of cap and bias in log2 units; untouched ones are scaled within the exponent
     const float sc = cap || biased ? 1.f : p.scale_log2;
     const uint64_t sc2 = f2(sc, sc);
-    float m = -INFINITY, l = 0.f;
+    float m = CAP ? p.cap_ref : -INFINITY, l = 0.f;
+    CapCoefficients coef;
+    if constexpr (CAP) coef = cap_coefficients(p.cap_in, p.scale_log2);
     bool ok = true;
     for (int t = 0; t < ntiles; ++t) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
@@ -547,56 +617,63 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) tmem_wait_ld(v.c[i]);
       const int k0 = key_lo + t * BN;
-      if (cap) cap_scores(v, p.cap_in, cap_log2);
-      if (biased) {
-        const float s0 = cap ? 1.f : p.scale_log2;
-        const int far = k0 + BN - 1 - (C + row);  // > 0: keys behind the query in this tile
-        if (__any_sync(0xffffffffu, far > 0 && hi > C + row + 1 && k0 < hi)) {
-          const float d0 = (float)(k0 - (C + row));
+      const int c0 = lo - k0, c1 = hi - k0;  // visible columns [c0, c1)
+      const bool whole_tile = __all_sync(0xffffffffu, c0 <= 0 && c1 >= BN);
+      // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S columns may
+      // take P(t)
+      if constexpr (CAP) {
+        l += whole_tile ? cap_row<false>(v, tS, c0, c1, coef, p.cap_in, cap_log2, p.cap_ref)
+                        : cap_row<true>(v, tS, c0, c1, coef, p.cap_in, cap_log2, p.cap_ref);
+        tmem_wait_st();
+      } else {
+        if (cap) cap_scores(v, p.cap_in, cap_log2, row_abs_max(v) * p.cap_in);
+        if (biased) {
+          const float s0 = cap ? 1.f : p.scale_log2;
+          const int far = k0 + BN - 1 - (C + row);  // > 0: keys behind the query in this tile
+          if (__any_sync(0xffffffffu, far > 0 && hi > C + row + 1 && k0 < hi)) {
+            const float d0 = (float)(k0 - (C + row));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                v.c[i][k] = fmaf(-slope, fabsf(d0 + (float)(32 * i + k)), v.c[i][k] * s0);
+          } else {  // every visible key is at or before the query: the bias is linear in the column
+            const uint64_t sl2 = f2(slope, slope), s02 = f2(s0, s0);
+            const float b0 = slope * (float)(k0 - (C + row));
+            const uint64_t b2 = f2(b0, b0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const uint64_t bias = ffma2(sl2, f2((float)(32 * i + k), (float)(32 * i + k + 1)), b2);
+                f2u(ffma2(f2(v.c[i][k], v.c[i][k + 1]), s02, bias), v.c[i][k], v.c[i][k + 1]);
+              }
+          }
+        }
+        if (!whole_tile) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              v.c[i][k] = fmaf(-slope, fabsf(d0 + (float)(32 * i + k)), v.c[i][k] * s0);
-        } else {  // every visible key is at or before the query: the bias is linear in the column
-          const uint64_t sl2 = f2(slope, slope), s02 = f2(s0, s0);
-          const float b0 = slope * (float)(k0 - (C + row));
-          const uint64_t b2 = f2(b0, b0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const uint64_t bias = ffma2(sl2, f2((float)(32 * i + k), (float)(32 * i + k + 1)), b2);
-              f2u(ffma2(f2(v.c[i][k], v.c[i][k + 1]), s02, bias), v.c[i][k], v.c[i][k + 1]);
-            }
+              v.c[i][k] = 32 * i + k >= c0 && 32 * i + k < c1 ? v.c[i][k] : -INFINITY;
         }
-      }
-      const int c0 = lo - k0, c1 = hi - k0;  // visible columns [c0, c1)
-      if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= BN)) {
+        const float mt = row_max(v) * sc;
+        float alpha = 1.f;
+        if (mt > m + kMaxGrowth) {  // the first visible tile, or the scores grew a lot
+          alpha = ex2(m - mt);
+          m = mt;
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const uint64_t n2 = f2(neg, neg);
+        uint64_t sum2 = f2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            v.c[i][k] = 32 * i + k >= c0 && 32 * i + k < c1 ? v.c[i][k] : -INFINITY;
+        for (int i = 0; i < 4; ++i) exp_chunk(v.c[i], sc2, n2, sum2, tS + 16 * i);
+        tmem_wait_st();
+        float s_lo, s_hi;
+        f2u(sum2, s_lo, s_hi);
+        l = l * alpha + (s_lo + s_hi);
+        if (t > 0) rescale_o<D>(tO, alpha);
       }
-      const float mt = row_max(v) * sc;
-      float alpha = 1.f;
-      if (mt > m + kMaxGrowth) {  // the first visible tile, or the scores grew a lot
-        alpha = ex2(m - mt);
-        m = mt;
-      }
-      const float neg = m == -INFINITY ? 0.f : -m;
-      const uint64_t n2 = f2(neg, neg);
-      uint64_t sum2 = f2(0.f, 0.f);
-      // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S
-      // columns may take P(t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) exp_chunk(v.c[i], sc2, n2, sum2, tS + 16 * i);
-      tmem_wait_st();
-      float s_lo, s_hi;
-      f2u(sum2, s_lo, s_hi);
-      l = l * alpha + (s_lo + s_hi);
-      if (t > 0) rescale_o<D>(tO, alpha);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Sm::bP + tile));
@@ -692,6 +769,9 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   p.scale_log2 = scale * kLog2e;
   p.softcap = mod.softcap;
   p.cap_in = mod.softcap > 0.f ? scale / mod.softcap : 0.f;
+  const float cap_log2 = mod.softcap * kLog2e;
+  p.cap_ref = cap_log2 > kCapRefBelow ? cap_log2 - kCapRefBelow : 0.f;
+  const bool fixed = mod.softcap > 0.f && cap_log2 <= kMaxCapLog2 && p.cap_in >= kMinCapIn && mod.alibi_slopes == nullptr;
   p.cu_q = a.cu_seqlens_q;
   p.cu_kv = a.cu_seqlens_kv;
   p.kv_start = mod.kv_start;
@@ -707,7 +787,8 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   if (p.tiles == 0) return cudaSuccess;
   if (p.tiles > 65535 || a.num_seqs > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid(tt ? a.num_q_heads : a.num_q_heads / 2, p.tiles, a.num_seqs);
-  auto kern = tt ? prefill_mod_kernel<D, true> : prefill_mod_kernel<D, false>;
+  auto kern = tt ? (fixed ? prefill_mod_kernel<D, true, true> : prefill_mod_kernel<D, true, false>)
+                 : (fixed ? prefill_mod_kernel<D, false, true> : prefill_mod_kernel<D, false, false>);
   // the register budgets assume the registers a thread of this launch gets; a build that gave the
   // kernel another count would leave an increase waiting, so refuse it
   cudaFuncAttributes fa;

@@ -499,6 +499,9 @@ PREFILLS = [
     ([300, 260], [20, 0], 10, 2, 64, 8.0, 150, True, True, 90),
     ([140], [500], 2, 2, 128, 0.0, 64, False, False, 600),
     ([600], [0], 2, 1, 64, 1.0, 300, False, True, 0),
+    ([200, 31], [0, 60], 4, 2, 128, 100.0, 0, False, False, 0),     # a cap past the fixed reference's
+    ([333], [0], 3, 1, 64, 55.0, 0, False, True, 40),
+    ([150], [20], 2, 1, 128, 0.02, 0, False, False, 0),
 ]
 
 
