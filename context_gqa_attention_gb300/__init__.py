@@ -203,7 +203,8 @@ def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        device = getattr(_CALL, "device", None)
+        return _raw_stream(torch.cuda.current_device() if device is None else device.index)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -238,12 +239,13 @@ def _on_first_tensors_device(fn):
 def _dev(t, name, dtype=None):
     if t is None:
         return
-    if not t.is_cuda:
-        raise CPError(1, f"{name} must be a CUDA tensor")
     want = getattr(_CALL, "device", None)
-    if want is not None and t.device != want:
-        raise CPError(1, f"{name} is on {t.device} but the call runs on {want}: every tensor "
-                         "of one call must be on the same device")
+    if t.device != want:
+        if not t.is_cuda:
+            raise CPError(1, f"{name} must be a CUDA tensor")
+        if want is not None:
+            raise CPError(1, f"{name} is on {t.device} but the call runs on {want}: every tensor "
+                             "of one call must be on the same device")
     if not t.is_contiguous():
         raise CPError(1, f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -634,18 +636,19 @@ def _shape(t, name, shape):
 def _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, dtype):
     """Checks of the paged pools and their tables; whether they hold 4-bit records (uint8)."""
     q4 = k_cache.dtype == torch.uint8
-    if k_cache.dim() != (4 if q4 else 5):
+    shape = k_cache.shape
+    if len(shape) != (4 if q4 else 5):
         raise CPError(1, "k_cache must be [cp, pool, Hkv, 16, d], or uint8 [cp, pool, Hkv, 9 d] (4-bit)")
-    _dev(k_cache, "k_cache", torch.uint8 if q4 else dtype)
+    _dev(k_cache, "k_cache", None if q4 else dtype)
     _dev(v_cache, "v_cache", k_cache.dtype)
     _dev(block_tables, "block_tables", torch.int32)
-    pool, heads = k_cache.shape[1], k_cache.shape[2] if Hkv is None else Hkv
-    want = (cp, pool, heads, 9 * d) if q4 else (cp, pool, heads, k_cache.shape[3], d)
-    _shape(k_cache, "k_cache", want)
-    _shape(v_cache, "v_cache", want)
-    if block_tables.dim() != 3 or block_tables.shape[:2] != (cp, B):
-        raise CPError(1, f"block_tables must be [cp, B, max_blocks] = [{cp}, {B}, ..] "
-                         f"(got {list(block_tables.shape)})")
+    if shape[0] != cp or shape[-1] != (9 * d if q4 else d) or (Hkv is not None and shape[2] != Hkv):
+        raise CPError(1, f"k_cache is {list(shape)}: cp = {cp}, head_dim = {d} and {Hkv or 'any number of'} "
+                         "kv heads want another shape")
+    _shape(v_cache, "v_cache", shape)
+    tables = block_tables.shape
+    if len(tables) != 3 or tables[0] != cp or tables[1] != B:
+        raise CPError(1, f"block_tables must be [cp, B, max_blocks] = [{cp}, {B}, ..] (got {list(tables)})")
     return q4
 
 

@@ -15,7 +15,7 @@
 //         softmax overlaps the other tile's two MMAs
 //   2-3   V guards: in a key tile that some row sees only in part they clear what must not reach
 //         the MMA (0 times an infinity is NaN), see below
-//   4-11  two softmax warpgroups, one thread per query row
+//   4-19  four softmax warpgroups, two per tile: a thread owns half of a query row's 128 scores
 // The keys a CTA walks are the union [key_lo, key_hi) of its rows' ranges, so windows and short
 // documents load their own keys only; tiles start at key_lo, not at a multiple of 128.
 //
@@ -35,18 +35,16 @@ using namespace sm100;
 
 constexpr int BM = 128;  // query rows per tile (TMEM lanes)
 constexpr int BN = 128;  // keys per tile
-constexpr int kThreads = 384;
+constexpr int BH = BN / 2;  // scores of a row per softmax thread
+constexpr int kThreads = 640;
 constexpr int kSlots = 4;                    // K / V ring
-constexpr int kRegsProducer = 88, kRegsSoftmax = 208;
-constexpr int kRegsLaunch = 168;             // registers a thread of the 384-thread launch
-static_assert(kRegsProducer + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register budgets exceed the launch");
 constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
 constexpr float kMaxGrowth = 8.f;            // log2 units the scores may exceed the running reference
 
 struct PrefillModParams {
   int B, Hq, Hkv, G, Nq, window, tiles;  // tiles: row tiles (items) of the longest sequence
   float scale_log2, softcap, cap_in;  // cap_in = scale / cap: y = cap_in q.k
-  float cap_ref;  // CAP: the fixed reference of the scores, log2 units
+  float cap_ref;  // CAP: the least reference of the scores, log2 units
   const int32_t* cu_q;
   const int32_t* cu_kv;  // null: the query rows
   const int32_t* kv_start;
@@ -107,28 +105,26 @@ CP_DEV uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A row's 128 scores: four chunks of 32 TMEM columns.
+// A thread's 64 scores: two chunks of 32 TMEM columns.
+constexpr int kChunks = BH / 32;
 struct Row {
-  float c[4][32];
+  float c[kChunks][32];
 };
 CP_DEV float row_max(const Row& v) {
-  float m[4];
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = -INFINITY;
+  for (int k = 0; k < 32; k += 4)
 #pragma unroll
-  for (int k = 0; k < 32; k += 2)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], v.c[i][k], v.c[i][k + 1]);
+    for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], v.c[i >> 1][k + 2 * (i & 1)], v.c[i >> 1][k + 2 * (i & 1) + 1]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 CP_DEV float row_abs_max(const Row& v) {
-  float m[4];
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = 0.f;
+  for (int k = 0; k < 32; k += 4)
 #pragma unroll
-  for (int k = 0; k < 32; k += 2)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], fabsf(v.c[i][k]), fabsf(v.c[i][k + 1]));
+    for (int i = 0; i < 4; ++i)
+      m[i] = fmaxf(fmaxf(m[i], fabsf(v.c[i >> 1][k + 2 * (i & 1)])), fabsf(v.c[i >> 1][k + 2 * (i & 1) + 1]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
@@ -140,7 +136,7 @@ CP_DEV void cap_poly(Row& v, float cap_in, float cap_log2, const float (&a)[N + 
 #pragma unroll
   for (int i = 0; i <= N; ++i) c[i] = f2(a[i] * cap_log2, a[i] * cap_log2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kChunks; ++i)
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
       const uint64_t y = fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2), u = fmul2(y, y);
@@ -164,7 +160,7 @@ CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y) {
   } else {  // 1 - 2 / (1 + e^2y): absolute error about 2^-22
     const float in = 2.f * kLog2e * cap_in;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kChunks; ++i)
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         v.c[i][k] = cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(v.c[i][k] * in));
@@ -172,41 +168,16 @@ CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y) {
 }
 
 // Capped scores are bounded, |x| <= cap log2(e), so with a cap of at most kMaxCapLog2 they need no
-// running maximum: against the fixed reference max(0, cap log2(e) - 40) every P lies within
-// [2^-120, 2^40], which fp32 sums and bf16 operands hold.  P then follows from the score in one chain
-// without a dependence on the rest of the row, and the polynomial's packed FMAs run under the
-// exponentials' special-function time.
+// running maximum: the row's maximum over the first tile, but at least cap log2(e) - kCapAbove, stays
+// the reference, and no P is above 2^kCapAbove (which fp32 sums and bf16 operands hold) while the
+// largest is at least 2^-kMaxCapLog2.  P then follows from the score in one chain without a dependence
+// on the rest of the row, and the polynomial's packed FMAs run under the exponentials' special-function
+// time.  (A reference that is one of the row's own scores makes its P exactly 1: with a constant one,
+// rows of a few keys lose up to 2^-9 to P's rounding that they need not.)
 constexpr float kMaxCapLog2 = 80.f;   // cap <= 55.4
+constexpr float kCapAbove = 80.f;
 constexpr float kMinCapIn = 1e-5f;    // the folded coefficients stay normal numbers
-constexpr float kCapRefBelow = 40.f;
 
-// P of a row, packed as bf16 pairs over its S columns in TMEM; returns the row's sum.  Columns
-// outside [c0, c1) are masked when MASK.
-template <bool MASK, typename X>
-CP_DEV float cap_exp_row(Row& v, uint32_t tS, int c0, int c1, X&& x2) {
-  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      float x, y;
-      f2u(x2(f2(v.c[i][k], v.c[i][k + 1])), x, y);
-      if constexpr (MASK) {
-        x = 32 * i + k >= c0 && 32 * i + k < c1 ? x : -INFINITY;
-        y = 32 * i + k + 1 >= c0 && 32 * i + k + 1 < c1 ? y : -INFINITY;
-      }
-      x = ex2(x);
-      y = ex2(y);
-      acc[(k >> 1) & 3] = fadd2(acc[(k >> 1) & 3], f2(x, y));
-      pk[k >> 1] = pack_bf16(x, y);
-    }
-    tmem_st16(tS + 16 * i, pk);
-  }
-  float lo, hi;
-  f2u(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), lo, hi);
-  return lo + hi;
-}
 struct CapCoefficients {
   uint64_t c[4];  // x = s (c0 + u (c1 + u (c2 + u c3))), u = s^2, for |cap_in s| <= kCapNear
 };
@@ -221,19 +192,29 @@ CP_DEV CapCoefficients cap_coefficients(float cap_in, float scale_log2) {
   }
   return r;
 }
-template <bool MASK>
-CP_DEV float cap_row(Row& v, uint32_t tS, int c0, int c1, const CapCoefficients& w, float cap_in, float cap_log2,
-                     float ref) {
+// P of a row whose scores all lie within kCapNear, packed as bf16 pairs over its S columns in TMEM; the
+// row's sum.
+CP_DEV float cap_near_row(Row& v, uint32_t tS, const CapCoefficients& w, float ref) {
   const uint64_t neg = f2(-ref, -ref);
-  const float y = row_abs_max(v) * cap_in;
-  if (__all_sync(0xffffffffu, y <= kCapNear)) {
-    return cap_exp_row<MASK>(v, tS, c0, c1, [&](uint64_t s) {
-      const uint64_t u = fmul2(s, s);
-      return ffma2(s, ffma2(ffma2(ffma2(w.c[3], u, w.c[2]), u, w.c[1]), u, w.c[0]), neg);
-    });
+  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const uint64_t s = f2(v.c[i][k], v.c[i][k + 1]), u = fmul2(s, s);
+      float x, y;
+      f2u(ffma2(s, ffma2(ffma2(ffma2(w.c[3], u, w.c[2]), u, w.c[1]), u, w.c[0]), neg), x, y);
+      x = ex2(x);
+      y = ex2(y);
+      acc[(k >> 1) & 3] = fadd2(acc[(k >> 1) & 3], f2(x, y));
+      pk[k >> 1] = pack_bf16(x, y);
+    }
+    tmem_st16(tS + 16 * i, pk);
   }
-  cap_scores(v, cap_in, cap_log2, y);
-  return cap_exp_row<MASK>(v, tS, c0, c1, [&](uint64_t s) { return fadd2(s, neg); });
+  float lo, hi;
+  f2u(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), lo, hi);
+  return lo + hi;
 }
 
 // P = 2^(x - ref) of 32 columns, packed as bf16 pairs over the row's own S columns in TMEM (the A
@@ -254,12 +235,12 @@ CP_DEV void exp_chunk(float (&a)[32], uint64_t sc2, uint64_t n2, uint64_t& sum2,
   tmem_st16(taddr, pk);
 }
 
-// O row *= alpha in TMEM (nothing to do when no lane of the warp needs it).
-template <int D>
+// COLS columns of an O row *= alpha in TMEM (nothing to do when no lane of the warp needs it).
+template <int COLS>
 CP_DEV void rescale_o(uint32_t tO, float alpha) {
   if (!__any_sync(0xffffffffu, alpha != 1.f)) return;
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
+  for (int c = 0; c < COLS / 32; ++c) {
     float o[32];
     tmem_ld32(tO + c * 32, o);
     tmem_wait_ld(o);
@@ -321,9 +302,22 @@ CP_DEV void restore(float (&o)[32], const __nv_bfloat16* v, long long stride, in
     }
 }
 
+// The two warps that hold the halves of the same 32 rows meet at a named barrier of their own.
+CP_DEV void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+CP_DEV bool pair_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0u;
+}
+
 // ------------------------------------------------------------------------------ kernel
-// TT: the two tiles are two row tiles of one head.  CAP: scores with nothing but a cap that allows the
-// fixed reference.
+// TT: the two tiles are two row tiles of one head.  CAP: scores with nothing but a cap that allows a
+// reference fixed at the first tile.
 template <int D, bool TT, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_mod_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -333,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int SPAN = TT ? 2 * BM : BM;  // query rows of an item
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_range[kThreads / 32][4];
+  __shared__ float s_rows[2][2][BM];  // [tile][half][row]: what the halves of a row tell each other
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- the item: heads fastest, then row tiles (the last, longest one first), then sequences
@@ -435,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Sm::bS + i), 1);
-      mbar_init(bar(Sm::bP + i), 4);
+      mbar_init(bar(Sm::bP + i), 8);
       mbar_init(bar(Sm::bO + i), 1);
       mbar_init(bar(Sm::bFix + i), 2);
     }
@@ -464,7 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = h0 / p.G;
 
   if (warp < 4) {
-    regs_dec<kRegsProducer>();
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer
       if (lane == 0) {
@@ -513,8 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_pv = [&](int tile, int slot, bool acc) {
           const uint64_t dv = desc_advance(dv0, (uint32_t)(slot * Sm::kKV));
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + 256u + (uint32_t)(tile * D), tmem + (uint32_t)(tile * BN + kk * 8),
+          for (int kk = 0; kk < BN / 16; ++kk)  // each half's P lies over the front of its own scores
+            mma_ts(tmem + 256u + (uint32_t)(tile * D),
+                   tmem + (uint32_t)(tile * BN + kk * 8 + (kk >= BH / 16 ? BH / 2 : 0)),
                    desc_advance(dv, kk * 16u * 128u), id_pv, acc || kk > 0);
         };
         bool ok = mbar_wait(bar(Sm::bQ), 0u, abort_flag, kBudget) &&
@@ -586,14 +581,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    regs_inc<kRegsSoftmax>();
-    // ------------------------------------------------------------------ softmax, one WG per tile
-    const int tile = (warp - 4) >> 2, q4 = warp & 3;
+    // ---------------------------------------------------------------- softmax, two warpgroups per tile
+    const int sw = warp - 4, tile = sw >> 3, half = (sw >> 2) & 1, q4 = warp & 3;
+    const int pair = 1 + tile * 4 + q4;  // named barrier of the warps with the same rows
     const int row = q_lo + (TT ? tile * BM : 0) + q4 * 32 + lane;  // within the sequence
     const int head = h0 + (TT ? 0 : tile);
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tS = tmem + lane_off + (uint32_t)(tile * BN);
-    const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(tile * D);
+    const uint32_t tS = tmem + lane_off + (uint32_t)(tile * BN + half * BH);
+    const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(tile * D + half * (D / 2));
+    float* const s_mine = &s_rows[tile][half][q4 * 32 + lane];
+    float* const s_other = &s_rows[tile][half ^ 1][q4 * 32 + lane];
     const bool valid = row < q_hi;
     const int lo = valid ? lo_of(row) : 0, hi = valid ? hi_of(row) : 0;
     const bool cap = p.softcap > 0.f;
@@ -601,78 +598,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool biased = p.slopes != nullptr;
     const float slope = biased ? __ldg(p.slopes + head) * kLog2e : 0.f;
     // scores come out of cap and bias in log2 units; untouched ones are scaled within the exponent
-    const float sc = cap || biased ? 1.f : p.scale_log2;
+    const float sc = CAP || cap || biased ? 1.f : p.scale_log2;
     const uint64_t sc2 = f2(sc, sc);
-    float m = CAP ? p.cap_ref : -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;
     CapCoefficients coef;
     if constexpr (CAP) coef = cap_coefficients(p.cap_in, p.scale_log2);
     bool ok = true;
     for (int t = 0; t < ntiles; ++t) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
-      if (!ok) break;
+      // a warp that gives up raises the abort flag; its partner gives up at its own wait, or where the
+      // two meet within the tile
+      if (!ok) {
+        if (lane == 0) fail();
+        __syncwarp();
+        // the votes below, as the partner will meet them
+        if (!CAP || t == 0) pair_any(pair, true);
+        if constexpr (!CAP) pair_any(pair, true);
+        break;
+      }
       tc_fence_after();
       Row v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, v.c[i]);
+      for (int i = 0; i < kChunks; ++i) tmem_ld32(tS + 32 * i, v.c[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_wait_ld(v.c[i]);
-      const int k0 = key_lo + t * BN;
-      const int c0 = lo - k0, c1 = hi - k0;  // visible columns [c0, c1)
-      const bool whole_tile = __all_sync(0xffffffffu, c0 <= 0 && c1 >= BN);
+      for (int i = 0; i < kChunks; ++i) tmem_wait_ld(v.c[i]);
+      const int k0 = key_lo + t * BN + half * BH;  // this thread's first key
+      const int c0 = lo - k0, c1 = hi - k0;        // visible columns [c0, c1)
+      const bool whole_tile = __all_sync(0xffffffffu, c0 <= 0 && c1 >= BH);
       // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S columns may
       // take P(t)
+      float y = 0.f;
+      bool near = false;
       if constexpr (CAP) {
-        l += whole_tile ? cap_row<false>(v, tS, c0, c1, coef, p.cap_in, cap_log2, p.cap_ref)
-                        : cap_row<true>(v, tS, c0, c1, coef, p.cap_in, cap_log2, p.cap_ref);
+        y = row_abs_max(v) * p.cap_in;
+        near = t > 0 && whole_tile && __all_sync(0xffffffffu, y <= kCapNear);
+      }
+      if (CAP && near) {
+        l += cap_near_row(v, tS, coef, m);
         tmem_wait_st();
       } else {
-        if (cap) cap_scores(v, p.cap_in, cap_log2, row_abs_max(v) * p.cap_in);
-        if (biased) {
+        if (CAP || cap) cap_scores(v, p.cap_in, cap_log2, CAP ? y : row_abs_max(v) * p.cap_in);
+        if (!CAP && biased) {
           const float s0 = cap ? 1.f : p.scale_log2;
-          const int far = k0 + BN - 1 - (C + row);  // > 0: keys behind the query in this tile
+          const int far = k0 + BH - 1 - (C + row);  // > 0: keys behind the query in this tile
           if (__any_sync(0xffffffffu, far > 0 && hi > C + row + 1 && k0 < hi)) {
             const float d0 = (float)(k0 - (C + row));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kChunks; ++i)
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 v.c[i][k] = fmaf(-slope, fabsf(d0 + (float)(32 * i + k)), v.c[i][k] * s0);
           } else {  // every visible key is at or before the query: the bias is linear in the column
-            const uint64_t sl2 = f2(slope, slope), s02 = f2(s0, s0);
-            const float b0 = slope * (float)(k0 - (C + row));
-            const uint64_t b2 = f2(b0, b0);
+            const uint64_t s02 = f2(s0, s0), step = f2(2.f * slope, 2.f * slope);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kChunks; ++i) {
+              const float b0 = slope * (float)(k0 + 32 * i - (C + row));
+              uint64_t bias = f2(b0, b0 + slope);
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
-                const uint64_t bias = ffma2(sl2, f2((float)(32 * i + k), (float)(32 * i + k + 1)), b2);
                 f2u(ffma2(f2(v.c[i][k], v.c[i][k + 1]), s02, bias), v.c[i][k], v.c[i][k + 1]);
+                bias = fadd2(bias, step);
               }
+            }
           }
         }
         if (!whole_tile) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < kChunks; ++i)
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               v.c[i][k] = 32 * i + k >= c0 && 32 * i + k < c1 ? v.c[i][k] : -INFINITY;
         }
-        const float mt = row_max(v) * sc;
         float alpha = 1.f;
-        if (mt > m + kMaxGrowth) {  // the first visible tile, or the scores grew a lot
-          alpha = ex2(m - mt);
-          m = mt;
+        if constexpr (CAP) {
+          if (t == 0) {  // the reference of both halves, for good
+            const float mt = row_max(v);
+            *s_mine = mt;
+            if (pair_any(pair, false)) {  // the partner gave up
+              ok = false;
+              break;
+            }
+            m = fmaxf(fmaxf(mt, *s_other), p.cap_ref);
+          }
+        } else {
+          // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8:
+          // the halves ask each other at one barrier, and exchange their maxima only then.
+          float mt = row_max(v) * sc;
+          if (pair_any(pair, mt > m + kMaxGrowth)) {
+            if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
+              ok = false;
+              break;
+            }
+            *s_mine = mt;
+            pair_sync(pair);
+            mt = fmaxf(mt, *s_other);
+            if (mt > m + kMaxGrowth) {
+              alpha = ex2(m - mt);
+              m = mt;
+            }
+            pair_sync(pair);  // both have read before either writes again
+          }
         }
         const float neg = m == -INFINITY ? 0.f : -m;
         const uint64_t n2 = f2(neg, neg);
         uint64_t sum2 = f2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) exp_chunk(v.c[i], sc2, n2, sum2, tS + 16 * i);
+        for (int i = 0; i < kChunks; ++i) exp_chunk(v.c[i], sc2, n2, sum2, tS + 16 * i);
         tmem_wait_st();
         float s_lo, s_hi;
         f2u(sum2, s_lo, s_hi);
         l = l * alpha + (s_lo + s_hi);
-        if (t > 0) rescale_o<D>(tO, alpha);
+        if (!CAP && t > 0) rescale_o<D / 2>(tO, alpha);
       }
       tc_fence_before();
       __syncwarp();
@@ -681,64 +717,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok)
       ok = __all_sync(0xffffffffu,
                       mbar_wait(bar(Sm::bO + tile), (uint32_t)(ntiles - 1) & 1u, abort_flag, kBudget));
+    if (!ok && lane == 0) fail();
+    ok = !pair_any(pair, !ok);
     if (ok) {
       tc_fence_after();
+      *s_mine = l;
+      pair_sync(pair);
+      l += *s_other;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const long long orow = (long long)(q0 + row) * p.Hq + head;
       // keys of this row within the tiles whose V the guards changed (none, nearly always)
       const int u0 = *(volatile int*)unclean, u1 = *(volatile int*)(unclean + 1);
       const int r0 = u1 < 0 ? 0 : max(lo, key_lo + u0 * BN), r1 = u1 < 0 ? 0 : min(hi, key_lo + (u1 + 1) * BN);
       const bool whole = row - lane + 32 <= q_hi;  // all 32 rows of this warp are real
-      // whole warps stage their rows in shared memory (tile 0 over the Q tiles, free since its last
-      // PV came after the other tile's last QK; tile 1 over the ring, its last PV being the CTA's
-      // last MMA) and write one contiguous output row per store instruction
-      const uint32_t sb = (tile == 0 ? sQ : sKV) + (uint32_t)(q4 * 32 * D * 2);
+      // whole warps stage their half rows in shared memory (tile 0 over the Q tiles, free since its last
+      // PV came after the other tile's last QK; tile 1 over the ring, its last PV being the CTA's last
+      // MMA) and write them out 8 bytes a lane, whole half rows per instruction.  128-byte rows of
+      // 64 columns, 16-byte pieces swizzled by the row; a half is a box of its own (d = 128) or half
+      // of one.
+      const uint32_t sb = (tile == 0 ? sQ : sKV) + (uint32_t)(q4 * 32 * D * 2 + (D == 128 ? half * 4096 : 0));
+      constexpr int kPieces = D / 16;  // of a half row
+      const int piece0 = D == 128 ? 0 : half * kPieces;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 64; ++c) {
+        const int col = half * (D / 2) + c * 32;
         float o[32];
         tmem_ld32(tO + c * 32, o);
         tmem_wait_ld(o);
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] *= inv;
-        if (r0 < r1) restore<D>(o, p.v + (long long)kv0 * p.Hkv * D, (long long)p.Hkv * D, g * D + c * 32, r0, r1);
+        if (r0 < r1) restore<D>(o, p.v + (long long)kv0 * p.Hkv * D, (long long)p.Hkv * D, g * D + col, r0, r1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 x = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
                                      pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
-          if (whole)  // 64-column boxes of 32 rows, 16-byte vectors swizzled by the row
+          if (whole)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             sb + (uint32_t)((c >> 1) * 4096 + lane * 128) +
-                             ((uint32_t)(((c & 1) * 4 + j) ^ (lane & 7)) << 4)),
+                             sb + (uint32_t)(lane * 128) + ((uint32_t)((piece0 + c * 4 + j) ^ (lane & 7)) << 4)),
                          "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                          : "memory");
           else if (valid)
-            *reinterpret_cast<uint4*>(p.out + orow * D + c * 32 + 8 * j) = x;
+            *reinterpret_cast<uint4*>(p.out + orow * D + col + 8 * j) = x;
         }
       }
       if (whole) {
         __syncwarp();
-        constexpr int E = D / 32;  // columns per lane
-        const int col = E * lane, cin = col % 64;
-        const uint32_t a0 = sb + (uint32_t)((col / 64) * 4096 + (cin % 8) * 2);
-        __nv_bfloat16* dst = p.out + ((long long)(q0 + row - lane) * p.Hq + head) * D + col;
+        constexpr int LR = 2 * kPieces, RI = 32 / LR;  // lanes per half row, rows per instruction
+        const int e8 = lane % LR;
+        __nv_bfloat16* dst = p.out + ((long long)(q0 + row - lane) * p.Hq + head) * D + half * (D / 2) + 4 * e8;
 #pragma unroll 8
-        for (int r = 0; r < 32; ++r) {
-          const uint32_t a = a0 + (uint32_t)(r * 128) + ((uint32_t)((cin / 8) ^ (r & 7)) << 4);
-          __nv_bfloat16* q = dst + (long long)r * p.Hq * D;
-          if constexpr (E == 4) {
-            uint2 x;
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
-            *reinterpret_cast<uint2*>(q) = x;
-          } else {
-            uint32_t x;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
-            *reinterpret_cast<uint32_t*>(q) = x;
-          }
+        for (int i = 0; i < 32; i += RI) {
+          const int r = i + lane / LR;
+          uint2 x;
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(x.x), "=r"(x.y)
+                       : "r"(sb + (uint32_t)(r * 128) + ((uint32_t)((piece0 + e8 / 2) ^ (r & 7)) << 4) + (e8 & 1) * 8u));
+          *reinterpret_cast<uint2*>(dst + (long long)r * p.Hq * D) = x;
         }
       }
-      if (valid) p.lse[orow] = l == 0.f ? -INFINITY : (log2f(l) - (m == -INFINITY ? 0.f : -m)) * kLn2;
-    } else if (lane == 0) {
-      fail();
+      if (valid && half == 0) p.lse[orow] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
     }
   }
 
@@ -770,7 +807,7 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   p.softcap = mod.softcap;
   p.cap_in = mod.softcap > 0.f ? scale / mod.softcap : 0.f;
   const float cap_log2 = mod.softcap * kLog2e;
-  p.cap_ref = cap_log2 > kCapRefBelow ? cap_log2 - kCapRefBelow : 0.f;
+  p.cap_ref = cap_log2 - kCapAbove;
   const bool fixed = mod.softcap > 0.f && cap_log2 <= kMaxCapLog2 && p.cap_in >= kMinCapIn && mod.alibi_slopes == nullptr;
   p.cu_q = a.cu_seqlens_q;
   p.cu_kv = a.cu_seqlens_kv;
@@ -789,13 +826,7 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   const dim3 grid(tt ? a.num_q_heads : a.num_q_heads / 2, p.tiles, a.num_seqs);
   auto kern = tt ? (fixed ? prefill_mod_kernel<D, true, true> : prefill_mod_kernel<D, true, false>)
                  : (fixed ? prefill_mod_kernel<D, false, true> : prefill_mod_kernel<D, false, false>);
-  // the register budgets assume the registers a thread of this launch gets; a build that gave the
-  // kernel another count would leave an increase waiting, so refuse it
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, Smem<D>::kAlloc, s>>>(mq, mk, mv, p);
   return cudaGetLastError();
