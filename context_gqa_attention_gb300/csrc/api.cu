@@ -811,7 +811,8 @@ cp_status cp_kv_cache_read(const cp_kv_read_args* a, void* stream) {
 }
 
 static cp_status check_mod(const cp_score_mod* m, bool prefill) {
-  REQUIRE(isfinite(m->softcap) && m->softcap >= 0.f, "softcap must be finite and >= 0");
+  REQUIRE(m->softcap == 0.f || (m->softcap >= 1e-6f && m->softcap <= 1e9f),
+          "softcap must be 0 (none) or within [1e-6, 1e9]");
   REQUIRE(m->window >= 0, "window must be >= 0");
   REQUIRE(prefill || m->prefix_lens == nullptr, "prefix_lens is a prefill argument");
   return CP_OK;
@@ -824,6 +825,8 @@ cp_status cp_attn_prefill_mod(const cp_prefill_args* a, const cp_score_mod* mod,
   if (a->mode != CP_PASS_KV) return fail(CP_ERR_UNSUPPORTED, "modified scores take contiguous k / v (CP_PASS_KV)");
   if (a->impl != CP_IMPL_AUTO && a->impl != CP_IMPL_TCGEN05)
     return fail(CP_ERR_UNSUPPORTED, "impl must be CP_IMPL_AUTO or CP_IMPL_TCGEN05 (got %d)", a->impl);
+  if (a->num_seqs > 65535 || a->max_seqlen_q > 65535 * 128)
+    return fail(CP_ERR_UNSUPPORTED, "at most 65535 sequences of 65535 * 128 new tokens");
   REQUIRE(a->cu_seqlens_q != nullptr, "cu_seqlens_q is null");
   REQUIRE_PTR(a->q);
   st = check_kv_source(a);
@@ -860,18 +863,26 @@ cp_status cp_decode_mod_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t cp,
     const long long w = share_of(window) + page - 1;
     share = share < w ? share : w;
   }
-  // Tokens per CTA: about `most`, fewer where that would leave SMs without work, and no fewer than
-  // a page for each of its four warps.
+  // Tokens per CTA: about `most`, fewer where that would leave SMs without their three CTAs, and no
+  // fewer than a page for each of its four warps.  Short contexts of few sequences: no more than eight
+  // parts, which one cluster merges.
   const long long most = q4 ? 4096 : 2048, least = 4 * page;
-  const long long base = (long long)num_seqs * num_kv_heads * cp;
   long long S = (share + most - 1) / most;
-  const long long want = (8ll * 152 + base - 1) / base;
+  // (three CTAs on each of 152 SMs, in whole clusters of eight parts: one wave, no CTA left over)
+  const long long slots = 3ll * 152 / ((long long)num_seqs * num_kv_heads);
+  const long long one_wave = (slots >= 8 ? slots / 8 * 8 : slots) / cp;
+  // or two waves without clusters, where that leaves each CTA enough to do
+  const long long base = (long long)num_seqs * num_kv_heads * cp, two_waves = (8ll * 152 + base - 1) / base;
+  const long long want = share / two_waves >= (q4 ? 2048 : 512) ? two_waves : one_wave;
   if (S < want) S = want;
+  if (share * cp <= 8 * 512 && S > 8 / cp) S = 8 / cp;
   if (S > (share + least - 1) / least) S = (share + least - 1) / least;
   if (S > 256 / cp) S = 256 / cp;
   if (S < 1) S = 1;
   long long st = (share + S - 1) / S;
-  st = (st + page - 1) / page * page;
+  // whole pages; the 4-bit kernel's four warps take four pages at a time
+  const long long unit = q4 && st > 16 * page ? 16 * page : page;
+  st = (st + unit - 1) / unit * unit;
   S = (share + st - 1) / st;
   *num_splits = (int32_t)S;
   *split_tokens = (int32_t)st;

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_mod_kerne
   constexpr int kRec = 2 * kPage * D;  // bytes of a head's page
   __shared__ __align__(16) WarpParts<D, HR> parts;
   Unit u;
-  if (!take_unit<T, D>(p, u)) return;
+  if (!take_unit<T, D, HR>(p, parts, u)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
 
   // table entries of this warp's pages pg0 + warp + j kWarps, 32 at a time (lane i holds the i-th), a
@@ -265,17 +265,46 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_mod_kerne
 
 // ------------------------------------------------------------------------------ fp32 caches
 // fp32 K and V keep their 24 bits, so the products run on the CUDA cores: two lanes per token for
-// q.k (half a row each), D / 4 lanes per token for P V; per page and warp as above.
+// q.k, alternating over its 16-byte vectors, D / 4 lanes per row for P V.  A page's K vectors are all in
+// flight at once, and refilled with the next page's as soon as the scores are computed; V's likewise
+// after the second product.
 template <int D, int HR>
 __global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModParams p) {
-  constexpr int NCH = D / 4;       // lanes per V row
-  constexpr int TG = 32 / NCH;     // V rows a warp reads at a time
+  constexpr int NCH = D / 4;      // lanes per V row
+  constexpr int TG = 32 / NCH;    // V rows a warp reads at a time
+  constexpr int NK = D / 8, NV = kPage / TG;
   __shared__ __align__(16) WarpParts<D, HR> parts;
   __shared__ __align__(16) float qs[HR][D];
   __shared__ float ps[kWarps][kPage][HR];
   Unit u;
-  if (!take_unit<float, D>(p, u)) return;
+  if (!take_unit<float, D, HR>(p, parts, u)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tk = lane >> 1, half = lane & 1, vc = lane % NCH, vt = lane / NCH;
+  const int32_t* trow = p.tables + ((long long)u.r * p.B + u.b) * p.max_blocks;
+  const int pg1 = (u.l1 + kPage - 1) / kPage;
+  const long long page_stride = (long long)p.Hkv * (kPage * D);
+  const long long unit_base = (long long)u.r * p.pool * page_stride + (long long)u.g * (kPage * D);
+  const float* const kbase = reinterpret_cast<const float*>(p.kc) + unit_base + tk * D + half * 4;
+  const float* const vbase = reinterpret_cast<const float*>(p.vc) + unit_base + vt * D + vc * 4;
+  auto page_of = [&](int pg) -> int {  // -1: none (its tokens are masked)
+    int id = -1;
+    if (pg < pg1 && pg < p.max_blocks) id = __ldg(trow + pg);
+    return id >= 0 && id < p.pool ? id : -1;
+  };
+  float4 k[NK], v[NV];
+  auto load_k = [&](int id) {
+#pragma unroll
+    for (int c = 0; c < NK; ++c) k[c] = __ldg(reinterpret_cast<const float4*>(kbase + id * page_stride) + 2 * c);
+  };
+  auto load_v = [&](int id) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(vbase + id * page_stride + i * TG * D));
+  };
+  int pg = u.l0 / kPage + warp, id = page_of(pg), id_nxt = page_of(pg + kWarps);
+  if (id >= 0) {
+    load_k(id);
+    load_v(id);
+  }
   const float* qg = static_cast<const float*>(p.q) + ((long long)u.b * p.Hq + (long long)u.g * p.G) * D;
   for (int i = threadIdx.x; i < HR * D; i += blockDim.x) (&qs[0][0])[i] = i < p.G * D ? qg[i] : 0.f;
   __syncthreads();
@@ -287,46 +316,37 @@ __global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModPa
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
   }
-  const int32_t* trow = p.tables + ((long long)u.r * p.B + u.b) * p.max_blocks;
-  const int pg1 = (u.l1 + kPage - 1) / kPage;
-  const int tk = lane >> 1, half = lane & 1, vc = lane % NCH, vt = lane / NCH;
   bool bad = false;
-  for (int pg = u.l0 / kPage + warp; pg < pg1; pg += kWarps) {
-    const int id = pg < p.max_blocks ? __ldg(trow + pg) : -1;
-    if (id < 0 || id >= p.pool) {
-      bad = true;
-      continue;
-    }
-    const long long at = (((long long)u.r * p.pool + id) * p.Hkv + u.g) * (kPage * D);
-    const float4* kr = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.kc) + at + tk * D);
-    const float4* vr = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.vc) + at);
+  for (; pg < pg1; pg += kWarps) {
     const int t0 = pg * kPage, t = t0 + tk;
-    const bool on = t >= u.a && t < u.l1;
+    const bool on = id >= 0 && t >= u.a && t < u.l1;
+    bad |= id < 0;
     float s[HR];
 #pragma unroll
     for (int h = 0; h < HR; ++h) s[h] = 0.f;
-#pragma unroll 4
-    for (int c = half; c < D / 4; c += 2) {  // the two lanes of a token alternate over its vectors
-      const float4 k = __ldg(kr + c);
+#pragma unroll
+    for (int c = 0; c < NK; ++c) {
 #pragma unroll
       for (int h = 0; h < HR; ++h) {
-        const float4 q = *reinterpret_cast<const float4*>(&qs[h][4 * c]);
-        s[h] += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+        const float4 q = *reinterpret_cast<const float4*>(&qs[h][8 * c + 4 * half]);
+        s[h] += q.x * k[c].x + q.y * k[c].y + q.z * k[c].z + q.w * k[c].w;
       }
     }
-    const float dist = distance(p, u, t);
+    if (id_nxt >= 0) load_k(id_nxt);
+    const int id_after = page_of(pg + 2 * kWarps);
+    const float dist = p.slopes != nullptr ? distance(p, u, t) : 0.f;
     float alpha[HR];
 #pragma unroll
     for (int h = 0; h < HR; ++h) {
       s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
-      float v = s[h] * p.scale;
-      if (p.softcap > 0.f) v = p.softcap * tanhf(v / p.softcap);
-      if (p.slopes != nullptr && h < p.G) v -= __ldg(p.slopes + u.g * p.G + h) * dist;
-      v = on ? v * kLog2e : -INFINITY;
-      const float m_new = fmaxf(m[h], warp_max(v));
+      float x = s[h] * p.scale;
+      if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
+      if (p.slopes != nullptr && h < p.G) x -= __ldg(p.slopes + u.g * p.G + h) * dist;
+      x = on ? x * kLog2e : -INFINITY;
+      const float m_new = fmaxf(m[h], warp_max(x));
       alpha[h] = m_new == m[h] ? 1.f : exp2f(m[h] - m_new);
       m[h] = m_new;
-      const float e = exp2f(v - (m_new == -INFINITY ? 0.f : m_new));
+      const float e = exp2f(x - (m_new == -INFINITY ? 0.f : m_new));
       l[h] = l[h] * alpha[h] + (half == 0 ? e : 0.f);
       if (half == 0) ps[warp][tk][h] = e;
     }
@@ -335,17 +355,22 @@ __global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModPa
     for (int h = 0; h < HR; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[h][e] *= alpha[h];
-#pragma unroll 4
-    for (int i = vt; i < kPage; i += TG) {
-      if (t0 + i < u.a || t0 + i >= u.l1) continue;  // 0 times whatever lies there could be NaN
-      const float4 v = __ldg(vr + i * NCH + vc);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int r = vt + i * TG;
+      // rows behind the sequence may hold anything, and 0 times NaN is NaN
+      const bool seen = id >= 0 && t0 + r >= u.a && t0 + r < u.l1;
+      const float4 x = seen ? v[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int h = 0; h < HR; ++h) {
-        const float w = ps[warp][i][h];
-        acc[h][0] += w * v.x, acc[h][1] += w * v.y, acc[h][2] += w * v.z, acc[h][3] += w * v.w;
+        const float w = ps[warp][r][h];
+        acc[h][0] += w * x.x, acc[h][1] += w * x.y, acc[h][2] += w * x.z, acc[h][3] += w * x.w;
       }
     }
+    if (id_nxt >= 0) load_v(id_nxt);
     __syncwarp();
+    id = id_nxt;
+    id_nxt = id_after;
   }
   if (bad && lane == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
 #pragma unroll
@@ -366,18 +391,11 @@ __global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModPa
 }
 
 template <int D>
-cudaError_t launch_d(const ModParams& p, int dtype, dim3 grid, cudaStream_t s) {
-  constexpr int n = kWarps * 32;
-  if (dtype == CP_F32) {
-    if (p.G <= 2) decode_mod_f32_kernel<D, 2><<<grid, n, 0, s>>>(p);
-    else if (p.G <= 4) decode_mod_f32_kernel<D, 4><<<grid, n, 0, s>>>(p);
-    else decode_mod_f32_kernel<D, 8><<<grid, n, 0, s>>>(p);
-  } else if (p.G <= 8) {
-    decode_mod_kernel<D, 1><<<grid, n, 0, s>>>(p);
-  } else {
-    decode_mod_kernel<D, 2><<<grid, n, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+cudaError_t launch_d(const ModParams& p, int dtype, cudaStream_t s) {
+  if (dtype == CP_F32)
+    return launch_decode(p.G <= 2 ? decode_mod_f32_kernel<D, 2> : p.G <= 4 ? decode_mod_f32_kernel<D, 4>
+                                                                          : decode_mod_f32_kernel<D, 8>, p, 0, s);
+  return launch_decode(p.G <= 8 ? decode_mod_kernel<D, 1> : decode_mod_kernel<D, 2>, p, 0, s);
 }
 
 }  // namespace
@@ -387,6 +405,5 @@ cudaError_t cp_launch_decode_mod(const cp_decode_args& a, const cp_score_mod& mo
                                  const CpDecodeWorkspace* ws, void* out, float* out_lse, cudaStream_t s) {
   using namespace cpattn;
   const ModParams p = decode_mod_params(a, mod, scale, ws, out, out_lse);
-  return a.head_dim == 64 ? launch_d<64>(p, a.dtype, decode_mod_grid(a), s)
-                          : launch_d<128>(p, a.dtype, decode_mod_grid(a), s);
+  return a.head_dim == 64 ? launch_d<64>(p, a.dtype, s) : launch_d<128>(p, a.dtype, s);
 }

@@ -16,9 +16,12 @@
 // quarter of the traffic the instruction pipes are as near as HBM.  Hence
 //  * a code becomes an MMA operand by one AND for two values (f16 subnormals, see codes());
 //  * the running reference of the softmax moves only when a score exceeds it by 2^8;
-//  * records go to shared memory by cp.async into a ring of each warp's own, two iterations ahead
-//    (loads that fit in registers alone left the warps waiting for DRAM two thirds of the time:
-//    64 sequences of 1024..32768 tokens, 32/8 heads, 349 us), 16 warps per SM.
+//  * whole records (9 d bytes are contiguous) go to a ring of each warp's own in shared memory by the
+//    copy engine, an iteration or two ahead; loads into registers left the warps waiting for DRAM two
+//    thirds of the time (64 sequences of 1024..32768 tokens, 32/8 heads: 349 us), 16-byte cp.async
+//    stopped at 83% of the copy bandwidth and took a tenth of the instructions (277 us);
+//  * several independent pages per iteration keep a warp issuing (Q4Shape): 263 us, 74% of the copy
+//    bandwidth.  What is left is instructions: without its arithmetic the same kernel runs at 95%.
 #include <cuda_fp16.h>
 
 #include "decode_mod.cuh"
@@ -44,19 +47,19 @@ CP_DEV uint32_t codes(uint32_t w) {
   return (J < 2 ? w : w >> 8) & (J % 2 == 0 ? 0x000f000fu : 0x00f000f0u);
 }
 constexpr float kCodeUnit = 16777216.f;  // 2^24: what a code's subnormal is multiplied by
+constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
 constexpr float kMaxFactor = 16384.f;    // f16 factors p scale stay below this many units
 
 // floor(log2 x) of a normal x > 0, and 2^e for e within [-126, 127] (the nearer end outside).
 CP_DEV int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 CP_DEV float pow2(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
-CP_DEV void cp_async16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-CP_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-CP_DEV void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// `bytes` (a multiple of 16) from global to shared memory by the copy engine, completing on an mbarrier.
+CP_DEV void bulk_load(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 CP_DEV uint4 lds128(uint32_t a) {
   uint4 x;
@@ -74,18 +77,19 @@ CP_DEV uint32_t lds32(uint32_t a) {
   return x;
 }
 
-// Tokens and the MMA.  Row r of S^T (r = gid, and gid + 8) is token row_token(r) of the page: V's rows
-// of one load (tid = 0..3) are then tokens tid, tid ^ 5, and 8 more, which with the ring's placement
-// of 16-byte pieces (piece c of a d = 128 row at c ^ 2 in tokens 2, 3, 6, 7, ..) keeps every
-// shared-memory read free of bank conflicts.
+// Tokens and the MMA.  Row r of S^T (r = gid, and gid + 8) is token row_token(r) of the page: K's pieces
+// of eight neighbouring lanes then lie in rows of both parities (no bank conflict), and V's rows of one
+// load (tid = 0..3) are four neighbours.
 CP_DEV int row_token(int r) { return (r >> 1) ^ ((r & 1) * 5); }
 
-// NT: tiles of 8 query heads.  NP: pages per iteration of a warp, two independent ones while their
-// registers fit.
+// NT: tiles of 8 query heads.  NP: pages per iteration of a warp.  Independent pages next to each other
+// are what keeps a warp issuing: four on 12 warps per SM beat two on 16 and one on 16 (d = 128, the batch
+// of 64: 263, 277 and 314 us; d = 64: 189, 193).  Two with a second tile of heads (147 against 163 us).
 template <int D, int NT>
 struct Q4Shape {
-    static constexpr int NP = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT == 1 ? 3 : 4;
+    static constexpr int NP = NT == 1 ? 4 : 2;
+  static constexpr int kStages = NP == 4 ? 2 : 3;
+  static constexpr int kCtas = NT == 1 ? 3 : 2;  // per SM
   static constexpr int kRec = 9 * D;
   static constexpr int kStage = NP * 2 * kRec;              // per warp: [page][K, V]
   static constexpr int kRing = kStages * kWarps * kStage;   // [stage][warp]
@@ -97,7 +101,7 @@ struct Q4Shape {
 };
 
 template <int D, int NT, bool MOD>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) decode_q4_kernel(const ModParams p) {
+__global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q4_kernel(const ModParams p) {
   using T = __nv_bfloat16;
   using Sh = Q4Shape<D, NT>;
   constexpr int NP = Sh::NP, ST = Sh::kStages, REC = Sh::kRec;
@@ -105,8 +109,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) decode_q4_kernel
   constexpr int GR = D / kQ4Group;
   constexpr int KS = D / 16;  // MMAs of each product
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(8) unsigned long long s_bar[kWarps][Sh::kStages];  // a stage's records have landed
+  WarpParts<D, HR>& parts = *reinterpret_cast<WarpParts<D, HR>*>(smem);  // over the ring, at the end
   Unit u;
-  if (!take_unit<T, D>(p, u)) return;
+  if (!take_unit<T, D, HR>(p, parts, u)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   const uint32_t ring = sm100::smem_u32(smem) + (uint32_t)(warp * Sh::kStage);
   auto stage_at = [&](int st) -> uint32_t { return ring + (uint32_t)(st * (kWarps * Sh::kStage)); };
@@ -125,38 +131,43 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) decode_q4_kernel
   int ids = fetch_ids(0), ids_next = fetch_ids(32);
   const int page_stride = p.Hkv * REC;  // Hkv <= 65535: below 2^31
   const long long unit_base = (long long)u.r * p.pool * page_stride + (long long)u.g * REC;
-  const uint8_t* const kl = p.kc + unit_base + 16 * lane;
-  const uint8_t* const vl = p.vc + unit_base + 16 * lane;
-  // the last pieces of K's and V's record (scales) share one instruction: 8 (4) lanes each
-  constexpr int kTail = D / 16;
-  const uint8_t* const tl = lane < kTail ? kl + 8 * D : vl + 8 * D - 16 * kTail;
-  const uint32_t dst_l = D == 128 ? 16u * (uint32_t)(lane ^ (((lane >> 3) & 1) << 1)) : 16u * (uint32_t)lane;
-  const uint32_t dst_t = lane < kTail ? 8u * D + 16u * lane : (uint32_t)REC + 8u * D + 16u * (lane - kTail);
-  uint32_t there = 0u;  // bit stage * NP + i: the page is in the pool (and was copied)
+  const uint8_t* const kb = p.kc + unit_base;
+  const uint8_t* const vb = p.vc + unit_base;
+  const uint32_t bars = sm100::smem_u32(&s_bar[warp][0]);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < ST; ++i) sm100::mbar_init(bars + 8u * i, 1);
+    sm100::fence_mbar_init();
+  }
+  __syncwarp();
+  uint32_t there = 0u;  // bit stage * NP + i: the page is in the pool (and is copied)
   auto issue = [&](int k, int st) {
     if (k < iters) {
       if ((k * NP & 31) == 0 && k > 0) {
         ids = ids_next;
         ids_next = fetch_ids(k * NP + 32);
       }
+      int id[NP], n = 0;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const int id = __shfl_sync(0xffffffffu, ids, (k * NP + i) & 31);
+        id[i] = __shfl_sync(0xffffffffu, ids, (k * NP + i) & 31);
         const uint32_t bit = 1u << (st * NP + i);
-        there = id >= 0 ? there | bit : there & ~bit;
-        if (id >= 0) {
-          const long long at = (long long)id * page_stride;
-          const uint32_t dst = stage_at(st) + (uint32_t)(i * 2 * REC);
+        there = id[i] >= 0 ? there | bit : there & ~bit;
+        n += id[i] >= 0;
+      }
+      const uint32_t bar = bars + 8u * (uint32_t)st;
+      if (lane == 0) {
+        sm100::mbar_expect_tx(bar, (uint32_t)(n * 2 * REC));  // (arrives; 0 bytes when no page is there)
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            cp_async16(dst + dst_l + 512u * c, kl + at + 512 * c);
-            cp_async16(dst + REC + dst_l + 512u * c, vl + at + 512 * c);
+        for (int i = 0; i < NP; ++i)
+          if (id[i] >= 0) {
+            const long long at = (long long)id[i] * page_stride;
+            const uint32_t dst = stage_at(st) + (uint32_t)(i * 2 * REC);
+            bulk_load(dst, kb + at, REC, bar);
+            bulk_load(dst + REC, vb + at, REC, bar);
           }
-          if (lane < 2 * kTail) cp_async16(dst + dst_t, tl + at);
-        }
       }
     }
-    cp_async_commit();
   };
 #pragma unroll
   for (int k = 0; k < ST - 1; ++k) issue(k, k);
@@ -250,10 +261,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) decode_q4_kernel
   constexpr uint32_t kRow = D / 2;
   uint32_t k_at, v0_at, v1_at;
   if constexpr (D == 128) {
-    k_at = (uint32_t)tok * kRow + (uint32_t)((tid ^ (((tok >> 1) & 1) << 1)) << 4);
-    const uint32_t piece = (uint32_t)(((gid >> 1) ^ (((tid >> 1) & 1) << 1)) << 4) + (gid & 1) * 8u;
-    v0_at = (uint32_t)tid * kRow + piece;
-    v1_at = (uint32_t)(tid ^ 5) * kRow + piece;
+    k_at = (uint32_t)tok * kRow + tid * 16u;
+    v0_at = (uint32_t)tid * kRow + gid * 8u;
+    v1_at = (uint32_t)(tid ^ 5) * kRow + gid * 8u;
   } else {
     k_at = (uint32_t)tok * kRow + tid * 8u;
     v0_at = (uint32_t)tid * kRow + gid * 4u;
@@ -270,11 +280,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) decode_q4_kernel
   };
 
   bool bad = false;
-  int st = 0;  // k mod ST
+  int st = 0;           // k mod ST
+  uint32_t phase = 0u;  // k / ST mod 2
   for (int k = 0; k < iters; ++k) {
     issue(k + ST - 1, st == 0 ? ST - 1 : st - 1);  // the stage that the last iteration read
-    cp_async_wait<ST - 1>();
-    __syncwarp();
+    if (!__all_sync(0xffffffffu, sm100::mbar_wait(bars + 8u * (uint32_t)st, phase, nullptr, kBudget))) {
+      if (lane == 0) report(p.err, CP_ERR_TIMEOUT);
+      // what was issued has another chance to land before the shared memory is given up
+      for (int j = k; j < min(k + ST, iters); ++j)
+        sm100::mbar_wait(bars + 8u * (uint32_t)(j % ST), (uint32_t)(j / ST) & 1u, nullptr, kBudget);
+      break;
+    }
     const uint32_t base = stage_at(st);
     int t0[NP];         // first local token of each page
     bool edge = false;  // some token of the pages is not visible
@@ -498,13 +514,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) decode_q4_kernel
     }
     __syncwarp();  // every lane has read the stage
     st = st + 1 == ST ? 0 : st + 1;
+    if (st == 0) phase ^= 1u;
   }
   if (bad && lane == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
 
   // ---- this warp's part: sums over the lanes that share a column, output rows per head
-  cp_async_wait<0>();
-  __syncthreads();  // the ring is free
-  WarpParts<D, HR>& parts = *reinterpret_cast<WarpParts<D, HR>*>(smem);
+  __syncthreads();  // every copy has landed and been read: the ring is free
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -530,13 +545,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) decode_q4_kernel
 }
 
 template <int D, int NT>
-cudaError_t launch_nt(const ModParams& p, bool mod, dim3 grid, cudaStream_t s) {
+cudaError_t launch_nt(const ModParams& p, bool mod, cudaStream_t s) {
   auto kern = mod ? decode_q4_kernel<D, NT, true> : decode_q4_kernel<D, NT, false>;
   constexpr int bytes = Q4Shape<D, NT>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  kern<<<grid, kWarps * 32, bytes, s>>>(p);
-  return cudaGetLastError();
+  return e == cudaSuccess ? launch_decode(kern, p, bytes, s) : e;
 }
 
 }  // namespace
@@ -547,7 +560,6 @@ cudaError_t cp_launch_decode_q4(const cp_decode_args& a, const cp_score_mod& mod
   using namespace cpattn;
   const ModParams p = decode_mod_params(a, mod, scale, ws, out, out_lse);
   const bool m = changes_scores(mod);
-  const dim3 grid = decode_mod_grid(a);
-  if (a.head_dim == 64) return p.G <= 8 ? launch_nt<64, 1>(p, m, grid, s) : launch_nt<64, 2>(p, m, grid, s);
-  return p.G <= 8 ? launch_nt<128, 1>(p, m, grid, s) : launch_nt<128, 2>(p, m, grid, s);
+  if (a.head_dim == 64) return p.G <= 8 ? launch_nt<64, 1>(p, m, s) : launch_nt<64, 2>(p, m, s);
+  return p.G <= 8 ? launch_nt<128, 1>(p, m, s) : launch_nt<128, 2>(p, m, s);
 }

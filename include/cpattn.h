@@ -414,7 +414,7 @@ int64_t cp_q4_record_bytes(int32_t head_dim);
  * p * inv_freq[j], j < rot_dim / 2.  Pair j of a q or k head, dims (j, j + rot_dim / 2)
  * (CP_ROPE_HALF) or (2 j, 2 j + 1) (CP_ROPE_PAIRS), becomes (x cos - y sin, y cos + x sin); dims
  * from rot_dim on stay.  V is not rotated.  Whole turns are dropped exactly, so far positions keep
- * full fp32 accuracy; results are rounded once, to `dtype`, or quantised from fp32 (cache_q4).
+ * their accuracy; results are rounded once, to `dtype`, or quantised from fp32 (cache_q4).
  * Rotated queries go to q_out; rotated keys go to the cache and, if k_out is given, there too.
  *   - q, k, v, q_out may be rows of a wider tensor: token t starts `*_stride` elements after token
  *     t - 1 (a fused projection's columns); the strides in bytes are multiples of 16.
@@ -422,6 +422,8 @@ int64_t cp_q4_record_bytes(int32_t head_dim);
  *     rot_dim = 0 with inv_freq NULL appends without rotating.
  *   - rows from cu_new[B] on (a padded batch) are neither read nor written, and a row with a
  *     negative position is skipped and reported.
+ *   - bf16 rows take their cosines and sines from the special-function unit (off by 2^-21 at most, far
+ *     below their own rounding), fp32 rows from the full-accuracy functions.
  *   - err: CP_ERR_DEVICE_BOUNDS for a row whose table entry is missing or outside the pool (its K/V
  *     are not written).  Rows that map to the same slot race.
  * ---------------------------------------------------------------------------- */
@@ -508,7 +510,7 @@ cp_status cp_kv_cache_read(const cp_kv_read_args* args, void* stream);
  * touch it, whatever they hold.
  * ---------------------------------------------------------------------------- */
 typedef struct cp_score_mod {
-  float softcap;                /* 0: none; finite, >= 0                                */
+  float softcap;                /* 0: none, else within [1e-6, 1e9]                     */
   int32_t window;               /* 0: none                                              */
   const float* alibi_slopes;    /* device f32 [Hq] or NULL                              */
   const int32_t* kv_start;      /* device: decode [B], prefill [Nq] (token-major); or NULL */
@@ -531,7 +533,7 @@ cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* m
 /* ------------------------------------------------------------------------------
  * Decode with modified scores (cp_partial_attn_decode_mod, cp_decode_attention_mod) and over the
  * 4-bit cache (cp_partial_attn_decode_q4, cp_decode_attention_q4; their args->dtype, the type of q
- * and out, is CP_BF16).  Arguments as in cp_partial_attn_decode / cp_decode_attention plus `mod`
+ * and out, is CP_BF16, and components of q are below 2^100).  Arguments as in cp_partial_attn_decode / cp_decode_attention plus `mod`
  * (NULL: none; prefix_lens must be NULL: a prefix is behind the query here).
  *
  * Splits are counted within the visible tokens: split s of a rank covers split_tokens local tokens

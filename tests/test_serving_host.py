@@ -88,6 +88,7 @@ DECODE = dict(dtype=1, num_seqs=2, num_q_heads=8, num_kv_heads=2, head_dim=128, 
     (dict(num_q_heads=7), {}, 1), (dict(split_tokens=40), {}, 1), (dict(num_splits=0), {}, 1),
     (dict(q=None), {}, 1), (dict(k_cache=ODD), {}, 1), (dict(seq_lens=None), {}, 1),
     ({}, dict(softcap=-1.0), 1), ({}, dict(softcap=math.inf), 1), ({}, dict(softcap=math.nan), 1),
+    ({}, dict(softcap=1e-9), 1), ({}, dict(softcap=1e12), 1),
     ({}, dict(window=-1), 1), ({}, dict(prefix_lens=P), 1),
 ])
 def test_decode_refusals(lib, name, bad, mod, status):
@@ -122,6 +123,7 @@ PREFILL = dict(mode=0, dtype=1, impl=0, num_seqs=1, num_q_heads=8, num_kv_heads=
     (dict(head_dim=32), {}, 2), (dict(num_q_heads=7), {}, 1), (dict(q_shard=0), {}, 1), (dict(k=None), {}, 1),
     (dict(v=ODD), {}, 1), (dict(cu_seqlens_q=None), {}, 1), (dict(debug=1), {}, 1),
     (dict(cu_seqlens_kv=P, total_kv=0), {}, 1), ({}, dict(softcap=-0.5), 1), ({}, dict(window=-2), 1),
+    (dict(num_seqs=70000), {}, 2), (dict(max_seqlen_q=1 << 24), {}, 2),
 ])
 def test_prefill_refusals(lib, bad, mod, status):
     a = _fill(_fill(cpa.PrefillArgs(), PREFILL), bad)
@@ -145,20 +147,29 @@ def test_the_binding_refuses_host_tensors():
         cpa.cp_rope_kv_cache_write(x, x, x, x, x, x, x, 1, 8)
 
 
+def _local_len(L, r, cp, I):
+    return L // (I * cp) * I + min(max(L % (I * cp) - r * I, 0), I)
+
+
+def test_local_len_is_the_deal():
+    for cp, I in [(1, 8), (2, 8), (3, 5), (8, 1)]:
+        for L in (0, 1, 17, 200):
+            assert [_local_len(L, r, cp, I) for r in range(cp)] == orc.local_lengths([L], cp, I)[:, 0].tolist()
+
+
 @pytest.mark.parametrize("B,Hkv", [(1, 1), (1, 8), (7, 2), (64, 8)])
 @pytest.mark.parametrize("cp,I", [(1, 8), (2, 8), (3, 5), (8, 1), (64, 16)])
 @pytest.mark.parametrize("q4", [False, True])
 def test_the_plan_covers_every_rank(lib, B, Hkv, cp, I, q4):
-    for L in (1, 15, 16, 17, 333, 1777, 32768, 1 << 20):
+    for L in (1, 15, 16, 17, 333, 1777, 32768, 1 << 20, (1 << 31) - 1):
         for W in (0, 1, 16, 100, 4096):
             S, st = cpa.cp_decode_mod_plan(B, Hkv, cp, I, L, window=W, q4=q4)
             assert S >= 1 and st >= 16 and st % 16 == 0 and cp * S <= 256
             for n in {L, max(1, L - 7), max(1, L // 2)}:        # any sequence up to the longest
                 lo = max(0, n - W) if W else 0
-                end, first = orc.local_lengths([n], cp, I)[:, 0], orc.local_lengths([lo], cp, I)[:, 0]
                 for r in range(cp):
-                    if first[r] < end[r]:
-                        assert end[r] - first[r] // 16 * 16 <= S * st, (L, W, n, r)
+                    end, first = _local_len(n, r, cp, I), _local_len(lo, r, cp, I)
+                    assert first >= end or end - first // 16 * 16 <= S * st, (L, W, n, r)
 
 
 def test_plan_refusals(lib):
