@@ -2,7 +2,9 @@
 context-parallel shards, LSE merge and the CP layout maps, on one GB300 (sm_103a).
 
 Argument marshalling only: every function below checks tensor placement, dtype and shape,
-then calls the C entry point of the same name on the current torch CUDA stream.  All the
+then calls the C entry point of the same name on the current torch CUDA stream (the serving
+calls -- rotate-and-append, read-back, 4-bit decode, modified scores -- do both in the native
+module built from csrc/binding.cpp).  All the
 arithmetic runs in the library's CUDA kernels; there is no fallback.  A missing or unbuilt
 library raises ``CPError``.
 
@@ -13,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 import threading
@@ -105,7 +108,7 @@ class KvReadArgs(ctypes.Structure):
                                    "v_out", "err")]
 
 
-_LIB = None
+_LIB = _BINDING = None
 
 # (name, restype, argtypes)
 _SIGS = [
@@ -183,8 +186,26 @@ def load(build_if_missing: bool = False):
                          ("cp_score_mod", ScoreMod)):
         if getattr(lib, name + "_size")() != ctypes.sizeof(struct):
             raise CPError(1, f"{name} layout mismatch between binding and library")
+    _load_binding()
     _LIB = lib
     return lib
+
+
+def _load_binding():
+    global _BINDING
+    if not os.path.exists(_build.BINDING):
+        raise CPError(3, f"{_build.BINDING} is missing: build it first "
+                         "(python -c 'import __graft_entry__ as g; g.build()')")
+    spec = importlib.util.spec_from_file_location("cpattn_binding", _build.BINDING)
+    _BINDING = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_BINDING)
+    _BINDING.set_error(CPError)
+
+
+def _binding():
+    if _BINDING is None:
+        load()
+    return _BINDING
 
 
 def _check(st):
@@ -628,48 +649,18 @@ def cp_q4_record_bytes(head_dim):
     return _LIB.cp_q4_record_bytes(head_dim)
 
 
-def _shape(t, name, shape):
-    if t.shape != shape:
-        raise CPError(1, f"{name} must be {list(shape)} (got {list(t.shape)})")
+_TYPE = {None: -1, torch.float32: CP_F32, torch.bfloat16: CP_BF16}
 
 
-def _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, dtype):
-    """Checks of the paged pools and their tables; whether they hold 4-bit records (uint8)."""
-    q4 = k_cache.dtype == torch.uint8
-    shape = k_cache.shape
-    if len(shape) != (4 if q4 else 5):
-        raise CPError(1, "k_cache must be [cp, pool, Hkv, 16, d], or uint8 [cp, pool, Hkv, 9 d] (4-bit)")
-    _dev(k_cache, "k_cache", None if q4 else dtype)
-    _dev(v_cache, "v_cache", k_cache.dtype)
-    _dev(block_tables, "block_tables", torch.int32)
-    if shape[0] != cp or shape[-1] != (9 * d if q4 else d) or (Hkv is not None and shape[2] != Hkv):
-        raise CPError(1, f"k_cache is {list(shape)}: cp = {cp}, head_dim = {d} and {Hkv or 'any number of'} "
-                         "kv heads want another shape")
-    _shape(v_cache, "v_cache", shape)
-    tables = block_tables.shape
-    if len(tables) != 3 or tables[0] != cp or tables[1] != B:
-        raise CPError(1, f"block_tables must be [cp, B, max_blocks] = [{cp}, {B}, ..] (got {list(tables)})")
-    return q4
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-def _token_rows(t, name, dtype):
-    """A [N, H, d] tensor whose heads are dense within a token; its token stride."""
-    if not t.is_cuda or t.device != _CALL.device:
-        raise CPError(1, f"{name} must be a CUDA tensor on {_CALL.device}")
-    if t.dim() != 3 or t.dtype != dtype:
-        raise CPError(1, f"{name} must be a {dtype} tensor [N, H, d]")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
-        raise CPError(1, f"the heads of a token of {name} must be contiguous (only the token stride is free)")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _on_gpu(name, first):
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise CPError(1, f"{name}: the first argument must be a CUDA tensor")
 
 
-def _index(t, name, n):
-    _dev(t, name, torch.int32)
-    if t.numel() != n:
-        raise CPError(1, f"{name} must have {n} entries (got {t.numel()})")
-
-
-@_on_first_tensors_device
 def cp_rope_kv_cache_write(k_new, v_new, cu_new, start_pos, k_cache, v_cache, block_tables, cp,
                            interleave, *, inv_freq=None, rope_style=CP_ROPE_HALF, q=None, q_out=None,
                            k_out=None, err=None, stream=None):
@@ -680,43 +671,10 @@ def cp_rope_kv_cache_write(k_new, v_new, cu_new, start_pos, k_cache, v_cache, bl
     records).  inv_freq: float64 CUDA tensor [rot_dim / 2] of radians per position (None: no
     rotation).  k_new, v_new and q may be column slices of a wider tensor (any token stride).
     q_out may be q.  Returns (q_out or None, k_out or None); k_out is written only if given."""
-    load()
-    N, Hkv, d = k_new.shape
-    B = cu_new.numel() - 1
-    k_stride = _token_rows(k_new, "k_new", k_new.dtype)
-    v_stride = _token_rows(v_new, "v_new", k_new.dtype)
-    _shape(v_new, "v_new", (N, Hkv, d))
-    _index(cu_new, "cu_new", B + 1)
-    _index(start_pos, "start_pos", B)
-    q4 = _paged(k_cache, v_cache, block_tables, cp, B, d, Hkv, k_new.dtype)
-    rot_dim = Hq = q_stride = q_out_stride = 0
-    if inv_freq is not None:
-        _dev(inv_freq, "inv_freq", torch.float64)
-        rot_dim = 2 * inv_freq.numel()
-    if q is not None:
-        q_stride, Hq = _token_rows(q, "q", k_new.dtype), q.shape[1]
-        _shape(q, "q", (N, Hq, d))
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        q_out_stride = _token_rows(q_out, "q_out", q.dtype)
-        _shape(q_out, "q_out", (N, Hq, d))
-    elif q_out is not None:
-        raise CPError(1, "q_out without q")
-    if k_out is not None:
-        _dev(k_out, "k_out", k_new.dtype)
-        _shape(k_out, "k_out", (N, Hkv, d))
-    _dev(err, "err", torch.int32)
-    a = RopeWriteArgs(_cp_dtype(k_new), q4, B, N, Hq, Hkv, d, cp, interleave, 16 if q4 else k_cache.shape[3],
-                      block_tables.shape[2], rope_style, rot_dim, 0, k_cache.shape[1], q_stride, k_stride,
-                      v_stride, q_out_stride, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cu_new), _ptr(start_pos),
-                      _ptr(inv_freq), _ptr(block_tables), _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _ptr(k_out),
-                      _ptr(err))
-    if N:
-        _check(_LIB.cp_rope_kv_cache_write(ctypes.byref(a), _stream(stream)))
-    return q_out, k_out
+    return _binding().rope_write(k_new, v_new, cu_new, start_pos, k_cache, v_cache, block_tables, cp, interleave,
+                                 inv_freq, rope_style, q, q_out, k_out, err, _handle(stream))
 
 
-@_on_first_tensors_device
 def cp_kv_cache_read(k_cache, v_cache, cu_out, start_pos, block_tables, cp, interleave, *, total=None,
                      out_dtype=None, k_out=None, v_out=None, err=None, stream=None):
     """Positions start_pos[b] + i of every sequence from the paged round-robin cache to contiguous
@@ -724,48 +682,16 @@ def cp_kv_cache_read(k_cache, v_cache, cu_out, start_pos, block_tables, cp, inte
     a cached context.  4-bit records (uint8 pools) come back as the values they stand for, in
     out_dtype (bf16 or f32; the pools' own dtype otherwise).  total: N, when cu_out[B] is not to be
     fetched from the device.  Returns (k_out, v_out)."""
-    load()
-    B = cu_out.numel() - 1
-    q4 = k_cache.dtype == torch.uint8
-    d = k_cache.shape[-1] // 9 if q4 else k_cache.shape[-1]
-    if out_dtype is None:
-        out_dtype = k_out.dtype if k_out is not None else torch.bfloat16 if q4 else k_cache.dtype
-    if not q4 and out_dtype != k_cache.dtype:
-        raise CPError(1, f"out_dtype must be the cache's {k_cache.dtype} (got {out_dtype})")
-    _paged(k_cache, v_cache, block_tables, cp, B, d, None, k_cache.dtype)
-    Hkv = k_cache.shape[2]
-    _index(cu_out, "cu_out", B + 1)
-    _index(start_pos, "start_pos", B)
-    _dev(err, "err", torch.int32)
+    binding = _binding()
     if total is None:
-        total = k_out.shape[0] if k_out is not None else int(cu_out[-1].item())
-    if k_out is None:
-        k_out = k_cache.new_empty((total, Hkv, d), dtype=out_dtype)
-    if v_out is None:
-        v_out = k_cache.new_empty((total, Hkv, d), dtype=out_dtype)
-    for n, t in (("k_out", k_out), ("v_out", v_out)):
-        _dev(t, n, out_dtype)
-        _shape(t, n, (total, Hkv, d))
-    a = KvReadArgs(_cp_dtype(k_out), q4, B, total, Hkv, d, cp, interleave, 16 if q4 else k_cache.shape[3],
-                   block_tables.shape[2], k_cache.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                   _ptr(cu_out), _ptr(start_pos), _ptr(k_out), _ptr(v_out), _ptr(err))
-    if total:
-        _check(_LIB.cp_kv_cache_read(ctypes.byref(a), _stream(stream)))
-    return k_out, v_out
+        _on_gpu("cp_kv_cache_read", k_cache)
+        total = -1 if k_out is not None else int(cu_out[-1].item())
+    if out_dtype not in _TYPE:
+        raise CPError(2, f"unsupported dtype {out_dtype}")
+    return binding.kv_read(k_cache, v_cache, cu_out, start_pos, block_tables, cp, interleave, total,
+                           _TYPE[out_dtype], k_out, v_out, err, _handle(stream))
 
 
-def _score_mod(Hq, softcap, window, alibi_slopes, kv_start, rows, prefix_lens=None, B=0):
-    if alibi_slopes is not None:
-        _dev(alibi_slopes, "alibi_slopes", torch.float32)
-        _shape(alibi_slopes, "alibi_slopes", (Hq,))
-    if kv_start is not None:
-        _index(kv_start, "kv_start", rows)
-    if prefix_lens is not None:
-        _index(prefix_lens, "prefix_lens", B)
-    return ScoreMod(softcap, window, _ptr(alibi_slopes), _ptr(kv_start), _ptr(prefix_lens))
-
-
-@_on_first_tensors_device
 def cp_attn_prefill_mod(q, cu_seqlens_q, k, v, *, cu_seqlens_kv=None, softcap=0.0, window=0,
                         alibi_slopes=None, kv_start=None, prefix_lens=None, max_seqlen_q=None,
                         softmax_scale=0.0, out=None, out_lse=None, err=None, stream=None):
@@ -773,36 +699,12 @@ def cp_attn_prefill_mod(q, cu_seqlens_q, k, v, *, cu_seqlens_kv=None, softcap=0.
     tanh cap, a distance bias alibi_slopes f32 [Hq], a sliding window, kv_start int32 [Nq] (first
     visible position of each row: its document) and prefix_lens int32 [B] (keys every query sees).
     bf16.  Returns (out [Nq, Hq, d] bf16, lse [Nq, Hq] f32)."""
-    load()
-    Nq, Hq, d = q.shape
-    B = cu_seqlens_q.numel() - 1
-    if out is None:
-        out = q.new_empty(q.shape)
-    if out_lse is None:
-        out_lse = q.new_empty((Nq, Hq), dtype=torch.float32)
-    for n, t, dt in (("q", q, torch.bfloat16), ("cu_seqlens_q", cu_seqlens_q, torch.int32),
-                     ("out", out, torch.bfloat16), ("out_lse", out_lse, torch.float32),
-                     ("err", err, torch.int32)):
-        _dev(t, n, dt)
-    _shape(out, "out", (Nq, Hq, d))
-    _shape(out_lse, "out_lse", (Nq, Hq))
+    binding = _binding()
     if max_seqlen_q is None:
-        max_seqlen_q = int((cu_seqlens_q[1:] - cu_seqlens_q[:-1]).max().item()) if B else 0
-    a = PrefillArgs()
-    a.mode, a.dtype, a.impl = CP_PASS_KV, CP_BF16, CP_IMPL_AUTO
-    a.num_seqs, a.num_q_heads, a.head_dim, a.cp = B, Hq, d, 1
-    a.softmax_scale, a.total_q, a.max_seqlen_q = softmax_scale, Nq, max_seqlen_q
-    a.q_shard = a.kv_shard = -1
-    a.cu_seqlens_q, a.q, a.err = _ptr(cu_seqlens_q), _ptr(q), _ptr(err)
-    _kv_source(a, k, v, cu_seqlens_kv, torch.bfloat16)
-    if k.dim() != 3 or k.shape[2] != d or (cu_seqlens_kv is None and k.shape[0] != Nq):
-        raise CPError(1, f"k and v must be [Nkv, Hkv, {d}] (Nkv = {Nq} without cu_seqlens_kv)")
-    if cu_seqlens_kv is not None:
-        _index(cu_seqlens_kv, "cu_seqlens_kv", B + 1)
-    m = _score_mod(Hq, softcap, window, alibi_slopes, kv_start, Nq, prefix_lens, B)
-    _check(_LIB.cp_attn_prefill_mod(ctypes.byref(a), ctypes.byref(m), _ptr(out), _ptr(out_lse),
-                                    _stream(stream)))
-    return out, out_lse
+        _on_gpu("cp_attn_prefill_mod", q)
+        max_seqlen_q = int(cu_seqlens_q.diff().max().item()) if cu_seqlens_q.numel() > 1 else 0
+    return binding.prefill(q, cu_seqlens_q, k, v, cu_seqlens_kv, softcap, window, alibi_slopes, kv_start, prefix_lens,
+                           max_seqlen_q, softmax_scale, out, out_lse, err, _handle(stream))
 
 
 def cp_decode_mod_plan(num_seqs, num_kv_heads, cp, interleave, max_seq_len, *, window=0, q4=False):
@@ -814,74 +716,16 @@ def cp_decode_mod_plan(num_seqs, num_kv_heads, cp, interleave, max_seq_len, *, w
     return ns.value, st.value
 
 
-def _decode_mod_args(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, q4, softcap, window,
-                     alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens, softmax_scale, err):
-    if q.dim() != 3:
-        raise CPError(1, "q must be [B, Hq, d]")
-    B, Hq, d = q.shape
-    _dev(q, "q")
-    if _paged(k_cache, v_cache, block_tables, cp, B, d, None, q.dtype) != q4:
-        raise CPError(1, "uint8 pools hold 4-bit records (the *_q4 calls); the *_mod calls take pools of q's dtype")
-    _index(seq_lens, "seq_lens", B)
-    _dev(err, "err", torch.int32)
-    Hkv = k_cache.shape[2]
-    if num_splits is None or split_tokens is None:
-        if max_seq_len is None:
-            max_seq_len = max(1, int(seq_lens.max().item()))
-        num_splits, split_tokens = cp_decode_mod_plan(B, Hkv, cp, interleave, max_seq_len, window=window,
-                                                      q4=q4)
-    a = DecodeArgs(_cp_dtype(q), B, Hq, Hkv, d, cp, interleave, 16 if q4 else k_cache.shape[3], num_splits,
-                   split_tokens, softmax_scale, block_tables.shape[2], k_cache.shape[1], _ptr(q), _ptr(k_cache),
-                   _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens), None, None, _ptr(err))
-    return a, _score_mod(Hq, softcap, window, alibi_slopes, kv_start, B)
+def _splits(q, seq_lens, max_seq_len, num_splits, split_tokens):
+    """(longest sequence to plan for or 0, num_splits, split_tokens) of a decode call's arguments."""
+    if num_splits is not None and split_tokens is not None:
+        return 0, num_splits, split_tokens
+    if max_seq_len is None:
+        _on_gpu("decode", q)
+        max_seq_len = max(1, int(seq_lens.max().item()))
+    return max_seq_len, 0, 0
 
 
-def _partial_decode(call, q4, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
-                    window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
-                    softmax_scale, out, lse, err, stream):
-    a, m = _decode_mod_args(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, q4, softcap,
-                            window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
-                            softmax_scale, err)
-    P, (B, Hq, d) = cp * a.num_splits, q.shape
-    if out is None:
-        out = torch.empty(P, B, Hq, d, dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty(P, B, Hq, dtype=torch.float32, device=q.device)
-    _dev(out, "out", torch.float32)
-    _dev(lse, "lse", torch.float32)
-    _shape(out, "out", (P, B, Hq, d))
-    _shape(lse, "lse", (P, B, Hq))
-    a.out, a.lse = _ptr(out), _ptr(lse)
-    _check(call(ctypes.byref(a), ctypes.byref(m), _stream(stream)))
-    return out, lse
-
-
-def _fused_decode(call, q4, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
-                  window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
-                  softmax_scale, workspace, out, out_lse, want_lse, err, stream):
-    a, m = _decode_mod_args(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, q4, softcap,
-                            window, alibi_slopes, kv_start, max_seq_len, num_splits, split_tokens,
-                            softmax_scale, err)
-    B, Hq, d = q.shape
-    if workspace is None:
-        need = cp_decode_workspace_size(B, Hq, a.num_kv_heads, d, cp, a.num_splits)
-        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    if out is None:
-        out = q.new_empty(q.shape)
-    if out_lse is None and want_lse:
-        out_lse = q.new_empty((B, Hq), dtype=torch.float32)
-    _dev(workspace, "workspace", torch.uint8)
-    _dev(out, "out", q.dtype)
-    _shape(out, "out", (B, Hq, d))
-    if out_lse is not None:
-        _dev(out_lse, "out_lse", torch.float32)
-        _shape(out_lse, "out_lse", (B, Hq))
-    _check(call(ctypes.byref(a), ctypes.byref(m), _ptr(workspace), workspace.numel(), _ptr(out),
-                _ptr(out_lse), _stream(stream)))
-    return out, out_lse
-
-
-@_on_first_tensors_device
 def cp_partial_attn_decode_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
                                softcap=0.0, window=0, alibi_slopes=None, kv_start=None,
                                max_seq_len=None, num_splits=None, split_tokens=None,
@@ -889,13 +733,13 @@ def cp_partial_attn_decode_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, 
     """cp_partial_attn_decode with modified scores (see cpattn.h): a tanh cap, a sliding window, a
     distance bias alibi_slopes f32 [Hq] and kv_start int32 [B] (first visible position).
     Returns (out [P, B, Hq, d], lse [P, B, Hq]), P = cp * num_splits."""
-    load()
-    return _partial_decode(_LIB.cp_partial_attn_decode_mod, False, q, k_cache, v_cache, block_tables,
-                           seq_lens, cp, interleave, softcap, window, alibi_slopes, kv_start,
-                           max_seq_len, num_splits, split_tokens, softmax_scale, out, lse, err, stream)
+    binding = _binding()
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    return binding.decode_partial(False, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
+                                  window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
+                                  softmax_scale, err, _handle(stream), out, lse)
 
 
-@_on_first_tensors_device
 def cp_decode_attention_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
                             softcap=0.0, window=0, alibi_slopes=None, kv_start=None,
                             max_seq_len=None, num_splits=None, split_tokens=None, softmax_scale=0.0,
@@ -903,38 +747,38 @@ def cp_decode_attention_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, int
                             stream=None):
     """cp_decode_attention with modified scores (see cp_partial_attn_decode_mod and cpattn.h).
     Returns (out [B, Hq, d] dtype of q, lse [B, Hq] f32 or None)."""
-    load()
-    return _fused_decode(_LIB.cp_decode_attention_mod, False, q, k_cache, v_cache, block_tables,
-                         seq_lens, cp, interleave, softcap, window, alibi_slopes, kv_start,
-                         max_seq_len, num_splits, split_tokens, softmax_scale, workspace, out, out_lse,
-                         want_lse, err, stream)
+    binding = _binding()
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    return binding.decode_fused(False, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
+                                window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
+                                softmax_scale, err, _handle(stream), workspace, out, out_lse, want_lse)
 
 
-@_on_first_tensors_device
 def cp_partial_attn_decode_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
                               softcap=0.0, window=0, alibi_slopes=None, kv_start=None,
                               max_seq_len=None, num_splits=None, split_tokens=None,
                               softmax_scale=0.0, out=None, lse=None, err=None, stream=None):
     """cp_partial_attn_decode over the 4-bit cache, uint8 [cp, pool, Hkv, 9 d] (see cpattn.h), bf16
     queries; scores may be modified as in cp_partial_attn_decode_mod."""
-    load()
-    return _partial_decode(_LIB.cp_partial_attn_decode_q4, True, q, k_cache, v_cache, block_tables,
-                           seq_lens, cp, interleave, softcap, window, alibi_slopes, kv_start,
-                           max_seq_len, num_splits, split_tokens, softmax_scale, out, lse, err, stream)
+    binding = _binding()
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    return binding.decode_partial(True, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
+                                  window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
+                                  softmax_scale, err, _handle(stream), out, lse)
 
 
-@_on_first_tensors_device
 def cp_decode_attention_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, *,
-                           softcap=0.0, window=0, alibi_slopes=None, kv_start=None, max_seq_len=None,
-                           num_splits=None, split_tokens=None, softmax_scale=0.0, workspace=None,
-                           out=None, out_lse=None, want_lse=True, err=None, stream=None):
+                           softcap=0.0, window=0, alibi_slopes=None, kv_start=None,
+                           max_seq_len=None, num_splits=None, split_tokens=None, softmax_scale=0.0,
+                           workspace=None, out=None, out_lse=None, want_lse=True, err=None,
+                           stream=None):
     """cp_decode_attention over the 4-bit cache, uint8 [cp, pool, Hkv, 9 d] (see cpattn.h), bf16
     queries; scores may be modified as in cp_partial_attn_decode_mod."""
-    load()
-    return _fused_decode(_LIB.cp_decode_attention_q4, True, q, k_cache, v_cache, block_tables, seq_lens,
-                         cp, interleave, softcap, window, alibi_slopes, kv_start, max_seq_len,
-                         num_splits, split_tokens, softmax_scale, workspace, out, out_lse, want_lse,
-                         err, stream)
+    binding = _binding()
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    return binding.decode_fused(True, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
+                                window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
+                                softmax_scale, err, _handle(stream), workspace, out, out_lse, want_lse)
 
 
 def default_scale(head_dim):

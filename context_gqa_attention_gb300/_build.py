@@ -1,16 +1,20 @@
-"""In-tree build of libcpattn.so for sm_103a (nvcc, one object per source, parallel)."""
+"""In-tree build for sm_103a: libcpattn.so (nvcc, one object per source, parallel) and the Python
+binding of its serving calls (the host compiler, against the torch that is installed)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libcpattn.so")
+BINDING = os.path.join(OUT_DIR, "cpattn_binding.so")
 SOURCES = ["api.cu", "prefill_simt.cu", "prefill_tc.cu", "decode.cu", "noalloc.cu",
            "cache.cu", "decode_mod.cu", "decode_q4.cu", "prefill_mod.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -26,7 +30,7 @@ def _nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
+    files = [os.path.join(CSRC, s) for s in SOURCES + ["binding.cpp"]]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "cpattn.h"))
     files.append(os.path.abspath(__file__))
@@ -34,14 +38,14 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu for sm_103a and link libcpattn.so next to this file."""
+    """Compile csrc/*.cu for sm_103a and link libcpattn.so, and the binding, next to this file."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
@@ -56,17 +60,40 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cxx = os.environ.get("CXX") or "g++"
+    binding_obj = os.path.join(OUT_DIR, "binding.o")
+
+    def compile_binding():
+        cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE]
+        for d in (sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+                  os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")):
+            cmd += ["-isystem", d]
+        r = subprocess.run([*cmd, "-c", os.path.join(CSRC, "binding.cpp"), "-o", binding_obj], capture_output=True,
+                           text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cxx} failed on binding.cpp:\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         for obj, log in ex.map(compile_one, SOURCES):
             objs.append(obj)
             if verbose and log:
                 print(log)
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    cmd = [cxx, "-shared", "-o", tmp, binding_obj, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", OUT_DIR, "-lcpattn", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
