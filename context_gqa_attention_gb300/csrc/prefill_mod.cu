@@ -64,7 +64,7 @@ struct Smem {
   static constexpr int oKV = 2 * kQ;
   static constexpr int oBar = oKV + kSlots * kKV;
   static constexpr int bQ = 0, bFull = 1, bEmpty = bFull + kSlots, bS = bEmpty + kSlots, bP = bS + 2,
-                       bO = bP + 2, bFix = bO + 2, bDone = bFix + 2, nBar = bDone + 1;
+                       bO = bP + 4, bFix = bO + 2, bDone = bFix + 2, nBar = bDone + 1;
   static constexpr int oMisc = oBar + nBar * 8;  // TMEM base, abort flag, first / last unclean tile
   static constexpr int kBytes = oMisc + 16;
   // the base is rounded up to the 1 KB swizzle atom; never below 120 KB, so that one CTA (and its
@@ -110,13 +110,13 @@ constexpr int kChunks = BH / 32;
 struct Row {
   float c[kChunks][32];
 };
-CP_DEV float row_max(const Row& v) {
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+CP_DEV float chunk_max(const float (&a)[32]) {
+  float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int k = 0; k < 32; k += 4)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = fmax3(m[i], v.c[i >> 1][k + 2 * (i & 1)], v.c[i >> 1][k + 2 * (i & 1) + 1]);
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int i = 0; i < 2; ++i) m[i] = fmax3(m[i], a[k + 2 * i], a[k + 2 * i + 1]);
+  return fmaxf(m[0], m[1]);
 }
 CP_DEV float row_abs_max(const Row& v) {
   float m[4] = {0.f, 0.f, 0.f, 0.f};
@@ -192,47 +192,49 @@ CP_DEV CapCoefficients cap_coefficients(float cap_in, float scale_log2) {
   }
   return r;
 }
-// P of a row whose scores all lie within kCapNear, packed as bf16 pairs over its S columns in TMEM; the
-// row's sum.
-CP_DEV float cap_near_row(Row& v, uint32_t tS, const CapCoefficients& w, float ref) {
-  const uint64_t neg = f2(-ref, -ref);
-  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      const uint64_t s = f2(v.c[i][k], v.c[i][k + 1]), u = fmul2(s, s);
-      float x, y;
-      f2u(ffma2(s, ffma2(ffma2(ffma2(w.c[3], u, w.c[2]), u, w.c[1]), u, w.c[0]), neg), x, y);
-      x = ex2(x);
-      y = ex2(y);
-      acc[(k >> 1) & 3] = fadd2(acc[(k >> 1) & 3], f2(x, y));
-      pk[k >> 1] = pack_bf16(x, y);
-    }
-    tmem_st16(tS + 16 * i, pk);
-  }
-  float lo, hi;
-  f2u(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), lo, hi);
-  return lo + hi;
-}
-
 // P = 2^(x - ref) of 32 columns, packed as bf16 pairs over the row's own S columns in TMEM (the A
 // operand of the PV MMA; bf16 is the tensor core's operand type), the sum kept in fp32.
-CP_DEV void exp_chunk(float (&a)[32], uint64_t sc2, uint64_t n2, uint64_t& sum2, uint32_t taddr) {
+// exponent(s): x - ref of a pair of columns, whose scores are s, in order.
+template <typename Exponent>
+CP_DEV float exp_columns(const float (&a)[32], uint32_t taddr, Exponent exponent) {
   uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
   uint32_t pk[16];
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
     float x, y;
-    f2u(ffma2(f2(a[k], a[k + 1]), sc2, n2), x, y);
+    f2u(exponent(f2(a[k], a[k + 1])), x, y);
     x = ex2(x);
     y = ex2(y);
     acc[(k >> 1) & 3] = fadd2(acc[(k >> 1) & 3], f2(x, y));
     pk[k >> 1] = pack_bf16(x, y);
   }
-  sum2 = fadd2(sum2, fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])));
   tmem_st16(taddr, pk);
+  float lo, hi;
+  f2u(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), lo, hi);
+  return lo + hi;
+}
+
+// A distance bias that is linear over a chunk (every key at or before the query) goes into the
+// exponent's FMA, and the reference takes the bound max(s) + bias at the chunk's last key, at most 31
+// slopes above its largest score: with slopes (log2 units) up to kMaxFold / 31 no P that matters is
+// lost, since fp32 and bf16 hold 2^-126.  Steeper slopes are added to the scores first.
+constexpr float kMaxFold = 40.f;
+
+// 8 TMEM columns of this lane's row to registers (complete on return), and back.
+CP_DEV void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+CP_DEV void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // COLS columns of an O row *= alpha in TMEM (nothing to do when no lane of the warp needs it).
@@ -240,13 +242,12 @@ template <int COLS>
 CP_DEV void rescale_o(uint32_t tO, float alpha) {
   if (!__any_sync(0xffffffffu, alpha != 1.f)) return;
 #pragma unroll
-  for (int c = 0; c < COLS / 32; ++c) {
-    float o[32];
-    tmem_ld32(tO + c * 32, o);
-    tmem_wait_ld(o);
+  for (int c = 0; c < COLS; c += 8) {  // few at a time: the row's scores are live in registers
+    float o[8];
+    tmem_ld8(tO + c, o);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) o[k] *= alpha;
-    tmem_st32(tO + c * 32, o);
+    for (int k = 0; k < 8; ++k) o[k] *= alpha;
+    tmem_st8(tO + c, o);
   }
   tmem_wait_st();
 }
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Sm::bS + i), 1);
-      mbar_init(bar(Sm::bP + i), 8);
+      mbar_init(bar(Sm::bP + 2 * i), 8);
+      mbar_init(bar(Sm::bP + 2 * i + 1), 8);
       mbar_init(bar(Sm::bO + i), 1);
       mbar_init(bar(Sm::bFix + i), 2);
     }
@@ -504,13 +506,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tmem + (uint32_t)(tile * BN), desc_advance(dq, off), desc_advance(dk, off), id_qk, kk > 0);
           }
         };
-        auto issue_pv = [&](int tile, int slot, bool acc) {
+        // O += P V of the tile: chunk c of both halves as soon as its P is there (each half's P lies over
+        // the front of its own scores)
+        auto pv_of = [&](int tile, int t, int slot) -> bool {
           const uint64_t dv = desc_advance(dv0, (uint32_t)(slot * Sm::kKV));
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)  // each half's P lies over the front of its own scores
-            mma_ts(tmem + 256u + (uint32_t)(tile * D),
-                   tmem + (uint32_t)(tile * BN + kk * 8 + (kk >= BH / 16 ? BH / 2 : 0)),
-                   desc_advance(dv, kk * 16u * 128u), id_pv, acc || kk > 0);
+          for (int c = 0; c < kChunks; ++c) {
+            if (!mbar_wait(bar(Sm::bP + 2 * tile + c), (uint32_t)t & 1u, abort_flag, kBudget)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int half = i >> 1, kk = 2 * c + (i & 1);  // 16-key step of the half
+              mma_ts(tmem + 256u + (uint32_t)(tile * D), tmem + (uint32_t)(tile * BN + half * BH + kk * 8),
+                     desc_advance(dv, (uint32_t)(half * (BH / 16) + kk) * 16u * 128u), id_pv, t > 0 || c > 0 || i > 0);
+            }
+          }
+          mma_commit(bar(Sm::bO + tile));
+          return true;
         };
         bool ok = mbar_wait(bar(Sm::bQ), 0u, abort_flag, kBudget) &&
                   mbar_wait(bar(Sm::bFull), 0u, abort_flag, kBudget);
@@ -528,11 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(bar(Sm::bFix + (t & 1)), (uint32_t)(t >> 1) & 1u, abort_flag, kBudget) &&
                mbar_wait(bar(Sm::bFull + sv), (uint32_t)(iv / kSlots) & 1u, abort_flag, kBudget);
           if (!ok) break;
-          ok = mbar_wait(bar(Sm::bP + 0), (uint32_t)t & 1u, abort_flag, kBudget);
+          ok = pv_of(0, t, sv);
           if (!ok) break;
-          tc_fence_after();
-          issue_pv(0, sv, t > 0);
-          mma_commit(bar(Sm::bO + 0));
           const bool more = t + 1 < ntiles;
           if (more) {
             ok = mbar_wait(bar(Sm::bFull + sk), (uint32_t)(ik / kSlots) & 1u, abort_flag, kBudget);
@@ -541,11 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_qk(0, sk);
             mma_commit(bar(Sm::bS + 0));
           }
-          ok = mbar_wait(bar(Sm::bP + 1), (uint32_t)t & 1u, abort_flag, kBudget);
+          ok = pv_of(1, t, sv);
           if (!ok) break;
-          tc_fence_after();
-          issue_pv(1, sv, t > 0);
-          mma_commit(bar(Sm::bO + 1));
           mma_commit(bar(Sm::bEmpty + sv));
           if (more) {
             issue_qk(1, sk);
@@ -599,11 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float slope = biased ? __ldg(p.slopes + head) * kLog2e : 0.f;
     // scores come out of cap and bias in log2 units; untouched ones are scaled within the exponent
     const float sc = CAP || cap || biased ? 1.f : p.scale_log2;
-    const uint64_t sc2 = f2(sc, sc);
     float m = -INFINITY, l = 0.f;
     CapCoefficients coef;
     if constexpr (CAP) coef = cap_coefficients(p.cap_in, p.scale_log2);
     bool ok = true;
+    // chunk i of this warp's P is in TMEM: its PV may start
+    auto stored = [&](int i) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Sm::bP + 2 * tile + i));
+    };
     for (int t = 0; t < ntiles; ++t) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
       // a warp that gives up raises the abort flag; its partner gives up at its own wait, or where the
@@ -634,85 +646,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         near = t > 0 && whole_tile && __all_sync(0xffffffffu, y <= kCapNear);
       }
       if (CAP && near) {
-        l += cap_near_row(v, tS, coef, m);
-        tmem_wait_st();
-      } else {
-        if (CAP || cap) cap_scores(v, p.cap_in, cap_log2, CAP ? y : row_abs_max(v) * p.cap_in);
-        if (!CAP && biased) {
-          const float s0 = cap ? 1.f : p.scale_log2;
-          const int far = k0 + BH - 1 - (C + row);  // > 0: keys behind the query in this tile
-          if (__any_sync(0xffffffffu, far > 0 && hi > C + row + 1 && k0 < hi)) {
-            const float d0 = (float)(k0 - (C + row));
+        const uint64_t n2 = f2(-m, -m);
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                v.c[i][k] = fmaf(-slope, fabsf(d0 + (float)(32 * i + k)), v.c[i][k] * s0);
-          } else {  // every visible key is at or before the query: the bias is linear in the column
-            const uint64_t s02 = f2(s0, s0), step = f2(2.f * slope, 2.f * slope);
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-              const float b0 = slope * (float)(k0 + 32 * i - (C + row));
-              uint64_t bias = f2(b0, b0 + slope);
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                f2u(ffma2(f2(v.c[i][k], v.c[i][k + 1]), s02, bias), v.c[i][k], v.c[i][k + 1]);
-                bias = fadd2(bias, step);
-              }
-            }
-          }
+        for (int i = 0; i < kChunks; ++i) {
+          l += exp_columns(v.c[i], tS + 16 * i, [&](uint64_t s) {
+            const uint64_t u = fmul2(s, s);
+            return ffma2(s, ffma2(ffma2(ffma2(coef.c[3], u, coef.c[2]), u, coef.c[1]), u, coef.c[0]), n2);
+          });
+          stored(i);
         }
-        if (!whole_tile) {
+        continue;
+      }
+      if (CAP || cap) cap_scores(v, p.cap_in, cap_log2, CAP ? y : row_abs_max(v) * p.cap_in);
+      const float s0 = cap ? 1.f : p.scale_log2;
+      const int behind = k0 - (C + row);  // this thread's first key, counted from the query
+      bool fold = false;                  // the bias goes into the exponent
+      if (!CAP && biased) {
+        if (__any_sync(0xffffffffu, behind + BH - 1 > 0 && hi > C + row + 1 && k0 < hi)) {  // keys past the query
 #pragma unroll
           for (int i = 0; i < kChunks; ++i)
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              v.c[i][k] = 32 * i + k >= c0 && 32 * i + k < c1 ? v.c[i][k] : -INFINITY;
-        }
-        float alpha = 1.f;
-        if constexpr (CAP) {
-          if (t == 0) {  // the reference of both halves, for good
-            const float mt = row_max(v);
-            *s_mine = mt;
-            if (pair_any(pair, false)) {  // the partner gave up
-              ok = false;
-              break;
-            }
-            m = fmaxf(fmaxf(mt, *s_other), p.cap_ref);
-          }
+              v.c[i][k] = fmaf(-slope, fabsf((float)behind + (float)(32 * i + k)), v.c[i][k] * s0);
+        } else if (slope >= 0.f && 31.f * slope <= kMaxFold) {
+          fold = true;
         } else {
+          const uint64_t s02 = f2(s0, s0), step = f2(2.f * slope, 2.f * slope);
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const float b0 = slope * (float)(behind + 32 * i);
+            uint64_t bias = f2(b0, b0 + slope);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              f2u(ffma2(f2(v.c[i][k], v.c[i][k + 1]), s02, bias), v.c[i][k], v.c[i][k + 1]);
+              bias = fadd2(bias, step);
+            }
+          }
+        }
+      }
+      if (!whole_tile) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v.c[i][k] = 32 * i + k >= c0 && 32 * i + k < c1 ? v.c[i][k] : -INFINITY;
+      }
+      if (!CAP || t == 0) {  // the row's largest score here, or what bounds it
+        float mt = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const float x = chunk_max(v.c[i]);
+          mt = fmaxf(mt, !CAP && fold ? fmaf(x, s0, slope * (float)(behind + 32 * i + 31)) : x * sc);
+        }
+        if constexpr (CAP) {  // the reference of both halves, for good
+          *s_mine = mt;
+          if (pair_any(pair, false)) {  // the partner gave up
+            ok = false;
+            break;
+          }
+          m = fmaxf(fmaxf(mt, *s_other), p.cap_ref);
+        } else if (pair_any(pair, mt > m + kMaxGrowth)) {
           // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8:
           // the halves ask each other at one barrier, and exchange their maxima only then.
-          float mt = row_max(v) * sc;
-          if (pair_any(pair, mt > m + kMaxGrowth)) {
-            if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
-              ok = false;
-              break;
-            }
-            *s_mine = mt;
-            pair_sync(pair);
-            mt = fmaxf(mt, *s_other);
-            if (mt > m + kMaxGrowth) {
-              alpha = ex2(m - mt);
-              m = mt;
-            }
-            pair_sync(pair);  // both have read before either writes again
+          if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
+            ok = false;
+            break;
           }
+          *s_mine = mt;
+          pair_sync(pair);
+          mt = fmaxf(mt, *s_other);
+          float alpha = 1.f;
+          if (mt > m + kMaxGrowth) {
+            alpha = ex2(m - mt);
+            m = mt;
+          }
+          pair_sync(pair);  // both have read before either writes again
+          l *= alpha;
+          if (t > 0) rescale_o<D / 2>(tO, alpha);
         }
-        const float neg = m == -INFINITY ? 0.f : -m;
-        const uint64_t n2 = f2(neg, neg);
-        uint64_t sum2 = f2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) exp_chunk(v.c[i], sc2, n2, sum2, tS + 16 * i);
-        tmem_wait_st();
-        float s_lo, s_hi;
-        f2u(sum2, s_lo, s_hi);
-        l = l * alpha + (s_lo + s_hi);
-        if (!CAP && t > 0) rescale_o<D / 2>(tO, alpha);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Sm::bP + tile));
+      const float neg = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        if (!CAP && fold) {
+          const uint64_t s02 = f2(s0, s0), step = f2(2.f * slope, 2.f * slope);
+          const float b0 = fmaf(slope, (float)(behind + 32 * i), neg);
+          uint64_t bias = f2(b0, b0 + slope);
+          l += exp_columns(v.c[i], tS + 16 * i, [&](uint64_t s) {
+            const uint64_t x = ffma2(s, s02, bias);
+            bias = fadd2(bias, step);
+            return x;
+          });
+        } else {
+          const uint64_t sc2 = f2(sc, sc), n2 = f2(neg, neg);
+          l += exp_columns(v.c[i], tS + 16 * i, [&](uint64_t s) { return ffma2(s, sc2, n2); });
+        }
+        stored(i);
+      }
     }
     if (ok)
       ok = __all_sync(0xffffffffu,
