@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = h0 / p.G;
 
   if (warp < 4) {
+    regs_dec<64>();  // 128 x 64 + 512 x 104 = the 640 x 96 registers of the launch: the rows' scores without spills
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer
       if (lane == 0) {
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax, two warpgroups per tile
+    regs_inc<104>();
     const int sw = warp - 4, tile = sw >> 3, half = (sw >> 2) & 1, q4 = warp & 3;
     const int pair = 1 + tile * 4 + q4;  // named barrier of the warps with the same rows
     const int row = q_lo + (TT ? tile * BM : 0) + q4 * 32 + lane;  // within the sequence
