@@ -115,13 +115,27 @@ struct WriteParams {
 constexpr int kWriteTokens = 2;  // most tokens a warp owns
 
 // Rotation.  The angle pos * inv_freq of a far position needs more bits than fp32 has, so it is
-// kept in turns: inv_freq / 2 pi as a 64-bit fraction of a turn (one fp64 multiply per frequency),
-// times the integer position modulo 2^64, which drops whole turns exactly.  The top 32 bits are
-// the angle in [-1/2, 1/2) turns, off by 2^-26 turns at most after the conversion to fp32.
-CP_DEV unsigned long long turns_of(double inv_freq) {
-  double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  return __double2ull_rz(t * 18446744073709551616.0);
+// kept in turns: inv_freq / 2 pi as a 64-bit fraction of a turn, times the integer position modulo
+// 2^64, which drops whole turns exactly.  The top 32 bits are the angle in [-1/2, 1/2) turns, off by
+// 2^-26 turns at most after the conversion to fp32.
+//
+// The fraction by integers, from inv_freq = mant 2^(e - 1075): mant times 2^66 / 2 pi (its first 64
+// bits), shifted.  The handful of fp64 operations that it takes otherwise, on a chip with two fp64 lanes
+// per SM and clock, cost more than the 64-bit products here (2 x 32768 tokens, 16/2 heads: 124 against
+// 120 us).
+CP_DEV unsigned long long turns_of(long long inv_freq) {
+  const int e = (int)(inv_freq >> 52) & 0x7ff;
+  const unsigned long long frac = (unsigned long long)inv_freq & 0xfffffffffffffull;
+  const unsigned long long mant = e == 0 ? frac : frac | (1ull << 52);
+  constexpr unsigned long long kPerTurn = 0xa2f9836e4e441529ull;  // floor(2^66 / 2 pi)
+  const unsigned long long lo = mant * kPerTurn, hi = __umul64hi(mant, kPerTurn);
+  const int right = 1077 - max(e, 1);  // turns 2^64 = mant kPerTurn 2^-right
+  unsigned long long t;
+  if (right >= 128) t = 0ull;
+  else if (right >= 64) t = hi >> (right - 64);
+  else if (right > 0) t = (lo >> right) | (hi << (64 - right));
+  else t = right > -64 ? lo << -right : 0ull;
+  return inv_freq < 0 ? 0ull - t : t;
 }
 
 // The pieces (of 8 dims) a head's thread j handles, and whether they are rotated.  Half style: a
@@ -144,8 +158,33 @@ CP_DEV Pieces pieces_of(int j, int rot, int half) {
   return s;
 }
 
+// Scales below this go the long way: their reciprocal or remainders may leave fp32's normal range.
+constexpr float kQ4Tiny = 9.860761315262648e-32f;  // 2^-103
+
+// min / max that keep a NaN
+CP_DEV float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+CP_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The integer nearest to t / d (ties to even), for 0 <= t / d well below 2^22 and inv = 1 / d to a few
+// ulps, without a division: round the product, and see by the remainder (exact: one fma, and a difference
+// of multiples of t's last place) whether the neighbour is nearer.
+CP_DEV float nearest_quotient(float t, float d, float half, float inv) {
+  constexpr float kRound = 12582912.f;  // 1.5 2^23: what is added to it is rounded to an integer
+  const float z = fmaf(t, inv, kRound), n = z - kRound, r = fmaf(-n, d, t), a = fabsf(r);
+  const bool off = a > half || (a == half && (__float_as_uint(z) & 1u) != 0u);
+  return off ? n + copysignf(1.f, r) : n;
+}
+
 // Codes of one head's row by the D / 16 neighbouring threads that hold it (pieces c0, c1 each):
-// per group of 64 dims the minimum rounded to bf16, the range above it / 15 rounded to bf16, and
+// per group of 64 dims the minimum rounded to bf16, the range above it / 15 rounded to bf16 (at least 0), and
 // code = nearest integer to (x - minimum) / scale, ties to even, within 0..15.  A group with an
 // infinity or a NaN (or a range beyond bf16) is stored as NaN.
 template <int D>
@@ -153,27 +192,25 @@ CP_DEV void quantise(const float (&a)[8], const float (&b)[8], const Pieces& s, 
                      int j, bool live) {
   constexpr int GR = D / kQ4Group, LPH = D / 16;
   float mna = a[0], mxa = a[0], mnb = b[0], mxb = b[0];
-  bool bad_a = false, bad_b = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    mna = fminf(mna, a[e]), mxa = fmaxf(mxa, a[e]), bad_a |= !isfinite(a[e]);
-    mnb = fminf(mnb, b[e]), mxb = fmaxf(mxb, b[e]), bad_b |= !isfinite(b[e]);
+  for (int e = 1; e < 8; ++e) {
+    mna = min_nan(mna, a[e]), mxa = max_nan(mxa, a[e]);
+    mnb = min_nan(mnb, b[e]), mxb = max_nan(mxb, b[e]);
   }
-  if (bad_a) mxa = INFINITY;  // an infinite range marks the group
-  if (bad_b) mxb = INFINITY;
   float sc[GR], mn[GR];
 #pragma unroll
   for (int g = 0; g < GR; ++g) {
     const bool ia = GR == 1 || (s.c0 >> 3) == g, ib = GR == 1 || (s.c1 >> 3) == g;
-    float lo = fminf(ia ? mna : INFINITY, ib ? mnb : INFINITY);
-    float hi = fmaxf(ia ? mxa : -INFINITY, ib ? mxb : -INFINITY);
+    float lo = min_nan(ia ? mna : INFINITY, ib ? mnb : INFINITY);
+    float hi = max_nan(ia ? mxa : -INFINITY, ib ? mxb : -INFINITY);
 #pragma unroll
     for (int o = 1; o < LPH; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     mn[g] = __bfloat162float(__float2bfloat16_rn(lo));
-    sc[g] = __bfloat162float(__float2bfloat16_rn((hi - mn[g]) / 15.f));
+    // (never below 0: the minimum's rounding may pass the greatest value of a nearly constant group)
+    sc[g] = __bfloat162float(__float2bfloat16_rn(max_nan((hi - mn[g]) / 15.f, 0.f)));
     if (!(isfinite(mn[g]) && isfinite(sc[g]))) {
       mn[g] = NAN;
       sc[g] = 0.f;
@@ -184,11 +221,16 @@ CP_DEV void quantise(const float (&a)[8], const float (&b)[8], const Pieces& s, 
     const int g = GR == 1 ? 0 : c >> 3;
     const float m = g == 0 ? mn[0] : mn[GR - 1], d = g == 0 ? sc[0] : sc[GR - 1];
     uint32_t w = 0;
+    if (d >= kQ4Tiny) {
+      const float inv = 1.f / d, half = 0.5f * d;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // (IEEE division: the code is the same wherever the same row is quantised)
-      const float n = d > 0.f ? fminf(fmaxf(rintf((x[e] - m) / d), 0.f), 15.f) : 0.f;
-      w |= (uint32_t)n << (4 * e);
+      for (int e = 0; e < 8; ++e) {
+        const float n = fminf(fmaxf(nearest_quotient(x[e] - m, d, half, inv), 0.f), 15.f);
+        w |= (__float_as_uint(n + 8388608.f) & 15u) << (4 * e);  // 2^23 + n: n in the low bits
+      }
+    } else if (d > 0.f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w |= (uint32_t)fminf(fmaxf(rintf((x[e] - m) / d), 0.f), 15.f) << (4 * e);
     }
     reinterpret_cast<uint32_t*>(rec + row * (D / 2))[q4_word<D>(c)] = w;
   };
@@ -292,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_write_kernel(const WritePara
 
   unsigned long long f[D / 64];  // frequencies lane, lane + 32 in turns per position
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) f[i] = lane + 32 * i < h ? turns_of(__ldg(p.inv_freq + lane + 32 * i)) : 0ull;
+  for (int i = 0; i < D / 64; ++i) f[i] = lane + 32 * i < h ? turns_of(__ldg(reinterpret_cast<const long long*>(p.inv_freq) + lane + 32 * i)) : 0ull;
   Slot mine;
   long long my_pos = -1;
   const bool in = locate(p.at, row0, min(row0 + lane, row0 + nt - 1), my_pos, mine);

@@ -397,10 +397,10 @@ cp_status cp_decode_attention_noalloc(const cp_decode_args* args, void* out, flo
  *                     8 consecutive dims, lowest nibble first, from dim 8 w (d = 64) or
  *                     64 (w mod 2) + 8 (w div 2) (d = 128: the two groups' words alternate);
  *   bytes [8 d, 9 d)  per token and group of 64 dims (token-major) the bf16 pair scale, minimum.
- * A code n stands for minimum + scale * n, scale >= 0.  Written as: minimum = the group's least value rounded
- * to bf16, scale = (greatest value - minimum) / 15 rounded to bf16, n = the nearest integer to
- * (value - minimum) / scale (ties to even) within 0 .. 15, 0 where the scale is 0.  A group that
- * holds an infinity or a NaN stands for NaN throughout.
+ * A code n stands for minimum + scale * n, scale >= 0.  Written as: minimum = the group's least
+ * value rounded to bf16, scale = (greatest value - minimum) / 15 rounded to bf16, at least 0,
+ * n = the nearest integer to (value - minimum) / scale (ties to even) within 0 .. 15, 0 where the
+ * scale is 0.  A group that holds an infinity or a NaN stands for NaN throughout.
  * ---------------------------------------------------------------------------- */
 /* Bytes of one record (9 * head_dim). */
 int64_t cp_q4_record_bytes(int32_t head_dim);
@@ -525,7 +525,8 @@ typedef struct cp_score_mod {
  * tiles some row of a query tile sees are loaded, so a window or short documents cost their own
  * keys.  args->out / args->lse are not used; args->err takes device-side errors.
  *   out      device bf16 [Nq][Hq][d];  out_lse  device f32 [Nq][Hq] (natural log).
- * Rows from cu_seqlens_q[B] on are left as they are.
+ * Rows from cu_seqlens_q[B] on are left as they are.  With a softcap up to 55 weights are kept
+ * relative to the first key tile's largest score: finite components of v are below 2^40 then.
  * ---------------------------------------------------------------------------- */
 cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* mod, void* out,
                               float* out_lse, void* stream);
@@ -533,8 +534,9 @@ cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* m
 /* ------------------------------------------------------------------------------
  * Decode with modified scores (cp_partial_attn_decode_mod, cp_decode_attention_mod) and over the
  * 4-bit cache (cp_partial_attn_decode_q4, cp_decode_attention_q4; their args->dtype, the type of q
- * and out, is CP_BF16, and components of q are below 2^100).  Arguments as in cp_partial_attn_decode / cp_decode_attention plus `mod`
- * (NULL: none; prefix_lens must be NULL: a prefix is behind the query here).
+ * and out, is CP_BF16, and components of q are below 2^100).  Arguments as in
+ * cp_partial_attn_decode / cp_decode_attention plus `mod` (NULL: none; prefix_lens must be NULL: a
+ * prefix is behind the query here).
  *
  * Splits are counted within the visible tokens: split s of a rank covers split_tokens local tokens
  * from s * split_tokens past the page of the first visible one, so a window needs splits for its

@@ -42,7 +42,7 @@ def q4_codes(row):
             sc[g], mn[g] = 0.0, np.nan
             continue
         mn[g] = to_bf16(x.min())
-        sc[g] = to_bf16((x.max() - mn[g]) / 15)
+        sc[g] = max(0.0, to_bf16((x.max() - mn[g]) / 15))   # the minimum's rounding may pass the maximum
         if sc[g] > 0:
             n[g * GROUP:(g + 1) * GROUP] = np.clip(np.rint((x - mn[g]) / sc[g]), 0, 15)
     return n, sc, mn

@@ -292,3 +292,30 @@ def test_a_decode_step_in_a_cuda_graph(lib):
             want = step(k2, v2, torch.zeros_like(ws))
             torch.cuda.synchronize()
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 128), ("bf16", 64), ("f32", 64)])
+def test_nearly_constant_rows_in_four_bits(lib, dt, d):
+    """A group whose minimum rounds above its greatest value is stored as that minimum with scale 0, and
+    decodes as such (a negative scale would make infinite weights of zero codes)."""
+    cp, I, lens = 2, 8, [50, 33]
+    k, v, t = _pool(lens, 2, d, cp, I, torch.uint8, True, 6)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    level = torch.tensor([257.3, -0.70123, 1000.9, 3e-5], device=DEV)
+    kn, vn = (level[torch.randint(0, 4, (sum(lens), 2, 1), generator=g, device=DEV)].expand(-1, -1, d) *
+              (1 + 1e-5 * torch.rand(sum(lens), 2, d, generator=g, device=DEV)) for _ in range(2))
+    kn, vn = kn.to(DT[dt]).contiguous(), vn.to(DT[dt]).contiguous()
+    zero = torch.zeros(2, **I32)
+    lib.cp_rope_kv_cache_write(kn, vn, _cu(lens), zero, k, v, t, cp, I)
+    scales = [x[..., 8 * d:].contiguous().view(torch.bfloat16)[..., ::2] for x in (k, v)]
+    assert all(bool((s.float()[torch.isfinite(s.float())] >= 0).all()) for s in scales)
+    K, V = lib.cp_kv_cache_read(k, v, _cu(lens), zero, t, cp, I, out_dtype=torch.float32)
+    assert bool(((V - vn.float()).abs() <= 2.0 ** -8 * vn.float().abs()).all())
+    q = torch.randn(2, 8, d, device=DEV, generator=g).to(torch.bfloat16) * 0.02
+    out, lse = lib.cp_decode_attention_q4(q, k, v, t, torch.tensor(lens, **I32), cp, I)
+    at = 0
+    for b, n in enumerate(lens):
+        one = torch.tensor([n - 1], device=DEV)
+        o, l, a, big = _attend(q[b:b + 1].double(), K[at:at + n].double(), V[at:at + n].double(), 0 * one, one + 1, one, 0.0, None)
+        _check(out[b:b + 1], lse[b:b + 1], o, l, a, big, 0.0, None, n, extra=float(V.abs().max()), what=f"sequence {b}")
+        at += n
