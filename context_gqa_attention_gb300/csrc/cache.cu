@@ -469,24 +469,44 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadParams p)
       [&](bool is_v, long long at, const uint4& x) { static_cast<uint4*>(is_v ? p.v_out : p.k_out)[at] = x; });
 }
 
-// 4-bit rows to the values they stand for: a lane turns one word (8 codes) into 8 values.
+// The 8 values of a word of codes.  A code in place (n 16^e, e its nibble within a half word) below 2^23
+// in the mantissa of 2^23 is a float without a conversion (a quarter of the rate of an addition);
+// scale / 16^e is exact, so each value is rounded once (the product is exact).
+// (10112 tokens of 8 heads, d = 128: 19.6 -> 17.5 us with two words a lane.)
+CP_DEV void q4_values(uint32_t w, uint32_t sm, float (&x)[8]) {
+  const float sc = bf16_lo(sm), mn = bf16_hi(sm);
+  float s = sc;
+#pragma unroll
+  for (int e = 0; e < 4; ++e, s *= 0.0625f) {
+    const uint32_t mask = 15u << (4 * e);
+    x[e] = fmaf(s, __uint_as_float((w & mask) | 0x4b000000u) - 8388608.f, mn);
+    x[e + 4] = fmaf(s, __uint_as_float((w >> 16 & mask) | 0x4b000000u) - 8388608.f, mn);
+  }
+}
+
+// 4-bit rows to the values they stand for: a lane turns two words (16 codes; of both groups, d = 128) into
+// 16 values.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadParams p) {
-  constexpr int GR = D / kQ4Group;
+  constexpr int GR = D / kQ4Group, V = D / 16;
   __shared__ Slot slots[kWarps][32];
-  stream_rows<D / 8, 4>(
+  stream_rows<V, 4>(
       p, slots[threadIdx.x >> 5],
       [&](bool is_v, long long head, int row, int c) {
         const uint8_t* rec = (is_v ? p.v_cache : p.k_cache) + head * q4_record_bytes(D);
-        return make_uint2(
-            __ldg(reinterpret_cast<const uint32_t*>(rec + row * (D / 2)) + q4_word<D>(c)),
-            __ldg(reinterpret_cast<const uint32_t*>(rec + 8 * D) + row * GR + (GR == 1 ? 0 : c >> 3)));
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(rec + row * (D / 2)) + c);
+        const uint32_t* sm = reinterpret_cast<const uint32_t*>(rec + 8 * D) + row * GR;
+        const uint32_t s0 = __ldg(sm);
+        return make_uint4(w.x, w.y, s0, GR == 2 ? __ldg(sm + GR - 1) : s0);
       },
-      [&](bool is_v, long long at, const uint2& w) {
+      [&](bool is_v, long long at, const uint4& w) {
         float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = q4_value(w.y, (w.x >> (4 * e)) & 15u);
-        store8(static_cast<T*>(is_v ? p.v_out : p.k_out) + 8 * at, x);
+        T* out = static_cast<T*>(is_v ? p.v_out : p.k_out) + at / V * D;
+        const int c = (int)(at % V);
+        q4_values(w.x, w.z, x);
+        store8(out + (GR == 2 ? 8 * c : 16 * c), x);
+        q4_values(w.y, w.w, x);
+        store8(out + (GR == 2 ? 64 + 8 * c : 16 * c + 8), x);
       });
 }
 

@@ -24,7 +24,4 @@ CP_DEV int q4_word(int c) {
 CP_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 CP_DEV float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// What code n of a (scale, minimum) word stands for, one rounding (the product is exact).
-CP_DEV float q4_value(uint32_t sm, uint32_t n) { return fmaf(bf16_lo(sm), (float)n, bf16_hi(sm)); }
-
 }  // namespace cpattn
