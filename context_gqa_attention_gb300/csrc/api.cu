@@ -863,19 +863,21 @@ cp_status cp_decode_mod_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t cp,
     const long long w = share_of(window) + page - 1;
     share = share < w ? share : w;
   }
-  // Tokens per CTA: about `most`, fewer where that would leave SMs without their three CTAs, and no
-  // fewer than a page for each of its four warps.  Short contexts of few sequences: no more than eight
-  // parts, which one cluster merges.
-  const long long most = q4 ? 4096 : 2048, least = 4 * page;
+  // Tokens per CTA: about `most`, fewer where that would leave SMs without CTAs, and no fewer than keep its
+  // four warps busy (`least`).  Short contexts: no more than eight parts, which one cluster merges (one
+  // sequence of 4242 tokens, 2 kv heads, 4 bits: 10.6 us with 8 parts, 13.4 with 67).
+  const long long most = q4 ? 4096 : 2048, least = (q4 ? 8 : 4) * page;
   long long S = (share + most - 1) / most;
-  // (three CTAs on each of 152 SMs, in whole clusters of eight parts: one wave, no CTA left over)
-  const long long slots = 3ll * 152 / ((long long)num_seqs * num_kv_heads);
-  const long long one_wave = (slots >= 8 ? slots / 8 * 8 : slots) / cp;
+  // (288 CTAs in clusters of eight run at once whichever kernel it is; whole clusters of 8, 4 or 2 parts:
+  // 8 sequences of 500..3911 tokens, 8 kv heads, 4 bits take 13.7 us in 256 CTAs and 23.0 in 512 places of
+  // which a quarter is empty)
+  const long long slots = 288 / ((long long)num_seqs * num_kv_heads);
+  const long long one_wave = (slots >= 8 ? slots / 8 * 8 : slots >= 4 ? 4 : slots) / cp;
   // or two waves without clusters, where that leaves each CTA enough to do
   const long long base = (long long)num_seqs * num_kv_heads * cp, two_waves = (8ll * 152 + base - 1) / base;
   const long long want = share / two_waves >= (q4 ? 2048 : 512) ? two_waves : one_wave;
   if (S < want) S = want;
-  if (share * cp <= 8 * 512 && S > 8 / cp) S = 8 / cp;
+  if (share * cp <= (q4 ? 6144 : 4096) && S > 8 / cp) S = 8 / cp;
   if (S > (share + least - 1) / least) S = (share + least - 1) / least;
   if (S > 256 / cp) S = 256 / cp;
   if (S < 1) S = 1;

@@ -392,10 +392,11 @@ __global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModPa
 
 template <int D>
 cudaError_t launch_d(const ModParams& p, int dtype, cudaStream_t s) {
-  if (dtype == CP_F32)
-    return launch_decode(p.G <= 2 ? decode_mod_f32_kernel<D, 2> : p.G <= 4 ? decode_mod_f32_kernel<D, 4>
-                                                                          : decode_mod_f32_kernel<D, 8>, p, 0, s);
-  return launch_decode(p.G <= 8 ? decode_mod_kernel<D, 1> : decode_mod_kernel<D, 2>, p, 0, s);
+  if (dtype != CP_F32)
+    return p.G <= 8 ? launch_decode(decode_mod_kernel<D, 1>, p, 0, 3, s) : launch_decode(decode_mod_kernel<D, 2>, p, 0, 2, s);
+  const int per_sm = D == 64 && p.G <= 4 ? 3 : 2;
+  return launch_decode(p.G <= 2 ? decode_mod_f32_kernel<D, 2> : p.G <= 4 ? decode_mod_f32_kernel<D, 4>
+                                                                        : decode_mod_f32_kernel<D, 8>, p, 0, per_sm, s);
 }
 
 }  // namespace

@@ -523,10 +523,11 @@ inline ModParams decode_mod_params(const cp_decode_args& a, const cp_score_mod& 
 // kv_start and window only move the ranges; the scores themselves change with the other two
 inline bool changes_scores(const cp_score_mod& mod) { return mod.softcap > 0.f || mod.alibi_slopes != nullptr; }
 
-// Launch of a decode kernel: fused calls whose CTAs all run at once (three per SM) in clusters
-// of up to eight of a (sequence, kv head)'s parts; larger ones without, since a cluster's CTAs start and
-// stay together and the empty splits of short sequences would hold their places.
-inline cudaError_t launch_decode(void (*kern)(const ModParams), ModParams p, size_t smem, cudaStream_t s) {
+// Launch of a decode kernel of which per_sm CTAs fit on an SM: fused calls whose CTAs all run at once in
+// clusters of up to eight of a (sequence, kv head)'s parts; larger ones without, since a cluster's CTAs
+// start and stay together and the empty splits of short sequences would hold their places.  (Clusters of
+// eight fill 8 of 9 places: 408 CTAs at three per SM, 288 at two.)
+inline cudaError_t launch_decode(void (*kern)(const ModParams), ModParams p, size_t smem, int per_sm, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.blockDim = dim3(kWarps * 32);
@@ -537,9 +538,9 @@ inline cudaError_t launch_decode(void (*kern)(const ModParams), ModParams p, siz
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  p.cluster = 1;
-  if (p.fused && parts > 1 && (long long)parts * p.Hkv * p.B <= 3ll * sms)
-    p.cluster = parts > 4 ? 8 : (parts > 2 ? 4 : 2);
+  p.cluster = parts > 4 ? 8 : (parts > 2 ? 4 : 2);
+  const long long ctas = (long long)(parts + p.cluster - 1) / p.cluster * p.cluster * p.Hkv * p.B;
+  if (!p.fused || parts == 1 || 9 * ctas > 8ll * per_sm * sms) p.cluster = 1;
   cudaLaunchAttribute at[1];
   if (p.cluster > 1) {
     cfg.gridDim = dim3((parts + p.cluster - 1) / p.cluster * p.cluster, p.Hkv, p.B);

@@ -87,7 +87,7 @@ CP_DEV int row_token(int r) { return (r >> 1) ^ ((r & 1) * 5); }
 // of 64: 263, 277 and 314 us; d = 64: 189, 193).  Two with a second tile of heads (147 against 163 us).
 template <int D, int NT>
 struct Q4Shape {
-    static constexpr int NP = NT == 1 ? 4 : 2;
+  static constexpr int NP = NT == 1 ? 4 : 2;
   static constexpr int kStages = NP == 4 ? 2 : 3;
   static constexpr int kCtas = NT == 1 ? 3 : 2;  // per SM
   static constexpr int kRec = 9 * D;
@@ -549,7 +549,7 @@ cudaError_t launch_nt(const ModParams& p, bool mod, cudaStream_t s) {
   auto kern = mod ? decode_q4_kernel<D, NT, true> : decode_q4_kernel<D, NT, false>;
   constexpr int bytes = Q4Shape<D, NT>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e == cudaSuccess ? launch_decode(kern, p, bytes, s) : e;
+  return e == cudaSuccess ? launch_decode(kern, p, bytes, Q4Shape<D, NT>::kCtas, s) : e;
 }
 
 }  // namespace
