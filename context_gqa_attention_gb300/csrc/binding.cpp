@@ -84,25 +84,29 @@ struct Args {
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     return (float)v;
   }
-  // the stream's handle, or None for the device's current stream
-  void* stream(const at::Device& device) {
-    PyObject* x = next();
-    if (x == Py_None) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
-    void* s = PyLong_AsVoidPtr(x);
-    if (s == nullptr && PyErr_Occurred()) throw python_error();
-    return s;
-  }
 };
 
-// A call's device and the checks of its tensors.
+// A call's device and stream, and the checks of its tensors.
 struct Call {
   at::Device device;
   c10::cuda::CUDAGuard guard;
+  mutable c10::cuda::OptionalCUDAStreamGuard on_stream;
   static const Tensor& on_gpu(const Tensor& first, const char* name) {
     if (!first.is_cuda()) refuse(std::string(name) + ": the first argument must be a CUDA tensor");
     return first;
   }
   Call(const Tensor& first, const char* name) : device(on_gpu(first, name).device()), guard(device) {}
+
+  // The handle of the stream argument, None for the device's current stream.  One that is given is current
+  // for the rest of the call: what is allocated and filled here belongs to it.
+  void* stream(Args& x) const {
+    PyObject* o = x.next();
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    void* s = PyLong_AsVoidPtr(o);
+    if (s == nullptr && PyErr_Occurred()) throw python_error();
+    on_stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), device.index()));
+    return s;
+  }
 
   void placed(const Tensor& t, const char* name) const {
     if (t.device() == device) return;
@@ -223,7 +227,7 @@ PyObject* rope_write(Args& x) {
   const Tensor* inv_freq = x.opt("inv_freq");
   a.rope_style = x.i32("rope_style");
   const Tensor *q = x.opt("q"), *q_out = x.opt("q_out"), *k_out = x.opt("k_out"), *err = x.opt("err");
-  void* stream = x.stream(c.device);
+  void* stream = c.stream(x);
 
   const at::ScalarType T = k.scalar_type();
   a.k_stride = c.token_rows(k, "k_new", T);
@@ -293,7 +297,7 @@ PyObject* kv_read(Args& x) {
   int64_t total = x.integer("total", -1, std::numeric_limits<int32_t>::max());
   const int32_t type = x.i32("out_dtype");
   const Tensor *k_out = x.opt("k_out"), *v_out = x.opt("v_out"), *err = x.opt("err");
-  void* stream = x.stream(c.device);
+  void* stream = c.stream(x);
 
   const bool q4 = kc.scalar_type() == at::kByte;
   const at::ScalarType T = type >= 0           ? (type == CP_BF16 ? at::kBFloat16 : at::kFloat)
@@ -371,7 +375,7 @@ PyObject* prefill(Args& x) {
   a.max_seqlen_q = x.i32("max_seqlen_q");
   a.softmax_scale = x.real();
   const Tensor *out = x.opt("out"), *out_lse = x.opt("out_lse"), *err = x.opt("err");
-  void* stream = x.stream(c.device);
+  void* stream = c.stream(x);
 
   dims(q, "q", 3, "[Nq, Hq, d]");
   c.dense(q, "q", at::kBFloat16);
@@ -428,7 +432,7 @@ struct Decode {
     a.split_tokens = x.i32("split_tokens");
     a.softmax_scale = x.real();
     err = x.opt("err");
-    stream = x.stream(c.device);
+    stream = c.stream(x);
 
     dims(q, "q", 3, "[B, Hq, d]");
     a.dtype = dtype_of(q);

@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_write_kernel(const WritePara
   constexpr int LPH = D / 16;    // lanes per head
   constexpr int HPW = 32 / LPH;  // heads the warp takes at a time
   __shared__ __align__(16) float cs_all[kWarps][2][D / 2];  // cosines, sines of a token's angles
+  chained_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long first = ((long long)blockIdx.x * kWarps + warp) * p.T;
   if (first >= p.N) return;
@@ -420,6 +421,7 @@ struct ReadParams {
 template <int V, int U, typename Load, typename Store>
 CP_DEV void stream_rows(const ReadParams& p, Slot* slots, Load load, Store store) {
   constexpr int RPW = 32 / V;  // rows the warp takes at a time
+  chained_start();
   const int lane = threadIdx.x & 31;
   const long long first = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.T;
   if (first >= p.N) return;
@@ -556,8 +558,7 @@ cudaError_t cp_launch_rope_write(const cp_rope_write_args& a, cudaStream_t s) {
   const long long per_cta = (long long)kWarps * p.T;
   const dim3 grid((unsigned)((p.N + per_cta - 1) / per_cta), (unsigned)((nh + each - 1) / each));
   auto go = [&](auto kern) -> cudaError_t {
-    kern<<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kern, dim3(grid), kThreads, 0, s, p);
   };
   const bool q4 = a.cache_q4 != 0, bf = a.dtype == CP_BF16;
   if (a.head_dim == 128) {
@@ -588,8 +589,7 @@ cudaError_t cp_launch_kv_read(const cp_kv_read_args& a, cudaStream_t s) {
   const long long per_cta = (long long)kWarps * p.T;
   const unsigned grid = (unsigned)((p.N + per_cta - 1) / per_cta);
   auto go = [&](auto kern) -> cudaError_t {
-    kern<<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kern, dim3(grid), kThreads, 0, s, p);
   };
   if (a.cache_q4) {
     if (d == 128) return a.out_dtype == CP_BF16 ? go(read_q4_kernel<__nv_bfloat16, 128>) : go(read_q4_kernel<float, 128>);

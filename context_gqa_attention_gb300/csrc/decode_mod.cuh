@@ -358,6 +358,7 @@ struct Unit {
 };
 template <typename T, int D, int HR>
 CP_DEV bool take_unit(const ModParams& p, WarpParts<D, HR>& parts, Unit& u) {
+  chained_start();
   u.g = blockIdx.y;
   if (p.cluster > 1) {  // a cluster's CTAs are neighbours in x: parts in order, a few past the last
     u.b = blockIdx.z;
@@ -541,15 +542,18 @@ inline cudaError_t launch_decode(void (*kern)(const ModParams), ModParams p, siz
   p.cluster = parts > 4 ? 8 : (parts > 2 ? 4 : 2);
   const long long ctas = (long long)(parts + p.cluster - 1) / p.cluster * p.cluster * p.Hkv * p.B;
   if (!p.fused || parts == 1 || 9 * ctas > 8ll * per_sm * sms) p.cluster = 1;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_chained
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   if (p.cluster > 1) {
     cfg.gridDim = dim3((parts + p.cluster - 1) / p.cluster * p.cluster, p.Hkv, p.B);
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = p.cluster;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = p.cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   } else {
     cfg.gridDim = dim3(p.S, p.Hkv, p.cp * p.B);
   }

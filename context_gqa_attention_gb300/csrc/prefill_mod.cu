@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_range[kThreads / 32][4];
   __shared__ float s_rows[2][2][BM];  // [tile][half][row]: what the halves of a row tell each other
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  chained_start();
 
   // ---- the item: heads fastest, then row tiles (the last, longest one first), then sequences
   const int h0 = blockIdx.x * (TT ? 1 : 2), b = blockIdx.z;
@@ -859,8 +860,7 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
                  : (fixed ? prefill_mod_kernel<D, false, true> : prefill_mod_kernel<D, false, false>);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, Smem<D>::kAlloc, s>>>(mq, mk, mv, p);
-  return cudaGetLastError();
+  return launch_chained(kern, grid, kThreads, Smem<D>::kAlloc, s, mq, mk, mv, p);
 }
 
 }  // namespace

@@ -190,6 +190,7 @@ def test_outputs_given_are_the_ones_returned(lib, t):
 
 def test_references_are_not_lost_or_kept(lib, t):
     """Returned outputs are owned by the caller alone; refused calls keep nothing."""
+    import gc
     import sys
     out = torch.empty_like(t["q"])
     before = [sys.getrefcount(x) for x in (*t.values(), out, None)][:-1]
@@ -200,6 +201,7 @@ def test_references_are_not_lost_or_kept(lib, t):
             decode(t, out=out, window=-1)
     assert [sys.getrefcount(x) for x in (*t.values(), out, None)][:-1] == before
     torch.cuda.synchronize()
+    gc.collect()                # (what earlier tests left to the collector is not this one's)
     used = torch.cuda.memory_allocated()
     for _ in range(10):
         decode(t)
@@ -230,6 +232,31 @@ def test_the_stream_given_is_the_one_used(lib, t):
         s.synchronize()
         torch.cuda.synchronize()
         assert float((out.float() - want.float()).abs().max()) <= 2.0 ** -7 * float(want.float().abs().max())
+
+
+def test_a_workspace_made_for_a_stream_is_filled_on_it(lib):
+    """Without a workspace the call zero-fills one on the stream it runs on, whatever the current one does."""
+    B, L, s = 64, 600, torch.cuda.Stream()
+    pages = -(-L // 32)
+    kc, vc = (_bf(cp, B * pages, 8, 16, d) for _ in range(2))
+    tables = torch.arange(B * pages, dtype=torch.int32, device=DEV).reshape(1, B, pages).repeat(cp, 1, 1)
+    q, sl = _bf(B, 32, d), torch.full((B,), L, dtype=torch.int32, device=DEV)
+    kw = dict(num_splits=5, split_tokens=64)        # more CTAs than run at once: merged through the counters
+    want = cpa.cp_decode_attention_mod(q, kc, vc, tables, sl, cp, I, **kw)[0].clone()
+    need = cpa.cp_decode_workspace_size(B, 32, 8, d, cp, 5)
+    big = torch.randn(4096, 4096, device=DEV)
+    out, lse = torch.empty_like(want), torch.empty(B, 32, device=DEV)
+    torch.cuda.synchronize()
+    for how in (None, s):
+        dirty = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        del dirty                                   # the next block of this size holds its bytes
+        for _ in range(20):
+            big @ big                               # the current stream is busy
+        cpa.cp_decode_attention_mod(q, kc, vc, tables, sl, cp, I, stream=how, out=out, out_lse=lse, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        out.zero_()
 
 
 def test_inference_mode_and_leaves_that_want_gradients(lib, t):

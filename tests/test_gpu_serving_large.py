@@ -319,3 +319,43 @@ def test_nearly_constant_rows_in_four_bits(lib, dt, d):
         o, l, a, big = _attend(q[b:b + 1].double(), K[at:at + n].double(), V[at:at + n].double(), 0 * one, one + 1, one, 0.0, None)
         _check(out[b:b + 1], lse[b:b + 1], o, l, a, big, 0.0, None, n, extra=float(V.abs().max()), what=f"sequence {b}")
         at += n
+
+
+def test_calls_that_feed_one_another(lib):
+    """Append, decode, read-back and prefill one after the other, each on what the one before it wrote,
+    with nothing between them, give what they give with a synchronization after each."""
+    B, Hq, Hkv, d, cp, I, L = 3, 8, 2, 128, 2, 8, 40
+    g = torch.Generator(device=DEV).manual_seed(8)
+    first = torch.randn(B, Hq + 2 * Hkv, d, generator=g, device=DEV).to(torch.bfloat16)
+    freq = torch.tensor(10000.0 ** (-np.arange(64) / 64), device=DEV)
+    cu1 = _cu([1] * B)
+    starts = [torch.full((B,), i, **I32) for i in range(L + 1)]
+    cus = [_cu([i] * B) for i in range(L + 1)]
+    for q4 in (False, True):
+        results = []
+        for wait in (True, False, False, False):
+            k, v, t = _pool([L] * B, Hkv, d, cp, I, torch.bfloat16, q4, 1)
+            k.zero_(), v.zero_()
+            call = lib.cp_decode_attention_q4 if q4 else lib.cp_decode_attention_mod
+            ws = torch.zeros(lib.cp_decode_workspace_size(B, Hq, Hkv, d, cp, 2), dtype=torch.uint8, device=DEV)
+            x, seen = first, []
+            for i in range(L):
+                q, kn, vn = x.split([Hq, Hkv, Hkv], 1)
+                q, _ = lib.cp_rope_kv_cache_write(kn, vn, cu1, starts[i], k, v, t, cp, I, inv_freq=freq, q=q)
+                if wait:
+                    torch.cuda.synchronize()
+                o, l = call(q, k, v, t, starts[i + 1], cp, I, num_splits=2, split_tokens=16, workspace=ws)
+                if wait:
+                    torch.cuda.synchronize()
+                rk, rv = lib.cp_kv_cache_read(k, v, cus[i + 1], starts[0], t, cp, I, total=B * (i + 1), out_dtype=torch.bfloat16)
+                if wait:
+                    torch.cuda.synchronize()
+                p, pl = lib.cp_attn_prefill_mod(o, cu1, rk, rv, cu_seqlens_kv=cus[i + 1], max_seqlen_q=1, softcap=9.0)
+                if wait:
+                    torch.cuda.synchronize()
+                x = torch.cat([p, rk.view(B, i + 1, Hkv, d)[:, i], o[:, :Hkv]], 1)
+                seen += [o, l, rk, rv, p, pl]
+            torch.cuda.synchronize()
+            results.append(seen)
+        for other in results[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(results[0], other))
