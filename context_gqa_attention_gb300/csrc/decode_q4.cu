@@ -20,8 +20,9 @@
 //    copy engine, an iteration or two ahead; loads into registers left the warps waiting for DRAM two
 //    thirds of the time (64 sequences of 1024..32768 tokens, 32/8 heads: 349 us), 16-byte cp.async
 //    stopped at 83% of the copy bandwidth and took a tenth of the instructions (277 us);
-//  * several independent pages per iteration keep a warp issuing (Q4Shape): 263 us, 74% of the copy
-//    bandwidth.  What is left is instructions: without its arithmetic the same kernel runs at 95%.
+//  * several independent pages per iteration keep a warp issuing (Q4Shape): 263 us, and 258 with the next
+//    call's CTAs placed early, 76% of the copy bandwidth.  What is left is instructions: without its
+//    arithmetic the same kernel runs at 95%.
 #include <cuda_fp16.h>
 
 #include "decode_mod.cuh"
@@ -237,9 +238,10 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
   const Mods<NT> mods(p, u, tid);
 
   // Per head of this thread's columns (2 tid, 2 tid + 1): reference m (log2; neg = -m, 0 before the
-  // first score; limit: the score past which it moves, in the scores' units) and the sum of this thread's tokens; per group the sum of P minimum (this thread's
-  // tokens) and the unit 1 / inv of the f16 factors P scale that o is in (a power of two; 2^126 before
-  // the first one, so that any factor worth keeping moves it).
+  // first score; limit: the score past which it moves, in the scores' units) and the sum of this
+  // thread's tokens; per group the sum of P minimum (this thread's tokens) and the unit 1 / inv of the
+  // f16 factors P scale that o is in (a power of two; 2^-126 before the first one, so that any factor
+  // worth keeping moves it).
   float m[NT][2], neg[NT][2], limit[NT][2], l[NT][2], pm[NT][GR][2], inv[NT][GR][2], o[NT][KS][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {

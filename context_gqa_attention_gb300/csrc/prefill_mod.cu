@@ -19,10 +19,12 @@
 // The keys a CTA walks are the union [key_lo, key_hi) of its rows' ranges, so windows and short
 // documents load their own keys only; tiles start at key_lo, not at a multiple of 128.
 //
-// Bound: the softmax warps' instruction issue (2 x 128 x 128 scores per key tile) against the
-// tensor pipe's 16.8 MFLOP per key tile.  The cap is therefore a polynomial on the packed fp32
-// pipe wherever a warp's scores allow it (tanh(y) / y in y^2, own least-maximum fits), and only
-// else 1 - 2 / (1 + e^2y), whose two special-function operations per score would bound the kernel.
+// Bound: the chain of a tile's softmax, PV and next QK (3.3k cycles a key tile, 3.7k with a cap, against
+// the tensor pipe's 2.05k), so everything on it is kept short: four softmax warpgroups rather than
+// two, PV started by halves of P, and the cap a polynomial on the packed fp32 pipe wherever a warp's
+// scores allow it (tanh(y) / y in y^2, own least-maximum fits), only else 1 - 2 / (1 + e^2y), two
+// special-function operations per score.  8192 tokens, 16/2 heads, d = 128: 234 us with cap 50 (61% of the
+// measured bf16 peak), 210 without, 261 with a distance bias; 16384 tokens in a window of 4096 with a cap 418.
 #include <cuda.h>
 
 #include "common.cuh"
