@@ -101,7 +101,13 @@ struct Q4Shape {
   static_assert(kQBytes <= kWarps * kStage, "the q operands take the last stage before the loop");
 };
 
-template <int D, int NT, bool MOD>
+// PK: pages that share a tile of scores.  With up to four heads a page's scores fill half of a tile's eight
+// columns, so the tile's other half takes another page's: Q's heads stand in both halves, of each page's
+// product a thread keeps the columns that are its page's, and everything between the products (scales,
+// exponentials, factors, transposes) is done once for two pages.  P V takes the halves in turn, the other
+// one zero; the halves keep sums of their own, joined at the end.  (The batch of 64, d = 128, 4 heads to a kv
+// head: 263 -> 247 us; with a cap and a bias 339 -> 292.)
+template <int D, int NT, int PK, bool MOD>
 __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q4_kernel(const ModParams p) {
   using T = __nv_bfloat16;
   using Sh = Q4Shape<D, NT>;
@@ -109,12 +115,15 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
   constexpr int HR = 8 * NT;
   constexpr int GR = D / kQ4Group;
   constexpr int KS = D / 16;  // MMAs of each product
+  constexpr int NS = NP / PK;  // score tiles per iteration
+  static_assert(PK == 1 || NT == 1, "only a group that fills half a tile shares it");
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(8) unsigned long long s_bar[kWarps][Sh::kStages];  // a stage's records have landed
   WarpParts<D, HR>& parts = *reinterpret_cast<WarpParts<D, HR>*>(smem);  // over the ring, at the end
   Unit u;
   if (!take_unit<T, D, HR>(p, parts, u)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const int mine = PK == 2 ? tid >> 1 : 0;  // which of a tile's pages this thread's columns belong to
   const uint32_t ring = sm100::smem_u32(smem) + (uint32_t)(warp * Sh::kStage);
   auto stage_at = [&](int st) -> uint32_t { return ring + (uint32_t)(st * (kWarps * Sh::kStage)); };
 
@@ -185,10 +194,11 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
 #pragma unroll
   for (int i0 = 0; i0 < HR * TPH; i0 += kWarps * 32) {
     const int i = i0 + (int)threadIdx.x, head = i / TPH, c = i % TPH;
+    const int from = PK == 2 ? head & 3 : head;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (head < p.G)
+    if (from < p.G)
       x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                               ((long long)u.b * p.Hq + (long long)u.g * p.G + head) * D) + c);
+                                               ((long long)u.b * p.Hq + (long long)u.g * p.G + from) * D) + c);
     const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
                         bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
     float mx = 0.f;
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
     }
   }
   __syncthreads();  // the ring's last stage is free
-  const Mods<NT> mods(p, u, tid);
+  const Mods<NT> mods(p, u, PK == 2 ? tid & 1 : tid);
 
   // Per head of this thread's columns (2 tid, 2 tid + 1): reference m (log2; neg = -m, 0 before the
   // first score; limit: the score past which it moves, in the scores' units) and the sum of this
@@ -294,56 +304,59 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
       break;
     }
     const uint32_t base = stage_at(st);
-    int t0[NP];         // first local token of each page
-    bool edge = false;  // some token of the pages is not visible
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      t0[i] = (pg0 + (k * kWarps + warp) * NP + i) * kPage;
-      edge |= !(there >> (st * NP + i) & 1u) || t0[i] < u.a || t0[i] + kPage > u.l1;
-    }
-    auto visible = [&](int i, int h) {
-      const int t = t0[i] + tok + 8 * h;
-      return (there >> (st * NP + i) & 1u) && t >= u.a && t < u.l1;
+    const int page0 = pg0 + (k * kWarps + warp) * NP;
+    // some token of the iteration's pages is not visible
+    const bool edge = (there >> (st * NP) & ((1u << NP) - 1u)) != (1u << NP) - 1u || page0 * kPage < u.a ||
+                      (page0 + NP) * kPage > u.l1;
+    auto token = [&](int j, int h) { return (page0 + PK * j + mine) * kPage + tok + 8 * h; };
+    auto visible = [&](int j, int h) {
+      const int t = token(j, h);
+      return (there >> (st * NP + PK * j + mine) & 1u) && t >= u.a && t < u.l1;
     };
 
-    // ---- S^T: rows = tokens row_token(gid), 8 on; columns = heads 2 tid, 2 tid + 1
-    float s[NP][NT][4];  // [token half * 2 + head], log2 units (MOD) or to be multiplied by qscale
+    // ---- S^T: rows = tokens row_token(gid), 8 on; columns = heads 2 tid, 2 tid + 1 (of page `mine`)
+    float s[NS][NT][4];  // [token half * 2 + head], log2 units (MOD) or to be multiplied by qscale
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const uint32_t rec = base + (uint32_t)(i * 2 * REC);
-      uint32_t w[2][2 * GR];  // [token half][word]: the groups' words in turn
+    for (int j = 0; j < NS; ++j) {
+      float c[PK][NT][GR][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (D == 128) {
-          const uint4 x = lds128(rec + k_at + (uint32_t)h * 8u * kRow);
-          w[h][0] = x.x, w[h][1] = x.y, w[h][2 * GR - 2] = x.z, w[h][2 * GR - 1] = x.w;
-        } else {
-          const uint2 x = lds64(rec + k_at + (uint32_t)h * 8u * kRow);
-          w[h][0] = x.x, w[h][1] = x.y;
-        }
-      }
-      uint32_t sm[2][GR];
-      load_scales(rec, 0, sm[0]);
-      load_scales(rec, 1, sm[1]);
-      float c[NT][GR][4];
+      for (int i = 0; i < PK; ++i) {
+        const uint32_t rec = base + (uint32_t)((PK * j + i) * 2 * REC);
+        uint32_t w[2][2 * GR];  // [token half][word]: the groups' words in turn
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) c[nt][gr][e] = 0.f;
-#pragma unroll
-      for (int wi = 0; wi < 2; ++wi)
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          const uint32_t w0 = w[0][wi * GR + gr], w1 = w[1][wi * GR + gr];
-          const int ks = gr * 4 + wi * 2;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816_f16(c[nt][gr], codes<0>(w0), codes<0>(w1), codes<1>(w0), codes<1>(w1), qb[nt][ks][0], qb[nt][ks][1]);
-            mma16816_f16(c[nt][gr], codes<2>(w0), codes<2>(w1), codes<3>(w0), codes<3>(w1), qb[nt][ks + 1][0], qb[nt][ks + 1][1]);
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (D == 128) {
+            const uint4 x = lds128(rec + k_at + (uint32_t)h * 8u * kRow);
+            w[h][0] = x.x, w[h][1] = x.y, w[h][2 * GR - 2] = x.z, w[h][2 * GR - 1] = x.w;
+          } else {
+            const uint2 x = lds64(rec + k_at + (uint32_t)h * 8u * kRow);
+            w[h][0] = x.x, w[h][1] = x.y;
           }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[i][nt][gr][e] = 0.f;
+#pragma unroll
+        for (int wi = 0; wi < 2; ++wi)
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) {
+            const uint32_t w0 = w[0][wi * GR + gr], w1 = w[1][wi * GR + gr];
+            const int ks = gr * 4 + wi * 2;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816_f16(c[i][nt][gr], codes<0>(w0), codes<0>(w1), codes<1>(w0), codes<1>(w1), qb[nt][ks][0], qb[nt][ks][1]);
+              mma16816_f16(c[i][nt][gr], codes<2>(w0), codes<2>(w1), codes<3>(w0), codes<3>(w1), qb[nt][ks + 1][0],
+                           qb[nt][ks + 1][1]);
+            }
+          }
+      }
+      uint32_t sm[2][GR];
+      const uint32_t rec = base + (uint32_t)((PK * j + mine) * 2 * REC);
+      load_scales(rec, 0, sm[0]);
+      load_scales(rec, 1, sm[1]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -351,24 +364,24 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float v = bf16_hi(sm[h][0]) * qsum[nt][0][e];
-            v = fmaf(bf16_lo(sm[h][0]), c[nt][0][2 * h + e], v);
+            v = fmaf(bf16_lo(sm[h][0]), mine == 0 ? c[0][nt][0][2 * h + e] : c[PK - 1][nt][0][2 * h + e], v);
             if constexpr (GR == 2) {
               v = fmaf(bf16_hi(sm[h][GR - 1]), qsum[nt][GR - 1][e], v);
-              v = fmaf(bf16_lo(sm[h][GR - 1]), c[nt][GR - 1][2 * h + e], v);
+              v = fmaf(bf16_lo(sm[h][GR - 1]), mine == 0 ? c[0][nt][GR - 1][2 * h + e] : c[PK - 1][nt][GR - 1][2 * h + e], v);
             }
-            s[i][nt][2 * h + e] = MOD ? v * qscale[nt][e] : v;
+            s[j][nt][2 * h + e] = MOD ? v * qscale[nt][e] : v;
           }
-      if constexpr (MOD) mods.apply(s[i], p, u, t0[i] + tok);
+      if constexpr (MOD) mods.apply(s[j], p, u, token(j, 0));
     }
     if (edge) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        bad |= !(there >> (st * NP + i) & 1u) && t0[i] < u.l1;
+      for (int j = 0; j < NS; ++j) {
+        bad |= !(there >> (st * NP + PK * j + mine) & 1u) && (page0 + PK * j + mine) * kPage < u.l1;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (!visible(i, h)) {
+          if (!visible(j, h)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[i][nt][2 * h] = s[i][nt][2 * h + 1] = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) s[j][nt][2 * h] = s[j][nt][2 * h + 1] = -INFINITY;
           }
       }
     }
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
       for (int h = 0; h < 2; ++h) {
         mx[nt][h] = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
 #pragma unroll
-        for (int i = 1; i < NP; ++i) mx[nt][h] = fmaxf(mx[nt][h], fmaxf(s[i][nt][h], s[i][nt][2 + h]));
+        for (int i = 1; i < NS; ++i) mx[nt][h] = fmaxf(mx[nt][h], fmaxf(s[i][nt][h], s[i][nt][2 + h]));
         grow |= mx[nt][h] > limit[nt][h];
       }
     if (__any_sync(0xffffffffu, grow)) {
@@ -403,23 +416,23 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
 
     // ---- P in place of the scores; its sums, and those of P minimum, keep 32 bits.  P scale goes to
     // the tensor cores as f16 (11 bits, the codes' type) in units that keep it below kMaxFactor.
-    uint32_t vs[NP][2][GR];
+    uint32_t vs[NS][2][GR];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const uint32_t rec = base + (uint32_t)((i * 2 + 1) * REC);
+    for (int i = 0; i < NS; ++i) {
+      const uint32_t rec = base + (uint32_t)(((PK * i + mine) * 2 + 1) * REC);
       load_scales(rec, 0, vs[i][0]);
       load_scales(rec, 1, vs[i][1]);
     }
     if (edge) {  // scales of masked rows may be anything: 0
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr) vs[i][h][gr] = visible(i, h) ? vs[i][h][gr] : 0u;
     }
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
+    for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -436,11 +449,11 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
             pm[nt][gr][1] = fmaf(s[i][nt][2 * h + 1], mn, pm[nt][gr][1]);
           }
       }
-    uint32_t pb[NP][NT][GR][2];
+    uint32_t pb[NS][NT][GR][2];
     auto factors = [&]() -> bool {  // true: one is too large for its unit
       __half2 top = __float2half2_rn(0.f);
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
           for (int c = 0; c < 2; ++c) {
             float f = 0.f;
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
+            for (int i = 0; i < NS; ++i)
 #pragma unroll
               for (int h = 0; h < 2; ++h) f = fmaxf(f, s[i][nt][2 * h + c] * bf16_lo(vs[i][h][gr]));
             f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, 4));
@@ -484,33 +497,43 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
       factors();
     }
 
-    // ---- O^T: rows = dims 8 gid + j and 8 gid + 4 + j of the group, columns = heads
+    // ---- O^T: rows = dims 8 gid + j and 8 gid + 4 + j of the group, columns = heads (of the pages' halves)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const uint32_t rec = base + (uint32_t)((i * 2 + 1) * REC);
-      uint32_t x[4][GR];  // tokens tid, tid ^ 5, and 8 on
+    for (int j = 0; j < NS; ++j) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t at = rec + (t & 1 ? v1_at : v0_at) + (uint32_t)(t >> 1) * 8u * kRow;
-        if constexpr (GR == 2) {
-          const uint2 y = lds64(at);
-          x[t][0] = y.x, x[t][GR - 1] = y.y;
-        } else {
-          x[t][0] = lds32(at);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) pb[j][nt][gr][h] = transpose8x8(pb[j][nt][gr][h]);
+#pragma unroll
+      for (int i = 0; i < PK; ++i) {
+        const uint32_t rec = base + (uint32_t)(((PK * j + i) * 2 + 1) * REC);
+        const bool on = PK == 1 || (gid >> 2) == i;
+        uint32_t x[4][GR];  // tokens tid, tid ^ 5, and 8 on
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t at = rec + (t & 1 ? v1_at : v0_at) + (uint32_t)(t >> 1) * 8u * kRow;
+          if constexpr (GR == 2) {
+            const uint2 y = lds64(at);
+            x[t][0] = y.x, x[t][GR - 1] = y.y;
+          } else {
+            x[t][0] = lds32(at);
+          }
         }
-      }
 #pragma unroll
-      for (int gr = 0; gr < GR; ++gr) {
-        const uint32_t ab0 = low_halves(x[0][gr], x[1][gr]), ab1 = high_halves(x[0][gr], x[1][gr]);
-        const uint32_t cd0 = low_halves(x[2][gr], x[3][gr]), cd1 = high_halves(x[2][gr], x[3][gr]);
+        for (int gr = 0; gr < GR; ++gr) {
+          const uint32_t ab0 = low_halves(x[0][gr], x[1][gr]), ab1 = high_halves(x[0][gr], x[1][gr]);
+          const uint32_t cd0 = low_halves(x[2][gr], x[3][gr]), cd1 = high_halves(x[2][gr], x[3][gr]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float(&op)[KS][4] = o[nt];
-          const uint32_t b0 = transpose8x8(pb[i][nt][gr][0]), b1 = transpose8x8(pb[i][nt][gr][1]);
-          mma16816_f16(op[gr * 4 + 0], codes<0>(ab0), codes<0>(ab1), codes<0>(cd0), codes<0>(cd1), b0, b1);
-          mma16816_f16(op[gr * 4 + 1], codes<1>(ab0), codes<1>(ab1), codes<1>(cd0), codes<1>(cd1), b0, b1);
-          mma16816_f16(op[gr * 4 + 2], codes<2>(ab0), codes<2>(ab1), codes<2>(cd0), codes<2>(cd1), b0, b1);
-          mma16816_f16(op[gr * 4 + 3], codes<3>(ab0), codes<3>(ab1), codes<3>(cd0), codes<3>(cd1), b0, b1);
+          for (int nt = 0; nt < NT; ++nt) {
+            float(&op)[KS][4] = o[nt];
+            const uint32_t b0 = on ? pb[j][nt][gr][0] : 0u, b1 = on ? pb[j][nt][gr][1] : 0u;
+            mma16816_f16(op[gr * 4 + 0], codes<0>(ab0), codes<0>(ab1), codes<0>(cd0), codes<0>(cd1), b0, b1);
+            mma16816_f16(op[gr * 4 + 1], codes<1>(ab0), codes<1>(ab1), codes<1>(cd0), codes<1>(cd1), b0, b1);
+            mma16816_f16(op[gr * 4 + 2], codes<2>(ab0), codes<2>(ab1), codes<2>(cd0), codes<2>(cd1), b0, b1);
+            mma16816_f16(op[gr * 4 + 3], codes<3>(ab0), codes<3>(ab1), codes<3>(cd0), codes<3>(cd1), b0, b1);
+          }
         }
       }
     }
@@ -518,40 +541,60 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
     st = st + 1 == ST ? 0 : st + 1;
     if (st == 0) phase ^= 1u;
   }
-  if (bad && lane == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
+  if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
 
-  // ---- this warp's part: sums over the lanes that share a column, output rows per head
+  // ---- this warp's part: sums over the lanes that share a column, output rows per head; two pages' halves
+  // of a tile (columns 4 apart, in lanes tid ^ 2) become one
   __syncthreads();  // every copy has landed and been read: the ring is free
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float sum = column_sum(l[nt][h]);
+      float sum = column_sum(l[nt][h]), ref = m[nt][h], keep = 1.f, add = 0.f;
+      if constexpr (PK == 2) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, ref, 2), l2 = __shfl_xor_sync(0xffffffffu, sum, 2);
+        ref = fmaxf(m[nt][h], m2);
+        // (a reference of -inf: no finite score, sums of 0 or NaN)
+        keep = m[nt][h] == ref || m[nt][h] == -INFINITY ? 1.f : exp2f(m[nt][h] - ref);
+        add = m2 == ref || m2 == -INFINITY ? 1.f : exp2f(m2 - ref);
+        sum = sum * keep + l2 * add;
+      }
       const int head = 8 * nt + 2 * tid + h;
-      if (gid == 0) {
-        parts.m[warp][head] = m[nt][h];
+      const bool write = PK == 1 || mine == 0;
+      if (gid == 0 && write) {
+        parts.m[warp][head] = ref;
         parts.l[warp][head] = sum;
       }
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {  // MMA j: codes j and j + 4 of word gid, times 16 for j odd
         const float y = column_sum(pm[nt][gr][h]), unit = pow2(-exponent(inv[nt][gr][h]));
         auto val = [&](int j, int e) {
-          return fmaf(o[nt][gr * 4 + j][e] * (j % 2 == 0 ? kCodeUnit : kCodeUnit / 16.f), unit, y);
+          const float x = fmaf(o[nt][gr * 4 + j][e] * (j % 2 == 0 ? kCodeUnit : kCodeUnit / 16.f), unit, y);
+          return PK == 1 ? x : x * keep + __shfl_xor_sync(0xffffffffu, x, 2) * add;
         };
-        float4* const at = reinterpret_cast<float4*>(&parts.o[warp][head][64 * gr + 8 * gid]);
-        at[0] = make_float4(val(0, h), val(1, h), val(2, h), val(3, h));
-        at[1] = make_float4(val(0, 2 + h), val(1, 2 + h), val(2, 2 + h), val(3, 2 + h));
+        const float4 a = make_float4(val(0, h), val(1, h), val(2, h), val(3, h));
+        const float4 b = make_float4(val(0, 2 + h), val(1, 2 + h), val(2, 2 + h), val(3, 2 + h));
+        if (write) {
+          float4* const at = reinterpret_cast<float4*>(&parts.o[warp][head][64 * gr + 8 * gid]);
+          at[0] = a;
+          at[1] = b;
+        }
       }
     }
   finish<T, D, HR>(p, parts, u.b, u.g, u.part, u.live);
 }
 
-template <int D, int NT>
-cudaError_t launch_nt(const ModParams& p, bool mod, cudaStream_t s) {
-  auto kern = mod ? decode_q4_kernel<D, NT, true> : decode_q4_kernel<D, NT, false>;
+template <int D, int NT, int PK>
+cudaError_t launch_q4(const ModParams& p, bool mod, cudaStream_t s) {
+  auto kern = mod ? decode_q4_kernel<D, NT, PK, true> : decode_q4_kernel<D, NT, PK, false>;
   constexpr int bytes = Q4Shape<D, NT>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   return e == cudaSuccess ? launch_decode(kern, p, bytes, Q4Shape<D, NT>::kCtas, s) : e;
+}
+template <int D>
+cudaError_t launch_d(const ModParams& p, bool mod, cudaStream_t s) {
+  if (p.G <= 4) return launch_q4<D, 1, 2>(p, mod, s);
+  return p.G <= 8 ? launch_q4<D, 1, 1>(p, mod, s) : launch_q4<D, 2, 1>(p, mod, s);
 }
 
 }  // namespace
@@ -562,6 +605,5 @@ cudaError_t cp_launch_decode_q4(const cp_decode_args& a, const cp_score_mod& mod
   using namespace cpattn;
   const ModParams p = decode_mod_params(a, mod, scale, ws, out, out_lse);
   const bool m = changes_scores(mod);
-  if (a.head_dim == 64) return p.G <= 8 ? launch_nt<64, 1>(p, m, s) : launch_nt<64, 2>(p, m, s);
-  return p.G <= 8 ? launch_nt<128, 1>(p, m, s) : launch_nt<128, 2>(p, m, s);
+  return a.head_dim == 64 ? launch_d<64>(p, m, s) : launch_d<128>(p, m, s);
 }

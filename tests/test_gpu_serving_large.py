@@ -89,6 +89,13 @@ LONG = [
     (64, 1500, 32, 2, 64, 3, 1, "bf16", False, 5.0, 0, False, True),
     (2, 12000, 4, 2, 128, 2, 8, "f32", False, 0.0, 0, True, False),
     (60, 900, 16, 4, 64, 2, 8, "f32", False, 20.0, 333, False, True),
+    # one to five query heads to a kv head: a tile of scores shared by two pages, and not
+    (5, 400, 3, 3, 128, 2, 8, "bf16", True, 0.0, 0, False, True),
+    (7, 300, 4, 2, 64, 1, 16, "bf16", True, 0.0, 100, True, False),
+    (6, 1200, 6, 2, 128, 2, 1, "bf16", True, 15.0, 0, True, True),
+    (9, 700, 8, 2, 64, 3, 5, "bf16", True, 0.0, 0, False, False),
+    (5, 900, 10, 2, 128, 1, 8, "bf16", True, 0.0, 0, False, True),
+    (64, 40, 4, 1, 128, 1, 8, "bf16", True, 0.0, 0, False, False),
 ]
 
 
