@@ -24,7 +24,7 @@
 // two, PV started by halves of P, and the cap a polynomial on the packed fp32 pipe wherever a warp's
 // scores allow it (tanh(y) / y in y^2, own least-maximum fits), only else 1 - 2 / (1 + e^2y), two
 // special-function operations per score.  8192 tokens, 16/2 heads, d = 128: 234 us with cap 50 (61% of the
-// measured bf16 peak), 210 without, 261 with a distance bias; 16384 tokens in a window of 4096 with a cap 418.
+// measured bf16 peak), 210 without, 222 with a distance bias; 16384 tokens in a window of 4096 with a cap 412.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -129,6 +129,9 @@ CP_DEV float row_abs_max(const Row& v) {
       m[i] = fmaxf(fmaxf(m[i], fabsf(v.c[i >> 1][k + 2 * (i & 1)])), fabsf(v.c[i >> 1][k + 2 * (i & 1) + 1]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
+
+// The lowest n of 64 bits (none for n <= 0, all for n >= 64).
+CP_DEV uint64_t first_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
 // cap tanh(y) in log2 units from y = cap_in * (q.k), N + 1 coefficients of tanh(y) / y in y^2.
 template <int N>
@@ -399,8 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const int ntiles = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
-  auto in_part = [&](int t) -> bool {  // some row of the CTA sees only a part of key tile t
-    const int k0 = key_lo + t * BN;
+  // With a distance bias the key tiles are walked from the last to the first: the bias is largest next to the
+  // query, so the running reference is met at once and stays (walking up, it moved at every tile of a steep
+  // head: 8192 tokens, 16/2 heads took 263 us, now 222).
+  const bool down = !CAP && p.slopes != nullptr;
+  auto key_tile = [&](int t) -> int { return down ? ntiles - 1 - t : t; };
+  auto in_part = [&](int kt) -> bool {  // some row of the CTA sees only a part of key tile kt
+    const int k0 = key_lo + kt * BN;
     return k0 < all_lo || k0 + BN > all_hi;
   };
 
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_expect_tx(bar(Sm::bFull + slot), Sm::kKV);
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
-            tma_load_2d(sKV + slot * Sm::kKV + kb * BN * 128, map, g * D + kb * 64, kv0 + key_lo + (i >> 1) * BN,
+            tma_load_2d(sKV + slot * Sm::kKV + kb * BN * 128, map, g * D + kb * 64, kv0 + key_lo + key_tile(i >> 1) * BN,
                         bar(Sm::bFull + slot));
           issued = i + 1;
         }
@@ -579,10 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) fail();
           break;
         }
-        if (in_part(t)) {
-          if (guard_v<D>(sbase + Sm::oKV + sv * Sm::kKV, key_hi - key_lo - t * BN, (warp - 2) * 32 + lane)) {
-            atomicMin(unclean, t);
-            atomicMax(unclean + 1, t);
+        const int kt = key_tile(t);
+        if (in_part(kt)) {
+          if (guard_v<D>(sbase + Sm::oKV + sv * Sm::kKV, key_hi - key_lo - kt * BN, (warp - 2) * 32 + lane)) {
+            atomicMin(unclean, kt);
+            atomicMax(unclean + 1, kt);
           }
           fence_proxy_async_smem();  // the MMA reads what was written here
         }
@@ -639,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kChunks; ++i) tmem_ld32(tS + 32 * i, v.c[i]);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) tmem_wait_ld(v.c[i]);
-      const int k0 = key_lo + t * BN + half * BH;  // this thread's first key
+      const int k0 = key_lo + key_tile(t) * BN + half * BH;  // this thread's first key
       const int c0 = lo - k0, c1 = hi - k0;        // visible columns [c0, c1)
       const bool whole_tile = __all_sync(0xffffffffu, c0 <= 0 && c1 >= BH);
       // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S columns may
@@ -689,11 +698,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!whole_tile) {
+      if (!whole_tile) {  // by bits, which become predicates seven at a time
+        const uint64_t seen = first_bits(c1) & ~first_bits(c0);
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i)
+        for (int i = 0; i < kChunks; ++i) {
+          const uint32_t w = (uint32_t)(seen >> (32 * i));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v.c[i][k] = 32 * i + k >= c0 && 32 * i + k < c1 ? v.c[i][k] : -INFINITY;
+          for (int k = 0; k < 32; ++k) v.c[i][k] = (w & (1u << k)) != 0u ? v.c[i][k] : -INFINITY;
+        }
       }
       if (!CAP || t == 0) {  // the row's largest score here, or what bounds it
         float mt = -INFINITY;
@@ -711,20 +723,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = fmaxf(fmaxf(mt, *s_other), p.cap_ref);
         } else if (pair_any(pair, mt > m + kMaxGrowth)) {
           // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8:
-          // the halves ask each other at one barrier, and exchange their maxima only then.
+          // the halves ask each other at one barrier, and exchange their maxima only then.  (The next write
+          // of s_mine comes after another vote, that is after both have read here.)
+          *s_mine = mt;
           if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
             ok = false;
             break;
           }
-          *s_mine = mt;
-          pair_sync(pair);
           mt = fmaxf(mt, *s_other);
           float alpha = 1.f;
           if (mt > m + kMaxGrowth) {
-            alpha = ex2(m - mt);
+            alpha = m == -INFINITY ? 1.f : ex2(m - mt);  // (no key yet: O is 0, as it stays)
             m = mt;
           }
-          pair_sync(pair);  // both have read before either writes again
           l *= alpha;
           if (t > 0) rescale_o<D / 2>(tO, alpha);
         }
