@@ -340,20 +340,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- the item: heads fastest, then row tiles (the last, longest one first), then sequences
   const int h0 = blockIdx.x * (TT ? 1 : 2), b = blockIdx.z;
   const int q0 = __ldg(p.cu_q + b), Tq = __ldg(p.cu_q + b + 1) - q0;
-  const int q_lo = (p.tiles - 1 - (int)blockIdx.y) * SPAN;
-  if (q_lo >= Tq) return;
-  const int q_hi = min(q_lo + SPAN, Tq);
   int kv0 = q0, Tkv = Tq;
   if (p.cu_kv != nullptr) {
     kv0 = __ldg(p.cu_kv + b);
     Tkv = __ldg(p.cu_kv + b + 1) - kv0;
   }
+  const int prefix = p.prefix != nullptr ? __ldg(p.prefix + b) : 0;
+  const int q_lo = (p.tiles - 1 - (int)blockIdx.y) * SPAN;
+  if (q_lo >= Tq) return;
+  const int q_hi = min(q_lo + SPAN, Tq);
   const int C = Tkv - Tq;  // cached tokens before the new ones
   if (C < 0) {             // fewer kv tokens than new queries: flagged, the item is skipped
     if (threadIdx.x == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int pre = p.prefix != nullptr ? min(__ldg(p.prefix + b), Tkv) : 0;
+  const int pre = min(prefix, Tkv);
   // keys [lo, hi) of a row of the sequence
   auto lo_of = [&](int row) -> int {
     int lo = 0;
@@ -362,65 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return min(lo, Tkv);
   };
   auto hi_of = [&](int row) -> int { return max(C + row + 1, pre); };
-  // union of the rows' ranges and the range that every row sees
-  int key_lo, key_hi, all_lo, all_hi;
-  if (p.kv_start == nullptr) {
-    key_lo = lo_of(q_lo);
-    key_hi = hi_of(q_hi - 1);
-    all_lo = lo_of(q_hi - 1);
-    all_hi = hi_of(q_lo);
-    if (q_hi - q_lo < SPAN) all_hi = -1;  // rows past the sequence see nothing
-  } else {
-    int v[4] = {0x7fffffff, 0, 0, 0x7fffffff};
-    for (int i = threadIdx.x; i < SPAN; i += kThreads) {
-      const int row = q_lo + i;
-      const int lo = row < q_hi ? lo_of(row) : 1, hi = row < q_hi ? hi_of(row) : 0;
-      if (lo < hi) {
-        v[0] = min(v[0], lo);
-        v[1] = max(v[1], hi);
-        v[2] = max(v[2], lo);
-        v[3] = min(v[3], hi);
-      } else {  // a row without keys: no tile is seen by every row
-        v[3] = -1;
-      }
-    }
-    v[0] = __reduce_min_sync(0xffffffffu, v[0]);
-    v[1] = __reduce_max_sync(0xffffffffu, v[1]);
-    v[2] = __reduce_max_sync(0xffffffffu, v[2]);
-    v[3] = __reduce_min_sync(0xffffffffu, v[3]);
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s_range[warp][i] = v[i];
-    }
-    __syncthreads();
-    key_lo = 0x7fffffff, key_hi = 0, all_lo = 0, all_hi = 0x7fffffff;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      key_lo = min(key_lo, s_range[w][0]);
-      key_hi = max(key_hi, s_range[w][1]);
-      all_lo = max(all_lo, s_range[w][2]);
-      all_hi = min(all_hi, s_range[w][3]);
-    }
-  }
-  const int ntiles = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
-  // With a distance bias the key tiles are walked from the last to the first: the bias is largest next to the
-  // query, so the running reference is met at once and stays (walking up, it moved at every tile of a steep
-  // head: 8192 tokens, 16/2 heads took 263 us, now 222).
-  const bool down = !CAP && p.slopes != nullptr;
-  auto key_tile = [&](int t) -> int { return down ? ntiles - 1 - t : t; };
-  auto in_part = [&](int kt) -> bool {  // some row of the CTA sees only a part of key tile kt
-    const int k0 = key_lo + kt * BN;
-    return k0 < all_lo || k0 + BN > all_hi;
-  };
-
-  if (ntiles == 0) {  // no row sees a key
-    for (int i = threadIdx.x; i < (q_hi - q_lo) * (TT ? 1 : 2); i += kThreads) {
-      const long long row = (long long)(q0 + q_lo + (TT ? i : i >> 1)) * p.Hq + h0 + (TT ? 0 : i & 1);
-      for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(p.out + row * D + c) = make_uint4(0u, 0u, 0u, 0u);
-      p.lse[row] = -INFINITY;
-    }
-    return;
-  }
-
+  // ---- barriers, Q and TMEM, while the rows' ranges come in
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sbase = smem_raw + (base - raw);
@@ -465,10 +408,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(misc), 512);
     tmem_relinquish();
   }
+
+  // union of the rows' ranges and the range that every row sees
+  int key_lo, key_hi, all_lo, all_hi;
+  if (p.kv_start == nullptr) {
+    key_lo = lo_of(q_lo);
+    key_hi = hi_of(q_hi - 1);
+    all_lo = lo_of(q_hi - 1);
+    all_hi = hi_of(q_lo);
+    if (q_hi - q_lo < SPAN) all_hi = -1;  // rows past the sequence see nothing
+  } else {
+    int v[4] = {0x7fffffff, 0, 0, 0x7fffffff};
+    for (int i = (int)threadIdx.x - 128; i >= 0 && i < SPAN; i += kThreads - 128) {  // (warps 0 and 1 set up)
+      const int row = q_lo + i;
+      const int lo = row < q_hi ? lo_of(row) : 1, hi = row < q_hi ? hi_of(row) : 0;
+      if (lo < hi) {
+        v[0] = min(v[0], lo);
+        v[1] = max(v[1], hi);
+        v[2] = max(v[2], lo);
+        v[3] = min(v[3], hi);
+      } else {  // a row without keys: no tile is seen by every row
+        v[3] = -1;
+      }
+    }
+    v[0] = __reduce_min_sync(0xffffffffu, v[0]);
+    v[1] = __reduce_max_sync(0xffffffffu, v[1]);
+    v[2] = __reduce_max_sync(0xffffffffu, v[2]);
+    v[3] = __reduce_min_sync(0xffffffffu, v[3]);
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_range[warp][i] = v[i];
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
+  if (p.kv_start != nullptr) {
+    key_lo = 0x7fffffff, key_hi = 0, all_lo = 0, all_hi = 0x7fffffff;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      key_lo = min(key_lo, s_range[w][0]);
+      key_hi = max(key_hi, s_range[w][1]);
+      all_lo = max(all_lo, s_range[w][2]);
+      all_hi = min(all_hi, s_range[w][3]);
+    }
+  }
+  const int ntiles = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
+  // With a distance bias the key tiles are walked from the last to the first: the bias is largest next to the
+  // query, so the running reference is met at once and stays (walking up, it moved at every tile of a steep
+  // head: 8192 tokens, 16/2 heads took 263 us, now 222).
+  const bool down = !CAP && p.slopes != nullptr;
+  auto key_tile = [&](int t) -> int { return down ? ntiles - 1 - t : t; };
+  auto in_part = [&](int kt) -> bool {  // some row of the CTA sees only a part of key tile kt
+    const int k0 = key_lo + kt * BN;
+    return k0 < all_lo || k0 + BN > all_hi;
+  };
+
+  if (ntiles == 0) {  // no row sees a key
+    for (int i = threadIdx.x; i < (q_hi - q_lo) * (TT ? 1 : 2); i += kThreads) {
+      const long long row = (long long)(q0 + q_lo + (TT ? i : i >> 1)) * p.Hq + h0 + (TT ? 0 : i & 1);
+      for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(p.out + row * D + c) = make_uint4(0u, 0u, 0u, 0u);
+      p.lse[row] = -INFINITY;
+    }
+    if (threadIdx.x == 0) mbar_wait(bar(Sm::bQ), 0u, nullptr, kBudget);  // Q has landed before the CTA exits
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+
   const int g = h0 / p.G;
 
   if (warp < 4) {
