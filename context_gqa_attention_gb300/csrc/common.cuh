@@ -145,7 +145,10 @@ bool cp_make_bf16_page_map(void* map, const void* base, unsigned long long rows)
 bool cp_make_bf16_page_map4(void* map, const void* base, unsigned long long rows);
 
 // Scratch of the fused decode: arrival counters [B][Hkv] (zero between calls), partial LSEs
-// [cp*S][B][Hq] and partial outputs [cp*S][B][Hq][d], each region 256-byte aligned.
+// [cp*S][B][Hq] and partial outputs [cp*S][B][Hq][d], each region 256-byte aligned.  The counters' region
+// has one size whatever the shape, so that the partials of one call never lie where another shape's
+// counters are expected to be zero.
+constexpr size_t kCpDecodeCounters = 65536;
 struct CpDecodeWorkspace {
   int32_t* counters;
   float* partial_lse;
@@ -154,7 +157,8 @@ struct CpDecodeWorkspace {
 inline size_t cp_align256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline size_t cp_decode_ws_layout(int B, int Hq, int Hkv, int d, int P, size_t* off_lse,
                                   size_t* off_out) {
-  const size_t c = cp_align256((size_t)B * Hkv * sizeof(int32_t));
+  const size_t n = (size_t)B * Hkv;
+  const size_t c = cp_align256((n > kCpDecodeCounters ? n : kCpDecodeCounters) * sizeof(int32_t));
   const size_t l = cp_align256((size_t)P * B * Hq * sizeof(float));
   const size_t o = cp_align256((size_t)P * B * Hq * d * sizeof(float));
   *off_lse = c;

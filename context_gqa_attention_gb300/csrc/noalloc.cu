@@ -97,7 +97,7 @@ extern "C" cp_status cp_decode_attention_noalloc(const cp_decode_args* a, void* 
   if (e != cudaSuccess) return cp_launch_status(e, "static scratch address");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // the arrival counters must start at zero whatever an earlier call left behind
-  e = cudaMemsetAsync(ws, 0, ol, s);
+  e = cudaMemsetAsync(ws, 0, (size_t)a->num_seqs * a->num_kv_heads * sizeof(int32_t), s);
   if (e != cudaSuccess) return cp_launch_status(e, "static scratch clear");
   CpDecodeWorkspace w;
   w.counters = static_cast<int32_t*>(ws);

@@ -332,7 +332,8 @@ cp_status cp_partial_attn_decode(const cp_decode_args* args, void* stream);
  * Requires cp * num_splits <= 256.
  * workspace: device scratch of at least cp_decode_workspace_size() bytes, 256-byte aligned,
  * zero-filled before its first use (the call leaves it reusable: its counters return to
- * zero).  Calls that use the same workspace must not overlap on the GPU.
+ * zero).  Calls of different shapes may share one (num_seqs * num_kv_heads <= 65536 each; more
+ * take one of their own).  Calls that use the same workspace must not overlap on the GPU.
  * ---------------------------------------------------------------------------- */
 cp_status cp_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                    int32_t head_dim, int32_t cp, int32_t num_splits,
@@ -545,7 +546,8 @@ cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* m
  * for a sequence is reported in err (CP_ERR_DEVICE_BOUNDS).  A sequence without a visible token
  * gives output 0 and LSE -inf (partials: all empty).
  * The fused calls take the workspace of cp_decode_attention (cp_decode_workspace_size, zero-filled
- * before its first use and left reusable); calls that use one workspace must not overlap.
+ * before its first use and left reusable, also for that call and for other shapes); calls that use
+ * one workspace must not overlap.
  * ---------------------------------------------------------------------------- */
 cp_status cp_decode_mod_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t cp, int32_t interleave,
                              int32_t max_seq_len, int32_t window, int32_t q4, int32_t* num_splits,

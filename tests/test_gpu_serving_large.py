@@ -366,3 +366,53 @@ def test_calls_that_feed_one_another(lib):
             results.append(seen)
         for other in results[1:]:
             assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("q4", [True, False])
+def test_two_graphs_share_a_workspace(lib, q4):
+    """Two captured decodes of different shapes over one workspace, replayed in turn with eager calls
+    between: every call leaves the workspace as the next one, of whatever shape, needs it."""
+    graphs, wants, outs = [], [], []
+    shapes = [(2, [900, 333], 16, 2, 6, 96), (40, [700] * 40, 16, 2, 3, 128)]      # in one cluster's reach, and not
+    need = max(lib.cp_decode_workspace_size(B, Hq, Hkv, 128, 2, S) for B, _, Hq, Hkv, S, _ in shapes)
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    call = lib.cp_decode_attention_q4 if q4 else lib.cp_decode_attention_mod
+    runs = []
+    for B, lens, Hq, Hkv, S, tokens in shapes:
+        k, v, t, _, _ = _fill(lib, lens, Hkv, 128, 2, 8, torch.bfloat16, q4, 1)
+        q, sl = torch.randn(B, Hq, 128, device=DEV).to(torch.bfloat16), torch.tensor(lens, **I32)
+
+        def run(q=q, k=k, v=v, t=t, sl=sl, S=S, tokens=tokens):
+            return call(q, k, v, t, sl, 2, 8, num_splits=S, split_tokens=tokens, workspace=ws)
+        runs.append(run)
+        wants.append([x.clone() for x in run()])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run())
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 0, 1, 0, 1, 1, 0):
+        for x in outs[i]:
+            x.zero_()
+        graphs[i].replay()
+        between = runs[1 - i]()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], wants[i]))
+        assert all(torch.equal(a, b) for a, b in zip(between, wants[1 - i]))
+    assert int(ws[:4 * 80].max()) == 0              # the counters are back at zero
+
+
+def test_the_plain_decode_shares_a_workspace_between_shapes(lib):
+    """cp_decode_attention, and the calls with modified scores after it, over one workspace."""
+    ws, runs = None, []
+    for B, L, S, tokens in ((2, 900, 6, 96), (40, 700, 6, 64)):
+        k, v, t, _, _ = _fill(lib, [L] * B, 2, 128, 2, 8, torch.bfloat16, False, 1)
+        q, sl = torch.randn(B, 16, 128, device=DEV).to(torch.bfloat16), torch.full((B,), L, **I32)
+        for call in (lib.cp_decode_attention, lib.cp_decode_attention_mod):
+            def run(ws, call=call, q=q, k=k, v=v, t=t, sl=sl, S=S, tokens=tokens):
+                return call(q, k, v, t, sl, 2, 8, num_splits=S, split_tokens=tokens, workspace=ws)
+            runs.append((run, [x.clone() for x in run(None)]))
+    ws = torch.zeros(max(lib.cp_decode_workspace_size(B, 16, 2, 128, 2, 6) for B in (2, 40)), dtype=torch.uint8, device=DEV)
+    for i in (0, 2, 1, 3, 2, 0, 3, 1, 0, 3):
+        run, want = runs[i]
+        assert all(torch.equal(a, b) for a, b in zip(run(ws), want))
