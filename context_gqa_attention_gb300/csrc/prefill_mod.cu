@@ -173,8 +173,8 @@ CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y) {
 }
 
 // Capped scores are bounded, |x| <= cap log2(e), so with a cap of at most kMaxCapLog2 they need no
-// running maximum: the row's maximum over the first tile, but at least cap log2(e) - kCapAbove, stays
-// the reference, and no P is above 2^kCapAbove (which fp32 sums and bf16 operands hold) while the
+// running maximum: the row's maximum over the first tile in which it sees a key, but at least cap log2(e) -
+// kCapAbove, stays the reference, and no P is above 2^kCapAbove (which fp32 sums and bf16 operands hold) while the
 // largest is at least 2^-kMaxCapLog2.  P then follows from the score in one chain without a dependence
 // on the rest of the row, and the polynomial's packed FMAs run under the exponentials' special-function
 // time.  (A reference that is one of the row's own scores makes its P exactly 1: with a constant one,
@@ -638,6 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(Sm::bP + 2 * tile + i));
     };
     for (int t = 0; t < ntiles; ++t) {
+      const int kt0 = key_lo + key_tile(t) * BN;
+      // CAP: a row's reference is set, for good, at the first tile in which it sees a key (both halves of
+      // a row say the same)
+      const bool first = CAP && m == -INFINITY && max(lo, kt0) < min(hi, kt0 + BN);
+      const bool some_first = CAP && __any_sync(0xffffffffu, first);
       ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
       // a warp that gives up raises the abort flag; its partner gives up at its own wait, or where the
       // two meet within the tile
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) fail();
         __syncwarp();
         // the votes below, as the partner will meet them
-        if (!CAP || t == 0) pair_any(pair, true);
+        if (!CAP || some_first) pair_any(pair, true);
         if constexpr (!CAP) pair_any(pair, true);
         break;
       }
@@ -655,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kChunks; ++i) tmem_ld32(tS + 32 * i, v.c[i]);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) tmem_wait_ld(v.c[i]);
-      const int k0 = key_lo + key_tile(t) * BN + half * BH;  // this thread's first key
-      const int c0 = lo - k0, c1 = hi - k0;        // visible columns [c0, c1)
+      const int k0 = kt0 + half * BH;        // this thread's first key
+      const int c0 = lo - k0, c1 = hi - k0;  // visible columns [c0, c1)
       const bool whole_tile = __all_sync(0xffffffffu, c0 <= 0 && c1 >= BH);
       // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S columns may
       // take P(t)
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool near = false;
       if constexpr (CAP) {
         y = row_abs_max(v) * p.cap_in;
-        near = t > 0 && whole_tile && __all_sync(0xffffffffu, y <= kCapNear);
+        near = !some_first && whole_tile && __all_sync(0xffffffffu, y <= kCapNear);
       }
       if (CAP && near) {
         const uint64_t n2 = f2(-m, -m);
@@ -714,20 +719,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; ++k) v.c[i][k] = (w & (1u << k)) != 0u ? v.c[i][k] : -INFINITY;
         }
       }
-      if (!CAP || t == 0) {  // the row's largest score here, or what bounds it
+      if (!CAP || some_first) {  // the row's largest score here, or what bounds it
         float mt = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
           const float x = chunk_max(v.c[i]);
           mt = fmaxf(mt, !CAP && fold ? fmaf(x, s0, slope * (float)(behind + 32 * i + 31)) : x * sc);
         }
-        if constexpr (CAP) {  // the reference of both halves, for good
+        if constexpr (CAP) {
           *s_mine = mt;
           if (pair_any(pair, false)) {  // the partner gave up
             ok = false;
             break;
           }
-          m = fmaxf(fmaxf(mt, *s_other), p.cap_ref);
+          if (first) m = fmaxf(fmaxf(mt, *s_other), p.cap_ref);
+          pair_sync(pair);  // both have read before either writes again
         } else if (pair_any(pair, mt > m + kMaxGrowth)) {
           // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8:
           // the halves ask each other at one barrier, and exchange their maxima only then.  (The next write

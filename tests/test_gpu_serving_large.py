@@ -416,3 +416,17 @@ def test_the_plain_decode_shares_a_workspace_between_shapes(lib):
     for i in (0, 2, 1, 3, 2, 0, 3, 1, 0, 3):
         run, want = runs[i]
         assert all(torch.equal(a, b) for a, b in zip(run(ws), want))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("cap", [0.0, 30.0, 50.0, 100.0])
+def test_prefill_rows_of_one_key_are_that_keys_value(lib, Hq, Hkv, d, cap):
+    """With a window of one key, and with documents of one token, every output is its own value row bit for
+    bit: the weight of a row's only key is 1, wherever in the sequence it lies."""
+    n = 700
+    q, k, v = (torch.randn(n, h, d, device=DEV).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    want = v.repeat_interleave(Hq // Hkv, 1)
+    start = torch.arange(n, **I32)
+    for kw in (dict(window=1), dict(kv_start=start), dict(kv_start=start, window=300)):
+        out, _ = lib.cp_attn_prefill_mod(q, _cu([n]), k, v, softcap=cap, max_seqlen_q=n, **kw)
+        assert torch.equal(out, want)
