@@ -307,6 +307,7 @@ def test_nearly_constant_rows_in_four_bits(lib, dt, d):
     decodes as such (a negative scale would make infinite weights of zero codes)."""
     cp, I, lens = 2, 8, [50, 33]
     k, v, t = _pool(lens, 2, d, cp, I, torch.uint8, True, 6)
+    k.zero_(), v.zero_()        # (pages end behind the sequences: their last rows are never written)
     g = torch.Generator(device=DEV).manual_seed(6)
     level = torch.tensor([257.3, -0.70123, 1000.9, 3e-5], device=DEV)
     kn, vn = (level[torch.randint(0, 4, (sum(lens), 2, 1), generator=g, device=DEV)].expand(-1, -1, d) *
