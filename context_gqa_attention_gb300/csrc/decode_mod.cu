@@ -265,12 +265,32 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_mod_kerne
 }
 
 // ------------------------------------------------------------------------------ fp32 caches
+// Two fp32 values per instruction: no more arithmetic a cycle, but half the instructions.
+CP_DEV uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+CP_DEV void f2u(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+CP_DEV uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+CP_DEV uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // fp32 K and V keep their 24 bits, so the products run on the CUDA cores: two lanes per token for
 // q.k, alternating over its 16-byte vectors, D / 4 lanes per row for P V.  A page's K vectors are all in
 // flight at once, and refilled with the next page's as soon as the scores are computed; V's likewise
 // after the second product.
+// Bound by latency and issue at 8 to 12 warps per SM (16 sequences of 300..4000 tokens, 16/2 heads,
+// d = 128, cap 30: 39 us; 45 with a maximum per page and scalar arithmetic).
 template <int D, int HR>
-__global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModParams p) {
+__global__ void __launch_bounds__(kWarps * 32, D == 64 && HR <= 4 ? 3 : 2) decode_mod_f32_kernel(const ModParams p) {
   constexpr int NCH = D / 4;      // lanes per V row
   constexpr int TG = 32 / NCH;    // V rows a warp reads at a time
   constexpr int NK = D / 8, NV = kPage / TG;
@@ -309,63 +329,81 @@ __global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModPa
   const float* qg = static_cast<const float*>(p.q) + ((long long)u.b * p.Hq + (long long)u.g * p.G) * D;
   for (int i = threadIdx.x; i < HR * D; i += blockDim.x) (&qs[0][0])[i] = i < p.G * D ? qg[i] : 0.f;
   __syncthreads();
-  float m[HR], l[HR], acc[HR][4];
+  float m[HR], l[HR];      // reference (log2), and the sum of this lane's token
+  uint64_t acc[HR][2];     // pairs of dims
 #pragma unroll
   for (int h = 0; h < HR; ++h) {
     m[h] = -INFINITY;
     l[h] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
+    acc[h][0] = acc[h][1] = f2(0.f, 0.f);
   }
   bool bad = false;
   for (; pg < pg1; pg += kWarps) {
     const int t0 = pg * kPage, t = t0 + tk;
     const bool on = id >= 0 && t >= u.a && t < u.l1;
     bad |= id < 0;
-    float s[HR];
+    uint64_t dot[HR];
 #pragma unroll
-    for (int h = 0; h < HR; ++h) s[h] = 0.f;
+    for (int h = 0; h < HR; ++h) dot[h] = f2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < NK; ++c) {
+      const uint64_t k0 = f2(k[c].x, k[c].y), k1 = f2(k[c].z, k[c].w);
 #pragma unroll
       for (int h = 0; h < HR; ++h) {
         const float4 q = *reinterpret_cast<const float4*>(&qs[h][8 * c + 4 * half]);
-        s[h] += q.x * k[c].x + q.y * k[c].y + q.z * k[c].z + q.w * k[c].w;
+        dot[h] = ffma2(f2(q.x, q.y), k0, ffma2(f2(q.z, q.w), k1, dot[h]));
       }
     }
     if (id_nxt >= 0) load_k(id_nxt);
     const int id_after = page_of(pg + 2 * kWarps);
     const float dist = p.slopes != nullptr ? distance(p, u, t) : 0.f;
-    float alpha[HR];
+    float s[HR];
+    bool grow = false;
 #pragma unroll
     for (int h = 0; h < HR; ++h) {
-      s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
-      float x = s[h] * p.scale;
+      float lo, hi;
+      f2u(dot[h], lo, hi);
+      lo += hi;
+      lo += __shfl_xor_sync(0xffffffffu, lo, 1);
+      float x = lo * p.scale;
       if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
       if (p.slopes != nullptr && h < p.G) x -= __ldg(p.slopes + u.g * p.G + h) * dist;
-      x = on ? x * kLog2e : -INFINITY;
-      const float m_new = fmaxf(m[h], warp_max(x));
-      alpha[h] = m_new == m[h] ? 1.f : exp2f(m[h] - m_new);
-      m[h] = m_new;
-      const float e = exp2f(x - (m_new == -INFINITY ? 0.f : m_new));
-      l[h] = l[h] * alpha[h] + (half == 0 ? e : 0.f);
-      if (half == 0) ps[warp][tk][h] = e;
+      s[h] = on ? x * kLog2e : -INFINITY;
+      grow |= s[h] > m[h] + kMaxGrowth;
+    }
+    if (__any_sync(0xffffffffu, grow)) {  // as in the bf16 kernel: rare
+#pragma unroll
+      for (int h = 0; h < HR; ++h) {
+        const float m_new = fmaxf(m[h], warp_max(s[h]));
+        const float alpha = m_new == m[h] ? 1.f : exp2f(m[h] - m_new);
+        m[h] = m_new;
+        l[h] *= alpha;
+        acc[h][0] = fmul2(acc[h][0], f2(alpha, alpha));
+        acc[h][1] = fmul2(acc[h][1], f2(alpha, alpha));
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < HR; ++h) {
+      const float e = exp2f(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+      if (half == 0) {
+        l[h] += e;
+        ps[warp][tk][h] = e;
+      }
     }
     __syncwarp();
-#pragma unroll
-    for (int h = 0; h < HR; ++h)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[h][e] *= alpha[h];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int r = vt + i * TG;
       // rows behind the sequence may hold anything, and 0 times NaN is NaN
       const bool seen = id >= 0 && t0 + r >= u.a && t0 + r < u.l1;
       const float4 x = seen ? v[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const uint64_t x0 = f2(x.x, x.y), x1 = f2(x.z, x.w);
 #pragma unroll
       for (int h = 0; h < HR; ++h) {
         const float w = ps[warp][r][h];
-        acc[h][0] += w * x.x, acc[h][1] += w * x.y, acc[h][2] += w * x.z, acc[h][3] += w * x.w;
+        const uint64_t w2 = f2(w, w);
+        acc[h][0] = ffma2(w2, x0, acc[h][0]);
+        acc[h][1] = ffma2(w2, x1, acc[h][1]);
       }
     }
     if (id_nxt >= 0) load_v(id_nxt);
@@ -381,12 +419,14 @@ __global__ void __launch_bounds__(kWarps * 32) decode_mod_f32_kernel(const ModPa
       parts.m[warp][h] = m[h];
       parts.l[warp][h] = sum;
     }
+    float a[4];
+    f2u(acc[h][0], a[0], a[1]);
+    f2u(acc[h][1], a[2], a[3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int o = NCH; o < 32; o <<= 1) acc[h][e] += __shfl_xor_sync(0xffffffffu, acc[h][e], o);
-    if (vt == 0)
-      *reinterpret_cast<float4*>(&parts.o[warp][h][4 * vc]) = make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]);
+      for (int o = NCH; o < 32; o <<= 1) a[e] += __shfl_xor_sync(0xffffffffu, a[e], o);
+    if (vt == 0) *reinterpret_cast<float4*>(&parts.o[warp][h][4 * vc]) = make_float4(a[0], a[1], a[2], a[3]);
   }
   finish<float, D, HR>(p, parts, u.b, u.g, u.part, u.live);
 }
