@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int prefix = p.prefix != nullptr ? __ldg(p.prefix + b) : 0;
   const int q_lo = (p.tiles - 1 - (int)blockIdx.y) * SPAN;
+  if (blockIdx.y == 0 && threadIdx.x == 0 && Tq - q_lo > SPAN) report(p.err, CP_ERR_DEVICE_BOUNDS);  // max_seqlen_q
   if (q_lo >= Tq) return;
   const int q_hi = min(q_lo + SPAN, Tq);
   const int C = Tkv - Tq;  // cached tokens before the new ones

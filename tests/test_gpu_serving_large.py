@@ -419,6 +419,17 @@ def test_the_plain_decode_shares_a_workspace_between_shapes(lib):
         assert all(torch.equal(a, b) for a, b in zip(run(ws), want))
 
 
+def test_prefill_reports_a_sequence_past_max_seqlen_q(lib):
+    for Hq, Hkv in ((4, 2), (3, 1)):
+        q, k, v = (torch.randn(700, h, 64, device=DEV).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+        full, _ = lib.cp_attn_prefill_mod(q, _cu([100, 600]), k, v, max_seqlen_q=600)
+        for longest, flagged in ((600, 0), (700, 0), (256, 5)):
+            err, out = torch.zeros(1, **I32), torch.zeros_like(q)
+            lib.cp_attn_prefill_mod(q, _cu([100, 600]), k, v, max_seqlen_q=longest, out=out, err=err)
+            assert int(err) == flagged and torch.equal(out[:356], full[:356])
+            assert torch.equal(out[356:], full[356:]) if not flagged else not out[356:].any()
+
+
 @pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64)])
 @pytest.mark.parametrize("cap", [0.0, 30.0, 50.0, 100.0])
 def test_prefill_rows_of_one_key_are_that_keys_value(lib, Hq, Hkv, d, cap):
