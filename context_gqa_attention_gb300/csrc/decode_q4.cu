@@ -244,7 +244,10 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
       for (int gr = 0; gr < GR; ++gr) qsum[nt][gr][c] = q_sums[head][gr];
     }
   }
-  __syncthreads();  // the ring's last stage is free
+  // the ring's last stage is free, and the copy engine writes it next: ordinary stores and loads of shared
+  // memory are ordered before its own by a proxy fence of every thread that made them
+  sm100::fence_proxy_async_smem();
+  __syncthreads();
   const Mods<NT> mods(p, u, PK == 2 ? tid & 1 : tid);
 
   // Per head of this thread's columns (2 tid, 2 tid + 1): reference m (log2; neg = -m, 0 before the
