@@ -224,13 +224,13 @@ CP_DEV void merge_store(void* out, float* out_lse, long long u, int lane, const 
 constexpr int kMergeUnits = 2;
 
 template <int D, bool BF16_OUT, int P>
-__global__ void __launch_bounds__(256) merge_small_kernel(const float* __restrict__ po,
-                                                          const float* __restrict__ pl,
+__global__ void __launch_bounds__(256) merge_small_kernel(const float* po,
+                                                          const float* pl,
                                                           long long units, void* out,
                                                           float* out_lse) {
   constexpr int E = D / 32, U = kMergeUnits;
   using V = typename MergeVec<D>::T;
-  griddep_wait();  // the partials' producer may still be finishing
+  griddep_wait();  // the partials' producer may still be finishing: ordinary loads, see chained_start
   // U units per warp, every load of all of them issued before any arithmetic (twice the
   // bytes in flight of one unit per warp)
   const long long u0 = (((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * U;
@@ -242,13 +242,13 @@ __global__ void __launch_bounds__(256) merge_small_kernel(const float* __restric
   for (int j = 0; j < U; ++j)
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      lp[j][p] = u0 + j < units ? __ldg(pl + (long long)p * units + u0 + j) * kLog2e : -INFINITY;
+      lp[j][p] = u0 + j < units ? ld(pl + (long long)p * units + u0 + j) * kLog2e : -INFINITY;
 #pragma unroll
   for (int j = 0; j < U; ++j)
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       if (lp[j][p] > -INFINITY)
-        x[j][p] = __ldg(reinterpret_cast<const V*>(po + ((long long)p * units + u0 + j) * D + lane * E));
+        x[j][p] = ld(reinterpret_cast<const V*>(po + ((long long)p * units + u0 + j) * D + lane * E));
       else
         x[j][p] = V{};
     }
@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(256) merge_small_kernel(const float* __restric
 // Any number of partials (the decode case, cp x splits): LSEs read 32 at a time across the
 // lanes; only non-empty partials' rows are read.
 template <int D, bool BF16_OUT>
-__global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ po,
-                                                    const float* __restrict__ pl, int P,
+__global__ void __launch_bounds__(256) merge_kernel(const float* po,
+                                                    const float* pl, int P,
                                                     long long units, void* out, float* out_lse) {
   constexpr int E = D / 32;
   using V = typename MergeVec<D>::T;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ po
   float M = -INFINITY;
   for (int p0 = 0; p0 < P; p0 += 32) {
     const int p = p0 + lane;
-    if (p < P) M = fmaxf(M, __ldg(pl + (long long)p * units + u) * kLog2e);
+    if (p < P) M = fmaxf(M, ld(pl + (long long)p * units + u) * kLog2e);
   }
   M = warp_max(M);
   float acc[E];
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ po
   if (M > -INFINITY) {
     for (int p0 = 0; p0 < P; p0 += 32) {
       const int p = p0 + lane;
-      const float lp = p < P ? __ldg(pl + (long long)p * units + u) * kLog2e : -INFINITY;
+      const float lp = p < P ? ld(pl + (long long)p * units + u) * kLog2e : -INFINITY;
       unsigned live = __ballot_sync(0xffffffffu, lp > -INFINITY);
       while (live) {  // non-empty partials of this group, four loads in flight at a time
         float w[4];
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ po
             const int j = __ffs(live) - 1;
             live &= live - 1;
             w[q] = exp2f(__shfl_sync(0xffffffffu, lp, j) - M);
-            x[q] = __ldg(reinterpret_cast<const V*>(po + ((long long)(p0 + j) * units + u) * D + lane * E));
+            x[q] = ld(reinterpret_cast<const V*>(po + ((long long)(p0 + j) * units + u) * D + lane * E));
             n = q + 1;
           }
         }

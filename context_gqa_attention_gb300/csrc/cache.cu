@@ -42,14 +42,14 @@ struct Placement {
 CP_DEV int seq_of(const Placement& p, int row0, int row) {
   if (p.B > 256) {
     const int s = seq_of_row(p.cu, p.B, row);
-    return row < __ldg(p.cu + s + 1) ? s : p.B;
+    return row < ld(p.cu + s + 1) ? s : p.B;
   }
   int s = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + (int)(threadIdx.x & 31);
-    s += __popc(__ballot_sync(0xffffffffu, b < p.B && __ldg(p.cu + b + 1) <= row0));
+    s += __popc(__ballot_sync(0xffffffffu, b < p.B && ld(p.cu + b + 1) <= row0));
   }
-  while (s < p.B && __ldg(p.cu + s + 1) <= row) ++s;
+  while (s < p.B && ld(p.cu + s + 1) <= row) ++s;
   return s;
 }
 
@@ -60,13 +60,13 @@ CP_DEV bool locate(const Placement& p, int row0, int row, long long& pos, Slot& 
   slot.row = 0;
   pos = -1;
   const int s = seq_of(p, row0, row);
-  if (s >= p.B || row < __ldg(p.cu + s)) return false;
-  pos = (long long)__ldg(p.start + s) + (row - __ldg(p.cu + s));
+  if (s >= p.B || row < ld(p.cu + s)) return false;
+  pos = (long long)ld(p.start + s) + (row - ld(p.cu + s));
   if (pos >= 0) {
     const unsigned turn = (unsigned)pos / (unsigned)p.I, l = turn / (unsigned)p.cp;  // positions fit 32 bits
     const int r = (int)(turn - l * (unsigned)p.cp);
     const long long local = (long long)l * p.I + ((unsigned)pos - turn * (unsigned)p.I), col = local / kQ4Page;
-    const int id = col < p.max_blocks ? __ldg(p.tables + ((long long)r * p.B + s) * p.max_blocks + col) : -1;
+    const int id = col < p.max_blocks ? ld(p.tables + ((long long)r * p.B + s) * p.max_blocks + col) : -1;
     if (id >= 0 && id < p.pool) {
       slot.head = (r * p.pool + id) * p.Hkv;
       slot.row = (int)(local % kQ4Page);
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_write_kernel(const WritePara
 
   unsigned long long f[D / 64];  // frequencies lane, lane + 32 in turns per position
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) f[i] = lane + 32 * i < h ? turns_of(__ldg(reinterpret_cast<const long long*>(p.inv_freq) + lane + 32 * i)) : 0ull;
+  for (int i = 0; i < D / 64; ++i) f[i] = lane + 32 * i < h ? turns_of(ld(reinterpret_cast<const long long*>(p.inv_freq) + lane + 32 * i)) : 0ull;
   Slot mine;
   long long my_pos = -1;
   const bool in = locate(p.at, row0, min(row0 + lane, row0 + nt - 1), my_pos, mine);
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadParams p)
   stream_rows<V, 4>(
       p, slots[threadIdx.x >> 5],
       [&](bool is_v, long long head, int row, int v) {
-        return __ldg(reinterpret_cast<const uint4*>(is_v ? p.v_cache : p.k_cache) + (head * kQ4Page + row) * V + v);
+        return ld(reinterpret_cast<const uint4*>(is_v ? p.v_cache : p.k_cache) + (head * kQ4Page + row) * V + v);
       },
       [&](bool is_v, long long at, const uint4& x) { static_cast<uint4*>(is_v ? p.v_out : p.k_out)[at] = x; });
 }
@@ -497,10 +497,10 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadParams p) {
       p, slots[threadIdx.x >> 5],
       [&](bool is_v, long long head, int row, int c) {
         const uint8_t* rec = (is_v ? p.v_cache : p.k_cache) + head * q4_record_bytes(D);
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(rec + row * (D / 2)) + c);
+        const uint2 w = ld(reinterpret_cast<const uint2*>(rec + row * (D / 2)) + c);
         const uint32_t* sm = reinterpret_cast<const uint32_t*>(rec + 8 * D) + row * GR;
-        const uint32_t s0 = __ldg(sm);
-        return make_uint4(w.x, w.y, s0, GR == 2 ? __ldg(sm + GR - 1) : s0);
+        const uint32_t s0 = ld(sm);
+        return make_uint4(w.x, w.y, s0, GR == 2 ? ld(sm + GR - 1) : s0);
       },
       [&](bool is_v, long long at, const uint4& w) {
         float x[8];

@@ -37,9 +37,15 @@ CP_DEV void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_de
 // one runs, as soon as all of this one's are, and wait until it has completed.  (Calls back to back on
 // a stream: one sequence's 4-bit decode 10.2 -> 7.8 us, 64 appended tokens 6.1 -> 4.4, a prefill of 8192
 // tokens 236 -> 230.)
+// What such a kernel reads may have been written while it was already there, so it reads with ordinary loads:
+// those of the non-coherent path (__ldg, ld.global.nc) are for data that nobody writes during the kernel's life.
 CP_DEV void chained_start() {
   griddep_launch_dependents();
   griddep_wait();
+}
+template <typename T>
+CP_DEV T ld(const T* p) {
+  return *p;
 }
 template <typename... K, typename... A>
 inline cudaError_t launch_chained(void (*kern)(K...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
@@ -93,11 +99,11 @@ CP_DEV int rank_local_len(long long L, int r, int cp, int I) {
 }
 
 // Sequence of a row: largest b with cu[b] <= row (cu non-decreasing, cu[0] = 0).
-CP_DEV int seq_of_row(const int32_t* __restrict__ cu, int num_seqs, int row) {
+CP_DEV int seq_of_row(const int32_t* cu, int num_seqs, int row) {
   int lo = 0, hi = num_seqs - 1;
   while (lo < hi) {
     int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= row) lo = mid; else hi = mid - 1;
+    if (ld(cu + mid) <= row) lo = mid; else hi = mid - 1;
   }
   return lo;
 }

@@ -26,8 +26,8 @@ namespace {
 struct Piece {  // 16 bytes of a row in 32-bit words
   uint32_t w[4];
 };
-CP_DEV void ldg_piece(Piece& x, const uint8_t* p) {
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+CP_DEV void load_piece(Piece& x, const uint8_t* p) {
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]) : "l"(p));
 }
 
@@ -44,7 +44,7 @@ struct PageK {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) ldg_piece(x[i][c], r + i * (16 * D) + c * 64);
+      for (int c = 0; c < D / 32; ++c) load_piece(x[i][c], r + i * (16 * D) + c * 64);
   }
 };
 template <int D>
@@ -55,7 +55,7 @@ struct PageV {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) ldg_piece(x[i][c], r + (i & 1) * (2 * D) + (i >> 1) * (16 * D) + c * 128);
+      for (int c = 0; c < D / 64; ++c) load_piece(x[i][c], r + (i & 1) * (2 * D) + (i >> 1) * (16 * D) + c * 128);
   }
 };
 
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_mod_kerne
   auto fetch_ids = [&](int j0) -> int {
     const int pg = pg0 + (j0 + lane) * kWarps + warp;
     int id = -1;
-    if (pg < pg1 && pg < p.max_blocks) id = __ldg(trow + pg);
+    if (pg < pg1 && pg < p.max_blocks) id = ld(trow + pg);
     return id >= 0 && id < p.pool ? id : -1;
   };
   int ids = fetch_ids(0), ids_next = fetch_ids(32);
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) decode_mod_kerne
     const int head = i / TPH, c = i % TPH;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (head < p.G)
-      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+      x = ld(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
                                                ((long long)u.b * p.Hq + (long long)u.g * p.G + head) * D) + c);
     *reinterpret_cast<uint4*>(&q_ops[head / 8][(head % 8) * 4 + c % 4][(c / 4) * 4]) = x;
   }
@@ -309,17 +309,17 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && HR <= 4 ? 3 : 2) decod
   const float* const vbase = reinterpret_cast<const float*>(p.vc) + unit_base + vt * D + vc * 4;
   auto page_of = [&](int pg) -> int {  // -1: none (its tokens are masked)
     int id = -1;
-    if (pg < pg1 && pg < p.max_blocks) id = __ldg(trow + pg);
+    if (pg < pg1 && pg < p.max_blocks) id = ld(trow + pg);
     return id >= 0 && id < p.pool ? id : -1;
   };
   float4 k[NK], v[NV];
   auto load_k = [&](int id) {
 #pragma unroll
-    for (int c = 0; c < NK; ++c) k[c] = __ldg(reinterpret_cast<const float4*>(kbase + id * page_stride) + 2 * c);
+    for (int c = 0; c < NK; ++c) k[c] = ld(reinterpret_cast<const float4*>(kbase + id * page_stride) + 2 * c);
   };
   auto load_v = [&](int id) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(vbase + id * page_stride + i * TG * D));
+    for (int i = 0; i < NV; ++i) v[i] = ld(reinterpret_cast<const float4*>(vbase + id * page_stride + i * TG * D));
   };
   int pg = u.l0 / kPage + warp, id = page_of(pg), id_nxt = page_of(pg + kWarps);
   if (id >= 0) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 && HR <= 4 ? 3 : 2) decod
       lo += __shfl_xor_sync(0xffffffffu, lo, 1);
       float x = lo * p.scale;
       if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
-      if (p.slopes != nullptr && h < p.G) x -= __ldg(p.slopes + u.g * p.G + h) * dist;
+      if (p.slopes != nullptr && h < p.G) x -= ld(p.slopes + u.g * p.G + h) * dist;
       s[h] = on ? x * kLog2e : -INFINITY;
       grow |= s[h] > m[h] + kMaxGrowth;
     }

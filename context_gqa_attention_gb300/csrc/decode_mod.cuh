@@ -63,7 +63,7 @@ struct Span {
 CP_DEV int first_visible(const ModParams& p, int b, int L) {
   int lo = 0;
   if (p.window > 0 && L > p.window) lo = L - p.window;
-  if (p.kv_start != nullptr) lo = max(lo, __ldg(p.kv_start + b));
+  if (p.kv_start != nullptr) lo = max(lo, ld(p.kv_start + b));
   return min(lo, max(L, 0));
 }
 // Tokens of rank r among positions [0, L), L >= 0.
@@ -329,7 +329,7 @@ CP_DEV void finish(const ModParams& p, WarpParts<D, HR>& w, int b, int g, int pa
     }
   }
   if (!p.fused || direct) return;
-  const int L = __ldg(p.seq_lens + b), lo = first_visible(p, b, L);
+  const int L = ld(p.seq_lens + b), lo = first_visible(p, b, L);
   merge_partials<T, D, HR>(p, w, b, g, p.cp * p.S, live, [&](int k) {
     return k % p.S < live_splits(p, rank_span(p, L, lo, k / p.S));
   });
@@ -371,7 +371,7 @@ CP_DEV bool take_unit(const ModParams& p, WarpParts<D, HR>& parts, Unit& u) {
     u.b = (int)(blockIdx.z / (unsigned)p.cp);
     u.part = u.r * p.S + u.split;
   }
-  u.L = __ldg(p.seq_lens + u.b);
+  u.L = ld(p.seq_lens + u.b);
   const int lo = first_visible(p, u.b, u.L);
   u.live = p.fused && p.cluster <= 1 ? live_total(p, u.L, lo) : 0;
   if (u.r < p.cp) {
@@ -422,7 +422,7 @@ struct Mods {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int head = 8 * nt + 2 * tid + c;
-        slope[nt][c] = p.slopes != nullptr && head < p.G ? __ldg(p.slopes + u.g * p.G + head) * kLog2e : 0.f;
+        slope[nt][c] = p.slopes != nullptr && head < p.G ? ld(p.slopes + u.g * p.G + head) * kLog2e : 0.f;
       }
   }
   CP_DEV void apply(float (&s)[NT][4], const ModParams& p, const Unit& u, int t) const {

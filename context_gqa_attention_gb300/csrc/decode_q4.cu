@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
   auto fetch_ids = [&](int j0) -> int {
     const int j = j0 + lane, pg = pg0 + (j / NP * kWarps + warp) * NP + j % NP;
     int id = -1;
-    if (pg < pg1 && pg < p.max_blocks) id = __ldg(trow + pg);
+    if (pg < pg1 && pg < p.max_blocks) id = ld(trow + pg);
     return id >= 0 && id < p.pool ? id : -1;
   };
   int ids = fetch_ids(0), ids_next = fetch_ids(32);
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
     const int from = PK == 2 ? head & 3 : head;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (from < p.G)
-      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+      x = ld(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
                                                ((long long)u.b * p.Hq + (long long)u.g * p.G + from) * D) + c);
     const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
                         bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};

@@ -339,13 +339,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the item: heads fastest, then row tiles (the last, longest one first), then sequences
   const int h0 = blockIdx.x * (TT ? 1 : 2), b = blockIdx.z;
-  const int q0 = __ldg(p.cu_q + b), Tq = __ldg(p.cu_q + b + 1) - q0;
+  const int q0 = ld(p.cu_q + b), Tq = ld(p.cu_q + b + 1) - q0;
   int kv0 = q0, Tkv = Tq;
   if (p.cu_kv != nullptr) {
-    kv0 = __ldg(p.cu_kv + b);
-    Tkv = __ldg(p.cu_kv + b + 1) - kv0;
+    kv0 = ld(p.cu_kv + b);
+    Tkv = ld(p.cu_kv + b + 1) - kv0;
   }
-  const int prefix = p.prefix != nullptr ? __ldg(p.prefix + b) : 0;
+  const int prefix = p.prefix != nullptr ? ld(p.prefix + b) : 0;
   const int q_lo = (p.tiles - 1 - (int)blockIdx.y) * SPAN;
   if (blockIdx.y == 0 && threadIdx.x == 0 && Tq - q_lo > SPAN) report(p.err, CP_ERR_DEVICE_BOUNDS);  // max_seqlen_q
   if (q_lo >= Tq) return;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto lo_of = [&](int row) -> int {
     int lo = 0;
     if (p.window > 0 && C + row >= p.window) lo = C + row - p.window + 1;
-    if (p.kv_start != nullptr) lo = max(lo, __ldg(p.kv_start + q0 + row));
+    if (p.kv_start != nullptr) lo = max(lo, ld(p.kv_start + q0 + row));
     return min(lo, Tkv);
   };
   auto hi_of = [&](int row) -> int { return max(C + row + 1, pre); };
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool cap = p.softcap > 0.f;
     const float cap_log2 = p.softcap * kLog2e;
     const bool biased = p.slopes != nullptr;
-    const float slope = biased ? __ldg(p.slopes + head) * kLog2e : 0.f;
+    const float slope = biased ? ld(p.slopes + head) * kLog2e : 0.f;
     // scores come out of cap and bias in log2 units; untouched ones are scaled within the exponent
     const float sc = CAP || cap || biased ? 1.f : p.scale_log2;
     float m = -INFINITY, l = 0.f;

@@ -27,3 +27,48 @@ def test_q4_records_that_land_over_the_query_operands(lib, d, Hq, Hkv):
         at += n
     for _ in range(200):
         assert all(torch.equal(x, y) for x, y in zip(lib.cp_decode_attention_q4(q, k, v, t, sl, 2, 8, **kw), first))
+
+
+@pytest.mark.parametrize("kind", ["f32", "f32_64", "bf16", "q4"])
+def test_steps_that_rewrite_what_the_step_before_read(lib, kind):
+    """Append, decode and merge of partials, step after step with nothing between them, over the same buffers: a
+    kernel is placed while the ones before it run, some of which read the lines (queries, half-filled pages,
+    partials) that the one just before it rewrites.  As with a synchronization after each call, bit for bit."""
+    dt = DT["f32"] if kind.startswith("f32") else DT["bf16"]
+    B, Hq, Hkv, d, cp, I, L, q4 = 4, 8, 2, 64 if kind == "f32_64" else 128, 2, 8, 60, kind == "q4"
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x = torch.randn(L, B, Hq + 2 * Hkv, d, generator=g, device=DEV).to(dt)
+    freq = torch.tensor(10000.0 ** (-np.arange(d // 2) / (d // 2)), device=DEV)
+    cu1 = _cu([1] * B)
+    at = [torch.full((B,), i, **I32) for i in range(L + 1)]
+    fused, part = ((lib.cp_decode_attention_q4, lib.cp_partial_attn_decode_q4) if q4 else
+                   (lib.cp_decode_attention_mod, lib.cp_partial_attn_decode_mod))
+    results = []
+    for wait in (True, False, False, False):
+        k, v, t = _pool([L] * B, Hkv, d, cp, I, dt, q4, 1)
+        k.zero_(), v.zero_()
+        ws = torch.zeros(lib.cp_decode_workspace_size(B, Hq, Hkv, d, cp, 2), dtype=torch.uint8, device=DEV)
+        q, out = (torch.zeros(B, Hq, d, dtype=dt, device=DEV) for _ in range(2))
+        lse, po = torch.zeros(B, Hq, device=DEV), torch.zeros(2 * cp, B, Hq, d, device=DEV)
+        pl = torch.zeros(2 * cp, B, Hq, device=DEV)
+        seen = [[torch.empty(B, Hq, d, dtype=dt, device=DEV) for _ in range(2)] for _ in range(L)]
+        torch.cuda.synchronize()
+
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+        for i in range(L):
+            qi, kn, vn = x[i].split([Hq, Hkv, Hkv], 1)
+            lib.cp_rope_kv_cache_write(kn, vn, cu1, at[i], k, v, t, cp, I, inv_freq=freq, q=qi, q_out=q)
+            done()
+            kw = dict(num_splits=2, split_tokens=16)
+            fused(q, k, v, t, at[i + 1], cp, I, workspace=ws, out=seen[i][0], out_lse=lse, **kw)
+            done()
+            part(q, k, v, t, at[i + 1], cp, I, out=po, lse=pl, **kw)
+            done()
+            lib.cp_lse_merge(po, pl, out=seen[i][1], out_dtype=dt)
+            done()
+        torch.cuda.synchronize()
+        results.append(seen)
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for x, y in zip(results[0], other) for a, b in zip(x, y))
