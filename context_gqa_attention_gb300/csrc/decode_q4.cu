@@ -404,15 +404,25 @@ __global__ void __launch_bounds__(kWarps * 32, (Q4Shape<D, NT>::kCtas)) decode_q
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const float before = m[nt][h];
           const float alpha = new_reference(MOD ? mx[nt][h] : mx[nt][h] * qscale[nt][h], m[nt][h], neg[nt][h]);
           limit[nt][h] = MOD ? m[nt][h] + kMaxGrowth : (m[nt][h] + kMaxGrowth) / qscale[nt][h];
           l[nt][h] *= alpha;
+          // What o holds shrinks, and its unit with it, so that later factors do not meet a unit set by tokens
+          // that no longer count: by whole powers of two of the reference itself, which o in units then leaves
+          // where it was to a factor of 2 however often the reference moves.  (alpha 0: nothing is left in o.)
+          const int down = alpha == 0.f ? 256 : m[nt][h] == before ? 0 : (int)(floorf(m[nt][h]) - floorf(before));
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) pm[nt][gr][h] *= alpha;
+          for (int gr = 0; gr < GR; ++gr) {
+            pm[nt][gr][h] *= alpha;
+            const int e = min(down, 126 - exponent(inv[nt][gr][h]));
+            const float keep = alpha * pow2(e);
+            inv[nt][gr][h] = pow2(exponent(inv[nt][gr][h]) + e);
 #pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            o[nt][i][h] *= alpha;
-            o[nt][i][2 + h] *= alpha;
+            for (int j = 0; j < 4; ++j) {
+              o[nt][gr * 4 + j][h] *= keep;
+              o[nt][gr * 4 + j][2 + h] *= keep;
+            }
           }
         }
     }

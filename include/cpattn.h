@@ -539,6 +539,9 @@ cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* m
  * and out, is CP_BF16, and components of q are below 2^100).  Arguments as in
  * cp_partial_attn_decode / cp_decode_attention plus `mod` (NULL: none; prefix_lens must be NULL: a
  * prefix is behind the query here).
+ * Weights and values are summed before they are divided: finite values in the cache are below 2^96.
+ * The 4-bit calls round weight times scale to f16 (11 bits), relative to the largest of those that still
+ * count, per group of 64 dims: of one below 2^-14 of that fewer bits are kept, below 2^-24 none.
  *
  * Splits are counted within the visible tokens: split s of a rank covers split_tokens local tokens
  * from s * split_tokens past the page of the first visible one, so a window needs splits for its
