@@ -162,9 +162,9 @@ struct CpDecodeWorkspace {
 };
 inline size_t cp_align256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline size_t cp_decode_ws_layout(int B, int Hq, int Hkv, int d, int P, size_t* off_lse,
-                                  size_t* off_out) {
+                                  size_t* off_out, size_t least_counters = kCpDecodeCounters) {
   const size_t n = (size_t)B * Hkv;
-  const size_t c = cp_align256((n > kCpDecodeCounters ? n : kCpDecodeCounters) * sizeof(int32_t));
+  const size_t c = cp_align256((n > least_counters ? n : least_counters) * sizeof(int32_t));
   const size_t l = cp_align256((size_t)P * B * Hq * sizeof(float));
   const size_t o = cp_align256((size_t)P * B * Hq * d * sizeof(float));
   *off_lse = c;

@@ -84,9 +84,10 @@ extern "C" cp_status cp_decode_attention_noalloc(const cp_decode_args* a, void* 
                                                  float* out_lse, void* stream) {
   const cp_status st = cp_check_decode_args_for_fused(a, out);
   if (st != CP_OK) return st;
+  // every call clears its own counters, so their region need not be the same for all shapes
   size_t ol = 0, oo = 0;
   const size_t need = cp_decode_ws_layout(a->num_seqs, a->num_q_heads, a->num_kv_heads,
-                                          a->head_dim, a->cp * a->num_splits, &ol, &oo);
+                                          a->head_dim, a->cp * a->num_splits, &ol, &oo, 0);
   if (need > CP_NOALLOC_SCRATCH_BYTES)
     return cp_fail_detail(CP_ERR_INVALID_ARG,
                           "cp_decode_attention_noalloc needs %zu bytes of scratch but its static "

@@ -374,7 +374,8 @@ cp_status cp_lse_merge(const float* partial_out, const float* partial_lse, int32
  * library (CP_NOALLOC_SCRATCH_BYTES = 48 MiB per GPU).  The array lives in a module of its own:
  * a process holds it on a GPU from its first call of this entry point there until it exits;
  * the other entry points never load it.  It allocates and frees nothing.
- *   - Sizes whose scratch (cp_decode_workspace_size) exceeds CP_NOALLOC_SCRATCH_BYTES are
+ *   - Sizes whose scratch (partials, their LSEs and num_seqs * num_kv_heads counters, 256-byte
+ *     aligned each; up to 256 KB less than cp_decode_workspace_size) exceeds CP_NOALLOC_SCRATCH_BYTES are
  *     rejected with CP_ERR_INVALID_ARG and a message naming both sizes.
  *   - The first call in a CUDA context looks up the array's device address (with that
  *     context's device current) and loads the array's module; make that first call before
