@@ -186,25 +186,31 @@ def load(build_if_missing: bool = False):
                          ("cp_score_mod", ScoreMod)):
         if getattr(lib, name + "_size")() != ctypes.sizeof(struct):
             raise CPError(1, f"{name} layout mismatch between binding and library")
-    _load_binding()
     _LIB = lib
     return lib
 
 
 def _load_binding():
-    global _BINDING
-    if not os.path.exists(_build.BINDING):
-        raise CPError(3, f"{_build.BINDING} is missing: build it first "
-                         "(python -c 'import __graft_entry__ as g; g.build()')")
+    built, here = _build.binding_built_for(), _build.binding_target()
+    if built != here:
+        raise CPError(3, (f"{_build.BINDING} is missing" if not built else f"{_build.BINDING} was built for {built}, "
+                          f"not {here}") + ": build it first (python -c 'import __graft_entry__ as g; g.build()')")
     spec = importlib.util.spec_from_file_location("cpattn_binding", _build.BINDING)
-    _BINDING = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_BINDING)
-    _BINDING.set_error(CPError)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        raise CPError(3, f"{_build.BINDING} does not load: {e}") from e
+    module.set_error(CPError)
+    return module
 
 
 def _binding():
+    """The native module of the serving calls, loaded by the first of them (the other calls do without)."""
+    global _BINDING
     if _BINDING is None:
         load()
+        _BINDING = _load_binding()
     return _BINDING
 
 

@@ -15,6 +15,7 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libcpattn.so")
 BINDING = os.path.join(OUT_DIR, "cpattn_binding.so")
+BUILT_FOR = os.path.join(OUT_DIR, "cpattn_binding.txt")  # the torch and Python that BINDING was built against
 SOURCES = ["api.cu", "prefill_simt.cu", "prefill_tc.cu", "decode.cu", "noalloc.cu",
            "cache.cu", "decode_mod.cu", "decode_q4.cu", "prefill_mod.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,8 +38,22 @@ def _inputs():
     return files
 
 
+def binding_target() -> str:
+    """What a binding that fits this process was built against."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_built_for() -> str:
+    """What the binding on disk was built against ('' if there is none)."""
+    if not (os.path.exists(BINDING) and os.path.exists(BUILT_FOR)):
+        return ""
+    with open(BUILT_FOR) as f:
+        return f.read()
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+    if not os.path.exists(LIB) or binding_built_for() != binding_target():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -87,6 +102,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    if os.path.exists(BUILT_FOR):  # (written again once the binding it describes is in place)
+        os.remove(BUILT_FOR)
     tmp = BINDING + ".tmp"
     cmd = [cxx, "-shared", "-o", tmp, binding_obj, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch",
            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", OUT_DIR, "-lcpattn", "-Wl,-rpath,$ORIGIN"]
@@ -94,6 +111,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BUILT_FOR, "w") as f:
+        f.write(binding_target())
     return LIB
 
 
