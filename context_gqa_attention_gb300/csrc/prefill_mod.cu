@@ -879,8 +879,8 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   p.err = a.err;
   const bool tt = p.G % 2 != 0;  // odd groups: two row tiles of one head share the K / V tiles
   const int span = tt ? 2 * BM : BM;
-  p.tiles = (a.max_seqlen_q + span - 1) / span;
-  if (p.tiles == 0) return cudaSuccess;
+  // at least one, which reports a sequence that is longer than a max_seqlen_q of 0
+  p.tiles = a.max_seqlen_q > 0 ? (a.max_seqlen_q + span - 1) / span : 1;
   if (p.tiles > 65535 || a.num_seqs > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid(tt ? a.num_q_heads : a.num_q_heads / 2, p.tiles, a.num_seqs);
   auto kern = tt ? (fixed ? prefill_mod_kernel<D, true, true> : prefill_mod_kernel<D, true, false>)

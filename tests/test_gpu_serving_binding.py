@@ -266,3 +266,19 @@ def test_inference_mode_and_leaves_that_want_gradients(lib, t):
     q = t["q"].clone().requires_grad_()
     got = decode(t, q=q)[0]
     assert torch.equal(got, want) and not got.requires_grad
+
+
+def test_prefill_told_that_no_sequence_has_rows(lib):
+    """max_seqlen_q = 0: a sequence longer than what one tile row holds is reported, rows of a padded batch whose
+    sequences are all empty are left as they are, and nothing is reported for those."""
+    for Hq, Hkv in ((4, 2), (3, 1)):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        q, k, v = (torch.randn(700, h, 64, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+        cu = torch.tensor([0, 100, 700], **i32)
+        want, want_lse = lib.cp_attn_prefill_mod(q, cu, k, v, max_seqlen_q=600)
+        err, out, lse = torch.zeros(1, **i32), torch.full_like(want, 9.0), torch.full_like(want_lse, 9.0)
+        lib.cp_attn_prefill_mod(q, cu, k, v, max_seqlen_q=0, out=out, out_lse=lse, err=err)
+        assert int(err) == 5 and torch.equal(out[:100], want[:100]) and torch.equal(lse[:100], want_lse[:100])
+        out.fill_(9.0), lse.fill_(9.0), err.zero_()
+        lib.cp_attn_prefill_mod(q, torch.zeros(3, **i32), k, v, out=out, out_lse=lse, err=err)
+        assert int(err) == 0 and bool((out == 9.0).all()) and bool((lse == 9.0).all())
