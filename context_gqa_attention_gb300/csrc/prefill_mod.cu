@@ -133,42 +133,43 @@ CP_DEV float row_abs_max(const Row& v) {
 // The lowest n of 64 bits (none for n <= 0, all for n >= 64).
 CP_DEV uint64_t first_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
-// cap tanh(y) in log2 units from y = cap_in * (q.k), N + 1 coefficients of tanh(y) / y in y^2.
-template <int N>
-CP_DEV void cap_poly(Row& v, float cap_in, float cap_log2, const float (&a)[N + 1]) {
-  const uint64_t in2 = f2(cap_in, cap_in);
-  uint64_t c[N + 1];
-#pragma unroll
-  for (int i = 0; i <= N; ++i) c[i] = f2(a[i] * cap_log2, a[i] * cap_log2);
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      const uint64_t y = fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2), u = fmul2(y, y);
-      uint64_t r = c[N];
-#pragma unroll
-      for (int j = N - 1; j >= 0; --j) r = ffma2(r, u, c[j]);
-      f2u(fmul2(r, y), v.c[i][k], v.c[i][k + 1]);
-    }
-}
-// Relative errors 5.5e-7 on |y| <= 0.5 and 6.3e-7 on |y| <= 1.25 (least-maximum fits to tanh).
+// cap tanh(y) in log2 units from y = cap_in * (q.k): a polynomial of tanh(y) / y in y^2 for |y| <= kCapFar
+// (relative error 6.3e-7, a least-maximum fit to tanh), beyond it 1 - 2 / (1 + e^2y) (absolute error about
+// 2^-22 of the cap).  Each score takes the form that its own size asks for: keys that a row does not see, and the
+// warp's other rows, can only make it wait for both.  y_max: the row's largest |cap_in s|.
 constexpr float kCapNear = 0.5f, kCapFar = 1.25f;
-// y: the row's largest |cap_in s|.
-CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y) {
-  if (__all_sync(0xffffffffu, y <= kCapNear)) {
-    const float a[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
-    cap_poly<3>(v, cap_in, cap_log2, a);
-  } else if (__all_sync(0xffffffffu, y <= kCapFar)) {
-    const float a[7] = {0.9999994039535522f, -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
-                        0.018229125067591667f, -0.004626906011253595f, 0.0005844940315000713f};
-    cap_poly<6>(v, cap_in, cap_log2, a);
-  } else {  // 1 - 2 / (1 + e^2y): absolute error about 2^-22
-    const float in = 2.f * kLog2e * cap_in;
+CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y_max) {
+  const float a[7] = {0.9999994039535522f, -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
+                      0.018229125067591667f, -0.004626906011253595f, 0.0005844940315000713f};
+  const uint64_t in2 = f2(cap_in, cap_in);
+  uint64_t c[7];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) c[i] = f2(a[i] * cap_log2, a[i] * cap_log2);
+  auto poly = [&](uint64_t y) {
+    const uint64_t u = fmul2(y, y);
+    uint64_t r = c[6];
+#pragma unroll
+    for (int j = 5; j >= 0; --j) r = ffma2(r, u, c[j]);
+    return fmul2(r, y);
+  };
+  if (__all_sync(0xffffffffu, y_max <= kCapFar)) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        v.c[i][k] = cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(v.c[i][k] * in));
+      for (int k = 0; k < 32; k += 2) f2u(poly(fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2)), v.c[i][k], v.c[i][k + 1]);
+  } else {
+    auto far = [&](float y) { return cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(y * (2.f * kLog2e))); };
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        const uint64_t y = fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2);
+        float y0, y1, x0, x1;
+        f2u(y, y0, y1);
+        f2u(poly(y), x0, x1);
+        v.c[i][k] = fabsf(y0) <= kCapFar ? x0 : far(y0);  // (NaN: far, and NaN)
+        v.c[i][k + 1] = fabsf(y1) <= kCapFar ? x1 : far(y1);
+      }
   }
 }
 
@@ -184,7 +185,8 @@ constexpr float kCapAbove = 80.f;
 constexpr float kMinCapIn = 1e-5f;    // the folded coefficients stay normal numbers
 
 struct CapCoefficients {
-  uint64_t c[4];  // x = s (c0 + u (c1 + u (c2 + u c3))), u = s^2, for |cap_in s| <= kCapNear
+  // x = s (c0 + u (c1 + u (c2 + u c3))), u = s^2, for |cap_in s| <= kCapNear (relative error 5.5e-7)
+  uint64_t c[4];
 };
 CP_DEV CapCoefficients cap_coefficients(float cap_in, float scale_log2) {
   const float a[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};

@@ -56,3 +56,46 @@ def test_v_scales_that_fall_while_the_scores_rise(lib, Hq, Hkv, d, cap, rise, fa
     for S, tokens in ((1, 576), (3, 192), (2, 320)):
         out, lse = lib.cp_decode_attention_q4(q, k, v, t, torch.tensor([n], **I32), cp, I, softcap=cap, num_splits=S, split_tokens=tokens)
         _check(out, lse, O, L, A, big, cap, None, n, extra=extra, what=f"{S} x {tokens}")
+
+
+# ------------------------------------------------------------------------------ capped prefill
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("cap", [4.0, 30.0, 100.0, 1e5, 1e9])
+@pytest.mark.parametrize("bad", ["inf", "nan", "large", "huge"])
+def test_keys_a_row_does_not_see_leave_its_capped_scores_alone(lib, Hq, Hkv, d, cap, bad):
+    """One bad key in the middle, and bad rows behind the last sequence: rows that do not see it come out bit for
+    bit as without it, with a cap and with a cap and a bias."""
+    new = [150, 400, 60]
+    r = torch.Generator(device=DEV).manual_seed(8)
+    q, k, v = (torch.randn(610, h, d, generator=r, device=DEV).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    start = torch.zeros(610, **I32)
+    start[150 + 300:550] = 300                       # a second document in the middle sequence
+    at = 150 + 230                                   # position 230 of the middle sequence
+    k2 = k.clone()
+    k2[at, 0, 5] = dict(inf=float("inf"), nan=float("nan"), large=1e4, huge=1e30)[bad]
+    sees = torch.zeros(610, dtype=torch.bool, device=DEV)
+    sees[at:150 + 300] = True                        # own document, from the key on, 120 keys wide
+    same = ~(sees[:, None] & (torch.arange(Hq, device=DEV) // (Hq // Hkv) == 0)[None])
+    slopes = 2.0 ** (-8 * (torch.arange(Hq, device=DEV, dtype=torch.float32) + 1) / Hq)
+    for alibi in (None, slopes):
+        kw = dict(window=120, kv_start=start, max_seqlen_q=400, softcap=cap, alibi_slopes=alibi)
+        clean = lib.cp_attn_prefill_mod(q, _cu(new), k, v, **kw)
+        out, lse = lib.cp_attn_prefill_mod(q, _cu(new), k2, v, **kw)
+        assert torch.equal(out[same], clean[0][same]) and torch.equal(lse[same], clean[1][same])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("cap", [0.5, 2.0, 20.0, 1e6, 1e9])
+def test_small_and_large_scores_under_one_cap(lib, Hq, Hkv, d, cap):
+    """Rows whose scores lie far below the cap next to rows (of the same warp) far above it: each to the accuracy
+    of its own scores, 2^-16 of the products' sum and 2^-20 of the capped score (tanh x <= x)."""
+    n = 300
+    g = torch.Generator(device=DEV).manual_seed(6)
+    q, k, v = (torch.randn(n, h, d, generator=g, device=DEV) for h in (Hq, Hkv, Hkv))
+    q[::2] *= 4 * cap
+    q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+    out, lse = lib.cp_attn_prefill_mod(q, _cu([n]), k, v, softcap=cap, max_seqlen_q=n)
+    for i in (0, 1, 2, 129, 200, 298, 299):
+        one = torch.tensor([i], device=DEV)
+        O, L, A, big = _attend(q[i:i + 1].double(), k.double(), v.double(), 0 * one, one + 1, one, cap, None)
+        _check(out[i:i + 1], lse[i:i + 1], O, L, A, min(big, 64 * cap) if i % 2 == 0 else big, min(cap, big), None, n, what=f"row {i}")
