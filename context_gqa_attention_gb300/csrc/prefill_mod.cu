@@ -46,7 +46,6 @@ constexpr float kMaxGrowth = 8.f;            // log2 units the scores may exceed
 struct PrefillModParams {
   int B, Hq, Hkv, G, Nq, window, tiles;  // tiles: row tiles (items) of the longest sequence
   float scale_log2, softcap, cap_in;  // cap_in = scale / cap: y = cap_in q.k
-  float cap_ref;  // CAP: the least reference of the scores, log2 units
   const int32_t* cu_q;
   const int32_t* cu_kv;  // null: the query rows
   const int32_t* kv_start;
@@ -173,15 +172,10 @@ CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y_max) {
   }
 }
 
-// Capped scores are bounded, |x| <= cap log2(e), so with a cap of at most kMaxCapLog2 they need no
-// running maximum: the row's maximum over the first tile in which it sees a key, but at least cap log2(e) -
-// kCapAbove, stays the reference, and no P is above 2^kCapAbove (which fp32 sums and bf16 operands hold) while the
-// largest is at least 2^-kMaxCapLog2.  P then follows from the score in one chain without a dependence
-// on the rest of the row, and the polynomial's packed FMAs run under the exponentials' special-function
-// time.  (A reference that is one of the row's own scores makes its P exactly 1: with a constant one,
-// rows of a few keys lose up to 2^-9 to P's rounding that they need not.)
-constexpr float kMaxCapLog2 = 80.f;   // cap <= 55.4
-constexpr float kCapAbove = 80.f;
+// Where no score of a row's tile can exceed the row's reference by more than the growth that every reference
+// is allowed (|x| <= |y| cap log2(e)) and all lie in the near form's range, which both halves of the row ask at
+// one barrier, P follows from the score in one chain, without the row's maximum, and the polynomial's packed FMAs
+// run under the exponentials' special-function time.
 constexpr float kMinCapIn = 1e-5f;    // the folded coefficients stay normal numbers
 
 struct CapCoefficients {
@@ -324,8 +318,8 @@ CP_DEV bool pair_any(int id, bool x) {
 }
 
 // ------------------------------------------------------------------------------ kernel
-// TT: the two tiles are two row tiles of one head.  CAP: scores with nothing but a cap that allows a
-// reference fixed at the first tile.
+// TT: the two tiles are two row tiles of one head.  CAP: scores with nothing but a cap, whose near tiles
+// take the short way.
 template <int D, bool TT, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_mod_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -630,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scores come out of cap and bias in log2 units; untouched ones are scaled within the exponent
     const float sc = CAP || cap || biased ? 1.f : p.scale_log2;
     float m = -INFINITY, l = 0.f;
+    float y_near = -INFINITY;  // CAP: the largest |cap_in s| of a near tile
     CapCoefficients coef;
     if constexpr (CAP) coef = cap_coefficients(p.cap_in, p.scale_log2);
     bool ok = true;
@@ -642,10 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int t = 0; t < ntiles; ++t) {
       const int kt0 = key_lo + key_tile(t) * BN;
-      // CAP: a row's reference is set, for good, at the first tile in which it sees a key (both halves of
-      // a row say the same)
-      const bool first = CAP && m == -INFINITY && max(lo, kt0) < min(hi, kt0 + BN);
-      const bool some_first = CAP && __any_sync(0xffffffffu, first);
       ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
       // a warp that gives up raises the abort flag; its partner gives up at its own wait, or where the
       // two meet within the tile
@@ -653,8 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) fail();
         __syncwarp();
         // the votes below, as the partner will meet them
-        if (!CAP || some_first) pair_any(pair, true);
-        if constexpr (!CAP) pair_any(pair, true);
+        for (int i = 0; i < (CAP ? 3 : 2); ++i) pair_any(pair, true);
         break;
       }
       tc_fence_after();
@@ -665,16 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kChunks; ++i) tmem_wait_ld(v.c[i]);
       const int k0 = kt0 + half * BH;        // this thread's first key
       const int c0 = lo - k0, c1 = hi - k0;  // visible columns [c0, c1)
-      const bool whole_tile = __all_sync(0xffffffffu, c0 <= 0 && c1 >= BH);
       // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S columns may
       // take P(t)
-      float y = 0.f;
-      bool near = false;
-      if constexpr (CAP) {
-        y = row_abs_max(v) * p.cap_in;
-        near = !some_first && whole_tile && __all_sync(0xffffffffu, y <= kCapNear);
-      }
-      if (CAP && near) {
+      const float y = CAP || cap ? row_abs_max(v) * p.cap_in : 0.f;
+      if (CAP && !pair_any(pair, !(c0 <= 0 && c1 >= BH && y <= y_near))) {  // (the abort flag: the votes below)
         const uint64_t n2 = f2(-m, -m);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
@@ -686,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (CAP || cap) cap_scores(v, p.cap_in, cap_log2, CAP ? y : row_abs_max(v) * p.cap_in);
+      if (CAP || cap) cap_scores(v, p.cap_in, cap_log2, y);
       const float s0 = cap ? 1.f : p.scale_log2;
       const int behind = k0 - (C + row);  // this thread's first key, counted from the query
       bool fold = false;                  // the bias goes into the exponent
@@ -713,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!whole_tile) {  // by bits, which become predicates seven at a time
+      if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= BH)) {  // by bits, which become predicates seven at a time
         const uint64_t seen = first_bits(c1) & ~first_bits(c0);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
@@ -722,39 +706,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; ++k) v.c[i][k] = (w & (1u << k)) != 0u ? v.c[i][k] : -INFINITY;
         }
       }
-      if (!CAP || some_first) {  // the row's largest score here, or what bounds it
-        float mt = -INFINITY;
+      float mt = -INFINITY;  // the row's largest score here, or what bounds it
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const float x = chunk_max(v.c[i]);
-          mt = fmaxf(mt, !CAP && fold ? fmaf(x, s0, slope * (float)(behind + 32 * i + 31)) : x * sc);
+      for (int i = 0; i < kChunks; ++i) {
+        const float x = chunk_max(v.c[i]);
+        mt = fmaxf(mt, !CAP && fold ? fmaf(x, s0, slope * (float)(behind + 32 * i + 31)) : x * sc);
+      }
+      // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8: the
+      // halves ask each other at one barrier, and exchange their maxima only then.  (The next write of s_mine
+      // comes after another vote, that is after both have read here.)  CAP: by more than 2^4, so that a row
+      // whose first tile shows it few keys does not keep a reference that few tiles are near to.
+      constexpr float kGrowth = CAP ? kMaxGrowth / 2.f : kMaxGrowth;
+      if (pair_any(pair, mt > m + kGrowth)) {
+        *s_mine = mt;
+        if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
+          ok = false;
+          break;
         }
-        if constexpr (CAP) {
-          *s_mine = mt;
-          if (pair_any(pair, false)) {  // the partner gave up
-            ok = false;
-            break;
-          }
-          if (first) m = fmaxf(fmaxf(mt, *s_other), p.cap_ref);
-          pair_sync(pair);  // both have read before either writes again
-        } else if (pair_any(pair, mt > m + kMaxGrowth)) {
-          // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8:
-          // the halves ask each other at one barrier, and exchange their maxima only then.  (The next write
-          // of s_mine comes after another vote, that is after both have read here.)
-          *s_mine = mt;
-          if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
-            ok = false;
-            break;
-          }
-          mt = fmaxf(mt, *s_other);
-          float alpha = 1.f;
-          if (mt > m + kMaxGrowth) {
-            alpha = m == -INFINITY ? 1.f : ex2(m - mt);  // (no key yet: O is 0, as it stays)
-            m = mt;
-          }
-          l *= alpha;
-          if (t > 0) rescale_o<D / 2>(tO, alpha);
+        mt = fmaxf(mt, *s_other);
+        float alpha = 1.f;
+        if (mt > m + kGrowth) {
+          alpha = m == -INFINITY ? 1.f : ex2(m - mt);  // (no key yet: O is 0, as it stays)
+          m = mt;
+          if constexpr (CAP) y_near = fminf(kCapNear, (m + kMaxGrowth) / cap_log2);
         }
+        l *= alpha;
+        if (t > 0) rescale_o<D / 2>(tO, alpha);
       }
       const float neg = m == -INFINITY ? 0.f : -m;
 #pragma unroll
@@ -867,9 +844,7 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   p.scale_log2 = scale * kLog2e;
   p.softcap = mod.softcap;
   p.cap_in = mod.softcap > 0.f ? scale / mod.softcap : 0.f;
-  const float cap_log2 = mod.softcap * kLog2e;
-  p.cap_ref = cap_log2 - kCapAbove;
-  const bool fixed = mod.softcap > 0.f && cap_log2 <= kMaxCapLog2 && p.cap_in >= kMinCapIn && mod.alibi_slopes == nullptr;
+  const bool folds = mod.softcap > 0.f && p.cap_in >= kMinCapIn && mod.alibi_slopes == nullptr;
   p.cu_q = a.cu_seqlens_q;
   p.cu_kv = a.cu_seqlens_kv;
   p.kv_start = mod.kv_start;
@@ -885,8 +860,8 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   p.tiles = a.max_seqlen_q > 0 ? (a.max_seqlen_q + span - 1) / span : 1;
   if (p.tiles > 65535 || a.num_seqs > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid(tt ? a.num_q_heads : a.num_q_heads / 2, p.tiles, a.num_seqs);
-  auto kern = tt ? (fixed ? prefill_mod_kernel<D, true, true> : prefill_mod_kernel<D, true, false>)
-                 : (fixed ? prefill_mod_kernel<D, false, true> : prefill_mod_kernel<D, false, false>);
+  auto kern = tt ? (folds ? prefill_mod_kernel<D, true, true> : prefill_mod_kernel<D, true, false>)
+                 : (folds ? prefill_mod_kernel<D, false, true> : prefill_mod_kernel<D, false, false>);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
   if (e != cudaSuccess) return e;
   return launch_chained(kern, grid, kThreads, Smem<D>::kAlloc, s, mq, mk, mv, p);

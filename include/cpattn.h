@@ -528,8 +528,8 @@ typedef struct cp_score_mod {
  * keys.  args->out / args->lse are not used; args->err takes device-side errors.
  *   out      device bf16 [Nq][Hq][d];  out_lse  device f32 [Nq][Hq] (natural log).
  * Rows from cu_seqlens_q[B] on are left as they are.  A sequence longer than max_seqlen_q is reported
- * in err (CP_ERR_DEVICE_BOUNDS) once rows of it are left out.  With a softcap up to 55 weights are kept
- * relative to the largest score of the row's first key tile: finite components of v are below 2^40 then.
+ * in err (CP_ERR_DEVICE_BOUNDS) once rows of it are left out.  Weights and values are summed before they
+ * are divided: finite components of v are below 2^96.
  * ---------------------------------------------------------------------------- */
 cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* mod, void* out,
                               float* out_lse, void* stream);

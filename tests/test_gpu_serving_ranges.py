@@ -99,3 +99,23 @@ def test_small_and_large_scores_under_one_cap(lib, Hq, Hkv, d, cap):
         one = torch.tensor([i], device=DEV)
         O, L, A, big = _attend(q[i:i + 1].double(), k.double(), v.double(), 0 * one, one + 1, one, cap, None)
         _check(out[i:i + 1], lse[i:i + 1], O, L, A, min(big, 64 * cap) if i % 2 == 0 else big, min(cap, big), None, n, what=f"row {i}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("cap,up", [(50.0, 40), (30.0, 40), (55.0, 40), (50.0, 90), (300.0, 90)])
+def test_capped_prefill_with_large_values_and_late_high_scores(lib, Hq, Hkv, d, cap, up):
+    """Scores at the cap's lower end in the first key tiles and at its upper end behind them, V up to 2^up.
+
+    Caps up to 55: scores past 7 caps, where tanh is 1 to 2^-20 whatever the products' sum is off by."""
+    n = 700
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q = torch.full((n, Hq, d), 8.0, dtype=torch.bfloat16, device=DEV)
+    k = torch.full((n, Hkv, d), -8.0, dtype=torch.bfloat16, device=DEV)
+    k[200:] = 8.0
+    k = k * (1 + 0.25 * torch.rand(n, Hkv, 1, generator=g, device=DEV)).to(torch.bfloat16)
+    v = ((0.5 + torch.rand(n, Hkv, d, generator=g, device=DEV) / 2) * 2.0 ** up).to(torch.bfloat16)
+    out, lse = lib.cp_attn_prefill_mod(q, _cu([n]), k, v, softcap=cap, max_seqlen_q=n)
+    at = torch.arange(n, device=DEV)
+    O, L, A, big = _attend(q.double(), k.double(), v.double(), 0 * at, at + 1, at, cap, None)
+    # 300: scores of 2 to 3 caps, whose tanh changes by at most 0.07 of what the products' sum is off by
+    _check(out, lse, O, L, A, 1.0 if cap < 100 else big, cap, None, n)
