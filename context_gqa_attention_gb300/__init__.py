@@ -13,9 +13,11 @@ never allocates); when omitted they are allocated here with ``torch.empty``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import importlib.util
+import inspect
 import math
 import os
 import threading
@@ -235,6 +237,23 @@ def _stream(stream=None):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _on(stream):
+    """What a call allocates, fills and reads back belongs to the stream that it runs on: on another one a
+    workspace could be cleared, or a block's last user finish, too late, and a length be read too early."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _largest(t, stream):
+    with _on(stream):
+        return int(t.max().item())
+
+
+def _longest(cu, stream):
+    """The longest of the sequences that cu delimits."""
+    with _on(stream):
+        return int(cu.diff().max().item()) if cu.numel() > 1 else 0
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -243,9 +262,11 @@ _CALL = threading.local()
 
 
 def _on_first_tensors_device(fn):
-    """Runs an entry point with its first tensor argument's device current (so the launch, the
-    stream and any tensor allocated here belong to that device) and makes every other tensor
+    """Runs an entry point with its first tensor argument's device, and the stream given, current (so
+    the launch, the stream and any tensor allocated here belong to them) and makes every other tensor
     argument check that it lives on the same device."""
+    at = list(inspect.signature(fn).parameters).index("stream") - 1  # among *args
+
     @functools.wraps(fn)
     def wrapper(first, *args, **kwargs):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
@@ -254,9 +275,10 @@ def _on_first_tensors_device(fn):
         prev = getattr(_CALL, "device", None)
         _CALL.device = device
         try:
-            if device.index == torch.cuda.current_device():
+            stream = args[at] if len(args) > at else kwargs.get("stream")
+            if stream is None and device.index == torch.cuda.current_device():
                 return fn(first, *args, **kwargs)
-            with torch.cuda.device(device):
+            with _on(stream), torch.cuda.device(device):
                 return fn(first, *args, **kwargs)
         finally:
             _CALL.device = prev
@@ -691,7 +713,7 @@ def cp_kv_cache_read(k_cache, v_cache, cu_out, start_pos, block_tables, cp, inte
     binding = _binding()
     if total is None:
         _on_gpu("cp_kv_cache_read", k_cache)
-        total = -1 if k_out is not None else int(cu_out[-1].item())
+        total = -1 if k_out is not None else _largest(cu_out[-1:], stream)
     if out_dtype not in _TYPE:
         raise CPError(2, f"unsupported dtype {out_dtype}")
     return binding.kv_read(k_cache, v_cache, cu_out, start_pos, block_tables, cp, interleave, total,
@@ -708,7 +730,7 @@ def cp_attn_prefill_mod(q, cu_seqlens_q, k, v, *, cu_seqlens_kv=None, softcap=0.
     binding = _binding()
     if max_seqlen_q is None:
         _on_gpu("cp_attn_prefill_mod", q)
-        max_seqlen_q = int(cu_seqlens_q.diff().max().item()) if cu_seqlens_q.numel() > 1 else 0
+        max_seqlen_q = _longest(cu_seqlens_q, stream)
     return binding.prefill(q, cu_seqlens_q, k, v, cu_seqlens_kv, softcap, window, alibi_slopes, kv_start, prefix_lens,
                            max_seqlen_q, softmax_scale, out, out_lse, err, _handle(stream))
 
@@ -722,13 +744,13 @@ def cp_decode_mod_plan(num_seqs, num_kv_heads, cp, interleave, max_seq_len, *, w
     return ns.value, st.value
 
 
-def _splits(q, seq_lens, max_seq_len, num_splits, split_tokens):
+def _splits(q, seq_lens, max_seq_len, num_splits, split_tokens, stream):
     """(longest sequence to plan for or 0, num_splits, split_tokens) of a decode call's arguments."""
     if num_splits is not None and split_tokens is not None:
         return 0, num_splits, split_tokens
     if max_seq_len is None:
         _on_gpu("decode", q)
-        max_seq_len = max(1, int(seq_lens.max().item()))
+        max_seq_len = max(1, _largest(seq_lens, stream))
     return max_seq_len, 0, 0
 
 
@@ -740,7 +762,7 @@ def cp_partial_attn_decode_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, 
     distance bias alibi_slopes f32 [Hq] and kv_start int32 [B] (first visible position).
     Returns (out [P, B, Hq, d], lse [P, B, Hq]), P = cp * num_splits."""
     binding = _binding()
-    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens, stream)
     return binding.decode_partial(False, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
                                   window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
                                   softmax_scale, err, _handle(stream), out, lse)
@@ -754,7 +776,7 @@ def cp_decode_attention_mod(q, k_cache, v_cache, block_tables, seq_lens, cp, int
     """cp_decode_attention with modified scores (see cp_partial_attn_decode_mod and cpattn.h).
     Returns (out [B, Hq, d] dtype of q, lse [B, Hq] f32 or None)."""
     binding = _binding()
-    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens, stream)
     return binding.decode_fused(False, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
                                 window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
                                 softmax_scale, err, _handle(stream), workspace, out, out_lse, want_lse)
@@ -767,7 +789,7 @@ def cp_partial_attn_decode_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, i
     """cp_partial_attn_decode over the 4-bit cache, uint8 [cp, pool, Hkv, 9 d] (see cpattn.h), bf16
     queries; scores may be modified as in cp_partial_attn_decode_mod."""
     binding = _binding()
-    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens, stream)
     return binding.decode_partial(True, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
                                   window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
                                   softmax_scale, err, _handle(stream), out, lse)
@@ -781,7 +803,7 @@ def cp_decode_attention_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, inte
     """cp_decode_attention over the 4-bit cache, uint8 [cp, pool, Hkv, 9 d] (see cpattn.h), bf16
     queries; scores may be modified as in cp_partial_attn_decode_mod."""
     binding = _binding()
-    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens)
+    longest, num_splits, split_tokens = _splits(q, seq_lens, max_seq_len, num_splits, split_tokens, stream)
     return binding.decode_fused(True, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
                                 window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
                                 softmax_scale, err, _handle(stream), workspace, out, out_lse, want_lse)

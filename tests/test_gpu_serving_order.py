@@ -72,3 +72,55 @@ def test_steps_that_rewrite_what_the_step_before_read(lib, kind):
         results.append(seen)
     for other in results[1:]:
         assert all(torch.equal(a, b) for x, y in zip(results[0], other) for a, b in zip(x, y))
+
+
+def test_a_call_given_a_stream_allocates_and_reads_lengths_on_it(lib):
+    """With stream= and the lengths still being written on that stream, a call that asks for the longest itself
+    plans for what they become; a workspace and outputs made for the call are not memory that work still
+    pending on the current stream uses."""
+    B, L, Hq, Hkv, d, cp, I = 64, 600, 32, 8, 128, 2, 8
+    s = torch.cuda.Stream()
+    k, v, t, _, _ = _fill(lib, [L] * B, Hkv, d, cp, I, DT["bf16"], False, 2)
+    q = torch.randn(B, Hq, d, device=DEV).to(torch.bfloat16)
+    qp, kp, vp = (torch.randn(900, h, d, device=DEV).to(torch.bfloat16) for h in (8, 2, 2))
+    lens, cu, zero = torch.full((B,), L, **I32), _cu([300, 600]), torch.zeros(B, **I32)
+    out0 = _cu([L] * B)
+    big = torch.randn(4096, 4096, device=DEV)
+
+    def merged(partials, stream):
+        return lib.cp_lse_merge(*partials, stream=stream)
+
+    def attend(call, **plan):
+        return lambda lens, cu, out0, kw: call(q, k, v, t, lens, cp, I, **plan, **kw)
+    calls = [
+        attend(lib.cp_decode_attention),
+        attend(lib.cp_decode_attention, num_splits=5, split_tokens=64),        # a workspace's counters
+        attend(lib.cp_decode_attention_mod),
+        lambda lens, cu, out0, kw: merged(lib.cp_partial_attn_decode(q, k, v, t, lens, cp, I, **kw), kw["stream"]),
+        lambda lens, cu, out0, kw: merged(lib.cp_partial_attn_decode_mod(q, k, v, t, lens, cp, I, **kw), kw["stream"]),
+        lambda lens, cu, out0, kw: lib.cp_kv_cache_read(k, v, out0, zero, t, cp, I, **kw),
+        lambda lens, cu, out0, kw: lib.cp_attn_prefill_mod(qp, cu, kp, vp, softcap=9.0, **kw),
+        lambda lens, cu, out0, kw: lib.cp_attn_prefill_fused(qp, cu, 2, kp, vp, stream=kw["stream"]),
+        lambda lens, cu, out0, kw: merged(lib.cp_partial_attn_prefill(qp, cu, 2, k=kp, v=vp, **kw), kw["stream"]),
+    ]
+    err = torch.zeros(1, **I32)
+    late = [torch.zeros_like(x) for x in (lens, cu, out0)]
+    for i, call in enumerate(calls):
+        want = [x.clone() for x in call(lens, cu, out0, dict(err=err, stream=None))]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for x in late:
+                x.zero_()
+            for _ in range(20):
+                big @ big
+            for x, y in zip(late, (lens, cu, out0)):
+                x.copy_(y)
+        # blocks of the outputs' and the workspace's sizes, free again, that the busy current stream will still fill
+        for _ in range(20):
+            big @ big
+        for n in {x.numel() * x.element_size() for x in want} | {lib.cp_decode_workspace_size(B, Hq, Hkv, d, cp, 5)}:
+            for _ in range(3):
+                torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255)
+        got = call(*late, dict(err=err, stream=s))
+        torch.cuda.synchronize()
+        assert int(err) == 0 and all(torch.equal(a, b) for a, b in zip(got, want)), i
