@@ -44,7 +44,7 @@ constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
 constexpr float kMaxGrowth = 8.f;            // log2 units the scores may exceed the running reference
 
 struct PrefillModParams {
-  int B, Hq, Hkv, G, Nq, window, tiles;  // tiles: row tiles (items) of the longest sequence
+  int Hq, Hkv, G, Nq, Nkv, window, tiles;  // Nq, Nkv: rows; tiles: row tiles (items) of the longest sequence
   float scale_log2, softcap, cap_in;  // cap_in = scale / cap: y = cap_in q.k
   const int32_t* cu_q;
   const int32_t* cu_kv;  // null: the query rows
@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (q_lo >= Tq) return;
   const int q_hi = min(q_lo + SPAN, Tq);
   const int C = Tkv - Tq;  // cached tokens before the new ones
-  if (C < 0) {             // fewer kv tokens than new queries: flagged, the item is skipped
+  // fewer kv tokens than new queries, or rows that the tensors do not have: flagged, the item is skipped
+  if (C < 0 || q0 < 0 || kv0 < 0 || (long long)q0 + Tq > p.Nq || (long long)kv0 + Tkv > p.Nkv) {
     if (threadIdx.x == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
     return;
   }
@@ -835,11 +836,11 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
       !cp_make_bf16_map_2d(&mk, a.k, hkv, nkv, hkv, BN) || !cp_make_bf16_map_2d(&mv, a.v, hkv, nkv, hkv, BN))
     return cudaErrorInvalidValue;
   PrefillModParams p;
-  p.B = a.num_seqs;
   p.Hq = a.num_q_heads;
   p.Hkv = a.num_kv_heads;
   p.G = a.num_q_heads / a.num_kv_heads;
   p.Nq = a.total_q;
+  p.Nkv = (int)nkv;
   p.window = mod.window;
   p.scale_log2 = scale * kLog2e;
   p.softcap = mod.softcap;

@@ -527,8 +527,9 @@ typedef struct cp_score_mod {
  * tiles some row of a query tile sees are loaded, so a window or short documents cost their own
  * keys.  args->out / args->lse are not used; args->err takes device-side errors.
  *   out      device bf16 [Nq][Hq][d];  out_lse  device f32 [Nq][Hq] (natural log).
- * Rows from cu_seqlens_q[B] on are left as they are.  A sequence longer than max_seqlen_q is reported
- * in err (CP_ERR_DEVICE_BOUNDS) once rows of it are left out.  Weights and values are summed before they
+ * Rows from cu_seqlens_q[B] on are left as they are.  Reported in err (CP_ERR_DEVICE_BOUNDS): a sequence
+ * longer than max_seqlen_q once rows of it are left out; one with fewer kv tokens than queries, or whose rows
+ * go past total_q or total_kv, which is skipped.  Weights and values are summed before they
  * are divided: finite components of v are below 2^96.
  * ---------------------------------------------------------------------------- */
 cp_status cp_attn_prefill_mod(const cp_prefill_args* args, const cp_score_mod* mod, void* out,

@@ -100,3 +100,26 @@ def test_prefill_stays_in_bounds(lib, new, ctx, Hq, Hkv, d):
         o.intact("out"), l.intact("lse")
         assert bool(torch.isfinite(o.view.float()).all())
         assert not bool(torch.isnan(l.view).any()) and math.isfinite(float(l.view.amax()))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (3, 1, 64)])
+def test_prefill_of_sequences_that_go_past_the_rows(lib, Hq, Hkv, d):
+    """cu_seqlens that claim more rows than the tensors have: that sequence is reported and skipped, the ones
+    before it are computed, and nothing behind the outputs' rows is written."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q, k, v = (torch.randn(500, h, d, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    cu = torch.tensor([0, 200, 400], **i32)
+    want, want_lse = lib.cp_attn_prefill_mod(q[:400], cu, k[:400], v[:400], softcap=9.0)
+    for cu_q, cu_kv, rows, err_want in (([0, 200, 400], None, 200, 5), ([0, 200, 400], [0, 200, 500], 200, 5),
+                                        ([0, 200, 2 ** 31 - 1], None, 200, 5), ([-5, 200, 400], None, 0, 5)):
+        buf, lbuf, err = torch.full((500, Hq, d), 9.0, device="cuda", dtype=torch.bfloat16), torch.full((500, Hq), 9.0, device="cuda"), torch.zeros(1, **i32)
+        n = 400 if cu_kv else 300                   # rows given; the buffers behind them go on
+        lib.cp_attn_prefill_mod(q[:n], torch.tensor(cu_q, **i32), k[:n], v[:n], softcap=9.0, max_seqlen_q=200, out=buf[:n], out_lse=lbuf[:n],
+                                cu_seqlens_kv=torch.tensor(cu_kv, **i32) if cu_kv else None, err=err)
+        assert int(err) == err_want
+        if rows:
+            assert torch.equal(buf[:rows], want[:rows]) and torch.equal(lbuf[:rows], want_lse[:rows])
+        if cu_q[0] == 0:
+            assert bool((buf[rows:] == 9.0).all()) and bool((lbuf[rows:] == 9.0).all())
+        else:                                       # its second sequence ends at 400 of 300 rows: nothing is left
+            assert bool((buf == 9.0).all())
