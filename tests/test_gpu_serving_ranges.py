@@ -119,3 +119,25 @@ def test_capped_prefill_with_large_values_and_late_high_scores(lib, Hq, Hkv, d, 
     O, L, A, big = _attend(q.double(), k.double(), v.double(), 0 * at, at + 1, at, cap, None)
     # 300: scores of 2 to 3 caps, whose tanh changes by at most 0.07 of what the products' sum is off by
     _check(out, lse, O, L, A, 1.0 if cap < 100 else big, cap, None, n)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "q4"])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_decode_of_the_largest_values(lib, kind, cap):
+    """V just below 2^96, the bound that the header gives, under scores that rise along the sequence."""
+    n, Hq, Hkv, d, cp, I = 1500, 8, 2, 128, 2, 8
+    dt, q4 = torch.float32 if kind == "f32" else torch.bfloat16, kind == "q4"
+    k, v, t = _pool([n], Hkv, d, cp, I, dt, q4, 3)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    kn = (torch.linspace(-2, 2, n, device=DEV)[:, None, None] + 0.1 * torch.randn(n, Hkv, d, generator=g, device=DEV)).to(dt)
+    vn = ((2 * torch.rand(n, Hkv, d, generator=g, device=DEV) - 1) * 2.0 ** 95.9).to(dt)
+    zero = torch.zeros(1, **I32)
+    lib.cp_rope_kv_cache_write(kn, vn, _cu([n]), zero, k, v, t, cp, I)
+    K, V = (x.double() for x in lib.cp_kv_cache_read(k, v, _cu([n]), zero, t, cp, I, out_dtype=torch.float32 if q4 else dt))
+    q = torch.full((1, Hq, d), 1.5, dtype=dt, device=DEV)
+    one = torch.tensor([n - 1], device=DEV)
+    O, L, A, big = _attend(q.double(), K, V, 0 * one, one + 1, one, cap, None)
+    fused = lib.cp_decode_attention_q4 if q4 else lib.cp_decode_attention_mod
+    for S, tokens in ((1, 752), (6, 128)):
+        out, lse = fused(q, k, v, t, torch.tensor([n], **I32), cp, I, softcap=cap, num_splits=S, split_tokens=tokens)
+        _check(out, lse, O, L, A, big, cap, None, n, f32=kind == "f32", extra=float(V.abs().max()) if q4 else 0.0, what=f"{S} x {tokens}")
