@@ -176,7 +176,11 @@ CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y_max) {
 // is allowed (|x| <= |y| cap log2(e)) and all lie in the near form's range, which both halves of the row ask at
 // one barrier, P follows from the score in one chain, without the row's maximum, and the polynomial's packed FMAs
 // run under the exponentials' special-function time.
-constexpr float kMinCapIn = 1e-5f;    // the folded coefficients stay normal numbers
+// The folded coefficients, up to scale (scale / cap)^6, and s^2, up to (cap / 2 scale)^2, stay normal numbers.
+inline bool cap_folds(float scale, float softcap) {
+  const double y = (double)scale / softcap, c = scale * y * y * y * y * y * y;
+  return y >= 1e-5 && c >= 1e-30 && c <= 1e30;
+}
 
 struct CapCoefficients {
   // x = s (c0 + u (c1 + u (c2 + u c3))), u = s^2, for |cap_in s| <= kCapNear (relative error 5.5e-7)
@@ -845,7 +849,7 @@ cudaError_t launch(const cp_prefill_args& a, const cp_score_mod& mod, float scal
   p.scale_log2 = scale * kLog2e;
   p.softcap = mod.softcap;
   p.cap_in = mod.softcap > 0.f ? scale / mod.softcap : 0.f;
-  const bool folds = mod.softcap > 0.f && p.cap_in >= kMinCapIn && mod.alibi_slopes == nullptr;
+  const bool folds = mod.softcap > 0.f && cap_folds(scale, mod.softcap) && mod.alibi_slopes == nullptr;
   p.cu_q = a.cu_seqlens_q;
   p.cu_kv = a.cu_seqlens_kv;
   p.kv_start = mod.kv_start;

@@ -141,3 +141,19 @@ def test_decode_of_the_largest_values(lib, kind, cap):
     for S, tokens in ((1, 752), (6, 128)):
         out, lse = fused(q, k, v, t, torch.tensor([n], **I32), cp, I, softcap=cap, num_splits=S, split_tokens=tokens)
         _check(out, lse, O, L, A, big, cap, None, n, f32=kind == "f32", extra=float(V.abs().max()) if q4 else 0.0, what=f"{S} x {tokens}")
+
+
+@pytest.mark.parametrize("cap,scale", [(1e-6, 1e3), (1e-3, 1e4), (1e-6, 1e-11), (1e-6, 1e-9), (1e9, 1e4), (1e9, 1e14), (3.0, 1e6)])
+def test_capped_prefill_at_the_ends_of_cap_and_scale(lib, cap, scale):
+    """Caps and softmax scales at the ends of what the calls take, with rows of zeros (scores of 0 under any of
+    them), small and ordinary rows."""
+    n, Hq, Hkv, d = 640, 4, 2, 64
+    g = torch.Generator(device=DEV).manual_seed(7)
+    q, k, v = (torch.randn(n, h, d, generator=g, device=DEV).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    for size in (0.0, min(1.0, 0.02 * cap / scale)):       # all near the middle of the cap, or 0
+        qs = (q.float() * size).to(torch.bfloat16)
+        out, lse = lib.cp_attn_prefill_mod(qs, _cu([n]), k, v, softcap=cap, softmax_scale=scale, max_seqlen_q=n)
+        for i in (0, 1, 270, 500, 639):
+            one = torch.tensor([i], device=DEV)
+            O, L, A, big = _attend(qs[i:i + 1].double() * (scale * math.sqrt(d)), k.double(), v.double(), 0 * one, one + 1, one, cap, None)
+            _check(out[i:i + 1], lse[i:i + 1], O, L, A, big, min(cap, big), None, n, what=f"{size}, row {i}")
