@@ -240,7 +240,9 @@ def _stream(stream=None):
 def _on(stream):
     """What a call allocates, fills and reads back belongs to the stream that it runs on: on another one a
     workspace could be cleared, or a block's last user finish, too late, and a length be read too early."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
 
 
 def _largest(t, stream):
