@@ -157,3 +157,24 @@ def test_capped_prefill_at_the_ends_of_cap_and_scale(lib, cap, scale):
             one = torch.tensor([i], device=DEV)
             O, L, A, big = _attend(qs[i:i + 1].double() * (scale * math.sqrt(d)), k.double(), v.double(), 0 * one, one + 1, one, cap, None)
             _check(out[i:i + 1], lse[i:i + 1], O, L, A, big, min(cap, big), None, n, what=f"{size}, row {i}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "q4"])
+@pytest.mark.parametrize("cap,scale", [(1e-6, 1e3), (1e-3, 1e4), (1e-6, 1e-11), (1e9, 1e4), (1e9, 1e14), (3.0, 1e6), (0.0, 1e6), (0.0, 1e-20)])
+def test_decode_at_the_ends_of_cap_and_scale(lib, kind, cap, scale):
+    """As the prefill above, over the caches."""
+    n, Hq, Hkv, d, cp, I = 700, 8, 2, 64, 2, 8
+    dt, q4 = torch.float32 if kind == "f32" else torch.bfloat16, kind == "q4"
+    k, v, t = _pool([n], Hkv, d, cp, I, dt, q4, 3)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    q, kn, vn = (torch.randn(m, h, d, generator=g, device=DEV).to(dt) for m, h in ((1, Hq), (n, Hkv), (n, Hkv)))
+    zero = torch.zeros(1, **I32)
+    lib.cp_rope_kv_cache_write(kn, vn, _cu([n]), zero, k, v, t, cp, I)
+    K, V = (x.double() for x in lib.cp_kv_cache_read(k, v, _cu([n]), zero, t, cp, I, out_dtype=torch.float32 if q4 else dt))
+    one = torch.tensor([n - 1], device=DEV)
+    call = lib.cp_decode_attention_q4 if q4 else lib.cp_decode_attention_mod
+    for size in (0.0, min(1.0, (0.02 * cap if cap else 0.5) / scale)):
+        qs = (q.float() * size).to(dt)
+        O, L, A, big = _attend(qs.double() * (scale * math.sqrt(d)), K, V, 0 * one, one + 1, one, cap, None)
+        out, lse = call(qs, k, v, t, torch.tensor([n], **I32), cp, I, softcap=cap, softmax_scale=scale)
+        _check(out, lse, O, L, A, big, min(cap, big), None, n, f32=kind == "f32", extra=float(V.abs().max()) if q4 else 0.0, what=f"{size}")
