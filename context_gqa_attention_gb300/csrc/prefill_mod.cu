@@ -689,15 +689,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (slope >= 0.f && 31.f * slope <= kMaxFold) {
           fold = true;
         } else {
-          const uint64_t s02 = f2(s0, s0), step = f2(2.f * slope, 2.f * slope);
+          // (the distance is stepped, exactly, not the bias: a steep one's roundings far away would otherwise stay
+          // in it next to the query)
+          const uint64_t s02 = f2(s0, s0), slope2 = f2(slope, slope), two = f2(2.f, 2.f);
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
-            const float b0 = slope * (float)(behind + 32 * i);
-            uint64_t bias = f2(b0, b0 + slope);
+            uint64_t at = f2((float)(behind + 32 * i), (float)(behind + 32 * i + 1));
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              f2u(ffma2(f2(v.c[i][k], v.c[i][k + 1]), s02, bias), v.c[i][k], v.c[i][k + 1]);
-              bias = fadd2(bias, step);
+              f2u(ffma2(slope2, at, fmul2(f2(v.c[i][k], v.c[i][k + 1]), s02)), v.c[i][k], v.c[i][k + 1]);
+              at = fadd2(at, two);
             }
           }
         }

@@ -178,3 +178,59 @@ def test_decode_at_the_ends_of_cap_and_scale(lib, kind, cap, scale):
         O, L, A, big = _attend(qs.double() * (scale * math.sqrt(d)), K, V, 0 * one, one + 1, one, cap, None)
         out, lse = call(qs, k, v, t, torch.tensor([n], **I32), cp, I, softcap=cap, softmax_scale=scale)
         _check(out, lse, O, L, A, big, min(cap, big), None, n, f32=kind == "f32", extra=float(V.abs().max()) if q4 else 0.0, what=f"{size}")
+
+
+# ------------------------------------------------------------------------------ slopes and limits
+@pytest.mark.parametrize("Hq,Hkv,d", [(6, 3, 128), (3, 1, 64)])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("prefix", [0, 400])
+def test_prefill_slopes_of_every_kind(lib, Hq, Hkv, d, cap, prefix):
+    """Slopes of 0, gentle, steep, negative (weights that grow with the distance) and past what the exponent takes."""
+    n, ctx = 500, 200
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q = torch.randn(n, Hq, d, generator=g, device=DEV).to(torch.bfloat16)
+    k, v = (torch.randn(n + ctx, Hkv, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    at = torch.arange(ctx, ctx + n, device=DEV)
+    hi = (at + 1).clamp(min=prefix)
+    for some in ([0.0, 0.3, 0.9], [1.0, 40.0, -0.01], [-0.2, 300.0, 1e-6]):
+        slopes = torch.tensor((some * 2)[:Hq], device=DEV)
+        out, lse = lib.cp_attn_prefill_mod(q, _cu([n]), k, v, cu_seqlens_kv=_cu([n + ctx]), softcap=cap, alibi_slopes=slopes, max_seqlen_q=n,
+                                           prefix_lens=torch.tensor([prefix], **I32) if prefix else None)
+        O, L, A, big = _attend(q.double(), k.double(), v.double(), 0 * at, hi, at, cap, slopes)
+        # the bias' own roundings: 2^-22 of the largest one among the keys that count (with a slope below 0, all of
+        # them; above 0, those within the scores' spread of the nearest key, which `big` covers)
+        far = float((-slopes).clamp(min=0).max()) * (n + ctx)
+        beyond = float((slopes * (prefix - ctx)).clamp(min=0).max()) if prefix else 0.0
+        _check(out, lse, O, L, A, big + (far + beyond) * 2.0 ** -6, cap, None, n, what=str(some))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "q4"])
+def test_limits_at_the_ends_of_their_types(lib, kind):
+    """Windows, document starts and prefixes of -2^31 and 2^31 - 1: no limit, or no key."""
+    n, Hq, Hkv, d, cp, I, top, low = 300, 4, 2, 64, 2, 8, 2 ** 31 - 1, -2 ** 31
+    dt, q4 = torch.float32 if kind == "f32" else torch.bfloat16, kind == "q4"
+    k, v, t = _pool([n], Hkv, d, cp, I, dt, q4, 3)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    q, kn, vn = (torch.randn(m, h, d, generator=g, device=DEV).to(dt) for m, h in ((n, Hq), (n, Hkv), (n, Hkv)))
+    lib.cp_rope_kv_cache_write(kn, vn, _cu([n]), torch.zeros(1, **I32), k, v, t, cp, I)
+    call = lib.cp_decode_attention_q4 if q4 else lib.cp_decode_attention_mod
+    sl = torch.tensor([n], **I32)
+    full = call(q[:1], k, v, t, sl, cp, I)
+    for kw in (dict(window=top), dict(kv_start=torch.tensor([low], **I32)), dict(window=top, kv_start=torch.tensor([-1], **I32))):
+        got = call(q[:1], k, v, t, sl, cp, I, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, full))
+    for lens, kw in ((sl, dict(kv_start=torch.tensor([top], **I32))), (torch.tensor([low], **I32), dict(max_seq_len=n)),
+                     (torch.tensor([low], **I32), dict(max_seq_len=n, window=5, kv_start=torch.tensor([top], **I32)))):
+        out, lse = call(q[:1], k, v, t, lens, cp, I, **kw)
+        assert not out.any() and bool(torch.isneginf(lse).all())
+    if kind != "bf16":
+        return
+    cu, full = _cu([n]), lib.cp_attn_prefill_mod(q, _cu([n]), kn, vn)
+    whole = lib.cp_attn_prefill_mod(q, cu, kn, vn, prefix_lens=torch.tensor([n], **I32))
+    at = lambda x: torch.full((n,), x, **I32)
+    for want, kw in ((full, dict(window=top)), (full, dict(kv_start=at(low))), (full, dict(prefix_lens=torch.tensor([low], **I32))),
+                     (whole, dict(prefix_lens=torch.tensor([top], **I32))), (whole, dict(prefix_lens=torch.tensor([top], **I32), kv_start=at(-7), window=top))):
+        got = lib.cp_attn_prefill_mod(q, cu, kn, vn, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), kw
+    out, lse = lib.cp_attn_prefill_mod(q, cu, kn, vn, kv_start=at(top), softcap=5.0)
+    assert not out.any() and bool(torch.isneginf(lse).all())
