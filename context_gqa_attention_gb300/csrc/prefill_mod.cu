@@ -132,50 +132,62 @@ CP_DEV float row_abs_max(const Row& v) {
 // The lowest n of 64 bits (none for n <= 0, all for n >= 64).
 CP_DEV uint64_t first_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; }
 
-// cap tanh(y) in log2 units from y = cap_in * (q.k): a polynomial of tanh(y) / y in y^2 for |y| <= kCapFar
-// (relative error 6.3e-7, a least-maximum fit to tanh), beyond it 1 - 2 / (1 + e^2y) (absolute error about
-// 2^-22 of the cap).  Each score takes the form that its own size asks for: keys that a row does not see, and the
-// warp's other rows, can only make it wait for both.  y_max: the row's largest |cap_in s|.
+// cap tanh(y) in log2 units from y = cap_in * (q.k): polynomials of tanh(y) / y in y^2 for |y| <= kCapNear and
+// kCapFar (relative errors 5.5e-7 and 6.3e-7, least-maximum fits to tanh), beyond 1 - 2 / (1 + e^2y) (absolute
+// error about 2^-22 of the cap).  y_max: the row's largest |cap_in s|.
+//
+// In a tile that all 32 rows see (`whole`) the warp's largest score chooses the form for all of them, but for large
+// caps, whose 2^-22 a small score would feel.  In one that some see in part, each score takes the form that its own
+// size asks for: keys that a row does not see can then only make it wait for both.
 constexpr float kCapNear = 0.5f, kCapFar = 1.25f;
-CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y_max) {
-  const float a[7] = {0.9999994039535522f, -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
-                      0.018229125067591667f, -0.004626906011253595f, 0.0005844940315000713f};
+constexpr float kCapSmall = 128.f;  // log2 units: 2^-22 of it is below the rounding of the products' sums
+template <int N, typename Put>
+CP_DEV void cap_poly(const Row& v, float cap_in, float cap_log2, const float (&a)[N + 1], Put put) {
   const uint64_t in2 = f2(cap_in, cap_in);
-  uint64_t c[7];
+  uint64_t c[N + 1];
 #pragma unroll
-  for (int i = 0; i < 7; ++i) c[i] = f2(a[i] * cap_log2, a[i] * cap_log2);
-  auto poly = [&](uint64_t y) {
-    const uint64_t u = fmul2(y, y);
-    uint64_t r = c[6];
+  for (int i = 0; i <= N; ++i) c[i] = f2(a[i] * cap_log2, a[i] * cap_log2);
 #pragma unroll
-    for (int j = 5; j >= 0; --j) r = ffma2(r, u, c[j]);
-    return fmul2(r, y);
-  };
-  if (__all_sync(0xffffffffu, y_max <= kCapFar)) {
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const uint64_t y = fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2), u = fmul2(y, y);
+      uint64_t r = c[N];
+#pragma unroll
+      for (int j = N - 1; j >= 0; --j) r = ffma2(r, u, c[j]);
+      put(i, k, y, fmul2(r, y));
+    }
+}
+CP_DEV void cap_scores(Row& v, float cap_in, float cap_log2, float y_max, bool whole) {
+  const float near[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
+  const float mid[7] = {0.9999994039535522f, -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
+                        0.018229125067591667f, -0.004626906011253595f, 0.0005844940315000713f};
+  auto far = [&](float y) { return cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(y * (2.f * kLog2e))); };
+  auto put = [&](int i, int k, uint64_t, uint64_t x) { f2u(x, v.c[i][k], v.c[i][k + 1]); };
+  if (whole && __all_sync(0xffffffffu, y_max <= kCapNear)) {
+    cap_poly<3>(v, cap_in, cap_log2, near, put);
+  } else if (__all_sync(0xffffffffu, y_max <= kCapFar)) {
+    cap_poly<6>(v, cap_in, cap_log2, mid, put);
+  } else if (whole && cap_log2 <= kCapSmall) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) f2u(poly(fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2)), v.c[i][k], v.c[i][k + 1]);
+      for (int k = 0; k < 32; ++k) v.c[i][k] = far(v.c[i][k] * cap_in);
   } else {
-    auto far = [&](float y) { return cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(y * (2.f * kLog2e))); };
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        const uint64_t y = fmul2(f2(v.c[i][k], v.c[i][k + 1]), in2);
-        float y0, y1, x0, x1;
-        f2u(y, y0, y1);
-        f2u(poly(y), x0, x1);
-        v.c[i][k] = fabsf(y0) <= kCapFar ? x0 : far(y0);  // (NaN: far, and NaN)
-        v.c[i][k + 1] = fabsf(y1) <= kCapFar ? x1 : far(y1);
-      }
+    cap_poly<6>(v, cap_in, cap_log2, mid, [&](int i, int k, uint64_t y, uint64_t x) {
+      float y0, y1, x0, x1;
+      f2u(y, y0, y1);
+      f2u(x, x0, x1);
+      v.c[i][k] = fabsf(y0) <= kCapFar ? x0 : far(y0);  // (NaN: far, and NaN)
+      v.c[i][k + 1] = fabsf(y1) <= kCapFar ? x1 : far(y1);
+    });
   }
 }
 
-// Where no score of a row's tile can exceed the row's reference by more than the growth that every reference
-// is allowed (|x| <= |y| cap log2(e)) and all lie in the near form's range, which both halves of the row ask at
-// one barrier, P follows from the score in one chain, without the row's maximum, and the polynomial's packed FMAs
-// run under the exponentials' special-function time.
+// A capped score is bounded, |x| <= min(|y|, 1) cap log2(e).  Where that says that none of a row's tile can exceed
+// the row's reference by more than the growth that every reference is allowed, which both halves of the row ask at
+// one barrier, the row's maximum need not be known; and if all lie in the near form's range, P follows from the
+// score in one chain, the polynomial's packed FMAs under the exponentials' special-function time.
 // The folded coefficients, up to scale (scale / cap)^6, and s^2, up to (cap / 2 scale)^2, stay normal numbers.
 inline bool cap_folds(float scale, float softcap) {
   const double y = (double)scale / softcap, c = scale * y * y * y * y * y * y;
@@ -322,8 +334,8 @@ CP_DEV bool pair_any(int id, bool x) {
 }
 
 // ------------------------------------------------------------------------------ kernel
-// TT: the two tiles are two row tiles of one head.  CAP: scores with nothing but a cap, whose near tiles
-// take the short way.
+// TT: the two tiles are two row tiles of one head.  CAP: scores with nothing but a cap, most of whose
+// tiles take a short way.
 template <int D, bool TT, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_mod_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -629,7 +641,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scores come out of cap and bias in log2 units; untouched ones are scaled within the exponent
     const float sc = CAP || cap || biased ? 1.f : p.scale_log2;
     float m = -INFINITY, l = 0.f;
-    float y_near = -INFINITY;  // CAP: the largest |cap_in s| of a near tile
     CapCoefficients coef;
     if constexpr (CAP) coef = cap_coefficients(p.cap_in, p.scale_log2);
     bool ok = true;
@@ -662,8 +673,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c0 = lo - k0, c1 = hi - k0;  // visible columns [c0, c1)
       // S(t) complete implies PV(t-1) complete (issued before QK(t)): O is stable and the S columns may
       // take P(t)
-      const float y = CAP || cap ? row_abs_max(v) * p.cap_in : 0.f;
-      if (CAP && !pair_any(pair, !(c0 <= 0 && c1 >= BH && y <= y_near))) {  // (the abort flag: the votes below)
+      float y = 0.f;
+      bool bounded = false, near = false;
+      if constexpr (CAP) {
+        y = row_abs_max(v) * p.cap_in;
+        // (a partner that gave up says no, and then takes part in the votes below)
+        bounded = !pair_any(pair, !(c0 <= 0 && c1 >= BH && fminf(y, 1.f) * cap_log2 <= m + kMaxGrowth));
+        near = bounded && __all_sync(0xffffffffu, y <= kCapNear);
+      }
+      if (CAP && near) {
         const uint64_t n2 = f2(-m, -m);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
@@ -675,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (CAP || cap) cap_scores(v, p.cap_in, cap_log2, y);
+      const bool whole = bounded || __all_sync(0xffffffffu, c0 <= 0 && c1 >= BH);
+      if (CAP || cap) cap_scores(v, p.cap_in, cap_log2, CAP ? y : row_abs_max(v) * p.cap_in, whole);
       const float s0 = cap ? 1.f : p.scale_log2;
       const int behind = k0 - (C + row);  // this thread's first key, counted from the query
       bool fold = false;                  // the bias goes into the exponent
@@ -703,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= BH)) {  // by bits, which become predicates seven at a time
+      if (!whole) {  // by bits, which become predicates seven at a time
         const uint64_t seen = first_bits(c1) & ~first_bits(c0);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
@@ -712,32 +731,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; ++k) v.c[i][k] = (w & (1u << k)) != 0u ? v.c[i][k] : -INFINITY;
         }
       }
-      float mt = -INFINITY;  // the row's largest score here, or what bounds it
+      if (!CAP || !bounded) {
+        float mt = -INFINITY;  // the row's largest score here, or what bounds it
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const float x = chunk_max(v.c[i]);
-        mt = fmaxf(mt, !CAP && fold ? fmaf(x, s0, slope * (float)(behind + 32 * i + 31)) : x * sc);
-      }
-      // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8: the
-      // halves ask each other at one barrier, and exchange their maxima only then.  (The next write of s_mine
-      // comes after another vote, that is after both have read here.)  CAP: by more than 2^4, so that a row
-      // whose first tile shows it few keys does not keep a reference that few tiles are near to.
-      constexpr float kGrowth = CAP ? kMaxGrowth / 2.f : kMaxGrowth;
-      if (pair_any(pair, mt > m + kGrowth)) {
-        *s_mine = mt;
-        if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
-          ok = false;
-          break;
+        for (int i = 0; i < kChunks; ++i) {
+          const float x = chunk_max(v.c[i]);
+          mt = fmaxf(mt, !CAP && fold ? fmaf(x, s0, slope * (float)(behind + 32 * i + 31)) : x * sc);
         }
-        mt = fmaxf(mt, *s_other);
-        float alpha = 1.f;
-        if (mt > m + kGrowth) {
-          alpha = m == -INFINITY ? 1.f : ex2(m - mt);  // (no key yet: O is 0, as it stays)
-          m = mt;
-          if constexpr (CAP) y_near = fminf(kCapNear, (m + kMaxGrowth) / cap_log2);
+        // The reference, the same in both halves, moves only when a score exceeds it by more than 2^8: the
+        // halves ask each other at one barrier, and exchange their maxima only then.  (The next write of s_mine
+        // comes after another vote, that is after both have read here.)  CAP: by more than 2^4, so that a row
+        // whose first tile shows it few keys does not keep a reference that bounds few tiles.
+        constexpr float kGrowth = CAP ? kMaxGrowth / 2.f : kMaxGrowth;
+        if (pair_any(pair, mt > m + kGrowth)) {
+          *s_mine = mt;
+          if (pair_any(pair, *abort_flag != 0u)) {  // both leave, or neither
+            ok = false;
+            break;
+          }
+          mt = fmaxf(mt, *s_other);
+          float alpha = 1.f;
+          if (mt > m + kGrowth) {
+            alpha = m == -INFINITY ? 1.f : ex2(m - mt);  // (no key yet: O is 0, as it stays)
+            m = mt;
+          }
+          l *= alpha;
+          if (t > 0) rescale_o<D / 2>(tO, alpha);
         }
-        l *= alpha;
-        if (t > 0) rescale_o<D / 2>(tO, alpha);
       }
       const float neg = m == -INFINITY ? 0.f : -m;
 #pragma unroll
