@@ -727,7 +727,8 @@ def cp_attn_prefill_mod(q, cu_seqlens_q, k, v, *, cu_seqlens_kv=None, softcap=0.
                         softmax_scale=0.0, out=None, out_lse=None, err=None, stream=None):
     """Prefill attention with modified scores over contiguous k, v [Nkv, Hkv, d] (see cpattn.h): a
     tanh cap, a distance bias alibi_slopes f32 [Hq], a sliding window, kv_start int32 [Nq] (first
-    visible position of each row: its document) and prefix_lens int32 [B] (keys every query sees).
+    visible position of each row: its document) and prefix_lens int32 [B] (keys that every query whose
+    window and document reach them sees).
     bf16.  Returns (out [Nq, Hq, d] bf16, lse [Nq, Hq] f32)."""
     binding = _binding()
     if max_seqlen_q is None:

@@ -868,7 +868,8 @@ cp_status cp_decode_mod_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t cp,
   // sequence of 4242 tokens, 2 kv heads, 4 bits: 10.6 us with 8 parts, 13.4 with 67).
   const long long most = q4 ? 4096 : 2048, least = (q4 ? 8 : 4) * page;
   long long S = (share + most - 1) / most;
-  // (288 CTAs in clusters of eight run at once whichever kernel it is; whole clusters of 8, 4 or 2 parts:
+  // (288 CTAs fit the GPU at once whichever kernel it is, in clusters of eight where three fit an SM; kernels of
+  // two to an SM are launched in clusters up to 270, see launch_decode.  Whole clusters of 8, 4 or 2 parts:
   // 8 sequences of 500..3911 tokens, 8 kv heads, 4 bits take 13.7 us in 256 CTAs and 23.0 in 512 places of
   // which a quarter is empty)
   const long long slots = 288 / ((long long)num_seqs * num_kv_heads);

@@ -296,8 +296,9 @@ CP_DEV void rotate(float (&a)[8], float (&b)[8], const Turns& w, int half) {
 }
 
 // Cosine and sine of an angle in turns.  fp32 rows take the full-accuracy function; rows that are
-// bf16 take the special-function unit's (off by 2^-21.4 at most on half a turn either way, 2^12 below
-// the rows' own rounding), a fifth of the instructions.
+// bf16 take the special-function unit's (off by 2^-21.4 at most on half a turn either way: 2^12 below the
+// rounding of a row stored as bf16, and where such a row is quantised, enough to give a value that lies
+// within 2^-21 of its pair's length of the middle between two codes the other one), a fifth of the instructions.
 template <typename T>
 CP_DEV void cos_sin(float turn, float& c, float& s) {
   if constexpr (sizeof(T) == 4) {

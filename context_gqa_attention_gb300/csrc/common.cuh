@@ -35,8 +35,8 @@ CP_DEV void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_de
 // Kernels of calls that follow one another closely (append, decode, ..) start like this, before their
 // first global access, and are launched by launch_chained: the next one's CTAs are placed while this
 // one runs, as soon as all of this one's are, and wait until it has completed.  (Calls back to back on
-// a stream: one sequence's 4-bit decode 10.2 -> 7.8 us, 64 appended tokens 6.1 -> 4.4, a prefill of 8192
-// tokens 236 -> 230.)
+// a stream: one sequence's 4-bit decode 10.2 -> 7.8 us, 64 appended tokens 6.1 -> 4.6, a prefill of 8192
+// tokens 6 us less of 240.)
 // What such a kernel reads may have been written while it was already there, so it reads with ordinary loads:
 // those of the non-coherent path (__ldg, ld.global.nc) are for data that nobody writes during the kernel's life.
 CP_DEV void chained_start() {

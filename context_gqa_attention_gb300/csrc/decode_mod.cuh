@@ -527,7 +527,7 @@ inline bool changes_scores(const cp_score_mod& mod) { return mod.softcap > 0.f |
 // Launch of a decode kernel of which per_sm CTAs fit on an SM: fused calls whose CTAs all run at once in
 // clusters of up to eight of a (sequence, kv head)'s parts; larger ones without, since a cluster's CTAs
 // start and stay together and the empty splits of short sequences would hold their places.  (Clusters of
-// eight fill 8 of 9 places: 408 CTAs at three per SM, 288 at two.)
+// eight fill 8 of 9 places: of 152 SMs, up to 405 CTAs at three per SM and 270 at two.)
 inline cudaError_t launch_decode(void (*kern)(const ModParams), ModParams p, size_t smem, int per_sm, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));

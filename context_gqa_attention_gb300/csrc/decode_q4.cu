@@ -20,9 +20,9 @@
 //    copy engine, an iteration or two ahead; loads into registers left the warps waiting for DRAM two
 //    thirds of the time (64 sequences of 1024..32768 tokens, 32/8 heads: 349 us), 16-byte cp.async
 //    stopped at 83% of the copy bandwidth and took a tenth of the instructions (277 us);
-//  * several independent pages per iteration keep a warp issuing (Q4Shape): 263 us, and 258 with the next
-//    call's CTAs placed early, 76% of the copy bandwidth.  What is left is instructions: without its
-//    arithmetic the same kernel runs at 95%.
+//  * several independent pages per iteration keep a warp issuing (Q4Shape): 263 us, and with up to four heads to
+//    a kv head two of them share a tile of scores: 243 us, 81% of the copy bandwidth (76% with five to eight
+//    heads).  What is left is instructions: without its arithmetic the same kernel runs at 95%.
 #include <cuda_fp16.h>
 
 #include "decode_mod.cuh"

@@ -23,8 +23,9 @@
 // the tensor pipe's 2.05k), so everything on it is kept short: four softmax warpgroups rather than
 // two, PV started by halves of P, and the cap a polynomial on the packed fp32 pipe wherever a warp's
 // scores allow it (tanh(y) / y in y^2, own least-maximum fits), only else 1 - 2 / (1 + e^2y), two
-// special-function operations per score.  8192 tokens, 16/2 heads, d = 128: 234 us with cap 50 (61% of the
-// measured bf16 peak), 210 without, 222 with a distance bias; 16384 tokens in a window of 4096 with a cap 412.
+// special-function operations per score.  8192 tokens, 16/2 heads, d = 128, in the calls' device time: 236 us with
+// cap 50 (61% of the measured bf16 peak), 314 with cap 5 and 401 with cap 1 (scores past the polynomials' range),
+// 205 without, 220 with a distance bias, 305 with both; 16384 tokens in a window of 4096 with cap 30: 421.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ntiles = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
   // With a distance bias the key tiles are walked from the last to the first: the bias is largest next to the
   // query, so the running reference is met at once and stays (walking up, it moved at every tile of a steep
-  // head: 8192 tokens, 16/2 heads took 263 us, now 222).
+  // head: 8192 tokens, 16/2 heads took 263 us, now 220).
   const bool down = !CAP && p.slopes != nullptr;
   auto key_tile = [&](int t) -> int { return down ? ntiles - 1 - t : t; };
   auto in_part = [&](int kt) -> bool {  // some row of the CTA sees only a part of key tile kt
@@ -493,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = h0 / p.G;
 
   if (warp < 4) {
-    regs_dec<64>();  // 128 x 64 + 512 x 104 = the 640 x 96 registers of the launch: the rows' scores without spills
+    regs_dec<64>();  // 128 x 64 + 512 x 104 = the 640 x 96 registers of the launch: the rows' scores in registers,
+                     // with 32 (d = 64: 52) bytes of spills beside them in the capped forms, 8 in the others of d = 64
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer
       if (lane == 0) {

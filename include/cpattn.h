@@ -425,7 +425,7 @@ int64_t cp_q4_record_bytes(int32_t head_dim);
  *   - rows from cu_new[B] on (a padded batch) are neither read nor written, and a row with a
  *     negative position is skipped and reported.
  *   - bf16 rows take their cosines and sines from the special-function unit (off by 2^-21 at most, far
- *     below their own rounding), fp32 rows from the full-accuracy functions.
+ *     below their own rounding, and below a 4-bit code's step), fp32 rows from the full-accuracy functions.
  *   - err: CP_ERR_DEVICE_BOUNDS for a row whose table entry is missing or outside the pool (its K/V
  *     are not written).  Rows that map to the same slot race.
  * ---------------------------------------------------------------------------- */
@@ -507,7 +507,8 @@ cp_status cp_kv_cache_read(const cp_kv_read_args* args, void* stream);
  *   lo = max(0, i - window + 1 if window > 0, kv_start of the row if given),
  *   hi = i + 1, or the sequence's prefix length (at most its kv length) where that is larger.
  * So `window` keys up to and with the query's own are seen; kv_start gives each row the first
- * position of its document in a packed sequence; keys of the prefix are seen by every query.
+ * position of its document in a packed sequence; keys of the prefix are seen by every query whose window
+ * and document reach them (lo holds for them too).
  * A row without a key (lo >= hi) gives output 0 and LSE -inf.  Keys a row does not see do not
  * touch it, whatever they hold.
  * ---------------------------------------------------------------------------- */
