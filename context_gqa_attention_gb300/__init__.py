@@ -3,8 +3,8 @@ context-parallel shards, LSE merge and the CP layout maps, on one GB300 (sm_103a
 
 Argument marshalling only: every function below checks tensor placement, dtype and shape,
 then calls the C entry point of the same name on the current torch CUDA stream (the serving
-calls -- rotate-and-append, read-back, 4-bit decode, modified scores -- do both in the native
-module built from csrc/binding.cpp).  All the
+calls -- rotate-and-append, read-back, 4-bit decode, modified scores, cross attention, beam search -- do
+both in the native module built from csrc/binding.cpp).  All the
 arithmetic runs in the library's CUDA kernels; there is no fallback.  A missing or unbuilt
 library raises ``CPError``.
 
@@ -37,7 +37,8 @@ __all__ = [
     "CP_ROPE_HALF", "CP_ROPE_PAIRS", "cp_rope_kv_cache_write", "cp_kv_cache_read",
     "cp_q4_record_bytes", "cp_attn_prefill_mod", "cp_decode_mod_plan",
     "cp_partial_attn_decode_mod", "cp_decode_attention_mod", "cp_partial_attn_decode_q4",
-    "cp_decode_attention_q4",
+    "cp_decode_attention_q4", "cp_cross_attention", "cp_cross_attention_workspace_size",
+    "cp_beam_select", "cp_beam_select_workspace_size", "cp_beam_reorder",
 ]
 
 CP_F32, CP_BF16 = 0, 1
@@ -110,6 +111,32 @@ class KvReadArgs(ctypes.Structure):
                                    "v_out", "err")]
 
 
+class CrossArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "max_seqlen_q", "max_seqlen_kv",
+                 "total_q", "total_kv")] + \
+               [("softmax_scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")] + \
+               [(n, _vp) for n in ("q", "k", "v", "cu_seqlens_q", "cu_seqlens_kv", "kv_lens", "key_ranges", "err")]
+
+
+class BeamSelectArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "num_seqs", "num_beams", "vocab", "num_candidates", "eos_token")] + \
+               [("logits_stride", ctypes.c_int64)] + \
+               [(n, _vp) for n in ("logits", "scores", "next_scores", "next_beams", "next_tokens", "cand_scores",
+                                   "cand_beams", "cand_tokens")]
+
+
+class BeamReorderArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("dtype", "cache_q4", "num_layers", "num_seqs", "num_beams", "num_kv_heads", "head_dim", "cp",
+                 "interleave", "block_size", "max_blocks", "reserved")] + \
+               [("pool_pages", ctypes.c_int64)] + \
+               [(n, _vp) for n in ("parents", "seq_lens", "tables_in", "own_pages", "tables_out", "k_cache",
+                                   "v_cache", "err")]
+
+
 _LIB = _BINDING = None
 
 # (name, restype, argtypes)
@@ -151,6 +178,14 @@ _SIGS = [
     ("cp_attn_prefill_mod", ctypes.c_int32, [ctypes.POINTER(PrefillArgs), ctypes.POINTER(ScoreMod), _vp,
                                              _vp, _vp]),
     ("cp_decode_mod_plan", ctypes.c_int32, [ctypes.c_int32] * 7 + [ctypes.POINTER(ctypes.c_int32)] * 2),
+    ("cp_cross_args_size", ctypes.c_size_t, []),
+    ("cp_beam_select_args_size", ctypes.c_size_t, []),
+    ("cp_beam_reorder_args_size", ctypes.c_size_t, []),
+    ("cp_cross_attention_workspace_size", ctypes.c_int32, [ctypes.POINTER(CrossArgs), ctypes.POINTER(ctypes.c_size_t)]),
+    ("cp_cross_attention", ctypes.c_int32, [ctypes.POINTER(CrossArgs), _vp, ctypes.c_size_t, _vp, _vp, _vp]),
+    ("cp_beam_select_workspace_size", ctypes.c_int32, [ctypes.c_int32] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    ("cp_beam_select", ctypes.c_int32, [ctypes.POINTER(BeamSelectArgs), _vp, ctypes.c_size_t, _vp]),
+    ("cp_beam_reorder", ctypes.c_int32, [ctypes.POINTER(BeamReorderArgs), _vp]),
 ] + [(f"cp_partial_attn_decode_{n}", ctypes.c_int32,
       [ctypes.POINTER(DecodeArgs), ctypes.POINTER(ScoreMod), _vp]) for n in ("mod", "q4")] + \
     [(f"cp_decode_attention_{n}", ctypes.c_int32,
@@ -185,7 +220,8 @@ def load(build_if_missing: bool = False):
     if lib.cp_decode_args_size() != ctypes.sizeof(DecodeArgs):
         raise CPError(1, "cp_decode_args layout mismatch between binding and library")
     for name, struct in (("cp_rope_write_args", RopeWriteArgs), ("cp_kv_read_args", KvReadArgs),
-                         ("cp_score_mod", ScoreMod)):
+                         ("cp_score_mod", ScoreMod), ("cp_cross_args", CrossArgs),
+                         ("cp_beam_select_args", BeamSelectArgs), ("cp_beam_reorder_args", BeamReorderArgs)):
         if getattr(lib, name + "_size")() != ctypes.sizeof(struct):
             raise CPError(1, f"{name} layout mismatch between binding and library")
     _LIB = lib
@@ -810,6 +846,82 @@ def cp_decode_attention_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, inte
     return binding.decode_fused(True, q, k_cache, v_cache, block_tables, seq_lens, cp, interleave, softcap,
                                 window, alibi_slopes, kv_start, longest, num_splits, split_tokens,
                                 softmax_scale, err, _handle(stream), workspace, out, out_lse, want_lse)
+
+
+# ---------------------------------------------------------- cross attention, beam search
+
+def cp_cross_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_kv, *,
+                                      dtype=torch.bfloat16):
+    """Bytes of workspace with which cp_cross_attention cuts the keys of these sizes into parts on the current
+    device (0: it does not)."""
+    load()
+    a = CrossArgs()
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise CPError(2, f"unsupported dtype {dtype}")
+    a.dtype, a.num_seqs, a.head_dim = _TYPE[dtype], num_seqs, head_dim
+    a.num_q_heads, a.num_kv_heads = num_q_heads, num_kv_heads
+    a.max_seqlen_q, a.max_seqlen_kv = max_seqlen_q, max_seqlen_kv
+    need = ctypes.c_size_t()
+    _check(_LIB.cp_cross_attention_workspace_size(ctypes.byref(a), ctypes.byref(need)))
+    return need.value
+
+
+def cp_cross_attention(q, cu_seqlens_q, k, v, cu_seqlens_kv, *, kv_lens=None, key_ranges=None, max_seqlen_q=None,
+                       max_seqlen_kv=None, softmax_scale=0.0, workspace=None, out=None, out_lse=None,
+                       want_lse=True, err=None, stream=None):
+    """Attention of q [Nq, Hq, d] over an encoder's states k, v [Nkv, Hkv, d], sequence by sequence (cu_seqlens_q,
+    cu_seqlens_kv int32 [B + 1]), without causality (see cpattn.h).  A decode step's query rows are its beams.
+
+    kv_lens int32 [B]: a sequence's keys are its first kv_lens[b] rows (a padded batch).  key_ranges int32
+    [Nq, 2]: each row sees the keys [lo, hi) of its sequence.  q, k and v may be column slices of a wider tensor
+    (any token stride).  bf16 or f32.  `workspace`: uint8 CUDA tensor of cp_cross_attention_workspace_size()
+    bytes; None allocates it, an empty one cuts nothing.  max_seqlen_q is fetched from the device if it is not
+    given; max_seqlen_kv only guides the cut (the average is taken).
+    Returns (out [Nq, Hq, d] dtype of q, lse [Nq, Hq] f32 or None)."""
+    binding = _binding()
+    if max_seqlen_q is None:
+        _on_gpu("cp_cross_attention", q)
+        max_seqlen_q = _longest(cu_seqlens_q, stream)
+    if max_seqlen_kv is None:
+        _on_gpu("cp_cross_attention", q)
+        max_seqlen_kv = -(-k.shape[0] // max(1, cu_seqlens_kv.numel() - 1))
+    return binding.cross(q, cu_seqlens_q, k, v, cu_seqlens_kv, kv_lens, key_ranges, max_seqlen_q, max_seqlen_kv,
+                         softmax_scale, workspace, out, out_lse, want_lse, err, _handle(stream))
+
+
+def cp_beam_select_workspace_size(num_seqs, num_beams, vocab, num_candidates):
+    """Bytes of scratch cp_beam_select needs (zero-filled before its first use)."""
+    load()
+    n = ctypes.c_size_t()
+    _check(_LIB.cp_beam_select_workspace_size(num_seqs, num_beams, vocab, num_candidates, ctypes.byref(n)))
+    return n.value
+
+
+def cp_beam_select(logits, scores, *, num_candidates=None, eos_token=-1, workspace=None, next_scores=None,
+                   next_beams=None, next_tokens=None, cand_scores=None, cand_beams=None, cand_tokens=None, stream=None):
+    """The best continuations of each sequence's beams: logits [B, K, vocab] (bf16 or f32, any row stride), scores
+    f32 [B, K] (see cpattn.h).  num_candidates: 2 K (or what there is) if not given.  `workspace`: zero-filled uint8
+    CUDA tensor of cp_beam_select_workspace_size() bytes, left reusable; None allocates it.
+    Returns (next_scores f32, next_beams, next_tokens int32 [B, K], cand_scores f32, cand_beams, cand_tokens
+    int32 [B, num_candidates]): the candidates in falling order, and the first K that are not eos_token."""
+    binding = _binding()
+    if num_candidates is None:
+        _on_gpu("cp_beam_select", logits)
+        K, V = logits.shape[-2:] if logits.dim() == 3 else (1, 1)
+        num_candidates = min(2 * K, K * V)
+    return binding.beam_select(logits, scores, num_candidates, eos_token, workspace, next_scores, next_beams,
+                               next_tokens, cand_scores, cand_beams, cand_tokens, _handle(stream))
+
+
+def cp_beam_reorder(parents, seq_lens, block_tables, own_pages, k_cache, v_cache, cp, interleave, *, tables_out=None,
+                    err=None, stream=None):
+    """Beam j of sequence b goes on from beam parents[b][j] (int32 [B, K]): its row of block_tables int32 [cp, B K,
+    max_blocks] becomes the parent's, and the page being filled is copied to the beam's own (own_pages, shaped as
+    block_tables; see cpattn.h).  seq_lens int32 [B]: tokens in the cache.  The pools are [cp, pool, Hkv, 16, d], uint8
+    [cp, pool, Hkv, 9 d] (4-bit records) or several layers of either [layers, ..]; None and None: tables only.
+    tables_out may be block_tables (in place).  Returns it, or a new tensor, whose further columns are undefined."""
+    return _binding().beam_reorder(parents, seq_lens, block_tables, own_pages, k_cache, v_cache, cp, interleave,
+                                   tables_out, err, _handle(stream))
 
 
 def default_scale(head_dim):

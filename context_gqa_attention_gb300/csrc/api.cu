@@ -6,7 +6,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "common.cuh"
+#include "cross.cuh"
 
 namespace {
 
@@ -946,6 +946,132 @@ cp_status cp_decode_attention_mod(const cp_decode_args* a, const cp_score_mod* m
 cp_status cp_decode_attention_q4(const cp_decode_args* a, const cp_score_mod* mod, void* workspace,
                                  size_t workspace_bytes, void* out, float* out_lse, void* stream) {
   return decode_mod_fused(a, mod, true, workspace, workspace_bytes, out, out_lse, stream);
+}
+
+size_t cp_cross_args_size(void) { return sizeof(cp_cross_args); }
+size_t cp_beam_select_args_size(void) { return sizeof(cp_beam_select_args); }
+size_t cp_beam_reorder_args_size(void) { return sizeof(cp_beam_reorder_args); }
+
+// The shape of a cross attention, and which kernel takes it: the tensor cores' tiles of 128 rows from 65 rows a kv
+// head on, the kernels for few rows (in f32 for any) below.
+static cp_status check_cross_shape(const cp_cross_args* a) {
+  REQUIRE(a != nullptr, "args is null");
+  REQUIRE(a->dtype == CP_F32 || a->dtype == CP_BF16, "dtype must be CP_F32 or CP_BF16");
+  REQUIRE(a->num_seqs >= 1 && a->num_seqs <= (1 << 24), "num_seqs must be >= 1 (got %d)", a->num_seqs);
+  REQUIRE(a->num_kv_heads >= 1 && a->num_kv_heads <= 65536 && a->num_q_heads >= 1 && a->num_q_heads % a->num_kv_heads == 0,
+          "num_q_heads must be a multiple of num_kv_heads");
+  const int G = a->num_q_heads / a->num_kv_heads, most = a->dtype == CP_BF16 ? 128 : 16;
+  if (G > most)
+    return fail(CP_ERR_UNSUPPORTED, "q heads per kv head must be 1 .. %d for this dtype (got %d)", most, G);
+  if (a->head_dim != 64 && a->head_dim != 128)
+    return fail(CP_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", a->head_dim);
+  REQUIRE(a->max_seqlen_q >= 0 && a->max_seqlen_kv >= 0, "max_seqlen_q and max_seqlen_kv must be >= 0");
+  return CP_OK;
+}
+static bool cross_few(const cp_cross_args* a) {
+  return a->dtype == CP_F32 || (int64_t)a->max_seqlen_q * (a->num_q_heads / a->num_kv_heads) <= 64;
+}
+
+cp_status cp_cross_attention_workspace_size(const cp_cross_args* a, size_t* bytes) {
+  const cp_status st = check_cross_shape(a);
+  if (st != CP_OK) return st;
+  REQUIRE(bytes != nullptr, "bytes is null");
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return launched(e, "device query");
+  *bytes = (cross_few(a) ? cp_cross_plan_few(*a, sms) : cp_cross_plan_tc(*a, sms)).bytes;
+  return ok();
+}
+
+cp_status cp_cross_attention(const cp_cross_args* a, void* workspace, size_t workspace_bytes, void* out, float* out_lse,
+                             void* stream) {
+  const cp_status st = check_cross_shape(a);
+  if (st != CP_OK) return st;
+  REQUIRE(a->total_q >= 0 && a->total_kv >= 0, "total_q and total_kv must be >= 0");
+  REQUIRE(a->cu_seqlens_q && a->cu_seqlens_kv, "cu_seqlens_q and cu_seqlens_kv are required");
+  const int per16 = a->dtype == CP_BF16 ? 8 : 4;  // elements in 16 bytes
+  auto stride_ok = [&](int64_t stride, int32_t heads) {
+    return stride % per16 == 0 && stride >= (int64_t)heads * a->head_dim;
+  };
+  REQUIRE(stride_ok(a->q_stride, a->num_q_heads) && stride_ok(a->k_stride, a->num_kv_heads) &&
+              stride_ok(a->v_stride, a->num_kv_heads),
+          "q_stride, k_stride and v_stride must hold a row and be multiples of 16 bytes");
+  REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, "workspace must be 256-byte aligned");
+  if (a->total_q == 0) return ok();
+  REQUIRE_PTR(a->q);
+  REQUIRE_PTR(out);
+  if (a->total_kv > 0) {
+    REQUIRE_PTR(a->k);
+    REQUIRE_PTR(a->v);
+  }
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / sqrtf((float)a->head_dim);
+  const auto go = cross_few(a) ? cp_launch_cross_few : cp_launch_cross_tc;
+  return launched(go(*a, scale, workspace, workspace_bytes, out, out_lse, as_stream(stream)), "cp_cross_attention launch");
+}
+
+static cp_status check_beam_sizes(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_candidates) {
+  REQUIRE(num_seqs >= 1 && num_seqs <= 65536, "num_seqs must be in [1, 65536] (got %d)", num_seqs);
+  REQUIRE(num_beams >= 1 && num_beams <= 32, "num_beams must be in [1, 32] (got %d)", num_beams);
+  REQUIRE(vocab >= 1 && vocab <= (1 << 30), "vocab must be in [1, 2^30] (got %d)", vocab);
+  REQUIRE(num_candidates >= num_beams && num_candidates <= 64, "num_candidates must be in [num_beams, 64] (got %d)",
+          num_candidates);
+  REQUIRE(num_candidates <= (int64_t)num_beams * vocab, "num_candidates = %d is more than num_beams * vocab", num_candidates);
+  return CP_OK;
+}
+
+cp_status cp_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_candidates,
+                                        size_t* bytes) {
+  const cp_status st = check_beam_sizes(num_seqs, num_beams, vocab, num_candidates);
+  if (st != CP_OK) return st;
+  REQUIRE(bytes != nullptr, "bytes is null");
+  *bytes = cp_beam_select_bytes(num_seqs, num_beams, vocab, num_candidates);
+  return ok();
+}
+
+cp_status cp_beam_select(const cp_beam_select_args* a, void* workspace, size_t workspace_bytes, void* stream) {
+  REQUIRE(a != nullptr, "args is null");
+  REQUIRE(a->dtype == CP_F32 || a->dtype == CP_BF16, "dtype must be CP_F32 or CP_BF16");
+  const cp_status st = check_beam_sizes(a->num_seqs, a->num_beams, a->vocab, a->num_candidates);
+  if (st != CP_OK) return st;
+  REQUIRE(a->eos_token < 0 || a->num_candidates >= 2 * a->num_beams,
+          "an eos_token needs num_candidates >= 2 * num_beams (got %d)", a->num_candidates);
+  REQUIRE(a->logits_stride >= a->vocab, "logits_stride must hold a row");
+  REQUIRE(a->logits != nullptr && (reinterpret_cast<uintptr_t>(a->logits) & (a->dtype == CP_BF16 ? 1u : 3u)) == 0,
+          "logits must be a non-null pointer aligned to its type");
+  REQUIRE(a->scores && a->next_scores && a->next_beams && a->next_tokens && a->cand_scores && a->cand_beams &&
+              a->cand_tokens,
+          "scores and outputs are required");
+  REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
+          "workspace must be a non-null 256-byte aligned pointer");
+  const size_t need = cp_beam_select_bytes(a->num_seqs, a->num_beams, a->vocab, a->num_candidates);
+  REQUIRE(workspace_bytes >= need, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+  REQUIRE(cp_beam_select_ctas(*a) < (1ll << 31), "too many logits");
+  return launched(cp_launch_beam_select(*a, workspace, as_stream(stream)), "cp_beam_select launch");
+}
+
+cp_status cp_beam_reorder(const cp_beam_reorder_args* a, void* stream) {
+  REQUIRE(a != nullptr, "args is null");
+  REQUIRE(a->cache_q4 == 0 || a->cache_q4 == 1, "cache_q4 must be 0 or 1");
+  REQUIRE(a->cache_q4 || a->dtype == CP_F32 || a->dtype == CP_BF16, "dtype must be CP_F32 or CP_BF16");
+  REQUIRE(a->num_layers >= 1 && a->num_layers <= 65536, "num_layers must be >= 1");
+  REQUIRE(a->num_seqs >= 1 && a->num_seqs <= (1 << 24), "num_seqs must be >= 1");
+  REQUIRE(a->num_beams >= 1 && a->num_beams <= 32, "num_beams must be in [1, 32] (got %d)", a->num_beams);
+  REQUIRE(a->num_kv_heads >= 1 && a->num_kv_heads <= 65536, "bad num_kv_heads");
+  const cp_status st = check_cache_shape(a->head_dim, a->cp, a->interleave, a->block_size, a->max_blocks,
+                                         a->pool_pages);
+  if (st != CP_OK) return st;
+  REQUIRE(a->reserved == 0, "reserved must be 0");
+  REQUIRE(a->parents && a->seq_lens && a->tables_in && a->own_pages && a->tables_out,
+          "parents, seq_lens and the tables are required");
+  const size_t table = (size_t)a->cp * a->num_seqs * a->num_beams * a->max_blocks * sizeof(int32_t);
+  const uintptr_t in = reinterpret_cast<uintptr_t>(a->tables_in), out = reinterpret_cast<uintptr_t>(a->tables_out),
+                  own = reinterpret_cast<uintptr_t>(a->own_pages);
+  REQUIRE(in == out || in + table <= out || out + table <= in, "tables_out must be tables_in or not overlap it");
+  REQUIRE(own + table <= out || out + table <= own, "tables_out must not overlap own_pages");
+  REQUIRE((a->k_cache == nullptr) == (a->v_cache == nullptr), "k_cache and v_cache go together");
+  REQUIRE(aligned16(a->k_cache) && aligned16(a->v_cache), "k_cache and v_cache must be 16-byte aligned");
+  return launched(cp_launch_beam_reorder(*a, as_stream(stream)), "cp_beam_reorder launch");
 }
 
 }  // extern "C"

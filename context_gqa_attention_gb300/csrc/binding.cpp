@@ -1,5 +1,5 @@
 // The Python binding of the serving calls (rotate-and-append, cache read-back, 4-bit decode, attention
-// with modified scores): checks the tensors, makes the outputs, fills the C structs and calls
+// with modified scores, cross attention, beam search): checks the tensors, makes the outputs, fills the C structs and calls
 // libcpattn.so.  A decode step's kernels run for 5 to 10 us; the same checks and structs in Python
 // (ctypes) took the host 24 us a call, here 5 to 6.5.
 //
@@ -498,6 +498,190 @@ PyObject* decode_fused(Args& x) {
   return pair(o, l);
 }
 
+// q, cu_q, k, v, cu_kv, kv_lens, key_ranges, max_seqlen_q, max_seqlen_kv, scale, workspace, out, out_lse, want_lse,
+// err, stream
+PyObject* cross(Args& x) {
+  const Tensor& q = x.tensor("q");
+  const Call c(q, "cp_cross_attention");
+  const Tensor &cu = x.tensor("cu_seqlens_q"), &k = x.tensor("k"), &v = x.tensor("v"), &cu_kv = x.tensor("cu_seqlens_kv");
+  const Tensor *kv_lens = x.opt("kv_lens"), *ranges = x.opt("key_ranges");
+  cp_cross_args a{};
+  a.max_seqlen_q = x.i32("max_seqlen_q");
+  a.max_seqlen_kv = x.i32("max_seqlen_kv");
+  a.softmax_scale = x.real();
+  const Tensor *given = x.opt("workspace"), *out = x.opt("out"), *out_lse = x.opt("out_lse");
+  const bool want_lse = x.flag("want_lse");
+  const Tensor* err = x.opt("err");
+  void* stream = c.stream(x);
+
+  const at::ScalarType T = q.scalar_type();
+  a.q_stride = c.token_rows(q, "q", T);
+  a.k_stride = c.token_rows(k, "k", T);
+  a.v_stride = c.token_rows(v, "v", T);
+  const int64_t N = q.size(0), Hq = q.size(1), d = q.size(2), B = cu.numel() - 1;
+  if (k.size(2) != d) refuse("k must be [Nkv, Hkv, " + std::to_string(d) + "] (got " + text(k.sizes()) + ")");
+  c.shaped(v, "v", {k.size(0), k.size(1), d});
+  a.dtype = dtype_of(q);
+  a.num_seqs = i32(B, "the number of sequences");
+  a.num_q_heads = i32(Hq, "the number of query heads");
+  a.num_kv_heads = i32(k.size(1), "the number of kv heads");
+  a.head_dim = i32(d, "head_dim");
+  a.total_q = i32(N, "the number of rows");
+  a.total_kv = i32(k.size(0), "the number of kv rows");
+  a.cu_seqlens_q = c.index(&cu, "cu_seqlens_q", B + 1);
+  a.cu_seqlens_kv = c.index(&cu_kv, "cu_seqlens_kv", B + 1);
+  a.kv_lens = c.index(kv_lens, "kv_lens", B);
+  a.key_ranges = c.index(ranges, "key_ranges", 2 * N);
+  a.q = in(q);
+  a.k = in(k);
+  a.v = in(v);
+  a.err = c.error_word(err);
+  const Tensor o = c.output(out, "out", {N, Hq, d}, T);
+  Tensor l;
+  if (out_lse != nullptr || want_lse) l = c.output(out_lse, "out_lse", {N, Hq}, at::kFloat);
+  Tensor workspace;
+  if (given != nullptr) {
+    c.dense(*given, "workspace", at::kByte);
+    workspace = *given;
+  } else {
+    size_t need = 0;
+    check(cp_cross_attention_workspace_size(&a, &need));
+    if (need > 0) workspace = at::empty({(int64_t)need}, at::TensorOptions().device(c.device).dtype(at::kByte));
+  }
+  const size_t bytes = workspace.defined() ? (size_t)workspace.numel() : 0;
+  check(cp_cross_attention(&a, bytes ? out_of(workspace) : nullptr, bytes, out_of(o),
+                           l.defined() ? static_cast<float*>(out_of(l)) : nullptr, stream));
+  return pair(o, l);
+}
+
+PyObject* tuple_of(std::initializer_list<Tensor> ts) {
+  PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
+  if (r == nullptr) throw python_error();
+  THPObjectPtr hold(r);
+  Py_ssize_t i = 0;
+  for (const Tensor& t : ts) {
+    PyObject* w = THPVariable_Wrap(t);
+    if (w == nullptr) throw python_error();
+    PyTuple_SET_ITEM(r, i++, w);
+  }
+  return hold.release();
+}
+
+// logits, scores, num_candidates, eos, workspace, the six outputs, stream
+PyObject* beam_select(Args& x) {
+  const Tensor& logits = x.tensor("logits");
+  const Call c(logits, "cp_beam_select");
+  const Tensor& scores = x.tensor("scores");
+  cp_beam_select_args a{};
+  a.num_candidates = x.i32("num_candidates");
+  a.eos_token = x.i32("eos_token");
+  const Tensor* given = x.opt("workspace");
+  const Tensor *ns = x.opt("next_scores"), *nb = x.opt("next_beams"), *nt = x.opt("next_tokens"),
+               *cs = x.opt("cand_scores"), *cb = x.opt("cand_beams"), *ct = x.opt("cand_tokens");
+  void* stream = c.stream(x);
+
+  dims(logits, "logits", 3, "[B, K, vocab]");
+  const int64_t B = logits.size(0), K = logits.size(1), V = logits.size(2);
+  // rows of one stride: beams of a sequence, and the sequences behind one another
+  const int64_t stride = K > 1 ? logits.stride(1) : B > 1 ? logits.stride(0) : V;
+  if (logits.numel() != 0 && ((V > 1 && logits.stride(2) != 1) || (K > 1 && B > 1 && logits.stride(0) != K * stride)))
+    refuse("the rows of logits must be contiguous and equally spaced (only the row stride is free)");
+  a.dtype = dtype_of(logits);
+  c.dense(scores, "scores", at::kFloat);
+  c.shaped(scores, "scores", {B, K});
+  a.num_seqs = i32(B, "the number of sequences");
+  a.num_beams = i32(K, "the number of beams");
+  a.vocab = i32(V, "vocab");
+  a.logits_stride = stride;
+  size_t need = 0;
+  check(cp_beam_select_workspace_size(a.num_seqs, a.num_beams, a.vocab, a.num_candidates, &need));
+  Tensor workspace;
+  if (given != nullptr) {
+    c.dense(*given, "workspace", at::kByte);
+    workspace = *given;
+  } else {
+    workspace = at::zeros({(int64_t)need}, at::TensorOptions().device(c.device).dtype(at::kByte));
+  }
+  const int64_t M = a.num_candidates;
+  const Tensor o0 = c.output(ns, "next_scores", {B, K}, at::kFloat), o1 = c.output(nb, "next_beams", {B, K}, at::kInt),
+               o2 = c.output(nt, "next_tokens", {B, K}, at::kInt), o3 = c.output(cs, "cand_scores", {B, M}, at::kFloat),
+               o4 = c.output(cb, "cand_beams", {B, M}, at::kInt), o5 = c.output(ct, "cand_tokens", {B, M}, at::kInt);
+  a.logits = in(logits);
+  a.scores = static_cast<const float*>(in(scores));
+  a.next_scores = static_cast<float*>(out_of(o0));
+  a.next_beams = static_cast<int32_t*>(out_of(o1));
+  a.next_tokens = static_cast<int32_t*>(out_of(o2));
+  a.cand_scores = static_cast<float*>(out_of(o3));
+  a.cand_beams = static_cast<int32_t*>(out_of(o4));
+  a.cand_tokens = static_cast<int32_t*>(out_of(o5));
+  check(cp_beam_select(&a, out_of(workspace), (size_t)workspace.numel(), stream));
+  return tuple_of({o0, o1, o2, o3, o4, o5});
+}
+
+// parents, seq_lens, tables, own_pages, k_cache, v_cache, cp, interleave, tables_out, err, stream
+PyObject* beam_reorder(Args& x) {
+  const Tensor& parents = x.tensor("parents");
+  const Call c(parents, "cp_beam_reorder");
+  const Tensor &lens = x.tensor("seq_lens"), &tables = x.tensor("block_tables"), &own = x.tensor("own_pages");
+  const Tensor *kc = x.opt("k_cache"), *vc = x.opt("v_cache");
+  cp_beam_reorder_args a{};
+  a.cp = x.i32("cp");
+  a.interleave = x.i32("interleave");
+  const Tensor *out = x.opt("tables_out"), *err = x.opt("err");
+  void* stream = c.stream(x);
+
+  dims(parents, "parents", 2, "[B, K]");
+  const int64_t B = parents.size(0), K = parents.size(1);
+  a.parents = c.index(&parents, "parents", B * K);
+  a.seq_lens = c.index(&lens, "seq_lens", B);
+  c.dense(tables, "block_tables", at::kInt);
+  if (tables.dim() != 3 || tables.size(0) != a.cp || tables.size(1) != B * K)
+    refuse("block_tables must be [cp, B K, max_blocks] = [" + std::to_string(a.cp) + ", " + std::to_string(B * K) +
+           ", ..] (got " + text(tables.sizes()) + ")");
+  c.dense(own, "own_pages", at::kInt);
+  if (own.sizes() != tables.sizes()) refuse("own_pages must be " + text(tables.sizes()) + " (got " + text(own.sizes()) + ")");
+  const Tensor o = c.output(out, "tables_out", {tables.size(0), tables.size(1), tables.size(2)}, at::kInt);
+  a.num_seqs = i32(B, "the number of sequences");
+  a.num_beams = i32(K, "the number of beams");
+  a.max_blocks = i32(tables.size(2), "max_blocks");
+  a.num_layers = 1;
+  a.block_size = 16;
+  if ((kc == nullptr) != (vc == nullptr)) refuse("k_cache and v_cache go together");
+  if (kc != nullptr) {
+    a.cache_q4 = kc->scalar_type() == at::kByte;
+    const int64_t nd = a.cache_q4 ? 4 : 5;
+    if (kc->dim() != nd && kc->dim() != nd + 1)
+      refuse("k_cache must be [cp, pool, Hkv, 16, d], or uint8 [cp, pool, Hkv, 9 d] (4-bit), or several layers of them "
+             "[layers, ..]");
+    c.dense(*kc, "k_cache", kc->scalar_type());
+    c.dense(*vc, "v_cache", kc->scalar_type());
+    if (vc->sizes() != kc->sizes()) refuse("v_cache must be " + text(kc->sizes()) + " (got " + text(vc->sizes()) + ")");
+    const int64_t at0 = kc->dim() - nd;
+    if (kc->size(at0) != a.cp || (a.cache_q4 && kc->size(-1) % 9 != 0))
+      refuse("k_cache is " + text(kc->sizes()) + ": cp = " + std::to_string(a.cp) + " wants another shape");
+    if (!a.cache_q4) a.dtype = dtype_of(*kc);
+    a.num_layers = i32(at0 ? kc->size(0) : 1, "the number of layers");
+    a.pool_pages = kc->size(at0 + 1);
+    a.num_kv_heads = i32(kc->size(at0 + 2), "the number of kv heads");
+    a.block_size = a.cache_q4 ? 16 : i32(kc->size(at0 + 3), "block_size");
+    a.head_dim = i32(a.cache_q4 ? kc->size(-1) / 9 : kc->size(-1), "head_dim");
+    a.k_cache = out_of(*kc);
+    a.v_cache = out_of(*vc);
+  } else {  // tables alone: any page number goes
+    a.pool_pages = std::numeric_limits<int32_t>::max();
+    a.num_kv_heads = 1;
+    a.head_dim = 128;
+  }
+  a.tables_in = static_cast<const int32_t*>(in(tables));
+  a.own_pages = static_cast<const int32_t*>(in(own));
+  a.tables_out = static_cast<int32_t*>(out_of(o));
+  a.err = c.error_word(err);
+  check(cp_beam_reorder(&a, stream));
+  PyObject* r = THPVariable_Wrap(o);
+  if (r == nullptr) throw python_error();
+  return r;
+}
+
 template <PyObject* (*F)(Args&), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -527,6 +711,9 @@ PyMethodDef methods[] = {
     ENTRY("prefill", prefill, 16),
     ENTRY("decode_partial", decode_partial, 20),
     ENTRY("decode_fused", decode_fused, 22),
+    ENTRY("cross", cross, 16),
+    ENTRY("beam_select", beam_select, 12),
+    ENTRY("beam_reorder", beam_reorder, 11),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "cpattn_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

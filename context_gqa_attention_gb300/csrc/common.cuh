@@ -141,6 +141,10 @@ cudaError_t cp_launch_decode(const cp_decode_args& a, float scale, cudaStream_t 
 bool cp_make_bf16_map_2d(void* map, const void* base, unsigned long long cols,
                          unsigned long long rows, unsigned long long pitch_elems,
                          unsigned box_rows);
+// 3D bf16 TMA descriptor over rows of `heads` heads of `cols` elements: box of 64 columns x box_heads heads x
+// box_rows rows, landing as box_rows * box_heads rows of 128 bytes; 128-byte swizzle, zero fill.
+bool cp_make_bf16_map_3d(void* map, const void* base, unsigned long long cols, unsigned long long heads,
+                         unsigned long long rows, unsigned long long pitch_elems, unsigned box_heads, unsigned box_rows);
 // 3D bf16 TMA descriptor over a paged pool of `rows` rows of d = 128 elements seen as
 // {64 columns, rows, 2 column halves}: one box {64, 16, 2} is a whole 16-row page, landing in
 // shared memory as [half][16 rows][128 bytes] (128-byte swizzle).  False if the driver refuses.
@@ -183,6 +187,11 @@ cudaError_t cp_launch_prefill_mod(const cp_prefill_args& a, const cp_score_mod& 
                                   float* out_lse, cudaStream_t s);
 cudaError_t cp_launch_rope_write(const cp_rope_write_args& a, cudaStream_t s);
 cudaError_t cp_launch_kv_read(const cp_kv_read_args& a, cudaStream_t s);
+
+size_t cp_beam_select_bytes(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_candidates);
+long long cp_beam_select_ctas(const cp_beam_select_args& a);
+cudaError_t cp_launch_beam_select(const cp_beam_select_args& a, void* workspace, cudaStream_t s);
+cudaError_t cp_launch_beam_reorder(const cp_beam_reorder_args& a, cudaStream_t s);
 
 // Host helpers exported by api.cu for entry points defined in other translation units.
 cp_status cp_check_decode_args_for_fused(const cp_decode_args* a, const void* out);

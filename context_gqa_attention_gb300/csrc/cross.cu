@@ -1,0 +1,521 @@
+// Cross attention (cp_cross_attention) of many query rows on the 5th-generation tensor cores: bf16 in, f32
+// accumulate.  No counterpart on the pages, whose attention is causal self-attention.
+//
+//   out_i = softmax over the keys j in [lo_i, hi_i) of scale q_i.k_j, times V
+//
+// Without causality every row of a sequence sees the same keys, so the G query heads of a kv head are packed: a
+// tile of 128 rows is floor(128 / G) tokens under all G heads (one 3D box of q), whatever G is, and a CTA works
+// on two consecutive tiles that share every K / V tile of 128 keys.  Warps:
+//   0      TMA producer: both Q tiles once, then K and V tiles through a 4-slot ring
+//   1      TMEM owner and MMA issuer (one thread): S = Q K^T, then O += P V with P read from TMEM; order
+//          PV0(t) | QK0(t+1) | PV1(t) | QK1(t+1), so a tile's softmax overlaps the other's two MMAs
+//   2-3    V guards: 0 times an infinity or a NaN is NaN, so they clear the V rows behind the last key, and with
+//          key ranges (RANGES) every element that is not finite in tiles that some row sees in part
+//   4-11   two softmax warpgroups, one a tile, a thread a row
+// Parts (CrossParams): the keys of the last wave's items, or of all when they are few, are cut so that every SM
+// has work; cross_merge_kernel joins them.
+//
+// Every wait is bounded; on expiry the CTA raises CP_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+
+#include "cross.cuh"
+#include "guard.cuh"
+#include "rows.cuh"
+
+namespace cpattn {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSlots = 4;
+constexpr int kRegsFirst = 88, kRegsSoftmax = 208, kRegsLaunch = 168;
+static_assert(kRegsFirst + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register budgets exceed the launch");
+constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
+
+template <int D>
+struct Smem {
+  static constexpr int kQ = BM * D * 2;
+  static constexpr int kKV = BN * D * 2;
+  static constexpr int oQ = 0;
+  static constexpr int oKV = 2 * kQ;
+  static constexpr int oBar = oKV + kSlots * kKV;
+  static constexpr int bQ = 0, bFull = 1, bEmpty = bFull + kSlots, bS = bEmpty + kSlots, bP = bS + 2, bO = bP + 2,
+                       bFix = bO + 2, bLast = bFix + 2, bDone = bLast + 1, nBar = bDone + 1;
+  static constexpr int oMisc = oBar + nBar * 8;  // TMEM base, abort flag, first / last unclean tile, keys
+  static constexpr int kBytes = oMisc + 32;
+  // the base is rounded up to the 1 KB swizzle atom; never below 120 KB, so that one CTA (and its 512 TMEM
+  // columns) has an SM to itself
+  static constexpr int kAlloc = (kBytes + 1024) > 120 * 1024 ? (kBytes + 1024) : 120 * 1024;
+  static_assert(kAlloc <= 232448, "dynamic shared memory beyond the 227 KB per-CTA limit");
+};
+
+// Columns outside [c0, c1) of a row's 128 scores.
+CP_DEV void mask_columns(float (&v)[32], int at, int c0, int c1) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = at + k >= c0 && at + k < c1 ? v[k] : -INFINITY;
+}
+
+template <int D, bool RANGES>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const CrossParams p) {
+  using Sm = Smem<D>;
+  constexpr int KB = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  chained_start();
+
+  // ---- the item, or the part of one
+  int piece = -1, part = 0;
+  unsigned index = blockIdx.x;
+  if ((int)index >= p.n_whole) {
+    piece = (int)index - p.n_whole;
+    part = piece % p.split_k;
+    index = (unsigned)p.n_whole + (unsigned)(piece / p.split_k);
+  }
+  const CrossItem w = cross_item(p, index, threadIdx.x == 0 && part == 0);
+  if (w.tokens == 0) return;
+  const int per_tile = p.span / 2;  // tokens
+  const int rows0 = min(w.tokens, per_tile) * p.G, rows1 = max(0, w.tokens - per_tile) * p.G;
+  const bool two = rows1 > 0;
+
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base - raw);
+  const uint32_t sQ = base + Sm::oQ, sKV = base + Sm::oKV;
+  auto bar = [&](int i) -> uint32_t { return base + (uint32_t)Sm::oBar + 8u * (uint32_t)i; };
+  int* misc = reinterpret_cast<int*>(sbase + Sm::oMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(misc + 1);
+  auto fail = [&]() {
+    *abort_flag = 1u;
+    report(p.err, CP_ERR_TIMEOUT);
+  };
+  if (threadIdx.x == 0) {
+    mbar_init(bar(Sm::bQ), 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar(Sm::bFull + s), 1);
+      mbar_init(bar(Sm::bEmpty + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Sm::bS + i), 1);
+      mbar_init(bar(Sm::bP + i), 4);
+      mbar_init(bar(Sm::bO + i), 1);
+      mbar_init(bar(Sm::bFix + i), 2);
+    }
+    mbar_init(bar(Sm::bLast), 1);
+    mbar_init(bar(Sm::bDone), 1);
+    misc[1] = 0;
+    misc[2] = 0x7fffffff;  // unclean tiles
+    misc[3] = -1;
+    misc[4] = 0x7fffffff;  // keys that some row sees
+    misc[5] = 0;
+    misc[6] = 0;           // keys that every row sees
+    misc[7] = 0x7fffffff;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_q);
+    mbar_expect_tx(bar(Sm::bQ), (two ? 2 : 1) * KB * per_tile * p.G * 128);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (i == 0 || two)
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          tma_load_3d(sQ + i * Sm::kQ + kb * BM * 128, &map_q, kb * 64, w.g * p.G, w.q0 + w.t0 + i * per_tile,
+                      bar(Sm::bQ));
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(misc), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (RANGES) {
+    for (int t = threadIdx.x; t < w.tokens; t += kThreads) {
+      int lo, hi;
+      cross_range(p, w, w.t0 + t, lo, hi);
+      if (lo < hi) {
+        atomicMin(misc + 4, lo);
+        atomicMax(misc + 5, hi);
+      }
+      atomicMax(misc + 6, lo);
+      atomicMin(misc + 7, hi);
+    }
+    __syncthreads();
+  }
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)misc[0];
+  const int key_lo = RANGES ? misc[4] : 0, key_hi = RANGES ? misc[5] : w.keys;
+  const int all_lo = RANGES ? misc[6] : 0, all_hi = RANGES ? misc[7] : w.keys;
+  // key tiles of this CTA, counted from key_lo
+  const int every = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
+  const int ta = piece < 0 ? 0 : (int)((long long)every * part / p.split_k);
+  const int ntiles = (piece < 0 ? every : (int)((long long)every * (part + 1) / p.split_k)) - ta;
+  const int k_first = key_lo + ta * BN;  // first key
+  auto in_part = [&](int t) -> bool {    // some row sees only a part of key tile t
+    const int k0 = k_first + t * BN;
+    return k0 + BN > all_hi || (RANGES && k0 < all_lo);
+  };
+  // Without ranges the guards have only the last V tile to clean, if at all.  It lands at a barrier of its own: on the
+  // ring's they would have to follow every phase, in step with the issuer.
+  const bool clean_last = !RANGES && in_part(ntiles - 1);
+  // where a row of tile i goes
+  auto out_row = [&](int i, int row) -> long long {
+    const int t = row / p.G;
+    return ((long long)w.q0 + w.t0 + i * per_tile + t) * p.Hq + w.g * p.G + (row - t * p.G);
+  };
+
+  if (ntiles <= 0) {  // no key
+    const int rows = rows0 + rows1;
+    for (int r = threadIdx.x; r < rows; r += kThreads) {
+      const int i = r >= rows0 ? 1 : 0, row = r - i * rows0;
+      if (piece >= 0) {
+        p.ws_lse[(long long)piece * p.rows + i * per_tile * p.G + row] = -INFINITY;
+        continue;
+      }
+      const long long o = out_row(i, row);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o * D);
+      for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr) p.lse[o] = -INFINITY;
+    }
+    if (threadIdx.x == 0) mbar_wait(bar(Sm::bQ), 0u, nullptr, kBudget);  // Q has landed before the CTA exits
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+
+  if (warp < 4) {
+    regs_dec<kRegsFirst>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+        bool ok = true;
+        int issued = 0;  // ring fills: K(t) is fill 2 t, V(t) fill 2 t + 1
+        for (int i = 0; i < 2 * ntiles; ++i) {
+          const int slot = i % kSlots;
+          if (!mbar_wait(bar(Sm::bEmpty + slot), ((uint32_t)(i / kSlots) & 1u) ^ 1u, abort_flag, kBudget)) {
+            ok = false;
+            break;
+          }
+          const CUtensorMap* map = (i & 1) ? &map_v : &map_k;
+          const uint32_t full = bar(clean_last && i == 2 * ntiles - 1 ? Sm::bLast : Sm::bFull + slot);
+          mbar_expect_tx(full, Sm::kKV);
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+            tma_load_2d(sKV + slot * Sm::kKV + kb * BN * 128, map, w.g * D + kb * 64, w.kv0 + k_first + (i >> 1) * BN,
+                        full);
+          issued = i + 1;
+        }
+        if (!ok) fail();
+        // every copy issued into this CTA's shared memory has landed before it exits
+        mbar_wait(bar(Sm::bQ), 0u, nullptr, kBudget);
+        for (int i = max(0, issued - kSlots); i < issued; ++i) {
+          if (clean_last && i == 2 * ntiles - 1) mbar_wait(bar(Sm::bLast), 0u, nullptr, kBudget);
+          else mbar_wait(bar(Sm::bFull + i % kSlots), (uint32_t)(i / kSlots) & 1u, nullptr, kBudget);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        const uint32_t id_qk = idesc_bf16_f32(BM, BN, false, false);
+        const uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
+        // descriptors built once and advanced: this thread is on the critical path
+        const uint64_t dq0 = desc_sw128(sQ, 16, 1024);
+        const uint64_t dk0 = desc_sw128(sKV, 16, 1024);
+        const uint64_t dv0 = desc_sw128(sKV, BN * 128, 1024);
+        auto issue_qk = [&](int tile, int slot) {
+          const uint64_t dq = desc_advance(dq0, (uint32_t)(tile * Sm::kQ));
+          const uint64_t dk = desc_advance(dk0, (uint32_t)(slot * Sm::kKV));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (BM * 128) + (kk % 4) * 32;
+            mma_ss(tmem + (uint32_t)(tile * BN), desc_advance(dq, off), desc_advance(dk, off), id_qk, kk > 0);
+          }
+          mma_commit(bar(Sm::bS + tile));
+        };
+        auto issue_pv = [&](int tile, int slot, bool acc) {
+          const uint64_t dv = desc_advance(dv0, (uint32_t)(slot * Sm::kKV));
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + 256u + (uint32_t)(tile * D), tmem + (uint32_t)(tile * BN + kk * 8),
+                   desc_advance(dv, kk * 16u * 128u), id_pv, acc || kk > 0);
+          mma_commit(bar(Sm::bO + tile));
+        };
+        bool ok = mbar_wait(bar(Sm::bQ), 0u, abort_flag, kBudget) && mbar_wait(bar(Sm::bFull), 0u, abort_flag, kBudget);
+        if (ok) {
+          tc_fence_after();
+          issue_qk(0, 0);
+          if (two) issue_qk(1, 0);
+          mma_commit(bar(Sm::bEmpty + 0));
+        }
+        for (int t = 0; ok && t < ntiles; ++t) {
+          const int iv = 2 * t + 1, ik = 2 * t + 2, sv = iv % kSlots, sk = ik % kSlots;
+          // V(t), with ranges and in a last tile in part as the guards leave it
+          if (!RANGES && clean_last && t == ntiles - 1) {
+            ok = mbar_wait(bar(Sm::bFix), 0u, abort_flag, kBudget);
+          } else {
+            ok = mbar_wait(bar(Sm::bFull + sv), (uint32_t)(iv / kSlots) & 1u, abort_flag, kBudget);
+            if (RANGES) ok = ok && mbar_wait(bar(Sm::bFix + (t & 1)), (uint32_t)(t >> 1) & 1u, abort_flag, kBudget);
+          }
+          ok = ok && mbar_wait(bar(Sm::bP + 0), (uint32_t)t & 1u, abort_flag, kBudget);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(0, sv, t > 0);
+          const bool more = t + 1 < ntiles;
+          if (more) {
+            ok = mbar_wait(bar(Sm::bFull + sk), (uint32_t)(ik / kSlots) & 1u, abort_flag, kBudget);
+            if (!ok) break;
+            tc_fence_after();
+            issue_qk(0, sk);
+          }
+          if (two) {
+            ok = mbar_wait(bar(Sm::bP + 1), (uint32_t)t & 1u, abort_flag, kBudget);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, sv, t > 0);
+          }
+          mma_commit(bar(Sm::bEmpty + sv));
+          if (more) {
+            if (two) issue_qk(1, sk);
+            mma_commit(bar(Sm::bEmpty + sk));
+          }
+        }
+        if (!ok) fail();
+        // every MMA issued by this thread has retired before TMEM is released
+        mma_commit(bar(Sm::bDone));
+        mbar_wait(bar(Sm::bDone), 0u, nullptr, kBudget);
+      }
+    } else {
+      // ---------------------------------------------------------------- V guards
+      // with ranges every tile, in step with the MMA issuer: a barrier's phases are told apart by parity alone
+      for (int t = RANGES ? 0 : ntiles - 1; t < ntiles; ++t) {
+        if (!RANGES && !clean_last) break;
+        const int iv = 2 * t + 1, sv = iv % kSlots;
+        const bool ok = __all_sync(0xffffffffu, RANGES ? mbar_wait(bar(Sm::bFull + sv), (uint32_t)(iv / kSlots) & 1u,
+                                                                   abort_flag, kBudget)
+                                                       : mbar_wait(bar(Sm::bLast), 0u, abort_flag, kBudget));
+        if (!ok) {
+          if (lane == 0) fail();
+          break;
+        }
+        uint8_t* tile = sbase + Sm::oKV + sv * Sm::kKV;
+        const int last = key_hi - k_first - t * BN;  // rows from here on are no key of any row
+        if constexpr (RANGES) {
+          if (in_part(t)) {
+            if (guard_v<D, BN>(tile, last, (warp - 2) * 32 + lane)) {
+              atomicMin(misc + 2, t);
+              atomicMax(misc + 3, t);
+            }
+            fence_proxy_async_smem();  // the MMA reads what was written here
+          }
+        } else {
+          for (int i = (warp - 2) * 32 + lane; i < Sm::kKV / 16; i += 64)
+            if (((i >> 3) & (BN - 1)) >= last) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Sm::bFix + (RANGES ? t & 1 : 0)));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax, one warpgroup per tile
+    regs_inc<kRegsSoftmax>();
+    const int tile = (warp - 4) >> 2, q4 = warp & 3;
+    const int row = q4 * 32 + lane, rows = tile == 0 ? rows0 : rows1;
+    if (rows > 0) {
+      const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+      const uint32_t tS = tmem + lane_off + (uint32_t)(tile * BN);
+      const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(tile * D);
+      int lo = 0, hi = w.keys;
+      if (RANGES && row < rows) cross_range(p, w, w.t0 + tile * per_tile + row / p.G, lo, hi);
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int t = 0; t < ntiles; ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
+        if (!ok) break;
+        tc_fence_after();
+        float s0[32], s1[32], s2[32], s3[32];
+        load_row(tS, s0, s1, s2, s3);
+        const int k0 = k_first + t * BN;
+        int lim = hi - 1 - k0;
+        if constexpr (RANGES) {
+          if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + BN)) {
+            mask_columns(s0, 0, lo - k0, hi - k0);
+            mask_columns(s1, 32, lo - k0, hi - k0);
+            mask_columns(s2, 64, lo - k0, hi - k0);
+            mask_columns(s3, 96, lo - k0, hi - k0);
+          }
+          lim = BN - 1;
+        }
+        const float alpha = row_max_update(s0, s1, s2, s3, lim, p.scale_log2, m);
+        // S(t) complete implies PV(t-1) complete (it was issued before QK(t)): O is stable and the S columns may
+        // take P(t)
+        l = l * alpha + row_exp_tmem(s0, s1, s2, s3, p.scale_log2, m, tS);
+        if (t > 0) rescale_o<D>(tO, alpha);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Sm::bP + tile));
+      }
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bO + tile), (uint32_t)(ntiles - 1) & 1u, abort_flag, kBudget));
+      if (ok) {
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float lse = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+        // what the guards took out of V and this row sees: p > 0 times it is itself, whatever p is
+        if constexpr (RANGES) {
+          const int u0 = *(volatile int*)(misc + 2), u1 = *(volatile int*)(misc + 3);
+          if (u1 >= 0) {
+            const int r0 = max(lo, k_first + u0 * BN), r1 = min(hi, k_first + (u1 + 1) * BN);
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (long long)w.kv0 * p.v_stride;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld(o);
+              if (row < rows) restore<D>(o, v, p.v_stride, w.g * D + c, r0, r1);
+              __syncwarp();
+              tmem_st32(tO + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // Rows go out through shared memory, one whole row an instruction: tile 0 over the Q tiles (free: its last
+        // PV came after the other tile's last QK), tile 1 over the ring (its last PV is the CTA's last MMA)
+        const int mine = min(32, rows - q4 * 32);  // rows of this warp
+        const uint32_t sb = (tile == 0 ? sQ : sKV) + (uint32_t)(q4 * 32 * D * (piece >= 0 ? 4 : 2));
+        if (piece >= 0) {
+          stage_rows_f32<D>(tO, inv, sb, lane);
+          __syncwarp();
+          const long long r0 = (long long)piece * p.rows + tile * per_tile * p.G + q4 * 32;
+          if (mine == 32) {
+            store_staged_f32<D>(sb, lane, p.ws_out + r0 * D, D);
+          } else if (mine > 0) {
+            for (int r = 0; r < mine; ++r)
+              for (int c = lane; c < D; c += 32) {
+                float x;
+                asm volatile("ld.shared.f32 %0, [%1];"
+                             : "=f"(x)
+                             : "r"(sb + (uint32_t)((c / 32) * 4096 + r * 128) +
+                                   ((uint32_t)(((c % 32) / 4) ^ (r & 7)) << 4) + (uint32_t)(c % 4) * 4u));
+                p.ws_out[(r0 + r) * D + c] = x;
+              }
+          }
+          if (lane < mine) p.ws_lse[r0 + lane] = lse;
+        } else if (mine > 0) {
+          stage_rows_bf16<D>(tO, inv, sb, lane);
+          __syncwarp();
+          const long long o = out_row(tile, min(row, rows - 1));
+          constexpr int E = D / 32;  // columns of a lane
+          const int col = E * lane;
+          const uint32_t a0 = sb + (uint32_t)((col / 64) * 4096 + (col % 8) * 2);
+          const int chunk = (col % 64) / 8;
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r) {
+            const long long at = __shfl_sync(0xffffffffu, o, r) * D + col;
+            if (r >= mine) break;
+            const uint32_t a = a0 + (uint32_t)(r * 128) + ((uint32_t)(chunk ^ (r & 7)) << 4);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at;
+            if constexpr (E == 4) {
+              uint2 x;
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
+              *reinterpret_cast<uint2*>(dst) = x;
+            } else {
+              uint32_t x;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
+              *reinterpret_cast<uint32_t*>(dst) = x;
+            }
+          }
+          if (lane < mine && p.lse != nullptr) p.lse[o] = lse;
+        }
+      } else if (lane == 0) {
+        fail();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const cp_cross_args& a, const CrossPlan& plan, float scale, void* ws, size_t ws_bytes, void* out,
+                   float* lse, cudaStream_t s) {
+  CrossParams p;
+  cp_cross_fill(p, a, plan, scale, ws, ws_bytes, out, lse);
+  CUtensorMap mq, mk, mv;
+  const unsigned per_tile = (unsigned)p.span / 2;
+  if (!cp_make_bf16_map_3d(&mq, a.q, D, (unsigned long long)p.Hq, (unsigned long long)p.Nq,
+                           (unsigned long long)a.q_stride, (unsigned)p.G, per_tile))
+    return cudaErrorInvalidValue;
+  if (p.Nkv > 0) {
+    const unsigned long long cols = (unsigned long long)p.Hkv * D, rows = (unsigned long long)p.Nkv;
+    if (!cp_make_bf16_map_2d(&mk, a.k, cols, rows, (unsigned long long)a.k_stride, BN) ||
+        !cp_make_bf16_map_2d(&mv, a.v, cols, rows, (unsigned long long)a.v_stride, BN))
+      return cudaErrorInvalidValue;
+  } else {
+    mk = mv = mq;  // (no key: never loaded from)
+  }
+  const long long grid = p.n_whole + (long long)p.n_split * p.split_k;
+  if (grid >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  auto kern = a.key_ranges != nullptr ? cross_kernel<D, true> : cross_kernel<D, false>;
+  // the warpgroups' register budgets assume the registers a thread of this launch gets; a build that gave the
+  // kernel another count would leave an increase waiting, so refuse it
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(kern, dim3((unsigned)grid), kThreads, Smem<D>::kAlloc, s, mq, mk, mv, p);
+  if (e != cudaSuccess || p.n_split == 0) return e;
+  return launch_merge<__nv_bfloat16, D>(p, s);
+}
+
+}  // namespace
+}  // namespace cpattn
+
+// Items take about 4 us and 1.7 us a key tile, one on an SM; a cut costs a merge of about 3 us.  The items of whole
+// waves stay whole; the rest are cut into the number of parts that ends soonest by that estimate.  With lengths
+// that differ, the items that there are can only be guessed, so all are cut or none.
+CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms) {
+  CrossPlan c;
+  const int G = a.num_q_heads / a.num_kv_heads;
+  c.span = 2 * (cpattn::BM / G);
+  c.tiles = a.max_seqlen_q > 0 ? (int)(((long long)a.max_seqlen_q + c.span - 1) / c.span) : 1;
+  c.rows = c.span * G;
+  c.items = (long long)a.num_seqs * a.num_kv_heads * c.tiles;
+  c.n_split = 0;
+  c.split_k = 1;
+  const bool even = (long long)a.num_seqs * a.max_seqlen_q <= a.total_q;
+  const double live = even ? (double)c.items
+                           : fmin((double)c.items, a.num_kv_heads * ((double)a.total_q / c.span + 0.5 * a.num_seqs));
+  const double key_tiles = ceil(a.max_seqlen_kv / (double)cpattn::BN);
+  const double waves = even ? floor(live / sms) : 0, rest = live - waves * sms;
+  double best = 0;
+  for (int k = 1; k <= 32 && k <= key_tiles && (k == 1 || rest * k <= 4.0 * sms); ++k) {
+    const double t = ceil(rest * k / sms) * (4 + 1.7 * ceil(key_tiles / k)) + (k > 1 ? 3 : 0);
+    if (k == 1 || t < 0.97 * best) {
+      best = t;
+      c.split_k = k;
+    }
+  }
+  if (c.split_k > 1) c.n_split = even ? (long long)rest : c.items;
+  if (c.n_split == 0) c.split_k = 1;
+  c.bytes = cp_cross_parts_bytes(c, a.head_dim);
+  return c;
+}
+
+cudaError_t cp_launch_cross_tc(const cp_cross_args& a, float scale, void* ws, size_t ws_bytes, void* out, float* lse,
+                               cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const CrossPlan plan = cp_cross_plan_tc(a, sms);
+  return a.head_dim == 64 ? cpattn::launch<64>(a, plan, scale, ws, ws_bytes, out, lse, s)
+                          : cpattn::launch<128>(a, plan, scale, ws, ws_bytes, out, lse, s);
+}

@@ -1,0 +1,179 @@
+// What the kernels of cp_cross_attention share (internal): the launch's parameters, a sequence's bounds, and the
+// merge of the parts of items whose keys were cut.
+#pragma once
+
+#include "common.cuh"
+
+namespace cpattn {
+namespace {
+
+// An item is `span` tokens of a sequence under the G query heads of a kv head: span * G query rows, row p being
+// token p / G, head p mod G, which all see the same keys (or, with key_ranges, some of them).  Items n_whole ..
+// of a launch are cut into split_k parts each, whose normalised rows and LSEs wait in the workspace.
+struct CrossParams {
+  int B, Hq, Hkv, G, Nq, Nkv, max_q, span, tiles;  // tiles: items of the longest sequence
+  int n_whole, n_split, split_k, rows;             // rows: of an item in the workspace
+  float scale_log2;
+  long long q_stride, k_stride, v_stride;
+  const int32_t *cu_q, *cu_kv, *kv_lens, *ranges;
+  const void *q, *k, *v;
+  void* out;
+  float* lse;  // or null
+  float *ws_out, *ws_lse;
+  int32_t* err;
+};
+
+struct CrossItem {
+  int b, g, t0, tokens;  // the sequence, the kv head, its first token and how many there are (0: nothing to do)
+  int q0, kv0, keys;     // first rows in q and k, v; keys of the sequence
+};
+// reporter: one thread of the item's first CTA, which says what is wrong with the sequence.
+CP_DEV CrossItem cross_item(const CrossParams& p, unsigned index, bool reporter) {
+  CrossItem w;
+  const unsigned tile = index % (unsigned)p.tiles, u = index / (unsigned)p.tiles;
+  w.g = (int)(u % (unsigned)p.Hkv);
+  w.b = (int)(u / (unsigned)p.Hkv);
+  w.t0 = (int)tile * p.span;
+  w.q0 = ld(p.cu_q + w.b);
+  w.kv0 = ld(p.cu_kv + w.b);
+  const long long Tq = (long long)ld(p.cu_q + w.b + 1) - w.q0, Tkv = (long long)ld(p.cu_kv + w.b + 1) - w.kv0;
+  reporter = reporter && tile == 0 && w.g == 0;
+  w.keys = (int)Tkv;
+  if (p.kv_lens != nullptr) {
+    const int n = ld(p.kv_lens + w.b);
+    if (reporter && (n < 0 || n > Tkv)) report(p.err, CP_ERR_DEVICE_BOUNDS);
+    w.keys = (int)max(0ll, min((long long)n, Tkv));
+  }
+  const bool bad = Tq < 0 || Tkv < 0 || w.q0 < 0 || w.kv0 < 0 || w.q0 + Tq > p.Nq || w.kv0 + Tkv > p.Nkv;
+  if (reporter && (bad || Tq > p.max_q)) report(p.err, CP_ERR_DEVICE_BOUNDS);
+  const long long here = min(Tq, (long long)p.max_q);
+  w.tokens = bad ? 0 : (int)max(0ll, min((long long)p.span, here - w.t0));
+  return w;
+}
+// The keys [lo, hi) of a token (within the sequence).
+CP_DEV void cross_range(const CrossParams& p, const CrossItem& w, int token, int& lo, int& hi) {
+  lo = 0, hi = w.keys;
+  if (p.ranges != nullptr) {
+    const int32_t* r = p.ranges + 2ll * (w.q0 + token);
+    lo = max(0, ld(r));
+    hi = min(w.keys, ld(r + 1));
+    if (lo >= hi) lo = hi = 0;
+  }
+}
+
+// Parts -> rows: out = sum_k e_k out_k / sum_k e_k with e_k = exp(lse_k - max lse); a part without a key has the
+// LSE -inf and its row is not read.  A warp takes a row, its lanes the dims.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_merge_kernel(const CrossParams p) {
+  constexpr int E = D / 32;
+  chained_start();
+  const CrossItem w = cross_item(p, (unsigned)p.n_whole + blockIdx.x, false);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long part0 = (long long)blockIdx.x * p.split_k;
+  for (int row = (int)blockIdx.y * 8 + warp; row < w.tokens * p.G; row += (int)gridDim.y * 8) {
+    float M = -INFINITY;
+    float x[4];  // LSEs in log2 units, 32 parts at a time across the lanes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = lane + 32 * i;
+      x[i] = k < p.split_k ? p.ws_lse[(part0 + k) * p.rows + row] * kLog2e : -INFINITY;
+      M = fmaxf(M, x[i]);
+    }
+    M = warp_max(M);
+    float sum = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= p.split_k) break;
+      const float mine = x[i] == -INFINITY ? 0.f : exp2f(x[i] - (M == -INFINITY ? 0.f : M));  // NaN stays
+      const int n = min(32, p.split_k - 32 * i);
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float e = __shfl_sync(0xffffffffu, mine, j);
+        if (e == 0.f) continue;
+        const float* src = p.ws_out + ((part0 + 32 * i + j) * p.rows + row) * D + lane * E;
+        sum += e;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          acc[0] += e * v.x, acc[1] += e * v.y, acc[2] += e * v.z, acc[3] += e * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] += e * v.x, acc[1] += e * v.y;
+        }
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long o = ((long long)w.q0 + w.t0 + row / p.G) * p.Hq + w.g * p.G + row % p.G;
+    T* dst = static_cast<T*>(p.out) + o * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if constexpr (sizeof(T) == 2) dst[e] = __float2bfloat16_rn(acc[e] * inv);
+      else dst[e] = acc[e] * inv;
+    }
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[o] = sum == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(sum)) * kLn2;
+  }
+}
+constexpr int kMaxParts = 128;
+
+template <typename T, int D>
+cudaError_t launch_merge(const CrossParams& p, cudaStream_t s) {
+  // eight rows a CTA until there are plenty
+  int y = (p.rows + 7) / 8;
+  while (y > 1 && (long long)p.n_split * y > 2048) y = (y + 1) / 2;
+  return launch_chained(cross_merge_kernel<T, D>, dim3((unsigned)p.n_split, (unsigned)y), 256, 0, s, p);
+}
+
+}  // namespace
+}  // namespace cpattn
+
+// How a launch is made of items and parts (host).
+struct CrossPlan {
+  int span, tiles, rows;
+  long long items, n_split;
+  int split_k;
+  size_t bytes;
+};
+CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms);
+CrossPlan cp_cross_plan_few(const cp_cross_args& a, int sms);
+cudaError_t cp_launch_cross_tc(const cp_cross_args& a, float scale, void* ws, size_t ws_bytes, void* out, float* lse,
+                               cudaStream_t s);
+cudaError_t cp_launch_cross_few(const cp_cross_args& a, float scale, void* ws, size_t ws_bytes, void* out, float* lse,
+                                cudaStream_t s);
+inline void cp_cross_fill(cpattn::CrossParams& p, const cp_cross_args& a, const CrossPlan& plan, float scale, void* ws,
+                          size_t ws_bytes, void* out, float* lse) {
+  p.B = a.num_seqs;
+  p.Hq = a.num_q_heads;
+  p.Hkv = a.num_kv_heads;
+  p.G = a.num_q_heads / a.num_kv_heads;
+  p.Nq = a.total_q;
+  p.Nkv = a.total_kv;
+  p.max_q = a.max_seqlen_q;
+  p.span = plan.span;
+  p.tiles = plan.tiles;
+  p.rows = plan.rows;
+  p.scale_log2 = scale * cpattn::kLog2e;
+  p.q_stride = a.q_stride;
+  p.k_stride = a.k_stride;
+  p.v_stride = a.v_stride;
+  p.cu_q = a.cu_seqlens_q;
+  p.cu_kv = a.cu_seqlens_kv;
+  p.kv_lens = a.kv_lens;
+  p.ranges = a.key_ranges;
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.out = out;
+  p.lse = lse;
+  p.err = a.err;
+  const bool cut = plan.split_k > 1 && ws != nullptr && ws_bytes >= plan.bytes;
+  p.n_split = cut ? (int)plan.n_split : 0;
+  p.n_whole = (int)(plan.items - p.n_split);
+  p.split_k = cut ? plan.split_k : 1;
+  p.ws_out = static_cast<float*>(ws);
+  p.ws_lse = cut ? p.ws_out + (size_t)plan.n_split * plan.split_k * plan.rows * a.head_dim : nullptr;
+}
+inline size_t cp_cross_parts_bytes(const CrossPlan& plan, int D) {
+  return plan.split_k > 1 ? (size_t)plan.n_split * plan.split_k * plan.rows * (D + 1) * sizeof(float) : 0;
+}

@@ -566,12 +566,152 @@ cp_status cp_partial_attn_decode_q4(const cp_decode_args* args, const cp_score_m
 cp_status cp_decode_attention_q4(const cp_decode_args* args, const cp_score_mod* mod, void* workspace,
                                  size_t workspace_bytes, void* out, float* out_lse, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * cp_cross_attention -- attention of decoder tokens over an encoder's states, whose number has nothing to do
+ * with theirs (no counterpart on the pages, whose attention is causal self-attention).
+ *
+ * Query row i of sequence b (rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 of q) attends the keys j of the
+ * sequence (rows cu_seqlens_kv[b] + j of k and v) with j in [lo, hi):
+ *   n = cu_seqlens_kv[b+1] - cu_seqlens_kv[b], or kv_lens[b] if given (a padded batch);
+ *   [lo, hi) = [0, n), or [max(0, key_ranges[i][0]), min(n, key_ranges[i][1])) if given (i: token-major row);
+ *   out_i = sum_j softmax_j(softmax_scale q_i.k_j) v_j.
+ * A row without a key gives output 0 and LSE -inf.  Keys a row does not see do not touch it, whatever they
+ * hold.  A decode step has one row for each beam: the beams of one source are the rows of one sequence, and
+ * its states are read once for all of them.
+ *   - q, k and v may be rows of a wider tensor (a projection's columns): row t starts `*_stride` elements
+ *     after row t - 1; the strides in bytes are multiples of 16.
+ *   - rows from cu_seqlens_q[B] on are left as they are.
+ *   - workspace: device scratch, 256-byte aligned, of cp_cross_attention_workspace_size() bytes, for cutting
+ *     the keys of long or few items into parts that run at once (0 bytes: not done for these sizes).  NULL or a
+ *     smaller one cuts nothing (the same results up to rounding).  No initialisation is needed; calls that
+ *     use one workspace must not overlap.
+ *   - err: CP_ERR_DEVICE_BOUNDS for a sequence whose rows go past total_q or total_kv or have negative lengths
+ *     (skipped), with more rows than max_seqlen_q (the rest is left out), or with kv_lens[b] outside
+ *     [0, its rows] (taken as the nearest of the two).  max_seqlen_kv only guides the cut: any value is right.
+ * Weights and values are summed before they are divided: finite components of v are below 2^96.
+ * bf16: P is rounded to bf16 for the tensor cores; num_q_heads / num_kv_heads <= 128.  f32: all in fp32, <= 16.
+ * ---------------------------------------------------------------------------- */
+typedef struct cp_cross_args {
+  int32_t dtype;                /* cp_dtype of q, k, v, out                             */
+  int32_t num_seqs;             /* B >= 1                                               */
+  int32_t num_q_heads;          /* Hq, multiple of num_kv_heads                         */
+  int32_t num_kv_heads;         /* Hkv                                                  */
+  int32_t head_dim;             /* d in {64, 128}                                       */
+  int32_t max_seqlen_q;         /* host: most query rows of a sequence                  */
+  int32_t max_seqlen_kv;        /* host: most keys of a sequence (guides the cut only)  */
+  int32_t total_q;              /* rows of q, out, out_lse                              */
+  int32_t total_kv;             /* rows of k, v                                         */
+  float softmax_scale;          /* <= 0 selects 1/sqrt(head_dim)                        */
+  int64_t q_stride, k_stride, v_stride;  /* elements between rows                       */
+  const void* q;                /* device [total_q][Hq][d]                              */
+  const void* k;                /* device [total_kv][Hkv][d]                            */
+  const void* v;                /* device [total_kv][Hkv][d]                            */
+  const int32_t* cu_seqlens_q;  /* device [B+1]                                         */
+  const int32_t* cu_seqlens_kv; /* device [B+1]                                         */
+  const int32_t* kv_lens;       /* device [B] or NULL                                   */
+  const int32_t* key_ranges;    /* device [total_q][2] or NULL                          */
+  int32_t* err;                 /* device int32 or NULL                                 */
+} cp_cross_args;
+
+cp_status cp_cross_attention_workspace_size(const cp_cross_args* args, size_t* bytes);
+/* out: device [total_q][Hq][d] of dtype; out_lse: device f32 [total_q][Hq] (natural log) or NULL. */
+cp_status cp_cross_attention(const cp_cross_args* args, void* workspace, size_t workspace_bytes, void* out,
+                             float* out_lse, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * cp_beam_select -- the best continuations of each sequence's beams (no counterpart on the pages).
+ *
+ * Continuation (k, v) of a sequence is its beam k followed by token v, with the score
+ *   scores[b][k] + logits[b][k][v] - log sum_u exp(logits[b][k][u]).
+ * cand_*[b] are the num_candidates best in falling order; of equal scores the lower k * vocab + v comes first.
+ * next_*[b] are the first num_beams of them whose token is not eos_token (< 0: any token): the beams that go on.
+ *   - a logit of -inf (a banned token) or NaN has the score -inf; logits of +inf share their beam's
+ *     probability; a beam without a token, or with the score -inf or NaN, has scores of -inf only.
+ *   - K = num_beams in 1 .. 32; num_candidates in K .. 64, at least 2 K with an eos_token, at most K * vocab.
+ *   - logits: rows of `vocab` elements, row b K + k starting logits_stride elements after the one before
+ *     (any alignment of the type's own).
+ *   - workspace: cp_beam_select_workspace_size() bytes, 256-byte aligned, zero-filled before its first use
+ *     and left reusable, also for other sizes and for the fused decodes; calls that use one workspace must not
+ *     overlap.  num_seqs <= 65536.
+ * Sums are fp32; scores are compared in 64 bits and rounded once.  The result does not depend on the order in
+ * which the GPU's blocks run.
+ * ---------------------------------------------------------------------------- */
+typedef struct cp_beam_select_args {
+  int32_t dtype;                /* cp_dtype of logits                                   */
+  int32_t num_seqs;             /* B                                                    */
+  int32_t num_beams;            /* K                                                    */
+  int32_t vocab;                /* tokens                                               */
+  int32_t num_candidates;       /* M                                                    */
+  int32_t eos_token;            /* < 0: none                                            */
+  int64_t logits_stride;        /* elements between rows, >= vocab                      */
+  const void* logits;           /* device [B K][vocab]                                  */
+  const float* scores;          /* device [B][K]                                        */
+  float* next_scores;           /* device [B][K]                                        */
+  int32_t* next_beams;          /* device [B][K]: the beam that each one continues      */
+  int32_t* next_tokens;         /* device [B][K]                                        */
+  float* cand_scores;           /* device [B][M]                                        */
+  int32_t* cand_beams;          /* device [B][M]                                        */
+  int32_t* cand_tokens;         /* device [B][M]                                        */
+} cp_beam_select_args;
+
+cp_status cp_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab,
+                                        int32_t num_candidates, size_t* bytes);
+cp_status cp_beam_select(const cp_beam_select_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * cp_beam_reorder -- the paged round-robin caches follow the selection ([PCP] Purpose: per-rank block tables).
+ *
+ * Beam j of sequence b, row b K + j of the tables, goes on from beam parents[b][j] of the same sequence.  All
+ * beams of b have seq_lens[b] cached tokens, of which rank r holds L_r (see cp_kv_interleave_layout).  Full pages
+ * never change, so they are shared: columns c < L_r / 16 of the new table take the parent's entries.  Column
+ * c = L_r / 16, the page being filled, becomes the beam's own page own_pages[r][b K + j][c], into which the
+ * L_r mod 16 rows of the parent's page are copied (nothing where that is the same page); the next tokens of the
+ * beam are then appended to a page of its own.  Further columns are left as they are.
+ *   - own_pages: a page of each rank's pool for each beam and column that it may come to fill, in no other
+ *     row or column, and none of another sequence's; columns that lie within a prompt are not read.
+ *   - every source row is read before any page is written, so parents may be any (a permutation, one for all).
+ *   - tables_out may be tables_in (replaced in place) or must not overlap it.  k_cache and v_cache may be NULL
+ *     (tables only); num_layers pools may lie one behind the other.
+ *   - err: CP_ERR_DEVICE_BOUNDS for a parent outside [0, K) (that beam is left as it is), a page outside the
+ *     pool (not copied; a column whose own page is bad keeps the parent's) or a length that the tables do not
+ *     hold (the sequence is left as it is).
+ * A pure copy: bit-exact; rows of a page from L_r mod 16 on are left as they are.
+ * ---------------------------------------------------------------------------- */
+typedef struct cp_beam_reorder_args {
+  int32_t dtype;                /* cp_dtype of the caches (ignored with cache_q4)       */
+  int32_t cache_q4;             /* 1: the caches are 4-bit records                      */
+  int32_t num_layers;           /* pools one behind the other, >= 1                     */
+  int32_t num_seqs;             /* B                                                    */
+  int32_t num_beams;            /* K in 1 .. 32                                         */
+  int32_t num_kv_heads;         /* Hkv                                                  */
+  int32_t head_dim;             /* d in {64, 128}                                       */
+  int32_t cp;                   /* logical ranks, 1..64                                 */
+  int32_t interleave;           /* I >= 1                                               */
+  int32_t block_size;           /* 16                                                   */
+  int32_t max_blocks;           /* columns of the tables                                */
+  int32_t reserved;             /* 0                                                    */
+  int64_t pool_pages;           /* pages in each rank's pool                            */
+  const int32_t* parents;       /* device [B][K]                                        */
+  const int32_t* seq_lens;      /* device [B] tokens in the cache                       */
+  const int32_t* tables_in;     /* device [cp][B K][max_blocks]                         */
+  const int32_t* own_pages;     /* device [cp][B K][max_blocks]                         */
+  int32_t* tables_out;          /* device [cp][B K][max_blocks]                         */
+  void* k_cache;                /* device [layers][cp][pool_pages][Hkv][16][d], or 4-bit records, or NULL */
+  void* v_cache;
+  int32_t* err;                 /* device int32 or NULL                                 */
+} cp_beam_reorder_args;
+
+cp_status cp_beam_reorder(const cp_beam_reorder_args* args, void* stream);
+
 /* sizeof() of the argument structs, so bindings can check their mirror. */
 size_t cp_prefill_args_size(void);
 size_t cp_decode_args_size(void);
 size_t cp_rope_write_args_size(void);
 size_t cp_kv_read_args_size(void);
 size_t cp_score_mod_size(void);
+size_t cp_cross_args_size(void);
+size_t cp_beam_select_args_size(void);
+size_t cp_beam_reorder_args_size(void);
 
 #ifdef __cplusplus
 }
