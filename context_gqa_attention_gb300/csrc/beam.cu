@@ -10,29 +10,37 @@ namespace {
 // ================================================================================ selection
 //   score(k, v) = scores[k] + x[k][v] - log sum_u exp(x[k][u])
 //
-// One pass over the logits.  A row is cut into slices; a CTA holds one in registers (up to eight 16-byte
-// vectors a thread, all in flight at once), takes its largest value and its sum of exp(x - largest), and keeps its
-// num_candidates largest values: every one of the M best continuations of a beam is among them.  The CTA that
-// finishes a sequence's last slice turns slices into beams and beams into the result.
+// One pass over the logits.  A row is cut into chunks, one a CTA (one a row when there are rows for the whole GPU).
+// A CTA streams its chunk through registers, the next vectors on their way while these are worked on, sums
+// exp(x - reference) and keeps what may be among its num_candidates largest values: every one of the M best
+// continuations of a beam is among those.  The CTA that finishes a sequence's last chunk turns chunks into beams and
+// beams into the result.
 //
-// The M largest of many, without sorting: each warp finds the w-th largest of its lanes' maxima, w = ceil(M / 8);
-// the least of the eight warps' is a bound that at least M values reach, and few more do (about 3 M of random
-// ones), so only those are compared with one another.  Where too many reach it (equal values), the M are taken
-// one after the other.
+// The M largest of many, without sorting: a lane knows the largest value it has met.  The w-th largest of a warp's 32
+// is a number that w values of the warp reach, so with w = ceil(M / 8) the least of the eight warps' is one that at least
+// M values reach.  Vectors below it are passed over; the others (about 30 in the first 16 KB, then ever fewer, as the
+// bound rises with the chunk) go to a list, and at the end those of their values that reach the last bound are
+// compared with one another.  Only the first bound takes a barrier: an older one is as valid.
+// A list that overflows (rising or equal values) is made again with the last bound, and if that fails too the M are
+// taken one after the other.
 //
-// Bound: HBM.  An element costs about six instructions (unpacking, maximum, packed difference, exponential, sum), which
-// eight resident warps a sub-partition keep below the time of its load.
+// Bound: HBM.  An element costs about five instructions (unpacking, maximum, packed difference and product,
+// exponential, sum), half of what the SM could issue in the time of its load.
 constexpr int kThreads = 256, kWarps = 8;
+constexpr int kVecs = 512;            // vectors that a chunk's values are taken from
 constexpr int kList = 1024;           // values that a CTA compares with one another
 constexpr int kMaxBeams = 32, kMaxCandidates = 64;
+constexpr float kMaxGrowth = 16.f;    // a lane's values may exceed what its sum is relative to
+constexpr float kMaxLogit = 1e5f;     // beyond, the rounding of log2(e) times a logit is too coarse for one pass
+constexpr float kMost = 3.402823466e38f;  // the largest finite value
 
 struct SelectParams {
-  int K, V, M, S, eos;
+  int K, V, M, S, chunk, eos;  // S: chunks of a row, chunk: their 16-byte vectors
   long long stride;  // elements between rows
   const void* logits;
   const float* scores;
   int32_t* counters;  // [B], zero between calls
-  float2* stats;      // [B K][S] largest value and sum
+  float2* stats;      // [B K][S] largest value, sum of exp(x - largest)
   uint2* best;        // [B K][S][M] value, token (-1: none)
   float *next_score, *cand_score;
   int32_t *next_beam, *next_token, *cand_beam, *cand_token;
@@ -44,14 +52,6 @@ CP_DEV uint32_t order32(float x) {
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 CP_DEV float value32(uint32_t k) { return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u)); }
-CP_DEV unsigned long long order64(double x) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
-  return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
-}
-CP_DEV double value64(unsigned long long k) {
-  return __longlong_as_double((long long)(k ^ ((unsigned long long)((long long)~k >> 63) | 0x8000000000000000ull)));
-}
-
 // The w-th largest of the lanes' keys (equal ones count as often as they come).
 CP_DEV uint32_t wth_largest(uint32_t key, int w, uint32_t& largest) {
   const uint32_t lane = threadIdx.x & 31;
@@ -63,8 +63,9 @@ CP_DEV uint32_t wth_largest(uint32_t key, int w, uint32_t& largest) {
   return cur;
 }
 
-// A 16-byte vector of logits as it was loaded, and its elements.  pin: what was made of it before is not kept in
-// registers for later (a slice's unpacked values are twice its size: 1 KB of spills a thread).
+CP_DEV float to_float(float x) { return x; }
+CP_DEV float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+// A 16-byte vector of logits as it was loaded, and its elements.
 template <typename T>
 struct Vec;
 template <>
@@ -83,7 +84,9 @@ struct Vec<float> {
   }
   CP_DEV float get(int i) const { return x[i]; }
   CP_DEV float max() const { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])); }  // (a NaN is passed over)
-  CP_DEV void pin() { asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3])); }
+  CP_DEV uint4 raw() const {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
 };
 template <>
 struct Vec<__nv_bfloat16> {
@@ -106,7 +109,7 @@ struct Vec<__nv_bfloat16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(pair(x[0]), pair(x[1])), __hmax2(pair(x[2]), pair(x[3])));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  CP_DEV void pin() { asm volatile("" : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3])); }
+  CP_DEV uint4 raw() const { return make_uint4(x[0], x[1], x[2], x[3]); }
 };
 
 CP_DEV float ex2_approx(float x) {
@@ -114,21 +117,17 @@ CP_DEV float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// exp(x - top) of a pair, added to sum (packed fp32).  The difference comes first: a logit's own size stays out of it.
-CP_DEV void add_exp2(uint64_t& sum, float x, float y, uint64_t minus_top) {
-  const float e = kLog2e;
-  uint64_t v, w;
+// 2^(x log2(e) - c) of a pair, added to sum (packed fp32).
+CP_DEV void add_exp2(uint64_t& sum, float x, float y, uint64_t log2e, uint64_t minus_c) {
+  uint64_t v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(e));
-  asm("add.f32x2 %0, %0, %1;" : "+l"(v) : "l"(minus_top));
-  asm("mul.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(log2e), "l"(minus_c));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
   x = ex2_approx(x);
   y = ex2_approx(y);
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
   asm("add.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(v));
 }
-
 // The block's sum, the same for every thread.
 CP_DEV float block_sum(float x, float* s_warp) {
   x = warp_sum(x);
@@ -157,127 +156,201 @@ CP_DEV void block_best(unsigned long long& key, unsigned long long& at, unsigned
   for (int w = 0; w < kWarps; ++w) take(s_key[w], s_at[w]);
 }
 
-// log2 of a positive sum: its exponent apart, so that the logarithm's rounding is that of a number below 0.6.
-CP_DEV double log2_split(float s) {
-  const int e = (int)((__float_as_uint(s) + 0x004afb0du) >> 23) - 127;  // s / 2^e in about [0.71, 1.42)
-  return (double)e + (double)log2f(ldexpf(s, -e));
+// A number as the sum of two fp32, the first of them the rounded sum: 48 bits, in fp32 arithmetic (Knuth's and Dekker's
+// exact sums), since fp64 is slow here.  Scores of different beams are compared in it.
+struct Pair {
+  float hi, lo;
+};
+CP_DEV Pair exact_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
 }
-constexpr double kLn2d = 0.69314718055994530942;
+CP_DEV Pair add(Pair a, Pair b) {
+  const Pair s = exact_sum(a.hi, b.hi);
+  const float e = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, e);
+  return {hi, fabsf(hi) <= kMost ? __fsub_rn(e, __fsub_rn(hi, s.hi)) : 0.f};
+}
+CP_DEV unsigned long long order_pair(Pair x) { return ((unsigned long long)order32(x.hi) << 32) | order32(x.lo); }
+// -log of a positive sum: the exponent apart, ln 2 in two parts of which the first has 15 bits (its products are exact),
+// so that the roundings are those of numbers below 0.5.
+CP_DEV Pair minus_log(float s) {
+  const int e = (int)((__float_as_uint(s) + 0x004afb0du) >> 23) - 127;  // s / 2^e in about [0.71, 1.42)
+  const float n = (float)e, l = logf(__uint_as_float(__float_as_uint(s) - ((uint32_t)e << 23)));
+  return exact_sum(-n * 0.693145751953125f, -fmaf(n, 1.42860682030941723e-6f, l));
+}
 
 struct SelectShared {
-  unsigned long long key[kList], at[kList];
+  uint4 vec[kVecs];  // of the chunk; then places [kList] of a sequence's candidates
+  unsigned long long key[kList];
+  int id[kVecs], rank[kList];
   unsigned long long w_key[kWarps], w_at[kWarps];
-  double base[kMaxBeams];  // score of the beam's largest logit
-  float top[kMaxBeams];    // that logit
   unsigned long long top_key[kMaxCandidates], top_at[kMaxCandidates];
-  uint32_t w_max[kWarps], w_th[kWarps];
+  Pair base[kMaxBeams];  // score of the beam's largest logit
+  float top[kMaxBeams];  // that logit
+  uint32_t w_max[kWarps];
+  alignas(16) uint32_t w_th[kWarps];
   float w_sum[kWarps];
-  int n, last;
-  unsigned char full[kMaxBeams], taken[kMaxCandidates];
+  int n, n2, last;
+  unsigned char taken[kMaxCandidates];
+  // what each warp publishes, as of now: the least of them
+  CP_DEV uint32_t bound() const {
+    uint32_t k[kWarps];
+    const uint32_t a = (uint32_t)__cvta_generic_to_shared(w_th);
+#pragma unroll
+    for (int i = 0; i < kWarps; i += 4)
+      asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(k[i]), "=r"(k[i + 1]), "=r"(k[i + 2]), "=r"(k[i + 3]) : "r"(a + 4u * i) : "memory");
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) k[0] = min(k[0], k[i]);
+    return k[0];
+  }
+  CP_DEV unsigned long long* at() { return reinterpret_cast<unsigned long long*>(vec); }
 };
+static_assert(sizeof(uint4) * kVecs >= sizeof(unsigned long long) * kList, "places");
 
-// The M best of a sequence, from its slices' sums and values, and the result.
+// rank[i]: how many of the list's n entries come before entry i (which starts at 0).  Four threads an entry.
+template <bool PLACES>
+CP_DEV void count_before(SelectShared& sh, int n) {
+  const int per = (n + 3) / 4, j0 = ((int)threadIdx.x >> 6) * per, j1 = min(n, j0 + per);
+#pragma unroll 1
+  for (int i = threadIdx.x & 63; i < n; i += 64) {
+    const unsigned long long key = sh.key[i], at = PLACES ? sh.at()[i] : 0ull;
+    int r = 0;
+#pragma unroll 4
+    for (int j = j0; j < j1; ++j)
+      r += sh.key[j] > key || (PLACES && sh.key[j] == key && sh.at()[j] < at);
+    if (r > 0) atomicAdd(&sh.rank[i], r);
+  }
+  __syncthreads();
+}
+
+// One of a sequence's candidates as (score, place), which order them; false: it has no probability.
+CP_DEV bool candidate(const SelectShared& sh, uint2 e, int k, unsigned long long& key, unsigned long long& at) {
+  const Pair base = sh.base[k];
+  const float x = __uint_as_float(e.x), top = sh.top[k];
+  const Pair score = top == INFINITY ? base : add(base, exact_sum(x, -top));
+  key = order_pair(score);
+  at = ((unsigned long long)k << 32) | e.y;
+  return (int32_t)e.y >= 0 && base.hi > -INFINITY && score.hi > -INFINITY && (top < INFINITY || x == INFINITY);
+}
+// Many equal scores: the M best one after the other.
+__device__ __noinline__ void slow_finish(const uint2* best, int n_all, int per, int M, SelectShared& sh) {
+  unsigned long long last_key = ~0ull, last_at = 0;
+  for (int r = 0; r < M; ++r) {
+    unsigned long long key = 0, at = ~0ull;
+    for (int i = threadIdx.x; i < n_all; i += kThreads) {
+      unsigned long long k, a;
+      if (!candidate(sh, __ldcg(best + i), i / per, k, a)) continue;
+      if ((k < last_key || (k == last_key && a > last_at)) && (k > key || (k == key && a < at))) key = k, at = a;
+    }
+    block_best(key, at, sh.w_key, sh.w_at);
+    if (threadIdx.x == 0) sh.top_key[r] = key, sh.top_at[r] = at;
+    last_key = key, last_at = at;
+  }
+}
+// Fewer than M with a probability: the rest are the first of the others, of score -inf.
+__device__ __noinline__ void fill_up(int n, int M, int V, SelectShared& sh) {
+  const int tid = threadIdx.x;
+  if (tid < kMaxCandidates) sh.taken[tid] = 0;
+  __syncthreads();
+  if (tid < n) {
+    const unsigned long long flat = (sh.top_at[tid] >> 32) * (unsigned)V + (uint32_t)sh.top_at[tid];
+    if (flat < kMaxCandidates) sh.taken[flat] = 1;
+  }
+  __syncthreads();
+  if (tid == 0)
+    for (int r = n, f = 0; r < M; ++f)
+      if (!sh.taken[f]) {
+        sh.top_key[r] = order_pair({-INFINITY, 0.f});
+        sh.top_at[r] = ((unsigned long long)(f / V) << 32) | (unsigned)(f % V);
+        ++r;
+      }
+}
+
+// The M best of a sequence, from its chunks' sums and values, and the result.
 CP_DEV void finish_sequence(const SelectParams& p, SelectShared& sh, int b) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // ---- beams: largest logit and its score.  full: some logit is +inf, and the probability lies on those alone.
+  const int per = p.S * p.M, n_all = p.K * per;
+  const uint2* best = p.best + (long long)b * n_all;
+  const int i0 = lane * kWarps + warp;  // (every warp has its share of a few candidates)
+  const uint2 e0 = i0 < n_all ? __ldcg(best + i0) : make_uint2(0u, 0xffffffffu);  // on its way meanwhile
+  // ---- beams: largest logit and its score.  Where that logit is +inf, the probability lies on those alone.
+#pragma unroll 1
   for (int k = warp; k < p.K; k += kWarps) {
     const long long row = (long long)b * p.K + k;
     const float2* st = p.stats + row * p.S;
-    float top = -INFINITY, sum = 0.f;
-    for (int s = lane; s < p.S; s += 32) top = fmaxf(top, __ldcg(&st[s]).x);
-    top = warp_max(top);
+    const float from = ld(p.scores + row);
+    float top = -INFINITY, sum = 0.f;  // of the lane's chunks, then of all
+#pragma unroll 1
     for (int s = lane; s < p.S; s += 32) {
-      const float2 x = __ldcg(&st[s]);
-      if (x.x > -INFINITY) sum += x.y * (x.x == top ? 1.f : exp2f((x.x - top) * kLog2e));
+      const float2 x = __ldcg(st + s);
+      if (x.x > -INFINITY) {
+        const float m = fmaxf(top, x.x);
+        sum = (top == m ? sum : sum * exp2f((top - m) * kLog2e)) + (x.x == m ? x.y : x.y * exp2f((x.x - m) * kLog2e));
+        top = m;
+      }
     }
-    sum = warp_sum(sum);
+    const float most = warp_max(top);
+    sum = warp_sum(top == most ? sum : sum * exp2f((top - most) * kLog2e));
     if (lane == 0) {
-      const float from = ld(p.scores + row);
-      sh.full[k] = top == INFINITY;
-      sh.top[k] = top;
-      sh.base[k] = sum > 0.f && from > -INFINITY ? (double)from - kLn2d * log2_split(sum) : -INFINITY;
+      sh.top[k] = most;
+      sh.base[k] = sum > 0.f && from > -INFINITY ? add({from, 0.f}, minus_log(sum)) : Pair{-INFINITY, 0.f};
     }
   }
   if (tid == 0) sh.n = 0;
   __syncthreads();
-  // ---- continuations in the order of (score, lower beam and token first)
-  const int per = p.S * p.M, n_all = p.K * per;
-  const uint2* best = p.best + (long long)b * n_all;
-  auto entry = [&](int i, unsigned long long& key, unsigned long long& at) -> bool {  // false: no probability
-    const uint2 e = __ldcg(best + i);
-    const int k = i / per;
-    const double base = sh.base[k];
-    const float x = __uint_as_float(e.x);
-    if ((int32_t)e.y < 0 || base == -INFINITY || (sh.full[k] && x != INFINITY)) return false;
-    key = order64(sh.full[k] ? base : base + ((double)x - (double)sh.top[k]));
-    at = (unsigned long long)k * (unsigned)p.V + e.y;
-    return true;
-  };
-  uint32_t mine = 0;
-  for (int i = tid; i < n_all; i += kThreads) {
-    unsigned long long key, at;
-    if (entry(i, key, at)) mine = max(mine, (uint32_t)(key >> 32));
-  }
-  uint32_t largest;
-  const uint32_t wth = wth_largest(mine, (p.M + kWarps - 1) / kWarps, largest);
-  if (lane == 0) sh.w_th[warp] = wth;
-  __syncthreads();
-  uint32_t bound = 0xffffffffu;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) bound = min(bound, sh.w_th[w]);
-  for (int i = tid; i < n_all; i += kThreads) {
-    unsigned long long key, at;
-    if (entry(i, key, at) && (uint32_t)(key >> 32) >= bound) {
+  // ---- candidates: a score that at least M reach, and those that reach it
+  unsigned long long key0, at0;
+  const bool real0 = candidate(sh, e0, min(i0 / per, p.K - 1), key0, at0);
+  unsigned long long* place = sh.at();
+  uint32_t mine = real0 ? (uint32_t)(key0 >> 32) : 0u, bound = 0u;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    auto take = [&](unsigned long long key, unsigned long long at) {
       const int j = atomicAdd(&sh.n, 1);
-      if (j < kList) sh.key[j] = key, sh.at[j] = at;
+      if (j < kList) sh.key[j] = key, place[j] = at, sh.rank[j] = 0;
+    };
+    if (pass == 1 && real0 && (uint32_t)(key0 >> 32) >= bound) take(key0, at0);
+#pragma unroll 1
+    for (int i = i0 + kThreads; i < n_all; i += kThreads) {
+      unsigned long long key, at;
+      if (!candidate(sh, __ldcg(best + i), i / per, key, at)) continue;
+      if (pass == 0) mine = max(mine, (uint32_t)(key >> 32));
+      else if ((uint32_t)(key >> 32) >= bound) take(key, at);
     }
+    if (pass == 1) break;
+    uint32_t largest;
+    const uint32_t wth = wth_largest(mine, (p.M + kWarps - 1) / kWarps, largest);
+    if (lane == 0) sh.w_th[warp] = wth;
+    __syncthreads();
+    bound = sh.bound();
   }
   __syncthreads();
   int n = sh.n;
-  if (n <= kList) {
-    for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long key = sh.key[i], at = sh.at[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += sh.key[j] > key || (sh.key[j] == key && sh.at[j] < at);
-      if (rank < p.M) sh.top_key[rank] = key, sh.top_at[rank] = at;
-    }
+  if (n > kList) {
+    slow_finish(best, n_all, per, n = p.M, sh);
+  } else {
+    count_before<true>(sh, n);
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads)
+      if (sh.rank[i] < p.M) sh.top_key[sh.rank[i]] = sh.key[i], sh.top_at[sh.rank[i]] = place[i];
     n = min(n, p.M);
-  } else {  // many equal scores: one after the other
-    unsigned long long last_key = ~0ull, last_at = 0;
-    n = p.M;
-    for (int r = 0; r < p.M; ++r) {
-      unsigned long long key = 0, at = ~0ull;
-      for (int i = tid; i < n_all; i += kThreads) {
-        unsigned long long k, a;
-        if (!entry(i, k, a)) continue;
-        if ((k < last_key || (k == last_key && a > last_at)) && (k > key || (k == key && a < at))) key = k, at = a;
-      }
-      block_best(key, at, sh.w_key, sh.w_at);
-      if (tid == 0) sh.top_key[r] = key, sh.top_at[r] = at;
-      last_key = key, last_at = at;
-    }
   }
   __syncthreads();
-  // ---- fewer than M with a probability: the rest are the first of the others, of score -inf
   if (n < p.M) {
-    if (tid < kMaxCandidates) sh.taken[tid] = 0;
-    __syncthreads();
-    if (tid < n && sh.top_at[tid] < kMaxCandidates) sh.taken[sh.top_at[tid]] = 1;
-    __syncthreads();
-    if (tid == 0)
-      for (int r = n, f = 0; r < p.M; ++f)
-        if (!sh.taken[f]) sh.top_key[r] = order64(-INFINITY), sh.top_at[r] = (unsigned long long)f, ++r;
+    fill_up(n, p.M, p.V, sh);
     __syncthreads();
   }
   // ---- all M, and the first K that go on
   if (warp == 0) {
     int on = 0;
+#pragma unroll 1
     for (int r0 = 0; r0 < p.M; r0 += 32) {
       const int r = r0 + lane;
       const bool real = r < p.M;
       const unsigned long long at = real ? sh.top_at[r] : 0ull;
-      const int beam = (int)(at / (unsigned)p.V), token = (int)(at % (unsigned)p.V);
-      const float score = real ? (float)value64(sh.top_key[r]) : 0.f;
+      const int beam = (int)(at >> 32), token = (int)(uint32_t)at;
+      const float score = real ? value32((uint32_t)(sh.top_key[r] >> 32)) : 0.f;
       if (real) {
         const long long o = (long long)b * p.M + r;
         p.cand_score[o] = score, p.cand_beam[o] = beam, p.cand_token[o] = token;
@@ -294,135 +367,259 @@ CP_DEV void finish_sequence(const SelectParams& p, SelectShared& sh, int b) {
   }
 }
 
-// NV: vectors a thread holds; a slice is NV * 256 of them, counted from the row's first 16-byte boundary.
+// A CTA's chunk of a row: the row's whole vectors [va, vb), and the elements before its first or behind its last one.
+template <typename T>
+struct Chunk {
+  const T *x, *vecs;  // the row, its first whole vector
+  int va, vb, V;
+  bool head, tail;
+  CP_DEV int first(int v) const { return (int)(vecs - x) + v * Vec<T>::N; }  // element of a vector's first place
+  CP_DEV void load(Vec<T>& r, int v) const {
+    if (v < vb) r.load(vecs + (long long)v * Vec<T>::N);
+    else r.clear();
+  }
+  // vectors va - 1 and vb: what the row has of them, if they are this chunk's
+  CP_DEV bool has_end(int v) const { return v < va ? head : tail; }
+  CP_DEV void load_end(Vec<T>& r, int v) const {
+    r.clear();
+    const int e = first(v);
+    if (has_end(v))
+#pragma unroll
+      for (int j = 0; j < Vec<T>::N; ++j)
+        if (e + j >= 0 && e + j < V) r.put(j, x[e + j]);
+  }
+  // any of the chunk's vectors in turn, for the slow ways: i = 0, 1 are its ends
+  CP_DEV int count() const { return vb - va + 2; }
+  CP_DEV int get(Vec<T>& r, int i) const {
+    const int v = i == 0 ? va - 1 : i == 1 ? vb : va + i - 2;
+    if (i < 2) load_end(r, v);
+    else load(r, v);
+    return first(v);
+  }
+};
+CP_DEV unsigned long long list_key(float y, int token) {
+  return ((unsigned long long)order32(y) << 32) | (0xffffffffu - (uint32_t)token);
+}
+
+// Sum of exp(x - most) where a NaN counts as -inf, and infinities share the probability.
+template <typename T>
+__device__ __noinline__ float slow_sum(const Chunk<T> c, float most) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < c.count(); i += kThreads) {
+    Vec<T> r;
+    c.get(r, i);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) {
+      const float y = r.get(j);
+      sum += y == most ? 1.f : y < most ? ex2_approx((y - most) * kLog2e) : 0.f;
+    }
+  }
+  return sum;
+}
+// The chunk's values that reach `least`, or where they are too many its M largest one after the other (into key[0 .. M)).
+template <typename T>
+__device__ __noinline__ int slow_list(const Chunk<T> c, float least, int M, SelectShared& sh) {
+  __syncthreads();
+  if (threadIdx.x == 0) sh.n = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < c.count(); i += kThreads) {
+    Vec<T> r;
+    const int e = c.get(r, i);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) {
+      const float y = r.get(j);
+      if (y >= least) {
+        const int at = atomicAdd(&sh.n, 1);
+        if (at < kList) sh.key[at] = list_key(y, e + j), sh.rank[at] = 0;
+      }
+    }
+  }
+  __syncthreads();
+  const int n = sh.n;
+  if (n <= kList) return n;
+  unsigned long long last = ~0ull;
+  for (int m = 0; m < M; ++m) {
+    unsigned long long best = 0, none = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < c.count(); i += kThreads) {
+      Vec<T> r;
+      const int e = c.get(r, i);
+#pragma unroll
+      for (int j = 0; j < Vec<T>::N; ++j) {
+        const float y = r.get(j);
+        if (y >= least) {
+          const unsigned long long k = list_key(y, e + j);
+          if (k < last && k > best) best = k;
+        }
+      }
+    }
+    block_best(best, none, sh.w_key, sh.w_at);
+    if (threadIdx.x == 0) sh.key[m] = best, sh.rank[m] = 0;
+    last = best;
+  }
+  __syncthreads();
+  return M;
+}
+
+// NV: vectors a thread takes at a time.
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads, NV >= 8 ? 4 : 5) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams p) {
   using W = Vec<T>;
   __shared__ SelectShared sh;
   chained_start();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long row = blockIdx.x / (unsigned)p.S;
-  const int slice = (int)(blockIdx.x % (unsigned)p.S), b = (int)(row / p.K);
-  const T* x = static_cast<const T*>(p.logits) + row * p.stride;
-  const int skew = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));  // elements before the row in its first vector
-  if (tid == 0) sh.n = 0;
+  const int part = (int)(blockIdx.x % (unsigned)p.S), b = (int)(row / p.K);
+  Chunk<T> c;
+  c.x = static_cast<const T*>(p.logits) + row * p.stride;
+  const int before = (int)((0u - (uint32_t)reinterpret_cast<uintptr_t>(c.x)) & 15u) / (int)sizeof(T);
+  const int vecs = max(0, p.V - before) / W::N;  // whole ones
+  c.vecs = c.x + before;
+  c.V = p.V;
+  c.va = min(part * p.chunk, vecs);
+  c.vb = min(c.va + p.chunk, vecs);
+  c.head = part == 0 && before > 0;
+  c.tail = part == p.S - 1 && before + vecs * W::N < p.V;
+  // warps whose lanes all have a vector in the first round, and how many of each one's values the bound counts
+  const int full_warps = min(kWarps, (c.vb - c.va) / 32), w = (p.M + max(full_warps, 1) - 1) / max(full_warps, 1);
+  if (tid == 0) sh.n = sh.n2 = 0;
+  if (lane == 0) sh.w_th[warp] = warp < full_warps ? order32(-INFINITY) : 0xffffffffu;
 
-  // ---- the slice in registers, what is no token as -inf
-  W v[NV];
-  int e0 = (slice * (NV * kThreads) + tid) * W::N - skew;
-  auto first = [&](int i) -> int { return e0 + i * (kThreads * W::N); };  // element of v[i].get(0)
+  // this lane's largest value, and what its sum is relative to (values far below any that counts, a mask's lowest ones,
+  // do not move it)
+  float top = -INFINITY, ref = -kMaxLogit;
+  // pairs of sums of 2^(x log2(e) - c), c = ref log2(e) rounded, which is made good at the end
+  uint64_t part_sum[2] = {0ull, 0ull}, minus_c, log2e;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(log2e) : "f"(kLog2e));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(minus_c) : "f"(kMaxLogit * kLog2e));
+  volatile uint32_t* th = sh.w_th;
+  // the w-th largest of the warp's lanes' largest values, published; and the bound as it stands
+  auto publish = [&]() {
+    uint32_t largest;
+    const uint32_t k = wth_largest(order32(top), w, largest);
+    if (lane == 0 && warp < full_warps) th[warp] = k;
+  };
+  const bool counted = full_warps > 0 && w <= 32;
+  auto bound = [&]() -> float { return counted ? fmaxf(value32(sh.bound()), -kMost) : -kMost; };  // (-inf reaches none)
+  // one round of vectors: sum, largest value, and the list
+  auto work = [&](auto& v, int v0, bool first_round) {
+    constexpr int kN = sizeof(v) / sizeof(W);
+    float vm[kN], mx = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = first(i);
-    if (e >= 0 && e + W::N <= p.V) {
-      v[i].load(x + e);
-    } else {
-      v[i].clear();
-#pragma unroll
-      for (int j = 0; j < W::N; ++j)
-        if (e + j >= 0 && e + j < p.V) v[i].put(j, x[e + j]);
+    for (int i = 0; i < kN; ++i) {
+      vm[i] = v[i].max();
+      mx = fmaxf(mx, vm[i]);
     }
-  }
-  float top = -INFINITY;
+    top = fmaxf(top, mx);
+    if (top > ref + kMaxGrowth) {  // (the first time, and rarely again)
+      const float f = ex2_approx((ref - top) * kLog2e);
+      uint64_t f2;
+      asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
 #pragma unroll
-  for (int i = 0; i < NV; ++i) top = fmaxf(top, v[i].max());
-
-  // ---- the slice's largest value, and a bound that at least M values reach
-  uint32_t largest;
-  const uint32_t wth = wth_largest(order32(top), (p.M + kWarps - 1) / kWarps, largest);
-  if (lane == 0) sh.w_max[warp] = largest, sh.w_th[warp] = wth;
+      for (int i = 0; i < 2; ++i) asm("mul.f32x2 %0, %0, %1;" : "+l"(part_sum[i]) : "l"(f2));
+      ref = top;
+      const float c = -ref * kLog2e;
+      asm("mov.b64 %0, {%1, %1};" : "=l"(minus_c) : "f"(c));
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int j = 0; j < W::N; j += 2) add_exp2(part_sum[(j >> 1) & 1], v[i].get(j), v[i].get(j + 1), log2e, minus_c);
+    if (first_round) {
+      publish();
+      __syncthreads();
+    }
+    const float least = bound();
+    if (mx >= least) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (vm[i] >= least) {
+          const int at = atomicAdd(&sh.n, 1);
+          if (at < kVecs) sh.vec[at] = v[i].raw(), sh.id[at] = v0 + i * kThreads;
+        }
+    }
+  };
+  constexpr int kRound = NV * kThreads;
+  W va[NV], vb[NV];
+  int v0 = c.va + tid;
+  auto load = [&](W (&v)[NV], int from) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c.load(v[i], from + i * kThreads);
+  };
+  load(va, v0);
+  const int rounds = max(1, (c.vb - c.va + kRound - 1) / kRound);
+#pragma unroll 1
+  for (int r = 0; r < rounds; r += 2, v0 += 2 * kRound) {
+    if (r + 1 < rounds) load(vb, v0 + kRound);
+    work(va, v0, r == 0);
+    if (r + 1 >= rounds) break;
+    if (r + 2 < rounds) load(va, v0 + 2 * kRound);
+    work(vb, v0 + kRound, false);
+    if (((r + 2) & (r + 1)) == 0) publish();  // after 2, 4, 8, .. rounds
+  }
+  if (warp == 0 && (c.head || c.tail)) {  // the row's ends: lane 0 and lane 1
+    W end[1];
+    const int v = lane == 0 ? c.va - 1 : c.vb;
+    if (lane < 2) c.load_end(end[0], v);
+    else end[0].clear();
+    work(end, v, false);
+  }
+  publish();
+  const uint32_t warp_top = __reduce_max_sync(0xffffffffu, order32(top));
+  if (lane == 0) sh.w_max[warp] = warp_top;
   __syncthreads();
-  uint32_t bound = 0xffffffffu;
-  largest = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) largest = max(largest, sh.w_max[w]), bound = min(bound, sh.w_th[w]);
-  const float most = value32(largest), least = value32(bound);
 
-  auto pin = [&]() {
+  // ---- the chunk's sum
+  uint32_t k_most = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i].pin();
-  };
-  pin();
-  // ---- sum, relative to the largest
-  float sum = 0.f;
-  if (most > -INFINITY) {
-    uint64_t part[2] = {0ull, 0ull}, minus;  // pairs of sums
-    asm("mov.b64 %0, {%1, %1};" : "=l"(minus) : "f"(-most));
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < W::N; j += 2) add_exp2(part[(j >> 1) & 1], v[i].get(j), v[i].get(j + 1), minus);
+  for (int i = 0; i < kWarps; ++i) k_most = max(k_most, sh.w_max[i]);
+  const float most = value32(k_most), least = bound();
+  float sum;
+  {
     float s[4];
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(part[0]));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(s[2]), "=f"(s[3]) : "l"(part[1]));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(part_sum[0]));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(s[2]), "=f"(s[3]) : "l"(part_sum[1]));
     sum = (s[0] + s[1]) + (s[2] + s[3]);
-    if (!(sum < INFINITY)) {  // a NaN, which counts as -inf, or infinities, which share the probability
-      sum = 0.f;
-      pin();
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < W::N; ++j) {
-          const float y = v[i].get(j);
-          sum += y == most ? 1.f : y < most ? ex2_approx((y - most) * kLog2e) : 0.f;
-        }
-    }
+    const float c = ref * kLog2e;
+    sum *= ex2_approx((ref - most) * kLog2e - fmaf(ref, kLog2e, -c));
+  }
+  sum = block_sum(sum, sh.w_sum);
+  if (!(sum < INFINITY) || fabsf(most) > kMaxLogit) {
+    __syncthreads();
+    sum = most > -INFINITY ? slow_sum(c, most) : 0.f;
+    sum = block_sum(sum, sh.w_sum);
   }
 
-  pin();
-  // ---- the values that reach the bound
-  if (top >= least && top > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (v[i].max() >= least)
-#pragma unroll
-        for (int j = 0; j < W::N; ++j) {
-          const float y = v[i].get(j);
-          if (y >= least && y > -INFINITY) {
-            const int at = atomicAdd(&sh.n, 1);
-            if (at < kList) sh.key[at] = ((unsigned long long)order32(y) << 32) | (0xffffffffu - (uint32_t)(first(i) + j));
-          }
-        }
-  }
-  sum = block_sum(sum, sh.w_sum);  // (a barrier: the list is complete)
-  const long long part = row * p.S + slice;
-  uint2* best = p.best + part * p.M;
-  const int n = sh.n;
-  auto keep = [&](int r, unsigned long long key) {
-    best[r] = make_uint2(__float_as_uint(value32((uint32_t)(key >> 32))), 0xffffffffu - (uint32_t)key);
-  };
-  if (n <= kList) {
-    for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long key = sh.key[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += sh.key[j] > key;
-      if (rank < p.M) keep(rank, key);
+  // ---- its M largest values, in order
+  const long long out = row * p.S + part;
+  uint2* best = p.best + out * p.M;
+  int n = sh.n;
+  if (n > kVecs) {
+    n = slow_list(c, least, p.M, sh);
+  } else {
+#pragma unroll 1
+    for (int i = tid; i < n * W::N; i += kThreads) {  // a thread an element
+      const float y = to_float(reinterpret_cast<const T*>(sh.vec)[i]);
+      if (y >= least) {
+        const int at = atomicAdd(&sh.n2, 1);
+        if (at < kList) sh.key[at] = list_key(y, c.first(sh.id[i / W::N]) + i % W::N), sh.rank[at] = 0;
+      }
     }
-    for (int r = n + tid; r < p.M; r += kThreads) best[r] = make_uint2(0xff800000u, 0xffffffffu);
-  } else {  // many equal values: one after the other
-    unsigned long long last = ~0ull;
-    for (int r = 0; r < p.M; ++r) {
-      unsigned long long key = 0, none = 0;
-      pin();
-      asm volatile("" : "+r"(e0));
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < W::N; ++j) {
-          const float y = v[i].get(j);
-          if (y >= least && y > -INFINITY) {
-            const unsigned long long k = ((unsigned long long)order32(y) << 32) | (0xffffffffu - (uint32_t)(first(i) + j));
-            if (k < last && k > key) key = k;
-          }
-        }
-      block_best(key, none, sh.w_key, sh.w_at);
-      if (tid == 0) keep(r, key);
-      last = key;
-    }
+    __syncthreads();
+    n = sh.n2;
+    if (n > kList) n = slow_list(c, least, p.M, sh);
   }
-  if (tid == 0) p.stats[part] = make_float2(most, sum);
+  count_before<false>(sh, n);
+#pragma unroll 1
+  for (int i = tid; i < n; i += kThreads)
+    if (sh.rank[i] < p.M)
+      best[sh.rank[i]] = make_uint2(__float_as_uint(value32((uint32_t)(sh.key[i] >> 32))), 0xffffffffu - (uint32_t)sh.key[i]);
+  for (int r = n + tid; r < p.M; r += kThreads) best[r] = make_uint2(0xff800000u, 0xffffffffu);
+  if (tid == 0) p.stats[out] = make_float2(most, sum);
 
-  // ---- the CTA that counts last has every slice of the sequence before it
+  // ---- the CTA that counts last has every chunk of the sequence before it
   __syncthreads();
   if (tid == 0) {
     int before;
@@ -434,18 +631,22 @@ __global__ void __launch_bounds__(kThreads, NV >= 8 ? 4 : 5) select_kernel(const
   if (sh.last) finish_sequence(p, sh, b);
 }
 
-// Slices: as long as leaves every SM some CTAs (the shorter ones cost more merging).
+// Chunks: one a row if that gives every SM its four CTAs or nearly; else as many as do, of 16 KB at least (shorter ones
+// cost the last CTA more than they save).  More rows than places: a third of the GPU's places each, so that the last
+// ones are short.
 struct SelectPlan {
-  int NV, S;
+  int NV, S, chunk;
 };
 SelectPlan select_plan(long long rows, int V, int elem) {
-  // 16-byte vectors that a row touches, which may start anywhere in one
-  const long long vecs = ((long long)V * elem + 16 - elem + 15) / 16;
-  for (int NV = 8; NV > 1; NV /= 2) {
-    const long long S = (vecs + NV * kThreads - 1) / (NV * kThreads);
-    if (rows * S >= 2 * 152) return {NV, (int)S};
-  }
-  return {1, (int)((vecs + kThreads - 1) / kThreads)};
+  constexpr long long kPlaces = 4 * 152;
+  // whole 16-byte vectors of a row, which may start anywhere in one (at most; its ends are apart); a vector a thread
+  const long long vecs = (long long)V * elem / 16, pieces = vecs > 0 ? (vecs + kThreads - 1) / kThreads : 1;
+  long long S = rows > kPlaces ? (3 * kPlaces + rows - 1) / rows : kPlaces / rows;
+  const long long most = rows > kPlaces ? (pieces + 7) / 8 : (pieces + 3) / 4;
+  if (S > most) S = most;
+  if (S < 1) S = 1;
+  const long long per = (pieces + S - 1) / S;
+  return {per >= 4 ? 4 : per >= 2 ? 2 : 1, (int)((pieces + per - 1) / per), (int)(per * kThreads)};
 }
 // Workspace: counters, each slice's sum, each slice's values.
 size_t select_layout(size_t slices, int M, size_t* stats, size_t* best) {
@@ -465,6 +666,7 @@ cudaError_t launch_select(const cp_beam_select_args& a, void* workspace, cudaStr
   p.V = a.vocab;
   p.M = a.num_candidates;
   p.S = plan.S;
+  p.chunk = plan.chunk;
   p.eos = a.eos_token;
   p.stride = a.logits_stride;
   p.logits = a.logits;
@@ -475,10 +677,7 @@ cudaError_t launch_select(const cp_beam_select_args& a, void* workspace, cudaStr
   p.next_score = a.next_scores, p.next_beam = a.next_beams, p.next_token = a.next_tokens;
   p.cand_score = a.cand_scores, p.cand_beam = a.cand_beams, p.cand_token = a.cand_tokens;
   const dim3 grid((unsigned)((long long)a.num_seqs * a.num_beams * plan.S));
-  auto kern = plan.NV == 8   ? select_kernel<T, 8>
-              : plan.NV == 4 ? select_kernel<T, 4>
-              : plan.NV == 2 ? select_kernel<T, 2>
-                             : select_kernel<T, 1>;
+  auto kern = plan.NV == 4 ? select_kernel<T, 4> : plan.NV == 2 ? select_kernel<T, 2> : select_kernel<T, 1>;
   return launch_chained(kern, grid, kThreads, 0, s, p);
 }
 
@@ -606,14 +805,13 @@ cudaError_t reorder_launch(const ReorderParams& p, cudaStream_t s) {
 }  // namespace
 }  // namespace cpattn
 
-// Enough for either type and for every smaller size: shorter slices are taken only where there are fewer than 2 * 152
-// of twice their length.
+// Enough for either type and for every smaller size: up to 4 * 152 rows there are at most so many chunks, beyond three
+// times as many and one a row.
 size_t cp_beam_select_bytes(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_candidates) {
-  using namespace cpattn;
   const size_t rows = (size_t)num_seqs * num_beams;
-  const size_t longest = rows * (((size_t)vocab * 4 + 15) / 16 / (8 * kThreads) + 1);
   size_t a, b;
-  return select_layout(longest > 4 * 152 ? longest : 4 * 152, num_candidates, &a, &b);
+  (void)vocab;
+  return cpattn::select_layout(rows > 4 * 152 ? rows + 3 * 4 * 152 : 4 * 152, num_candidates, &a, &b);
 }
 long long cp_beam_select_ctas(const cp_beam_select_args& a) {
   const long long rows = (long long)a.num_seqs * a.num_beams;
