@@ -953,14 +953,14 @@ size_t cp_beam_select_args_size(void) { return sizeof(cp_beam_select_args); }
 size_t cp_beam_reorder_args_size(void) { return sizeof(cp_beam_reorder_args); }
 
 // The shape of a cross attention, and which kernel takes it: the tensor cores' tiles of 128 rows from 65 rows a kv
-// head on, the kernels for few rows (in f32 for any) below.
+// head on, the kernel for few rows (in f32 for any) below.
 static cp_status check_cross_shape(const cp_cross_args* a) {
   REQUIRE(a != nullptr, "args is null");
   REQUIRE(a->dtype == CP_F32 || a->dtype == CP_BF16, "dtype must be CP_F32 or CP_BF16");
   REQUIRE(a->num_seqs >= 1 && a->num_seqs <= (1 << 24), "num_seqs must be >= 1 (got %d)", a->num_seqs);
   REQUIRE(a->num_kv_heads >= 1 && a->num_kv_heads <= 65536 && a->num_q_heads >= 1 && a->num_q_heads % a->num_kv_heads == 0,
           "num_q_heads must be a multiple of num_kv_heads");
-  const int G = a->num_q_heads / a->num_kv_heads, most = a->dtype == CP_BF16 ? 128 : 16;
+  const int G = a->num_q_heads / a->num_kv_heads, most = a->dtype == CP_BF16 ? 128 : 64;
   if (G > most)
     return fail(CP_ERR_UNSUPPORTED, "q heads per kv head must be 1 .. %d for this dtype (got %d)", most, G);
   if (a->head_dim != 64 && a->head_dim != 128)

@@ -9,9 +9,11 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/core/DimVector.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -156,6 +158,56 @@ struct Call {
     dense(*given, name, dtype);
     shaped(*given, name, shape);
     return *given;
+  }
+};
+
+// New outputs of one call share an allocation (an allocation through the dispatcher costs the host about a microsecond, as
+// much as a quarter of a small call; a tensor over memory that is there a fifth of that).
+struct Outputs {
+  struct One {
+    const Tensor* given;
+    const char* name;
+    at::DimVector shape;
+    at::ScalarType dtype;
+    Tensor* to;
+  };
+  const Call& c;
+  c10::SmallVector<One, 6> all;
+  explicit Outputs(const Call& call) : c(call) {}
+  void add(Tensor& to, const Tensor* given, const char* name, std::initializer_list<int64_t> shape, at::ScalarType dtype) {
+    all.push_back({given, name, at::DimVector(shape), dtype, &to});
+  }
+  void make() {
+    size_t bytes = 0;
+    auto size_of = [](const One& o) {
+      size_t n = c10::elementSize(o.dtype);
+      for (const int64_t d : o.shape) n *= (size_t)d;
+      return (n + 255) / 256 * 256;
+    };
+    for (const One& o : all) {
+      if (o.given == nullptr) {
+        bytes += size_of(o);
+        continue;
+      }
+      c.dense(*o.given, o.name, o.dtype);
+      if (o.given->sizes() != at::IntArrayRef(o.shape))
+        refuse(std::string(o.name) + " must be " + text(o.shape) + " (got " + text(o.given->sizes()) + ")");
+      *o.to = *o.given;
+    }
+    if (bytes == 0) bytes = 1;
+    c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
+    c10::Storage memory;  // of the call's device and stream, both current
+    size_t at = 0;
+    for (const One& o : all) {
+      if (o.given != nullptr) continue;
+      if (!memory) memory = c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes, from->allocate(bytes), from, true));
+      Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(memory), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                          c10::scalarTypeToTypeMeta(o.dtype));
+      t.unsafeGetTensorImpl()->set_sizes_contiguous(o.shape);
+      t.unsafeGetTensorImpl()->set_storage_offset((int64_t)(at / c10::elementSize(o.dtype)));
+      at += size_of(o);
+      *o.to = std::move(t);
+    }
   }
 };
 
@@ -536,9 +588,11 @@ PyObject* cross(Args& x) {
   a.k = in(k);
   a.v = in(v);
   a.err = c.error_word(err);
-  const Tensor o = c.output(out, "out", {N, Hq, d}, T);
-  Tensor l;
-  if (out_lse != nullptr || want_lse) l = c.output(out_lse, "out_lse", {N, Hq}, at::kFloat);
+  Tensor o, l;
+  Outputs made(c);
+  made.add(o, out, "out", {N, Hq, d}, T);
+  if (out_lse != nullptr || want_lse) made.add(l, out_lse, "out_lse", {N, Hq}, at::kFloat);
+  made.make();
   Tensor workspace;
   if (given != nullptr) {
     c.dense(*given, "workspace", at::kByte);
@@ -603,9 +657,15 @@ PyObject* beam_select(Args& x) {
     workspace = at::zeros({(int64_t)need}, at::TensorOptions().device(c.device).dtype(at::kByte));
   }
   const int64_t M = a.num_candidates;
-  const Tensor o0 = c.output(ns, "next_scores", {B, K}, at::kFloat), o1 = c.output(nb, "next_beams", {B, K}, at::kInt),
-               o2 = c.output(nt, "next_tokens", {B, K}, at::kInt), o3 = c.output(cs, "cand_scores", {B, M}, at::kFloat),
-               o4 = c.output(cb, "cand_beams", {B, M}, at::kInt), o5 = c.output(ct, "cand_tokens", {B, M}, at::kInt);
+  Tensor o0, o1, o2, o3, o4, o5;
+  Outputs made(c);
+  made.add(o0, ns, "next_scores", {B, K}, at::kFloat);
+  made.add(o1, nb, "next_beams", {B, K}, at::kInt);
+  made.add(o2, nt, "next_tokens", {B, K}, at::kInt);
+  made.add(o3, cs, "cand_scores", {B, M}, at::kFloat);
+  made.add(o4, cb, "cand_beams", {B, M}, at::kInt);
+  made.add(o5, ct, "cand_tokens", {B, M}, at::kInt);
+  made.make();
   a.logits = in(logits);
   a.scores = static_cast<const float*>(in(scores));
   a.next_scores = static_cast<float*>(out_of(o0));

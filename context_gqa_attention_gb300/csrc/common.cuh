@@ -141,6 +141,9 @@ cudaError_t cp_launch_decode(const cp_decode_args& a, float scale, cudaStream_t 
 bool cp_make_bf16_map_2d(void* map, const void* base, unsigned long long cols,
                          unsigned long long rows, unsigned long long pitch_elems,
                          unsigned box_rows);
+// The same of f32: box of 32 columns (128 bytes).
+bool cp_make_f32_map_2d(void* map, const void* base, unsigned long long cols, unsigned long long rows,
+                        unsigned long long pitch_elems, unsigned box_rows);
 // 3D bf16 TMA descriptor over rows of `heads` heads of `cols` elements: box of 64 columns x box_heads heads x
 // box_rows rows, landing as box_rows * box_heads rows of 128 bytes; 128-byte swizzle, zero fill.
 bool cp_make_bf16_map_3d(void* map, const void* base, unsigned long long cols, unsigned long long heads,

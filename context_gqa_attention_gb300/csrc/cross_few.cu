@@ -183,11 +183,15 @@ CP_DEV Keys part_keys(const CrossParams& p, const CrossItem& w, int tile, int pa
   return k;
 }
 
-// ------------------------------------------------------------------------------ bf16: tensor-core MMAs
-// m16n8k16 MMAs on the legacy tensor path: a 128-row tcgen05 tile would be padding.  A producer warp brings tiles of
+// ------------------------------------------------------------------------------ the kernel
+// MMAs of 16 rows on the legacy tensor path: a 128-row tcgen05 tile would be padding.  A producer warp brings tiles of
 // K and V through a ring (TMA, 128-byte swizzle); consumer warp (m, k) owns the 16 rows m and the k-th slice of every
 // tile's keys, with a softmax reference of its own, so warps meet at the end only.  The reference moves when a score
 // exceeds it by more than 2^8, which a vote of the warp finds; rows' sums stay in the lanes until the end.
+//
+// f32: each operand is the sum of two tf32 numbers, high and low, and a product the sum of three (high high, high low,
+// low high): 22 bits of each operand count, and the sums are fp32.  A step of the reduction is 32 bytes in both types
+// (16 bf16, 8 tf32), so their tiles and fragments lie alike.
 CP_DEV void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -196,12 +200,37 @@ CP_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-CP_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+CP_DEV void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+CP_DEV void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+CP_DEV uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+// x = high + low, both tf32.  An infinity or a NaN stays in the high part; `fin` is that part where it is finite, else 0:
+// the factor of the other operand's low part, which may be 0.
+CP_DEV void split(float x, uint32_t& hi, uint32_t& lo, uint32_t& fin) {
+  hi = tf32(x);
+  const float rest = x - __uint_as_float(hi);
+  const bool ok = rest == rest;
+  lo = tf32(ok ? rest : 0.f);
+  fin = ok ? hi : 0u;
+}
+CP_DEV void split(float x, uint32_t& hi, uint32_t& lo) {
+  uint32_t fin;
+  split(x, hi, lo, fin);
 }
 CP_DEV uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -213,42 +242,52 @@ CP_DEV bool clean(uint32_t& w) {
   w &= ~((bad >> 15) * 0xffffu);
   return bad != 0u;
 }
+CP_DEV float as_float(float x) { return x; }
+CP_DEV float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-template <int D, int MT>
+template <typename T, int D, int MT>
 struct Few {
-  static constexpr int kWK = MT == 4 ? 2 : 4;      // slices of a tile's keys
+  static constexpr bool kF32 = sizeof(T) == 4;
+  static constexpr int kWK = MT == 4 ? 2 : 4;        // slices of a tile's keys
   static constexpr int kConsumers = MT * kWK;
   static constexpr int kThreads = 32 * (kConsumers + 1);
-  static constexpr int kTile = D == 128 ? 64 : 128;  // keys
+  static constexpr int kBytes = 16384;               // of a tile of K or of V
+  static constexpr int kTile = kBytes / (D * (int)sizeof(T));  // keys
   static constexpr int kKeys = kTile / kWK;          // of a warp
-  static constexpr int kStep = kKeys < 32 ? kKeys : 32;
-  static constexpr int kBytes = kTile * D * 2;       // of K or of V: 16 KB
-  static constexpr int kStages = MT == 1 ? 2 : 6;
-  static constexpr int kCtas = MT == 1 ? 3 : 1;      // on an SM
+  static constexpr int kMaxStep = kF32 ? 16 : 32;
+  static constexpr int kStep = kKeys < kMaxStep ? kKeys : kMaxStep;
+  static constexpr int kBoxCols = 128 / (int)sizeof(T), kBoxes = D / kBoxCols;
+  static constexpr int kSteps = D * (int)sizeof(T) / 32;  // of the reduction over a row
+  // q as A fragments in registers (bf16, one row group), or in shared memory: rows 16 bytes apart in the banks; f32: high
+  // parts, then low parts
+  static constexpr bool kQRegs = !kF32 && MT == 1;
+  static constexpr int kQPitch = D * (int)sizeof(T) + 16;
+  static constexpr int kQBytes = kQRegs ? 0 : 16 * MT * kQPitch * (kF32 ? 2 : 1);
   using Parts = Slices<D, kWK, 16 * MT>;
-  static constexpr int kRing = kStages * 2 * kBytes;
-  static constexpr int oBar = kRing > (int)sizeof(Parts) ? kRing : ((int)sizeof(Parts) + 15) / 16 * 16;
-  static constexpr int kSmem = oBar + 16 * kStages + 1024;  // (the base is rounded up to the swizzle atom)
+  static constexpr int align16(int x) { return (x + 15) / 16 * 16; }
+  static constexpr int smem_of(int stages) {
+    const int work = stages * 2 * kBytes + kQBytes, parts = align16((int)sizeof(Parts));
+    return (work > parts ? work : parts) + 16 * stages + 1024;  // (the base is rounded up to the swizzle atom)
+  }
+  static constexpr int ctas_of(int stages) { return 232448 / (smem_of(stages) + 1024); }
+  // CTAs on an SM, and stages of the ring
+  static constexpr int kCtas = MT == 1 && ctas_of(2) >= 3 ? 3 : ctas_of(2) >= 2 ? 2 : 1;
+  static constexpr int kStages = ctas_of(4) >= kCtas ? 4 : ctas_of(3) >= kCtas ? 3 : 2;
+  static constexpr int kRing = kStages * 2 * kBytes, oQ = kRing;
+  static constexpr int oBar = smem_of(kStages) - 1024 - 16 * kStages;
+  static constexpr int kSmem = smem_of(kStages);
 };
 
-template <int D, int MT, bool RANGES>
-__global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
+template <typename T, int D, int MT, bool RANGES>
+__global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
     few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const CrossParams p,
                const int parts, const int cluster) {
-  using F = Few<D, MT>;
-  constexpr int KB = D / 64, NT = F::kStep / 8;
+  using F = Few<T, D, MT>;
+  constexpr int NT = F::kStep / 8;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_range[4];
   __shared__ uint32_t s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  chained_start();
-  const int part = (int)(blockIdx.x % (unsigned)parts);
-  const CrossItem w = cross_item(p, blockIdx.x / (unsigned)parts, threadIdx.x == 0 && part == 0);
-  if (w.tokens == 0) return;  // (as every CTA of the cluster does)
-  const int piece = p.n_split > 0 ? (int)blockIdx.x : -1;
-  const Keys key = part_keys<RANGES>(p, w, F::kTile, part, parts, s_range);
-  const int ntiles = (key.end - key.first + F::kTile - 1) / F::kTile;
-
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sbase = smem_raw + (base - raw);
@@ -262,6 +301,51 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
     }
     s_abort = 0u;
     fence_mbar_init();
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  chained_start();
+  const int part = (int)(blockIdx.x % (unsigned)parts);
+  const CrossItem w = cross_item(p, blockIdx.x / (unsigned)parts, threadIdx.x == 0 && part == 0);
+  if (w.tokens == 0) return;  // (as every CTA of the cluster does)
+  const int piece = p.n_split > 0 ? (int)blockIdx.x : -1;
+  const Keys key = part_keys<RANGES>(p, w, F::kTile, part, parts, s_range);
+  const int ntiles = (key.end - key.first + F::kTile - 1) / F::kTile;
+  const int rows = w.tokens * p.G;
+  auto q_row = [&](int row) -> const T* {
+    const int t = row / p.G;
+    return static_cast<const T*>(p.q) + ((long long)w.q0 + w.t0 + t) * p.q_stride + (w.g * p.G + row - t * p.G) * D;
+  };
+  auto load = [&](int t) {  // tile t into its stage
+    const int s = t % F::kStages;
+    const uint32_t dst = base + (uint32_t)(s * 2 * F::kBytes);
+    mbar_expect_tx(full(s), 2 * F::kBytes);
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int kb = 0; kb < F::kBoxes; ++kb)
+        tma_load_2d(dst + v * F::kBytes + kb * F::kTile * 128, v ? &map_v : &map_k, w.g * D + kb * F::kBoxCols,
+                    w.kv0 + key.first + t * F::kTile, full(s));
+  };
+  // the first tiles are on their way while the rows of q come in
+  const int early = min(ntiles, F::kStages);
+  if (threadIdx.x == 0)
+    for (int t = 0; t < early; ++t) load(t);
+  if constexpr (!F::kQRegs) {
+    constexpr int kVec = 16 / (int)sizeof(T);
+    for (int i = threadIdx.x; i < 16 * MT * (D / kVec); i += F::kThreads) {
+      const int row = i / (D / kVec), c = (i % (D / kVec)) * kVec;
+      uint8_t* dst = sbase + F::oQ + row * F::kQPitch + c * (int)sizeof(T);
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows) x = *reinterpret_cast<const uint4*>(q_row(row) + c);
+      if constexpr (F::kF32) {
+        uint4 lo;
+        split(__uint_as_float(x.x), x.x, lo.x), split(__uint_as_float(x.y), x.y, lo.y);
+        split(__uint_as_float(x.z), x.z, lo.z), split(__uint_as_float(x.w), x.w, lo.w);
+        *reinterpret_cast<uint4*>(dst + 16 * MT * F::kQPitch) = lo;
+      }
+      *reinterpret_cast<uint4*>(dst) = x;
+    }
   }
   __syncthreads();
   auto fail = [&]() {
@@ -277,25 +361,14 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   if (warp == F::kConsumers) {
     // ---- producer
-    if (lane == 0 && ntiles > 0) {
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-      int issued = 0;
-      for (int t = 0; t < ntiles; ++t) {
-        const int s = t % F::kStages;
-        if (!mbar_wait(empty(s), ((uint32_t)(t / F::kStages) & 1u) ^ 1u, abort_flag, kBudget)) {
+    if (lane == 0) {
+      int issued = early;
+      for (int t = early; t < ntiles; ++t) {
+        if (!mbar_wait(empty(t % F::kStages), ((uint32_t)(t / F::kStages) & 1u) ^ 1u, abort_flag, kBudget)) {
           fail();
           break;
         }
-        const uint32_t dst = base + (uint32_t)(s * 2 * F::kBytes);
-        mbar_expect_tx(full(s), 2 * F::kBytes);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          tma_load_2d(dst + kb * F::kTile * 128, &map_k, w.g * D + kb * 64, w.kv0 + key.first + t * F::kTile, full(s));
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          tma_load_2d(dst + F::kBytes + kb * F::kTile * 128, &map_v, w.g * D + kb * 64,
-                      w.kv0 + key.first + t * F::kTile, full(s));
+        load(t);
         issued = t + 1;
       }
       // every copy has landed before the CTA goes on to use the ring
@@ -303,24 +376,26 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
         mbar_wait(full(t % F::kStages), (uint32_t)(t / F::kStages) & 1u, nullptr, kBudget);
     }
     __syncwarp();
-  } else if (wm * 16 < w.tokens * p.G) {
-    // ---- a consumer's rows of q, as A fragments, and their keys
-    const int rows = w.tokens * p.G;
-    uint32_t qa[D / 16][4];
+  } else if (wm * 16 < rows) {
+    // ---- a consumer's rows and their keys
+    uint32_t qa[F::kQRegs ? F::kSteps : 1][4];
     int lo[2] = {0, 0}, hi[2] = {w.keys, w.keys};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = wm * 16 + gid + 8 * r, t = row / p.G;
+      const int row = wm * 16 + gid + 8 * r;
       const bool real = row < rows;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                               (real ? ((long long)w.q0 + w.t0 + t) * p.q_stride + (w.g * p.G + row - t * p.G) * D : 0);
+      if constexpr (F::kQRegs) {
+        const T* q = q_row(real ? row : 0);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qa[k][r] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * tig) : 0u;
-        qa[k][r + 2] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * tig) : 0u;
+        for (int k = 0; k < F::kSteps; ++k) {
+          qa[k][r] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * tig) : 0u;
+          qa[k][r + 2] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * tig) : 0u;
+        }
       }
-      if (RANGES && real) cross_range(p, w, w.t0 + t, lo[r], hi[r]);
+      if (RANGES && real) cross_range(p, w, w.t0 + row / p.G, lo[r], hi[r]);
     }
+    // q's fragment of a step: matrices (rows 0-7, 8-15) x (its first, second 16 bytes)
+    const uint32_t sq = base + (uint32_t)(F::oQ + (wm * 16 + (lane & 15)) * F::kQPitch + (lane >> 4) * 16);
     int u0 = 0x7fffffff, u1 = -1;  // steps whose V held infinities or NaN that were taken out
     const float sc = p.scale_log2;
     bool ok = true;
@@ -329,24 +404,62 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
       ok = __all_sync(0xffffffffu, mbar_wait(full(s), (uint32_t)(t / F::kStages) & 1u, abort_flag, kBudget));
       if (!ok) break;
       const uint32_t sk = base + (uint32_t)(s * 2 * F::kBytes), sv = sk + (uint32_t)F::kBytes;
-#pragma unroll
+#pragma unroll 1
       for (int st = 0; st < F::kKeys / F::kStep; ++st) {
-        const int r0 = wk * F::kKeys + st * F::kStep;     // first row of the tile
-        const int k0 = key.first + t * F::kTile + r0;     // first key
+        const int r0 = wk * F::kKeys + st * F::kStep;  // first row of the tile
+        const int k0 = key.first + t * F::kTile + r0;  // first key
         if (k0 >= key.end) break;
         float c[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
-        // S = Q K^T: a matrix of 8 keys x 8 dims is 8 rows of 16 bytes
+        // S = Q K^T: a matrix is 8 keys' 16 bytes
+        auto k_at = [&](int row, int k, int chunk) -> uint32_t {  // 16-byte chunk of the step-pairs' 128 bytes
+          return sk + (uint32_t)((k / 4) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4);
+        };
+        auto qk = [&](float (&c)[4], const uint32_t (&a)[4], const uint32_t (&al)[4], uint32_t b0, uint32_t b1) {
+          if constexpr (F::kF32) {
+            uint32_t h0, h1, l0, l1, f0, f1;
+            split(__uint_as_float(b0), h0, l0, f0);
+            split(__uint_as_float(b1), h1, l1, f1);
+            mma_tf32(c, al, f0, f1);
+            mma_tf32(c, a, l0, l1);
+            mma_tf32(c, a, h0, h1);
+          } else {
+            mma_bf16(c, a, b0, b1);
+          }
+        };
+        auto q_step = [&](int k, uint32_t (&a)[4], uint32_t (&al)[4]) {
+          if constexpr (F::kQRegs) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
+            for (int i = 0; i < 4; ++i) a[i] = qa[k][i];
+          } else {
+            ldsm4(a, sq + 32u * k);
+            if constexpr (F::kF32) ldsm4(al, sq + 32u * k + 16 * MT * F::kQPitch);
+          }
+        };
+        if constexpr (NT == 1) {
 #pragma unroll
-          for (int i = 0; i < NT; i += 2) {
-            const int row = r0 + 8 * i + ((lane >> 4) << 3) + (lane & 7), chunk = 2 * (k & 3) + ((lane >> 3) & 1);
-            uint32_t b[4];
-            ldsm4(b, sk + (uint32_t)((k / 4) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
-            mma16816(c[i], qa[k], b[0], b[1]);
-            mma16816(c[i + 1], qa[k], b[2], b[3]);
+          for (int k = 0; k < F::kSteps; k += 2) {
+            uint32_t b[4], a[4], al[4];
+            ldsm4(b, k_at(r0 + (lane & 7), k, 2 * (k & 3) + (lane >> 3)));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              q_step(k + i, a, al);
+              qk(c[0], a, al, b[2 * i], b[2 * i + 1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < F::kSteps; ++k) {
+            uint32_t a[4], al[4];
+            q_step(k, a, al);
+#pragma unroll
+            for (int i = 0; i + 1 < NT; i += 2) {
+              uint32_t b[4];
+              ldsm4(b, k_at(r0 + 8 * i + ((lane >> 4) << 3) + (lane & 7), k, 2 * (k & 3) + ((lane >> 3) & 1)));
+              qk(c[i], a, al, b[0], b[1]);
+              qk(c[i + 1], a, al, b[2], b[3]);
+            }
           }
         }
         const bool whole = k0 + F::kStep <= key.end && (!RANGES || (k0 >= key.all_lo && k0 + F::kStep <= key.all_hi));
@@ -396,7 +509,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
         }
         if (k0 + F::kStep > key.end) {  // V rows that are no key of any row
           const int n = key.end - k0;
-          for (int i = lane; i < KB * F::kStep * 8; i += 32) {
+          for (int i = lane; i < F::kBoxes * F::kStep * 8; i += 32) {
             const int row = (i >> 3) % F::kStep, kb = i / (8 * F::kStep);
             if (row >= n)
               *reinterpret_cast<uint4*>(sbase + (sv - base) + kb * F::kTile * 128 + (r0 + row) * 128 + (i & 7) * 16) =
@@ -404,23 +517,51 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
           }
           __syncwarp();
         }
-        // O += P V: the scores' fragments are the MMA's A operand as they lie; matrices of V are read transposed
+        // O += P V: the scores' fragments are the MMA's A operand as they lie (f32: its columns tig and tig + 4 are keys
+        // 2 tig and 2 tig + 1, and so are the rows of V's fragments)
         bool bad = false;
+        if constexpr (F::kF32) {
 #pragma unroll
-        for (int i = 0; i < NT; i += 2) {
-          const uint32_t pa[4] = {pack2(c[i][0], c[i][1]), pack2(c[i][2], c[i][3]), pack2(c[i + 1][0], c[i + 1][1]),
-                                  pack2(c[i + 1][2], c[i + 1][3])};
-          const int row = r0 + 8 * i + (((lane >> 3) & 1) << 3) + (lane & 7);
+          for (int i = 0; i < NT; ++i) {
+            uint32_t ph[4], pl[4];
+            split(c[i][0], ph[0], pl[0]), split(c[i][2], ph[1], pl[1]);
+            split(c[i][1], ph[2], pl[2]), split(c[i][3], ph[3], pl[3]);
+            const int row = r0 + 8 * i + 2 * tig;
 #pragma unroll
-          for (int n = 0; n < D / 8; n += 2) {
-            const int chunk = (n & 7) + (lane >> 4);
-            uint32_t b[4];
-            ldsm4_t(b, sv + (uint32_t)((n / 8) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
-            if (RANGES && !whole)
+            for (int n = 0; n < D / 8; ++n) {
+              float x[2];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) bad = clean(b[e]) || bad;
-            mma16816(o[n], pa, b[0], b[1]);
-            mma16816(o[n + 1], pa, b[2], b[3]);
+              for (int e = 0; e < 2; ++e) {
+                const int chunk = 2 * (n & 3) + (gid >> 2);
+                x[e] = *reinterpret_cast<const float*>(sbase + (sv - base) + (n / 4) * F::kTile * 128 + (row + e) * 128 +
+                                                       ((chunk ^ ((row + e) & 7)) << 4) + (gid & 3) * 4);
+                if (RANGES && !whole && !isfinite(x[e])) x[e] = 0.f, bad = true;
+              }
+              uint32_t h0, h1, l0, l1, f0, f1;
+              split(x[0], h0, l0, f0);
+              split(x[1], h1, l1, f1);
+              mma_tf32(o[n], pl, f0, f1);
+              mma_tf32(o[n], ph, l0, l1);
+              mma_tf32(o[n], ph, h0, h1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i + 1 < NT; i += 2) {
+            const uint32_t pa[4] = {pack2(c[i][0], c[i][1]), pack2(c[i][2], c[i][3]), pack2(c[i + 1][0], c[i + 1][1]),
+                                    pack2(c[i + 1][2], c[i + 1][3])};
+            const int row = r0 + 8 * i + (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+            for (int n = 0; n < D / 8; n += 2) {
+              const int chunk = (n & 7) + (lane >> 4);
+              uint32_t b[4];
+              ldsm4_t(b, sv + (uint32_t)((n / 8) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
+              if (RANGES && !whole)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bad = clean(b[e]) || bad;
+              mma_bf16(o[n], pa, b[0], b[1]);
+              mma_bf16(o[n + 1], pa, b[2], b[3]);
+            }
           }
         }
         if (RANGES && __any_sync(0xffffffffu, bad)) u0 = min(u0, k0), u1 = max(u1, k0 + F::kStep);
@@ -431,8 +572,8 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
     if (!ok && lane == 0) fail();
     if (RANGES && u1 >= 0) {
       // what was taken out of V for the rows that see it: p > 0 times it is itself, whatever p is.  The warp's keys
-      // are every kTile-th slice of kKeys.
-      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (long long)w.kv0 * p.v_stride + w.g * D;
+      // are one slice in kWK of every tile.
+      const T* v = static_cast<const T*>(p.v) + (long long)w.kv0 * p.v_stride + w.g * D;
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         for (int j = max(u0, lo[r]); j < min(min(u1, hi[r]), key.end); ++j)
@@ -441,7 +582,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
             for (int i = 0; i < D / 8; ++i)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float x = __bfloat162float(v[j * p.v_stride + 8 * i + 2 * tig + e]);
+                const float x = as_float(v[j * p.v_stride + 8 * i + 2 * tig + e]);
                 if (!isfinite(x)) o[i][2 * r + e] += x;
               }
     }
@@ -470,173 +611,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
       if (tig == 0) slices.m[wk][row] = m[r], slices.l[wk][row] = l[r];
     }
   }
-  finish<__nv_bfloat16>(p, w, slices, cluster, piece);
-}
-
-// ------------------------------------------------------------------------------ f32: CUDA cores
-// A CTA of four warps takes up to R query rows; warp k takes every fourth group of eight keys.  Scores: lane (row, key
-// pair), q from shared memory, k broadcast; output: lane (four or two dims), all rows.  Tiles of 32 keys through two
-// stages of shared memory.  Any number of rows: further items read the states again (from L2).
-template <int D, int R>
-struct Plain {
-  static constexpr int kTile = 32, kPad = D + 4;  // (rows 16 bytes apart in the banks)
-  using Parts = Slices<D, 4, R>;
-  static constexpr int kStage = 2 * kTile * D * 4;
-  static constexpr int kRing = 2 * kStage;
-  static constexpr int oQ = kRing > (int)sizeof(Parts) ? kRing : ((int)sizeof(Parts) + 15) / 16 * 16;
-  static constexpr int oP = oQ + R * kPad * 4;
-  static constexpr int kSmem = oP + 4 * 8 * R * 4;
-};
-CP_DEV void cp_async16(uint32_t dst, const void* src, bool real) {  // 16 bytes, zeros where there are none
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-
-template <int D, int R, bool RANGES>
-__global__ void __launch_bounds__(128) plain_kernel(const CrossParams p, const int parts,
-                                                                         const int cluster) {
-  using F = Plain<D, R>;
-  constexpr int E = D / 32;        // dims of a lane in the output
-  constexpr int KPL = 8 * R / 32;  // keys of a lane in the scores (R = 4, 8, 16: 1, 2, 4)
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_range[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  chained_start();
-  const int part = (int)(blockIdx.x % (unsigned)parts);
-  const CrossItem w = cross_item(p, blockIdx.x / (unsigned)parts, threadIdx.x == 0 && part == 0);
-  if (w.tokens == 0) return;  // (as every CTA of the cluster does)
-  const int piece = p.n_split > 0 ? (int)blockIdx.x : -1;
-  const Keys key = part_keys<RANGES>(p, w, F::kTile, part, parts, s_range);
-  const int ntiles = (key.end - key.first + F::kTile - 1) / F::kTile;
-  const int rows = w.tokens * p.G;
-  float* sq = reinterpret_cast<float*>(smem + F::oQ);
-  float* sp = reinterpret_cast<float*>(smem + F::oP) + warp * 8 * R;  // the warp's weights [key][row]
-
-  const float* kbase = static_cast<const float*>(p.k) + (long long)w.kv0 * p.k_stride + w.g * D;
-  const float* vbase = static_cast<const float*>(p.v) + (long long)w.kv0 * p.v_stride + w.g * D;
-  auto load = [&](int t) {
-    const uint32_t dst = smem_u32(smem) + (uint32_t)((t & 1) * F::kStage);
-    for (int i = threadIdx.x; i < 2 * F::kTile * D / 4; i += 128) {
-      const int which = i / (F::kTile * D / 4), row = (i / (D / 4)) % F::kTile, c = (i % (D / 4)) * 4;
-      const int j = key.first + t * F::kTile + row;
-      const bool real = j < key.end;
-      const float* src = which == 0 ? kbase + (real ? j : 0) * p.k_stride + c : vbase + (real ? j : 0) * p.v_stride + c;
-      cp_async16(dst + (uint32_t)((which * F::kTile + row) * D + c) * 4u, src, real);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  if (ntiles > 0) load(0);
-  for (int i = threadIdx.x; i < R * (D / 4); i += 128) {
-    const int row = i / (D / 4), c = (i % (D / 4)) * 4, t = row / p.G;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < rows)
-      x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
-                                           ((long long)w.q0 + w.t0 + t) * p.q_stride + (w.g * p.G + row - t * p.G) * D + c);
-    *reinterpret_cast<float4*>(sq + row * F::kPad + c) = x;
-  }
-  // scores: this lane's row and first key of the warp's eight
-  const int row = lane % R, kk = (lane / R) * KPL;
-  int lo = 0, hi = w.keys;
-  if (RANGES && row < rows) cross_range(p, w, w.t0 + row / p.G, lo, hi);
-  lo = max(lo, key.first), hi = min(hi, key.end);
-  float m = -INFINITY, l = 0.f;  // of the lane's row, the same in its lanes (l: each lane's own keys)
-  float o[R][E];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[r][e] = 0.f;
-  for (int t = 0; t < ntiles; ++t) {
-    if (t + 1 < ntiles) {
-      load(t + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
-    __syncthreads();
-    const float* tk = reinterpret_cast<const float*>(smem + (t & 1) * F::kStage) + warp * 8 * D;
-    const float* tv = tk + F::kTile * D;
-    const int k0 = key.first + t * F::kTile + warp * 8;
-    if (k0 < key.end) {
-      float s[KPL];
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) s[i] = 0.f;
-#pragma unroll 8
-      for (int c = 0; c < D; c += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(sq + row * F::kPad + c);
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) {
-          const float4 k = *reinterpret_cast<const float4*>(tk + (kk + i) * D + c);
-          s[i] = fmaf(q.x, k.x, s[i]), s[i] = fmaf(q.y, k.y, s[i]);
-          s[i] = fmaf(q.z, k.z, s[i]), s[i] = fmaf(q.w, k.w, s[i]);
-        }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) {
-        const int j = k0 + kk + i;
-        s[i] = j >= lo && j < hi ? s[i] : -INFINITY;
-        top = fmaxf(top, s[i] * p.scale_log2);
-      }
-      if (__any_sync(0xffffffffu, top > m + kMaxGrowth)) {
-#pragma unroll
-        for (int x = R; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        float alpha = 1.f;
-        if (top > m) {
-          alpha = m == -INFINITY ? 1.f : exp2f(m - top);
-          m = top;
-        }
-        l *= alpha;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float a = __shfl_sync(0xffffffffu, alpha, r);
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[r][e] *= a;
-        }
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) {
-        const float e = exp2f(fmaf(s[i], p.scale_log2, -ref));
-        l += e;
-        sp[(kk + i) * R + row] = RANGES && s[i] == -INFINITY ? -1.f : e;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float v[E];
-        if constexpr (E == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(tv + j * D + lane * 4);
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(tv + j * D + lane * 2);
-          v[0] = x.x, v[1] = x.y;
-        }
-#pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          const float4 q = *reinterpret_cast<const float4*>(sp + j * R + r);
-          const float pr[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              // (0 times an infinity or a NaN is NaN: a key that a row does not see, weight -1, stays out)
-              if (RANGES) o[r + i][e] = pr[i] < 0.f ? o[r + i][e] : fmaf(pr[i], v[e], o[r + i][e]);
-              else o[r + i][e] = fmaf(pr[i], v[e], o[r + i][e]);
-            }
-        }
-      }
-    }
-    __syncthreads();  // the stage may be filled again, the weights written again
-  }
-  __syncthreads();
-  auto& slices = *reinterpret_cast<typename F::Parts*>(smem);
-#pragma unroll
-  for (int x = R; x < 32; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
-  if (lane < R) slices.m[warp][lane] = m, slices.l[warp][lane] = l;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int e = 0; e < E; ++e) slices.o[warp][r][lane * E + e] = o[r][e];
-  finish<float>(p, w, slices, cluster, piece);
+  finish<T>(p, w, slices, cluster, piece);
 }
 
 // ------------------------------------------------------------------------------ launches
@@ -676,50 +651,45 @@ Meet meet(const CrossPlan& plan, const CrossParams& p, int in_cluster) {
   return {in_cluster, in_cluster};
 }
 
-template <int D, int MT>
+template <typename T, int D, int MT>
 cudaError_t launch_few(const CrossParams& p, const CUtensorMap& mk, const CUtensorMap& mv, long long items, Meet m,
                        cudaStream_t s) {
-  using F = Few<D, MT>;
-  auto kern = p.ranges != nullptr ? few_kernel<D, MT, true> : few_kernel<D, MT, false>;
+  using F = Few<T, D, MT>;
+  auto kern = p.ranges != nullptr ? few_kernel<T, D, MT, true> : few_kernel<T, D, MT, false>;
   return launch_parts(kern, items, m.parts, m.cluster, F::kThreads, F::kSmem, s, mk, mv, p);
 }
-template <int D, int R>
-cudaError_t launch_plain(const CrossParams& p, long long items, Meet m, cudaStream_t s) {
-  auto kern = p.ranges != nullptr ? plain_kernel<D, R, true> : plain_kernel<D, R, false>;
-  return launch_parts(kern, items, m.parts, m.cluster, 128, Plain<D, R>::kSmem, s, p);
-}
 
-template <int D>
-cudaError_t launch_d(const cp_cross_args& a, const CrossPlan& plan, int in_cluster, const CrossParams& p, cudaStream_t s) {
-  const Meet m = meet(plan, p, in_cluster);
-  cudaError_t e;
-  if (a.dtype == CP_F32) {
-    e = plan.rows <= 4 ? launch_plain<D, 4>(p, plan.items, m, s)
-        : plan.rows <= 8 ? launch_plain<D, 8>(p, plan.items, m, s)
-                         : launch_plain<D, 16>(p, plan.items, m, s);
-    if (e != cudaSuccess || p.n_split == 0) return e;
-    return launch_merge<float, D>(p, s);
-  }
+template <typename T, int D>
+cudaError_t launch_t(const cp_cross_args& a, const CrossPlan& plan, Meet m, const CrossParams& p, cudaStream_t s) {
   CUtensorMap mk, mv;
-  constexpr unsigned tile = Few<D, 1>::kTile;
-  const unsigned long long cols = (unsigned long long)p.Hkv * D, rows = (unsigned long long)p.Nkv;
-  const void *k = p.Nkv > 0 ? p.k : p.q, *v = p.Nkv > 0 ? p.v : p.q;  // (no key: never loaded from)
-  const unsigned long long n = p.Nkv > 0 ? rows : 1, ks = p.Nkv > 0 ? a.k_stride : cols, vs = p.Nkv > 0 ? a.v_stride : cols;
-  if (!cp_make_bf16_map_2d(&mk, k, cols, n, ks, tile) || !cp_make_bf16_map_2d(&mv, v, cols, n, vs, tile))
+  constexpr unsigned tile = Few<T, D, 1>::kTile;
+  const unsigned long long cols = (unsigned long long)p.Hkv * D;
+  const bool any = p.Nkv > 0;  // (no key: never loaded from)
+  const unsigned long long n = any ? p.Nkv : 1, ks = any ? a.k_stride : cols, vs = any ? a.v_stride : cols;
+  const auto make = sizeof(T) == 4 ? cp_make_f32_map_2d : cp_make_bf16_map_2d;
+  if (!make(&mk, any ? p.k : p.q, cols, n, ks, tile) || !make(&mv, any ? p.v : p.q, cols, n, vs, tile))
     return cudaErrorInvalidValue;
-  e = plan.rows <= 16 ? launch_few<D, 1>(p, mk, mv, plan.items, m, s)
-      : plan.rows <= 32 ? launch_few<D, 2>(p, mk, mv, plan.items, m, s)
-                        : launch_few<D, 4>(p, mk, mv, plan.items, m, s);
+  const cudaError_t e = plan.rows <= 16 ? launch_few<T, D, 1>(p, mk, mv, plan.items, m, s)
+                        : plan.rows <= 32 ? launch_few<T, D, 2>(p, mk, mv, plan.items, m, s)
+                                          : launch_few<T, D, 4>(p, mk, mv, plan.items, m, s);
   if (e != cudaSuccess || p.n_split == 0) return e;
-  return launch_merge<__nv_bfloat16, D>(p, s);
+  return launch_merge<T, D>(p, s);
 }
 
-// CTAs that are resident at once.
-int slots_of(const cp_cross_args& a, int rows, int sms) { return sms * (a.dtype == CP_F32 || rows <= 16 ? 3 : 1); }
+// Keys of a tile, and CTAs that are resident at once.
+int tile_of(const cp_cross_args& a) { return 16384 / (a.head_dim * (a.dtype == CP_F32 ? 4 : 2)); }
+template <typename T, int D>
+int ctas_of(int rows) {
+  return rows <= 16 ? Few<T, D, 1>::kCtas : rows <= 32 ? Few<T, D, 2>::kCtas : Few<T, D, 4>::kCtas;
+}
+int slots_of(const cp_cross_args& a, int rows, int sms) {
+  if (a.dtype == CP_F32) return sms * (a.head_dim == 64 ? ctas_of<float, 64>(rows) : ctas_of<float, 128>(rows));
+  return sms * (a.head_dim == 64 ? ctas_of<__nv_bfloat16, 64>(rows) : ctas_of<__nv_bfloat16, 128>(rows));
+}
 
 // Parts of an item that meet in a cluster: as many as fill the GPU, each with a tile at least.
 int cluster_of(const cp_cross_args& a, const CrossPlan& c, int sms) {
-  const int tile = a.dtype == CP_F32 ? 32 : a.head_dim == 128 ? 64 : 128;
+  const int tile = tile_of(a);
   const long long key_tiles = ((long long)a.max_seqlen_kv + tile - 1) / tile, slots = slots_of(a, c.rows, sms);
   int parts = 1;
   while (parts < kMaxCluster && 2 * parts <= key_tiles && c.items * parts < slots) parts *= 2;
@@ -732,7 +702,7 @@ int cluster_of(const cp_cross_args& a, const CrossPlan& c, int sms) {
 CrossPlan cp_cross_plan_few(const cp_cross_args& a, int sms) {
   CrossPlan c;
   const int G = a.num_q_heads / a.num_kv_heads;
-  const int most = a.dtype == CP_F32 ? 16 / G : 64 / G;  // tokens of an item
+  const int most = 64 / G;  // tokens of an item
   c.span = a.max_seqlen_q < most ? (a.max_seqlen_q > 0 ? a.max_seqlen_q : 1) : most;
   c.tiles = a.max_seqlen_q > 0 ? (int)(((long long)a.max_seqlen_q + c.span - 1) / c.span) : 1;
   c.rows = c.span * G;
@@ -741,7 +711,7 @@ CrossPlan cp_cross_plan_few(const cp_cross_args& a, int sms) {
   c.split_k = 1;
   // more parts than a cluster takes, through the workspace: where eight leave most of the GPU idle and the keys are
   // many enough to pay for a second launch
-  const int tile = a.dtype == CP_F32 ? 32 : a.head_dim == 128 ? 64 : 128;
+  const int tile = cpattn::tile_of(a);
   const long long key_tiles = ((long long)a.max_seqlen_kv + tile - 1) / tile, slots = cpattn::slots_of(a, c.rows, sms);
   if (c.items * cpattn::kMaxCluster * 2 <= slots && key_tiles >= 8 * cpattn::kMaxCluster) {
     long long k = slots / c.items;
@@ -763,7 +733,9 @@ cudaError_t cp_launch_cross_few(const cp_cross_args& a, float scale, void* ws, s
   const CrossPlan plan = cp_cross_plan_few(a, sms);
   cpattn::CrossParams p;
   cp_cross_fill(p, a, plan, scale, ws, ws_bytes, out, lse);
-  const int in_cluster = cpattn::cluster_of(a, plan, sms);
-  return a.head_dim == 64 ? cpattn::launch_d<64>(a, plan, in_cluster, p, s)
-                          : cpattn::launch_d<128>(a, plan, in_cluster, p, s);
+  const cpattn::Meet m = cpattn::meet(plan, p, cpattn::cluster_of(a, plan, sms));
+  if (a.dtype == CP_F32)
+    return a.head_dim == 64 ? cpattn::launch_t<float, 64>(a, plan, m, p, s) : cpattn::launch_t<float, 128>(a, plan, m, p, s);
+  return a.head_dim == 64 ? cpattn::launch_t<__nv_bfloat16, 64>(a, plan, m, p, s)
+                          : cpattn::launch_t<__nv_bfloat16, 128>(a, plan, m, p, s);
 }

@@ -37,7 +37,7 @@ CROSS = dict(dtype=1, num_seqs=2, num_q_heads=8, num_kv_heads=2, head_dim=128, m
 
 @pytest.mark.parametrize("bad,status", [
     (dict(dtype=2), 1), (dict(num_seqs=0), 1), (dict(num_kv_heads=0), 1), (dict(num_q_heads=7), 1),
-    (dict(num_q_heads=0), 1), (dict(num_q_heads=258), 2), (dict(dtype=0, num_q_heads=34), 2), (dict(head_dim=96), 2),
+    (dict(num_q_heads=0), 1), (dict(num_q_heads=258), 2), (dict(dtype=0, num_q_heads=130), 2), (dict(head_dim=96), 2),
     (dict(max_seqlen_q=-1), 1), (dict(max_seqlen_kv=-1), 1), (dict(total_q=-1), 1), (dict(total_kv=-1), 1),
     (dict(cu_seqlens_q=None), 1), (dict(cu_seqlens_kv=None), 1), (dict(q=None), 1), (dict(k=ODD), 1), (dict(v=None), 1),
     (dict(q_stride=1020), 1), (dict(q_stride=1016), 1), (dict(k_stride=248), 1), (dict(v_stride=260), 1),
