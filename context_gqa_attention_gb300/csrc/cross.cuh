@@ -36,11 +36,11 @@ CP_DEV CrossItem cross_item(const CrossParams& p, unsigned index, bool reporter)
   w.t0 = (int)tile * p.span;
   w.q0 = ld(p.cu_q + w.b);
   w.kv0 = ld(p.cu_kv + w.b);
-  const long long Tq = (long long)ld(p.cu_q + w.b + 1) - w.q0, Tkv = (long long)ld(p.cu_kv + w.b + 1) - w.kv0;
+  const int q1 = ld(p.cu_q + w.b + 1), kv1 = ld(p.cu_kv + w.b + 1), n = p.kv_lens != nullptr ? ld(p.kv_lens + w.b) : 0;
+  const long long Tq = (long long)q1 - w.q0, Tkv = (long long)kv1 - w.kv0;
   reporter = reporter && tile == 0 && w.g == 0;
   w.keys = (int)Tkv;
   if (p.kv_lens != nullptr) {
-    const int n = ld(p.kv_lens + w.b);
     if (reporter && (n < 0 || n > Tkv)) report(p.err, CP_ERR_DEVICE_BOUNDS);
     w.keys = (int)max(0ll, min((long long)n, Tkv));
   }

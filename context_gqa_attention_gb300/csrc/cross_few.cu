@@ -66,7 +66,7 @@ CP_DEV float natural_lse(float M, float L) {
 // What W slices of the CTA's keys made of R rows, in shared memory: reference, sum, unnormalised row.
 template <int D, int W, int R>
 struct Slices {
-  float o[W][R][D];
+  float o[W][R][D + 8];  // (rows 32 bytes apart in the banks)
   float m[W][R], l[W][R];
 };
 
@@ -189,9 +189,10 @@ CP_DEV Keys part_keys(const CrossParams& p, const CrossItem& w, int tile, int pa
 // tile's keys, with a softmax reference of its own, so warps meet at the end only.  The reference moves when a score
 // exceeds it by more than 2^8, which a vote of the warp finds; rows' sums stay in the lanes until the end.
 //
-// f32: each operand is the sum of two tf32 numbers, high and low, and a product the sum of three (high high, high low,
-// low high): 22 bits of each operand count, and the sums are fp32.  A step of the reduction is 32 bytes in both types
-// (16 bf16, 8 tf32), so their tiles and fragments lie alike.
+// f32: each operand is the sum of three bf16 numbers (high, middle, low: 24 bits) and a product the sum of the six of
+// theirs that count, in fp32.  (Three products of tf32 pairs took three times as long: 25 cycles of a sub-partition each
+// against 8.4 for twice the work.  CUDA cores need 32 times fewer rows' worth of padding, but a shared-memory read for
+// every four of their products.)
 CP_DEV void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -207,31 +208,6 @@ CP_DEV void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-CP_DEV void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-CP_DEV uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
-}
-// x = high + low, both tf32.  An infinity or a NaN stays in the high part; `fin` is that part where it is finite, else 0:
-// the factor of the other operand's low part, which may be 0.
-CP_DEV void split(float x, uint32_t& hi, uint32_t& lo, uint32_t& fin) {
-  hi = tf32(x);
-  const float rest = x - __uint_as_float(hi);
-  const bool ok = rest == rest;
-  lo = tf32(ok ? rest : 0.f);
-  fin = ok ? hi : 0u;
-}
-CP_DEV void split(float x, uint32_t& hi, uint32_t& lo) {
-  uint32_t fin;
-  split(x, hi, lo, fin);
-}
 CP_DEV uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -242,13 +218,32 @@ CP_DEV bool clean(uint32_t& w) {
   w &= ~((bad >> 15) * 0xffffu);
   return bad != 0u;
 }
+// x and y = high + middle + low, as pairs of bf16.
+CP_DEV void split(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
+  h = pack2(x, y);
+  x -= __uint_as_float(h << 16), y -= __uint_as_float(h & 0xffff0000u);
+  m = pack2(x, y);
+  x -= __uint_as_float(m << 16), y -= __uint_as_float(m & 0xffff0000u);
+  l = pack2(x, y);
+}
 CP_DEV float as_float(float x) { return x; }
 CP_DEV float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The six products that count, the small ones first.
+CP_DEV void mma_parts(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&am)[4], const uint32_t (&al)[4],
+                      const uint32_t (&h)[2], const uint32_t (&m)[2], const uint32_t (&l)[2]) {
+  mma_bf16(c, al, h[0], h[1]);
+  mma_bf16(c, ah, l[0], l[1]);
+  mma_bf16(c, am, m[0], m[1]);
+  mma_bf16(c, am, h[0], h[1]);
+  mma_bf16(c, ah, m[0], m[1]);
+  mma_bf16(c, ah, h[0], h[1]);
+}
 
 template <typename T, int D, int MT>
 struct Few {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kWK = MT == 4 ? 2 : 4;        // slices of a tile's keys
+  static constexpr int kWK = MT == 4 || (kF32 && D == 128) ? 2 : 4;  // slices of a tile's keys
   static constexpr int kConsumers = MT * kWK;
   static constexpr int kThreads = 32 * (kConsumers + 1);
   static constexpr int kBytes = 16384;               // of a tile of K or of V
@@ -256,13 +251,13 @@ struct Few {
   static constexpr int kKeys = kTile / kWK;          // of a warp
   static constexpr int kMaxStep = kF32 ? 16 : 32;
   static constexpr int kStep = kKeys < kMaxStep ? kKeys : kMaxStep;
+  static_assert(kStep % 16 == 0, "steps of the second product");
   static constexpr int kBoxCols = 128 / (int)sizeof(T), kBoxes = D / kBoxCols;
-  static constexpr int kSteps = D * (int)sizeof(T) / 32;  // of the reduction over a row
-  // q as A fragments in registers (bf16, one row group), or in shared memory: rows 16 bytes apart in the banks; f32: high
-  // parts, then low parts
+  // q as A fragments in registers (bf16, one row group), or in shared memory: rows 16 bytes apart in the banks; f32: the
+  // three parts one behind the other
   static constexpr bool kQRegs = !kF32 && MT == 1;
-  static constexpr int kQPitch = D * (int)sizeof(T) + 16;
-  static constexpr int kQBytes = kQRegs ? 0 : 16 * MT * kQPitch * (kF32 ? 2 : 1);
+  static constexpr int kQPitch = D * 2 + 16, kQPart = 16 * MT * kQPitch;
+  static constexpr int kQBytes = kQRegs ? 0 : kQPart * (kF32 ? 3 : 1);
   using Parts = Slices<D, kWK, 16 * MT>;
   static constexpr int align16(int x) { return (x + 15) / 16 * 16; }
   static constexpr int smem_of(int stages) {
@@ -284,6 +279,7 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
                const int parts, const int cluster) {
   using F = Few<T, D, MT>;
   constexpr int NT = F::kStep / 8;
+  constexpr bool kRestore = RANGES || F::kF32;  // V may be cleaned
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_range[4];
   __shared__ uint32_t s_abort;
@@ -332,19 +328,26 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
   if (threadIdx.x == 0)
     for (int t = 0; t < early; ++t) load(t);
   if constexpr (!F::kQRegs) {
-    constexpr int kVec = 16 / (int)sizeof(T);
-    for (int i = threadIdx.x; i < 16 * MT * (D / kVec); i += F::kThreads) {
-      const int row = i / (D / kVec), c = (i % (D / kVec)) * kVec;
-      uint8_t* dst = sbase + F::oQ + row * F::kQPitch + c * (int)sizeof(T);
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (row < rows) x = *reinterpret_cast<const uint4*>(q_row(row) + c);
-      if constexpr (F::kF32) {
-        uint4 lo;
-        split(__uint_as_float(x.x), x.x, lo.x), split(__uint_as_float(x.y), x.y, lo.y);
-        split(__uint_as_float(x.z), x.z, lo.z), split(__uint_as_float(x.w), x.w, lo.w);
-        *reinterpret_cast<uint4*>(dst + 16 * MT * F::kQPitch) = lo;
+    for (int i = threadIdx.x; i < 16 * MT * (D / 8); i += F::kThreads) {
+      const int row = i / (D / 8), c = (i % (D / 8)) * 8;
+      uint4* dst = reinterpret_cast<uint4*>(sbase + F::oQ + row * F::kQPitch + c * 2);
+      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+      if (row < rows) {
+        const uint4* q = reinterpret_cast<const uint4*>(q_row(row) + c);
+        x = q[0];
+        if constexpr (F::kF32) y = q[1];
       }
-      *reinterpret_cast<uint4*>(dst) = x;
+      if constexpr (F::kF32) {
+        uint4 h, m, l;
+        split(__uint_as_float(x.x), __uint_as_float(x.y), h.x, m.x, l.x);
+        split(__uint_as_float(x.z), __uint_as_float(x.w), h.y, m.y, l.y);
+        split(__uint_as_float(y.x), __uint_as_float(y.y), h.z, m.z, l.z);
+        split(__uint_as_float(y.z), __uint_as_float(y.w), h.w, m.w, l.w);
+        dst[F::kQPart / 16] = m;
+        dst[2 * F::kQPart / 16] = l;
+        x = h;
+      }
+      *dst = x;
     }
   }
   __syncthreads();
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
     __syncwarp();
   } else if (wm * 16 < rows) {
     // ---- a consumer's rows and their keys
-    uint32_t qa[F::kQRegs ? F::kSteps : 1][4];
+    uint32_t qa[F::kQRegs ? D / 16 : 1][4];
     int lo[2] = {0, 0}, hi[2] = {w.keys, w.keys};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
       if constexpr (F::kQRegs) {
         const T* q = q_row(real ? row : 0);
 #pragma unroll
-        for (int k = 0; k < F::kSteps; ++k) {
+        for (int k = 0; k < D / 16; ++k) {
           qa[k][r] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * tig) : 0u;
           qa[k][r + 2] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * tig) : 0u;
         }
@@ -412,53 +415,39 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
         float c[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
-        // S = Q K^T: a matrix is 8 keys' 16 bytes
-        auto k_at = [&](int row, int k, int chunk) -> uint32_t {  // 16-byte chunk of the step-pairs' 128 bytes
-          return sk + (uint32_t)((k / 4) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4);
-        };
-        auto qk = [&](float (&c)[4], const uint32_t (&a)[4], const uint32_t (&al)[4], uint32_t b0, uint32_t b1) {
-          if constexpr (F::kF32) {
-            uint32_t h0, h1, l0, l1, f0, f1;
-            split(__uint_as_float(b0), h0, l0, f0);
-            split(__uint_as_float(b1), h1, l1, f1);
-            mma_tf32(c, al, f0, f1);
-            mma_tf32(c, a, l0, l1);
-            mma_tf32(c, a, h0, h1);
-          } else {
-            mma_bf16(c, a, b0, b1);
-          }
-        };
-        auto q_step = [&](int k, uint32_t (&a)[4], uint32_t (&al)[4]) {
+        // S = Q K^T
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t a[F::kF32 ? 3 : 1][4];
           if constexpr (F::kQRegs) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = qa[k][i];
+            for (int i = 0; i < 4; ++i) a[0][i] = qa[k][i];
           } else {
-            ldsm4(a, sq + 32u * k);
-            if constexpr (F::kF32) ldsm4(al, sq + 32u * k + 16 * MT * F::kQPitch);
+#pragma unroll
+            for (int i = 0; i < (F::kF32 ? 3 : 1); ++i) ldsm4(a[i], sq + 32u * k + (uint32_t)(i * F::kQPart));
           }
-        };
-        if constexpr (NT == 1) {
+          if constexpr (F::kF32) {
 #pragma unroll
-          for (int k = 0; k < F::kSteps; k += 2) {
-            uint32_t b[4], a[4], al[4];
-            ldsm4(b, k_at(r0 + (lane & 7), k, 2 * (k & 3) + (lane >> 3)));
+            for (int i = 0; i < NT; ++i) {
+              const int row = r0 + 8 * i + gid;
+              uint32_t h[2], m[2], l[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              q_step(k + i, a, al);
-              qk(c[0], a, al, b[2 * i], b[2 * i + 1]);
+              for (int e = 0; e < 2; ++e) {  // dims 16 k + 8 e + 2 tig and the next
+                const int chunk = 4 * (k & 1) + 2 * e + (tig >> 1);
+                const float2 x = *reinterpret_cast<const float2*>(sbase + (sk - base) + (k / 2) * F::kTile * 128 + row * 128 +
+                                                                  ((chunk ^ (row & 7)) << 4) + (tig & 1) * 8);
+                split(x.x, x.y, h[e], m[e], l[e]);
+              }
+              mma_parts(c[i], a[0], a[1], a[2], h, m, l);
             }
-          }
-        } else {
+          } else {
 #pragma unroll
-          for (int k = 0; k < F::kSteps; ++k) {
-            uint32_t a[4], al[4];
-            q_step(k, a, al);
-#pragma unroll
-            for (int i = 0; i + 1 < NT; i += 2) {
+            for (int i = 0; i < NT; i += 2) {  // a matrix is 8 keys' 16 bytes
+              const int row = r0 + 8 * i + ((lane >> 4) << 3) + (lane & 7), chunk = 2 * (k & 3) + ((lane >> 3) & 1);
               uint32_t b[4];
-              ldsm4(b, k_at(r0 + 8 * i + ((lane >> 4) << 3) + (lane & 7), k, 2 * (k & 3) + ((lane >> 3) & 1)));
-              qk(c[i], a, al, b[0], b[1]);
-              qk(c[i + 1], a, al, b[2], b[3]);
+              ldsm4(b, sk + (uint32_t)((k / 4) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
+              mma_bf16(c[i], a[0], b[0], b[1]);
+              mma_bf16(c[i + 1], a[0], b[2], b[3]);
             }
           }
         }
@@ -517,37 +506,39 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
           }
           __syncwarp();
         }
-        // O += P V: the scores' fragments are the MMA's A operand as they lie (f32: its columns tig and tig + 4 are keys
-        // 2 tig and 2 tig + 1, and so are the rows of V's fragments)
+        // O += P V: the scores' fragments are the MMA's A operand as they lie
         bool bad = false;
-        if constexpr (F::kF32) {
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            uint32_t ph[4], pl[4];
-            split(c[i][0], ph[0], pl[0]), split(c[i][2], ph[1], pl[1]);
-            split(c[i][1], ph[2], pl[2]), split(c[i][3], ph[3], pl[3]);
-            const int row = r0 + 8 * i + 2 * tig;
+        for (int i = 0; i < NT; i += 2) {
+          if constexpr (F::kF32) {
+            uint32_t ph[4], pm[4], pl[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              split(c[i + (e >> 1)][2 * (e & 1)], c[i + (e >> 1)][2 * (e & 1) + 1], ph[e], pm[e], pl[e]);
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
-              float x[2];
+              uint32_t h[2], m[2], l[2];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int chunk = 2 * (n & 3) + (gid >> 2);
-                x[e] = *reinterpret_cast<const float*>(sbase + (sv - base) + (n / 4) * F::kTile * 128 + (row + e) * 128 +
-                                                       ((chunk ^ ((row + e) & 7)) << 4) + (gid & 3) * 4);
-                if (RANGES && !whole && !isfinite(x[e])) x[e] = 0.f, bad = true;
+              for (int e = 0; e < 2; ++e) {  // keys 2 tig + 8 e and the next, dim 8 n + gid
+                float x[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                  const int row = r0 + 8 * i + 8 * e + 2 * tig + f, chunk = 2 * (n & 3) + (gid >> 2);
+                  x[f] = *reinterpret_cast<const float*>(sbase + (sv - base) + (n / 4) * F::kTile * 128 + row * 128 +
+                                                         ((chunk ^ (row & 7)) << 4) + (gid & 3) * 4);
+                }
+                split(x[0], x[1], h[e], m[e], l[e]);
+                // (an infinity's middle part would be NaN, and 0 times it is NaN)
+                const uint32_t odd = ((h[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                if (odd != 0u) {
+                  const uint32_t keep = ~((odd >> 15) * 0xffffu);
+                  h[e] &= keep, m[e] &= keep, l[e] &= keep;
+                  bad = true;
+                }
               }
-              uint32_t h0, h1, l0, l1, f0, f1;
-              split(x[0], h0, l0, f0);
-              split(x[1], h1, l1, f1);
-              mma_tf32(o[n], pl, f0, f1);
-              mma_tf32(o[n], ph, l0, l1);
-              mma_tf32(o[n], ph, h0, h1);
+              mma_parts(o[n], ph, pm, pl, h, m, l);
             }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i + 1 < NT; i += 2) {
+          } else {
             const uint32_t pa[4] = {pack2(c[i][0], c[i][1]), pack2(c[i][2], c[i][3]), pack2(c[i + 1][0], c[i + 1][1]),
                                     pack2(c[i + 1][2], c[i + 1][3])};
             const int row = r0 + 8 * i + (((lane >> 3) & 1) << 3) + (lane & 7);
@@ -564,13 +555,13 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
             }
           }
         }
-        if (RANGES && __any_sync(0xffffffffu, bad)) u0 = min(u0, k0), u1 = max(u1, k0 + F::kStep);
+        if (kRestore && __any_sync(0xffffffffu, bad)) u0 = min(u0, k0), u1 = max(u1, k0 + F::kStep);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
     }
     if (!ok && lane == 0) fail();
-    if (RANGES && u1 >= 0) {
+    if (kRestore && u1 >= 0) {
       // what was taken out of V for the rows that see it: p > 0 times it is itself, whatever p is.  The warp's keys
       // are one slice in kWK of every tile.
       const T* v = static_cast<const T*>(p.v) + (long long)w.kv0 * p.v_stride + w.g * D;
@@ -687,13 +678,18 @@ int slots_of(const cp_cross_args& a, int rows, int sms) {
   return sms * (a.head_dim == 64 ? ctas_of<__nv_bfloat16, 64>(rows) : ctas_of<__nv_bfloat16, 128>(rows));
 }
 
-// Parts of an item that meet in a cluster: as many as fill the GPU, each with a tile at least.
+// Parts of an item that meet in a cluster: as many as the GPU takes at once, each with a tile at least.  More items than
+// that: parts of eight tiles or more until there are four times as many as the GPU takes, so that the last ones are short.
 int cluster_of(const cp_cross_args& a, const CrossPlan& c, int sms) {
   const int tile = tile_of(a);
   const long long key_tiles = ((long long)a.max_seqlen_kv + tile - 1) / tile, slots = slots_of(a, c.rows, sms);
-  int parts = 1;
-  while (parts < kMaxCluster && 2 * parts <= key_tiles && c.items * parts < slots) parts *= 2;
-  return parts;
+  long long parts = slots / c.items;
+  if (parts < 1) {
+    parts = (4 * slots + c.items - 1) / c.items;
+    if (parts > key_tiles / 8) parts = key_tiles / 8;
+  }
+  if (parts > key_tiles) parts = key_tiles;
+  return (int)(parts < 1 ? 1 : parts > kMaxCluster ? kMaxCluster : parts);
 }
 
 }  // namespace

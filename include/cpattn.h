@@ -589,8 +589,8 @@ cp_status cp_decode_attention_q4(const cp_decode_args* args, const cp_score_mod*
  *     (skipped), with more rows than max_seqlen_q (the rest is left out), or with kv_lens[b] outside
  *     [0, its rows] (taken as the nearest of the two).  max_seqlen_kv only guides the cut: any value is right.
  * Weights and values are summed before they are divided: finite components of v are below 2^96.
- * bf16: P is rounded to bf16 for the tensor cores; num_q_heads / num_kv_heads <= 128.  f32: operands
- * count with 22 bits (pairs of tf32 numbers), sums are fp32; <= 64.
+ * bf16: P is rounded to bf16 for the tensor cores; num_q_heads / num_kv_heads <= 128.  f32: products
+ * of 24 bits summed in fp32; <= 64.
  * ---------------------------------------------------------------------------- */
 typedef struct cp_cross_args {
   int32_t dtype;                /* cp_dtype of q, k, v, out                             */
