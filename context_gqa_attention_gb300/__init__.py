@@ -851,9 +851,10 @@ def cp_decode_attention_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, inte
 # ---------------------------------------------------------- cross attention, beam search
 
 def cp_cross_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_kv, *,
-                                      dtype=torch.bfloat16):
+                                      total_q=None, total_kv=None, padded=False, dtype=torch.bfloat16):
     """Bytes of workspace with which cp_cross_attention cuts the keys of these sizes into parts on the current
-    device (0: it does not)."""
+    device (0: it does not).  total_q, total_kv: rows of q and of k (num_seqs of the longest, if not given); padded:
+    the call gets kv_lens or key_ranges."""
     load()
     a = CrossArgs()
     if dtype not in (torch.bfloat16, torch.float32):
@@ -861,6 +862,10 @@ def cp_cross_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_
     a.dtype, a.num_seqs, a.head_dim = _TYPE[dtype], num_seqs, head_dim
     a.num_q_heads, a.num_kv_heads = num_q_heads, num_kv_heads
     a.max_seqlen_q, a.max_seqlen_kv = max_seqlen_q, max_seqlen_kv
+    a.total_q = num_seqs * max_seqlen_q if total_q is None else total_q
+    a.total_kv = num_seqs * max_seqlen_kv if total_kv is None else total_kv
+    if padded:
+        a.kv_lens = 1       # (whether there is one is all that counts here)
     need = ctypes.c_size_t()
     _check(_LIB.cp_cross_attention_workspace_size(ctypes.byref(a), ctypes.byref(need)))
     return need.value

@@ -40,18 +40,20 @@ struct Smem {
   static constexpr int oBar = oKV + kSlots * kKV;
   static constexpr int bQ = 0, bFull = 1, bEmpty = bFull + kSlots, bS = bEmpty + kSlots, bP = bS + 2, bO = bP + 2,
                        bFix = bO + 2, bLast = bFix + 2, bDone = bLast + 1, nBar = bDone + 1;
-  static constexpr int oMisc = oBar + nBar * 8;  // TMEM base, abort flag, first / last unclean tile, keys
-  static constexpr int kBytes = oMisc + 32;
+  static constexpr int oMisc = oBar + nBar * 8;  // TMEM base, abort flag, first / last unclean tile, keys of each row tile
+  static constexpr int kBytes = oMisc + 48;
   // the base is rounded up to the 1 KB swizzle atom; never below 120 KB, so that one CTA (and its 512 TMEM
   // columns) has an SM to itself
   static constexpr int kAlloc = (kBytes + 1024) > 120 * 1024 ? (kBytes + 1024) : 120 * 1024;
   static_assert(kAlloc <= 232448, "dynamic shared memory beyond the 227 KB per-CTA limit");
 };
 
-// Columns outside [c0, c1) of a row's 128 scores.
-CP_DEV void mask_columns(float (&v)[32], int at, int c0, int c1) {
+// Columns outside [c0, c1), by bits, which become predicates several at a time.
+CP_DEV uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+CP_DEV void mask_columns(float (&v)[32], int c0, int c1) {
+  const uint32_t seen = first_bits(c1) & ~first_bits(c0);
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v[k] = at + k >= c0 && at + k < c1 ? v[k] : -INFINITY;
+  for (int k = 0; k < 32; ++k) v[k] = (seen & (1u << k)) != 0u ? v[k] : -INFINITY;
 }
 
 template <int D, bool RANGES>
@@ -106,10 +108,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc[1] = 0;
     misc[2] = 0x7fffffff;  // unclean tiles
     misc[3] = -1;
-    misc[4] = 0x7fffffff;  // keys that some row sees
-    misc[5] = 0;
-    misc[6] = 0;           // keys that every row sees
-    misc[7] = 0x7fffffff;
+    for (int i = 4; i < 12; i += 4) {
+      misc[i] = 0x7fffffff;  // [4, 5): keys that some row of tile 0 sees, [6, 7): that every row sees; then tile 1
+      misc[i + 1] = 0;
+      misc[i + 2] = 0;
+      misc[i + 3] = 0x7fffffff;
+    }
     fence_mbar_init();
     tma_prefetch_desc(&map_q);
     mbar_expect_tx(bar(Sm::bQ), (two ? 2 : 1) * KB * per_tile * p.G * 128);
@@ -131,28 +135,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = threadIdx.x; t < w.tokens; t += kThreads) {
       int lo, hi;
       cross_range(p, w, w.t0 + t, lo, hi);
+      int* m = misc + (t < per_tile ? 4 : 8);
       if (lo < hi) {
-        atomicMin(misc + 4, lo);
-        atomicMax(misc + 5, hi);
+        atomicMin(m, lo);
+        atomicMax(m + 1, hi);
       }
-      atomicMax(misc + 6, lo);
-      atomicMin(misc + 7, hi);
+      atomicMax(m + 2, lo);
+      atomicMin(m + 3, hi);
     }
     __syncthreads();
   }
   tc_fence_after();
   const uint32_t tmem = (uint32_t)misc[0];
-  const int key_lo = RANGES ? misc[4] : 0, key_hi = RANGES ? misc[5] : w.keys;
-  const int all_lo = RANGES ? misc[6] : 0, all_hi = RANGES ? misc[7] : w.keys;
-  // key tiles of this CTA, counted from key_lo
+  // Key tiles of this CTA, counted from the first key that some row sees; each row tile works on those that one of its
+  // rows sees.
+  const int key_lo = RANGES ? min(misc[4], misc[8]) : 0, key_hi = RANGES ? max(misc[5], misc[9]) : w.keys;
   const int every = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
   const int ta = piece < 0 ? 0 : (int)((long long)every * part / p.split_k);
   const int ntiles = (piece < 0 ? every : (int)((long long)every * (part + 1) / p.split_k)) - ta;
   const int k_first = key_lo + ta * BN;  // first key
-  auto in_part = [&](int t) -> bool {    // some row sees only a part of key tile t
+  int t_lo[2], t_hi[2], all_lo[2], all_hi[2];  // a row tile's key tiles; the keys that all its rows see
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int lo = RANGES ? misc[4 + 4 * i] : 0, hi = RANGES ? misc[5 + 4 * i] : w.keys;
+    const bool any = (i == 0 || two) && lo < hi;
+    t_lo[i] = any ? min(ntiles, max(0, (lo - k_first) / BN)) : 0;
+    t_hi[i] = any ? max(t_lo[i], min(ntiles, (hi - k_first + BN - 1) / BN)) : 0;
+    all_lo[i] = RANGES ? misc[6 + 4 * i] : 0;
+    all_hi[i] = RANGES ? misc[7 + 4 * i] : w.keys;
+  }
+  auto has = [&](int i, int t) -> bool { return t >= t_lo[i] && t < t_hi[i]; };
+  auto in_part = [&](int t) -> bool {  // some row that works on key tile t sees only a part of it
     const int k0 = k_first + t * BN;
-    return k0 + BN > all_hi || (RANGES && k0 < all_lo);
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = r || (has(i, t) && (k0 + BN > all_hi[i] || (RANGES && k0 < all_lo[i])));
+    return r;
   };
+  // keys of tile t that some row may see; 32 or fewer (a last tile) take a short way
+  auto keys_in = [&](int t) -> int { return key_hi - k_first - t * BN; };
   // Without ranges the guards have only the last V tile to clean, if at all.  It lands at a barrier of its own: on the
   // ring's they would have to follow every phase, in step with the issuer.
   const bool clean_last = !RANGES && in_part(ntiles - 1);
@@ -232,23 +253,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(bar(Sm::bS + tile));
         };
-        auto issue_pv = [&](int tile, int slot, bool acc) {
+        auto issue_pv = [&](int tile, int slot, bool acc, bool few) {
           const uint64_t dv = desc_advance(dv0, (uint32_t)(slot * Sm::kKV));
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
+          for (int kk = 0; kk < BN / 16; ++kk) {
+            if (kk == 2 && few) break;
             mma_ts(tmem + 256u + (uint32_t)(tile * D), tmem + (uint32_t)(tile * BN + kk * 8),
                    desc_advance(dv, kk * 16u * 128u), id_pv, acc || kk > 0);
+          }
           mma_commit(bar(Sm::bO + tile));
         };
         bool ok = mbar_wait(bar(Sm::bQ), 0u, abort_flag, kBudget) && mbar_wait(bar(Sm::bFull), 0u, abort_flag, kBudget);
         if (ok) {
           tc_fence_after();
-          issue_qk(0, 0);
-          if (two) issue_qk(1, 0);
+          if (has(0, 0)) issue_qk(0, 0);
+          if (has(1, 0)) issue_qk(1, 0);
           mma_commit(bar(Sm::bEmpty + 0));
         }
         for (int t = 0; ok && t < ntiles; ++t) {
           const int iv = 2 * t + 1, ik = 2 * t + 2, sv = iv % kSlots, sk = ik % kSlots;
+          const bool few = keys_in(t) <= 32;
           // V(t), with ranges and in a last tile in part as the guards leave it
           if (!RANGES && clean_last && t == ntiles - 1) {
             ok = mbar_wait(bar(Sm::bFix), 0u, abort_flag, kBudget);
@@ -256,26 +280,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait(bar(Sm::bFull + sv), (uint32_t)(iv / kSlots) & 1u, abort_flag, kBudget);
             if (RANGES) ok = ok && mbar_wait(bar(Sm::bFix + (t & 1)), (uint32_t)(t >> 1) & 1u, abort_flag, kBudget);
           }
-          ok = ok && mbar_wait(bar(Sm::bP + 0), (uint32_t)t & 1u, abort_flag, kBudget);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(0, sv, t > 0);
+          if (has(0, t)) {
+            ok = ok && mbar_wait(bar(Sm::bP + 0), (uint32_t)(t - t_lo[0]) & 1u, abort_flag, kBudget);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(0, sv, t > t_lo[0], few);
+          }
           const bool more = t + 1 < ntiles;
           if (more) {
-            ok = mbar_wait(bar(Sm::bFull + sk), (uint32_t)(ik / kSlots) & 1u, abort_flag, kBudget);
+            ok = ok && mbar_wait(bar(Sm::bFull + sk), (uint32_t)(ik / kSlots) & 1u, abort_flag, kBudget);
             if (!ok) break;
             tc_fence_after();
-            issue_qk(0, sk);
+            if (has(0, t + 1)) issue_qk(0, sk);
           }
-          if (two) {
-            ok = mbar_wait(bar(Sm::bP + 1), (uint32_t)t & 1u, abort_flag, kBudget);
+          if (has(1, t)) {
+            ok = ok && mbar_wait(bar(Sm::bP + 1), (uint32_t)(t - t_lo[1]) & 1u, abort_flag, kBudget);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(1, sv, t > 0);
+            issue_pv(1, sv, t > t_lo[1], few);
           }
+          if (!ok) break;
           mma_commit(bar(Sm::bEmpty + sv));
           if (more) {
-            if (two) issue_qk(1, sk);
+            if (has(1, t + 1)) issue_qk(1, sk);
             mma_commit(bar(Sm::bEmpty + sk));
           }
         }
@@ -321,7 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_inc<kRegsSoftmax>();
     const int tile = (warp - 4) >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane, rows = tile == 0 ? rows0 : rows1;
-    if (rows > 0) {
+    const int t0 = t_lo[tile], t1 = t_hi[tile];
+    if (rows > 0 && t0 == t1) {  // no key for this tile's rows
+      if (row < rows) {
+        const long long o = out_row(tile, row);
+        if (piece >= 0) {
+          p.ws_lse[(long long)piece * p.rows + tile * per_tile * p.G + row] = -INFINITY;
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o * D);
+          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse != nullptr) p.lse[o] = -INFINITY;
+        }
+      }
+    } else if (rows > 0) {
       const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
       const uint32_t tS = tmem + lane_off + (uint32_t)(tile * BN);
       const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(tile * D);
@@ -329,34 +368,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (RANGES && row < rows) cross_range(p, w, w.t0 + tile * per_tile + row / p.G, lo, hi);
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int t = 0; t < ntiles; ++t) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)t & 1u, abort_flag, kBudget));
+      for (int t = t0; t < t1; ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bS + tile), (uint32_t)(t - t0) & 1u, abort_flag, kBudget));
         if (!ok) break;
         tc_fence_after();
-        float s0[32], s1[32], s2[32], s3[32];
-        load_row(tS, s0, s1, s2, s3);
         const int k0 = k_first + t * BN;
-        int lim = hi - 1 - k0;
-        if constexpr (RANGES) {
-          if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + BN)) {
-            mask_columns(s0, 0, lo - k0, hi - k0);
-            mask_columns(s1, 32, lo - k0, hi - k0);
-            mask_columns(s2, 64, lo - k0, hi - k0);
-            mask_columns(s3, 96, lo - k0, hi - k0);
+        float s0[32], s1[32], s2[32], s3[32];
+        float alpha;
+        if (keys_in(t) <= 32) {  // a last tile of few keys
+          tmem_ld32(tS, s0);
+          tmem_wait_ld(s0);
+          mask_columns(s0, lo - k0, hi - k0);
+          float mt = s0[0];
+#pragma unroll
+          for (int k = 1; k < 32; ++k) mt = fmaxf(mt, s0[k]);
+          mt *= p.scale_log2;
+          alpha = 1.f;
+          if (mt > m + kRescaleThreshold) {
+            alpha = ex2(m - mt);
+            m = mt;
           }
-          lim = BN - 1;
+          const float neg = m == -INFINITY ? 0.f : -m;
+          uint64_t sum2 = f2(0.f, 0.f);
+          exp_pack_tmem(s0, f2(p.scale_log2, p.scale_log2), f2(neg, neg), sum2, tS);
+          tmem_wait_st();
+          float a, b;
+          f2u(sum2, a, b);
+          l = l * alpha + (a + b);
+        } else {
+          load_row(tS, s0, s1, s2, s3);
+          int lim = hi - 1 - k0;
+          if constexpr (RANGES) {
+            if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + BN)) {
+              mask_columns(s0, lo - k0, hi - k0);
+              mask_columns(s1, lo - k0 - 32, hi - k0 - 32);
+              mask_columns(s2, lo - k0 - 64, hi - k0 - 64);
+              mask_columns(s3, lo - k0 - 96, hi - k0 - 96);
+            }
+            lim = BN - 1;
+          }
+          alpha = row_max_update(s0, s1, s2, s3, lim, p.scale_log2, m);
+          // S(t) complete implies PV(t-1) complete (it was issued before QK(t)): O is stable and the S columns may
+          // take P(t)
+          l = l * alpha + row_exp_tmem(s0, s1, s2, s3, p.scale_log2, m, tS);
         }
-        const float alpha = row_max_update(s0, s1, s2, s3, lim, p.scale_log2, m);
-        // S(t) complete implies PV(t-1) complete (it was issued before QK(t)): O is stable and the S columns may
-        // take P(t)
-        l = l * alpha + row_exp_tmem(s0, s1, s2, s3, p.scale_log2, m, tS);
-        if (t > 0) rescale_o<D>(tO, alpha);
+        if (t > t0) rescale_o<D>(tO, alpha);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Sm::bP + tile));
       }
       if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bO + tile), (uint32_t)(ntiles - 1) & 1u, abort_flag, kBudget));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bO + tile), (uint32_t)(t1 - t0 - 1) & 1u, abort_flag, kBudget));
+      // (with ranges a row tile may be done before the other, whose operands lie where it would stage its rows)
+      if (RANGES && ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(Sm::bDone), 0u, abort_flag, kBudget));
       if (ok) {
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -478,32 +542,41 @@ cudaError_t launch(const cp_cross_args& a, const CrossPlan& plan, float scale, v
 }  // namespace
 }  // namespace cpattn
 
-// Items take about 4 us and 1.7 us a key tile, one on an SM; a cut costs a merge of about 3 us.  The items of whole
-// waves stay whole; the rest are cut into the number of parts that ends soonest by that estimate.  With lengths
-// that differ, the items that there are can only be guessed, so all are cut or none.
+// Time of an item: about 2.5 us and 1.75 a key tile (d = 64: 3 and 1.3), one on an SM; a part takes 3 us more to write its
+// fp32 rows, and the merge about 3 us and 0.05 a part.
+// Of items that are all alike, those of whole waves stay whole and the rest are cut into the number of parts that ends
+// soonest by that estimate.  Where they differ, how many there are and how long can only be guessed from the totals, and all
+// are cut or none: the load of an SM and half of the longest item decide.
 CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms) {
   CrossPlan c;
   const int G = a.num_q_heads / a.num_kv_heads;
+  const double B = a.num_seqs;
   c.span = 2 * (cpattn::BM / G);
   c.tiles = a.max_seqlen_q > 0 ? (int)(((long long)a.max_seqlen_q + c.span - 1) / c.span) : 1;
   c.rows = c.span * G;
   c.items = (long long)a.num_seqs * a.num_kv_heads * c.tiles;
   c.n_split = 0;
   c.split_k = 1;
-  const bool even = (long long)a.num_seqs * a.max_seqlen_q <= a.total_q;
-  const double live = even ? (double)c.items
-                           : fmin((double)c.items, a.num_kv_heads * ((double)a.total_q / c.span + 0.5 * a.num_seqs));
-  const double key_tiles = ceil(a.max_seqlen_kv / (double)cpattn::BN);
-  const double waves = even ? floor(live / sms) : 0, rest = live - waves * sms;
+  const bool alike = a.key_ranges == nullptr && a.kv_lens == nullptr &&
+                     (a.num_seqs == 1 || (B * a.max_seqlen_q <= a.total_q && B * a.max_seqlen_kv <= a.total_kv));
+  const double most = ceil(a.max_seqlen_kv / (double)cpattn::BN);
+  const double usual = alike ? most : fmin(most, ceil(a.total_kv / B / cpattn::BN));
+  const double live = alike ? (double)c.items
+                            : fmin((double)c.items, a.num_kv_heads * ((double)a.total_q / c.span + 0.5 * B));
+  const double fixed = a.head_dim == 64 ? 3 : 2.5, tile = a.head_dim == 64 ? 1.3 : 1.75;
+  const double waves = alike ? floor(live / sms) : 0, rest = live - waves * sms;
   double best = 0;
-  for (int k = 1; k <= 32 && k <= key_tiles && (k == 1 || rest * k <= 4.0 * sms); ++k) {
-    const double t = ceil(rest * k / sms) * (4 + 1.7 * ceil(key_tiles / k)) + (k > 1 ? 3 : 0);
+  for (int k = 1; k <= 32 && k <= most && (k == 1 || rest * k <= 4.0 * sms); ++k) {
+    const double set_up = k > 1 ? fixed + 3 : fixed;
+    const double part = set_up + tile * ceil(usual / k), longest = set_up + tile * ceil(most / k);
+    double t = alike ? ceil(rest * k / sms) * part : fmax(rest * k * part / sms + 0.5 * longest, longest);
+    if (k > 1) t += 3 + 0.05 * rest * k;
     if (k == 1 || t < 0.97 * best) {
       best = t;
       c.split_k = k;
     }
   }
-  if (c.split_k > 1) c.n_split = even ? (long long)rest : c.items;
+  if (c.split_k > 1) c.n_split = alike ? (long long)rest : c.items;
   if (c.n_split == 0) c.split_k = 1;
   c.bytes = cp_cross_parts_bytes(c, a.head_dim);
   return c;

@@ -13,37 +13,36 @@ namespace {
 // the V rows behind the last key that any row sees (another sequence's tokens, or anything behind
 // the last sequence), and in the others every element that is not finite; they say whether there
 // was one, and the rows that do see it add it back at the end (see restore).
+// Nearly always there is none, so the tile is only read, several vectors at a time (the MMAs wait for this: cleaning
+// each vector as it came took 5k cycles a tile, longer than the tile's softmax).
 template <int D, int BN>
 CP_DEV bool guard_v(uint8_t* sv, int last, int part) {
-  bool unclean = false;
   // 16-byte vectors of the tile's two (one) 64-column blocks, 128 rows of 128 bytes each; the
   // swizzle only permutes the vectors within a row
-  constexpr int kVec = BN * D * 2 / 16;
-#pragma unroll 4
-  for (int i = part; i < kVec; i += 64) {
-    const int row = (i >> 3) & (BN - 1);
-    uint4* p = reinterpret_cast<uint4*>(sv) + i;
-    if (row >= last) {
-      *p = make_uint4(0u, 0u, 0u, 0u);
-      continue;
-    }
-    uint4 x = *p;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-    uint32_t any = 0;
-    // exponent of all ones: adding one to it carries into the sign's place
+  constexpr int kVec = BN * D * 2 / 16, kAtOnce = 8;
+  uint4* v = reinterpret_cast<uint4*>(sv);
+  // exponent of all ones: adding one to it carries into the sign's place
+  auto odd = [](uint32_t w) -> uint32_t { return (w & 0x7f807f80u) + 0x00800080u; };
+  if (last < BN)
+    for (int i = part; i < kVec; i += 64)
+      if (((i >> 3) & (BN - 1)) >= last) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int i = part; i < kVec; i += 64 * kAtOnce) {
+    uint4 x[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) any |= ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-    if (any != 0u) {
+    for (int k = 0; k < kAtOnce; ++k) x[k] = v[i + 64 * k];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t bad = ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-        w[e] &= ~((bad >> 15) * 0xffffu);  // 0xffff in each half that is not finite
-      }
-      *p = x;
-      unclean = true;
-    }
+    for (int k = 0; k < kAtOnce; ++k) any |= (odd(x[k].x) | odd(x[k].y)) | (odd(x[k].z) | odd(x[k].w));
   }
-  return unclean;
+  if ((any & 0x80008000u) == 0u) return false;
+#pragma unroll 1
+  for (int i = part; i < kVec; i += 64) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(v + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] &= ~(((odd(w[e]) & 0x80008000u) >> 15) * 0xffffu);  // 0xffff in each half that is not finite
+  }
+  return true;
 }
 
 // What the guard took out of V for a row that sees it: p > 0 times an infinity or a NaN is that
