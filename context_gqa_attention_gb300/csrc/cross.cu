@@ -559,6 +559,7 @@ CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms) {
   c.split_k = 1;
   const bool alike = a.key_ranges == nullptr && a.kv_lens == nullptr &&
                      (a.num_seqs == 1 || (B * a.max_seqlen_q <= a.total_q && B * a.max_seqlen_kv <= a.total_kv));
+  c.ordered = !alike && a.num_seqs > 1 && a.num_seqs <= 32;
   const double most = ceil(a.max_seqlen_kv / (double)cpattn::BN);
   const double usual = alike ? most : fmin(most, ceil(a.total_kv / B / cpattn::BN));
   const double live = alike ? (double)c.items

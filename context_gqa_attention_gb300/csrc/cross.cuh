@@ -13,6 +13,7 @@ namespace {
 struct CrossParams {
   int B, Hq, Hkv, G, Nq, Nkv, max_q, span, tiles;  // tiles: items of the longest sequence
   int n_whole, n_split, split_k, rows;             // rows: of an item in the workspace
+  int ordered;                                     // items in the order of their keys (see cross_item)
   float scale_log2;
   long long q_stride, k_stride, v_stride;
   const int32_t *cu_q, *cu_kv, *kv_lens, *ranges;
@@ -27,27 +28,71 @@ struct CrossItem {
   int b, g, t0, tokens;  // the sequence, the kv head, its first token and how many there are (0: nothing to do)
   int q0, kv0, keys;     // first rows in q and k, v; keys of the sequence
 };
-// reporter: one thread of the item's first CTA, which says what is wrong with the sequence.
-CP_DEV CrossItem cross_item(const CrossParams& p, unsigned index, bool reporter) {
+// A sequence's rows and keys, as the tensors allow.
+CP_DEV CrossItem cross_sequence(const CrossParams& p, int b, int& rows, bool& report_it) {
   CrossItem w;
-  const unsigned tile = index % (unsigned)p.tiles, u = index / (unsigned)p.tiles;
-  w.g = (int)(u % (unsigned)p.Hkv);
-  w.b = (int)(u / (unsigned)p.Hkv);
-  w.t0 = (int)tile * p.span;
-  w.q0 = ld(p.cu_q + w.b);
-  w.kv0 = ld(p.cu_kv + w.b);
-  const int q1 = ld(p.cu_q + w.b + 1), kv1 = ld(p.cu_kv + w.b + 1), n = p.kv_lens != nullptr ? ld(p.kv_lens + w.b) : 0;
+  w.b = b;
+  w.q0 = ld(p.cu_q + b);
+  w.kv0 = ld(p.cu_kv + b);
+  const int q1 = ld(p.cu_q + b + 1), kv1 = ld(p.cu_kv + b + 1), n = p.kv_lens != nullptr ? ld(p.kv_lens + b) : 0;
   const long long Tq = (long long)q1 - w.q0, Tkv = (long long)kv1 - w.kv0;
-  reporter = reporter && tile == 0 && w.g == 0;
   w.keys = (int)Tkv;
+  report_it = Tq > p.max_q;
   if (p.kv_lens != nullptr) {
-    if (reporter && (n < 0 || n > Tkv)) report(p.err, CP_ERR_DEVICE_BOUNDS);
+    report_it = report_it || n < 0 || n > Tkv;
     w.keys = (int)max(0ll, min((long long)n, Tkv));
   }
   const bool bad = Tq < 0 || Tkv < 0 || w.q0 < 0 || w.kv0 < 0 || w.q0 + Tq > p.Nq || w.kv0 + Tkv > p.Nkv;
-  if (reporter && (bad || Tq > p.max_q)) report(p.err, CP_ERR_DEVICE_BOUNDS);
-  const long long here = min(Tq, (long long)p.max_q);
-  w.tokens = bad ? 0 : (int)max(0ll, min((long long)p.span, here - w.t0));
+  report_it = report_it || bad;
+  rows = bad ? 0 : (int)min(Tq, (long long)p.max_q);
+  return w;
+}
+// The item of an index; every lane of a warp asks for the same.  reporter: one thread of the item's first CTA, which says
+// what is wrong with the sequence.
+//
+// ordered (up to 32 sequences of different lengths, one a lane): the sequences with the most keys first, so that the last
+// items are short, and indexes without rows behind all others.
+CP_DEV CrossItem cross_item(const CrossParams& p, unsigned index, bool reporter) {
+  CrossItem w;
+  int rows;
+  bool wrong;
+  if (p.ordered) {
+    const int lane = (int)(threadIdx.x & 31), mine = min(lane, p.B - 1);
+    w = cross_sequence(p, mine, rows, wrong);
+    if (reporter && index == 0) {  // (thread 0 sees one sequence: it looks through the others)
+      for (int b = 0; b < p.B; ++b) {
+        int r;
+        bool x;
+        cross_sequence(p, b, r, x);
+        if (x) report(p.err, CP_ERR_DEVICE_BOUNDS);
+      }
+    }
+    __syncwarp();
+    const int n = lane < p.B ? (rows + p.span - 1) / p.span : 0;
+    int start = 0;  // items of the sequences before this one
+    for (int j = 0; j < p.B; ++j) {
+      const int k = __shfl_sync(0xffffffffu, w.keys, j), m = __shfl_sync(0xffffffffu, n, j);
+      if (k > w.keys || (k == w.keys && j < lane)) start += m;
+    }
+    const unsigned u = index / (unsigned)p.Hkv;
+    const uint32_t found = __ballot_sync(0xffffffffu, u >= (unsigned)start && u < (unsigned)(start + n));
+    const int at = found != 0u ? __ffs(found) - 1 : 0;
+    w.b = __shfl_sync(0xffffffffu, w.b, at);
+    w.q0 = __shfl_sync(0xffffffffu, w.q0, at);
+    w.kv0 = __shfl_sync(0xffffffffu, w.kv0, at);
+    w.keys = __shfl_sync(0xffffffffu, w.keys, at);
+    rows = __shfl_sync(0xffffffffu, rows, at);
+    w.g = (int)(index % (unsigned)p.Hkv);
+    w.t0 = (int)(u - (unsigned)__shfl_sync(0xffffffffu, start, at)) * p.span;
+    w.tokens = found != 0u ? min(p.span, rows - w.t0) : 0;
+    return w;
+  }
+  const unsigned tile = index % (unsigned)p.tiles, u = index / (unsigned)p.tiles;
+  w = cross_sequence(p, (int)(u / (unsigned)p.Hkv), rows, wrong);
+  w.g = (int)(u % (unsigned)p.Hkv);
+  w.t0 = (int)tile * p.span;
+  if (reporter && wrong && tile == 0 && w.g == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
+  w.tokens = max(0, min(p.span, rows - w.t0));
   return w;
 }
 // The keys [lo, hi) of a token (within the sequence).
@@ -130,7 +175,7 @@ cudaError_t launch_merge(const CrossParams& p, cudaStream_t s) {
 
 // How a launch is made of items and parts (host).
 struct CrossPlan {
-  int span, tiles, rows;
+  int span, tiles, rows, ordered;
   long long items, n_split;
   int split_k;
   size_t bytes;
@@ -153,6 +198,7 @@ inline void cp_cross_fill(cpattn::CrossParams& p, const cp_cross_args& a, const 
   p.span = plan.span;
   p.tiles = plan.tiles;
   p.rows = plan.rows;
+  p.ordered = plan.ordered;
   p.scale_log2 = scale * cpattn::kLog2e;
   p.q_stride = a.q_stride;
   p.k_stride = a.k_stride;

@@ -706,6 +706,7 @@ CrossPlan cp_cross_plan_few(const cp_cross_args& a, int sms) {
   c.items = (long long)a.num_seqs * a.num_kv_heads * c.tiles;
   c.n_split = 0;
   c.split_k = 1;
+  c.ordered = 0;
   // more parts than a cluster takes, through the workspace: where eight leave most of the GPU idle and the keys are
   // many enough to pay for a second launch
   const int tile = cpattn::tile_of(a);
