@@ -2,6 +2,8 @@
 // over beams and vocabulary) and cp_beam_reorder (the beams' tables and partly filled pages follow the
 // selection).  No counterpart on the pages, whose caches these are: "[Feature] Prefill Context Parallel (PCP)
 // basic support" (vLLM PR 28718), Purpose: per-rank block tables.
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace cpattn {
@@ -688,11 +690,11 @@ cudaError_t launch_select(const cp_beam_select_args& a, void* workspace, cudaStr
 //
 // A beam's own page may be another's source, so nothing is written before all that it replaces has been read: a
 // thread owns one 16-byte place of the page (row, vector), loads it from the K parents' pages and stores it to the
-// K beams' pages.  No shared memory, no barrier, K loads in flight a thread.  The tables go the same way, a
+// K beams' pages, K loads in flight at once, then takes the next place.  The tables go the same way, a
 // thread a column.  Tables that are replaced in place wait for the pages' copies in a launch of their own.
 // Bound: HBM for the full batch, else the launch and one chain of dependent loads (length, table entry, rows).
 struct ReorderParams {
-  int B, K, cp, I, max_blocks, Hkv, layers2, chunks;  // layers2: pools of K and of V; chunks: CTAs a pool
+  int B, K, cp, I, max_blocks, Hkv, layers2, ctas;    // layers2: pools of K and of V; ctas: of a (sequence, rank)'s pages
   int row_vecs, head_vecs, tail_at, tail_words;       // 16-byte vectors of a row and of a head's page; 4-bit records: place and words a row of the scales
   long long pool, layer_vecs;
   const int32_t *parents, *seq_lens, *tables_in, *own;
@@ -701,17 +703,21 @@ struct ReorderParams {
   int32_t* err;
 };
 
-// 1-D grid: (sequence, rank) slowest; within it the tables' CTA first (it has the most to do), then pools and chunks.
+// 1-D grid: (sequence, rank) slowest; within it the tables' CTA, then those that share the places of all pools.  As many as
+// the GPU takes at once: before its first place each goes through a chain of dependent loads (length, parents, tables).
+constexpr int kReorderThreads = 128;
+constexpr int reorder_ctas(int kmax) { return kmax <= 4 ? 8 : kmax <= 8 ? 5 : kmax <= 16 ? 3 : 2; }  // on an SM
 template <int KMAX>
-__global__ void __launch_bounds__(256) reorder_kernel(const ReorderParams p) {
-  __shared__ int s_parent[KMAX];
-  __shared__ long long s_src[KMAX], s_dst[KMAX];  // pages; -1: nothing to copy
+__global__ void __launch_bounds__(kReorderThreads, reorder_ctas(KMAX)) reorder_kernel(const ReorderParams p) {
+  __shared__ int s_parent[KMAX], s_own[KMAX];        // -1: none
+  __shared__ long long s_src[KMAX], s_dst[KMAX];     // 16-byte vectors from the pool's start; -1: nothing to copy
   chained_start();
   const int tables = p.tables_out != nullptr ? 1 : 0;
-  const unsigned per = (unsigned)(tables + (p.k != nullptr ? p.layers2 * p.chunks : 0));
+  const unsigned per = (unsigned)(tables + (p.k != nullptr ? p.ctas : 0));
   const unsigned unit = blockIdx.x / per, job = blockIdx.x % per;
   const int b = (int)(unit / (unsigned)p.cp), r = (int)(unit % (unsigned)p.cp);
   const int L = ld(p.seq_lens + b);
+  int parent = threadIdx.x < p.K ? ld(p.parents + (long long)b * p.K + threadIdx.x) : -1;
   const int held = L > 0 ? rank_local_len(L, r, p.cp, p.I) : 0;
   const int col = held / 16, fill = held % 16;
   const long long row0 = ((long long)r * p.B + b) * p.K;  // of the tables
@@ -722,84 +728,88 @@ __global__ void __launch_bounds__(256) reorder_kernel(const ReorderParams p) {
     if (first && threadIdx.x == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
     return;
   }
+  const int cta = (int)job - tables, places = p.Hkv * fill * p.row_vecs;  // of a pool
+  if (!first && (long long)cta * kReorderThreads >= (long long)places * p.layers2) return;  // (few tokens in the page)
   if (threadIdx.x < p.K) {
     const int j = threadIdx.x;
-    int parent = ld(p.parents + (long long)b * p.K + j);
     if (parent < 0 || parent >= p.K) {
       if (first) report(p.err, CP_ERR_DEVICE_BOUNDS);
       parent = -1;
     }
-    s_parent[j] = parent;
-    long long src = -1, dst = -1;
+    int src = -1, dst = -1;
     if (parent >= 0 && col < p.max_blocks) {
       dst = ld(p.own + (row0 + j) * p.max_blocks + col);
+      if (fill > 0) src = ld(p.tables_in + (row0 + parent) * p.max_blocks + col);
       if (dst < 0 || dst >= p.pool) {
         if (first) report(p.err, CP_ERR_DEVICE_BOUNDS);
         dst = -1;
-      } else if (fill > 0) {
-        src = ld(p.tables_in + (row0 + parent) * p.max_blocks + col);
-        if (src < 0 || src >= p.pool) {
-          if (first) report(p.err, CP_ERR_DEVICE_BOUNDS);
-          src = -1;
-        }
+      } else if (fill > 0 && (src < 0 || src >= p.pool)) {
+        if (first) report(p.err, CP_ERR_DEVICE_BOUNDS);
+        src = -1;
       }
     }
-    s_src[j] = src;
-    s_dst[j] = dst;
+    const long long page = (long long)p.Hkv * p.head_vecs;
+    const bool moves = src >= 0 && dst >= 0 && src != dst;
+    s_parent[j] = parent;
+    s_own[j] = dst;
+    s_src[j] = moves ? src * page : -1;
+    s_dst[j] = dst * page;
   }
   __syncthreads();
 
   if (tables && job == 0) {
-    for (int c = threadIdx.x; c <= col && c < p.max_blocks; c += blockDim.x) {
+    for (int c = threadIdx.x; c <= col && c < p.max_blocks; c += kReorderThreads) {
       int32_t id[KMAX];
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if (j < p.K && s_parent[j] >= 0)
-          id[j] = c == col && s_dst[j] >= 0 ? (int32_t)s_dst[j] : ld(p.tables_in + (row0 + s_parent[j]) * p.max_blocks + c);
+          id[j] = c == col && s_own[j] >= 0 ? s_own[j] : ld(p.tables_in + (row0 + s_parent[j]) * p.max_blocks + c);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if (j < p.K && s_parent[j] >= 0) p.tables_out[(row0 + j) * p.max_blocks + c] = id[j];
     }
     return;
   }
-  if (fill == 0) return;
-  const int pool = (int)(job - tables) / p.chunks, chunk = (int)(job - tables) % p.chunks;
-  uint4* base = ((pool & 1) ? p.v : p.k) + (pool >> 1) * p.layer_vecs + (long long)r * p.pool * p.Hkv * p.head_vecs;
-  const long long page = (long long)p.Hkv * p.head_vecs;
-  auto moves = [&](int j) -> bool { return j < p.K && s_src[j] >= 0 && s_dst[j] >= 0 && s_src[j] != s_dst[j]; };
-  for (int i = chunk * 256 + threadIdx.x; i < p.Hkv * fill * p.row_vecs; i += p.chunks * 256) {
-    const int q = i / p.row_vecs, h = q / fill;
-    uint4* place = base + (long long)h * p.head_vecs + (q % fill) * p.row_vecs + i % p.row_vecs;
-    uint4 x[KMAX];
+  // head h of page 0 of pool i
+  auto head = [&](int i, int h) -> uint4* {
+    return ((i & 1) ? p.v : p.k) + (i >> 1) * p.layer_vecs + ((long long)r * p.pool * p.Hkv + h) * p.head_vecs;
+  };
+  // what place j of the K pages is replaced by, all of it read first
+  auto move = [&](auto* place, int scale) {
+    std::remove_reference_t<decltype(*place)> x[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
-      if (moves(j)) x[j] = place[s_src[j] * page];
+      if (j < p.K && s_src[j] >= 0) x[j] = place[s_src[j] * scale];
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
-      if (moves(j)) place[s_dst[j] * page] = x[j];
+      if (j < p.K && s_src[j] >= 0) place[s_dst[j] * scale] = x[j];
+  };
+#pragma unroll 1
+  for (long long at = (long long)cta * kReorderThreads + threadIdx.x; at < (long long)places * p.layers2; at += p.ctas * kReorderThreads) {
+    const int pool = (int)(at / places), i = (int)(at - (long long)pool * places), q = i / p.row_vecs, h = q / fill;
+    move(head(pool, h) + (q - h * fill) * p.row_vecs + (i - q * p.row_vecs), 1);
   }
   if (p.tail_words > 0) {  // 4-bit records: the rows' scales and minima
-    for (int i = chunk * 256 + threadIdx.x; i < p.Hkv * fill * p.tail_words; i += p.chunks * 256) {
-      const int h = i / (fill * p.tail_words);
-      uint32_t* place = reinterpret_cast<uint32_t*>(base + (long long)h * p.head_vecs + p.tail_at) + i % (fill * p.tail_words);
-      uint32_t x[KMAX];
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j)
-        if (moves(j)) x[j] = place[s_src[j] * page * 4];
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j)
-        if (moves(j)) place[s_dst[j] * page * 4] = x[j];
+    const int words = p.Hkv * fill * p.tail_words;
+#pragma unroll 1
+    for (long long at = (long long)cta * kReorderThreads + threadIdx.x; at < (long long)words * p.layers2; at += p.ctas * kReorderThreads) {
+      const int pool = (int)(at / words), i = (int)(at - (long long)pool * words), h = i / (fill * p.tail_words);
+      move(reinterpret_cast<uint32_t*>(head(pool, h) + p.tail_at) + (i - h * fill * p.tail_words), 4);
     }
   }
 }
 
-cudaError_t reorder_launch(const ReorderParams& p, cudaStream_t s) {
-  const long long per = (p.tables_out != nullptr ? 1 : 0) + (p.k != nullptr ? (long long)p.layers2 * p.chunks : 0);
-  const long long grid = (long long)p.B * p.cp * per;
+cudaError_t reorder_launch(ReorderParams p, cudaStream_t s) {
+  const int kmax = p.K <= 4 ? 4 : p.K <= 8 ? 8 : p.K <= 16 ? 16 : 32;
+  const long long units = (long long)p.B * p.cp, slots = 152ll * reorder_ctas(kmax);
+  const long long most = ((long long)p.Hkv * 15 * p.row_vecs * p.layers2 + kReorderThreads - 1) / kReorderThreads;
+  const long long ctas = (slots + units - 1) / units;
+  p.ctas = (int)(ctas < most ? ctas : most);
+  const long long grid = units * ((p.tables_out != nullptr ? 1 : 0) + (p.k != nullptr ? p.ctas : 0));
   if (grid == 0) return cudaSuccess;
   if (grid >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  auto kern = p.K <= 4 ? reorder_kernel<4> : p.K <= 8 ? reorder_kernel<8> : p.K <= 16 ? reorder_kernel<16> : reorder_kernel<32>;
-  return launch_chained(kern, dim3((unsigned)grid), 256, 0, s, p);
+  auto kern = kmax == 4 ? reorder_kernel<4> : kmax == 8 ? reorder_kernel<8> : kmax == 16 ? reorder_kernel<16> : reorder_kernel<32>;
+  return launch_chained(kern, dim3((unsigned)grid), kReorderThreads, 0, s, p);
 }
 
 }  // namespace
@@ -836,7 +846,6 @@ cudaError_t cp_launch_beam_reorder(const cp_beam_reorder_args& a, cudaStream_t s
   p.head_vecs = (a.cache_q4 ? 9 * a.head_dim : 16 * row_bytes) / 16;
   p.tail_at = a.cache_q4 ? 8 * a.head_dim / 16 : 0;
   p.tail_words = a.cache_q4 ? a.head_dim / 64 : 0;
-  p.chunks = (p.Hkv * 15 * p.row_vecs + 511) / 512;  // two places a thread at most
   p.pool = a.pool_pages;
   p.layer_vecs = (long long)a.cp * a.pool_pages * a.num_kv_heads * p.head_vecs;
   p.parents = a.parents;
