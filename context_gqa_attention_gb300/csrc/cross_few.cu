@@ -265,8 +265,9 @@ struct Few {
     return (work > parts ? work : parts) + 16 * stages + 1024;  // (the base is rounded up to the swizzle atom)
   }
   static constexpr int ctas_of(int stages) { return 232448 / (smem_of(stages) + 1024); }
-  // CTAs on an SM, and stages of the ring
-  static constexpr int kCtas = MT == 1 && ctas_of(2) >= 3 ? 3 : ctas_of(2) >= 2 ? 2 : 1;
+  // CTAs on an SM, and stages of the ring (three CTAs of two stages: 106 us for 64 sequences of 512 .. 4096 states and 8 kv
+  // heads, two of three stages 98.6)
+  static constexpr int kCtas = ctas_of(2) >= 2 ? 2 : 1;
   static constexpr int kStages = ctas_of(4) >= kCtas ? 4 : ctas_of(3) >= kCtas ? 3 : 2;
   static constexpr int kRing = kStages * 2 * kBytes, oQ = kRing;
   static constexpr int oBar = smem_of(kStages) - 1024 - 16 * kStages;
@@ -290,7 +291,8 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
   auto full = [&](int s) -> uint32_t { return base + (uint32_t)F::oBar + 16u * (uint32_t)s; };
   auto empty = [&](int s) -> uint32_t { return full(s) + 8u; };
   volatile uint32_t* abort_flag = &s_abort;
-  if (threadIdx.x == 0) {
+  const bool producer = warp == F::kConsumers;
+  if (producer && lane == 0) {
     for (int s = 0; s < F::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), F::kConsumers);
@@ -323,12 +325,14 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
         tma_load_2d(dst + v * F::kBytes + kb * F::kTile * 128, v ? &map_v : &map_k, w.g * D + kb * F::kBoxCols,
                     w.kv0 + key.first + t * F::kTile, full(s));
   };
-  // the first tiles are on their way while the rows of q come in
+  // the first tiles are on their way while the other warps bring the rows of q
   const int early = min(ntiles, F::kStages);
-  if (threadIdx.x == 0)
-    for (int t = 0; t < early; ++t) load(t);
-  if constexpr (!F::kQRegs) {
-    for (int i = threadIdx.x; i < 16 * MT * (D / 8); i += F::kThreads) {
+  if (producer) {
+    if (lane == 0)
+      for (int t = 0; t < early; ++t) load(t);
+    __syncwarp();
+  } else if constexpr (!F::kQRegs) {
+    for (int i = threadIdx.x; i < 16 * MT * (D / 8); i += 32 * F::kConsumers) {
       const int row = i / (D / 8), c = (i % (D / 8)) * 8;
       uint4* dst = reinterpret_cast<uint4*>(sbase + F::oQ + row * F::kQPitch + c * 2);
       uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  if (warp == F::kConsumers) {
+  if (producer) {
     // ---- producer
     if (lane == 0) {
       int issued = early;
@@ -680,7 +684,7 @@ int slots_of(const cp_cross_args& a, int rows, int sms) {
 
 // Parts of an item that meet in a cluster: as many as the GPU takes at once, each with a tile at least.  More items than
 // that: parts of eight tiles or more until there are twice as many as the GPU takes, so that the last ones are short (64 sequences
-// of 512 .. 4096 states, 8 kv heads: 101.5 us; 105.5 whole, 109 with four times as many).
+// of 512 .. 4096 states, 8 kv heads, three CTAs on an SM: 101.5 us; 105.5 whole, 109 with four times as many).
 int cluster_of(const cp_cross_args& a, const CrossPlan& c, int sms) {
   const int tile = tile_of(a);
   const long long key_tiles = ((long long)a.max_seqlen_kv + tile - 1) / tile, slots = slots_of(a, c.rows, sms);
