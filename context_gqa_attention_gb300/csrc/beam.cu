@@ -274,7 +274,8 @@ CP_DEV void finish_sequence(const SelectParams& p, SelectShared& sh, int b) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = p.S * p.M, n_all = p.K * per;
   const uint2* best = p.best + (long long)b * n_all;
-  const int i0 = lane * kWarps + warp;  // (every warp has its share of a few candidates)
+  // every warp has its share of a few candidates, and of each place in the chunks' lists
+  const int i0 = lane * kWarps + ((warp + lane) & (kWarps - 1));
   const uint2 e0 = i0 < n_all ? __ldcg(best + i0) : make_uint2(0u, 0xffffffffu);  // on its way meanwhile
   // ---- beams: largest logit and its score.  Where that logit is +inf, the probability lies on those alone.
 #pragma unroll 1
@@ -302,30 +303,35 @@ CP_DEV void finish_sequence(const SelectParams& p, SelectShared& sh, int b) {
   if (tid == 0) sh.n = 0;
   __syncthreads();
   // ---- candidates: a score that at least M reach, and those that reach it
-  unsigned long long key0, at0;
-  const bool real0 = candidate(sh, e0, min(i0 / per, p.K - 1), key0, at0);
+  // (a thread keeps its two best; only where both are among them does it look through its others once more)
+  unsigned long long key[2] = {0, 0}, at[2] = {0, 0};
+  auto keep = [&](uint2 e, int i) {
+    unsigned long long k, a;
+    if (!candidate(sh, e, i / per, k, a) || k <= key[1]) return;
+    if (k > key[0]) key[1] = key[0], at[1] = at[0], key[0] = k, at[0] = a;
+    else key[1] = k, at[1] = a;
+  };
+  keep(e0, min(i0, n_all - 1));
+#pragma unroll 2
+  for (int i = i0 + kThreads; i < n_all; i += kThreads) keep(__ldcg(best + i), i);
+  uint32_t largest;
+  const uint32_t wth = wth_largest((uint32_t)(key[0] >> 32), (p.M + kWarps - 1) / kWarps, largest);
+  if (lane == 0) sh.w_th[warp] = wth;
+  __syncthreads();
+  const uint32_t bound = sh.bound();
   unsigned long long* place = sh.at();
-  uint32_t mine = real0 ? (uint32_t)(key0 >> 32) : 0u, bound = 0u;
+  auto take = [&](unsigned long long key, unsigned long long at) {
+    const int j = atomicAdd(&sh.n, 1);
+    if (j < kList) sh.key[j] = key, place[j] = at, sh.rank[j] = 0;
+  };
+  if (key[1] > 0 && (uint32_t)(key[1] >> 32) >= bound) {
 #pragma unroll 1
-  for (int pass = 0;; ++pass) {
-    auto take = [&](unsigned long long key, unsigned long long at) {
-      const int j = atomicAdd(&sh.n, 1);
-      if (j < kList) sh.key[j] = key, place[j] = at, sh.rank[j] = 0;
-    };
-    if (pass == 1 && real0 && (uint32_t)(key0 >> 32) >= bound) take(key0, at0);
-#pragma unroll 1
-    for (int i = i0 + kThreads; i < n_all; i += kThreads) {
-      unsigned long long key, at;
-      if (!candidate(sh, __ldcg(best + i), i / per, key, at)) continue;
-      if (pass == 0) mine = max(mine, (uint32_t)(key >> 32));
-      else if ((uint32_t)(key >> 32) >= bound) take(key, at);
+    for (int i = i0; i < n_all; i += kThreads) {
+      unsigned long long k, a;
+      if (candidate(sh, __ldcg(best + i), i / per, k, a) && (uint32_t)(k >> 32) >= bound) take(k, a);
     }
-    if (pass == 1) break;
-    uint32_t largest;
-    const uint32_t wth = wth_largest(mine, (p.M + kWarps - 1) / kWarps, largest);
-    if (lane == 0) sh.w_th[warp] = wth;
-    __syncthreads();
-    bound = sh.bound();
+  } else if (key[0] > 0 && (uint32_t)(key[0] >> 32) >= bound) {
+    take(key[0], at[0]);
   }
   __syncthreads();
   int n = sh.n;
@@ -634,18 +640,19 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
 }
 
 // Chunks: one a row if that gives every SM its four CTAs or nearly; else as many as do, of 16 KB at least (shorter ones
-// cost the last CTA more than they save).  More rows than places: a third of the GPU's places each, so that the last
-// ones are short.
+// cost the last CTA more than they save), and where beams and candidates are many no more than give it 1024 values to
+// look through.  More rows than places: a third of the GPU's places each, so that the last ones are short.
 struct SelectPlan {
   int NV, S, chunk;
 };
-SelectPlan select_plan(long long rows, int V, int elem) {
+SelectPlan select_plan(long long rows, int K, int M, int V, int elem) {
   constexpr long long kPlaces = 4 * 152;
   // whole 16-byte vectors of a row, which may start anywhere in one (at most; its ends are apart); a vector a thread
   const long long vecs = (long long)V * elem / 16, pieces = vecs > 0 ? (vecs + kThreads - 1) / kThreads : 1;
   long long S = rows > kPlaces ? (3 * kPlaces + rows - 1) / rows : kPlaces / rows;
-  const long long most = rows > kPlaces ? (pieces + 7) / 8 : (pieces + 3) / 4;
+  const long long most = rows > kPlaces ? (pieces + 7) / 8 : (pieces + 3) / 4, lists = 1024 / ((long long)K * M);
   if (S > most) S = most;
+  if (S > 2 && S > lists) S = lists > 2 ? lists : 2;
   if (S < 1) S = 1;
   const long long per = (pieces + S - 1) / S;
   return {per >= 4 ? 4 : per >= 2 ? 2 : 1, (int)((pieces + per - 1) / per), (int)(per * kThreads)};
@@ -660,7 +667,7 @@ size_t select_layout(size_t slices, int M, size_t* stats, size_t* best) {
 
 template <typename T>
 cudaError_t launch_select(const cp_beam_select_args& a, void* workspace, cudaStream_t s) {
-  const SelectPlan plan = select_plan((long long)a.num_seqs * a.num_beams, a.vocab, sizeof(T));
+  const SelectPlan plan = select_plan((long long)a.num_seqs * a.num_beams, a.num_beams, a.num_candidates, a.vocab, sizeof(T));
   size_t o_stats, o_best;
   select_layout((size_t)a.num_seqs * a.num_beams * plan.S, a.num_candidates, &o_stats, &o_best);
   SelectParams p;
@@ -825,7 +832,7 @@ size_t cp_beam_select_bytes(int32_t num_seqs, int32_t num_beams, int32_t vocab, 
 }
 long long cp_beam_select_ctas(const cp_beam_select_args& a) {
   const long long rows = (long long)a.num_seqs * a.num_beams;
-  return rows * cpattn::select_plan(rows, a.vocab, a.dtype == CP_BF16 ? 2 : 4).S;
+  return rows * cpattn::select_plan(rows, a.num_beams, a.num_candidates, a.vocab, a.dtype == CP_BF16 ? 2 : 4).S;
 }
 cudaError_t cp_launch_beam_select(const cp_beam_select_args& a, void* workspace, cudaStream_t s) {
   return a.dtype == CP_BF16 ? cpattn::launch_select<__nv_bfloat16>(a, workspace, s)
