@@ -1,6 +1,6 @@
 // Host side of the C ABI (include/cpattn.h): argument validation, error reporting and the
 // launches of the integer layout kernels and the LSE merge.  Attention kernels live in
-// prefill_tc.cu, prefill_simt.cu and decode.cu.
+// prefill_*.cu, decode*.cu and cross*.cu, beam search in beam.cu.
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -952,8 +952,7 @@ size_t cp_cross_args_size(void) { return sizeof(cp_cross_args); }
 size_t cp_beam_select_args_size(void) { return sizeof(cp_beam_select_args); }
 size_t cp_beam_reorder_args_size(void) { return sizeof(cp_beam_reorder_args); }
 
-// The shape of a cross attention, and which kernel takes it: the tensor cores' tiles of 128 rows from 65 rows a kv
-// head on, the kernel for few rows (in f32 for any) below.
+// The shape of a cross attention.
 static cp_status check_cross_shape(const cp_cross_args* a) {
   REQUIRE(a != nullptr, "args is null");
   REQUIRE(a->dtype == CP_F32 || a->dtype == CP_BF16, "dtype must be CP_F32 or CP_BF16");
@@ -966,12 +965,10 @@ static cp_status check_cross_shape(const cp_cross_args* a) {
   if (a->head_dim != 64 && a->head_dim != 128)
     return fail(CP_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", a->head_dim);
   REQUIRE(a->max_seqlen_q >= 0 && a->max_seqlen_kv >= 0, "max_seqlen_q and max_seqlen_kv must be >= 0");
+  REQUIRE((double)a->num_seqs * a->num_kv_heads * cp_cross_tiles(*a) < 2147483648.0,
+          "num_seqs * num_kv_heads * max_seqlen_q: too many work items");
   return CP_OK;
 }
-static bool cross_few(const cp_cross_args* a) {
-  return a->dtype == CP_F32 || (int64_t)a->max_seqlen_q * (a->num_q_heads / a->num_kv_heads) <= 64;
-}
-
 cp_status cp_cross_attention_workspace_size(const cp_cross_args* a, size_t* bytes) {
   const cp_status st = check_cross_shape(a);
   if (st != CP_OK) return st;
@@ -980,7 +977,7 @@ cp_status cp_cross_attention_workspace_size(const cp_cross_args* a, size_t* byte
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return launched(e, "device query");
-  *bytes = (cross_few(a) ? cp_cross_plan_few(*a, sms) : cp_cross_plan_tc(*a, sms)).bytes;
+  *bytes = (cp_cross_few(*a) ? cp_cross_plan_few(*a, sms) : cp_cross_plan_tc(*a, sms)).bytes;
   return ok();
 }
 
@@ -1006,7 +1003,7 @@ cp_status cp_cross_attention(const cp_cross_args* a, void* workspace, size_t wor
     REQUIRE_PTR(a->v);
   }
   const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / sqrtf((float)a->head_dim);
-  const auto go = cross_few(a) ? cp_launch_cross_few : cp_launch_cross_tc;
+  const auto go = cp_cross_few(*a) ? cp_launch_cross_few : cp_launch_cross_tc;
   return launched(go(*a, scale, workspace, workspace_bytes, out, out_lse, as_stream(stream)), "cp_cross_attention launch");
 }
 

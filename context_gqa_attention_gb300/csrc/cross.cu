@@ -549,11 +549,10 @@ cudaError_t launch(const cp_cross_args& a, const CrossPlan& plan, float scale, v
 // are cut or none: the load of an SM and half of the longest item decide.
 CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms) {
   CrossPlan c;
-  const int G = a.num_q_heads / a.num_kv_heads;
   const double B = a.num_seqs;
-  c.span = 2 * (cpattn::BM / G);
-  c.tiles = a.max_seqlen_q > 0 ? (int)(((long long)a.max_seqlen_q + c.span - 1) / c.span) : 1;
-  c.rows = c.span * G;
+  c.span = cp_cross_span(a);
+  c.tiles = cp_cross_tiles(a);
+  c.rows = c.span * (a.num_q_heads / a.num_kv_heads);
   c.items = (long long)a.num_seqs * a.num_kv_heads * c.tiles;
   c.n_split = 0;
   c.split_k = 1;

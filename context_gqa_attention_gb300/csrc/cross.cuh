@@ -180,6 +180,20 @@ struct CrossPlan {
   int split_k;
   size_t bytes;
 };
+// The kernel for few rows takes f32, and bf16 of up to 64 rows a kv head; the tensor cores' tiles of 128 rows the rest.
+inline bool cp_cross_few(const cp_cross_args& a) {
+  return a.dtype == CP_F32 || (long long)a.max_seqlen_q * (a.num_q_heads / a.num_kv_heads) <= 64;
+}
+// Tokens of an item: 64 rows of the kernel for few rows (or what there is), two row tiles of the other.
+inline int cp_cross_span(const cp_cross_args& a) {
+  const int G = a.num_q_heads / a.num_kv_heads;
+  if (!cp_cross_few(a)) return 2 * (128 / G);
+  return a.max_seqlen_q <= 0 ? 1 : a.max_seqlen_q < 64 / G ? a.max_seqlen_q : 64 / G;
+}
+inline int cp_cross_tiles(const cp_cross_args& a) {
+  const int span = cp_cross_span(a);
+  return a.max_seqlen_q > 0 ? (int)(((long long)a.max_seqlen_q + span - 1) / span) : 1;
+}
 CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms);
 CrossPlan cp_cross_plan_few(const cp_cross_args& a, int sms);
 cudaError_t cp_launch_cross_tc(const cp_cross_args& a, float scale, void* ws, size_t ws_bytes, void* out, float* lse,

@@ -702,11 +702,9 @@ int cluster_of(const cp_cross_args& a, const CrossPlan& c, int sms) {
 
 CrossPlan cp_cross_plan_few(const cp_cross_args& a, int sms) {
   CrossPlan c;
-  const int G = a.num_q_heads / a.num_kv_heads;
-  const int most = 64 / G;  // tokens of an item
-  c.span = a.max_seqlen_q < most ? (a.max_seqlen_q > 0 ? a.max_seqlen_q : 1) : most;
-  c.tiles = a.max_seqlen_q > 0 ? (int)(((long long)a.max_seqlen_q + c.span - 1) / c.span) : 1;
-  c.rows = c.span * G;
+  c.span = cp_cross_span(a);
+  c.tiles = cp_cross_tiles(a);
+  c.rows = c.span * (a.num_q_heads / a.num_kv_heads);
   c.items = (long long)a.num_seqs * a.num_kv_heads * c.tiles;
   c.n_split = 0;
   c.split_k = 1;

@@ -627,8 +627,9 @@ cp_status cp_cross_attention(const cp_cross_args* args, void* workspace, size_t 
  * cand_*[b] are the num_candidates best in falling order; of equal scores the lower k * vocab + v comes first.
  * next_*[b] are the first num_beams of them whose token is not eos_token (< 0: any token): the beams that go on.
  *   - a logit of -inf (a banned token) or NaN has the score -inf; logits of +inf share their beam's
- *     probability; a beam without a token, or with the score -inf or NaN, has scores of -inf only.
- *   - K = num_beams in 1 .. 32; num_candidates in K .. 64, at least 2 K with an eos_token, at most K * vocab.
+ *     probability; a beam without a token, or whose own score is not finite, has scores of -inf only.
+ *   - K = num_beams in 1 .. 32; num_candidates in K .. 64, at least 2 K with an eos_token, at most K * vocab;
+ *     vocab <= 2^30.  next_scores may be scores (replaced in place); no other output may overlap an input.
  *   - logits: rows of `vocab` elements, row b K + k starting logits_stride elements after the one before
  *     (any alignment of the type's own).
  *   - workspace: cp_beam_select_workspace_size() bytes, 256-byte aligned, zero-filled before its first use

@@ -38,7 +38,7 @@ def select(logits, scores, M, eos=-1):
     for k in range(K):
         x = np.where(np.isnan(logits[k]), -np.inf, np.asarray(logits[k], dtype=np.float64))
         m = x.max()
-        if m == -np.inf or not scores[k] > -np.inf:
+        if m == -np.inf or not np.isfinite(scores[k]):
             continue
         if m == np.inf:
             flat[k] = np.where(x == np.inf, scores[k] - np.log((x == np.inf).sum()), -np.inf)

@@ -42,6 +42,7 @@ CROSS = dict(dtype=1, num_seqs=2, num_q_heads=8, num_kv_heads=2, head_dim=128, m
     (dict(cu_seqlens_q=None), 1), (dict(cu_seqlens_kv=None), 1), (dict(q=None), 1), (dict(k=ODD), 1), (dict(v=None), 1),
     (dict(q_stride=1020), 1), (dict(q_stride=1016), 1), (dict(k_stride=248), 1), (dict(v_stride=260), 1),
     (dict(dtype=0, v_stride=514), 1), (dict(k_stride=-256), 1),
+    (dict(num_seqs=1 << 20, max_seqlen_q=1 << 20), 1), (dict(dtype=0, num_seqs=1 << 24, max_seqlen_q=1 << 20), 1),
 ])
 def test_cross_refusals(lib, bad, status):
     a = _fill(_fill(cpa.CrossArgs(), CROSS), bad)

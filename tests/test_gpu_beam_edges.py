@@ -1,0 +1,92 @@
+"""Cross attention and beam selection at their edges: batches on both sides of the ordered items' 32 sequences, many
+heads to a kv head, guard words around outputs and workspace, scores that are not finite, scores replaced in place,
+rows of logits past 32-bit offsets."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_beam import check_select
+from test_gpu_cross import check, exact
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+I32 = dict(dtype=torch.int32, device=DEV)
+
+
+def _cu(lens):
+    return torch.tensor(np.cumsum([0] + list(lens)), **I32)
+
+
+# B, rows of a sequence up to, keys up to, Hq, Hkv, d, dtype
+BATCHES = [(32, 90, 300, 8, 2, 64, "bf16"), (33, 90, 300, 8, 2, 64, "bf16"), (45, 150, 700, 6, 2, 128, "bf16"),
+           (2, 40, 900, 100, 1, 128, "bf16"), (3, 2, 4000, 128, 2, 64, "bf16"), (3, 1, 2600, 64, 1, 128, "f32"),
+           (40, 6, 900, 12, 4, 64, "f32"), (40, 5, 3000, 12, 4, 128, "bf16")]
+
+
+@pytest.mark.parametrize("B,T,S,Hq,Hkv,d,dtype", BATCHES)
+@pytest.mark.parametrize("ranged", [False, True])
+def test_padded_batches_between_guards(lib, B, T, S, Hq, Hkv, d, dtype, ranged):
+    r = np.random.default_rng(B + S)
+    rows, keys = r.integers(0, T + 1, B), r.integers(0, S + 1, B)
+    rows[0], keys[0], rows[-1], keys[-1] = T, S, 1, 0            # the longest; a row without a key
+    g = torch.Generator(device=DEV).manual_seed(B)
+    n, pad = int(rows.sum()), 64
+    q = torch.randn(n, Hq, d, generator=g, device=DEV).to(DT[dtype])
+    k, v = (torch.randn(B * S, Hkv, d, generator=g, device=DEV).to(DT[dtype]) for _ in range(2))
+    hidden = (torch.arange(S, device=DEV)[None] >= torch.tensor(keys, device=DEV)[:, None]).reshape(-1)
+    k[hidden], v[hidden] = math.nan, math.inf
+    ranges = None
+    if ranged:
+        lo = torch.randint(0, S, (n,), generator=g, device=DEV)
+        ranges = torch.stack([lo, lo + torch.randint(0, S, (n,), generator=g, device=DEV)], -1).int().contiguous()
+    spans = [(int(a), int(t), b * S, int(m)) for b, (a, t, m) in enumerate(zip(np.cumsum([0] + list(rows)), rows, keys))]
+    if ranged:
+        clipped = ranges.clone()
+        for a, t, _, m in spans:
+            clipped[a:a + t] = clipped[a:a + t].clamp(max=m)
+    want = exact(q, k, v, spans, d ** -0.5, clipped if ranged else None)
+
+    need = lib.cp_cross_attention_workspace_size(B, Hq, Hkv, d, T, S, total_q=n, total_kv=B * S, padded=True, dtype=DT[dtype])
+    ws = torch.full((need + 2 * 256,), 0xa5, dtype=torch.uint8, device=DEV)
+    out = torch.full((n + 2 * pad, Hq, d), 12345.0, dtype=DT[dtype], device=DEV)
+    lse = torch.full((n + 2 * pad, Hq), 12345.0, device=DEV)
+    err = torch.zeros(1, **I32)
+    lib.cp_cross_attention(q, _cu(rows), k, v, _cu([S] * B), kv_lens=torch.tensor(keys, **I32), key_ranges=ranges,
+                           max_seqlen_q=T, max_seqlen_kv=S, workspace=ws[256:256 + need], out=out[pad:pad + n],
+                           out_lse=lse[pad:pad + n], err=err)
+    assert int(err) == 0
+    check(out[pad:pad + n], lse[pad:pad + n], want, dtype == "f32")
+    mark = torch.tensor(12345.0, dtype=DT[dtype], device=DEV)
+    for x, m in ((out, mark), (lse, 12345.0)):
+        assert bool((x[:pad] == m).all()) and bool((x[pad + n:] == m).all())
+    assert bool((ws[:256] == 0xa5).all()) and bool((ws[256 + need:] == 0xa5).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_that_are_not_finite_and_scores_in_place(lib, dtype):
+    g = torch.Generator(device=DEV).manual_seed(5)
+    logits = (3 * torch.randn(4, 4, 5000, generator=g, device=DEV)).to(DT[dtype])
+    scores = torch.tensor([[math.inf, -1.5, math.nan, -math.inf], [-2.0, -math.inf, -1.0, -1.25],
+                           [math.inf, math.inf, math.nan, math.nan], [-3e38, -1.0, -3.4e38, -0.5]], device=DEV)
+    got = lib.cp_beam_select(logits, scores, num_candidates=8, eos_token=17)
+    for b in (0, 1, 2):
+        check_select([x[b:b + 1] for x in got], logits[b:b + 1], scores[b:b + 1], 8, 17)
+    assert set(got[4][3].tolist()) <= {1, 3}
+    mine = scores.clone()
+    again = lib.cp_beam_select(logits, mine, num_candidates=8, eos_token=17, next_scores=mine)
+    assert again[0].data_ptr() == mine.data_ptr()
+    for x, y in zip(got, again):
+        assert torch.equal(x, y)
+
+
+def test_rows_of_logits_past_32_bit_offsets(lib):
+    K, V, stride = 3, 70001, 1_100_000_003                      # the last row starts behind 2^31 elements
+    flat = torch.empty(2 * stride + V, dtype=torch.bfloat16, device=DEV)
+    logits = flat.as_strided((1, K, V), (K * stride, stride, 1))
+    small = (3 * torch.randn(1, K, V, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)).bfloat16()
+    logits.copy_(small)
+    scores = torch.tensor([[-4.0, -3.0, -1.0]], device=DEV)
+    check_select(lib.cp_beam_select(logits, scores, eos_token=2), small, scores, 6, 2)

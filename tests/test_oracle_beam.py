@@ -48,6 +48,8 @@ def test_selection_of_what_has_no_probability():
     assert all(c[0] == -inf for c in best[4:])
     best, _ = bo.select(np.zeros((2, 3)), np.array([-inf, 0.0]), 5)
     assert [c[1:] for c in best] == [(1, 0), (1, 1), (1, 2), (0, 0), (0, 1)]
+    best, on = bo.select(np.zeros((3, 2)), np.array([inf, np.nan, 1.0]), 4, eos=0)
+    assert [c[1:] for c in best] == [(2, 0), (2, 1), (0, 0), (0, 1)] and [c[1:] for c in on] == [(2, 1), (0, 1)]
 
 
 def test_selection_against_torch():
