@@ -17,7 +17,7 @@ LIB = os.path.join(OUT_DIR, "libcpattn.so")
 BINDING = os.path.join(OUT_DIR, "cpattn_binding.so")
 BUILT_FOR = os.path.join(OUT_DIR, "cpattn_binding.txt")  # the torch and Python that BINDING was built against
 SOURCES = ["api.cu", "prefill_simt.cu", "prefill_tc.cu", "decode.cu", "noalloc.cu",
-           "cache.cu", "decode_mod.cu", "decode_q4.cu", "prefill_mod.cu", "beam.cu", "cross.cu", "cross_few.cu"]
+           "cache.cu", "decode_mod.cu", "decode_q4.cu", "prefill_mod.cu", "beam.cu", "cross.cu", "cross_few.cu", "cross_f32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]

@@ -1,264 +1,42 @@
-// Cross attention (cp_cross_attention) of few query rows: the beams of a source in a decode step, a short prompt;
-// and of any number of rows in f32.  No counterpart on the pages, whose attention is causal self-attention.
+// Cross attention (cp_cross_attention) of few query rows in bf16: the beams of a source in a decode step, a short prompt.
+// No counterpart on the pages, whose attention is causal self-attention.
 //
 //   out_i = softmax over the keys j in [lo_i, hi_i) of scale q_i.k_j, times V
 //
 // The rows of an item (CrossParams) are all that a kv head's states are read for, so the time is that of the states:
 // bytes, not operations.  Parts of the keys run at once and meet in a cluster's shared memory (up to eight), or in
 // the workspace (cross_merge_kernel) where a few long items have to fill the GPU.
-#include <cuda.h>
-
-#include "cross.cuh"
-#include "sm100.cuh"
+#include "cross_few.cuh"
 
 namespace cpattn {
 namespace {
-
-using namespace sm100;
-
-constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
-constexpr float kMaxGrowth = 8.f;            // log2 units the scores may exceed the running reference
-constexpr int kMaxCluster = 8;
-
-CP_DEV uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-CP_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-CP_DEV uint32_t peer_addr(const void* mine, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
-  return a;
-}
-CP_DEV float peer_ld(uint32_t a) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
-  return x;
-}
-CP_DEV float4 peer_ld4(uint32_t a) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
-  return x;
-}
-
-// ------------------------------------------------------------------------------ results
-template <typename T>
-CP_DEV void put4(void* out, long long at, float4 v) {
-  if constexpr (sizeof(T) == 2) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
-  }
-}
-// Two sets of (reference in log2 units, sum, row) as one: the factor of a set whose reference is m.  (One of -inf saw
-// no finite score: its sums are 0, or NaN.)
-CP_DEV float factor(float m, float M) { return m == M || m == -INFINITY ? 1.f : exp2f(m - M); }
-CP_DEV float natural_lse(float M, float L) {
-  return L == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
-}
-
-// What W slices of the CTA's keys made of R rows, in shared memory: reference, sum, unnormalised row.
-template <int D, int W, int R>
-struct Slices {
-  float o[W][R][D + 8];  // (rows 32 bytes apart in the banks)
-  float m[W][R], l[W][R];
-};
-
-// Slices -> the CTA's part; parts -> result, or to the workspace.  cluster: parts that meet in shared memory (1: none).
-template <typename T, int D, int W, int R>
-CP_DEV void finish(const CrossParams& p, const CrossItem& w, Slices<D, W, R>& s, int cluster, int piece) {
-  constexpr int V = D / 4;
-  const int rows = w.tokens * p.G;
-  auto out_row = [&](int row) -> long long {
-    return ((long long)w.q0 + w.t0 + row / p.G) * p.Hq + w.g * p.G + row % p.G;
-  };
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * V; i += blockDim.x) {
-    const int row = i / V, dd = (i % V) * 4;
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) M = fmaxf(M, s.m[k][row]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const float e = factor(s.m[k][row], M);
-      const float4 x = *reinterpret_cast<const float4*>(&s.o[k][row][dd]);
-      L += e * s.l[k][row];
-      o.x += e * x.x, o.y += e * x.y, o.z += e * x.z, o.w += e * x.w;
-    }
-    if (cluster > 1) {
-      *reinterpret_cast<float4*>(&s.o[0][row][dd]) = o;  // (only this thread read these)
-      continue;
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    if (piece >= 0) {
-      const long long at = (long long)piece * p.rows + row;
-      *reinterpret_cast<float4*>(p.ws_out + at * D + dd) = o;
-      if (dd == 0) p.ws_lse[at] = natural_lse(M, L);
-    } else {
-      put4<T>(p.out, out_row(row) * D + dd, o);
-      if (dd == 0 && p.lse != nullptr) p.lse[out_row(row)] = natural_lse(M, L);
-    }
-  }
-  if (cluster <= 1) return;
-  __syncthreads();  // (the slices' references have been read)
-  for (int row = threadIdx.x; row < rows; row += blockDim.x) {
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) M = fmaxf(M, s.m[k][row]);
-#pragma unroll
-    for (int k = 0; k < W; ++k) L += factor(s.m[k][row], M) * s.l[k][row];
-    s.m[0][row] = M;
-    s.l[0][row] = L;
-  }
-  cluster_sync();
-  const int rank = (int)cluster_rank();
-  for (int i = rank + cluster * (int)threadIdx.x; i < rows * V; i += cluster * (int)blockDim.x) {
-    const int row = i / V, dd = (i % V) * 4;
-    float m[kMaxCluster], l[kMaxCluster], M = -INFINITY, L = 0.f;
-    float4 x[kMaxCluster], o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
-      m[c] = -INFINITY, l[c] = 0.f;
-      if (c < cluster) {
-        m[c] = peer_ld(peer_addr(&s.m[0][row], c));
-        l[c] = peer_ld(peer_addr(&s.l[0][row], c));
-        x[c] = peer_ld4(peer_addr(&s.o[0][row][dd], c));
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, m[c]);
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c)
-      if (c < cluster) {
-        const float e = factor(m[c], M);
-        L += e * l[c];
-        o.x += e * x[c].x, o.y += e * x[c].y, o.z += e * x[c].z, o.w += e * x[c].w;
-      }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    put4<T>(p.out, out_row(row) * D + dd, o);
-    if (dd == 0 && p.lse != nullptr) p.lse[out_row(row)] = natural_lse(M, L);
-  }
-  cluster_sync();  // no CTA leaves while another reads its shared memory
-}
-
-// The keys that some row of the item sees, the CTA's part of them [first, end) in whole tiles, and the keys that every
-// row sees.
-struct Keys {
-  int first, end, all_lo, all_hi;
-};
-template <bool RANGES>
-CP_DEV Keys part_keys(const CrossParams& p, const CrossItem& w, int tile, int part, int parts, int (&s_range)[4]) {
-  Keys k;
-  int lo = 0, hi = w.keys;
-  k.all_lo = 0, k.all_hi = w.keys;
-  if constexpr (RANGES) {
-    if (threadIdx.x == 0) s_range[0] = s_range[3] = 0x7fffffff, s_range[1] = s_range[2] = 0;
-    __syncthreads();
-    for (int t = threadIdx.x; t < w.tokens; t += blockDim.x) {
-      int a, b;
-      cross_range(p, w, w.t0 + t, a, b);
-      if (a < b) {
-        atomicMin(s_range, a);
-        atomicMax(s_range + 1, b);
-      }
-      atomicMax(s_range + 2, a);
-      atomicMin(s_range + 3, b);
-    }
-    __syncthreads();
-    lo = s_range[0], hi = s_range[1], k.all_lo = s_range[2], k.all_hi = s_range[3];
-  }
-  const int every = lo < hi ? (hi - lo + tile - 1) / tile : 0;
-  const int a = (int)((long long)every * part / parts), b = (int)((long long)every * (part + 1) / parts);
-  k.first = every > 0 ? lo + a * tile : 0;
-  k.end = a < b ? min(hi, lo + b * tile) : k.first;
-  return k;
-}
 
 // ------------------------------------------------------------------------------ the kernel
 // MMAs of 16 rows on the legacy tensor path: a 128-row tcgen05 tile would be padding.  A producer warp brings tiles of
 // K and V through a ring (TMA, 128-byte swizzle); consumer warp (m, k) owns the 16 rows m and the k-th slice of every
 // tile's keys, with a softmax reference of its own, so warps meet at the end only.  The reference moves when a score
 // exceeds it by more than 2^8, which a vote of the warp finds; rows' sums stay in the lanes until the end.
-//
-// f32: each operand is the sum of three bf16 numbers (high, middle, low: 24 bits) and a product the sum of the six of
-// theirs that count, in fp32.  (Three products of tf32 pairs took three times as long: 25 cycles of a sub-partition each
-// against 8.4 for twice the work.  CUDA cores need 32 times fewer rows' worth of padding, but a shared-memory read for
-// every four of their products.)
-CP_DEV void ldsm4(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-CP_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-CP_DEV void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-CP_DEV uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 // Halves that are infinite or NaN become 0; whether there were any.
 CP_DEV bool clean(uint32_t& w) {
   const uint32_t bad = ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // an exponent of all ones carries
   w &= ~((bad >> 15) * 0xffffu);
   return bad != 0u;
 }
-// x and y = high + middle + low, as pairs of bf16.
-CP_DEV void split(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
-  h = pack2(x, y);
-  x -= __uint_as_float(h << 16), y -= __uint_as_float(h & 0xffff0000u);
-  m = pack2(x, y);
-  x -= __uint_as_float(m << 16), y -= __uint_as_float(m & 0xffff0000u);
-  l = pack2(x, y);
-}
-CP_DEV float as_float(float x) { return x; }
-CP_DEV float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// The six products that count, the small ones first.
-CP_DEV void mma_parts(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&am)[4], const uint32_t (&al)[4],
-                      const uint32_t (&h)[2], const uint32_t (&m)[2], const uint32_t (&l)[2]) {
-  mma_bf16(c, al, h[0], h[1]);
-  mma_bf16(c, ah, l[0], l[1]);
-  mma_bf16(c, am, m[0], m[1]);
-  mma_bf16(c, am, h[0], h[1]);
-  mma_bf16(c, ah, m[0], m[1]);
-  mma_bf16(c, ah, h[0], h[1]);
-}
-
-template <typename T, int D, int MT>
+template <int D, int MT>
 struct Few {
-  static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kWK = MT == 4 || (kF32 && D == 128) ? 2 : 4;  // slices of a tile's keys
+  static constexpr int kWK = MT == 4 ? 2 : 4;        // slices of a tile's keys
   static constexpr int kConsumers = MT * kWK;
   static constexpr int kThreads = 32 * (kConsumers + 1);
   static constexpr int kBytes = 16384;               // of a tile of K or of V
-  static constexpr int kTile = kBytes / (D * (int)sizeof(T));  // keys
+  static constexpr int kTile = kBytes / (D * 2);  // keys
   static constexpr int kKeys = kTile / kWK;          // of a warp
-  static constexpr int kMaxStep = kF32 ? 16 : 32;
-  static constexpr int kStep = kKeys < kMaxStep ? kKeys : kMaxStep;
+  static constexpr int kStep = kKeys < 32 ? kKeys : 32;
   static_assert(kStep % 16 == 0, "steps of the second product");
-  static constexpr int kBoxCols = 128 / (int)sizeof(T), kBoxes = D / kBoxCols;
-  // q as A fragments in registers (bf16, one row group), or in shared memory: rows 16 bytes apart in the banks; f32: the
-  // three parts one behind the other
-  static constexpr bool kQRegs = !kF32 && MT == 1;
-  static constexpr int kQPitch = D * 2 + 16, kQPart = 16 * MT * kQPitch;
-  static constexpr int kQBytes = kQRegs ? 0 : kQPart * (kF32 ? 3 : 1);
-  using Parts = Slices<D, kWK, 16 * MT>;
+  static constexpr int kBoxes = D / 64;
+  // q as A fragments in registers (one row group), or in shared memory: rows 16 bytes apart in the banks
+  static constexpr bool kQRegs = MT == 1;
+  static constexpr int kQPitch = D * 2 + 16, kQBytes = kQRegs ? 0 : 16 * MT * kQPitch;
+  using Parts = Slices<D, kWK, 16 * MT, 8>;
   static constexpr int align16(int x) { return (x + 15) / 16 * 16; }
   static constexpr int smem_of(int stages) {
     const int work = stages * 2 * kBytes + kQBytes, parts = align16((int)sizeof(Parts));
@@ -274,13 +52,13 @@ struct Few {
   static constexpr int kSmem = smem_of(kStages);
 };
 
-template <typename T, int D, int MT, bool RANGES>
-__global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
+template <int D, int MT, bool RANGES>
+__global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
     few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const CrossParams p,
                const int parts, const int cluster) {
-  using F = Few<T, D, MT>;
+  using F = Few<D, MT>;
+  using T = __nv_bfloat16;
   constexpr int NT = F::kStep / 8;
-  constexpr bool kRestore = RANGES || F::kF32;  // V may be cleaned
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_range[4];
   __shared__ uint32_t s_abort;
@@ -322,7 +100,7 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
     for (int v = 0; v < 2; ++v)
 #pragma unroll
       for (int kb = 0; kb < F::kBoxes; ++kb)
-        tma_load_2d(dst + v * F::kBytes + kb * F::kTile * 128, v ? &map_v : &map_k, w.g * D + kb * F::kBoxCols,
+        tma_load_2d(dst + v * F::kBytes + kb * F::kTile * 128, v ? &map_v : &map_k, w.g * D + kb * 64,
                     w.kv0 + key.first + t * F::kTile, full(s));
   };
   // the first tiles are on their way while the other warps bring the rows of q
@@ -335,22 +113,8 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
     for (int i = threadIdx.x; i < 16 * MT * (D / 8); i += 32 * F::kConsumers) {
       const int row = i / (D / 8), c = (i % (D / 8)) * 8;
       uint4* dst = reinterpret_cast<uint4*>(sbase + F::oQ + row * F::kQPitch + c * 2);
-      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-      if (row < rows) {
-        const uint4* q = reinterpret_cast<const uint4*>(q_row(row) + c);
-        x = q[0];
-        if constexpr (F::kF32) y = q[1];
-      }
-      if constexpr (F::kF32) {
-        uint4 h, m, l;
-        split(__uint_as_float(x.x), __uint_as_float(x.y), h.x, m.x, l.x);
-        split(__uint_as_float(x.z), __uint_as_float(x.w), h.y, m.y, l.y);
-        split(__uint_as_float(y.x), __uint_as_float(y.y), h.z, m.z, l.z);
-        split(__uint_as_float(y.z), __uint_as_float(y.w), h.w, m.w, l.w);
-        dst[F::kQPart / 16] = m;
-        dst[2 * F::kQPart / 16] = l;
-        x = h;
-      }
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows) x = *reinterpret_cast<const uint4*>(q_row(row) + c);
       *dst = x;
     }
   }
@@ -422,37 +186,20 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
         // S = Q K^T
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          uint32_t a[F::kF32 ? 3 : 1][4];
+          uint32_t a[4];
           if constexpr (F::kQRegs) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[0][i] = qa[k][i];
+            for (int i = 0; i < 4; ++i) a[i] = qa[k][i];
           } else {
-#pragma unroll
-            for (int i = 0; i < (F::kF32 ? 3 : 1); ++i) ldsm4(a[i], sq + 32u * k + (uint32_t)(i * F::kQPart));
+            ldsm4(a, sq + 32u * k);
           }
-          if constexpr (F::kF32) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const int row = r0 + 8 * i + gid;
-              uint32_t h[2], m[2], l[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {  // dims 16 k + 8 e + 2 tig and the next
-                const int chunk = 4 * (k & 1) + 2 * e + (tig >> 1);
-                const float2 x = *reinterpret_cast<const float2*>(sbase + (sk - base) + (k / 2) * F::kTile * 128 + row * 128 +
-                                                                  ((chunk ^ (row & 7)) << 4) + (tig & 1) * 8);
-                split(x.x, x.y, h[e], m[e], l[e]);
-              }
-              mma_parts(c[i], a[0], a[1], a[2], h, m, l);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < NT; i += 2) {  // a matrix is 8 keys' 16 bytes
-              const int row = r0 + 8 * i + ((lane >> 4) << 3) + (lane & 7), chunk = 2 * (k & 3) + ((lane >> 3) & 1);
-              uint32_t b[4];
-              ldsm4(b, sk + (uint32_t)((k / 4) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
-              mma_bf16(c[i], a[0], b[0], b[1]);
-              mma_bf16(c[i + 1], a[0], b[2], b[3]);
-            }
+          for (int i = 0; i < NT; i += 2) {  // a matrix is 8 keys' 16 bytes
+            const int row = r0 + 8 * i + ((lane >> 4) << 3) + (lane & 7), chunk = 2 * (k & 3) + ((lane >> 3) & 1);
+            uint32_t b[4];
+            ldsm4(b, sk + (uint32_t)((k / 4) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
+            mma_bf16(c[i], a, b[0], b[1]);
+            mma_bf16(c[i + 1], a, b[2], b[3]);
           }
         }
         const bool whole = k0 + F::kStep <= key.end && (!RANGES || (k0 >= key.all_lo && k0 + F::kStep <= key.all_hi));
@@ -514,58 +261,28 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
-          if constexpr (F::kF32) {
-            uint32_t ph[4], pm[4], pl[4];
+          const uint32_t pa[4] = {pack2(c[i][0], c[i][1]), pack2(c[i][2], c[i][3]), pack2(c[i + 1][0], c[i + 1][1]),
+                                  pack2(c[i + 1][2], c[i + 1][3])};
+          const int row = r0 + 8 * i + (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              split(c[i + (e >> 1)][2 * (e & 1)], c[i + (e >> 1)][2 * (e & 1) + 1], ph[e], pm[e], pl[e]);
+          for (int n = 0; n < D / 8; n += 2) {
+            const int chunk = (n & 7) + (lane >> 4);
+            uint32_t b[4];
+            ldsm4_t(b, sv + (uint32_t)((n / 8) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
+            if (RANGES && !whole)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              uint32_t h[2], m[2], l[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {  // keys 2 tig + 8 e and the next, dim 8 n + gid
-                float x[2];
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                  const int row = r0 + 8 * i + 8 * e + 2 * tig + f, chunk = 2 * (n & 3) + (gid >> 2);
-                  x[f] = *reinterpret_cast<const float*>(sbase + (sv - base) + (n / 4) * F::kTile * 128 + row * 128 +
-                                                         ((chunk ^ (row & 7)) << 4) + (gid & 3) * 4);
-                }
-                split(x[0], x[1], h[e], m[e], l[e]);
-                // (an infinity's middle part would be NaN, and 0 times it is NaN)
-                const uint32_t odd = ((h[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-                if (odd != 0u) {
-                  const uint32_t keep = ~((odd >> 15) * 0xffffu);
-                  h[e] &= keep, m[e] &= keep, l[e] &= keep;
-                  bad = true;
-                }
-              }
-              mma_parts(o[n], ph, pm, pl, h, m, l);
-            }
-          } else {
-            const uint32_t pa[4] = {pack2(c[i][0], c[i][1]), pack2(c[i][2], c[i][3]), pack2(c[i + 1][0], c[i + 1][1]),
-                                    pack2(c[i + 1][2], c[i + 1][3])};
-            const int row = r0 + 8 * i + (((lane >> 3) & 1) << 3) + (lane & 7);
-#pragma unroll
-            for (int n = 0; n < D / 8; n += 2) {
-              const int chunk = (n & 7) + (lane >> 4);
-              uint32_t b[4];
-              ldsm4_t(b, sv + (uint32_t)((n / 8) * F::kTile * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4));
-              if (RANGES && !whole)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) bad = clean(b[e]) || bad;
-              mma_bf16(o[n], pa, b[0], b[1]);
-              mma_bf16(o[n + 1], pa, b[2], b[3]);
-            }
+              for (int e = 0; e < 4; ++e) bad = clean(b[e]) || bad;
+            mma_bf16(o[n], pa, b[0], b[1]);
+            mma_bf16(o[n + 1], pa, b[2], b[3]);
           }
         }
-        if (kRestore && __any_sync(0xffffffffu, bad)) u0 = min(u0, k0), u1 = max(u1, k0 + F::kStep);
+        if (RANGES && __any_sync(0xffffffffu, bad)) u0 = min(u0, k0), u1 = max(u1, k0 + F::kStep);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
     }
     if (!ok && lane == 0) fail();
-    if (kRestore && u1 >= 0) {
+    if (RANGES && u1 >= 0) {
       // what was taken out of V for the rows that see it: p > 0 times it is itself, whatever p is.  The warp's keys
       // are one slice in kWK of every tile.
       const T* v = static_cast<const T*>(p.v) + (long long)w.kv0 * p.v_stride + w.g * D;
@@ -577,7 +294,7 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
             for (int i = 0; i < D / 8; ++i)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float x = as_float(v[j * p.v_stride + 8 * i + 2 * tig + e]);
+                const float x = __bfloat162float(v[j * p.v_stride + 8 * i + 2 * tig + e]);
                 if (!isfinite(x)) o[i][2 * r + e] += x;
               }
     }
@@ -609,34 +326,6 @@ __global__ void __launch_bounds__(Few<T, D, MT>::kThreads, Few<T, D, MT>::kCtas)
   finish<T>(p, w, slices, cluster, piece);
 }
 
-// ------------------------------------------------------------------------------ launches
-// Grid: items, each one's parts side by side (a cluster's are neighbours).
-template <typename... K, typename... A>
-cudaError_t launch_parts(void (*kern)(K...), long long items, int parts, int cluster, int threads, size_t smem,
-                         cudaStream_t s, A... args) {
-  if (items * parts >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * parts));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cluster > 1) {
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)cluster;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  return cudaLaunchKernelEx(&cfg, kern, args..., parts, cluster);
-}
-
 // Parts that meet in a cluster, or (`cut`) in the workspace.
 struct Meet {
   int parts, cluster;
@@ -646,55 +335,58 @@ Meet meet(const CrossPlan& plan, const CrossParams& p, int in_cluster) {
   return {in_cluster, in_cluster};
 }
 
-template <typename T, int D, int MT>
+template <int D, int MT>
 cudaError_t launch_few(const CrossParams& p, const CUtensorMap& mk, const CUtensorMap& mv, long long items, Meet m,
                        cudaStream_t s) {
-  using F = Few<T, D, MT>;
-  auto kern = p.ranges != nullptr ? few_kernel<T, D, MT, true> : few_kernel<T, D, MT, false>;
+  using F = Few<D, MT>;
+  auto kern = p.ranges != nullptr ? few_kernel<D, MT, true> : few_kernel<D, MT, false>;
   return launch_parts(kern, items, m.parts, m.cluster, F::kThreads, F::kSmem, s, mk, mv, p);
 }
 
-template <typename T, int D>
-cudaError_t launch_t(const cp_cross_args& a, const CrossPlan& plan, Meet m, const CrossParams& p, cudaStream_t s) {
+template <int D>
+cudaError_t launch_d(const cp_cross_args& a, const CrossPlan& plan, Meet m, const CrossParams& p, cudaStream_t s) {
   CUtensorMap mk, mv;
-  constexpr unsigned tile = Few<T, D, 1>::kTile;
-  const unsigned long long cols = (unsigned long long)p.Hkv * D;
-  const bool any = p.Nkv > 0;  // (no key: never loaded from)
-  const unsigned long long n = any ? p.Nkv : 1, ks = any ? a.k_stride : cols, vs = any ? a.v_stride : cols;
-  const auto make = sizeof(T) == 4 ? cp_make_f32_map_2d : cp_make_bf16_map_2d;
-  if (!make(&mk, any ? p.k : p.q, cols, n, ks, tile) || !make(&mv, any ? p.v : p.q, cols, n, vs, tile))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = plan.rows <= 16 ? launch_few<T, D, 1>(p, mk, mv, plan.items, m, s)
-                        : plan.rows <= 32 ? launch_few<T, D, 2>(p, mk, mv, plan.items, m, s)
-                                          : launch_few<T, D, 4>(p, mk, mv, plan.items, m, s);
+  if (!few_maps(a, p, Few<D, 1>::kTile, &mk, &mv)) return cudaErrorInvalidValue;
+  const cudaError_t e = plan.rows <= 16 ? launch_few<D, 1>(p, mk, mv, plan.items, m, s)
+                        : plan.rows <= 32 ? launch_few<D, 2>(p, mk, mv, plan.items, m, s)
+                                          : launch_few<D, 4>(p, mk, mv, plan.items, m, s);
   if (e != cudaSuccess || p.n_split == 0) return e;
-  return launch_merge<T, D>(p, s);
+  return launch_merge<__nv_bfloat16, D>(p, s);
 }
 
-// Keys of a tile, and CTAs that are resident at once.
+// 16 KB of keys (what the plan counts in), and CTAs that are resident at once.
 int tile_of(const cp_cross_args& a) { return 16384 / (a.head_dim * (a.dtype == CP_F32 ? 4 : 2)); }
-template <typename T, int D>
+template <int D>
 int ctas_of(int rows) {
-  return rows <= 16 ? Few<T, D, 1>::kCtas : rows <= 32 ? Few<T, D, 2>::kCtas : Few<T, D, 4>::kCtas;
+  return rows <= 16 ? Few<D, 1>::kCtas : rows <= 32 ? Few<D, 2>::kCtas : Few<D, 4>::kCtas;
 }
 int slots_of(const cp_cross_args& a, int rows, int sms) {
-  if (a.dtype == CP_F32) return sms * (a.head_dim == 64 ? ctas_of<float, 64>(rows) : ctas_of<float, 128>(rows));
-  return sms * (a.head_dim == 64 ? ctas_of<__nv_bfloat16, 64>(rows) : ctas_of<__nv_bfloat16, 128>(rows));
+  if (a.dtype == CP_F32) return sms * cp_cross_f32_ctas(rows);
+  return sms * (a.head_dim == 64 ? ctas_of<64>(rows) : ctas_of<128>(rows));
 }
 
-// Parts of an item that meet in a cluster: as many as the GPU takes at once, each with a tile at least.  More items than
-// that: parts of eight tiles or more until there are twice as many as the GPU takes, so that the last ones are short (64 sequences
-// of 512 .. 4096 states, 8 kv heads, three CTAs on an SM: 101.5 us; 105.5 whole, 109 with four times as many).
+// Parts of an item that meet in a cluster, by an estimate.  A CTA takes about 4.5 us and a time for each tile of its part;
+// all together no less than the memory's rate allows (f32: or the tensor pipe's, for NB blocks of 8 rows).  If all run at
+// once the longest decides, else the load of a place and most of the longest.  How far lengths differ is only known from
+// the totals; of a padded batch they are taken to be about half of the longest.  (22 sequences of 674 .. 5392 states, 8 kv
+// heads, 24 rows: 94 us whole, 72 in three; 64 of 512 .. 4096, 16 rows: 105.5 whole, 98.6 in two, 109 in four; 43 of up to
+// 268, 4 kv heads: 6.6 whole, 11.2 in two; f32, 4 of up to 7668, 8 kv heads, 9 rows: 84 in three, 51 in eight.)
 int cluster_of(const cp_cross_args& a, const CrossPlan& c, int sms) {
-  const int tile = tile_of(a);
-  const long long key_tiles = ((long long)a.max_seqlen_kv + tile - 1) / tile, slots = slots_of(a, c.rows, sms);
-  long long parts = slots / c.items;
-  if (parts < 1) {
-    parts = (2 * slots + c.items - 1) / c.items;
-    if (parts > key_tiles / 8) parts = key_tiles / 8;
+  const bool f32 = a.dtype == CP_F32;
+  const double tile = tile_of(a), slots = slots_of(a, c.rows, sms), items = (double)c.items;
+  const double longest = ceil(a.max_seqlen_kv / tile);
+  const double usual = fmin(a.kv_lens != nullptr && a.num_seqs > 1 ? 0.55 * longest : longest, a.total_kv / (double)a.num_seqs / tile);
+  const double each = f32 ? 1.1 : c.rows <= 16 ? 0.55 : 1.0;
+  const double all = 3 + items * usual * fmax(0.0051, f32 ? 0.22 / sms * ceil(c.rows / 8.0) : 0.0);
+  int best = 1;
+  double least = 0;
+  for (int k = 1; k <= kMaxCluster && (k == 1 || k <= longest); ++k) {
+    const double ctas = items * k, most = 4.5 + each * ceil(longest / k);
+    const double t = ctas <= slots ? fmax(most, all)
+                                   : fmax(ctas / slots * (4.5 + each * usual / k), all + 3 * ctas / slots) + 0.75 * most;
+    if (k == 1 || t < 0.97 * least) best = k, least = t;
   }
-  if (parts > key_tiles) parts = key_tiles;
-  return (int)(parts < 1 ? 1 : parts > kMaxCluster ? kMaxCluster : parts);
+  return best;
 }
 
 }  // namespace
@@ -734,8 +426,6 @@ cudaError_t cp_launch_cross_few(const cp_cross_args& a, float scale, void* ws, s
   cpattn::CrossParams p;
   cp_cross_fill(p, a, plan, scale, ws, ws_bytes, out, lse);
   const cpattn::Meet m = cpattn::meet(plan, p, cpattn::cluster_of(a, plan, sms));
-  if (a.dtype == CP_F32)
-    return a.head_dim == 64 ? cpattn::launch_t<float, 64>(a, plan, m, p, s) : cpattn::launch_t<float, 128>(a, plan, m, p, s);
-  return a.head_dim == 64 ? cpattn::launch_t<__nv_bfloat16, 64>(a, plan, m, p, s)
-                          : cpattn::launch_t<__nv_bfloat16, 128>(a, plan, m, p, s);
+  if (a.dtype == CP_F32) return cp_launch_cross_f32(a, plan, m.parts, m.cluster, scale, ws, ws_bytes, out, lse, s);
+  return a.head_dim == 64 ? cpattn::launch_d<64>(a, plan, m, p, s) : cpattn::launch_d<128>(a, plan, m, p, s);
 }
