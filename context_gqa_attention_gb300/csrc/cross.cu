@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kSlots = 4;
-constexpr int kRegsFirst = 88, kRegsSoftmax = 208, kRegsLaunch = 168;
+constexpr int kRegsFirst = 72, kRegsSoftmax = 216, kRegsLaunch = 168;
 static_assert(kRegsFirst + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register budgets exceed the launch");
 constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
 
@@ -64,22 +64,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int KB = D / 64;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  chained_start();
-
-  // ---- the item, or the part of one
-  int piece = -1, part = 0;
-  unsigned index = blockIdx.x;
-  if ((int)index >= p.n_whole) {
-    piece = (int)index - p.n_whole;
-    part = piece % p.split_k;
-    index = (unsigned)p.n_whole + (unsigned)(piece / p.split_k);
-  }
-  const CrossItem w = cross_item(p, index, threadIdx.x == 0 && part == 0);
-  if (w.tokens == 0) return;
-  const int per_tile = p.span / 2;  // tokens
-  const int rows0 = min(w.tokens, per_tile) * p.G, rows1 = max(0, w.tokens - per_tile) * p.G;
-  const bool two = rows1 > 0;
-
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sbase = smem_raw + (base - raw);
@@ -91,6 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1u;
     report(p.err, CP_ERR_TIMEOUT);
   };
+  // what needs nothing of the call's memory comes before the last call is waited for
   if (threadIdx.x == 0) {
     mbar_init(bar(Sm::bQ), 1);
     for (int s = 0; s < kSlots; ++s) {
@@ -116,6 +101,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
     tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(misc), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)misc[0];
+  chained_start();
+
+  // ---- the item, or the part of one
+  int piece = -1, part = 0;
+  unsigned index = blockIdx.x;
+  if ((int)index >= p.n_whole) {
+    piece = (int)index - p.n_whole;
+    part = piece % p.split_k;
+    index = (unsigned)p.n_whole + (unsigned)(piece / p.split_k);
+  }
+  const CrossItem w = cross_item(p, index, threadIdx.x == 0 && part == 0);
+  if (w.tokens == 0) {
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int per_tile = p.span / 2;  // tokens
+  const int rows0 = min(w.tokens, per_tile) * p.G, rows1 = max(0, w.tokens - per_tile) * p.G;
+  const bool two = rows1 > 0;
+  if (threadIdx.x == 0) {
     mbar_expect_tx(bar(Sm::bQ), (two ? 2 : 1) * KB * per_tile * p.G * 128);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -125,28 +140,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(sQ + i * Sm::kQ + kb * BM * 128, &map_q, kb * 64, w.g * p.G, w.q0 + w.t0 + i * per_tile,
                       bar(Sm::bQ));
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(misc), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  if constexpr (RANGES) {
-    for (int t = threadIdx.x; t < w.tokens; t += kThreads) {
-      int lo, hi;
-      cross_range(p, w, w.t0 + t, lo, hi);
-      int* m = misc + (t < per_tile ? 4 : 8);
-      if (lo < hi) {
+  if constexpr (RANGES) {  // a softmax warp a stretch of its row tile's tokens
+    if (warp >= 4) {
+      const int i = (warp - 4) >> 2, first = i * per_tile, n = min(per_tile, w.tokens - first);
+      int lo = 0x7fffffff, hi = 0, all_lo = 0, all_hi = 0x7fffffff;
+      for (int t = (int)threadIdx.x - 128 - 128 * i; t < n; t += 128) {
+        int a, b;
+        cross_range(p, w, w.t0 + first + t, a, b);
+        if (a < b) lo = min(lo, a), hi = max(hi, b);
+        all_lo = max(all_lo, a), all_hi = min(all_hi, b);
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+      all_lo = __reduce_max_sync(0xffffffffu, all_lo), all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+      if (lane == 0) {
+        int* m = misc + 4 + 4 * i;
         atomicMin(m, lo);
         atomicMax(m + 1, hi);
+        atomicMax(m + 2, all_lo);
+        atomicMin(m + 3, all_hi);
       }
-      atomicMax(m + 2, lo);
-      atomicMin(m + 3, hi);
     }
     __syncthreads();
   }
-  tc_fence_after();
-  const uint32_t tmem = (uint32_t)misc[0];
   // Key tiles of this CTA, counted from the first key that some row sees; each row tile works on those that one of its
   // rows sees.
   const int key_lo = RANGES ? min(misc[4], misc[8]) : 0, key_hi = RANGES ? max(misc[5], misc[9]) : w.keys;
@@ -207,8 +222,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer
       if (lane == 0) {
-        tma_prefetch_desc(&map_k);
-        tma_prefetch_desc(&map_v);
         bool ok = true;
         int issued = 0;  // ring fills: K(t) is fill 2 t, V(t) fill 2 t + 1
         for (int i = 0; i < 2 * ntiles; ++i) {
@@ -469,24 +482,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage_rows_bf16<D>(tO, inv, sb, lane);
           __syncwarp();
           const long long o = out_row(tile, min(row, rows - 1));
-          constexpr int E = D / 32;  // columns of a lane
-          const int col = E * lane;
-          const uint32_t a0 = sb + (uint32_t)((col / 64) * 4096 + (col % 8) * 2);
-          const int chunk = (col % 64) / 8;
+          constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes of a row, 16 bytes each, and rows at a time
+          const int c = lane % kLanes;
+          const uint32_t a0 = sb + (uint32_t)((c / 8) * 4096);
 #pragma unroll 8
-          for (int r = 0; r < 32; ++r) {
-            const long long at = __shfl_sync(0xffffffffu, o, r) * D + col;
-            if (r >= mine) break;
-            const uint32_t a = a0 + (uint32_t)(r * 128) + ((uint32_t)(chunk ^ (r & 7)) << 4);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at;
-            if constexpr (E == 4) {
-              uint2 x;
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
-              *reinterpret_cast<uint2*>(dst) = x;
-            } else {
-              uint32_t x;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
-              *reinterpret_cast<uint32_t*>(dst) = x;
+          for (int r0 = 0; r0 < 32; r0 += kAt) {
+            const int r = r0 + lane / kLanes;
+            const long long at = __shfl_sync(0xffffffffu, o, r) * D + 8 * c;
+            if (r0 >= mine) break;
+            if (r < mine) {
+              uint4 x;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                           : "r"(a0 + (uint32_t)(r * 128) + ((uint32_t)((c & 7) ^ (r & 7)) << 4)));
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at) = x;
             }
           }
           if (lane < mine && p.lse != nullptr) p.lse[o] = lse;
