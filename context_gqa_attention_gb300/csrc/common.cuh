@@ -141,9 +141,10 @@ cudaError_t cp_launch_decode(const cp_decode_args& a, float scale, cudaStream_t 
 bool cp_make_bf16_map_2d(void* map, const void* base, unsigned long long cols,
                          unsigned long long rows, unsigned long long pitch_elems,
                          unsigned box_rows);
-// The same of f32: box of 32 columns (128 bytes).
-bool cp_make_f32_map_2d(void* map, const void* base, unsigned long long cols, unsigned long long rows,
-                        unsigned long long pitch_elems, unsigned box_rows);
+// 3D TMA descriptor over rows of `blocks` x 128 bytes of bf16 or f32 (elem: bytes), seen as {128 bytes, rows, blocks}: one
+// box of box_rows rows x box_blocks blocks lands as [block][row][128 bytes]; 128-byte swizzle, zero fill.
+bool cp_make_columns_map(void* map, const void* base, int elem, unsigned long long blocks, unsigned long long rows,
+                         unsigned long long pitch_elems, unsigned box_rows, unsigned box_blocks);
 // 3D bf16 TMA descriptor over rows of `heads` heads of `cols` elements: box of 64 columns x box_heads heads x
 // box_rows rows, landing as box_rows * box_heads rows of 128 bytes; 128-byte swizzle, zero fill.
 bool cp_make_bf16_map_3d(void* map, const void* base, unsigned long long cols, unsigned long long heads,

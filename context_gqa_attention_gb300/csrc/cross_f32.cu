@@ -27,15 +27,15 @@ CP_DEV void split(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
 
 // The products are taken transposed, S^T = K Q^T and O^T = V^T P^T: a tile of K or V is an MMA's 16 rows and the query rows
 // are its 8 columns, so that 5 beams are padded to 8, and the many splits of K and V serve all query rows.  A producer warp
-// brings tiles of 8 KB through a ring (TMA, 128-byte swizzle); consumer warp (m, g) takes every kGroups-th tile for the NB
+// brings tiles of 16 keys through a ring (TMA, 128-byte swizzle); consumer warp (m, g) takes every kGroups-th tile for the NB
 // columns' blocks m, with a softmax reference of its own, so warps meet at the end only.  (Tiles of a warp's own, because
 // what bounds a warp is the latency of its chains: six MMAs on each accumulator.)
 template <int D, int NB, int MW>
 struct Fp32 {
   static constexpr int kRows = 8 * NB * MW;
-  static constexpr int kBytes = 8192, kTile = kBytes / (D * 4), kBoxes = D / 32;
-  // CTAs on an SM, and consumer warps of a block of rows (a CTA of 256 threads leaves them 255 registers)
-  static constexpr int kCtas = NB <= 2 ? 2 : 1, kGroups = NB <= 2 ? 4 : MW == 1 ? 7 : 3;
+  static constexpr int kTile = 16, kBytes = kTile * D * 4, kBoxes = D / 32;
+  // CTAs on an SM, and warps that take turns at the tiles: as many as the registers allow (128, 168, 255 a thread)
+  static constexpr int kCtas = NB <= 2 ? 2 : 1, kGroups = MW == 2 ? 3 : NB == 1 && D == 64 ? 7 : NB <= 2 ? 5 : 7;
   static constexpr int kConsumers = MW * kGroups, kThreads = 32 * (kConsumers + 1);
   // q as bf16, rows 16 bytes apart in the banks, the three parts one behind the other
   static constexpr int kQPitch = D * 2 + 16, kQPart = kRows * kQPitch;
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_range[4];
   __shared__ uint32_t s_abort;
+  __shared__ int s_issued;  // tiles whose copies have been issued
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
       mbar_init(empty(s), MW);
     }
     s_abort = 0u;
+    s_issued = F::kStages;  // (or all)
     fence_mbar_init();
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
@@ -95,12 +97,8 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
     const int s = t % F::kStages;
     const uint32_t dst = base + (uint32_t)(s * 2 * F::kBytes);
     mbar_expect_tx(full(s), 2 * F::kBytes);
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-#pragma unroll
-      for (int kb = 0; kb < F::kBoxes; ++kb)
-        tma_load_2d(dst + v * F::kBytes + kb * F::kTile * 128, v ? &map_v : &map_k, w.g * D + kb * 32,
-                    w.kv0 + key.first + t * F::kTile, full(s));
+    tma_load_3d(dst, &map_k, 0, w.kv0 + key.first + t * F::kTile, w.g * F::kBoxes, full(s));
+    tma_load_3d(dst + F::kBytes, &map_v, 0, w.kv0 + key.first + t * F::kTile, w.g * F::kBoxes, full(s));
   };
   // the first tiles are on their way while the other warps bring the rows of q
   const int early = min(ntiles, F::kStages);
@@ -133,6 +131,19 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
     *abort_flag = 1u;
     report(p.err, CP_ERR_TIMEOUT);
   };
+  // Tile t is there.  A barrier's phases are told apart by parity alone, and a warp has not seen the tile that was in the stage
+  // before: only once t has been issued is that one's phase over for certain.
+  const uint32_t issued_at = smem_u32(&s_issued);
+  auto arrived = [&](int t) -> bool {
+    const long long t0 = clock64();
+    for (uint32_t it = 1; t >= F::kStages; ++it) {
+      int n;
+      asm volatile("ld.acquire.cta.shared.b32 %0, [%1];" : "=r"(n) : "r"(issued_at) : "memory");
+      if (n > t) break;
+      if ((it & 31u) == 0 && (*abort_flag != 0u || clock64() - t0 > kBudget)) return false;
+    }
+    return mbar_wait(full(t % F::kStages), (uint32_t)(t / F::kStages) & 1u, abort_flag, kBudget);
+  };
 
   const int gid = lane >> 2, tig = lane & 3;
   const int wm = warp / F::kGroups, group = warp % F::kGroups, row0 = wm * 8 * NB;
@@ -156,6 +167,7 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
         }
         load(t);
         issued = t + 1;
+        asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(issued_at), "r"(issued) : "memory");
       }
       // every copy has landed before the CTA goes on to use the ring
       for (int t = max(0, issued - F::kStages); t < issued; ++t)
@@ -181,144 +193,140 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
     bool ok = true;
     for (int t = group; t < ntiles; t += F::kGroups) {
       const int s = t % F::kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(full(s), (uint32_t)(t / F::kStages) & 1u, abort_flag, kBudget));
+      ok = __all_sync(0xffffffffu, arrived(t));
       if (!ok) break;
       const uint8_t *pk = sbase + s * 2 * F::kBytes, *pv = pk + F::kBytes;
-#pragma unroll 1
-      for (int r0 = 0; r0 < F::kTile; r0 += 16) {
-        const int k0 = key.first + t * F::kTile + r0;  // first key
-        if (k0 >= key.end) break;
-        // S^T = K Q^T: keys gid (and + 8), rows 2 tig (and the next)
-        float c[NB][4], chain[kChains][NB][4];
+      const int k0 = key.first + t * F::kTile;  // first key
+      // S^T = K Q^T: keys gid (and + 8), rows 2 tig (and the next)
+      float c[NB][4], chain[kChains][NB][4];
 #pragma unroll
-        for (int i = 0; i < kChains; ++i)
+      for (int i = 0; i < kChains; ++i)
 #pragma unroll
-          for (int n = 0; n < NB; ++n) chain[i][n][0] = chain[i][n][1] = chain[i][n][2] = chain[i][n][3] = 0.f;
+        for (int n = 0; n < NB; ++n) chain[i][n][0] = chain[i][n][1] = chain[i][n][2] = chain[i][n][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t h[4], md[4], lw[4];
+      for (int k = 0; k < KS; ++k) {
+        uint32_t h[4], md[4], lw[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {  // key gid + 8 (e & 1), dims 16 k + 8 (e >> 1) + 2 tig and the next
-            const int row = r0 + gid + 8 * (e & 1), chunk = 4 * (k & 1) + 2 * (e >> 1) + (tig >> 1);
-            const float2 x = *reinterpret_cast<const float2*>(pk + (k / 2) * F::kTile * 128 + row * 128 +
-                                                              ((chunk ^ (row & 7)) << 4) + (tig & 1) * 8);
-            split(x.x, x.y, h[e], md[e], lw[e]);
-          }
+        for (int e = 0; e < 4; ++e) {  // key gid + 8 (e & 1), dims 16 k + 8 (e >> 1) + 2 tig and the next
+          const int row = gid + 8 * (e & 1), chunk = 4 * (k & 1) + 2 * (e >> 1) + (tig >> 1);
+          const float2 x = *reinterpret_cast<const float2*>(pk + (k / 2) * F::kTile * 128 + row * 128 +
+                                                            ((chunk ^ (row & 7)) << 4) + (tig & 1) * 8);
+          split(x.x, x.y, h[e], md[e], lw[e]);
+        }
 #pragma unroll
-          for (int n = 0; n < NB; n += 2) {
-            uint32_t bh[4], bm[4], bl[4];
-            const uint32_t a = sq + (uint32_t)(8 * n * F::kQPitch) + 32u * k + (n + 1 < NB ? second : 0u);
-            ldsm4(bh, a);
-            ldsm4(bm, a + F::kQPart);
-            ldsm4(bl, a + 2 * F::kQPart);
+        for (int n = 0; n < NB; n += 2) {
+          uint32_t bh[4], bm[4], bl[4];
+          const uint32_t a = sq + (uint32_t)(8 * n * F::kQPitch) + 32u * k + (n + 1 < NB ? second : 0u);
+          ldsm4(bh, a);
+          ldsm4(bm, a + F::kQPart);
+          ldsm4(bl, a + 2 * F::kQPart);
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              if (n + f >= NB) break;
-              float(&d)[4] = chain[k % kChains][n + f];
-              mma_bf16(d, lw, bh[2 * f], bh[2 * f + 1]);
-              mma_bf16(d, h, bl[2 * f], bl[2 * f + 1]);
-              mma_bf16(d, md, bm[2 * f], bm[2 * f + 1]);
-              mma_bf16(d, md, bh[2 * f], bh[2 * f + 1]);
-              mma_bf16(d, h, bm[2 * f], bm[2 * f + 1]);
-              mma_bf16(d, h, bh[2 * f], bh[2 * f + 1]);
-            }
+          for (int f = 0; f < 2; ++f) {
+            if (n + f >= NB) break;
+            float(&d)[4] = chain[k % kChains][n + f];
+            mma_bf16(d, lw, bh[2 * f], bh[2 * f + 1]);
+            mma_bf16(d, h, bl[2 * f], bl[2 * f + 1]);
+            mma_bf16(d, md, bm[2 * f], bm[2 * f + 1]);
+            mma_bf16(d, md, bh[2 * f], bh[2 * f + 1]);
+            mma_bf16(d, h, bm[2 * f], bm[2 * f + 1]);
+            mma_bf16(d, h, bh[2 * f], bh[2 * f + 1]);
           }
         }
-        const bool whole = k0 + 16 <= key.end && (!RANGES || (k0 >= key.all_lo && k0 + 16 <= key.all_hi));
-        float top[NB][2];
-        bool moves = false;
+      }
+      const bool whole = k0 + 16 <= key.end && (!RANGES || (k0 >= key.all_lo && k0 + 16 <= key.all_hi));
+      float top[NB][2];
+      bool moves = false;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          c[n][e] = chain[0][n][e], c[n][e + 2] = chain[0][n][e + 2];
+          if (kChains > 1) c[n][e] += chain[kChains - 1][n][e], c[n][e + 2] += chain[kChains - 1][n][e + 2];
+          if (!whole) {
+            const int a = max(lo[n][e], key.first) - k0, b = min(hi[n][e], key.end) - k0;
+            if (gid < a || gid >= b) c[n][e] = -INFINITY;
+            if (gid + 8 < a || gid + 8 >= b) c[n][e + 2] = -INFINITY;
+          }
+          top[n][e] = fmaxf(c[n][e], c[n][e + 2]) * sc;
+          moves = moves || top[n][e] > m[n][e] + kMaxGrowth;
+        }
+      if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            c[n][e] = chain[0][n][e], c[n][e + 2] = chain[0][n][e + 2];
-            if (kChains > 1) c[n][e] += chain[kChains - 1][n][e], c[n][e + 2] += chain[kChains - 1][n][e + 2];
-            if (!whole) {
-              const int a = max(lo[n][e], key.first) - k0, b = min(hi[n][e], key.end) - k0;
-              if (gid < a || gid >= b) c[n][e] = -INFINITY;
-              if (gid + 8 < a || gid + 8 >= b) c[n][e + 2] = -INFINITY;
+            float x = top[n][e], alpha = 1.f;
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            if (x > m[n][e]) {
+              alpha = m[n][e] == -INFINITY ? 1.f : ex2(m[n][e] - x);  // (no key yet: sums of 0)
+              m[n][e] = x;
             }
-            top[n][e] = fmaxf(c[n][e], c[n][e + 2]) * sc;
-            moves = moves || top[n][e] > m[n][e] + kMaxGrowth;
+            l[n][e] *= alpha;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) o[i][n][e] *= alpha, o[i][n][e + 2] *= alpha;
           }
-        if (__any_sync(0xffffffffu, moves)) {
+      }
+      // P^T as B fragments (three parts), two keys a lane: the transposed scores' accumulators
+      uint32_t ph[NB][2], pm[NB][2], pl[NB][2];
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
+      for (int n = 0; n < NB; ++n) {
+        const float n0 = m[n][0] == -INFINITY ? 0.f : -m[n][0], n1 = m[n][1] == -INFINITY ? 0.f : -m[n][1];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = top[n][e], alpha = 1.f;
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              if (x > m[n][e]) {
-                alpha = m[n][e] == -INFINITY ? 1.f : ex2(m[n][e] - x);  // (no key yet: sums of 0)
-                m[n][e] = x;
-              }
-              l[n][e] *= alpha;
+        for (int e = 0; e < 4; ++e) c[n][e] = ex2(fmaf(c[n][e], sc, (e & 1) ? n1 : n0));
+        l[n][0] += c[n][0] + c[n][2];
+        l[n][1] += c[n][1] + c[n][3];
 #pragma unroll
-              for (int i = 0; i < KS; ++i) o[i][n][e] *= alpha, o[i][n][e + 2] *= alpha;
-            }
+        for (int e = 0; e < 2; ++e) {
+          split(c[n][2 * e], c[n][2 * e + 1], ph[n][e], pm[n][e], pl[n][e]);
+          ph[n][e] = transposed(ph[n][e]), pm[n][e] = transposed(pm[n][e]), pl[n][e] = transposed(pl[n][e]);
         }
-        // P^T as B fragments (three parts), two keys a lane: the transposed scores' accumulators
-        uint32_t ph[NB][2], pm[NB][2], pl[NB][2];
+      }
+      if (k0 + 16 > key.end) {  // V rows that are no key of any row
+        const int z = key.end - k0;
+        for (int i = lane; i < F::kBoxes * 16 * 8; i += 32) {
+          const int row = (i >> 3) & 15, kb = i >> 7;
+          if (row >= z)
+            *reinterpret_cast<uint4*>(sbase + s * 2 * F::kBytes + F::kBytes + kb * F::kTile * 128 + row * 128 +
+                                      (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+      }
+      // O^T += V^T P^T
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        uint32_t h[4], md[4], lw[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // dim 16 i + 8 (e & 1) + gid, keys 8 (e >> 1) + 2 tig and the next
+          float x[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int row = 8 * (e >> 1) + 2 * tig + f, chunk = 4 * (i & 1) + 2 * (e & 1) + (gid >> 2);
+            x[f] = *reinterpret_cast<const float*>(pv + (i / 2) * F::kTile * 128 + row * 128 +
+                                                   ((chunk ^ (row & 7)) << 4) + (gid & 3) * 4);
+          }
+          split(x[0], x[1], h[e], md[e], lw[e]);
+          // (an infinity's middle part would be NaN, and 0 times it is NaN)
+          const uint32_t odd = ((h[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+          if (odd != 0u) {
+            const uint32_t keep = ~((odd >> 15) * 0xffffu);
+            h[e] &= keep, md[e] &= keep, lw[e] &= keep;
+            bad = true;
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          const float n0 = m[n][0] == -INFINITY ? 0.f : -m[n][0], n1 = m[n][1] == -INFINITY ? 0.f : -m[n][1];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) c[n][e] = ex2(fmaf(c[n][e], sc, (e & 1) ? n1 : n0));
-          l[n][0] += c[n][0] + c[n][2];
-          l[n][1] += c[n][1] + c[n][3];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            split(c[n][2 * e], c[n][2 * e + 1], ph[n][e], pm[n][e], pl[n][e]);
-            ph[n][e] = transposed(ph[n][e]), pm[n][e] = transposed(pm[n][e]), pl[n][e] = transposed(pl[n][e]);
-          }
+          mma_bf16(o[i][n], lw, ph[n][0], ph[n][1]);
+          mma_bf16(o[i][n], h, pl[n][0], pl[n][1]);
+          mma_bf16(o[i][n], md, pm[n][0], pm[n][1]);
+          mma_bf16(o[i][n], md, ph[n][0], ph[n][1]);
+          mma_bf16(o[i][n], h, pm[n][0], pm[n][1]);
+          mma_bf16(o[i][n], h, ph[n][0], ph[n][1]);
         }
-        if (k0 + 16 > key.end) {  // V rows that are no key of any row
-          const int z = key.end - k0;
-          for (int i = lane; i < F::kBoxes * 16 * 8; i += 32) {
-            const int row = (i >> 3) & 15, kb = i >> 7;
-            if (row >= z)
-              *reinterpret_cast<uint4*>(sbase + s * 2 * F::kBytes + F::kBytes + kb * F::kTile * 128 + (r0 + row) * 128 +
-                                        (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          __syncwarp();
-        }
-        // O^T += V^T P^T
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          uint32_t h[4], md[4], lw[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {  // dim 16 i + 8 (e & 1) + gid, keys 8 (e >> 1) + 2 tig and the next
-            float x[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int row = r0 + 8 * (e >> 1) + 2 * tig + f, chunk = 4 * (i & 1) + 2 * (e & 1) + (gid >> 2);
-              x[f] = *reinterpret_cast<const float*>(pv + (i / 2) * F::kTile * 128 + row * 128 +
-                                                     ((chunk ^ (row & 7)) << 4) + (gid & 3) * 4);
-            }
-            split(x[0], x[1], h[e], md[e], lw[e]);
-            // (an infinity's middle part would be NaN, and 0 times it is NaN)
-            const uint32_t odd = ((h[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-            if (odd != 0u) {
-              const uint32_t keep = ~((odd >> 15) * 0xffffu);
-              h[e] &= keep, md[e] &= keep, lw[e] &= keep;
-              bad = true;
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            mma_bf16(o[i][n], lw, ph[n][0], ph[n][1]);
-            mma_bf16(o[i][n], h, pl[n][0], pl[n][1]);
-            mma_bf16(o[i][n], md, pm[n][0], pm[n][1]);
-            mma_bf16(o[i][n], md, ph[n][0], ph[n][1]);
-            mma_bf16(o[i][n], h, pm[n][0], pm[n][1]);
-            mma_bf16(o[i][n], h, ph[n][0], ph[n][1]);
-          }
-        }
-        if (__any_sync(0xffffffffu, bad)) u0 = min(u0, k0), u1 = max(u1, k0 + 16);
       }
+      if (__any_sync(0xffffffffu, bad)) u0 = min(u0, k0), u1 = max(u1, k0 + 16);
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
     }
@@ -343,12 +351,11 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
   } else {
     // a warp without rows keeps the ring going
     for (int t = group; t < ntiles; t += F::kGroups) {
-      const int s = t % F::kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(full(s), (uint32_t)(t / F::kStages) & 1u, abort_flag, kBudget))) {
+      if (!__all_sync(0xffffffffu, arrived(t))) {
         if (lane == 0) fail();
         break;
       }
-      if (lane == 0) mbar_arrive(empty(s));
+      if (lane == 0) mbar_arrive(empty(t % F::kStages));
     }
   }
   __syncthreads();  // the ring is done with

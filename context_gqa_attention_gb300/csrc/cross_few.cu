@@ -96,12 +96,8 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
     const int s = t % F::kStages;
     const uint32_t dst = base + (uint32_t)(s * 2 * F::kBytes);
     mbar_expect_tx(full(s), 2 * F::kBytes);
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-#pragma unroll
-      for (int kb = 0; kb < F::kBoxes; ++kb)
-        tma_load_2d(dst + v * F::kBytes + kb * F::kTile * 128, v ? &map_v : &map_k, w.g * D + kb * 64,
-                    w.kv0 + key.first + t * F::kTile, full(s));
+    tma_load_3d(dst, &map_k, 0, w.kv0 + key.first + t * F::kTile, w.g * F::kBoxes, full(s));
+    tma_load_3d(dst + F::kBytes, &map_v, 0, w.kv0 + key.first + t * F::kTile, w.g * F::kBoxes, full(s));
   };
   // the first tiles are on their way while the other warps bring the rows of q
   const int early = min(ntiles, F::kStages);

@@ -233,8 +233,10 @@ inline bool few_maps(const cp_cross_args& a, const CrossParams& p, int tile, CUt
   const unsigned long long cols = (unsigned long long)p.Hkv * a.head_dim;
   const bool any = p.Nkv > 0;  // (no key: never loaded from)
   const unsigned long long n = any ? p.Nkv : 1, ks = any ? a.k_stride : cols, vs = any ? a.v_stride : cols;
-  const auto make = a.dtype == CP_F32 ? cp_make_f32_map_2d : cp_make_bf16_map_2d;
-  return make(k, any ? p.k : p.q, cols, n, ks, tile) && make(v, any ? p.v : p.q, cols, n, vs, tile);
+  const int elem = a.dtype == CP_F32 ? 4 : 2;
+  const unsigned blocks = (unsigned)(a.head_dim * elem / 128);
+  return cp_make_columns_map(k, any ? p.k : p.q, elem, cols * elem / 128, n, ks, tile, blocks) &&
+         cp_make_columns_map(v, any ? p.v : p.q, elem, cols * elem / 128, n, vs, tile, blocks);
 }
 
 }  // namespace

@@ -1322,17 +1322,18 @@ bool cp_make_bf16_map_2d(void* map, const void* base, unsigned long long cols,
   return cpattn::make_map(static_cast<CUtensorMap*>(map), base, cols, rows, pitch_elems, box_rows);
 }
 
-bool cp_make_f32_map_2d(void* map, const void* base, unsigned long long cols, unsigned long long rows,
-                        unsigned long long pitch_elems, unsigned box_rows) {
+bool cp_make_columns_map(void* map, const void* base, int elem, unsigned long long blocks, unsigned long long rows,
+                         unsigned long long pitch_elems, unsigned box_rows, unsigned box_blocks) {
   cpattn::EncodeTiledFn fn = cpattn::encode_fn();
   if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {pitch_elems * 4};
-  cuuint32_t box[2] = {32, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t cols = 128 / elem;
+  cuuint64_t dims[3] = {cols, rows, blocks};
+  cuuint64_t strides[2] = {pitch_elems * elem, 128};
+  cuuint32_t box[3] = {cols, box_rows, box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(static_cast<CUtensorMap*>(map), elem == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool cp_make_bf16_map_3d(void* map, const void* base, unsigned long long cols, unsigned long long heads,

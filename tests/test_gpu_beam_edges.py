@@ -65,6 +65,19 @@ def test_padded_batches_between_guards(lib, B, T, S, Hq, Hkv, d, dtype, ranged):
     assert bool((ws[:256] == 0xa5).all()) and bool((ws[256 + need:] == 0xa5).all())
 
 
+@pytest.mark.parametrize("T,Hq,d", [(5, 1, 128), (15, 1, 128), (9, 3, 64)])
+def test_many_tiles_in_flight_on_every_sm(lib, T, Hq, d):
+    """f32 under load: copies of consecutive tiles land in any order, and a warp takes only some of them."""
+    B, S = 152, 2000
+    g = torch.Generator(device=DEV).manual_seed(T)
+    k, v = (torch.randn(B * S, 1, d, generator=g, device=DEV) for _ in range(2))
+    q = torch.randn(B * T, Hq, d, generator=g, device=DEV)
+    spans = [(b * T, T, b * S, S) for b in range(B)]
+    for _ in range(3):
+        out, lse = lib.cp_cross_attention(q, _cu([T] * B), k, v, _cu([S] * B), max_seqlen_q=T, max_seqlen_kv=S)
+    check(out, lse, exact(q, k, v, spans, d ** -0.5), True)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_scores_that_are_not_finite_and_scores_in_place(lib, dtype):
     g = torch.Generator(device=DEV).manual_seed(5)
