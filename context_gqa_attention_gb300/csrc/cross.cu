@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per_tile = p.span / 2;  // tokens
   const int rows0 = min(w.tokens, per_tile) * p.G, rows1 = max(0, w.tokens - per_tile) * p.G;
   const bool two = rows1 > 0;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {  // (a copy takes its thread about 100 cycles; the producer's first ones go out meanwhile)
     mbar_expect_tx(bar(Sm::bQ), (two ? 2 : 1) * KB * per_tile * p.G * 128);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -233,10 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const CUtensorMap* map = (i & 1) ? &map_v : &map_k;
           const uint32_t full = bar(clean_last && i == 2 * ntiles - 1 ? Sm::bLast : Sm::bFull + slot);
           mbar_expect_tx(full, Sm::kKV);
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-            tma_load_2d(sKV + slot * Sm::kKV + kb * BN * 128, map, w.g * D + kb * 64, w.kv0 + k_first + (i >> 1) * BN,
-                        full);
+          tma_load_3d(sKV + slot * Sm::kKV, map, 0, w.kv0 + k_first + (i >> 1) * BN, w.g * KB, full);
           issued = i + 1;
         }
         if (!ok) fail();
@@ -525,9 +522,9 @@ cudaError_t launch(const cp_cross_args& a, const CrossPlan& plan, float scale, v
                            (unsigned long long)a.q_stride, (unsigned)p.G, per_tile))
     return cudaErrorInvalidValue;
   if (p.Nkv > 0) {
-    const unsigned long long cols = (unsigned long long)p.Hkv * D, rows = (unsigned long long)p.Nkv;
-    if (!cp_make_bf16_map_2d(&mk, a.k, cols, rows, (unsigned long long)a.k_stride, BN) ||
-        !cp_make_bf16_map_2d(&mv, a.v, cols, rows, (unsigned long long)a.v_stride, BN))
+    const unsigned long long blocks = (unsigned long long)p.Hkv * (D / 64), rows = (unsigned long long)p.Nkv;
+    if (!cp_make_columns_map(&mk, a.k, 2, blocks, rows, (unsigned long long)a.k_stride, BN, D / 64) ||
+        !cp_make_columns_map(&mv, a.v, 2, blocks, rows, (unsigned long long)a.v_stride, BN, D / 64))
       return cudaErrorInvalidValue;
   } else {
     mk = mv = mq;  // (no key: never loaded from)
