@@ -4,7 +4,12 @@
 //   out_i = softmax over the keys j in [lo_i, hi_i) of scale q_i.k_j, times V
 //
 // Each operand is the sum of three bf16 numbers (high, middle, low: 24 bits) and a product the sum of the six of theirs
-// that count, in fp32, on the legacy tensor path.
+// that count, in fp32, on the legacy tensor path.  (Products of tf32 pairs, three of them: 25 cycles of a sub-partition each
+// against 8.1 for a bf16 MMA, which has twice the work.)
+//
+// Bound: for up to 8 rows a kv head HBM once there is work for every SM (152 sequences of 2000 states, d = 128: 5.8 TB/s, 85%
+// of the copy; d = 64: 5.2); for 16 rows 4.5 TB/s, for 32 the tensor pipe at 3.1.  8 sequences of 0 .. 900 states, 5 beams of
+// 16 heads, d = 64: 15.6 us against 3.5 for their bytes: the start, the longest part, the cluster's meeting.
 #include "cross_few.cuh"
 
 namespace cpattn {
@@ -29,7 +34,9 @@ CP_DEV void split(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
 // are its 8 columns, so that 5 beams are padded to 8, and the many splits of K and V serve all query rows.  A producer warp
 // brings tiles of 16 keys through a ring (TMA, 128-byte swizzle); consumer warp (m, g) takes every kGroups-th tile for the NB
 // columns' blocks m, with a softmax reference of its own, so warps meet at the end only.  (Tiles of a warp's own, because
-// what bounds a warp is the latency of its chains: six MMAs on each accumulator.)
+// what bounds a warp is the latency of its chains: six MMAs on each accumulator, 20 cycles each.  With the query rows as the
+// MMA's 16 rows and warps on slices of the same tiles: 80 us where this takes 54, for 4 sequences of up to 7668 states, 9 rows, 8 kv
+// heads.)
 template <int D, int NB, int MW>
 struct Fp32 {
   static constexpr int kRows = 8 * NB * MW;
