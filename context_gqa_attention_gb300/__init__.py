@@ -853,7 +853,7 @@ def cp_decode_attention_q4(q, k_cache, v_cache, block_tables, seq_lens, cp, inte
 def cp_cross_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_kv, *,
                                       total_q=None, total_kv=None, padded=False, dtype=torch.bfloat16):
     """Bytes of workspace with which cp_cross_attention cuts the keys of these sizes into parts on the current
-    device (0: it does not).  total_q, total_kv: rows of q and of k (num_seqs of the longest, if not given); padded:
+    device (0: it needs none).  total_q, total_kv: rows of q and of k (num_seqs of the longest, if not given); padded:
     the call gets kv_lens or key_ranges."""
     load()
     a = CrossArgs()
@@ -880,7 +880,7 @@ def cp_cross_attention(q, cu_seqlens_q, k, v, cu_seqlens_kv, *, kv_lens=None, ke
     kv_lens int32 [B]: a sequence's keys are its first kv_lens[b] rows (a padded batch).  key_ranges int32
     [Nq, 2]: each row sees the keys [lo, hi) of its sequence.  q, k and v may be column slices of a wider tensor
     (any token stride).  bf16 or f32.  `workspace`: uint8 CUDA tensor of cp_cross_attention_workspace_size()
-    bytes; None allocates it, an empty one cuts nothing.  max_seqlen_q is fetched from the device if it is not
+    bytes; None allocates it, an empty one leaves out the cuts that need it.  max_seqlen_q is fetched from the device if it is not
     given; max_seqlen_kv only guides the cut (the average is taken).
     Returns (out [Nq, Hq, d] dtype of q, lse [Nq, Hq] f32 or None)."""
     binding = _binding()

@@ -12,8 +12,8 @@
 //   2-3    V guards: 0 times an infinity or a NaN is NaN, so they clear the V rows behind the last key, and with
 //          key ranges (RANGES) every element that is not finite in tiles that some row sees in part
 //   4-11   two softmax warpgroups, one a tile, a thread a row
-// Parts (CrossParams): the keys of the last wave's items, or of all when they are few, are cut so that every SM
-// has work; cross_merge_kernel joins them.
+// Parts: the keys of the last wave's items, or of all when they are few, are cut so that every SM has work; they meet in the
+// shared memory of a cluster (CLUSTER), or in the workspace, where cross_merge_kernel joins them.
 //
 // Bound: the chain of a row tile, softmax - PV - QK^T, about 2780 cycles a key tile of two row tiles (d = 128) against 2150 of
 // MMA: 8192 tokens over 6404 states, 16/2 heads, d = 128 take 292 us (1.47 PFLOP/s, 78% of the measured peak).  Short items: the
@@ -35,9 +35,8 @@ constexpr int kThreads = 384;
 constexpr int kSlots = 4;
 constexpr int kRegsFirst = 72, kRegsSoftmax = 216, kRegsLaunch = 168;
 static_assert(kRegsFirst + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register budgets exceed the launch");
-constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
 
-template <int D>
+template <int D, bool CLUSTER>
 struct Smem {
   static constexpr int kQ = BM * D * 2;
   static constexpr int kKV = BN * D * 2;
@@ -47,7 +46,9 @@ struct Smem {
   static constexpr int bQ = 0, bFull = 1, bEmpty = bFull + kSlots, bS = bEmpty + kSlots, bP = bS + 2, bO = bP + 2,
                        bFix = bO + 2, bLast = bFix + 2, bDone = bLast + 1, nBar = bDone + 1;
   static constexpr int oMisc = oBar + nBar * 8;  // TMEM base, abort flag, first / last unclean tile, keys of each row tile
-  static constexpr int kBytes = oMisc + 48;
+  static constexpr int oM = oMisc + 48, oL = oM + 4 * 2 * BM;  // of a cluster: a row's reference and sum,
+  static constexpr int oW = oL + 4 * 2 * BM;                    // and the parts' weights of this CTA's share of the rows
+  static constexpr int kBytes = CLUSTER ? oW + 4 * kMaxCluster * BM : oM;
   // the base is rounded up to the 1 KB swizzle atom; never below 120 KB, so that one CTA (and its 512 TMEM
   // columns) has an SM to itself
   static constexpr int kAlloc = (kBytes + 1024) > 120 * 1024 ? (kBytes + 1024) : 120 * 1024;
@@ -62,11 +63,11 @@ CP_DEV void mask_columns(float (&v)[32], int c0, int c1) {
   for (int k = 0; k < 32; ++k) v[k] = (seen & (1u << k)) != 0u ? v[k] : -INFINITY;
 }
 
-template <int D, bool RANGES>
+template <int D, bool RANGES, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const CrossParams p) {
-  using Sm = Smem<D>;
+  using Sm = Smem<D, CLUSTER>;
   constexpr int KB = D / 64;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -123,7 +124,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- the item, or the part of one
   int piece = -1, part = 0;
   unsigned index = blockIdx.x;
-  if ((int)index >= p.n_whole) {
+  if (CLUSTER) {
+    part = (int)(index % (unsigned)p.cluster);
+    index /= (unsigned)p.cluster;
+  } else if ((int)index >= p.n_whole) {
     piece = (int)index - p.n_whole;
     part = piece % p.split_k;
     index = (unsigned)p.n_whole + (unsigned)(piece / p.split_k);
@@ -172,8 +176,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rows sees.
   const int key_lo = RANGES ? min(misc[4], misc[8]) : 0, key_hi = RANGES ? max(misc[5], misc[9]) : w.keys;
   const int every = key_lo < key_hi ? (key_hi - key_lo + BN - 1) / BN : 0;
-  const int ta = piece < 0 ? 0 : (int)((long long)every * part / p.split_k);
-  const int ntiles = (piece < 0 ? every : (int)((long long)every * (part + 1) / p.split_k)) - ta;
+  int ta = 0, ntiles = every;
+  if (CLUSTER || piece >= 0) {
+    const int parts = CLUSTER ? p.cluster : p.split_k;
+    ta = (int)((long long)every * part / parts);
+    ntiles = (int)((long long)every * (part + 1) / parts) - ta;
+  }
   const int k_first = key_lo + ta * BN;  // first key
   int t_lo[2], t_hi[2], all_lo[2], all_hi[2];  // a row tile's key tiles; the keys that all its rows see
 #pragma unroll
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return ((long long)w.q0 + w.t0 + i * per_tile + t) * p.Hq + w.g * p.G + (row - t * p.G);
   };
 
-  if (ntiles <= 0) {  // no key
+  if (!CLUSTER && ntiles <= 0) {  // no key
     const int rows = rows0 + rows1;
     for (int r = threadIdx.x; r < rows; r += kThreads) {
       const int i = r >= rows0 ? 1 : 0, row = r - i * rows0;
@@ -279,8 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(bar(Sm::bO + tile));
         };
-        bool ok = mbar_wait(bar(Sm::bQ), 0u, abort_flag, kBudget) && mbar_wait(bar(Sm::bFull), 0u, abort_flag, kBudget);
-        if (ok) {
+        bool ok = (CLUSTER && ntiles == 0) || (mbar_wait(bar(Sm::bQ), 0u, abort_flag, kBudget) &&
+                                  mbar_wait(bar(Sm::bFull), 0u, abort_flag, kBudget));
+        if (ok && (!CLUSTER || ntiles > 0)) {
           tc_fence_after();
           if (has(0, 0)) issue_qk(0, 0);
           if (has(1, 0)) issue_qk(1, 0);
@@ -365,10 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = (warp - 4) >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane, rows = tile == 0 ? rows0 : rows1;
     const int t0 = t_lo[tile], t1 = t_hi[tile];
+    float* row_m = reinterpret_cast<float*>(sbase + Sm::oM) + tile * BM + row;  // (CLUSTER)
+    float* row_l = reinterpret_cast<float*>(sbase + Sm::oL) + tile * BM + row;
     if (rows > 0 && t0 == t1) {  // no key for this tile's rows
       if (row < rows) {
         const long long o = out_row(tile, row);
-        if (piece >= 0) {
+        if constexpr (CLUSTER) {
+          *row_m = -INFINITY, *row_l = 0.f;
+        } else if (piece >= 0) {
           p.ws_lse[(long long)piece * p.rows + tile * per_tile * p.G + row] = -INFINITY;
         } else {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o * D);
@@ -462,8 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Rows go out through shared memory, one whole row an instruction: tile 0 over the Q tiles (free: its last
         // PV came after the other tile's last QK), tile 1 over the ring (its last PV is the CTA's last MMA)
         const int mine = min(32, rows - q4 * 32);  // rows of this warp
-        const uint32_t sb = (tile == 0 ? sQ : sKV) + (uint32_t)(q4 * 32 * D * (piece >= 0 ? 4 : 2));
-        if (piece >= 0) {
+        const bool f32 = CLUSTER || piece >= 0;
+        const uint32_t sb = (tile == 0 ? sQ : sKV) + (uint32_t)(q4 * 32 * D * (f32 ? 4 : 2));
+        if constexpr (CLUSTER) {
+          stage_rows_f32<D>(tO, 1.f, sb, lane);
+          *row_m = m, *row_l = l;
+        } else if (piece >= 0) {
           stage_rows_f32<D>(tO, inv, sb, lane);
           __syncwarp();
           const long long r0 = (long long)piece * p.rows + tile * per_tile * p.G + q4 * 32;
@@ -507,6 +524,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         fail();
       }
     }
+    if constexpr (CLUSTER) {
+      // ---- the parts' rows as one: CTA r takes the r-th share of them
+      __syncwarp();
+      cluster_sync();
+      const int n = rows0 + rows1, rank = (int)cluster_rank(), k = p.cluster;
+      const int r0 = n * rank / k, mine = n * (rank + 1) / k - r0, tid = (int)threadIdx.x - 128;
+      float* weight = reinterpret_cast<float*>(sbase + Sm::oW);
+      auto slot = [&](int r) { return r < rows0 ? r : BM + r - rows0; };  // of a row of the item among those of both tiles
+      if (tid < mine) {
+        const uint32_t at = 4u * (uint32_t)slot(r0 + tid);
+        float ms[kMaxCluster], ls[kMaxCluster], M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          ms[c] = c < k ? peer_ld(peer_addr(sbase + Sm::oM, c) + at) : -INFINITY;
+          ls[c] = c < k ? peer_ld(peer_addr(sbase + Sm::oL, c) + at) : 0.f;
+          M = fmaxf(M, ms[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          ms[c] = ls[c] == 0.f ? 0.f : factor(ms[c], M);
+          L += ms[c] * ls[c];
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) weight[c * BM + tid] = ms[c] * inv;
+        if (p.lse != nullptr) p.lse[r0 + tid < rows0 ? out_row(0, r0 + tid) : out_row(1, r0 + tid - rows0)] = natural_lse(M, L);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      for (int i = tid; i < mine * (D / 4); i += 256) {
+        const int r = i / (D / 4), c4 = i % (D / 4), s = slot(r0 + r), row32 = s & 31;
+        const uint32_t at = (uint32_t)((s >> 7) * 2 * Sm::kQ + (s & 127) / 32 * (32 * D * 4) + (c4 / 8) * 4096 + row32 * 128) +
+                            ((uint32_t)((c4 & 7) ^ (row32 & 7)) << 4);
+        float4 x[kMaxCluster], o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float e[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          e[c] = c < k ? weight[c * BM + r] : 0.f;
+          if (e[c] != 0.f) x[c] = peer_ld4(peer_addr(sbase, c) + at);
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (e[c] != 0.f) o.x += e[c] * x[c].x, o.y += e[c] * x[c].y, o.z += e[c] * x[c].z, o.w += e[c] * x[c].w;
+        const long long to = (r0 + r < rows0 ? out_row(0, r0 + r) : out_row(1, r0 + r - rows0)) * D + 4 * c4;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another reads its shared memory
+    }
+  }
+  if (CLUSTER && warp < 4) {
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -536,17 +606,18 @@ cudaError_t launch(const cp_cross_args& a, const CrossPlan& plan, float scale, v
     mk = mv = mq;  // (no key: never loaded from)
   }
   const long long grid = p.n_whole + (long long)p.n_split * p.split_k;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  auto kern = a.key_ranges != nullptr ? cross_kernel<D, true> : cross_kernel<D, false>;
+  if (grid * p.cluster >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  auto kern = a.key_ranges != nullptr ? cross_kernel<D, true, false>
+              : p.cluster > 1         ? cross_kernel<D, false, true>
+                                      : cross_kernel<D, false, false>;
   // the warpgroups' register budgets assume the registers a thread of this launch gets; a build that gave the
   // kernel another count would leave an increase waiting, so refuse it
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
-  if (e != cudaSuccess) return e;
-  e = launch_chained(kern, dim3((unsigned)grid), kThreads, Smem<D>::kAlloc, s, mq, mk, mv, p);
+  const int smem = p.cluster > 1 ? Smem<D, true>::kAlloc : Smem<D, false>::kAlloc;
+  e = launch_parts(kern, grid, p.cluster, p.cluster, kThreads, smem, s, mq, mk, mv, p);
   if (e != cudaSuccess || p.n_split == 0) return e;
   return launch_merge<__nv_bfloat16, D>(p, s);
 }
@@ -554,11 +625,16 @@ cudaError_t launch(const cp_cross_args& a, const CrossPlan& plan, float scale, v
 }  // namespace
 }  // namespace cpattn
 
-// Time of an item: about 2.5 us and 1.75 a key tile (d = 64: 3 and 1.3), one on an SM; a part takes 3 us more to write its
-// fp32 rows, and the merge about 3 us and 0.05 a part.
-// Of items that are all alike, those of whole waves stay whole and the rest are cut into the number of parts that ends
-// soonest by that estimate.  Where they differ, how many there are and how long can only be guessed from the totals, and all
-// are cut or none: the load of an SM and half of the longest item decide.
+// Time of an item: about 2.5 us and 1.75 a key tile (d = 64: 3 and 1.3), one on an SM.  Its keys are cut in one of two ways.
+// Parts that meet in the workspace take 3 us more to write their fp32 rows, and the merge about 3 us and 0.05 a part; of items
+// that are all alike, those of whole waves stay whole and the rest are cut.  Parts of every item that meet in a cluster (up
+// to eight CTAs) take 4 us more (d = 128: 6 to 8, the fewer parts the more), and pay only where all clusters run at once: the
+// clusters of k CTAs that find k free SMs in one group are 76, 46, 36, 28, 23, 15 and 15 for k = 2 .. 8 by the occupancy query, some
+// fewer here, since other GPUs have other SMs switched off.  (8 items of 2000 states, d = 64: 13.1 us through the workspace, 12.0
+// in clusters of eight; 16: 16.1 and 13.3 in clusters of six, 22.4 of eight, which take turns; 32: 17.9 and 14.5 of four.)
+// Not for rows with ranges, whose keys are fewer than the totals say.
+// Where items differ, how many there are and how long can only be guessed from the totals: the load of an SM and half of the
+// longest item decide.
 CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms) {
   CrossPlan c;
   const double B = a.num_seqs;
@@ -588,6 +664,17 @@ CrossPlan cp_cross_plan_tc(const cp_cross_args& a, int sms) {
       c.split_k = k;
     }
   }
+  c.cluster = 1;
+  constexpr int kAtOnce[cpattn::kMaxCluster + 1] = {0, 0, 72, 44, 34, 26, 22, 14, 14};  // of 152 SMs
+  for (int k = 2; k <= cpattn::kMaxCluster && k <= most && a.key_ranges == nullptr; ++k) {
+    if (live * 152 > kAtOnce[k] * sms) break;
+    const double t = fixed + (a.head_dim == 64 ? 3.4 + 2.4 / k : 4.8 + 6.0 / k) + tile * ceil(most / k);
+    if (t < 0.97 * best) {
+      best = t;
+      c.cluster = k;
+    }
+  }
+  if (c.cluster > 1) c.split_k = 1;
   if (c.split_k > 1) c.n_split = alike ? (long long)rest : c.items;
   if (c.n_split == 0) c.split_k = 1;
   c.bytes = cp_cross_parts_bytes(c, a.head_dim);

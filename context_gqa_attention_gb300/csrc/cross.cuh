@@ -1,11 +1,42 @@
 // What the kernels of cp_cross_attention share (internal): the launch's parameters, a sequence's bounds, and the
-// merge of the parts of items whose keys were cut.
+// meeting of the parts of items whose keys were cut: in a cluster's shared memory, or in the workspace.
 #pragma once
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace cpattn {
 namespace {
+
+using namespace sm100;
+
+constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
+constexpr int kMaxCluster = 8;
+
+CP_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+CP_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+CP_DEV uint32_t peer_addr(const void* mine, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
+  return a;
+}
+CP_DEV float peer_ld(uint32_t a) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+CP_DEV float4 peer_ld4(uint32_t a) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
+  return x;
+}
 
 // An item is `span` tokens of a sequence under the G query heads of a kv head: span * G query rows, row p being
 // token p / G, head p mod G, which all see the same keys (or, with key_ranges, some of them).  Items n_whole ..
@@ -14,6 +45,7 @@ struct CrossParams {
   int B, Hq, Hkv, G, Nq, Nkv, max_q, span, tiles;  // tiles: items of the longest sequence
   int n_whole, n_split, split_k, rows;             // rows: of an item in the workspace
   int ordered;                                     // items in the order of their keys (see cross_item)
+  int cluster;                                     // many rows: parts of every item that meet in a cluster (1: none)
   float scale_log2;
   long long q_stride, k_stride, v_stride;
   const int32_t *cu_q, *cu_kv, *kv_lens, *ranges;
@@ -106,6 +138,13 @@ CP_DEV void cross_range(const CrossParams& p, const CrossItem& w, int token, int
   }
 }
 
+// Two sets of (reference in log2 units, sum, row) as one: the factor of a set whose reference is m.  (One of -inf saw
+// no finite score: its sums are 0, or NaN.)
+CP_DEV float factor(float m, float M) { return m == M || m == -INFINITY ? 1.f : exp2f(m - M); }
+CP_DEV float natural_lse(float M, float L) {
+  return L == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
+}
+
 // Parts -> rows: out = sum_k e_k out_k / sum_k e_k with e_k = exp(lse_k - max lse); a part without a key has the
 // LSE -inf and its row is not read.  A warp takes a row, its lanes the dims.
 template <typename T, int D>
@@ -170,12 +209,39 @@ cudaError_t launch_merge(const CrossParams& p, cudaStream_t s) {
   return launch_chained(cross_merge_kernel<T, D>, dim3((unsigned)p.n_split, (unsigned)y), 256, 0, s, p);
 }
 
+// Grid: items, each one's parts side by side (a cluster's are neighbours).
+template <typename... K, typename... A>
+cudaError_t launch_parts(void (*kern)(K...), long long items, int parts, int cluster, int threads, size_t smem,
+                         cudaStream_t s, A... args) {
+  if (items * parts >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * parts));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace
 }  // namespace cpattn
 
 // How a launch is made of items and parts (host).
 struct CrossPlan {
-  int span, tiles, rows, ordered;
+  int span, tiles, rows, ordered, cluster;
   long long items, n_split;
   int split_k;
   size_t bytes;
@@ -213,6 +279,7 @@ inline void cp_cross_fill(cpattn::CrossParams& p, const cp_cross_args& a, const 
   p.tiles = plan.tiles;
   p.rows = plan.rows;
   p.ordered = plan.ordered;
+  p.cluster = plan.cluster;
   p.scale_log2 = scale * cpattn::kLog2e;
   p.q_stride = a.q_stride;
   p.k_stride = a.k_stride;

@@ -391,7 +391,7 @@ cudaError_t launch_f32(const CrossParams& p, const CUtensorMap& mk, const CUtens
                        int cluster, cudaStream_t s) {
   using F = Fp32<D, NB, MW>;
   auto kern = p.ranges != nullptr ? f32_kernel<D, NB, MW, true> : f32_kernel<D, NB, MW, false>;
-  return launch_parts(kern, items, parts, cluster, F::kThreads, F::kSmem, s, mk, mv, p);
+  return launch_parts(kern, items, parts, cluster, F::kThreads, F::kSmem, s, mk, mv, p, parts, cluster);
 }
 template <int D>
 cudaError_t launch_d(const cp_cross_args& a, const CrossPlan& plan, int parts, int cluster, const CrossParams& p,

@@ -339,7 +339,7 @@ cudaError_t launch_few(const CrossParams& p, const CUtensorMap& mk, const CUtens
                        cudaStream_t s) {
   using F = Few<D, MT>;
   auto kern = p.ranges != nullptr ? few_kernel<D, MT, true> : few_kernel<D, MT, false>;
-  return launch_parts(kern, items, m.parts, m.cluster, F::kThreads, F::kSmem, s, mk, mv, p);
+  return launch_parts(kern, items, m.parts, m.cluster, F::kThreads, F::kSmem, s, mk, mv, p, m.parts, m.cluster);
 }
 
 template <int D>
@@ -400,6 +400,7 @@ CrossPlan cp_cross_plan_few(const cp_cross_args& a, int sms) {
   c.n_split = 0;
   c.split_k = 1;
   c.ordered = 0;
+  c.cluster = 1;  // (cluster_of says)
   // more parts than a cluster takes, through the workspace: where eight leave most of the GPU idle and the keys are
   // many enough to pay for a second launch
   const int tile = cpattn::tile_of(a);

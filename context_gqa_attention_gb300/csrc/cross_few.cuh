@@ -4,41 +4,11 @@
 #include <cuda.h>
 
 #include "cross.cuh"
-#include "sm100.cuh"
 
 namespace cpattn {
 namespace {
 
-using namespace sm100;
-
-constexpr long long kBudget = 4000000000ll;  // SM cycles per wait (~2 s)
 constexpr float kMaxGrowth = 8.f;            // log2 units the scores may exceed the running reference
-constexpr int kMaxCluster = 8;
-
-CP_DEV uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-CP_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-CP_DEV uint32_t peer_addr(const void* mine, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
-  return a;
-}
-CP_DEV float peer_ld(uint32_t a) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
-  return x;
-}
-CP_DEV float4 peer_ld4(uint32_t a) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
-  return x;
-}
 
 // ------------------------------------------------------------------------------ results
 template <typename T>
@@ -51,13 +21,6 @@ CP_DEV void put4(void* out, long long at, float4 v) {
     *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
   }
 }
-// Two sets of (reference in log2 units, sum, row) as one: the factor of a set whose reference is m.  (One of -inf saw
-// no finite score: its sums are 0, or NaN.)
-CP_DEV float factor(float m, float M) { return m == M || m == -INFINITY ? 1.f : exp2f(m - M); }
-CP_DEV float natural_lse(float M, float L) {
-  return L == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
-}
-
 // What W slices of the CTA's keys made of R rows, in shared memory: reference, sum, unnormalised row.
 // PAD: what keeps the rows' banks apart, for the kernel's way of writing them.
 template <int D, int W, int R, int PAD>
@@ -198,34 +161,6 @@ CP_DEV void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_
 CP_DEV uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// ------------------------------------------------------------------------------ launches
-// Grid: items, each one's parts side by side (a cluster's are neighbours).
-template <typename... K, typename... A>
-cudaError_t launch_parts(void (*kern)(K...), long long items, int parts, int cluster, int threads, size_t smem,
-                         cudaStream_t s, A... args) {
-  if (items * parts >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * parts));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cluster > 1) {
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)cluster;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  return cudaLaunchKernelEx(&cfg, kern, args..., parts, cluster);
 }
 
 // The maps of k and v, a tile of whose keys is fetched at a time.

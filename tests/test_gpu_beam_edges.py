@@ -78,6 +78,48 @@ def test_many_tiles_in_flight_on_every_sm(lib, T, Hq, d):
     check(out, lse, exact(q, k, v, spans, d ** -0.5), True)
 
 
+# B, rows of a sequence up to, keys up to, Hq, Hkv, d: few items of many rows, whose parts meet in clusters
+MEETING = [(1, 300, 2000, 2, 2, 64), (1, 1000, 1000, 6, 2, 64), (3, 200, 1500, 2, 2, 64), (2, 700, 2500, 4, 1, 128),
+           (1, 2048, 3500, 2, 2, 128), (5, 40, 1200, 16, 2, 64), (4, 90, 260, 3, 1, 64), (1, 129, 700, 65, 1, 64)]
+
+
+@pytest.mark.parametrize("B,T,S,Hq,Hkv,d", MEETING)
+@pytest.mark.parametrize("padded", [False, True])
+def test_parts_that_meet_in_clusters(lib, B, T, S, Hq, Hkv, d, padded):
+    """Sequences that end inside a part, or hold no key of it; infinities and NaN behind a sequence's keys; twice the same."""
+    r = np.random.default_rng(S)
+    rows, keys = r.integers(0, T + 1, B), r.integers(0, S + 1, B)
+    rows[0], keys[0], keys[-1] = T, S, (S if B == 1 else 3)
+    held = np.full(B, S) if padded else keys
+    g = torch.Generator(device=DEV).manual_seed(S)
+    n = int(rows.sum())
+    q = torch.randn(n, Hq, d, generator=g, device=DEV).bfloat16()
+    k, v = (torch.randn(int(held.sum()), Hkv, d, generator=g, device=DEV).bfloat16() for _ in range(2))
+    starts = np.cumsum([0] + list(held))
+    for b in range(B):
+        k[starts[b] + keys[b]:starts[b + 1]], v[starts[b] + keys[b]:starts[b + 1]] = math.nan, math.inf
+    spans = [(int(a), int(t), int(s), int(m)) for a, t, s, m in zip(np.cumsum([0] + list(rows)), rows, starts, keys)]
+    f = lambda: lib.cp_cross_attention(q, _cu(rows), k, v, _cu(held), kv_lens=torch.tensor(keys, **I32) if padded else None,
+                                       max_seqlen_q=T, max_seqlen_kv=S)
+    out, lse = f()
+    check(out, lse, exact(q, k, v, spans, d ** -0.5), False)
+    again = f()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("T", [200, 3])
+def test_a_visible_nan_in_one_part(lib, T):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    q, k, v = (torch.randn(n, 2, 64, generator=g, device=DEV).bfloat16() for n in (T, 2000, 2000))
+    v[1700, 0, 5], v[3, 1, 7] = math.nan, math.inf
+    out, lse = lib.cp_cross_attention(q, _cu([T]), k, v, _cu([2000]), max_seqlen_q=T)
+    assert bool(out[:, 0, 5].isnan().all()) and bool(out[:, 1, 7].isposinf().all()) and bool(lse.isfinite().all())
+    v[1700, 0, 5] = v[3, 1, 7] = 0
+    clean, _ = lib.cp_cross_attention(q, _cu([T]), k, v, _cu([2000]), max_seqlen_q=T)
+    out[:, 0, 5], out[:, 1, 7] = clean[:, 0, 5], clean[:, 1, 7]
+    assert torch.equal(out, clean)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_scores_that_are_not_finite_and_scores_in_place(lib, dtype):
     g = torch.Generator(device=DEV).manual_seed(5)
