@@ -34,6 +34,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kVecs = 512;            // vectors that a chunk's values are taken from
 constexpr int kList = 1024;           // values that a CTA compares with one another
+constexpr int kDirect = 96;           // of few values every thread counts those before its own; of more, four threads
 constexpr int kMaxBeams = 32, kMaxCandidates = 64;
 constexpr float kMaxGrowth = 16.f;    // a lane's values may exceed what its sum is relative to
 constexpr float kMaxLogit = 1e5f;     // beyond, the rounding of log2(e) times a logit is too coarse for one pass
@@ -338,6 +339,31 @@ CP_DEV void finish_sequence(const SelectParams& p, SelectShared& sh, int b) {
   }
   __syncthreads();
   int n = sh.n;
+  if (n >= p.M && n <= kDirect) {
+    // a thread an entry: how many come before it, and how many of those go on
+    if (tid < n) {
+      const unsigned long long key = sh.key[tid], at = place[tid];
+      int rank = 0, on = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const unsigned long long a = place[j], k = sh.key[j];
+        const bool before = k > key || (k == key && a < at);
+        rank += before;
+        on += before && (int)(uint32_t)a != p.eos;
+      }
+      const int beam = (int)(at >> 32), token = (int)(uint32_t)at;
+      const float score = value32((uint32_t)(key >> 32));
+      if (rank < p.M) {
+        const long long o = (long long)b * p.M + rank;
+        p.cand_score[o] = score, p.cand_beam[o] = beam, p.cand_token[o] = token;
+        if (token != p.eos && on < p.K) {
+          const long long to = (long long)b * p.K + on;
+          p.next_score[to] = score, p.next_beam[to] = beam, p.next_token[to] = token;
+        }
+      }
+    }
+    return;
+  }
   if (n > kList) {
     slow_finish(best, n_all, per, n = p.M, sh);
   } else {
@@ -622,11 +648,22 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
     n = sh.n2;
     if (n > kList) n = slow_list(c, least, p.M, sh);
   }
-  count_before<false>(sh, n);
+  auto put = [&](int rank, unsigned long long key) {
+    if (rank < p.M) best[rank] = make_uint2(__float_as_uint(value32((uint32_t)(key >> 32))), 0xffffffffu - (uint32_t)key);
+  };
+  if (n <= kDirect) {
+    if (tid < n) {
+      const unsigned long long key = sh.key[tid];
+      int rank = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank += sh.key[j] > key;
+      put(rank, key);
+    }
+  } else {
+    count_before<false>(sh, n);
 #pragma unroll 1
-  for (int i = tid; i < n; i += kThreads)
-    if (sh.rank[i] < p.M)
-      best[sh.rank[i]] = make_uint2(__float_as_uint(value32((uint32_t)(sh.key[i] >> 32))), 0xffffffffu - (uint32_t)sh.key[i]);
+    for (int i = tid; i < n; i += kThreads) put(sh.rank[i], sh.key[i]);
+  }
   for (int r = n + tid; r < p.M; r += kThreads) best[r] = make_uint2(0xff800000u, 0xffffffffu);
   if (tid == 0) p.stats[out] = make_float2(most, sum);
 
