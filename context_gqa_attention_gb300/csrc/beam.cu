@@ -27,9 +27,9 @@ namespace {
 // taken one after the other.
 //
 // Bound: HBM.  An element costs about five instructions (unpacking, maximum, packed difference and product,
-// exponential, sum), half of what the SM could issue in the time of its load.  64 x 8 rows of 128000 bf16 logits take 33 us
-// (3.97 TB/s, 58% of the copy): 21 us of stream at the copy's rate, then 7 in which all rows sum, list and rank at once.
-// One sequence of 4 x 32000 f32: 6.8 us, latency.  Not kept: two to four chunks a row for that batch (38 to 40 us), three CTAs
+// exponential, sum), half of what the SM could issue in the time of its load.  64 x 8 rows of 128000 bf16 logits take 32.6
+// us (4.02 TB/s, 59% of the copy): 21 us of stream at the copy's rate, then 7 in which all rows sum, list and rank at once.
+// One sequence of 4 x 32000 f32: 6.2 us, latency.  Not kept: two to four chunks a row for that batch (38 to 40 us), three CTAs
 // an SM, scalar exponentials (the same).
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kVecs = 512;            // vectors that a chunk's values are taken from
@@ -740,8 +740,8 @@ cudaError_t launch_select(const cp_beam_select_args& a, void* workspace, cudaStr
 // K beams' pages, K loads in flight at once, then takes the next place.  The tables go the same way, a
 // thread a column.  Tables that are replaced in place wait for the pages' copies in a launch of their own.
 // Bound: the launch and one chain of dependent loads (length, table entry, rows: 2300 cycles to the first row, then about 2000
-// a place).  64 x 8 beams of 64 .. 2048 tokens, 8 heads of 128, two ranks, bf16: 9.6 us (54% of the copy); 24 layers of 6 x 5
-// beams: 12.3; one sequence 2.7.  Not kept: two places at a time (14.8 us for the layers), a loop without its divisions (14.6: the
+// a place).  64 x 8 beams of 64 .. 2048 tokens, 8 heads of 128, two ranks, bf16: 9.5 us (54% of the copy); 24 layers of 6 x 5
+// beams: 12.2; one sequence 2.8.  Not kept: two places at a time (14.8 us for the layers), a loop without its divisions (14.6: the
 // loads then meet in the same banks of memory more often), blocks of 64 threads, more or fewer CTAs an SM.
 struct ReorderParams {
   int B, K, cp, I, max_blocks, Hkv, layers2, ctas;    // layers2: pools of K and of V; ctas: of a (sequence, rank)'s pages

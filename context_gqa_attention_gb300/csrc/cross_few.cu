@@ -12,7 +12,7 @@ namespace cpattn {
 namespace {
 
 // ------------------------------------------------------------------------------ the kernel
-// 64 sequences of 512 .. 4096 states, 4 beams of 32/8 heads, d = 128: 96.5 us (6.23 TB/s, 92% of the copy); one sequence of 1500
+// 64 sequences of 512 .. 4096 states, 4 beams of 32/8 heads, d = 128: 97.5 us (6.17 TB/s, 91% of the copy); one sequence of 1500
 // states, 16 heads, d = 64: 6.5 us, latency of the launch, the first loads and the cluster's meeting.
 //
 // MMAs of 16 rows on the legacy tensor path: a 128-row tcgen05 tile would be padding.  A producer warp brings tiles of
