@@ -287,9 +287,10 @@ CP_DEV void finish_sequence(const SelectParams& p, SelectShared& sh, int b) {
     const long long row = (long long)b * p.K + k;
     const float2* st = p.stats + row * p.S;
     const float from = ld(p.scores + row);
-    float top = -INFINITY, sum = 0.f;  // of the lane's chunks, then of all
+    const float2 first = lane < p.S ? __ldcg(st + lane) : make_float2(-INFINITY, 0.f);
+    float top = first.x, sum = first.y;  // of the lane's chunks, then of all
 #pragma unroll 1
-    for (int s = lane; s < p.S; s += 32) {
+    for (int s = lane + 32; s < p.S; s += 32) {
       const float2 x = __ldcg(st + s);
       if (x.x > -INFINITY) {
         const float m = fmaxf(top, x.x);
@@ -297,8 +298,9 @@ CP_DEV void finish_sequence(const SelectParams& p, SelectShared& sh, int b) {
         top = m;
       }
     }
-    const float most = warp_max(top);
-    sum = warp_sum(top == most ? sum : sum * exp2f((top - most) * kLog2e));
+    const float most = value32(__reduce_max_sync(0xffffffffu, order32(top)));
+    sum = top == most ? sum : sum * exp2f((top - most) * kLog2e);
+    if (p.S > 1) sum = warp_sum(sum);
     if (lane == 0) {
       sh.top[k] = most;
       sh.base[k] = sum > 0.f && from > -INFINITY ? add({from, 0.f}, minus_log(sum)) : Pair{-INFINITY, 0.f};
@@ -505,7 +507,6 @@ template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams p) {
   using W = Vec<T>;
   __shared__ SelectShared sh;
-  chained_start();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long row = blockIdx.x / (unsigned)p.S;
   const int part = (int)(blockIdx.x % (unsigned)p.S), b = (int)(row / p.K);
@@ -581,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
   constexpr int kRound = NV * kThreads;
   W va[NV], vb[NV];
   int v0 = c.va + tid;
+  chained_start();  // (nothing of the call's memory has been touched)
   auto load = [&](W (&v)[NV], int from) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) c.load(v[i], from + i * kThreads);

@@ -145,3 +145,33 @@ def test_rows_of_logits_past_32_bit_offsets(lib):
     logits.copy_(small)
     scores = torch.tensor([[-4.0, -3.0, -1.0]], device=DEV)
     check_select(lib.cp_beam_select(logits, scores, eos_token=2), small, scores, 6, 2)
+
+
+def test_calls_at_once_on_two_streams(lib):
+    """Each kind of call in flight on one stream while the others run on another: the results of one after the other."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    normal = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    jobs = []
+    for T, S, Hq, Hkv, d, dtype in [(300, 2000, 2, 2, 64, "bf16"), (1000, 3000, 8, 2, 128, "bf16"), (4, 1500, 8, 8, 64, "bf16"),
+                                    (5, 1200, 4, 2, 128, "f32"), (8, 16384, 4, 1, 128, "bf16")]:
+        q, k, v = (normal(n, h, d).to(DT[dtype]) for n, h in ((2 * T, Hq), (2 * S, Hkv), (2 * S, Hkv)))
+        a = (q, _cu([T, T]), k, v, _cu([S, S]))
+        jobs.append(lambda a=a, T=T, S=S: lib.cp_cross_attention(*a, max_seqlen_q=T, max_seqlen_kv=S))
+    logits, scores = (3 * normal(6, 5, 50257)).bfloat16(), normal(6, 5)
+    jobs.append(lambda: lib.cp_beam_select(logits, scores, eos_token=3))
+    parents = torch.randint(0, 4, (3, 4), generator=g, device=DEV).int()
+    tables, lens = torch.arange(12 * 3, **I32).reshape(1, 12, 3), torch.tensor([40, 16, 5], **I32)
+    jobs.append(lambda: (lib.cp_beam_reorder(parents, lens, tables, tables, None, None, 1, 16, tables_out=torch.zeros_like(tables)),))
+    want = [[x.clone() for x in f()] for f in jobs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for r in range(12):
+        for i in range(len(jobs)):
+            for n, s in enumerate(streams):
+                at = (i + r + n * (1 + r % 5)) % len(jobs)
+                with torch.cuda.stream(s):
+                    got.append((at, jobs[at]()))
+    torch.cuda.synchronize()
+    for at, out in got:
+        for x, y in zip(out, want[at]):
+            assert torch.equal(x, y), at
