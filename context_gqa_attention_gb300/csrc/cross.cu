@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)misc[0];
-  chained_start();
 
   // ---- the item, or the part of one
   int piece = -1, part = 0;

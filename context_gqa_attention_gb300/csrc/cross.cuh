@@ -79,7 +79,8 @@ CP_DEV CrossItem cross_sequence(const CrossParams& p, int b, int& rows, bool& re
   rows = bad ? 0 : (int)min(Tq, (long long)p.max_q);
   return w;
 }
-// The item of an index; every lane of a warp asks for the same.  reporter: one thread of the item's first CTA, which says
+// The item of an index, once the last call is done with the memory (chained_start); every lane of a warp asks for the
+// same.  reporter: one thread of the item's first CTA, which says
 // what is wrong with the sequence.
 //
 // ordered (up to 32 sequences of different lengths, one a lane): the sequences with the most keys first, so that the last
@@ -89,6 +90,7 @@ CP_DEV CrossItem cross_item(const CrossParams& p, unsigned index, bool reporter)
   int rows;
   bool wrong;
   if (p.ordered) {
+    chained_start();
     const int lane = (int)(threadIdx.x & 31), mine = min(lane, p.B - 1);
     w = cross_sequence(p, mine, rows, wrong);
     if (reporter && index == 0) {  // (thread 0 sees one sequence: it looks through the others)
@@ -120,9 +122,11 @@ CP_DEV CrossItem cross_item(const CrossParams& p, unsigned index, bool reporter)
     return w;
   }
   const unsigned tile = index % (unsigned)p.tiles, u = index / (unsigned)p.tiles;
-  w = cross_sequence(p, (int)(u / (unsigned)p.Hkv), rows, wrong);
-  w.g = (int)(u % (unsigned)p.Hkv);
-  w.t0 = (int)tile * p.span;
+  const int b = (int)(u / (unsigned)p.Hkv), g = (int)(u % (unsigned)p.Hkv), t0 = (int)tile * p.span;
+  chained_start();
+  w = cross_sequence(p, b, rows, wrong);
+  w.g = g;
+  w.t0 = t0;
   if (reporter && wrong && tile == 0 && w.g == 0) report(p.err, CP_ERR_DEVICE_BOUNDS);
   w.tokens = max(0, min(p.span, rows - w.t0));
   return w;
@@ -150,7 +154,6 @@ CP_DEV float natural_lse(float M, float L) {
 template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_merge_kernel(const CrossParams p) {
   constexpr int E = D / 32;
-  chained_start();
   const CrossItem w = cross_item(p, (unsigned)p.n_whole + blockIdx.x, false);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long part0 = (long long)blockIdx.x * p.split_k;

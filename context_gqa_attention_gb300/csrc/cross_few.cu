@@ -83,7 +83,6 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  chained_start();
   const int part = (int)(blockIdx.x % (unsigned)parts);
   const CrossItem w = cross_item(p, blockIdx.x / (unsigned)parts, threadIdx.x == 0 && part == 0);
   if (w.tokens == 0) return;  // (as every CTA of the cluster does)
