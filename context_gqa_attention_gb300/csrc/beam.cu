@@ -27,9 +27,9 @@ namespace {
 // taken one after the other.
 //
 // Bound: HBM.  An element costs about five instructions (unpacking, maximum, packed difference and product,
-// exponential, sum), half of what the SM could issue in the time of its load.  64 x 8 rows of 128000 bf16 logits take 32.6
-// us (4.02 TB/s, 59% of the copy): 21 us of stream at the copy's rate, then 7 in which all rows sum, list and rank at once.
-// One sequence of 4 x 32000 f32: 6.2 us, latency.  Not kept: two to four chunks a row for that batch (38 to 40 us), three CTAs
+// exponential, sum), half of what the SM could issue in the time of its load.  64 x 8 rows of 128000 bf16 logits take 32.0
+// us (4.10 TB/s, 60% of the copy): 21 us of stream at the copy's rate, then 7 in which all rows sum, list and rank at once.
+// One sequence of 4 x 32000 f32: 5.5 us, latency.  Not kept: two to four chunks a row for that batch (38 to 40 us), three CTAs
 // an SM, scalar exponentials (the same).
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kVecs = 512;            // vectors that a chunk's values are taken from

@@ -9,7 +9,7 @@
 //
 // Bound: for up to 8 rows a kv head HBM once there is work for every SM (152 sequences of 2000 states, d = 128: 5.8 TB/s, 85%
 // of the copy; d = 64: 5.2); for 16 rows 4.5 TB/s, for 32 the tensor pipe at 3.1.  8 sequences of 0 .. 900 states, 5 beams of
-// 16 heads, d = 64: 15.4 us against 3.5 for their bytes: the start, the longest part, the cluster's meeting.
+// 16 heads, d = 64: 15.3 us against 3.5 for their bytes: the start, the longest part, the cluster's meeting.
 #include "cross_few.cuh"
 
 namespace cpattn {

@@ -12,8 +12,8 @@ namespace cpattn {
 namespace {
 
 // ------------------------------------------------------------------------------ the kernel
-// 64 sequences of 512 .. 4096 states, 4 beams of 32/8 heads, d = 128: 97.5 us (6.17 TB/s, 91% of the copy); one sequence of 1500
-// states, 16 heads, d = 64: 6.5 us, latency of the launch, the first loads and the cluster's meeting.
+// 64 sequences of 512 .. 4096 states, 4 beams of 32/8 heads, d = 128: 97.4 us (6.17 TB/s, 91% of the copy); one sequence of 1500
+// states, 16 heads, d = 64: 6.2 us, latency of the launch, the first loads and the cluster's meeting.
 //
 // MMAs of 16 rows on the legacy tensor path: a 128-row tcgen05 tile would be padding.  A producer warp brings tiles of
 // K and V through a ring (TMA, 128-byte swizzle); consumer warp (m, k) owns the 16 rows m and the k-th slice of every
