@@ -30,6 +30,22 @@ CP_DEV void split(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
   l = pack2(x, y);
 }
 
+// A score that the parts' products left NaN, once more.  Where an element's bf16 is an infinity (the element is one, or a
+// number above 3.39e38 that rounds to one) its lower parts are NaN, and so is every product of them: such a score is the sum
+// of the elements' own products.  Others stay as they are.
+template <int D>
+CP_DEV float odd_score(const float* q, const float* k, float c) {
+  float s = 0.f;
+  bool odd = false;
+#pragma unroll 1
+  for (int i = 0; i < D; ++i) {
+    const float x = ld(q + i), y = ld(k + i);
+    odd = odd || max(__float_as_uint(x) & 0x7fffffffu, __float_as_uint(y) & 0x7fffffffu) >= 0x7f7f8000u;
+    s = fmaf(x, y, s);
+  }
+  return odd ? s : c;
+}
+
 // The products are taken transposed, S^T = K Q^T and O^T = V^T P^T: a tile of K or V is an MMA's 16 rows and the query rows
 // are its 8 columns, so that 5 beams are padded to 8, and the many splits of K and V serve all query rows.  A producer warp
 // brings tiles of 16 keys through a ring (TMA, 128-byte swizzle); consumer warp (m, g) takes every kGroups-th tile for the NB
@@ -241,7 +257,7 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
       }
       const bool whole = k0 + 16 <= key.end && (!RANGES || (k0 >= key.all_lo && k0 + 16 <= key.all_hi));
       float top[NB][2];
-      bool moves = false;
+      bool moves = false, odd = false;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -253,6 +269,24 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
             if (gid < a || gid >= b) c[n][e] = -INFINITY;
             if (gid + 8 < a || gid + 8 >= b) c[n][e + 2] = -INFINITY;
           }
+          odd = odd || isnan(c[n][e]) || isnan(c[n][e + 2]);
+        }
+      if (odd) {  // (rare; a masked score is -inf, so a NaN is that of a key that the row sees)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = row0 + 8 * n + 2 * tig + (e & 1), t = row / p.G;
+            if (row < rows && isnan(c[n][e]))
+              c[n][e] = odd_score<D>(
+                  static_cast<const float*>(p.q) + ((long long)w.q0 + w.t0 + t) * p.q_stride + (w.g * p.G + row - t * p.G) * D,
+                  static_cast<const float*>(p.k) + ((long long)w.kv0 + k0 + gid + 8 * (e >> 1)) * p.k_stride + w.g * D, c[n][e]);
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
           top[n][e] = fmaxf(c[n][e], c[n][e + 2]) * sc;
           moves = moves || top[n][e] > m[n][e] + kMaxGrowth;
         }
