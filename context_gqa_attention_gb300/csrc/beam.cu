@@ -36,7 +36,8 @@ constexpr int kVecs = 512;            // vectors that a chunk's values are taken
 constexpr int kList = 1024;           // values that a CTA compares with one another
 constexpr int kDirect = 96;           // of few values every thread counts those before its own; of more, four threads
 constexpr int kMaxBeams = 32, kMaxCandidates = 64;
-constexpr float kMaxGrowth = 16.f;    // a lane's values may exceed what its sum is relative to
+constexpr float kMaxGrowth = 11.f;    // a lane's values may exceed what its sum is relative to (in log2 units below 16, where
+                                      // an exponent is rounded by 2^-21 at most)
 constexpr float kMaxLogit = 1e5f;     // beyond, the rounding of log2(e) times a logit is too coarse for one pass
 constexpr float kMost = 3.402823466e38f;  // the largest finite value
 
@@ -134,6 +135,7 @@ CP_DEV void add_exp2(uint64_t& sum, float x, float y, uint64_t log2e, uint64_t m
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
   asm("add.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(v));
 }
+CP_DEV float low(uint64_t pair) { return __uint_as_float((uint32_t)pair); }
 // The block's sum, the same for every thread.
 CP_DEV float block_sum(float x, float* s_warp) {
   x = warp_sum(x);
@@ -528,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
   // this lane's largest value, and what its sum is relative to (values far below any that counts, a mask's lowest ones,
   // do not move it)
   float top = -INFINITY, ref = -kMaxLogit;
-  // pairs of sums of 2^(x log2(e) - c), c = ref log2(e) rounded, which is made good at the end
+  // pairs of sums of 2^(x log2(e) - c), c = ref log2(e) rounded.  They move by differences of the c's as they were rounded
+  // (up to 2^-7, for logits near 1e5), not of the references
   uint64_t part_sum[2] = {0ull, 0ull}, minus_c, log2e;
   asm("mov.b64 %0, {%1, %1};" : "=l"(log2e) : "f"(kLog2e));
   asm("mov.b64 %0, {%1, %1};" : "=l"(minus_c) : "f"(kMaxLogit * kLog2e));
@@ -552,14 +555,13 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
     }
     top = fmaxf(top, mx);
     if (top > ref + kMaxGrowth) {  // (the first time, and rarely again)
-      const float f = ex2_approx((ref - top) * kLog2e);
+      const float now = __fmul_rn(-top, kLog2e), f = ex2_approx(__fsub_rn(now, low(minus_c)));
       uint64_t f2;
       asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
 #pragma unroll
       for (int i = 0; i < 2; ++i) asm("mul.f32x2 %0, %0, %1;" : "+l"(part_sum[i]) : "l"(f2));
       ref = top;
-      const float c = -ref * kLog2e;
-      asm("mov.b64 %0, {%1, %1};" : "=l"(minus_c) : "f"(c));
+      asm("mov.b64 %0, {%1, %1};" : "=l"(minus_c) : "f"(now));
     }
 #pragma unroll
     for (int i = 0; i < kN; ++i)
@@ -621,8 +623,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
     asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(part_sum[0]));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(s[2]), "=f"(s[3]) : "l"(part_sum[1]));
     sum = (s[0] + s[1]) + (s[2] + s[3]);
-    const float c = ref * kLog2e;
-    sum *= ex2_approx((ref - most) * kLog2e - fmaf(ref, kLog2e, -c));
+    sum *= ex2_approx(fmaf(-most, kLog2e, -low(minus_c)));
   }
   sum = block_sum(sum, sh.w_sum);
   if (!(sum < INFINITY) || fabsf(most) > kMaxLogit) {
