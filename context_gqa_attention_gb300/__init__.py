@@ -854,7 +854,8 @@ def cp_cross_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_
                                       total_q=None, total_kv=None, padded=False, dtype=torch.bfloat16):
     """Bytes of workspace with which cp_cross_attention cuts the keys of these sizes into parts on the current
     device (0: it needs none).  total_q, total_kv: rows of q and of k (num_seqs of the longest, if not given); padded:
-    the call gets kv_lens or key_ranges."""
+    the call gets kv_lens or key_ranges (the most that calls with either or both take).  Other sizes, smaller ones
+    too, may be cut into more."""
     load()
     a = CrossArgs()
     if dtype not in (torch.bfloat16, torch.float32):
@@ -864,11 +865,12 @@ def cp_cross_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_
     a.max_seqlen_q, a.max_seqlen_kv = max_seqlen_q, max_seqlen_kv
     a.total_q = num_seqs * max_seqlen_q if total_q is None else total_q
     a.total_kv = num_seqs * max_seqlen_kv if total_kv is None else total_kv
-    if padded:
-        a.kv_lens = 1       # (whether there is one is all that counts here)
-    need = ctypes.c_size_t()
-    _check(_LIB.cp_cross_attention_workspace_size(ctypes.byref(a), ctypes.byref(need)))
-    return need.value
+    most, need = 0, ctypes.c_size_t()
+    for lens, ranges in ((1, None), (None, 1), (1, 1)) if padded else ((None, None),):
+        a.kv_lens, a.key_ranges = lens, ranges       # (whether there are any is all that counts here)
+        _check(_LIB.cp_cross_attention_workspace_size(ctypes.byref(a), ctypes.byref(need)))
+        most = max(most, need.value)
+    return most
 
 
 def cp_cross_attention(q, cu_seqlens_q, k, v, cu_seqlens_kv, *, kv_lens=None, key_ranges=None, max_seqlen_q=None,
