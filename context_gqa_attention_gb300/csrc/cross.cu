@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float lse = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
-        // what the guards took out of V and this row sees: p > 0 times it is itself, whatever p is
+        // what the guards took out of V and this row sees: p > 0 times it is itself, however small p
         if constexpr (RANGES) {
           const int u0 = *(volatile int*)(misc + 2), u1 = *(volatile int*)(misc + 3);
           if (u1 >= 0) {
@@ -546,8 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           L += ms[c] * ls[c];
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
+        // (-1: a part without keys, whose rows are not read; a weight of 0 times what is not finite is NaN)
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) weight[c * BM + tid] = ms[c] * inv;
+        for (int c = 0; c < kMaxCluster; ++c) weight[c * BM + tid] = ls[c] == 0.f ? -1.f : ms[c] * inv;
         if (p.lse != nullptr) p.lse[r0 + tid < rows0 ? out_row(0, r0 + tid) : out_row(1, r0 + tid - rows0)] = natural_lse(M, L);
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -559,12 +560,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float e[kMaxCluster];
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
-          e[c] = c < k ? weight[c * BM + r] : 0.f;
-          if (e[c] != 0.f) x[c] = peer_ld4(peer_addr(sbase, c) + at);
+          e[c] = c < k ? weight[c * BM + r] : -1.f;
+          if (!(e[c] < 0.f)) x[c] = peer_ld4(peer_addr(sbase, c) + at);
         }
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)
-          if (e[c] != 0.f) o.x += e[c] * x[c].x, o.y += e[c] * x[c].y, o.z += e[c] * x[c].z, o.w += e[c] * x[c].w;
+          if (!(e[c] < 0.f)) o.x += e[c] * x[c].x, o.y += e[c] * x[c].y, o.z += e[c] * x[c].z, o.w += e[c] * x[c].w;
         const long long to = (r0 + r < rows0 ? out_row(0, r0 + r) : out_row(1, r0 + r - rows0)) * D + 4 * c4;
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
       }

@@ -150,7 +150,8 @@ CP_DEV float natural_lse(float M, float L) {
 }
 
 // Parts -> rows: out = sum_k e_k out_k / sum_k e_k with e_k = exp(lse_k - max lse); a part without a key has the
-// LSE -inf and its row is not read.  A warp takes a row, its lanes the dims.
+// LSE -inf and its row is not read, another one's is, even for a weight that underflows: 0 times what is not finite is NaN.
+// A warp takes a row, its lanes the dims.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_merge_kernel(const CrossParams p) {
   constexpr int E = D / 32;
@@ -173,12 +174,12 @@ __global__ void __launch_bounds__(256) cross_merge_kernel(const CrossParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (32 * i >= p.split_k) break;
-      const float mine = x[i] == -INFINITY ? 0.f : exp2f(x[i] - (M == -INFINITY ? 0.f : M));  // NaN stays
+      const float mine = x[i] == -INFINITY ? -1.f : exp2f(x[i] - (M == -INFINITY ? 0.f : M));  // (NaN stays; -1: no key)
       const int n = min(32, p.split_k - 32 * i);
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
         const float e = __shfl_sync(0xffffffffu, mine, j);
-        if (e == 0.f) continue;
+        if (e < 0.f) continue;
         const float* src = p.ws_out + ((part0 + 32 * i + j) * p.rows + row) * D + lane * E;
         sum += e;
         if constexpr (E == 4) {

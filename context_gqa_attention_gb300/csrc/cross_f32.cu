@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(Fp32<D, NB, MW>::kThreads, Fp32<D, NB, MW>::kC
     }
     if (!ok && lane == 0) fail();
     if (u1 >= 0) {
-      // what was taken out of V for the rows that see it: p > 0 times it is itself, whatever p is
+      // what was taken out of V for the rows that see it: p > 0 times it is itself, however small p
       const float* v = static_cast<const float*>(p.v) + (long long)w.kv0 * p.v_stride + w.g * D;
 #pragma unroll
       for (int n = 0; n < NB; ++n)

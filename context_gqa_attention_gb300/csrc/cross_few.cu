@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, Few<D, MT>::kCtas)
     }
     if (!ok && lane == 0) fail();
     if (RANGES && u1 >= 0) {
-      // what was taken out of V for the rows that see it: p > 0 times it is itself, whatever p is.  The warp's keys
+      // what was taken out of V for the rows that see it: p > 0 times it is itself, however small p.  The warp's keys
       // are one slice in kWK of every tile.
       const T* v = static_cast<const T*>(p.v) + (long long)w.kv0 * p.v_stride + w.g * D;
 #pragma unroll

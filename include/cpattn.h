@@ -589,7 +589,9 @@ cp_status cp_decode_attention_q4(const cp_decode_args* args, const cp_score_mod*
  *   - err: CP_ERR_DEVICE_BOUNDS for a sequence whose rows go past total_q or total_kv or have negative lengths
  *     (skipped), with more rows than max_seqlen_q (the rest is left out), or with kv_lens[b] outside
  *     [0, its rows] (taken as the nearest of the two).  max_seqlen_kv only guides the cut: any value is right.
- * Weights and values are summed before they are divided: finite components of v are below 2^96.
+ * Weights and values are summed before they are divided: finite components of v are below 2^96.  One that is not
+ * finite, in a key that the row sees, makes that component of the row infinite or NaN, however small the key's
+ * weight: NaN where that is 0 in 32 bits, which depends on how the keys are cut.
  * bf16: P is rounded to bf16 for the tensor cores; num_q_heads / num_kv_heads <= 128.  f32: products
  * of 24 bits summed in fp32; <= 64.
  * ---------------------------------------------------------------------------- */
