@@ -910,7 +910,8 @@ def cp_beam_select(logits, scores, *, num_candidates=None, eos_token=-1, workspa
     f32 [B, K] (see cpattn.h).  num_candidates: 2 K (or what there is) if not given.  `workspace`: zero-filled uint8
     CUDA tensor of cp_beam_select_workspace_size() bytes, left reusable; None allocates it.
     Returns (next_scores f32, next_beams, next_tokens int32 [B, K], cand_scores f32, cand_beams, cand_tokens
-    int32 [B, num_candidates]): the candidates in falling order, and the first K that are not eos_token."""
+    int32 [B, num_candidates]): the candidates in falling order, and the first K that are not eos_token.  The new ones
+    among them lie in one allocation, which lives as long as any of them; resize none of them."""
     binding = _binding()
     if num_candidates is None:
         _on_gpu("cp_beam_select", logits)

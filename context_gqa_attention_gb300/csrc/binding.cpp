@@ -161,8 +161,10 @@ struct Call {
   }
 };
 
-// New outputs of one call share an allocation (an allocation through the dispatcher costs the host about a microsecond, as
-// much as a quarter of a small call; a tensor over memory that is there a fifth of that).
+// The outputs of a call: those given, checked, and new ones, straight from the caching allocator (an allocation through the
+// dispatcher costs the host about a microsecond, a quarter of a small call).  New ones are apart, so that who keeps the
+// LSEs does not keep the rows; or `together` in one allocation, where they are small and many (the selection's six: 4.7 us
+// of the host a call, 7.0 apart).
 struct Outputs {
   struct One {
     const Tensor* given;
@@ -177,16 +179,21 @@ struct Outputs {
   void add(Tensor& to, const Tensor* given, const char* name, std::initializer_list<int64_t> shape, at::ScalarType dtype) {
     all.push_back({given, name, at::DimVector(shape), dtype, &to});
   }
-  void make() {
-    size_t bytes = 0;
-    auto size_of = [](const One& o) {
-      size_t n = c10::elementSize(o.dtype);
-      for (const int64_t d : o.shape) n *= (size_t)d;
-      return (n + 255) / 256 * 256;
-    };
+  static size_t bytes_of(const One& o) {
+    size_t n = c10::elementSize(o.dtype);
+    for (const int64_t d : o.shape) n *= (size_t)d;
+    return n;
+  }
+  // of the call's device and stream, both current
+  static c10::Storage memory(size_t bytes) {
+    c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
+    return c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes, from->allocate(bytes), from, true));
+  }
+  void make(bool together) {
+    size_t sum = 0;
     for (const One& o : all) {
       if (o.given == nullptr) {
-        bytes += size_of(o);
+        sum += (bytes_of(o) + 255) / 256 * 256;
         continue;
       }
       c.dense(*o.given, o.name, o.dtype);
@@ -194,18 +201,16 @@ struct Outputs {
         refuse(std::string(o.name) + " must be " + text(o.shape) + " (got " + text(o.given->sizes()) + ")");
       *o.to = *o.given;
     }
-    if (bytes == 0) bytes = 1;
-    c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
-    c10::Storage memory;  // of the call's device and stream, both current
+    c10::Storage shared;
     size_t at = 0;
     for (const One& o : all) {
       if (o.given != nullptr) continue;
-      if (!memory) memory = c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes, from->allocate(bytes), from, true));
-      Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(memory), c10::DispatchKeySet(c10::DispatchKey::CUDA),
-                                                          c10::scalarTypeToTypeMeta(o.dtype));
+      if (together && !shared) shared = memory(sum);
+      Tensor t = at::detail::make_tensor<c10::TensorImpl>(together ? c10::Storage(shared) : memory(bytes_of(o)),
+                                                          c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(o.dtype));
       t.unsafeGetTensorImpl()->set_sizes_contiguous(o.shape);
-      t.unsafeGetTensorImpl()->set_storage_offset((int64_t)(at / c10::elementSize(o.dtype)));
-      at += size_of(o);
+      if (together) t.unsafeGetTensorImpl()->set_storage_offset((int64_t)(at / c10::elementSize(o.dtype)));
+      at += (bytes_of(o) + 255) / 256 * 256;
       *o.to = std::move(t);
     }
   }
@@ -592,7 +597,7 @@ PyObject* cross(Args& x) {
   Outputs made(c);
   made.add(o, out, "out", {N, Hq, d}, T);
   if (out_lse != nullptr || want_lse) made.add(l, out_lse, "out_lse", {N, Hq}, at::kFloat);
-  made.make();
+  made.make(false);
   Tensor workspace;
   if (given != nullptr) {
     c.dense(*given, "workspace", at::kByte);
@@ -665,7 +670,7 @@ PyObject* beam_select(Args& x) {
   made.add(o3, cs, "cand_scores", {B, M}, at::kFloat);
   made.add(o4, cb, "cand_beams", {B, M}, at::kInt);
   made.add(o5, ct, "cand_tokens", {B, M}, at::kInt);
-  made.make();
+  made.make(true);
   a.logits = in(logits);
   a.scores = static_cast<const float*>(in(scores));
   a.next_scores = static_cast<float*>(out_of(o0));
