@@ -927,7 +927,8 @@ def cp_beam_reorder(parents, seq_lens, block_tables, own_pages, k_cache, v_cache
     max_blocks] becomes the parent's, and the page being filled is copied to the beam's own (own_pages, shaped as
     block_tables; see cpattn.h).  seq_lens int32 [B]: tokens in the cache.  The pools are [cp, pool, Hkv, 16, d], uint8
     [cp, pool, Hkv, 9 d] (4-bit records) or several layers of either [layers, ..]; None and None: tables only.
-    tables_out may be block_tables (in place).  Returns it, or a new tensor, whose further columns are undefined."""
+    tables_out may be block_tables (in place).  Returns it, or new tables: a copy of block_tables where they are left as
+    they are."""
     return _binding().beam_reorder(parents, seq_lens, block_tables, own_pages, k_cache, v_cache, cp, interleave,
                                    tables_out, err, _handle(stream))
 

@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
@@ -741,6 +742,11 @@ PyObject* beam_reorder(Args& x) {
   a.own_pages = static_cast<const int32_t*>(in(own));
   a.tables_out = static_cast<int32_t*>(out_of(o));
   a.err = c.error_word(err);
+  if (out == nullptr) {  // what is left as it is (bad parents, bad lengths, further columns) holds the pages it had
+    const cudaError_t e = cudaMemcpyAsync(a.tables_out, a.tables_in, (size_t)o.nbytes(), cudaMemcpyDeviceToDevice,
+                                          static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) refuse(std::string("cp_beam_reorder: ") + cudaGetErrorString(e), CP_ERR_CUDA);
+  }
   check(cp_beam_reorder(&a, stream));
   PyObject* r = THPVariable_Wrap(o);
   if (r == nullptr) throw python_error();
