@@ -882,8 +882,9 @@ def cp_cross_attention(q, cu_seqlens_q, k, v, cu_seqlens_kv, *, kv_lens=None, ke
     kv_lens int32 [B]: a sequence's keys are its first kv_lens[b] rows (a padded batch).  key_ranges int32
     [Nq, 2]: each row sees the keys [lo, hi) of its sequence.  q, k and v may be column slices of a wider tensor
     (any token stride).  bf16 or f32.  `workspace`: uint8 CUDA tensor of cp_cross_attention_workspace_size()
-    bytes; None allocates it, an empty one leaves out the cuts that need it.  max_seqlen_q is fetched from the device if it is not
-    given; max_seqlen_kv only guides the cut (the average is taken).
+    bytes, left dirty (not the zero-filled one of other calls); None allocates it, an empty one leaves out the cuts that
+    need it.  max_seqlen_q is fetched from the device if it is not given; max_seqlen_kv only guides the cut (the average is
+    taken).
     Returns (out [Nq, Hq, d] dtype of q, lse [Nq, Hq] f32 or None)."""
     binding = _binding()
     if max_seqlen_q is None:
@@ -908,7 +909,8 @@ def cp_beam_select(logits, scores, *, num_candidates=None, eos_token=-1, workspa
                    next_beams=None, next_tokens=None, cand_scores=None, cand_beams=None, cand_tokens=None, stream=None):
     """The best continuations of each sequence's beams: logits [B, K, vocab] (bf16 or f32, any row stride), scores
     f32 [B, K] (see cpattn.h).  num_candidates: 2 K (or what there is) if not given.  `workspace`: zero-filled uint8
-    CUDA tensor of cp_beam_select_workspace_size() bytes, left reusable; None allocates it.
+    CUDA tensor of cp_beam_select_workspace_size() bytes, left reusable, for fused decodes of up to 65536 sequences x kv
+    heads too; None allocates it.
     Returns (next_scores f32, next_beams, next_tokens int32 [B, K], cand_scores f32, cand_beams, cand_tokens
     int32 [B, num_candidates]): the candidates in falling order, and the first K that are not eos_token.  The new ones
     among them lie in one allocation, which lives as long as any of them; resize none of them."""
