@@ -27,8 +27,8 @@ namespace {
 // taken one after the other.
 //
 // Bound: HBM.  An element costs about five instructions (unpacking, maximum, packed difference and product,
-// exponential, sum), half of what the SM could issue in the time of its load.  64 x 8 rows of 128000 bf16 logits take 32.0
-// us (4.10 TB/s, 60% of the copy): 21 us of stream at the copy's rate, then 7 in which all rows sum, list and rank at once.
+// exponential, sum), half of what the SM could issue in the time of its load.  64 x 8 rows of 128000 bf16 logits take 32.3
+// us (4.06 TB/s, 60% of the copy): 21 us of stream at the copy's rate, then 7 in which all rows sum, list and rank at once.
 // One sequence of 4 x 32000 f32: 5.5 us, latency.  Not kept: two to four chunks a row for that batch (38 to 40 us), three CTAs
 // an SM, scalar exponentials (the same).
 constexpr int kThreads = 256, kWarps = 8;
@@ -684,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_kernel(const SelectParams 
 
 // Chunks: one a row if that gives every SM its four CTAs or nearly; else as many as do, of 16 KB at least (shorter ones
 // cost the last CTA more than they save), and where beams and candidates are many no more than give it 1024 values to
-// look through.  More rows than places: a third of the GPU's places each, so that the last ones are short.
+// look through.  More rows than places: a third of the GPU's places each, so that the last ones are short.  152 SMs are
+// GB300's: the workspace's size follows from the cut and does not ask the device.
 struct SelectPlan {
   int NV, S, chunk;
 };
@@ -854,7 +855,7 @@ __global__ void __launch_bounds__(kReorderThreads, reorder_ctas(KMAX)) reorder_k
 
 cudaError_t reorder_launch(ReorderParams p, cudaStream_t s) {
   const int kmax = p.K <= 4 ? 4 : p.K <= 8 ? 8 : p.K <= 16 ? 16 : 32;
-  const long long units = (long long)p.B * p.cp, slots = 152ll * reorder_ctas(kmax);
+  const long long units = (long long)p.B * p.cp, slots = 152ll * reorder_ctas(kmax);  // (GB300's SMs; any number is right)
   const long long most = ((long long)p.Hkv * 15 * p.row_vecs * p.layers2 + kReorderThreads - 1) / kReorderThreads;
   const long long ctas = (slots + units - 1) / units;
   p.ctas = (int)(ctas < most ? ctas : most);

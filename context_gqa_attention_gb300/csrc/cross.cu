@@ -16,10 +16,10 @@
 // shared memory of a cluster (CLUSTER), or in the workspace, where cross_merge_kernel joins them.
 //
 // Bound: the chain of a row tile, softmax - PV - QK^T, about 2780 cycles a key tile of two row tiles (d = 128) against 2150 of
-// MMA: 8192 tokens over 6404 states, 16/2 heads, d = 128 take 292 to 308 us by the board (74 to 78% of the measured peak).  Short items: the
+// MMA: 8192 tokens over 6404 states, 16/2 heads, d = 128 take 292 to 315 us by the board (73 to 78% of the measured peak).  Short items: the
 // start (about 4000 cycles: item, Q, first K tile and scores) and the way out (1700 to 3500).  9 prompts of 1 .. 447 tokens over
-// 200 .. 1500 states, 16 heads, d = 64: 18.5 us; 3 texts of 600 .. 2500 tokens with ranges of 1025 of 3000 .. 8000 states, 32/8
-// heads, d = 128: 112 us (33%: a quarter of the row tiles lies across two ranges and sees both).
+// 200 .. 1500 states, 16 heads, d = 64: 19.1 us; 3 texts of 600 .. 2500 tokens with ranges of 1025 of 3000 .. 8000 states, 32/8
+// heads, d = 128: 113 us (33%: an eighth of the row tiles lies across two ranges and sees both).
 //
 // Every wait is bounded; on expiry the CTA raises CP_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns.
 #include <cuda.h>

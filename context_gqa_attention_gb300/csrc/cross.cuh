@@ -250,11 +250,12 @@ struct CrossPlan {
   int split_k;
   size_t bytes;
 };
-// The kernel for few rows takes f32, and bf16 of up to 64 rows a kv head; the tensor cores' tiles of 128 rows the rest.
+// Items of up to 64 rows: f32 (cross_f32.cu), and bf16 of up to 64 rows a kv head (cross_few.cu).  The tensor cores' tiles of
+// 128 rows take the rest (cross.cu).
 inline bool cp_cross_few(const cp_cross_args& a) {
   return a.dtype == CP_F32 || (long long)a.max_seqlen_q * (a.num_q_heads / a.num_kv_heads) <= 64;
 }
-// Tokens of an item: 64 rows of the kernel for few rows (or what there is), two row tiles of the other.
+// Tokens of an item: 64 rows of the kernels for few rows (or what there is), two row tiles of the other.
 inline int cp_cross_span(const cp_cross_args& a) {
   const int G = a.num_q_heads / a.num_kv_heads;
   if (!cp_cross_few(a)) return 2 * (128 / G);

@@ -9,7 +9,7 @@
 //
 // Bound: for up to 8 rows a kv head HBM once there is work for every SM (152 sequences of 2000 states, d = 128: 5.8 TB/s, 85%
 // of the copy; d = 64: 5.2); for 16 rows 4.5 TB/s, for 32 the tensor pipe at 3.1.  8 sequences of 0 .. 900 states, 5 beams of
-// 16 heads, d = 64: 15.3 us against 3.5 for their bytes: the start, the longest part, the cluster's meeting.
+// 16 heads, d = 64: 15.4 us against 3.5 for their bytes: the start, the longest part, the cluster's meeting.
 #include "cross_few.cuh"
 
 namespace cpattn {
@@ -31,8 +31,8 @@ CP_DEV void split(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
 }
 
 // A score that the parts' products left NaN, once more.  Where an element's bf16 is an infinity (the element is one, or a
-// number above 3.39e38 that rounds to one) its lower parts are NaN, and so is every product of them: such a score is the sum
-// of the elements' own products.  Others stay as they are.
+// number above 3.39e38 that rounds to one) its lowest part is NaN, and so is every product of it: such a score is the sum of
+// the elements' own products.  Others stay as they are.
 template <int D>
 __device__ __noinline__ float odd_score(const float* q, const float* k, float c) {
   float s = 0.f;
@@ -42,7 +42,7 @@ __device__ __noinline__ float odd_score(const float* q, const float* k, float c)
     s = fmaf(x, y, s);
   };
 #pragma unroll 1
-  for (int i = 0; i < D && !isnan(s); i += 4) {  // (a NaN stays: rows of NaN take little longer)
+  for (int i = 0; i < D && !isnan(s); i += 4) {  // (a NaN stays: 300 rows of NaN over 8000 keys 0.78 ms, others 0.41)
     const float4 x = *reinterpret_cast<const float4*>(q + i), y = *reinterpret_cast<const float4*>(k + i);
     take(x.x, y.x), take(x.y, y.y), take(x.z, y.z), take(x.w, y.w);
   }

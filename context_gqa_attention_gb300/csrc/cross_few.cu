@@ -368,7 +368,7 @@ int slots_of(const cp_cross_args& a, int rows, int sms) {
 // once the longest decides, else the load of a place and most of the longest.  How far lengths differ is only known from
 // the totals; of a padded batch they are taken to be about half of the longest.  (22 sequences of 674 .. 5392 states, 8 kv
 // heads, 24 rows: 94 us whole, 72 in three; 64 of 512 .. 4096, 16 rows: 105.5 whole, 98.6 in two, 109 in four; 43 of up to
-// 268, 4 kv heads: 6.6 whole, 11.2 in two; f32, 4 of up to 7668, 8 kv heads, 9 rows: 84 in three, 51 in eight.)
+// 268, 4 kv heads: 6.6 whole, 11.2 in two; f32, 4 of up to 7668, 8 kv heads, 9 rows: 84 in three, 54 in eight.)
 int cluster_of(const cp_cross_args& a, const CrossPlan& c, int sms) {
   const bool f32 = a.dtype == CP_F32;
   const double tile = tile_of(a), slots = slots_of(a, c.rows, sms), items = (double)c.items;
