@@ -593,7 +593,7 @@ cp_status cp_decode_attention_q4(const cp_decode_args* args, const cp_score_mod*
  * finite, in a key that the row sees, makes that component of the row infinite or NaN, however small the key's
  * weight: NaN where that is 0 in 32 bits, which depends on how the keys are cut.
  * bf16: P is rounded to bf16 for the tensor cores; num_q_heads / num_kv_heads <= 128.  f32: products
- * of 24 bits summed in fp32; <= 64.
+ * of 24 bits (fewer of numbers below 2^-100) summed in fp32; <= 64.
  * ---------------------------------------------------------------------------- */
 typedef struct cp_cross_args {
   int32_t dtype;                /* cp_dtype of q, k, v, out                             */
