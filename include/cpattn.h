@@ -584,8 +584,9 @@ cp_status cp_decode_attention_q4(const cp_decode_args* args, const cp_score_mod*
  *   - workspace: device scratch, 256-byte aligned, of cp_cross_attention_workspace_size() bytes, for cutting
  *     the keys of long or few items into parts that meet in memory (0 bytes: none for these sizes).  The size is
  *     that of the call's own arguments, of kv_lens and key_ranges whether they are NULL.  NULL or a smaller one
- *     cuts nothing so (the same results up to rounding).  No initialisation is needed, and none is left: not a
- *     workspace that the selection or a fused decode wants zero-filled.  Calls that use one must not overlap.
+ *     cuts nothing so (the same results up to rounding).  No initialisation is needed.  The call leaves it dirty:
+ *     it may not be one that cp_beam_select or a fused decode expects zero-filled.  Calls that use one must not
+ *     overlap.
  *   - err: CP_ERR_DEVICE_BOUNDS for a sequence whose rows go past total_q or total_kv or have negative lengths
  *     (skipped), with more rows than max_seqlen_q (the rest is left out), or with kv_lens[b] outside
  *     [0, its rows] (taken as the nearest of the two).  max_seqlen_kv only guides the cut: any value is right.
